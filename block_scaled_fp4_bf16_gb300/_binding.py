@@ -45,6 +45,12 @@ MX_MMA_MXF4NVF4_2X = 1
 MX_MMA_MXF4NVF4_4X = 2
 MX_CALIBRATE_MAX_STEPS = 1 << 20
 MX_BUILD_BOUNDS_CHECK = 1
+MX_LINEAR_MAX_TOKENS = 32
+MX_MOE_MAX_TOKENS = 64
+MX_MOE_MAX_EXPERTS = 512
+MX_MOE_MAX_TOP_K = 16
+MX_ACT_SILU = 0
+MX_ACT_GELU = 1
 
 _lock = threading.Lock()
 _lib = None
@@ -60,6 +66,19 @@ class mx_quantize_tensor(ctypes.Structure):
 class mx_gemm_epilogue(ctypes.Structure):
     """include/mxfp4.h: optional GEMM epilogue (bias FP32 [n], beta * D_in, GELU)."""
     _fields_ = [("bias", ctypes.c_void_p), ("beta", ctypes.c_float), ("gelu", ctypes.c_int)]
+
+
+class mx_moe_matrix(ctypes.Structure):
+    """include/mxfp4.h: one FP4 matrix of every expert, stacked."""
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("tensor_scales", ctypes.c_void_p)]
+
+
+class mx_moe_weights(ctypes.Structure):
+    """include/mxfp4.h: the experts of a layer (see moe_weights)."""
+    _fields_ = [("format", ctypes.c_int), ("activation", ctypes.c_int),
+                ("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64),
+                ("gate", mx_moe_matrix), ("up", mx_moe_matrix), ("down", mx_moe_matrix)]
 
 
 class MXError(RuntimeError):
@@ -129,6 +148,18 @@ def lib() -> ctypes.CDLL:
         L.mxfp4_gemm_static_workspace.restype = i32
         L.mxfp4_gemm_static_workspace.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, i32,
                                                   i32, vp]
+        L.mx_linear_bf16.restype = i32
+        L.mx_linear_bf16.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, i64, vp, i64, i32, ep, vp]
+        L.mx_moe_route_bf16.restype = i32
+        L.mx_moe_route_bf16.argtypes = [vp, i64, i64, i64, vp, i64, vp, i32, i32, vp, vp, vp]
+        L.mx_moe_workspace_bytes.restype = sz
+        L.mx_moe_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        mw = ctypes.POINTER(mx_moe_weights)
+        L.mx_moe_experts_bf16.restype = i32
+        L.mx_moe_experts_bf16.argtypes = [vp, i64, i64, vp, vp, i32, mw, vp, i64, vp, sz, vp]
+        L.mx_moe_layer_bf16.restype = i32
+        L.mx_moe_layer_bf16.argtypes = [vp, i64, i64, vp, vp, i32, i32, mw, vp, vp, vp, i64, vp, sz,
+                                        vp]
         L.mx_device_status.restype = i32
         L.mx_device_status.argtypes = [vp]
         L.mx_selftest_wait_timeout.restype = i32
@@ -321,6 +352,56 @@ def mxfp4_gemm_static_workspace(a_codes, a_scales, b_codes, b_scales, d, m, n, k
     return _check("mxfp4_gemm_static_workspace", lib().mxfp4_gemm_static_workspace(
         _ptr(a_codes), _ptr(a_scales), _ptr(b_codes), _ptr(b_scales), _ptr(d), m, n, k, layout,
         out_dtype, split_k, _stream(stream)))
+
+
+def mx_linear_bf16(x, tokens, k, ld_x, fmt, w_codes, w_scales, w_tensor_scale, n, y, ld_y,
+                   out_dtype=MX_OUT_BF16, bias=None, beta=0.0, gelu=False, stream=None):
+    """y = act(x W^T + beta * y_in + bias) for a few BF16 rows and an FP4 weight."""
+    return _check("mx_linear_bf16", lib().mx_linear_bf16(
+        _ptr(x), tokens, k, ld_x, fmt, _ptr(w_codes), _ptr(w_scales), _ptr(w_tensor_scale), n,
+        _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _stream(stream)))
+
+
+def mx_moe_route_bf16(x, tokens, hidden, ld_x, router, experts, bias, top_k, normalize, ids,
+                      weights, stream=None):
+    return _check("mx_moe_route_bf16", lib().mx_moe_route_bf16(
+        _ptr(x), tokens, hidden, ld_x, _ptr(router), experts, _ptr(bias), top_k, int(normalize),
+        _ptr(ids), _ptr(weights), _stream(stream)))
+
+
+def moe_weights(fmt, experts, hidden, inter, gate, up, down, activation=MX_ACT_SILU):
+    """The descriptor of a layer's experts: gate, up and down are (codes, scales,
+    tensor_scales) of the stacked matrices (tensor_scales None for MXFP4).  It is
+    made once and keeps the tensors alive."""
+    w = mx_moe_weights(fmt, activation, experts, hidden, inter,
+                       *(mx_moe_matrix(*(_ptr(t) for t in m)) for m in (gate, up, down)))
+    w.tensors = (gate, up, down)
+    return w
+
+
+def mx_moe_workspace_bytes(tokens: int, hidden: int, inter: int, top_k: int) -> int:
+    return lib().mx_moe_workspace_bytes(tokens, hidden, inter, top_k)
+
+
+def mx_moe_experts_bf16(x, tokens, ld_x, ids, weights, top_k, moe, y, ld_y, workspace=None,
+                        workspace_bytes=None, stream=None):
+    """moe: an mx_moe_weights (moe_weights)."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
+    return _check("mx_moe_experts_bf16", lib().mx_moe_experts_bf16(
+        _ptr(x), tokens, ld_x, _ptr(ids), _ptr(weights), top_k, moe, _ptr(y), ld_y,
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mx_moe_layer_bf16(x, tokens, ld_x, router, router_bias, top_k, normalize, moe, ids, weights, y,
+                      ld_y, workspace=None, workspace_bytes=None, stream=None):
+    """moe: an mx_moe_weights (moe_weights); ids and weights receive the router's choice."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
+    return _check("mx_moe_layer_bf16", lib().mx_moe_layer_bf16(
+        _ptr(x), tokens, ld_x, _ptr(router), _ptr(router_bias), top_k, int(normalize), moe,
+        _ptr(ids), _ptr(weights), _ptr(y), ld_y, _ptr(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def mx_device_status(stream=None) -> int:

@@ -869,6 +869,372 @@ MX_API int nvfp4_gemm_ex(const void *a_codes, const void *a_scales, const void *
                      epilogue, workspace, workspace_bytes, stream);
 }
 
+// ---- products of a few tokens
+
+namespace {
+
+Range span(const void *p, uint64_t bytes) {
+  const uintptr_t b = reinterpret_cast<uintptr_t>(p);
+  return p ? Range{b, b + static_cast<uintptr_t>(bytes)} : Range{0, 0};
+}
+
+// Bytes from the first to the last element of `rows` rows.
+uint64_t row_bytes(int64_t rows, int64_t cols, int64_t ld, uint64_t elem) {
+  return rows <= 0 ? 0 : static_cast<uint64_t>((rows - 1) * ld + cols) * elem;
+}
+
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// x of the few-token calls: BF16 [tokens, k].  `cols` names k in messages.
+int few_check_x(const char *fn, const void *x, int64_t tokens, int64_t max_tokens, int64_t k,
+                int64_t ld_x, const char *cols) {
+  if (!x) return fail(MX_ERR_INVALID_ARG, "%s: x is null", fn);
+  if (tokens < 0 || tokens > max_tokens)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: tokens = %lld (0..%lld)", fn,
+                static_cast<long long>(tokens), static_cast<long long>(max_tokens));
+  if (k <= 0 || k % 32 != 0 || k >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: %s = %lld (a positive multiple of 32 below 2^31)", fn,
+                cols, static_cast<long long>(k));
+  if (ld_x < k || ld_x >= (int64_t(1) << 40))
+    return fail(MX_ERR_INVALID_ARG, "%s: ld_x = %lld (>= %s = %lld, below 2^40)", fn,
+                static_cast<long long>(ld_x), cols, static_cast<long long>(k));
+  if (!aligned16(x) || ld_x % 8 != 0)
+    return fail(MX_ERR_ALIGNMENT, "%s: %s", fn,
+                !aligned16(x) ? "x is not 16-byte aligned"
+                              : "ld_x is not a multiple of 8 elements (16 bytes)");
+  return MX_OK;
+}
+
+// A stack of `count` FP4 matrices [rows, k] (rows, k already checked).
+int few_check_matrix(const char *fn, const char *name, int format, const void *codes,
+                     const void *scales, const float *ts, int64_t rows, int64_t k) {
+  if (!codes || !scales)
+    return fail(MX_ERR_INVALID_ARG, "%s: %s %s is null", fn, name, !codes ? "codes" : "scales");
+  if ((format == MX_FMT_NVFP4) != (ts != nullptr))
+    return fail(MX_ERR_INVALID_ARG, "%s: %s tensor scale %s", fn, name,
+                ts ? "must be null for MXFP4" : "is null (NVFP4 needs it)");
+  if (!aligned16(codes) || !aligned16(scales) || !aligned4(ts))
+    return fail(MX_ERR_ALIGNMENT, "%s: %s %s", fn, name,
+                !aligned16(codes) ? "codes are not 16-byte aligned"
+                : !aligned16(scales) ? "scales are not 16-byte aligned"
+                                     : "tensor scale is not 4-byte aligned");
+  if ((rows + 127) / 128 * 128 * (k / block_of(format)) >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: %s [%lld, %lld] has 2^31 or more scale blocks", fn,
+                name, static_cast<long long>(rows), static_cast<long long>(k));
+  return MX_OK;
+}
+
+// The ranges of a stack of matrices: codes, scales, tensor scales.
+void matrix_ranges(const mx::FewMatrix &m, int format, int64_t count, int64_t rows, int64_t k,
+                   Range *out) {
+  out[0] = span(m.codes, static_cast<uint64_t>(count) * static_cast<uint64_t>(rows * (k / 2)));
+  out[1] = span(m.scales, static_cast<uint64_t>(count) *
+                              mx_scale_bytes(rows, k, format, MX_SCALE_TCGEN05));
+  out[2] = span(m.ts, static_cast<uint64_t>(count) * sizeof(float));
+}
+
+// No output overlaps an input or another output.
+int check_disjoint(const char *fn, const Range *out, int nout, const Range *in, int nin) {
+  for (int o = 0; o < nout; ++o) {
+    for (int i = 0; i < nin; ++i)
+      if (overlap(out[o], in[i]))
+        return fail(MX_ERR_INVALID_ARG, "%s: an output or the workspace overlaps an input", fn);
+    for (int p = o + 1; p < nout; ++p)
+      if (overlap(out[o], out[p]))
+        return fail(MX_ERR_INVALID_ARG, "%s: two outputs (or an output and the workspace) overlap",
+                    fn);
+  }
+  return MX_OK;
+}
+
+static_assert(MX_LINEAR_MAX_TOKENS == mx::kLinearMaxTokens, "few-token limits");
+static_assert(MX_MOE_MAX_TOKENS == mx::kMoeMaxTokens && MX_MOE_MAX_EXPERTS == mx::kMoeMaxExperts &&
+                  MX_MOE_MAX_TOP_K == mx::kMoeMaxTopK,
+              "few-token limits");
+
+constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+size_t moe_h_bytes(int64_t pairs, int64_t inter) {
+  return round256(static_cast<size_t>(pairs) * static_cast<size_t>(inter) * sizeof(float));
+}
+size_t moe_z_bytes(int64_t pairs, int64_t hidden) {
+  return round256(static_cast<size_t>(pairs) * static_cast<size_t>(hidden) * sizeof(float));
+}
+size_t moe_counter_bytes(int64_t hidden) {
+  return round256(static_cast<size_t>((hidden + mx::kMoeCounterRows - 1) / mx::kMoeCounterRows) *
+                  sizeof(uint32_t));
+}
+
+int route_check(const char *fn, const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,
+                const void *router, int64_t experts, const float *bias, int top_k, int normalize,
+                const int32_t *ids, const float *weights) {
+  const int rc = few_check_x(fn, x, tokens, MX_MOE_MAX_TOKENS, hidden, ld_x, "hidden");
+  if (rc != MX_OK) return rc;
+  if (!router || !ids || !weights)
+    return fail(MX_ERR_INVALID_ARG, "%s: %s is null", fn,
+                !router ? "router" : !ids ? "ids" : "weights");
+  if (normalize != 0 && normalize != 1)
+    return fail(MX_ERR_INVALID_ARG, "%s: normalize = %d (0 or 1)", fn, normalize);
+  if (experts < 1 || experts > MX_MOE_MAX_EXPERTS)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: experts = %lld (1..%d)", fn,
+                static_cast<long long>(experts), MX_MOE_MAX_EXPERTS);
+  if (top_k < 1 || top_k > MX_MOE_MAX_TOP_K || top_k > experts)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: top_k = %d (1..%d and at most %lld experts)", fn,
+                top_k, MX_MOE_MAX_TOP_K, static_cast<long long>(experts));
+  if (!aligned16(router)) return fail(MX_ERR_ALIGNMENT, "%s: router is not 16-byte aligned", fn);
+  if (!aligned4(bias) || !aligned4(ids) || !aligned4(weights))
+    return fail(MX_ERR_ALIGNMENT, "%s: %s is not 4-byte aligned", fn,
+                !aligned4(bias) ? "bias" : !aligned4(ids) ? "ids" : "weights");
+  const Range in[3] = {span(x, row_bytes(tokens, hidden, ld_x, 2)),
+                       span(router, static_cast<uint64_t>(experts * hidden) * 2),
+                       span(bias, static_cast<uint64_t>(experts) * 4)};
+  const uint64_t slots = static_cast<uint64_t>(tokens) * static_cast<uint64_t>(top_k) * 4;
+  const Range out[2] = {span(ids, slots), span(weights, slots)};
+  return check_disjoint(fn, out, 2, in, 3);
+}
+
+mx::FewMatrix few_matrix(const mx_moe_matrix &m) {
+  return mx::FewMatrix{static_cast<const uint8_t *>(m.codes), static_cast<const uint8_t *>(m.scales),
+                       m.tensor_scales};
+}
+
+// Checks of the experts' part of a call; fills its launch arguments.
+int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
+                  const float *weights, int top_k, const mx_moe_weights *moe, const void *y,
+                  int64_t ld_y, const void *workspace, size_t workspace_bytes, mx::MoeArgs *a) {
+  if (!moe) return fail(MX_ERR_INVALID_ARG, "%s: the experts' descriptor is null", fn);
+  if (!valid_format(moe->format))
+    return fail(MX_ERR_INVALID_ARG, "%s: format %d (MX_FMT_MXFP4 = 0 or MX_FMT_NVFP4 = 1)", fn,
+                moe->format);
+  if (moe->activation != MX_ACT_SILU && moe->activation != MX_ACT_GELU)
+    return fail(MX_ERR_INVALID_ARG, "%s: activation %d (MX_ACT_SILU = 0 or MX_ACT_GELU = 1)", fn,
+                moe->activation);
+  int rc = few_check_x(fn, x, tokens, MX_MOE_MAX_TOKENS, moe->hidden, ld_x, "hidden");
+  if (rc != MX_OK) return rc;
+  if (!ids || !weights || !y)
+    return fail(MX_ERR_INVALID_ARG, "%s: %s is null", fn, !ids ? "ids" : !weights ? "weights" : "y");
+  if (moe->inter <= 0 || moe->inter % 32 != 0 || moe->inter >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: inter = %lld (a positive multiple of 32 below 2^31)",
+                fn, static_cast<long long>(moe->inter));
+  if (moe->experts < 1 || moe->experts > MX_MOE_MAX_EXPERTS)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: experts = %lld (1..%d)", fn,
+                static_cast<long long>(moe->experts), MX_MOE_MAX_EXPERTS);
+  if (top_k < 1 || top_k > MX_MOE_MAX_TOP_K)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: top_k = %d (1..%d)", fn, top_k, MX_MOE_MAX_TOP_K);
+  if (ld_y < moe->hidden || ld_y >= (int64_t(1) << 40))
+    return fail(MX_ERR_INVALID_ARG, "%s: ld_y = %lld (>= hidden = %lld, below 2^40)", fn,
+                static_cast<long long>(ld_y), static_cast<long long>(moe->hidden));
+  const struct {
+    const char *name;
+    const mx_moe_matrix *m;
+    int64_t rows, k;
+  } mats[3] = {{"gate", &moe->gate, moe->inter, moe->hidden},
+               {"up", &moe->up, moe->inter, moe->hidden},
+               {"down", &moe->down, moe->hidden, moe->inter}};
+  for (const auto &m : mats) {
+    rc = few_check_matrix(fn, m.name, moe->format, m.m->codes, m.m->scales, m.m->tensor_scales,
+                          m.rows, m.k);
+    if (rc != MX_OK) return rc;
+  }
+  if (!aligned16(y) || !aligned4(ids) || !aligned4(weights))
+    return fail(MX_ERR_ALIGNMENT, "%s: %s", fn,
+                !aligned16(y) ? "y is not 16-byte aligned"
+                : !aligned4(ids) ? "ids is not 4-byte aligned" : "weights is not 4-byte aligned");
+  const size_t need = mx_moe_workspace_bytes(tokens, moe->hidden, moe->inter, top_k);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(MX_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes, got %zu%s", fn, need,
+                  workspace ? workspace_bytes : size_t(0), workspace ? "" : " (null)");
+    if (!aligned16(workspace))
+      return fail(MX_ERR_ALIGNMENT, "%s: workspace is not 16-byte aligned", fn);
+  }
+  *a = mx::MoeArgs{};
+  a->x = x;
+  a->ld_x = ld_x;
+  a->tokens = static_cast<int>(tokens);
+  a->top_k = top_k;
+  a->experts = static_cast<int>(moe->experts);
+  a->hidden = static_cast<int>(moe->hidden);
+  a->inter = static_cast<int>(moe->inter);
+  a->fmt = moe->format == MX_FMT_MXFP4 ? 0 : 1;
+  a->gelu = moe->activation == MX_ACT_GELU;
+  a->ids = ids;
+  a->weights = weights;
+  a->gate = few_matrix(moe->gate);
+  a->up = few_matrix(moe->up);
+  a->down = few_matrix(moe->down);
+  a->y = const_cast<void *>(y);
+  a->ld_y = ld_y;
+  const int64_t pairs = tokens * top_k;
+  char *ws = static_cast<char *>(const_cast<void *>(workspace));
+  a->h = reinterpret_cast<float *>(ws);
+  a->z = reinterpret_cast<float *>(ws + moe_h_bytes(pairs, moe->inter));
+  a->counters = reinterpret_cast<uint32_t *>(ws + moe_h_bytes(pairs, moe->inter) +
+                                             moe_z_bytes(pairs, moe->hidden));
+  Range in[12];
+  in[0] = span(x, row_bytes(tokens, moe->hidden, ld_x, 2));
+  in[1] = span(ids, static_cast<uint64_t>(pairs) * 4);
+  in[2] = span(weights, static_cast<uint64_t>(pairs) * 4);
+  matrix_ranges(a->gate, moe->format, moe->experts, moe->inter, moe->hidden, in + 3);
+  matrix_ranges(a->up, moe->format, moe->experts, moe->inter, moe->hidden, in + 6);
+  matrix_ranges(a->down, moe->format, moe->experts, moe->hidden, moe->inter, in + 9);
+  const Range out[2] = {span(y, row_bytes(tokens, moe->hidden, ld_y, 2)), span(workspace, need)};
+  return check_disjoint(fn, out, 2, in, 12);
+}
+
+}  // namespace
+
+MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
+                          const void *w_codes, const void *w_scales, const float *w_tensor_scale,
+                          int64_t n, void *y, int64_t ld_y, int out_dtype,
+                          const mx_gemm_epilogue *epilogue, void *stream) {
+  clear_detail();
+  const char *fn = "mx_linear_bf16";
+  if (!valid_format(format))
+    return fail(MX_ERR_INVALID_ARG, "%s: format %d (MX_FMT_MXFP4 = 0 or MX_FMT_NVFP4 = 1)", fn,
+                format);
+  int rc = few_check_x(fn, x, tokens, MX_LINEAR_MAX_TOKENS, k, ld_x, "k");
+  if (rc != MX_OK) return rc;
+  if (!y) return fail(MX_ERR_INVALID_ARG, "%s: y is null", fn);
+  if (n <= 0 || n % 32 != 0 || n >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: n = %lld (a positive multiple of 32 below 2^31)", fn,
+                static_cast<long long>(n));
+  rc = few_check_matrix(fn, "weight", format, w_codes, w_scales, w_tensor_scale, n, k);
+  if (rc != MX_OK) return rc;
+  if (out_dtype != MX_OUT_BF16 && out_dtype != MX_OUT_FP32)
+    return fail(MX_ERR_UNSUPPORTED_FEATURE, "%s: out_dtype %d (MX_OUT_BF16 = 0 or MX_OUT_FP32 = 1)",
+                fn, out_dtype);
+  if (ld_y < n || ld_y >= (int64_t(1) << 40))
+    return fail(MX_ERR_INVALID_ARG, "%s: ld_y = %lld (>= n = %lld, below 2^40)", fn,
+                static_cast<long long>(ld_y), static_cast<long long>(n));
+  if (!aligned16(y)) return fail(MX_ERR_ALIGNMENT, "%s: y is not 16-byte aligned", fn);
+  if (epilogue && epilogue->gelu != 0 && epilogue->gelu != 1)
+    return fail(MX_ERR_INVALID_ARG, "%s: epilogue gelu = %d (0 or 1)", fn, epilogue->gelu);
+  if (epilogue && epilogue->bias && !aligned16(epilogue->bias))
+    return fail(MX_ERR_ALIGNMENT, "%s: bias is not 16-byte aligned", fn);
+  mx::LinearArgs a{};
+  a.x = x;
+  a.ld_x = ld_x;
+  a.tokens = static_cast<int>(tokens);
+  a.n = n;
+  a.k = k;
+  a.fmt = format == MX_FMT_MXFP4 ? 0 : 1;
+  a.w = mx::FewMatrix{static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales),
+                      w_tensor_scale};
+  a.y = y;
+  a.ld_y = ld_y;
+  a.out_fp32 = out_dtype == MX_OUT_FP32;
+  if (epilogue) {
+    a.bias = epilogue->bias;
+    a.beta = epilogue->beta;
+    a.gelu = epilogue->gelu;
+  }
+  Range in[5];
+  in[0] = span(x, row_bytes(tokens, k, ld_x, 2));
+  in[1] = span(a.bias, static_cast<uint64_t>(n) * sizeof(float));
+  matrix_ranges(a.w, format, 1, n, k, in + 2);
+  const Range out[1] = {span(y, row_bytes(tokens, n, ld_y, a.out_fp32 ? 4 : 2))};
+  rc = check_disjoint(fn, out, 1, in, 5);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0) return MX_OK;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  return launch_rc(fn, mx::launch_linear(a, static_cast<cudaStream_t>(stream)));
+}
+
+MX_API int mx_moe_route_bf16(const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,
+                             const void *router, int64_t experts, const float *bias, int top_k,
+                             int normalize, int32_t *ids, float *weights, void *stream) {
+  clear_detail();
+  const char *fn = "mx_moe_route_bf16";
+  int rc = route_check(fn, x, tokens, hidden, ld_x, router, experts, bias, top_k, normalize, ids,
+                       weights);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0) return MX_OK;
+  const mx::RouteArgs a{x,     ld_x,  static_cast<int>(tokens), static_cast<int>(hidden),
+                        static_cast<int>(experts), top_k, normalize, router, bias, ids, weights,
+                        dev->status};
+  return launch_rc(fn, mx::launch_moe_route(a, static_cast<cudaStream_t>(stream)));
+}
+
+MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k) {
+  if (tokens < 1 || tokens > MX_MOE_MAX_TOKENS || top_k < 1 || top_k > MX_MOE_MAX_TOP_K ||
+      hidden <= 0 || inter <= 0 || hidden >= (int64_t(1) << 31) || inter >= (int64_t(1) << 31))
+    return 0;
+  const int64_t pairs = tokens * top_k;
+  return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) + moe_counter_bytes(hidden);
+}
+
+MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
+                               const float *weights, int top_k, const mx_moe_weights *moe, void *y,
+                               int64_t ld_y, void *workspace, size_t workspace_bytes,
+                               void *stream) {
+  clear_detail();
+  const char *fn = "mx_moe_experts_bf16";
+  mx::MoeArgs a;
+  int rc = experts_check(fn, x, tokens, ld_x, ids, weights, top_k, moe, y, ld_y, workspace,
+                         workspace_bytes, &a);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0) return MX_OK;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  return launch_rc(fn, mx::launch_moe_experts(a, static_cast<cudaStream_t>(stream)));
+}
+
+MX_API int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const void *router,
+                             const float *router_bias, int top_k, int normalize,
+                             const mx_moe_weights *moe, int32_t *ids, float *weights, void *y,
+                             int64_t ld_y, void *workspace, size_t workspace_bytes,
+                             void *stream) {
+  clear_detail();
+  const char *fn = "mx_moe_layer_bf16";
+  mx::MoeArgs a;
+  int rc = experts_check(fn, x, tokens, ld_x, ids, weights, top_k, moe, y, ld_y, workspace,
+                         workspace_bytes, &a);
+  if (rc != MX_OK) return rc;
+  rc = route_check(fn, x, tokens, moe->hidden, ld_x, router, moe->experts, router_bias, top_k,
+                   normalize, ids, weights);
+  if (rc != MX_OK) return rc;
+  {
+    // what the router reads and writes against the experts' inputs and outputs
+    const uint64_t slots = static_cast<uint64_t>(tokens) * static_cast<uint64_t>(top_k) * 4;
+    const Range choice[2] = {span(ids, slots), span(weights, slots)};
+    Range fixed[9];
+    matrix_ranges(a.gate, moe->format, moe->experts, moe->inter, moe->hidden, fixed);
+    matrix_ranges(a.up, moe->format, moe->experts, moe->inter, moe->hidden, fixed + 3);
+    matrix_ranges(a.down, moe->format, moe->experts, moe->hidden, moe->inter, fixed + 6);
+    rc = check_disjoint(fn, choice, 2, fixed, 9);
+    if (rc != MX_OK) return rc;
+    const Range gate_in[2] = {span(router, static_cast<uint64_t>(moe->experts * moe->hidden) * 2),
+                              span(router_bias, static_cast<uint64_t>(moe->experts) * 4)};
+    const Range out[2] = {span(y, row_bytes(tokens, moe->hidden, ld_y, 2)),
+                          span(workspace, mx_moe_workspace_bytes(tokens, moe->hidden, moe->inter,
+                                                                 top_k))};
+    rc = check_disjoint(fn, out, 2, gate_in, 2);
+    if (rc != MX_OK) return rc;
+  }
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0) return MX_OK;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  const mx::RouteArgs r{x,      ld_x,        a.tokens, a.hidden, a.experts, top_k, normalize,
+                        router, router_bias, ids,      weights,  dev->status};
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = mx::launch_moe_route(r, s);
+  return launch_rc(fn, e != cudaSuccess ? e : mx::launch_moe_experts(a, s));
+}
+
 MX_API int mx_device_status(void *stream) {
   clear_detail();
   DeviceInfo *dev = nullptr;

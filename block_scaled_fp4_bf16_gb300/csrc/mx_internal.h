@@ -178,6 +178,68 @@ int gemm_static_workspace_call(const void *a_codes, const void *a_scales, const 
 cudaError_t launch_calibrate_mma(int form, int pair, int64_t steps, unsigned long long *cycles,
                                  uint32_t *status, int num_sms, cudaStream_t s, int *units);
 
+// A stack of FP4 matrices [rows, k]: packed codes and tcgen05-order scales of
+// each expert one after the other (one matrix for mx_linear_bf16).
+struct FewMatrix {
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const float *ts;  // NVFP4: one per matrix; MXFP4: null
+};
+
+// y[t, n] = epilogue(sum_k x[t, k] W[n, k]) for tokens <= kLinearMaxTokens.
+constexpr int kLinearMaxTokens = 32;
+struct LinearArgs {
+  const void *x;
+  int64_t ld_x;
+  int tokens;
+  int64_t n, k;
+  int fmt;  // 0 MXFP4, 1 NVFP4
+  FewMatrix w;
+  void *y;
+  int64_t ld_y;
+  int out_fp32;
+  const float *bias;
+  float beta;
+  int gelu;
+  int num_sms;
+  uint32_t *status;
+};
+cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s);
+
+constexpr int kMoeMaxTokens = 64;
+constexpr int kMoeMaxExperts = 512;
+constexpr int kMoeMaxTopK = 16;
+struct RouteArgs {
+  const void *x;
+  int64_t ld_x;
+  int tokens, hidden, experts, top_k, normalize;
+  const void *router;
+  const float *bias;
+  int32_t *ids;
+  float *weights;
+  uint32_t *status;
+};
+cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s);
+
+struct MoeArgs {
+  const void *x;
+  int64_t ld_x;
+  int tokens, top_k, experts, hidden, inter;
+  int fmt, gelu;
+  const int32_t *ids;
+  const float *weights;
+  FewMatrix gate, up, down;
+  void *y;
+  int64_t ld_y;
+  float *h;            // [tokens * top_k, inter]
+  float *z;            // [tokens * top_k, hidden]
+  uint32_t *counters;  // one per kMoeCounterRows rows of hidden
+  int num_sms;
+  uint32_t *status;
+};
+constexpr int kMoeCounterRows = 32;
+cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
+
 // Launch with programmatic stream serialization (the kernel itself orders
 // its global-memory accesses after its predecessor with griddep_wait).
 template <typename... KArgs, typename... Args>

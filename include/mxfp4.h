@@ -375,6 +375,112 @@ int nvfp4_gemm_ex(const void *a_codes, const void *a_scales, const void *b_codes
                   const mx_gemm_epilogue *epilogue, void *workspace, size_t workspace_bytes,
                   void *stream);
 
+/* ---- products of a few tokens ---------------------------------------------
+ * The GEMMs above quantize both operands and take their rows in multiples of
+ * 32.  Decoding has one to a few dozen rows: there the weights' bytes are the
+ * whole cost, and the activations can stay BF16.  The calls below multiply a
+ * few BF16 rows by the same FP4 weights (codes and MX_SCALE_TCGEN05 scales, as
+ * mx_quantize_bf16 writes them and the GEMMs read them).  The pages have no
+ * counterpart; they are this library's own addition.
+ *
+ * Numerics.  A weight is code * block scale (* tensor scale), each factor
+ * exact.  An activation enters the products as FP16 times one power of two for
+ * each (token, 128 consecutive elements): a BF16 value is held exactly unless
+ * it is below 2^-31 of the largest of its 128, and then to within 2^-40 of
+ * that largest.  Sums are binary32.  Infinities and NaN in x reach the outputs
+ * of their token.  A UE8M0 scale byte of 255 is NaN. */
+
+/* Most rows of x that mx_linear_bf16 takes. */
+#define MX_LINEAR_MAX_TOKENS 32
+
+/* y[t, n] = act(sum_k x[t, k] W[n, k] + beta * y_in[t, n] + bias[n]), t < tokens.
+ *   x:  BF16 [tokens, k], row stride ld_x elements (ld_x >= k, ld_x % 8 == 0);
+ *   w_codes [n, k / 2], w_scales: MX_SCALE_TCGEN05 order; w_tensor_scale: one
+ *       device float for NVFP4, NULL for MXFP4;
+ *   y:  out [tokens, n], row stride ld_y elements (ld_y >= n), BF16 or FP32;
+ *   epilogue: as for mxfp4_gemm_ex (NULL: none; beta * y_in reads y);
+ *   tokens 0..MX_LINEAR_MAX_TOKENS (0 launches nothing), k % 32 == 0,
+ *   n % 32 == 0.  y must not overlap an input (MX_ERR_INVALID_ARG).
+ * Launches one kernel and needs no workspace. */
+int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
+                   const void *w_codes, const void *w_scales, const float *w_tensor_scale,
+                   int64_t n, void *y, int64_t ld_y, int out_dtype,
+                   const mx_gemm_epilogue *epilogue, void *stream);
+
+/* ---- mixture of experts, a few tokens ----------------------------------- */
+#define MX_MOE_MAX_TOKENS 64
+#define MX_MOE_MAX_EXPERTS 512
+#define MX_MOE_MAX_TOP_K 16
+
+#define MX_ACT_SILU 0 /* g / (1 + exp(-g)) */
+#define MX_ACT_GELU 1 /* g Phi(g)          */
+
+/* The router.  logits[t, e] = sum_h x[t, h] R[e, h] + bias[e] in binary32; for
+ * each token the top_k experts by descending logit (equal logits: the lowest
+ * index first; NaN ranks above every number), written to ids[t, 0..top_k-1];
+ * weights[t, j] = exp(l_j) / sum exp(l), the sum over the chosen experts when
+ * normalize is 1 and over all experts when it is 0.  An expert whose logit is
+ * -inf (a bias of -inf switches it off) is never chosen: a slot that is left
+ * over gets id -1 and weight 0.
+ *   x: BF16 [tokens, hidden], row stride ld_x (>= hidden, % 8 == 0);
+ *   router: BF16 [experts, hidden], packed; bias: device FP32 [experts] or NULL;
+ *   ids: out int32 [tokens, top_k]; weights: out FP32 [tokens, top_k];
+ *   hidden % 32 == 0, experts 1..MX_MOE_MAX_EXPERTS, top_k 1..MX_MOE_MAX_TOP_K
+ *   and <= experts, tokens 0..MX_MOE_MAX_TOKENS.
+ * The outputs must not overlap an input or each other.  Launches one kernel. */
+int mx_moe_route_bf16(const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,
+                      const void *router, int64_t experts, const float *bias, int top_k,
+                      int normalize, int32_t *ids, float *weights, void *stream);
+
+/* One matrix of every expert, stacked: expert e's codes start at
+ * e * rows * k / 2 bytes, its scales (MX_SCALE_TCGEN05) at
+ * e * mx_scale_bytes(rows, k, format, MX_SCALE_TCGEN05). */
+typedef struct mx_moe_matrix {
+  const void *codes;
+  const void *scales;
+  const float *tensor_scales; /* NVFP4: device FP32 [experts]; MXFP4: NULL */
+} mx_moe_matrix;
+
+/* The experts of a layer (host memory, read before a call returns). */
+typedef struct mx_moe_weights {
+  int format;     /* MX_FMT_MXFP4 or MX_FMT_NVFP4 */
+  int activation; /* MX_ACT_SILU or MX_ACT_GELU   */
+  int64_t experts, hidden, inter;
+  mx_moe_matrix gate; /* per expert [inter, hidden] */
+  mx_moe_matrix up;   /* per expert [inter, hidden] */
+  mx_moe_matrix down; /* per expert [hidden, inter] */
+} mx_moe_weights;
+
+/* Workspace bytes of the two calls below: the hidden values and the weighted
+ * outputs of every (token, slot) pair in binary32, and counters.  0 for
+ * invalid arguments.  Nothing in it needs to start at any value. */
+size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k);
+
+/* y[t] = sum_j weights[t, j] D_e (act(G_e x_t) * U_e x_t), e = ids[t, j].
+ * A slot whose id is outside 0..experts-1 adds nothing (a token with no other
+ * slots gets 0); an expert may come more than once.  The slots of a token are
+ * added in their order.
+ *   x: BF16 [tokens, hidden], row stride ld_x (>= hidden, % 8 == 0);
+ *   ids int32, weights FP32 [tokens, top_k] (device, 4-byte aligned);
+ *   y: out BF16 [tokens, hidden], row stride ld_y (>= hidden);
+ *   hidden % 32 == 0, inter % 32 == 0; tokens 0..MX_MOE_MAX_TOKENS;
+ *   workspace: mx_moe_workspace_bytes(...) bytes, 16-byte aligned.
+ * The hidden values act(G x) * U x are kept in binary32 and enter the second
+ * product as FP16 times a power of two for each 128 (a rounding of 2^-12,
+ * an eighth of the output's own).  y and the workspace must not overlap an
+ * input or each other.  Launches two kernels and reads the chosen experts'
+ * weights only. */
+int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
+                        const float *weights, int top_k, const mx_moe_weights *moe, void *y,
+                        int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The whole layer: mx_moe_route_bf16 into ids and weights (outputs), then
+ * mx_moe_experts_bf16 of that choice.  Launches three kernels. */
+int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const void *router,
+                      const float *router_bias, int top_k, int normalize,
+                      const mx_moe_weights *moe, int32_t *ids, float *weights, void *y,
+                      int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Size of the fixed device scratch array of mxfp4_gemm_static_workspace. */
 #define MX_STATIC_WORKSPACE_BYTES (16u << 20) /* 16 MiB */
 
