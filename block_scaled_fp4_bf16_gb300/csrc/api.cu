@@ -1019,6 +1019,9 @@ int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, c
   if (moe->experts < 1 || moe->experts > MX_MOE_MAX_EXPERTS)
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: experts = %lld (1..%d)", fn,
                 static_cast<long long>(moe->experts), MX_MOE_MAX_EXPERTS);
+  if (moe->experts * moe->hidden >= (int64_t(1) << 31) ||
+      moe->experts * moe->inter >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: a stack of 2^31 or more rows", fn);
   if (top_k < 1 || top_k > MX_MOE_MAX_TOP_K)
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: top_k = %d (1..%d)", fn, top_k, MX_MOE_MAX_TOP_K);
   if (ld_y < moe->hidden || ld_y >= (int64_t(1) << 40))
@@ -1315,6 +1318,18 @@ struct SetupRecord {
 std::mutex g_setup_mutex;
 std::vector<SetupRecord> g_setup;  // one per kernel instance and context: a few dozen
 }  // namespace
+
+bool encode_few_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k / 2), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k / 2)};
+  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1u, 1u};
+  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 bool kernel_setup_get(const void *func, int *value) {
   const CUcontext ctx = current_context();

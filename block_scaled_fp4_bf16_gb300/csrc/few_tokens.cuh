@@ -5,10 +5,10 @@
 // tokens.  The weights' bytes bound it (4.25 or 4.5 bits each; at 6.8 TB/s an
 // SM has to take 45 codes a clock), so the kernel is built to keep weight
 // copies in flight and to spend few instructions on a code:
-//   - a warp owns a range of K and walks it in stages of 128: codes, scales and
-//     activations of a stage come by cp.async into the warp's own ring in shared
-//     memory, and run on over the end of one tile into the next; warps meet
-//     only to add their partial sums;
+//   - a warp owns a range of K and walks it in stages of 128: codes come by one
+//     TMA copy, scales and activations by bulk copies, into the warp's own ring
+//     in shared memory, and run on over the end of one tile into the next;
+//     warps meet only to add their partial sums;
 //   - E2M1 becomes FP16 by the conversion instruction, two codes at once, and
 //     multiplies on the 16 x 8 x 16 FP16 product with binary32 sums, the
 //     weights on its 16-row side (measured: 90 codes a clock per SM converted,
@@ -19,6 +19,8 @@
 //   - activations become FP16 times a power of two for each (token, 128): BF16
 //     values keep all their bits unless they lie 2^-31 below the largest of the
 //     128.
+// What bounds the arithmetic is the integer pipe (two instructions a clock per
+// SM), where the conversions run: half an instruction a code.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -31,50 +33,18 @@ namespace few {
 
 constexpr int kStageK = 128;  // K elements of a stage
 
-// Bytes of a token's row in a stage, padded so that a quarter warp's 16-byte
-// reads (two tokens) fall on distinct banks.
-template <typename XT>
-constexpr int x_pitch() {
-  return sizeof(XT) == 2 ? 256 + 64 : 512 + 16;
-}
+// Bytes of a stage's scales: 512-byte tiles of 128 rows, one (MXFP4) or two
+// (NVFP4) for each of the SEGS runs of rows.
+template <int FMT, int SEGS>
+constexpr int kScaleBytes = (FMT == 0 ? 512 : 1024) * SEGS;
 
-// A multiple of 64: stage_product steps between chunks by flipping address bits.
-template <int FMT, int MT, typename XT>
-__host__ __device__ constexpr int stage_bytes(int tokens) {
-  return (16 * MT * (64 + (FMT == 0 ? 4 : 8)) + tokens * x_pitch<XT>() + 63) / 64 * 64;
-}
+// Codes and scales; a multiple of 512 (the period of the codes' 64-byte swizzle).
+template <int FMT, int MT, int SEGS>
+constexpr int kStageBytes = 16 * MT * 64 + kScaleBytes<FMT, SEGS>;
 
-// One matrix of a stack: codes, scales and their extents (of the whole stack,
-// for the bounds-checked build).
-struct Rows {
-  const uint8_t *codes;
-  const uint8_t *scales;
-  int64_t code_off, scale_off;    // of this matrix in the stack
-  int64_t code_end, scale_end;    // extents of the stack
-};
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *base, int64_t off, bool valid,
-                                           int64_t extent, uint32_t *status) {
-  valid = valid && in_bounds(off, 16, extent, status);
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst),
-               "l"(static_cast<const char *>(base) + (valid ? off : 0)), "r"(valid ? 16 : 0)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *base, int64_t off, bool valid,
-                                          int64_t extent, uint32_t *status) {
-  valid = valid && in_bounds(off, 4, extent, status);
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst),
-               "l"(static_cast<const char *>(base) + (valid ? off : 0)), "r"(valid ? 4 : 0)
-               : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+// Bytes of a warp's decoded scales: four FP32 (MXFP4) or eight FP16 pairs a row.
+template <int FMT, int MT>
+constexpr int kDecodedBytes = 16 * MT * (FMT == 0 ? 16 : 32);
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -96,6 +66,12 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
   uint2 v;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
   return v;
+}
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
 }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
@@ -141,11 +117,6 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -154,238 +125,436 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
 
 // ---------------------------------------------------------------- copies in
 
-// Copies the codes and scales of stage `s` of R = 16 MT rows into `dst`.  The
-// rows are two halves of 8 MT that begin at row first[0] of m[0] and first[1] of
-// m[1] (the same matrix, 8 MT apart, unless the tile holds gate and up rows);
-// rows at or past n and K blocks at or past k become zeros.
-template <int FMT, int MT>
-__device__ __forceinline__ void load_weights(uint32_t dst, const Rows (&m)[2], const int (&first)[2],
-                                             int n, int k, int s, uint32_t *status) {
-  constexpr int R = 16 * MT, kHalf = R / 2;
-  const int lane = threadIdx.x & 31;
-  // codes: 64 bytes of a row in four 16-byte chunks (one 32-block each), chunk c
-  // of row r at c ^ (r / 2 % 4): ldmatrix then reads without bank conflicts
-  const int chunk = lane & 3, row0 = lane >> 2;
-  const int64_t ldb = k >> 1;
-  const bool k_in = s * kStageK + chunk * 32 < k;
-#pragma unroll
-  for (int j = 0; j < R / 8; ++j) {
-    const int h = j * 8 >= kHalf ? 1 : 0;
-    const int row = row0 + j * 8;
-    const int at = first[h] + row - h * kHalf;
-    cp_async16(dst + row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4), m[h].codes,
-               m[h].code_off + at * ldb + (s * 64 + chunk * 16), k_in && at < n, m[h].code_end,
-               status);
-  }
-  // scales: the four (MXFP4) or eight bytes of a row, one tile column each word
-  constexpr int kCols = FMT == 0 ? 1 : 2;
-  const int tiles = (k / (FMT == 0 ? 32 : 16) + 3) >> 2;
-  const uint32_t sdst = dst + R * 64;
-#pragma unroll
-  for (int i0 = 0; i0 < R * kCols; i0 += 32) {
-    const int i = i0 + lane;
-    const int row = i % R, q = i / R;
-    if (i < R * kCols) {
-      const bool h = row >= kHalf;
-      const int at = h ? first[1] + row - kHalf : first[0] + row, col = s * kCols + q;
-      const int64_t off = (h ? m[1].scale_off : m[0].scale_off) +
-                          (static_cast<int64_t>(at >> 7) * tiles + col) * 512 + (at & 31) * 16 +
-                          ((at >> 5) & 3) * 4;
-      cp_async4(sdst + row * (4 * kCols) + q * 4, h ? m[1].scales : m[0].scales, off,
-                col < tiles && at < n, h ? m[1].scale_end : m[0].scale_end, status);
-    }
-  }
-}
+// One run of rows of a stage: the codes' map (rows of the whole stack), its
+// first row there, and the scales of its matrix.
+struct Run {
+  const CUtensorMap *codes;
+  int code_row;            // first row in the map
+  const uint8_t *scales;   // of this matrix
+  int row;                 // first row in this matrix
+  int64_t scale_end;       // bytes of its scales
+};
 
-// Copies stage `s` of `count` rows of x (row r of the stage at offset
-// row_off(r), in elements) into `dst`.
-template <typename XT, typename RowOff>
-__device__ __forceinline__ void load_x(uint32_t dst, const void *x, int64_t extent, int count, int k,
-                                       int s, const RowOff &row_off, uint32_t *status) {
-  constexpr int kChunk = 16 / sizeof(XT), kChunks = kStageK / kChunk;
-  const int lane = threadIdx.x & 31;
-  for (int i = lane; i < count * kChunks; i += 32) {
-    const int r = i / kChunks, c = i % kChunks;
-    const int64_t at = row_off(r) + s * kStageK + c * kChunk;
-    cp_async16(dst + r * x_pitch<XT>() + c * 16, x, at * static_cast<int64_t>(sizeof(XT)),
-               s * kStageK + c * kChunk < k, extent, status);
+// A warp's ring of stages, each with a barrier that counts its copies' bytes.
+// `abort` (shared by the CTA) is raised when a wait runs out: the copies stop,
+// the waits return at once, and the CTA ends after its outstanding copies.
+struct Ring {
+  uint32_t base, bars;
+  int stage_size, slots;
+  volatile uint32_t *abort;
+  uint32_t *status;
+  int put = 0, get = 0;
+  uint32_t get_phase = 0;
+  int outstanding = 0;
+
+  __device__ __forceinline__ uint32_t stage(int slot) const { return base + slot * stage_size; }
+
+  // Whole warp.  Starts the copies of stage s of 16 MT rows in SEGS runs; tiles:
+  // scale tiles along K.
+  template <int FMT, int MT, int SEGS>
+  __device__ __forceinline__ void fill(const Run (&runs)[SEGS], int s, int tiles) {
+    constexpr int kRunRows = 16 * MT / SEGS;
+    if (*abort) return;
+    const uint32_t dst = stage(put), bar = bars + put * 8;
+    const uint32_t scale_bytes = FMT == 0 ? 512u : (tiles - 2 * s > 1 ? 1024u : 512u);
+    if (elect_one()) {
+      mbar_arrive_expect_tx(bar, 16 * MT * 64 + SEGS * scale_bytes);
+#pragma unroll
+      for (int i = 0; i < SEGS; ++i) {
+        tma_load_2d(dst + i * kRunRows * 64, runs[i].codes, s * 64, runs[i].code_row, bar);
+        const int64_t off = (static_cast<int64_t>(runs[i].row >> 7) * tiles +
+                             s * (FMT == 0 ? 1 : 2)) * 512;
+        bulk_load(dst + 16 * MT * 64 + i * kScaleBytes<FMT, 1>,
+                  runs[i].scales + (in_bounds(off, scale_bytes, runs[i].scale_end, status) ? off : 0),
+                  scale_bytes, bar);
+      }
+    }
+    if (++put == slots) put = 0;
+    ++outstanding;
   }
-}
+
+  // Whole warp.  Waits for the next stage; false when a wait ran out.
+  __device__ __forceinline__ bool wait() {
+    return mbar_wait_warp(bars + get * 8, get_phase, abort, status);
+  }
+
+  // The stage that wait() gave is read (after a __syncwarp it may be filled again).
+  __device__ __forceinline__ void next() {
+    --outstanding;
+    if (++get == slots) get = 0, get_phase ^= 1u;
+  }
+
+  // After an abort: no copy may still be writing when the CTA ends.
+  __device__ __forceinline__ void drain() {
+    for (; outstanding > 0; next()) mbar_drain(bars + get * 8, get_phase);
+  }
+};
 
 // ---------------------------------------------------------------- a stage's product
 
-// The activations of one 8-token tile as the product's right operand: b[block]
-// holds K elements 8 t .. 8 t + 7 of the 32-block for token g (lane = 4 g + t),
-// as FP16 after a multiplication by 2^(14 - floor(log2 max)) of the token's 128.
-// Returns the inverse, 2^(floor(log2 max) - 14).
-template <typename XT>
-__device__ __forceinline__ float x_fragments(uint32_t row, bool valid, uint32_t (&b)[4][4]) {
-  const int t = threadIdx.x & 3;
-  if constexpr (sizeof(XT) == 2) {
-    uint32_t top = 0;
+// The activations in shared memory: FP16 [token][K of the slice], rows `pitch`
+// bytes apart, and for each stage of 128 the tokens' factors.  The padding of a
+// row makes a quarter warp's 16-byte reads (two tokens) fall on distinct banks.
+__host__ __device__ constexpr int x_pitch(int stages) { return stages * kStageK * 2 + 64; }
+
+// Whole CTA (W warps).  Writes `count` rows of x, K elements [k0, k0 + 128
+// stages), as FP16 at xs: each 128 times 2^(14 - floor(log2 max)), and the
+// inverse to factors[stage * kTokens + token].  Elements at or past k are 0.
+// row(i): the i-th row; extent: elements of x from its base (bounds-checked
+// build).  A half warp takes 128 elements, eight a lane.
+template <typename XT, int W, int kTokens, typename Row>
+__device__ __forceinline__ void stage_x(uint32_t xs, float *factors, const void *x, int64_t extent,
+                                        int count, int stages, int k0, int k, const Row &row,
+                                        uint32_t *status) {
+  constexpr int kBatch = sizeof(XT) == 2 ? 4 : 2;  // loads in flight
+  const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
+  const int tasks = count * stages, pitch = x_pitch(stages);
+  for (int base = 0; base < tasks; base += kBatch * 2 * W) {
+    uint4 raw[kBatch][sizeof(XT) / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint4 v = valid ? lds128(row + i * 64 + t * 16) : make_uint4(0, 0, 0, 0);
-      b[i][0] = v.x, b[i][1] = v.y, b[i][2] = v.z, b[i][3] = v.w;
+    for (int j = 0; j < kBatch; ++j) {
+      const int task = base + j * 2 * W + half;
+      const int r = task / stages, at = k0 + (task - r * stages) * kStageK + l * 8;
 #pragma unroll
-      for (int j = 0; j < 4; j += 2)
-        top = __vimax3_u16x2(top, b[i][j] & 0x7FFF7FFFu, b[i][j + 1] & 0x7FFF7FFFu);
-    }
-    uint32_t e = max(top & 0xFFFFu, top >> 16);
-    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 1));
-    e = max(e, __shfl_xor_sync(0xFFFFFFFFu, e, 2));
-    e = max(e >> 7, 15u);  // exponent field of the largest, kept where both factors are normal
-    const uint32_t f = (268u - e) * 0x00800080u;
+      for (int q = 0; q < static_cast<int>(sizeof(XT) / 2); ++q) raw[j][q] = make_uint4(0, 0, 0, 0);
+      if (task < tasks && at < k) {
+        const int64_t off = row(r) + at;
+        if (in_bounds(off, 8, extent, status)) {
+          const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const XT *>(x) + off);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t v = mul_bf16x2(b[i][j], f);
-        b[i][j] = pack_f16x2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+          for (int q = 0; q < static_cast<int>(sizeof(XT) / 2); ++q) raw[j][q] = p[q];
+        }
       }
     }
-    return __uint_as_float((e - 14u) << 23);
-  } else {
-    float v[4][8], top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < kBatch; ++j) {
+      const int task = base + j * 2 * W + half;
+      float v[8];
+      if constexpr (sizeof(XT) == 2) {
+        const uint32_t w[4] = {raw[j][0].x, raw[j][0].y, raw[j][0].z, raw[j][0].w};
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 q = valid ? lds128(row + i * 128 + t * 32 + j * 16) : make_uint4(0, 0, 0, 0);
-        v[i][4 * j] = __uint_as_float(q.x), v[i][4 * j + 1] = __uint_as_float(q.y);
-        v[i][4 * j + 2] = __uint_as_float(q.z), v[i][4 * j + 3] = __uint_as_float(q.w);
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = __uint_as_float(w[i] << 16);
+          v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          v[4 * q] = __uint_as_float(raw[j][q].x), v[4 * q + 1] = __uint_as_float(raw[j][q].y);
+          v[4 * q + 2] = __uint_as_float(raw[j][q].z), v[4 * q + 3] = __uint_as_float(raw[j][q].w);
+        }
       }
+      float top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(v[i][j]));
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(v[i]));
+#pragma unroll
+      for (int m = 8; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+      // exponent field of the largest, kept where both factors are normal
+      const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
+      const float f = __uint_as_float((268u - e) << 23);
+      if (task < tasks) {
+        const int r = task / stages, s = task - r * stages;
+        sts128(xs + r * pitch + s * (kStageK * 2) + l * 16,
+               make_uint4(pack_f16x2(v[0] * f, v[1] * f), pack_f16x2(v[2] * f, v[3] * f),
+                          pack_f16x2(v[4] * f, v[5] * f), pack_f16x2(v[6] * f, v[7] * f)));
+        if (l == 0) factors[s * kTokens + r] = __uint_as_float((e - 14u) << 23);
+      }
     }
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
-    const float f = __uint_as_float((268u - e) << 23);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[i][j] = pack_f16x2(v[i][2 * j] * f, v[i][2 * j + 1] * f);
-    }
-    return __uint_as_float((e - 14u) << 23);
   }
 }
 
-// total += the product of the stage at `st`: element [m][n][i] is row 16 m + g
-// (+ 8 for i >= 2), token 8 n + 2 t + (i & 1).
-template <int FMT, int MT, int NT, typename XT>
-__device__ __forceinline__ void stage_product(uint32_t st, int count, float (&total)[MT][NT][4]) {
-  constexpr int R = 16 * MT;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const uint32_t scales = st + R * 64, xs = scales + R * (FMT == 0 ? 4 : 8);
-  uint32_t b[NT][4][4];
-  float sx[NT][2];
+// Decodes the scales of a stage (`raw`: SEGS runs of 512-byte tiles) once for
+// the warp: row r of the 16 MT gets its scales of the stage at dec, as four FP32
+// (MXFP4) or, for each half of a 32-block, four FP16 pairs (NVFP4).  A 16-byte
+// row of a tile holds the words of rows l, l + 32, l + 64, l + 96; run i starts
+// at row first[i] of its matrix.
+// Blocks past K (`blocks` of the four are inside) get the scale 0: their codes
+// are 0, but the bytes there need not be.
+template <int FMT, int MT, int SEGS>
+__device__ __forceinline__ void decode_scales(uint32_t raw, const int (&first)[SEGS], int blocks,
+                                              uint32_t dec) {
+  constexpr int kRunRows = 16 * MT / SEGS;
+  constexpr int kWordBlocks = FMT == 0 ? 4 : 2;  // 32-blocks of a word
+  const uint32_t keep0 = blocks >= kWordBlocks ? ~0u : (1u << (32 / kWordBlocks * blocks)) - 1u;
+  const uint32_t keep1 = blocks >= 4 ? ~0u : blocks <= 2 ? 0u : 0xFFFFu;  // NVFP4's second word
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    const float s = x_fragments<XT>(xs + (8 * n + g) * x_pitch<XT>(), 8 * n + g < count, b[n]);
-    sx[n][0] = __shfl_sync(0xFFFFFFFFu, s, t * 8);
-    sx[n][1] = __shfl_sync(0xFFFFFFFFu, s, t * 8 + 4);
+  for (int i = 0; i < SEGS; ++i) {
+#pragma unroll
+    for (int r0 = 0; r0 < kRunRows; r0 += 32) {
+      if (kRunRows < 32 && lane >= kRunRows) continue;
+      const int in_tile = (first[i] & 127) + r0 + lane;  // a run does not cross a tile
+      const uint32_t at = raw + i * kScaleBytes<FMT, 1> + (in_tile & 31) * 16 + (in_tile >> 5) * 4;
+      const uint32_t row = i * kRunRows + r0 + lane;
+      if constexpr (FMT == 0) {
+        const uint32_t w = lds32(at) & keep0;
+        const uint32_t p = ue8m0x2_bf16x2(w), q = ue8m0x2_bf16x2(w >> 16);
+        sts128(dec + row * 16, make_uint4(p << 16, p & 0xFFFF0000u, q << 16, q & 0xFFFF0000u));
+      } else {
+        const uint32_t w0 = lds32(at) & keep0, w1 = lds32(at + 512) & keep1;
+        const uint32_t a = e4m3x2_f16x2(w0), b = e4m3x2_f16x2(w0 >> 16), c = e4m3x2_f16x2(w1),
+                       d = e4m3x2_f16x2(w1 >> 16);
+        sts128(dec + row * 32, make_uint4(__byte_perm(a, 0, 0x1010), __byte_perm(b, 0, 0x1010),
+                                          __byte_perm(c, 0, 0x1010), __byte_perm(d, 0, 0x1010)));
+        sts128(dec + row * 32 + 16,
+               make_uint4(__byte_perm(a, 0, 0x3232), __byte_perm(b, 0, 0x3232),
+                          __byte_perm(c, 0, 0x3232), __byte_perm(d, 0, 0x3232)));
+      }
+    }
   }
+  __syncwarp();
+}
+
+// total += the product of the stage at `st` (scales decoded at `dec`) and the
+// activations at `xs` (`count` tokens, rows `pitch` apart, factors at `sx`):
+// element [m][n][i] is row 16 m + g (+ 8 for i >= 2), token 8 n + 2 t + (i & 1),
+// lane = 4 g + t.  Lane t holds K elements 8 t .. 8 t + 7 of each 32-block, of
+// the codes and of x alike.
+template <int FMT, int MT, int NT, int NTM>
+__device__ __forceinline__ void stage_product(uint32_t st, uint32_t dec, uint32_t xs, int pitch,
+                                              uint32_t sx, int count, float (&total)[MT][NTM][4]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   // ldmatrix lane addresses: rows l % 8 (+ 8), blocks l / 16 (+ 2)
   const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8;
   const uint32_t lbase = st + lrow * 64 + (((lane >> 4) ^ ((lrow >> 1) & 3)) << 4);
+  float acc[MT][NT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
-    float acc[NT][4];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-    float s0[4], s1[4];       // MXFP4: scales of rows g, g + 8 for the four blocks
-    uint32_t q0[4], q1[4];    // NVFP4: this lane's group scale as FP16 pairs
-    if constexpr (FMT == 0) {
-      const uint32_t w0 = lds32(scales + (16 * m + g) * 4), w1 = lds32(scales + (16 * m + g + 8) * 4);
+    for (int n = 0; n < NT; ++n) acc[m][n][0] = acc[m][n][1] = acc[m][n][2] = acc[m][n][3] = 0.0f;
+  }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t p0 = ue8m0x2_bf16x2(w0 >> (16 * i)), p1 = ue8m0x2_bf16x2(w1 >> (16 * i));
-        s0[2 * i] = __uint_as_float(p0 << 16), s0[2 * i + 1] = __uint_as_float(p0 & 0xFFFF0000u);
-        s1[2 * i] = __uint_as_float(p1 << 16), s1[2 * i + 1] = __uint_as_float(p1 & 0xFFFF0000u);
-      }
-    } else {
-      const uint2 w0 = lds64(scales + (16 * m + g) * 8), w1 = lds64(scales + (16 * m + g + 8) * 8);
-      // lanes t = 0, 1 hold the first 16 of a 32-block, t = 2, 3 the second
-      const uint32_t pick = t < 2 ? 0x2200u : 0x3311u;
-      const uint32_t u[4] = {__byte_perm(w0.x, 0, pick), __byte_perm(w0.y, 0, pick),
-                             __byte_perm(w1.x, 0, pick), __byte_perm(w1.y, 0, pick)};
+  for (int half = 0; half < 2; ++half) {
+    uint4 b[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        q0[2 * i] = e4m3x2_f16x2(u[i]), q0[2 * i + 1] = e4m3x2_f16x2(u[i] >> 16);
-        q1[2 * i] = e4m3x2_f16x2(u[2 + i]), q1[2 * i + 1] = e4m3x2_f16x2(u[2 + i] >> 16);
+        b[n][i] = make_uint4(0, 0, 0, 0);
+        if (8 * n + g < count)
+          b[n][i] = lds128(xs + (8 * n + g) * pitch + (2 * half + i) * 64 + t * 16);
       }
     }
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int m = 0; m < MT; ++m) {
       uint32_t w[4];  // rows g, g + 8 of block 2 half, then of block 2 half + 1
       ldmatrix_x4((lbase + m * 1024) ^ (half * 32), w);
+      // scales of rows g and g + 8 for the two blocks: FP32 (MXFP4), or this
+      // lane's half of each block as FP16 pairs (NVFP4)
+      constexpr int kRow = FMT == 0 ? 16 : 32;
+      const uint32_t at = dec + (16 * m + g) * kRow + (FMT == 0 ? 0 : (t >> 1) * 16) + half * 8;
+      const uint2 s0 = lds64(at), s1 = lds64(at + 8 * kRow);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int blk = 2 * half + i;
         uint32_t a0[4], a1[4];
         e2m1x8_f16(w[2 * i], a0);
         e2m1x8_f16(w[2 * i + 1], a1);
+        const uint32_t q0 = i == 0 ? s0.x : s0.y, q1 = i == 0 ? s1.x : s1.y;
         if constexpr (FMT == 1) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            a0[j] = mul_f16x2(a0[j], q0[blk]);
-            a1[j] = mul_f16x2(a1[j], q1[blk]);
+            a0[j] = mul_f16x2(a0[j], q0);
+            a1[j] = mul_f16x2(a1[j], q1);
           }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          float(&c)[4] = acc[m][n];
           if constexpr (FMT == 0) {
             const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
             float d[4];
-            mma_16816(d, a0[0], a1[0], a0[1], a1[1], b[n][blk][0], b[n][blk][1], zero);
-            mma_16816(d, a0[2], a1[2], a0[3], a1[3], b[n][blk][2], b[n][blk][3], d);
-            acc[n][0] = __fmaf_rn(s0[blk], d[0], acc[n][0]);
-            acc[n][1] = __fmaf_rn(s0[blk], d[1], acc[n][1]);
-            acc[n][2] = __fmaf_rn(s1[blk], d[2], acc[n][2]);
-            acc[n][3] = __fmaf_rn(s1[blk], d[3], acc[n][3]);
+            mma_16816(d, a0[0], a1[0], a0[1], a1[1], b[n][i].x, b[n][i].y, zero);
+            mma_16816(d, a0[2], a1[2], a0[3], a1[3], b[n][i].z, b[n][i].w, d);
+            c[0] = __fmaf_rn(__uint_as_float(q0), d[0], c[0]);
+            c[1] = __fmaf_rn(__uint_as_float(q0), d[1], c[1]);
+            c[2] = __fmaf_rn(__uint_as_float(q1), d[2], c[2]);
+            c[3] = __fmaf_rn(__uint_as_float(q1), d[3], c[3]);
           } else {
-            mma_16816(acc[n], a0[0], a1[0], a0[1], a1[1], b[n][blk][0], b[n][blk][1], acc[n]);
-            mma_16816(acc[n], a0[2], a1[2], a0[3], a1[3], b[n][blk][2], b[n][blk][3], acc[n]);
+            mma_16816(c, a0[0], a1[0], a0[1], a1[1], b[n][i].x, b[n][i].y, c);
+            mma_16816(c, a0[2], a1[2], a0[3], a1[3], b[n][i].z, b[n][i].w, c);
           }
         }
       }
     }
+  }
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+  for (int n = 0; n < NT; ++n) {
+    const uint2 f = lds64(sx + (8 * n + 2 * t) * 4);
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        total[m][n][i] = __fmaf_rn(sx[n][i & 1], acc[n][i], total[m][n][i]);
+        total[m][n][i] =
+            __fmaf_rn(__uint_as_float(i & 1 ? f.y : f.x), acc[m][n][i], total[m][n][i]);
     }
   }
 }
 
-// ---------------------------------------------------------------- joining the warps
+// ---------------------------------------------------------------- the whole walk
 
-// The sums of a CTA's warps: each writes its totals to `red` (float4 [warps][MT NT
-// 32]), and after a barrier unit u (= (m NT + n) 32 + lane) is their sum in the
-// order of the warps.
-template <int MT, int NT>
-__device__ __forceinline__ void write_totals(float4 *red, int warp, const float (&total)[MT][NT][4]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int m = 0; m < MT; ++m) {
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      red[(warp * MT * NT + m * NT + n) * 32 + lane] =
-          make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
+// Shared memory of a CTA, in order: the warps' rings, the warps' sums (a warp's
+// decoded scales lie in its own part of them: they are dead when it writes its
+// sums), barriers and the abort flag, factors and activations.
+template <int FMT, int MT, int NT, int SEGS, int W, int S>
+struct Layout {
+  static constexpr int kRing = W * S * kStageBytes<FMT, MT, SEGS>;
+  static constexpr int kWarpRed = MT * NT * 512;
+  static_assert(kDecodedBytes<FMT, MT> <= kWarpRed, "the decoded scales' place");
+  static constexpr int kRed = W * kWarpRed;
+  static constexpr int kBars = W * S * 8 + 16;
+  __host__ __device__ static constexpr int x_bytes(int tokens, int stages) {
+    return tokens * x_pitch(stages) + stages * NT * 8 * 4;
   }
+  // Stages of K whose activations fit beside the rest in `bytes`.
+  __host__ __device__ static constexpr int fitting_stages(int tokens, int bytes) {
+    return (bytes - kRing - kRed - kBars - tokens * 64) / (tokens * kStageK * 2 + NT * 8 * 4);
+  }
+  __host__ __device__ static constexpr int total(int tokens, int stages) {
+    return kRing + kRed + x_bytes(tokens, stages) + kBars;
+  }
+};
+
+// How the warps divide an item of 16 MT rows_w x K: `rows_w` warps side by side
+// along the rows, the others along K; x is held `x_stages` stages at a time.
+struct Split {
+  int rows_w;
+  int x_stages;
+};
+
+// Walks this CTA's items.  Each is R = 16 MT rows_w rows
+// times the tokens of a group; Policy gives for an item:
+//   start(item, end)     whole CTA, once, after the set-up that touches no global
+//                        memory: waits for the previous kernel, sets the items
+//   group(item)          the tokens' group (its activations are staged when it changes)
+//   count(item)          its tokens (<= 8 NT)
+//   row_off(item, i)     offset in x (elements) of its i-th token
+//   runs(item, wr, runs) the rows of row-warp wr
+//   finish(item, sums)   whole CTA: sums(wr, m, n, lane) gives four sums (all warps
+//                        of the K split added, in their order)
+// The warps meet in finish() and where activations are staged.
+template <int FMT, int MT, int NT, int SEGS, int W, int S, typename XT, typename Policy>
+__device__ __forceinline__ void walk(char *smem, Policy &policy, const void *x,
+                                     int64_t x_extent, int k, Split split, uint32_t *status) {
+  using L = Layout<FMT, MT, NT, SEGS, W, S>;
+  const int warp = threadIdx.x >> 5;
+  const int wr = warp % split.rows_w, wk = warp / split.rows_w, kw = W / split.rows_w;
+  char *at = smem + L::kRing;
+  float4 *red = reinterpret_cast<float4 *>(at);
+  const uint32_t dec = smem_u32(at) + warp * L::kWarpRed;
+  at += L::kRed;
+  const uint32_t bars = smem_u32(at);
+  volatile uint32_t *abort = reinterpret_cast<volatile uint32_t *>(at + W * S * 8);
+  at += L::kBars;
+  float *factors = reinterpret_cast<float *>(at);
+  const uint32_t xs = smem_u32(at + split.x_stages * NT * 8 * 4);
+  if (threadIdx.x == 0) *abort = 0;
+  if (threadIdx.x < W * S) mbar_init(bars + threadIdx.x * 8, 1);
+  fence_barrier_init();
+  Ring ring{smem_u32(smem) + warp * S * kStageBytes<FMT, MT, SEGS>, bars + warp * S * 8,
+            kStageBytes<FMT, MT, SEGS>, S, abort, status};
+
+  const int stages = (k + kStageK - 1) / kStageK, tiles = (k / (FMT == 0 ? 32 : 16) + 3) >> 2;
+  const int slices = (stages + split.x_stages - 1) / split.x_stages;
+  // this warp's stages of slice i: [lo, hi)
+  const auto share = [&](int i, int &lo, int &hi) {
+    const int first = i * split.x_stages, len = min(split.x_stages, stages - first);
+    lo = first + len * wk / kw;
+    hi = first + len * (wk + 1) / kw;
+  };
+  int item = 0, item_end = 0;
+  // the copies' place in the warp's sequence of stages, ahead of the product's
+  int put_item = item, put_slice = 0, put_s, put_hi;
+  Run put_runs[SEGS];
+  const auto fill = [&]() {
+    while (put_item < item_end && put_s == put_hi) {
+      if (++put_slice == slices) {
+        put_slice = 0;
+        if (++put_item < item_end) policy.runs(put_item, wr, put_runs);
+      }
+      share(put_slice, put_s, put_hi);
+    }
+    if (put_item < item_end) ring.fill<FMT, MT, SEGS>(put_runs, put_s++, tiles);
+  };
+  __syncthreads();
+  policy.start(item, item_end);
+  put_item = item;
+  share(0, put_s, put_hi);
+  if (slices == 1 && put_s == put_hi) put_item = item_end;  // no share of K
+  if (put_item < item_end) policy.runs(put_item, wr, put_runs);
+  for (int i = 0; i < S - 1; ++i) fill();
+
+  int staged = -1;
+  for (; item < item_end; ++item) {
+    const int count = policy.count(item), group = policy.group(item);
+    Run runs[SEGS];
+    policy.runs(item, wr, runs);
+    int first[SEGS];
+#pragma unroll
+    for (int i = 0; i < SEGS; ++i) first[i] = runs[i].row;
+    float total[MT][NT][4] = {};
+    for (int slice = 0; slice < slices; ++slice) {
+      const int len = min(split.x_stages, stages - slice * split.x_stages);
+      if (group * slices + slice != staged) {
+        if (staged >= 0) __syncthreads();
+        stage_x<XT, W, 8 * NT>(xs, factors, x, x_extent, count, len,
+                               slice * split.x_stages * kStageK, k,
+                               [&](int i) { return policy.row_off(item, i); }, status);
+        __syncthreads();
+        staged = group * slices + slice;
+      }
+      const int pitch = x_pitch(len);
+      int lo, hi;
+      share(slice, lo, hi);
+      for (int s = lo; s < hi; ++s) {
+        const bool ok = ring.wait();
+        fill();
+        if (!ok) break;
+        const uint32_t st = ring.stage(ring.get);
+        decode_scales<FMT, MT, SEGS>(st + 16 * MT * 64, first, min((k >> 5) - 4 * s, 4), dec);
+        const int sl = s - slice * split.x_stages;
+        const uint32_t sx = smem_u32(factors) + sl * NT * 8 * 4;
+        if (NT == 1 || count > 8 * (NT - 1) || (NT == 4 && count > 16))
+          stage_product<FMT, MT, NT, NT>(st, dec, xs + sl * kStageK * 2, pitch, sx, count, total);
+        else if (NT == 4 && count > 8)
+          stage_product<FMT, MT, (NT == 4 ? 2 : 1), NT>(st, dec, xs + sl * kStageK * 2, pitch, sx,
+                                                        count, total);
+        else
+          stage_product<FMT, MT, 1, NT>(st, dec, xs + sl * kStageK * 2, pitch, sx, count, total);
+        ring.next();
+        __syncwarp();
+      }
+    }
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        red[((warp * MT + m) * NT + n) * 32 + lane] =
+            make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
+    }
+    __syncthreads();
+    policy.finish(item, [&](int r, int m, int n, int l) {
+      float4 sum = red[((r * MT + m) * NT + n) * 32 + l];
+      for (int w = r + split.rows_w; w < W; w += split.rows_w) {
+        const float4 v = red[((w * MT + m) * NT + n) * 32 + l];
+        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+      }
+      return sum;
+    });
+    __syncthreads();
+  }
+  ring.drain();
 }
 
-template <int UNITS>
-__device__ __forceinline__ float4 sum_totals(const float4 *red, int warps, int unit) {
-  float4 s = red[unit];
-  for (int w = 1; w < warps; ++w) {
-    const float4 v = red[w * UNITS + unit];
-    s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
-  }
+// The split of an item's K and rows over the warps: along K while every warp
+// gets a stage, the rest along the rows.
+inline Split make_split(int warps, int stages, int fitting) {
+  Split s{1, fitting < stages ? fitting : stages};
+  while (s.rows_w < warps && warps / s.rows_w > s.x_stages) s.rows_w *= 2;
   return s;
 }
+
+constexpr int kMaxSmem = 227 * 1024;
 
 }  // namespace few
 

@@ -1,120 +1,126 @@
 // mx_linear_bf16: a few BF16 rows times an FP4 weight.
+#include <cstdlib>
 #include "few_tokens.cuh"
 
 namespace mx {
 namespace {
 
-constexpr int kMaxSmem = 227 * 1024;
 
 struct LinearParams {
   LinearArgs a;
-  int tiles;   // row tiles of 16 MT rows
-  int stages;  // ring depth of a warp
+  few::Split split;
+  int items;  // of 16 kRowTiles split.rows_w rows
 };
 
-// Persistent over row tiles: tile blockIdx.x, + gridDim.x, ...  Each of the W
-// warps takes its share of K in every tile.
-template <int FMT, int MT, int NT, int W, int S>
-__global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p) {
-  extern __shared__ __align__(128) char smem[];
-  constexpr int R = 16 * MT, kUnits = MT * NT * 32;
-  const LinearArgs &a = p.a;
-  griddep_launch_dependents();
-  const int warp = threadIdx.x >> 5;
-  const int k = static_cast<int>(a.k), n = static_cast<int>(a.n);
-  const int stage_size = few::stage_bytes<FMT, MT, uint16_t>(a.tokens);
-  float4 *red = reinterpret_cast<float4 *>(smem);
-  const uint32_t ring = smem_u32(smem) + W * kUnits * 16 + warp * S * stage_size;
-  const int all = (k + few::kStageK - 1) / few::kStageK;
-  const int s_begin = all * warp / W, s_end = all * (warp + 1) / W;
-  const int64_t blocks = k / (FMT == 0 ? 32 : 16);
-  const few::Rows m0{a.w.codes, a.w.scales, 0, 0, a.n * (a.k / 2),
-                     (a.n + 127) / 128 * ((blocks + 3) / 4) * 512};
-  const few::Rows rows[2] = {m0, m0};
-  const int64_t x_extent = ((a.tokens - 1) * a.ld_x + a.k) * 2;
+// Items are row tiles; all have the same tokens.
+template <int FMT, int NT, int kRowTiles>
+struct LinearPolicy {
+  static constexpr int kRows = 16 * kRowTiles;
+  const LinearParams &p;
+  const CUtensorMap *map;
+  int64_t scale_end;
 
-  // the copies' place: tile and stage, ahead of the product's
-  int ptile = blockIdx.x, ps = s_begin, pslot = 0;
-  const auto issue = [&]() {
-    if (s_begin < s_end && ptile < p.tiles) {
-      const uint32_t dst = ring + pslot * stage_size;
-      const int first[2] = {ptile * R, ptile * R + R / 2};
-      few::load_weights<FMT, MT>(dst, rows, first, n, k, ps, a.status);
-      few::load_x<uint16_t>(dst + R * (64 + (FMT == 0 ? 4 : 8)), a.x, x_extent, a.tokens, k, ps,
-                            [&](int r) { return r * a.ld_x; }, a.status);
-      if (++ps == s_end) ps = s_begin, ptile += gridDim.x;
-      if (++pslot == S) pslot = 0;
-    }
-    few::cp_async_commit();
-  };
-
-  griddep_wait();
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) issue();
-  const float alpha = FMT == 1 ? *a.w.ts : 1.0f;
-  int slot = 0;
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
-    float total[MT][NT][4] = {};
-    for (int s = s_begin; s < s_end; ++s) {
-      few::cp_async_wait<S - 2>();
-      __syncwarp();
-      issue();
-      few::stage_product<FMT, MT, NT, uint16_t>(ring + slot * stage_size, a.tokens, total);
-      if (++slot == S) slot = 0;
-    }
-    few::write_totals<MT, NT>(red, warp, total);
-    __syncthreads();
-    for (int u = threadIdx.x; u < kUnits; u += W * 32) {
-      const float4 v = few::sum_totals<kUnits>(red, W, u);
-      const int lane = u & 31, mn = u >> 5;
-      const int row0 = tile * R + (mn / NT) * 16 + (lane >> 2), col0 = (mn % NT) * 8 + (lane & 3) * 2;
+  __device__ void start(int &item, int &end) const {
+    item = static_cast<int>(static_cast<int64_t>(p.items) * blockIdx.x / gridDim.x);
+    end = static_cast<int>(static_cast<int64_t>(p.items) * (blockIdx.x + 1) / gridDim.x);
+    griddep_wait();
+  }
+  __device__ int group(int) const { return 0; }
+  __device__ int count(int) const { return p.a.tokens; }
+  __device__ int64_t row_off(int, int i) const { return i * p.a.ld_x; }
+  __device__ void runs(int item, int wr, few::Run (&r)[1]) const {
+    const int64_t row = (static_cast<int64_t>(item) * p.split.rows_w + wr) * kRows;
+    // a tile past the last row gets zeros, and reads (and drops) the last one's scales
+    r[0] = few::Run{map, static_cast<int>(min(row, p.a.n)), p.a.w.scales,
+                    static_cast<int>(min(row, (p.a.n - 1) / kRows * kRows)), scale_end};
+  }
+  template <typename Sums>
+  __device__ void finish(int item, const Sums &sums) const {
+    const LinearArgs &a = p.a;
+    const int tiles = (a.tokens + 7) / 8;
+    const float alpha = FMT == 1 ? *a.w.ts : 1.0f;
+    for (int u = threadIdx.x; u < p.split.rows_w * kRowTiles * tiles * 32; u += blockDim.x) {
+      const int lane = u & 31, q = u >> 5;
+      const int n = q % tiles, m = q / tiles % kRowTiles, wr = q / (tiles * kRowTiles);
+      const float4 v = sums(wr, m, n, lane);
+      const int64_t row0 =
+          (static_cast<int64_t>(item) * p.split.rows_w + wr) * kRows + m * 16 + (lane >> 2);
+      const int col0 = n * 8 + (lane & 3) * 2;
       const float f[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = row0 + (i >> 1) * 8, col = col0 + (i & 1);
-        const int64_t at = col * a.ld_y + row;
-        if (row >= n || col >= a.tokens ||
-            !in_bounds(at, 1, (a.tokens - 1) * a.ld_y + a.n, a.status))
+        const int64_t row = row0 + (i >> 1) * 8;
+        const int col = col0 + (i & 1);
+        const int64_t o = col * a.ld_y + row;
+        if (row >= a.n || col >= a.tokens ||
+            !in_bounds(o, 1, (a.tokens - 1) * a.ld_y + a.n, a.status))
           continue;
         float y = FMT == 1 ? f[i] * alpha : f[i];
         if (a.beta != 0.0f)
-          y = __fmaf_rn(a.beta, a.out_fp32 ? static_cast<const float *>(a.y)[at] : bf16_value(a.y, at),
-                        y);
+          y = __fmaf_rn(a.beta, a.out_fp32 ? static_cast<const float *>(a.y)[o] : bf16_value(a.y, o), y);
         if (a.bias != nullptr) y = __fadd_rn(y, a.bias[row]);
         if (a.gelu) y = gelu_f32x2(make_float2(y, y)).x;
         if (a.out_fp32)
-          static_cast<float *>(a.y)[at] = y;
+          static_cast<float *>(a.y)[o] = y;
         else
-          static_cast<uint16_t *>(a.y)[at] = bf16_bits(y);
+          static_cast<uint16_t *>(a.y)[o] = bf16_bits(y);
       }
     }
-    __syncthreads();
   }
+};
+
+template <int FMT, int NT, int kRowTiles, int W, int S>
+__global__ void __launch_bounds__(W * 32, 1)
+    linear_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ LinearParams p) {
+  extern __shared__ __align__(1024) char smem[];
+  const LinearArgs &a = p.a;
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) prefetch_tmap(&map);
+  const int64_t blocks = a.k / (FMT == 0 ? 32 : 16);
+  LinearPolicy<FMT, NT, kRowTiles> policy{p, &map, (a.n + 127) / 128 * ((blocks + 3) / 4) * 512};
+  few::walk<FMT, kRowTiles, NT, 1, W, S, uint16_t>(smem, policy, a.x,
+                                                   (a.tokens - 1) * a.ld_x + a.k,
+                                                   static_cast<int>(a.k), p.split, a.status);
 }
 
-template <int FMT, int MT, int NT, int W, int S>
+template <int FMT, int NT, int kRowTiles, int W, int S>
 cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
-  const auto kernel = linear_kernel<FMT, MT, NT, W, S>;
+  using L = few::Layout<FMT, kRowTiles, NT, 1, W, S>;
+  static_assert(L::fitting_stages(8 * NT, few::kMaxSmem) >= 4, "shared memory");
+  const auto kernel = linear_kernel<FMT, NT, kRowTiles, W, S>;
   const void *func = reinterpret_cast<const void *>(kernel);
   if (!kernel_setup_get(func, nullptr)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, few::kMaxSmem);
     if (e != cudaSuccess) return e;
     kernel_setup_put(func, 0);
   }
-  LinearParams p{a, static_cast<int>((a.n + 16 * MT - 1) / (16 * MT)), S};
-  const size_t smem = W * MT * NT * 512 +
-                      static_cast<size_t>(W) * S * few::stage_bytes<FMT, MT, uint16_t>(a.tokens);
-  const int grid = p.tiles < a.num_sms ? p.tiles : a.num_sms;
-  return launch_pdl(kernel, dim3(grid), dim3(W * 32), smem, s, p);
+  const int stages = static_cast<int>((a.k + few::kStageK - 1) / few::kStageK);
+  LinearParams p{a, few::make_split(W, stages, L::fitting_stages(a.tokens, few::kMaxSmem)), 0};
+  constexpr int kRows = 16 * kRowTiles;
+  const int64_t rows = kRows * p.split.rows_w;
+  p.items = static_cast<int>((a.n + rows - 1) / rows);
+  CUtensorMap map;
+  if (!encode_few_map(&map, a.w.codes, a.n, a.k, kRows)) return cudaErrorInvalidValue;
+  const int grid = p.items < a.num_sms ? p.items : a.num_sms;
+  return launch_pdl(kernel, dim3(grid), dim3(W * 32), L::total(a.tokens, p.split.x_stages), s, map, p);
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const LinearArgs &a, cudaStream_t s) {
-  const bool small = a.n < 64 * static_cast<int64_t>(a.num_sms);
-  if (a.tokens <= 8) return small ? launch<FMT, 2, 1, 8, 4>(a, s) : launch<FMT, 4, 1, 8, 3>(a, s);
-  if (a.tokens <= 16) return small ? launch<FMT, 2, 2, 8, 3>(a, s) : launch<FMT, 4, 2, 8, 2>(a, s);
-  return launch<FMT, 2, 4, 6, 2>(a, s);
+  static const int v = getenv("V") ? atoi(getenv("V")) : 0;
+  if (a.tokens <= 8) {
+    if (v == 1) return launch<FMT, 1, 2, 16, 3>(a, s);
+    if (v == 2) return launch<FMT, 1, 4, 8, 2>(a, s);
+    if (v == 3) return launch<FMT, 1, 4, 8, 3>(a, s);
+    if (v == 4) return launch<FMT, 1, 4, 12, 2>(a, s);
+    if (v == 5) return launch<FMT, 1, 4, 8, 4>(a, s);
+    if (v == 6) return launch<FMT, 1, 4, 8, 5>(a, s);
+    if (v == 7) return launch<FMT, 1, 2, 8, 4>(a, s);
+    return launch<FMT, 1, 4, 16, 2>(a, s);
+  }
+  if (a.tokens <= 16) return launch<FMT, 2, 2, 16, 2>(a, s);
+  return launch<FMT, 4, 2, 8, 3>(a, s);
 }
 
 }  // namespace

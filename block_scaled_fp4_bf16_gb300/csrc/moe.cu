@@ -7,70 +7,6 @@ namespace {
 
 constexpr int kWarps = 8;
 
-// Byte offset of the scale of (row, block) in the tcgen05 tile order; tiles =
-// ceil(blocks of a row / 4).
-__device__ __forceinline__ int64_t scale_offset(int64_t row, int64_t block, int64_t tiles) {
-  return ((row >> 7) * tiles + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
-         (block & 3);
-}
-
-// A scale byte's value: UE8M0 (255 is NaN) or E4M3.
-template <int FMT>
-__device__ __forceinline__ float scale_value(uint32_t byte) {
-  if constexpr (FMT == 0) {
-    return byte == 255u ? __uint_as_float(0x7FFFFFFFu)
-                        : __uint_as_float(max(byte << 23, 0x00400000u));
-  } else {
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(byte)));
-    return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-  }
-}
-
-// The two E2M1 codes of a byte as FP16 (low nibble in the low half), exact.
-__device__ __forceinline__ uint32_t e2m1x2_f16x2(uint32_t byte) {
-  uint32_t h;
-  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(byte));
-  return h;
-}
-
-// One warp: sum over k of weight (row) times x for `count` (<= N) rows of x,
-// the full sum in every lane.  x(i, k) gives element k of the i-th row.
-template <int FMT, int N, typename X>
-__device__ __forceinline__ void warp_row_dot(const uint8_t *codes, const uint8_t *scales,
-                                             int64_t row, int64_t k, int count, const X &x,
-                                             float (&acc)[N]) {
-  const int lane = threadIdx.x & 31;
-  const int64_t tiles = (k / (FMT == 0 ? 32 : 16) + 3) / 4;
-#pragma unroll
-  for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-  for (int64_t w = lane; w < k / 8; w += 32) {
-    const uint32_t word = *reinterpret_cast<const uint32_t *>(codes + row * (k / 2) + w * 4);
-    const float s = scale_value<FMT>(scales[scale_offset(row, FMT == 0 ? w / 4 : w / 2, tiles)]);
-    float v[8];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float2 f = __half22float2(__halves2half2(
-          __ushort_as_half(static_cast<unsigned short>(e2m1x2_f16x2(word >> (8 * b)) & 0xFFFFu)),
-          __ushort_as_half(static_cast<unsigned short>(e2m1x2_f16x2(word >> (8 * b)) >> 16))));
-      v[2 * b] = f.x * s;
-      v[2 * b + 1] = f.y * s;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i < count) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i] = __fmaf_rn(v[j], x(i, w * 8 + j), acc[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) acc[i] += __shfl_xor_sync(0xFFFFFFFFu, acc[i], m);
-  }
-}
-
 // Order of the logits as unsigned integers: NaN first, then descending.
 __device__ __forceinline__ uint32_t logit_key(float v) {
   const uint32_t u = __float_as_uint(v);
@@ -129,63 +65,282 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   }
 }
 
-// h[p, i] = act(G_e x)[i] (U_e x)[i] for pair p = t * top_k + j, e = ids[p].
-template <int FMT>
-__global__ void __launch_bounds__(kWarps * 32) up_kernel(const MoeArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int p = blockIdx.y, t = p / a.top_k;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-  const int e = a.ids[p];
-  if (e < 0 || e >= a.experts || row >= a.inter) return;
-  const int64_t blocks = a.hidden / (FMT == 0 ? 32 : 16);
-  const int64_t code_bytes = static_cast<int64_t>(a.inter) * (a.hidden / 2);
-  const int64_t scale_bytes = ((a.inter + 127ll) / 128) * ((blocks + 3) / 4) * 512;
-  const auto x = [&](int, int64_t k) { return bf16_value(a.x, t * a.ld_x + k); };
-  float g[1], u[1];
-  warp_row_dot<FMT, 1>(a.gate.codes + e * code_bytes, a.gate.scales + e * scale_bytes, row,
-                       a.hidden, 1, x, g);
-  warp_row_dot<FMT, 1>(a.up.codes + e * code_bytes, a.up.scales + e * scale_bytes, row, a.hidden, 1,
-                       x, u);
-  if ((threadIdx.x & 31) != 0) return;
-  const float gv = FMT == 1 ? g[0] * a.gate.ts[e] : g[0];
-  const float uv = FMT == 1 ? u[0] * a.up.ts[e] : u[0];
-  const float act = a.gelu ? gelu_f32x2(make_float2(gv, gv)).x : gv / (1.0f + expf(-gv));
-  a.h[static_cast<int64_t>(p) * a.inter + row] = act * uv;
+// ---------------------------------------------------------------- the experts
+
+// The (token, slot) pairs by expert, in shared memory: groups of up to
+// kGroup pairs of one expert.  Every CTA makes them from the ids (at most 1024).
+struct Groups {
+  uint16_t *list;    // pairs, sorted by expert
+  uint16_t *expert;  // of a group
+  uint16_t *begin;   // of a group in list
+  uint16_t *size;
+  int count;
+
+  static constexpr int bytes(int pairs) { return pairs * 8 + 16; }
+};
+
+// Whole CTA of W warps.  `at`: Groups::bytes(pairs) bytes; `scratch`: 2 * W *
+// experts bytes.  An expert's pairs are in ascending order (every CTA has to
+// make the same groups): a warp counts its run of the pairs, and an expert's
+// pairs of the earlier warps come first.
+template <int W>
+__device__ __forceinline__ Groups make_groups(char *at, char *scratch, const int32_t *ids, int pairs,
+                                              int experts, int group, uint32_t *status) {
+  Groups g;
+  g.list = reinterpret_cast<uint16_t *>(at);
+  g.expert = g.list + pairs;
+  g.begin = g.expert + pairs;
+  g.size = g.begin + pairs;
+  constexpr int kRuns = (kMoeMaxTokens * kMoeMaxTopK + 32 * W - 1) / (32 * W);  // of 32, a warp
+  int *total = reinterpret_cast<int *>(at + pairs * 8);
+  uint16_t *counts = reinterpret_cast<uint16_t *>(scratch);  // [W][experts]
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int chunks = (pairs + 31) / 32, per_warp = (chunks + W - 1) / W;
+  for (int i = threadIdx.x; i < W * experts; i += W * 32) counts[i] = 0;
+  __syncthreads();
+  int expert[kRuns], rank[kRuns];
+#pragma unroll
+  for (int c = 0; c < kRuns; ++c) {
+    const int p = (warp * per_warp + c) * 32 + lane;
+    expert[c] = c < per_warp && p < pairs && in_bounds(p, 1, pairs, status) ? ids[p] : -1;
+    if (expert[c] >= experts) expert[c] = -1;
+  }
+#pragma unroll
+  for (int c = 0; c < kRuns; ++c) {
+    if (c >= per_warp) break;
+    const uint32_t same = __match_any_sync(0xFFFFFFFFu, expert[c]);
+    const int before = __popc(same & ((1u << lane) - 1u));
+    uint16_t *count = counts + warp * experts + expert[c];
+    if (expert[c] >= 0) rank[c] = *count + before;
+    __syncwarp();
+    if (expert[c] >= 0 && before == 0) *count += static_cast<uint16_t>(__popc(same));
+    __syncwarp();
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t pair0 = 0, group0 = 0;
+    for (int e0 = 0; e0 < experts; e0 += 32) {
+      const int e = e0 + lane;
+      uint32_t n = 0;
+      if (e < experts)
+        for (int w = 0; w < W; ++w) n += counts[w * experts + e];
+      const uint32_t q = (n + group - 1) / group;
+      uint32_t sum = n | (q << 16);  // both prefix sums at once (each below 2^16)
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, sum, d);
+        if (lane >= d) sum += v;
+      }
+      const uint32_t pair = pair0 + (sum & 0xFFFFu) - n, first = group0 + (sum >> 16) - q;
+      if (e < experts) {
+        uint32_t base = pair;  // where the expert's pairs of each warp begin
+        for (int w = 0; w < W; ++w) {
+          const uint32_t c = counts[w * experts + e];
+          counts[w * experts + e] = static_cast<uint16_t>(base);
+          base += c;
+        }
+      }
+      for (uint32_t j = 0; j < q; ++j) {
+        g.expert[first + j] = static_cast<uint16_t>(e);
+        g.begin[first + j] = static_cast<uint16_t>(pair + j * group);
+        g.size[first + j] = static_cast<uint16_t>(min(n - j * group, static_cast<uint32_t>(group)));
+      }
+      const uint32_t last = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      pair0 += last & 0xFFFFu;
+      group0 += last >> 16;
+    }
+    if (lane == 0) *total = static_cast<int>(group0);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < kRuns; ++c) {
+    if (c < per_warp && expert[c] >= 0)
+      g.list[counts[warp * experts + expert[c]] + rank[c]] =
+          static_cast<uint16_t>((warp * per_warp + c) * 32 + lane);
+  }
+  __syncthreads();
+  g.count = *total;
+  return g;
 }
 
-// y[t, n] = sum_j w_tj (D_e h_p)[n].
-template <int FMT>
-__global__ void __launch_bounds__(kWarps * 32) down_kernel(const MoeArgs a) {
+struct MoeParams {
+  MoeArgs a;
+  few::Split split;
+  int tiles;        // row tiles of a group
+  int group;        // pairs of a group at most
+  int groups_at;    // of the groups in shared memory, after the walk's part
+};
+
+// UP: tiles of 16 MT / 2 gate rows and as many up rows of `inter`, h as output.
+// Else: 16 MT rows of `hidden`, z as output.  Items: group-major, so that a CTA's
+// consecutive items share their activations.
+template <int FMT, int MT, int W, bool UP>
+struct ExpertPolicy {
+  static constexpr int kRows = UP ? 8 * MT : 16 * MT;  // output rows of a warp
+  static constexpr int kSegs = UP ? 2 : 1;
+  const MoeParams &p;
+  const CUtensorMap *map0, *map1;
+  char *smem;  // the walk's part: scratch before its first copy
+  Groups g;
+
+  __device__ int rows() const { return UP ? p.a.inter : p.a.hidden; }
+  __device__ int length() const { return UP ? p.a.hidden : p.a.inter; }
+
+  __device__ void start(int &item, int &end) {
+    griddep_wait();
+    g = make_groups<W>(smem + p.groups_at, smem, p.a.ids, p.a.tokens * p.a.top_k, p.a.experts, p.group,
+                    p.a.status);
+    const int64_t items = static_cast<int64_t>(g.count) * p.tiles;
+    item = static_cast<int>(items * blockIdx.x / gridDim.x);
+    end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+    fence_proxy_async_smem();  // the scratch is overwritten by copies
+    __syncthreads();
+  }
+  __device__ int group(int item) const { return item / p.tiles; }
+  __device__ int count(int item) const { return g.size[item / p.tiles]; }
+  __device__ int pair(int item, int i) const { return g.list[g.begin[item / p.tiles] + i]; }
+  __device__ int64_t row_off(int item, int i) const {
+    const int q = pair(item, i);
+    return UP ? (q / p.a.top_k) * p.a.ld_x : static_cast<int64_t>(q) * p.a.inter;
+  }
+  __device__ void runs(int item, int wr, few::Run (&r)[kSegs]) const {
+    const int e = g.expert[item / p.tiles];
+    const int row = (item % p.tiles * p.split.rows_w + wr) * kRows;
+    const int64_t blocks = length() / (FMT == 0 ? 32 : 16);
+    const int64_t scale_bytes = (rows() + 127ll) / 128 * ((blocks + 3) / 4) * 512;
+    // a tile past the last row reads rows of the next expert or zeros, and is dropped
+    const int code_row = e * rows() + min(row, rows());
+    const int in = min(row, (rows() - 1) / kRows * kRows);
+    const FewMatrix &m0 = UP ? p.a.gate : p.a.down;
+    r[0] = few::Run{map0, code_row, m0.scales + e * scale_bytes, in, scale_bytes};
+    if constexpr (UP) r[1] = few::Run{map1, code_row, p.a.up.scales + e * scale_bytes, in, scale_bytes};
+  }
+  template <typename Sums>
+  __device__ void finish(int item, const Sums &sums) const {
+    const int e = g.expert[item / p.tiles], n_tokens = count(item);
+    const float a0 = FMT == 1 ? (UP ? p.a.gate.ts : p.a.down.ts)[e] : 1.0f;
+    const float a1 = FMT == 1 && UP ? p.a.up.ts[e] : 1.0f;
+    constexpr int kM = UP ? MT / 2 : MT;
+    const int col_tiles = (n_tokens + 7) / 8;
+    const int64_t extent = static_cast<int64_t>(p.a.tokens) * p.a.top_k * rows();
+    for (int u = threadIdx.x; u < p.split.rows_w * kM * col_tiles * 32; u += blockDim.x) {
+      const int lane = u & 31, q = u >> 5;
+      const int n = q % col_tiles, m = q / col_tiles % kM, wr = q / (col_tiles * kM);
+      const float4 v = sums(wr, m, n, lane);
+      float f[4] = {v.x * a0, v.y * a0, v.z * a0, v.w * a0};
+      if constexpr (UP) {
+        const float4 w = sums(wr, m + kM, n, lane);
+        const float up[4] = {w.x * a1, w.y * a1, w.z * a1, w.w * a1};
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          float2 act;
+          if (p.a.gelu)
+            act = gelu_f32x2(make_float2(f[i], f[i + 1]));
+          else
+            act = make_float2(f[i] / (1.0f + expf(-f[i])), f[i + 1] / (1.0f + expf(-f[i + 1])));
+          f[i] = act.x * up[i];
+          f[i + 1] = act.y * up[i + 1];
+        }
+      }
+      const int row0 = (item % p.tiles * p.split.rows_w + wr) * kRows + m * 16 + (lane >> 2);
+      const int col0 = n * 8 + (lane & 3) * 2;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = row0 + (i >> 1) * 8, col = col0 + (i & 1);
+        if (row >= rows() || col >= n_tokens) continue;
+        const int64_t o = static_cast<int64_t>(pair(item, col)) * rows() + row;
+        if (in_bounds(o, 1, extent, p.a.status)) (UP ? p.a.h : p.a.z)[o] = f[i];
+      }
+    }
+  }
+};
+
+template <int FMT, int MT, int NT, int W, int S, bool UP>
+__global__ void __launch_bounds__(W * 32, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap map0, const __grid_constant__ CUtensorMap map1,
+                  const __grid_constant__ MoeParams p) {
+  extern __shared__ __align__(1024) char smem[];
+  griddep_launch_dependents();
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&map0);
+    if (UP) prefetch_tmap(&map1);
+  }
+  ExpertPolicy<FMT, MT, W, UP> policy{p, &map0, &map1, smem, {}};
+  const MoeArgs &a = p.a;
+  if constexpr (UP)
+    few::walk<FMT, MT, NT, 2, W, S, uint16_t>(smem, policy, a.x,
+                                              (a.tokens - 1) * a.ld_x + a.hidden, a.hidden, p.split,
+                                              a.status);
+  else
+    few::walk<FMT, MT, NT, 1, W, S, float>(smem, policy, a.h,
+                                           static_cast<int64_t>(a.tokens) * a.top_k * a.inter,
+                                           a.inter, p.split, a.status);
+}
+
+// y[t] = sum_j w_tj z[t, j], in the order of the slots.
+__global__ void __launch_bounds__(256) combine_kernel(const MoeArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  const int t = blockIdx.y;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-  if (row >= a.hidden) return;
-  const int64_t blocks = a.inter / (FMT == 0 ? 32 : 16);
-  const int64_t code_bytes = static_cast<int64_t>(a.hidden) * (a.inter / 2);
-  const int64_t scale_bytes = ((a.hidden + 127ll) / 128) * ((blocks + 3) / 4) * 512;
-  float y = 0.0f;
+  const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 2;
+  if (c >= a.hidden) return;
+  float y0 = 0.0f, y1 = 0.0f;
   for (int j = 0; j < a.top_k; ++j) {
     const int p = t * a.top_k + j, e = a.ids[p];
     if (e < 0 || e >= a.experts) continue;
-    float z[1];
-    warp_row_dot<FMT, 1>(
-        a.down.codes + e * code_bytes, a.down.scales + e * scale_bytes, row, a.inter, 1,
-        [&](int, int64_t k) { return a.h[static_cast<int64_t>(p) * a.inter + k]; }, z);
-    y = __fmaf_rn(a.weights[p], FMT == 1 ? z[0] * a.down.ts[e] : z[0], y);
+    const float w = a.weights[p];
+    const int64_t o = static_cast<int64_t>(p) * a.hidden + c;
+    if (!in_bounds(o, 2, static_cast<int64_t>(a.tokens) * a.top_k * a.hidden, a.status)) continue;
+    const float2 z = *reinterpret_cast<const float2 *>(a.z + o);
+    y0 = __fmaf_rn(w, z.x, y0);
+    y1 = __fmaf_rn(w, z.y, y1);
   }
-  if ((threadIdx.x & 31) == 0) static_cast<uint16_t *>(a.y)[t * a.ld_y + row] = bf16_bits(y);
+  const int64_t o = t * a.ld_y + c;
+  if (!in_bounds(o, 2, (a.tokens - 1) * a.ld_y + a.hidden, a.status)) return;
+  uint16_t *y = static_cast<uint16_t *>(a.y) + o;
+  y[0] = bf16_bits(y0);
+  y[1] = bf16_bits(y1);
 }
 
-template <int FMT>
+template <int FMT, int MT, int NT, int W, int S, bool UP>
+cudaError_t launch_product(const MoeArgs &a, cudaStream_t s) {
+  using L = few::Layout<FMT, MT, NT, UP ? 2 : 1, W, S>;
+  const auto kernel = expert_kernel<FMT, MT, NT, W, S, UP>;
+  const void *func = reinterpret_cast<const void *>(kernel);
+  if (!kernel_setup_get(func, nullptr)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, few::kMaxSmem);
+    if (e != cudaSuccess) return e;
+    kernel_setup_put(func, 0);
+  }
+  const int k = UP ? a.hidden : a.inter, rows = UP ? a.inter : a.hidden;
+  const int pairs = a.tokens * a.top_k;
+  const int group = pairs < 8 * NT ? pairs : 8 * NT;
+  const int budget = few::kMaxSmem - Groups::bytes(pairs);
+  MoeParams p{a, few::make_split(W, (k + few::kStageK - 1) / few::kStageK,
+                                 L::fitting_stages(group, budget)), 0, 8 * NT, 0};
+  const int tile = (UP ? 8 * MT : 16 * MT) * p.split.rows_w;
+  p.tiles = (rows + tile - 1) / tile;
+  p.groups_at = L::total(group, p.split.x_stages);
+  CUtensorMap map0, map1;
+  const int box = UP ? 8 * MT : 16 * MT;
+  const int64_t stacked = static_cast<int64_t>(a.experts) * rows;
+  if (!encode_few_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, box) ||
+      !encode_few_map(&map1, UP ? a.up.codes : a.down.codes, stacked, k, box))
+    return cudaErrorInvalidValue;
+  const int most = a.experts < pairs ? a.experts : pairs;
+  const int64_t items = static_cast<int64_t>(most + pairs / (8 * NT)) * p.tiles;
+  const int grid = items < a.num_sms ? static_cast<int>(items) : a.num_sms;
+  return launch_pdl(kernel, dim3(grid), dim3(W * 32), p.groups_at + Groups::bytes(pairs), s, map0,
+                    map1, p);
+}
+
+template <int FMT, int NT, int W, int S>
 cudaError_t launch_experts(const MoeArgs &a, cudaStream_t s) {
-  const dim3 block(kWarps * 32);
-  const cudaError_t e = launch_pdl(
-      up_kernel<FMT>, dim3((a.inter + kWarps - 1) / kWarps, a.tokens * a.top_k), block, 0, s, a);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(down_kernel<FMT>, dim3((a.hidden + kWarps - 1) / kWarps, a.tokens), block, 0, s,
-                    a);
+  cudaError_t e = launch_product<FMT, 4, NT, W, S, true>(a, s);
+  if (e == cudaSuccess) e = launch_product<FMT, 4, NT, W, S, false>(a, s);
+  if (e == cudaSuccess)
+    e = launch_pdl(combine_kernel, dim3((a.hidden + 511) / 512, a.tokens), dim3(256), 0, s, a);
+  return e;
 }
 
 }  // namespace
@@ -195,7 +350,8 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s) {
 }
 
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s) {
-  return a.fmt == 0 ? launch_experts<0>(a, s) : launch_experts<1>(a, s);
+  if (a.tokens <= 8) return a.fmt == 0 ? launch_experts<0, 1, 8, 3>(a, s) : launch_experts<1, 1, 8, 3>(a, s);
+  return a.fmt == 0 ? launch_experts<0, 2, 8, 2>(a, s) : launch_experts<1, 2, 8, 2>(a, s);
 }
 
 }  // namespace mx
