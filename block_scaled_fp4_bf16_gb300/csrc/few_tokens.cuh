@@ -206,15 +206,20 @@ template <typename XT, int W, int kTokens, typename Row>
 __device__ __forceinline__ void stage_x(uint32_t xs, float *factors, const void *x, int64_t extent,
                                         int count, int stages, int k0, int k, const Row &row,
                                         uint32_t *status) {
-  constexpr int kBatch = sizeof(XT) == 2 ? 4 : 2;  // loads in flight
+  constexpr int kBatch = sizeof(XT) == 2 ? 8 : 4;  // tasks whose loads are in flight
   const int half = threadIdx.x >> 4, l = threadIdx.x & 15;
   const int tasks = count * stages, pitch = x_pitch(stages);
+  // task / stages by a multiplication (tasks * stages < 2^32)
+  const uint32_t inv = (0xFFFFFFFFu / stages) + 1u;
+  const auto token = [&](int task) {
+    return stages == 1 ? task : static_cast<int>(__umulhi(static_cast<uint32_t>(task), inv));
+  };
   for (int base = 0; base < tasks; base += kBatch * 2 * W) {
     uint4 raw[kBatch][sizeof(XT) / 2];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int task = base + j * 2 * W + half;
-      const int r = task / stages, at = k0 + (task - r * stages) * kStageK + l * 8;
+      const int r = token(task), at = k0 + (task - r * stages) * kStageK + l * 8;
 #pragma unroll
       for (int q = 0; q < static_cast<int>(sizeof(XT) / 2); ++q) raw[j][q] = make_uint4(0, 0, 0, 0);
       if (task < tasks && at < k) {
@@ -253,7 +258,7 @@ __device__ __forceinline__ void stage_x(uint32_t xs, float *factors, const void 
       const uint32_t e = max(__float_as_uint(top) >> 23, 15u);
       const float f = __uint_as_float((268u - e) << 23);
       if (task < tasks) {
-        const int r = task / stages, s = task - r * stages;
+        const int r = token(task), s = task - r * stages;
         sts128(xs + r * pitch + s * (kStageK * 2) + l * 16,
                make_uint4(pack_f16x2(v[0] * f, v[1] * f), pack_f16x2(v[2] * f, v[3] * f),
                           pack_f16x2(v[4] * f, v[5] * f), pack_f16x2(v[6] * f, v[7] * f)));
@@ -392,61 +397,83 @@ __device__ __forceinline__ void stage_product(uint32_t st, uint32_t dec, uint32_
 
 // ---------------------------------------------------------------- the whole walk
 
-// Shared memory of a CTA, in order: the warps' rings, the warps' sums (a warp's
-// decoded scales lie in its own part of them: they are dead when it writes its
-// sums), barriers and the abort flag, factors and activations.
+// How a CTA's W warps and its shared memory serve its items.  An item is
+// 16 MT rows_w rows times a group's tokens; rows_w warps stand side by side along
+// the rows, the W / rows_w others along K.  Up to `batch` items of a group are
+// taken together, and x is held `x_stages` stages of K at a time: the slices are
+// the outer loop, so that x is converted once for a batch, and the sums of a
+// batch's items wait in shared memory from slice to slice.
+struct Split {
+  int rows_w;
+  int x_stages;
+  int batch;
+};
+
+// Shared memory of a CTA, in order: the warps' rings, the warps' sums [batch][W]
+// (the decoded scales of the item at work lie in its own part: its sums are in
+// registers meanwhile), barriers and the abort flag, factors and activations.
 template <int FMT, int MT, int NT, int SEGS, int W, int S>
 struct Layout {
   static constexpr int kRing = W * S * kStageBytes<FMT, MT, SEGS>;
   static constexpr int kWarpRed = MT * NT * 512;
   static_assert(kDecodedBytes<FMT, MT> <= kWarpRed, "the decoded scales' place");
-  static constexpr int kRed = W * kWarpRed;
   static constexpr int kBars = W * S * 8 + 16;
-  __host__ __device__ static constexpr int x_bytes(int tokens, int stages) {
-    return tokens * x_pitch(stages) + stages * NT * 8 * 4;
+  static int total(int tokens, const Split &s) {
+    return kRing + s.batch * W * kWarpRed + kBars + tokens * x_pitch(s.x_stages) +
+           s.x_stages * NT * 8 * 4;
   }
-  // Stages of K whose activations fit beside the rest in `bytes`.
-  __host__ __device__ static constexpr int fitting_stages(int tokens, int bytes) {
-    return (bytes - kRing - kRed - kBars - tokens * 64) / (tokens * kStageK * 2 + NT * 8 * 4);
-  }
-  __host__ __device__ static constexpr int total(int tokens, int stages) {
-    return kRing + kRed + x_bytes(tokens, stages) + kBars;
+  // The split for `items` items a CTA (at rows_w = 1) of `stages` stages: along K
+  // while every warp has at least `least` stages, else along the rows; as many
+  // items together as a CTA has (if the sums of all K do not come at once); all
+  // of x where it fits.
+  static Split split(int tokens, int stages, int least, int items, int bytes) {
+    Split s{1, 0, 1};
+    while (s.rows_w < W && stages < least * (W / s.rows_w)) s.rows_w *= 2;
+    items = (items + s.rows_w - 1) / s.rows_w;
+    const auto fitting = [&](int batch) {
+      return (bytes - kRing - batch * W * kWarpRed - kBars - tokens * 64) /
+             (tokens * kStageK * 2 + NT * 8 * 4);
+    };
+    s.x_stages = fitting(1);
+    if (s.x_stages >= stages) {
+      s.x_stages = stages;
+      while (s.batch < 2 && s.batch < items && fitting(s.batch + 1) >= stages) ++s.batch;
+      return s;
+    }
+    while (s.batch < items && fitting(s.batch + 1) >= W / s.rows_w) ++s.batch;
+    // whole rounds of the warps along K
+    s.x_stages = fitting(s.batch);
+    if (s.x_stages > W / s.rows_w) s.x_stages = s.x_stages / (W / s.rows_w) * (W / s.rows_w);
+    return s;
   }
 };
 
-// How the warps divide an item of 16 MT rows_w x K: `rows_w` warps side by side
-// along the rows, the others along K; x is held `x_stages` stages at a time.
-struct Split {
-  int rows_w;
-  int x_stages;
-};
-
-// Walks this CTA's items.  Each is R = 16 MT rows_w rows
-// times the tokens of a group; Policy gives for an item:
+// Walks this CTA's items.  Policy gives
 //   start(item, end)     whole CTA, once, after the set-up that touches no global
 //                        memory: waits for the previous kernel, sets the items
-//   group(item)          the tokens' group (its activations are staged when it changes)
+//   group(item)          the tokens' group (items of a group are consecutive)
 //   count(item)          its tokens (<= 8 NT)
 //   row_off(item, i)     offset in x (elements) of its i-th token
 //   runs(item, wr, runs) the rows of row-warp wr
-//   finish(item, sums)   whole CTA: sums(wr, m, n, lane) gives four sums (all warps
-//                        of the K split added, in their order)
-// The warps meet in finish() and where activations are staged.
+//   put(item, wr, m, n, lane, sums)  the four sums (or, with SEGS == 2, those of
+//                        the first run's and of the second run's rows) of a unit
+// The warps meet where activations are staged, and, if K is divided among them,
+// around the sums of a batch.
 template <int FMT, int MT, int NT, int SEGS, int W, int S, typename XT, typename Policy>
-__device__ __forceinline__ void walk(char *smem, Policy &policy, const void *x,
-                                     int64_t x_extent, int k, Split split, uint32_t *status) {
+__device__ __forceinline__ void walk(char *smem, Policy &policy, const void *x, int64_t x_extent,
+                                     int k, const Split &split, uint32_t *status) {
   using L = Layout<FMT, MT, NT, SEGS, W, S>;
-  const int warp = threadIdx.x >> 5;
+  constexpr int kUnits = MT * NT * 32;  // float4 of a warp's sums
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int wr = warp % split.rows_w, wk = warp / split.rows_w, kw = W / split.rows_w;
   char *at = smem + L::kRing;
   float4 *red = reinterpret_cast<float4 *>(at);
-  const uint32_t dec = smem_u32(at) + warp * L::kWarpRed;
-  at += L::kRed;
+  at += split.batch * W * L::kWarpRed;
   const uint32_t bars = smem_u32(at);
   volatile uint32_t *abort = reinterpret_cast<volatile uint32_t *>(at + W * S * 8);
   at += L::kBars;
-  float *factors = reinterpret_cast<float *>(at);
-  const uint32_t xs = smem_u32(at + split.x_stages * NT * 8 * 4);
+  const uint32_t factors = smem_u32(at);
+  const uint32_t xs = factors + split.x_stages * NT * 8 * 4;
   if (threadIdx.x == 0) *abort = 0;
   if (threadIdx.x < W * S) mbar_init(bars + threadIdx.x * 8, 1);
   fence_barrier_init();
@@ -462,96 +489,136 @@ __device__ __forceinline__ void walk(char *smem, Policy &policy, const void *x,
     hi = first + len * (wk + 1) / kw;
   };
   int item = 0, item_end = 0;
-  // the copies' place in the warp's sequence of stages, ahead of the product's
-  int put_item = item, put_slice = 0, put_s, put_hi;
+  // items of the batch that begins at `first`
+  const auto batch_of = [&](int first) {
+    int n = 1;
+    while (n < split.batch && first + n < item_end && policy.group(first + n) == policy.group(first))
+      ++n;
+    return n;
+  };
+  // the copies' place in the warp's sequence of batches, slices, items and
+  // stages, ahead of the product's
+  int put_first = 0, put_n = 0, put_i = 0, put_slice = 0, put_s = 0, put_lo = 0, put_hi = 0;
   Run put_runs[SEGS];
   const auto fill = [&]() {
-    while (put_item < item_end && put_s == put_hi) {
-      if (++put_slice == slices) {
-        put_slice = 0;
-        if (++put_item < item_end) policy.runs(put_item, wr, put_runs);
+    while (put_first < item_end && put_s == put_hi) {
+      if (++put_i == put_n) {
+        put_i = 0;
+        if (++put_slice == slices) {
+          put_slice = 0;
+          put_first += put_n;
+          if (put_first >= item_end) break;
+          put_n = batch_of(put_first);
+        }
+        share(put_slice, put_lo, put_hi);
       }
-      share(put_slice, put_s, put_hi);
+      put_s = put_lo;
+      if (put_n > 1 || put_slice == 0) policy.runs(put_first + put_i, wr, put_runs);
     }
-    if (put_item < item_end) ring.fill<FMT, MT, SEGS>(put_runs, put_s++, tiles);
+    if (put_first < item_end) ring.fill<FMT, MT, SEGS>(put_runs, put_s++, tiles);
   };
   __syncthreads();
   policy.start(item, item_end);
-  put_item = item;
-  share(0, put_s, put_hi);
-  if (slices == 1 && put_s == put_hi) put_item = item_end;  // no share of K
-  if (put_item < item_end) policy.runs(put_item, wr, put_runs);
+  put_first = item;
+  share(0, put_lo, put_hi);
+  put_s = put_lo;
+  if (put_first < item_end) {
+    put_n = batch_of(put_first);
+    policy.runs(put_first, wr, put_runs);
+  }
+  if (slices == 1 && put_lo == put_hi) put_first = item_end;  // no share of K
   for (int i = 0; i < S - 1; ++i) fill();
 
   int staged = -1;
-  for (; item < item_end; ++item) {
-    const int count = policy.count(item), group = policy.group(item);
-    Run runs[SEGS];
-    policy.runs(item, wr, runs);
-    int first[SEGS];
-#pragma unroll
-    for (int i = 0; i < SEGS; ++i) first[i] = runs[i].row;
-    float total[MT][NT][4] = {};
+  while (item < item_end) {
+    const int n_items = batch_of(item), count = policy.count(item), group = policy.group(item);
     for (int slice = 0; slice < slices; ++slice) {
       const int len = min(split.x_stages, stages - slice * split.x_stages);
-      if (group * slices + slice != staged) {
+      if (slices > 1 || group != staged) {
         if (staged >= 0) __syncthreads();
-        stage_x<XT, W, 8 * NT>(xs, factors, x, x_extent, count, len,
+        stage_x<XT, W, 8 * NT>(xs, reinterpret_cast<float *>(at), x, x_extent, count, len,
                                slice * split.x_stages * kStageK, k,
                                [&](int i) { return policy.row_off(item, i); }, status);
         __syncthreads();
-        staged = group * slices + slice;
+        staged = group;
       }
       const int pitch = x_pitch(len);
       int lo, hi;
       share(slice, lo, hi);
-      for (int s = lo; s < hi; ++s) {
-        const bool ok = ring.wait();
-        fill();
-        if (!ok) break;
-        const uint32_t st = ring.stage(ring.get);
-        decode_scales<FMT, MT, SEGS>(st + 16 * MT * 64, first, min((k >> 5) - 4 * s, 4), dec);
-        const int sl = s - slice * split.x_stages;
-        const uint32_t sx = smem_u32(factors) + sl * NT * 8 * 4;
-        if (NT == 1 || count > 8 * (NT - 1) || (NT == 4 && count > 16))
-          stage_product<FMT, MT, NT, NT>(st, dec, xs + sl * kStageK * 2, pitch, sx, count, total);
-        else if (NT == 4 && count > 8)
-          stage_product<FMT, MT, (NT == 4 ? 2 : 1), NT>(st, dec, xs + sl * kStageK * 2, pitch, sx,
-                                                        count, total);
-        else
-          stage_product<FMT, MT, 1, NT>(st, dec, xs + sl * kStageK * 2, pitch, sx, count, total);
-        ring.next();
+      for (int i = 0; i < n_items; ++i) {
+        float4 *sums = red + (i * W + warp) * kUnits;
+        const uint32_t dec = smem_u32(sums);
+        Run runs[SEGS];
+        policy.runs(item + i, wr, runs);
+        int first[SEGS];
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) first[j] = runs[j].row;
+        float total[MT][NT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float4 v = slice == 0 ? make_float4(0.0f, 0.0f, 0.0f, 0.0f)
+                                        : sums[(m * NT + n) * 32 + lane];
+            total[m][n][0] = v.x, total[m][n][1] = v.y, total[m][n][2] = v.z, total[m][n][3] = v.w;
+          }
+        }
         __syncwarp();
+        for (int s = lo; s < hi; ++s) {
+          const bool ok = ring.wait();
+          fill();
+          if (!ok) break;
+          const uint32_t st = ring.stage(ring.get);
+          decode_scales<FMT, MT, SEGS>(st + 16 * MT * 64, first, min((k >> 5) - 4 * s, 4), dec);
+          const int sl = s - slice * split.x_stages;
+          const uint32_t sx = factors + sl * NT * 8 * 4, xa = xs + sl * kStageK * 2;
+          if (NT == 1 || count > (NT == 4 ? 16 : 8))
+            stage_product<FMT, MT, NT, NT>(st, dec, xa, pitch, sx, count, total);
+          else if (NT == 4 && count > 8)
+            stage_product<FMT, MT, (NT == 4 ? 2 : 1), NT>(st, dec, xa, pitch, sx, count, total);
+          else
+            stage_product<FMT, MT, 1, NT>(st, dec, xa, pitch, sx, count, total);
+          ring.next();
+          __syncwarp();
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+            sums[(m * NT + n) * 32 + lane] =
+                make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
+        }
       }
     }
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        red[((warp * MT + m) * NT + n) * 32 + lane] =
-            make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
-    }
-    __syncthreads();
-    policy.finish(item, [&](int r, int m, int n, int l) {
-      float4 sum = red[((r * MT + m) * NT + n) * 32 + l];
+    // the warps' sums, added in the order of the warps
+    constexpr int kM = MT / SEGS;
+    const int col_tiles = (count + 7) / 8;
+    const auto add = [&](int i, int r, int unit) {
+      float4 v = red[(i * W + r) * kUnits + unit];
       for (int w = r + split.rows_w; w < W; w += split.rows_w) {
-        const float4 v = red[((w * MT + m) * NT + n) * 32 + l];
-        sum.x += v.x, sum.y += v.y, sum.z += v.z, sum.w += v.w;
+        const float4 o = red[(i * W + w) * kUnits + unit];
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
       }
-      return sum;
-    });
-    __syncthreads();
+      return v;
+    };
+    // kw == 1: a warp's sums are its own
+    if (kw > 1) __syncthreads();
+    const int step = kw > 1 ? W : 1;
+    for (int i = 0; i < n_items; ++i) {
+      const int units = (kw > 1 ? split.rows_w : 1) * kM * col_tiles;
+      for (int u = kw > 1 ? warp : 0; u < units; u += step) {
+        const int n = u % col_tiles, q = u / col_tiles, m = q % kM;
+        const int r = kw > 1 ? q / kM : wr;
+        float4 v[SEGS];
+#pragma unroll
+        for (int j = 0; j < SEGS; ++j) v[j] = add(i, r, ((m + j * kM) * NT + n) * 32 + lane);
+        policy.put(item + i, r, m, n, lane, v);
+      }
+    }
+    if (kw > 1) __syncthreads();
+    item += n_items;
   }
   ring.drain();
-}
-
-// The split of an item's K and rows over the warps: along K while every warp
-// gets a stage, the rest along the rows.
-inline Split make_split(int warps, int stages, int fitting) {
-  Split s{1, fitting < stages ? fitting : stages};
-  while (s.rows_w < warps && warps / s.rows_w > s.x_stages) s.rows_w *= 2;
-  return s;
 }
 
 constexpr int kMaxSmem = 227 * 1024;

@@ -34,37 +34,30 @@ struct LinearPolicy {
     r[0] = few::Run{map, static_cast<int>(min(row, p.a.n)), p.a.w.scales,
                     static_cast<int>(min(row, (p.a.n - 1) / kRows * kRows)), scale_end};
   }
-  template <typename Sums>
-  __device__ void finish(int item, const Sums &sums) const {
+  __device__ void put(int item, int wr, int m, int n, int lane, const float4 (&v)[1]) const {
     const LinearArgs &a = p.a;
-    const int tiles = (a.tokens + 7) / 8;
     const float alpha = FMT == 1 ? *a.w.ts : 1.0f;
-    for (int u = threadIdx.x; u < p.split.rows_w * kRowTiles * tiles * 32; u += blockDim.x) {
-      const int lane = u & 31, q = u >> 5;
-      const int n = q % tiles, m = q / tiles % kRowTiles, wr = q / (tiles * kRowTiles);
-      const float4 v = sums(wr, m, n, lane);
-      const int64_t row0 =
-          (static_cast<int64_t>(item) * p.split.rows_w + wr) * kRows + m * 16 + (lane >> 2);
-      const int col0 = n * 8 + (lane & 3) * 2;
-      const float f[4] = {v.x, v.y, v.z, v.w};
+    const int64_t row0 =
+        (static_cast<int64_t>(item) * p.split.rows_w + wr) * kRows + m * 16 + (lane >> 2);
+    const int col0 = n * 8 + (lane & 3) * 2;
+    const float f[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + (i >> 1) * 8;
-        const int col = col0 + (i & 1);
-        const int64_t o = col * a.ld_y + row;
-        if (row >= a.n || col >= a.tokens ||
-            !in_bounds(o, 1, (a.tokens - 1) * a.ld_y + a.n, a.status))
-          continue;
-        float y = FMT == 1 ? f[i] * alpha : f[i];
-        if (a.beta != 0.0f)
-          y = __fmaf_rn(a.beta, a.out_fp32 ? static_cast<const float *>(a.y)[o] : bf16_value(a.y, o), y);
-        if (a.bias != nullptr) y = __fadd_rn(y, a.bias[row]);
-        if (a.gelu) y = gelu_f32x2(make_float2(y, y)).x;
-        if (a.out_fp32)
-          static_cast<float *>(a.y)[o] = y;
-        else
-          static_cast<uint16_t *>(a.y)[o] = bf16_bits(y);
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int64_t row = row0 + (i >> 1) * 8;
+      const int col = col0 + (i & 1);
+      const int64_t o = col * a.ld_y + row;
+      if (row >= a.n || col >= a.tokens ||
+          !in_bounds(o, 1, (a.tokens - 1) * a.ld_y + a.n, a.status))
+        continue;
+      float y = FMT == 1 ? f[i] * alpha : f[i];
+      if (a.beta != 0.0f)
+        y = __fmaf_rn(a.beta, a.out_fp32 ? static_cast<const float *>(a.y)[o] : bf16_value(a.y, o), y);
+      if (a.bias != nullptr) y = __fadd_rn(y, a.bias[row]);
+      if (a.gelu) y = gelu_f32x2(make_float2(y, y)).x;
+      if (a.out_fp32)
+        static_cast<float *>(a.y)[o] = y;
+      else
+        static_cast<uint16_t *>(a.y)[o] = bf16_bits(y);
     }
   }
 };
@@ -86,7 +79,6 @@ __global__ void __launch_bounds__(W * 32, 1)
 template <int FMT, int NT, int kRowTiles, int W, int S>
 cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
   using L = few::Layout<FMT, kRowTiles, NT, 1, W, S>;
-  static_assert(L::fitting_stages(8 * NT, few::kMaxSmem) >= 4, "shared memory");
   const auto kernel = linear_kernel<FMT, NT, kRowTiles, W, S>;
   const void *func = reinterpret_cast<const void *>(kernel);
   if (!kernel_setup_get(func, nullptr)) {
@@ -95,32 +87,37 @@ cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kernel_setup_put(func, 0);
   }
-  const int stages = static_cast<int>((a.k + few::kStageK - 1) / few::kStageK);
-  LinearParams p{a, few::make_split(W, stages, L::fitting_stages(a.tokens, few::kMaxSmem)), 0};
   constexpr int kRows = 16 * kRowTiles;
+  const int stages = static_cast<int>((a.k + few::kStageK - 1) / few::kStageK);
+  const int64_t row_tiles = (a.n + kRows - 1) / kRows;
+  const int64_t each = (row_tiles + a.num_sms - 1) / a.num_sms;
+  LinearParams p{a, L::split(a.tokens, stages, getenv("LEAST") ? atoi(getenv("LEAST")) : 1, static_cast<int>(each < 64 ? each : 64),
+                             few::kMaxSmem), 0};
   const int64_t rows = kRows * p.split.rows_w;
   p.items = static_cast<int>((a.n + rows - 1) / rows);
   CUtensorMap map;
   if (!encode_few_map(&map, a.w.codes, a.n, a.k, kRows)) return cudaErrorInvalidValue;
   const int grid = p.items < a.num_sms ? p.items : a.num_sms;
-  return launch_pdl(kernel, dim3(grid), dim3(W * 32), L::total(a.tokens, p.split.x_stages), s, map, p);
+  return launch_pdl(kernel, dim3(grid), dim3(W * 32), L::total(a.tokens, p.split), s, map, p);
 }
 
 template <int FMT>
 cudaError_t launch_fmt(const LinearArgs &a, cudaStream_t s) {
   static const int v = getenv("V") ? atoi(getenv("V")) : 0;
   if (a.tokens <= 8) {
-    if (v == 1) return launch<FMT, 1, 2, 16, 3>(a, s);
-    if (v == 2) return launch<FMT, 1, 4, 8, 2>(a, s);
-    if (v == 3) return launch<FMT, 1, 4, 8, 3>(a, s);
-    if (v == 4) return launch<FMT, 1, 4, 12, 2>(a, s);
-    if (v == 5) return launch<FMT, 1, 4, 8, 4>(a, s);
-    if (v == 6) return launch<FMT, 1, 4, 8, 5>(a, s);
-    if (v == 7) return launch<FMT, 1, 2, 8, 4>(a, s);
-    return launch<FMT, 1, 4, 16, 2>(a, s);
+    if (v == 1) return launch<FMT, 1, 2, 8, 4>(a, s);
+    if (v == 2) return launch<FMT, 1, 2, 16, 3>(a, s);
+    if (v == 3) return launch<FMT, 1, 4, 8, 4>(a, s);
+    return launch<FMT, 1, 4, 8, 3>(a, s);
   }
-  if (a.tokens <= 16) return launch<FMT, 2, 2, 16, 2>(a, s);
-  return launch<FMT, 4, 2, 8, 3>(a, s);
+  if (a.tokens <= 16) {
+    if (v == 1) return launch<FMT, 2, 2, 8, 3>(a, s);
+    if (v == 2) return launch<FMT, 2, 2, 16, 2>(a, s);
+    if (v == 3) return launch<FMT, 2, 4, 8, 3>(a, s);
+    return launch<FMT, 2, 4, 8, 2>(a, s);
+  }
+  if (v == 1) return launch<FMT, 4, 2, 8, 3>(a, s);
+  return launch<FMT, 4, 2, 8, 2>(a, s);
 }
 
 }  // namespace

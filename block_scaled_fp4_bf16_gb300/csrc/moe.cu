@@ -1,5 +1,6 @@
 // Mixture of experts for a few tokens: the router, and the two products of the
 // chosen experts.
+#include <cstdlib>
 #include "few_tokens.cuh"
 
 namespace mx {
@@ -215,42 +216,33 @@ struct ExpertPolicy {
     r[0] = few::Run{map0, code_row, m0.scales + e * scale_bytes, in, scale_bytes};
     if constexpr (UP) r[1] = few::Run{map1, code_row, p.a.up.scales + e * scale_bytes, in, scale_bytes};
   }
-  template <typename Sums>
-  __device__ void finish(int item, const Sums &sums) const {
+  __device__ void put(int item, int wr, int m, int n, int lane, const float4 (&v)[kSegs]) const {
     const int e = g.expert[item / p.tiles], n_tokens = count(item);
     const float a0 = FMT == 1 ? (UP ? p.a.gate.ts : p.a.down.ts)[e] : 1.0f;
-    const float a1 = FMT == 1 && UP ? p.a.up.ts[e] : 1.0f;
-    constexpr int kM = UP ? MT / 2 : MT;
-    const int col_tiles = (n_tokens + 7) / 8;
+    float f[4] = {v[0].x * a0, v[0].y * a0, v[0].z * a0, v[0].w * a0};
+    if constexpr (UP) {
+      const float a1 = FMT == 1 ? p.a.up.ts[e] : 1.0f;
+      const float up[4] = {v[1].x * a1, v[1].y * a1, v[1].z * a1, v[1].w * a1};
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        float2 act;
+        if (p.a.gelu)
+          act = gelu_f32x2(make_float2(f[i], f[i + 1]));
+        else
+          act = make_float2(f[i] / (1.0f + expf(-f[i])), f[i + 1] / (1.0f + expf(-f[i + 1])));
+        f[i] = act.x * up[i];
+        f[i + 1] = act.y * up[i + 1];
+      }
+    }
+    const int row0 = (item % p.tiles * p.split.rows_w + wr) * kRows + m * 16 + (lane >> 2);
+    const int col0 = n * 8 + (lane & 3) * 2;
     const int64_t extent = static_cast<int64_t>(p.a.tokens) * p.a.top_k * rows();
-    for (int u = threadIdx.x; u < p.split.rows_w * kM * col_tiles * 32; u += blockDim.x) {
-      const int lane = u & 31, q = u >> 5;
-      const int n = q % col_tiles, m = q / col_tiles % kM, wr = q / (col_tiles * kM);
-      const float4 v = sums(wr, m, n, lane);
-      float f[4] = {v.x * a0, v.y * a0, v.z * a0, v.w * a0};
-      if constexpr (UP) {
-        const float4 w = sums(wr, m + kM, n, lane);
-        const float up[4] = {w.x * a1, w.y * a1, w.z * a1, w.w * a1};
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          float2 act;
-          if (p.a.gelu)
-            act = gelu_f32x2(make_float2(f[i], f[i + 1]));
-          else
-            act = make_float2(f[i] / (1.0f + expf(-f[i])), f[i + 1] / (1.0f + expf(-f[i + 1])));
-          f[i] = act.x * up[i];
-          f[i + 1] = act.y * up[i + 1];
-        }
-      }
-      const int row0 = (item % p.tiles * p.split.rows_w + wr) * kRows + m * 16 + (lane >> 2);
-      const int col0 = n * 8 + (lane & 3) * 2;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = row0 + (i >> 1) * 8, col = col0 + (i & 1);
-        if (row >= rows() || col >= n_tokens) continue;
-        const int64_t o = static_cast<int64_t>(pair(item, col)) * rows() + row;
-        if (in_bounds(o, 1, extent, p.a.status)) (UP ? p.a.h : p.a.z)[o] = f[i];
-      }
+    for (int i = 0; i < 4; ++i) {
+      const int row = row0 + (i >> 1) * 8, col = col0 + (i & 1);
+      if (row >= rows() || col >= n_tokens) continue;
+      const int64_t o = static_cast<int64_t>(pair(item, col)) * rows() + row;
+      if (in_bounds(o, 1, extent, p.a.status)) (UP ? p.a.h : p.a.z)[o] = f[i];
     }
   }
 };
@@ -315,19 +307,20 @@ cudaError_t launch_product(const MoeArgs &a, cudaStream_t s) {
   const int k = UP ? a.hidden : a.inter, rows = UP ? a.inter : a.hidden;
   const int pairs = a.tokens * a.top_k;
   const int group = pairs < 8 * NT ? pairs : 8 * NT;
-  const int budget = few::kMaxSmem - Groups::bytes(pairs);
-  MoeParams p{a, few::make_split(W, (k + few::kStageK - 1) / few::kStageK,
-                                 L::fitting_stages(group, budget)), 0, 8 * NT, 0};
-  const int tile = (UP ? 8 * MT : 16 * MT) * p.split.rows_w;
-  p.tiles = (rows + tile - 1) / tile;
-  p.groups_at = L::total(group, p.split.x_stages);
+  const int most = a.experts < pairs ? a.experts : pairs;  // experts with a pair
+  const int box = UP ? 8 * MT : 16 * MT;                   // output rows of a warp
+  const int64_t row_tiles = (rows + box - 1) / box, all = row_tiles * (most + pairs / (8 * NT));
+  const int64_t each = (all + a.num_sms - 1) / a.num_sms;
+  MoeParams p{a, L::split(group, (k + few::kStageK - 1) / few::kStageK, getenv("LEAST") ? atoi(getenv("LEAST")) : 1,
+                          static_cast<int>(each < 64 ? each : 64),
+                          few::kMaxSmem - Groups::bytes(pairs)), 0, 8 * NT, 0};
+  p.tiles = static_cast<int>((row_tiles + p.split.rows_w - 1) / p.split.rows_w);
+  p.groups_at = L::total(group, p.split);
   CUtensorMap map0, map1;
-  const int box = UP ? 8 * MT : 16 * MT;
   const int64_t stacked = static_cast<int64_t>(a.experts) * rows;
   if (!encode_few_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, box) ||
       !encode_few_map(&map1, UP ? a.up.codes : a.down.codes, stacked, k, box))
     return cudaErrorInvalidValue;
-  const int most = a.experts < pairs ? a.experts : pairs;
   const int64_t items = static_cast<int64_t>(most + pairs / (8 * NT)) * p.tiles;
   const int grid = items < a.num_sms ? static_cast<int>(items) : a.num_sms;
   return launch_pdl(kernel, dim3(grid), dim3(W * 32), p.groups_at + Groups::bytes(pairs), s, map0,
