@@ -960,9 +960,8 @@ size_t moe_h_bytes(int64_t pairs, int64_t inter) {
 size_t moe_z_bytes(int64_t pairs, int64_t hidden) {
   return round256(static_cast<size_t>(pairs) * static_cast<size_t>(hidden) * sizeof(float));
 }
-size_t moe_counter_bytes(int64_t hidden) {
-  return round256(static_cast<size_t>((hidden + mx::kMoeCounterRows - 1) / mx::kMoeCounterRows) *
-                  sizeof(uint32_t));
+size_t moe_images_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k) {
+  return round256(mx::moe_image_bytes(tokens, hidden) + mx::moe_image_bytes(tokens * top_k, inter));
 }
 
 int route_check(const char *fn, const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,
@@ -1072,8 +1071,9 @@ int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, c
   char *ws = static_cast<char *>(const_cast<void *>(workspace));
   a->h = reinterpret_cast<float *>(ws);
   a->z = reinterpret_cast<float *>(ws + moe_h_bytes(pairs, moe->inter));
-  a->counters = reinterpret_cast<uint32_t *>(ws + moe_h_bytes(pairs, moe->inter) +
-                                             moe_z_bytes(pairs, moe->hidden));
+  a->image = reinterpret_cast<uint8_t *>(a->z) + moe_z_bytes(pairs, moe->hidden);
+  a->factors = reinterpret_cast<float *>(
+      a->image + moe_images_bytes(tokens, moe->hidden, moe->inter, top_k));
   Range in[12];
   in[0] = span(x, row_bytes(tokens, moe->hidden, ld_x, 2));
   in[1] = span(ids, static_cast<uint64_t>(pairs) * 4);
@@ -1171,7 +1171,9 @@ MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t int
       hidden <= 0 || inter <= 0 || hidden >= (int64_t(1) << 31) || inter >= (int64_t(1) << 31))
     return 0;
   const int64_t pairs = tokens * top_k;
-  return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) + moe_counter_bytes(hidden);
+  return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) +
+         moe_images_bytes(tokens, hidden, inter, top_k) +
+         round256(static_cast<size_t>(tokens + pairs) * sizeof(float));
 }
 
 MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
@@ -1329,6 +1331,11 @@ bool encode_few_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k,
   return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_codes_window_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k,
+                             int box_rows) {
+  return encode_codes_map(tm, codes, rows, k, box_rows) == MX_OK;
 }
 
 bool kernel_setup_get(const void *func, int *value) {

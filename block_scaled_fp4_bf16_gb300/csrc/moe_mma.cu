@@ -1,0 +1,602 @@
+// The experts' products on the FP4 tensor cores, activations as sums of FP4.
+//
+// The weights' bytes bound these products, so no instruction should touch a
+// weight: codes and scales go from memory to the block-scaled FP4 product as
+// they lie.  For that the activations have to be FP4 too, without losing their
+// digits: a value is written as a sum of eight E2M1 digits,
+//     x = 2^e (q_0 + 2^-2 q_1 + 2^-5 q_2 + ... + 2^-20 q_7),   e for its block,
+// each digit the rounding of what the ones before it left (what is left after
+// q_0 is at most 1 of 6, after every other at most 1/2 of 4, so eight digits
+// reach 2^-21 of the block's scale: a BF16 value is exact unless its last bit
+// lies below that).  The digits of a token are eight rows of the product's
+// narrow operand, and the epilogue adds their eight sums in binary32.  The FP4
+// rate makes the eightfold product cheaper than converting the weights: M = 128,
+// N = 32 (four tokens), K = 64 a step.
+//
+// split_kernel makes the digits (an "image": for a row and 256 elements of K the
+// eight rows of 128 bytes as the product reads them, 128-byte swizzle included,
+// and their scales), expert_mma_kernel streams weights and images.
+#include "moe_groups.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kDigits = 8;
+constexpr int kImageK = 256;                   // elements of K of a stage
+constexpr int kImageCodes = kDigits * 128;     // bytes of codes
+// Bytes of scales: for each word of four blocks (MXFP4 two, NVFP4 four in a
+// stage) the eight rows' words, 16 bytes apart.
+template <int FMT>
+constexpr int kImageScales = (FMT == 0 ? 2 : 4) * kDigits * 16;
+constexpr int kImageBytes = kImageCodes + kImageScales<1>;  // of either format
+
+// Weight of digit p: 2^-kShift[p].
+__host__ __device__ constexpr int digit_shift(int p) { return p == 0 ? 0 : 3 * p - 1; }
+
+struct SplitParams {
+  const void *x;        // BF16 or FP32 rows
+  int64_t ld, extent;   // row stride, elements from x's base (bounds-checked build)
+  int rows, k, stages;
+  const int32_t *ids;   // a row whose id is outside 0..experts-1 is skipped (null: none is)
+  int experts;
+  uint8_t *image;       // [rows][stages][kImageBytes]
+  float *factors;       // NVFP4: [rows], the power of two of a row
+  uint32_t *status;
+};
+
+constexpr int kSplitWarps = 8;
+
+// Largest e with |v| <= 6 * 2^e for |v| <= top, as small as it can be; top > 0.
+__device__ __forceinline__ int block_exponent(float top) {
+  const uint32_t u = __float_as_uint(top);
+  if (u < 0x00800000u) return -127;  // subnormal: 2^-126 at most
+  const int e = static_cast<int>(u >> 23) - 127;
+  return (u & 0x007FFFFFu) > 0x00400000u ? e - 1 : e - 2;
+}
+
+// 2^e for -149 <= e <= 127.
+__device__ __forceinline__ float pow2(int e) {
+  return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23)
+                   : __uint_as_float(1u << (e + 149));
+}
+
+// Eight consecutive elements of row `r` from k0 + 8 lane (zeros past k).
+template <typename XT>
+__device__ __forceinline__ void load8(const SplitParams &p, int r, int at, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+  const int64_t off = r * p.ld + at;
+  if (at >= p.k || !in_bounds(off, 8, p.extent, p.status)) return;
+  const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + off);
+  if constexpr (sizeof(XT) == 2) {
+    const uint4 q = src[0];
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const uint4 q = src[j];
+      v[4 * j] = __uint_as_float(q.x), v[4 * j + 1] = __uint_as_float(q.y);
+      v[4 * j + 2] = __uint_as_float(q.z), v[4 * j + 3] = __uint_as_float(q.w);
+    }
+  }
+}
+
+// Row blockIdx.y, stages blockIdx.x * kSplitWarps ..: a warp makes the image of one
+// stage, eight elements a lane.  MXFP4: UE8M0 scales for 32 (four lanes), digit p
+// with the scale 2^(e - shift p); NVFP4: E4M3 for 16 (two lanes), a power of two
+// relative to the row's factor, the digits' weights left to the reader.  A block
+// that holds an infinity or NaN gets the scale NaN.
+template <int FMT, typename XT>
+__global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitParams p) {
+  __shared__ float tops[kSplitWarps];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (p.ids != nullptr) {
+    const int e = p.ids[r];
+    if (e < 0 || e >= p.experts) return;
+  }
+  const int stage = blockIdx.x * kSplitWarps + warp;
+  float v[8];
+  load8<XT>(p, r, stage * kImageK + lane * 8, v);
+  int row_e = 0;  // NVFP4: exponent of the row's factor
+  if constexpr (FMT == 1) {
+    float top = 0.0f;
+    for (int s = warp; s < p.stages; s += kSplitWarps) {
+      float u[8];
+      load8<XT>(p, r, s * kImageK + lane * 8, u);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float a = fabsf(u[i]);
+        if (a < __uint_as_float(0x7F800000u)) top = fmaxf(top, a);
+      }
+    }
+    top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, tops[w]);
+    // the largest block's scale becomes 2^8, the largest power of two of E4M3
+    row_e = max(block_exponent(top) - 8, -118);
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.factors[r] = pow2(row_e);
+  }
+  if (stage >= p.stages) return;
+  float top = 0.0f;
+  uint32_t odd = 0;  // an infinity or NaN here
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    top = fmaxf(top, fabsf(v[i]));
+    odd |= (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
+  }
+#pragma unroll
+  for (int m = 1; m < (FMT == 0 ? 4 : 2); m <<= 1) {
+    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
+    odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, m);
+  }
+  int e = block_exponent(top);
+  uint32_t byte;
+  if constexpr (FMT == 0) {
+    e = max(e, -127);
+    byte = odd ? 255u : static_cast<uint32_t>(e + 127);
+  } else {
+    const int j = min(max(e - row_e, -9), 8);  // 2^-9 is E4M3's least
+    e = row_e + j;
+    byte = odd ? 0x7Fu : j >= -6 ? static_cast<uint32_t>(j + 7) << 3 : 1u << (j + 9);
+  }
+  uint8_t *out = p.image + (static_cast<int64_t>(r) * p.stages + stage) * kImageBytes;
+  // v 2^-e, in two steps where one power of two would not be a normal number
+  const float f0 = pow2(min(-e, 100)), f1 = pow2(-e - min(-e, 100));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = odd ? 0.0f : v[i] * f0 * f1;
+#pragma unroll
+  for (int d = 0; d < kDigits; ++d) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = cvt_e2m1x2(v[2 * i], v[2 * i + 1]);
+      uint32_t h;
+      asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(c));
+      const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+      const float up = d == 0 ? 4.0f : 8.0f;
+      v[2 * i] = (v[2 * i] - q.x) * up;
+      v[2 * i + 1] = (v[2 * i + 1] - q.y) * up;
+      w |= c << (8 * i);
+    }
+    if (FMT == 0 && digit_shift(d) > e + 127) w = 0;  // no scale that small
+    // row d of the 8 x 128 byte tile, 16-byte chunk lane / 4, swizzled
+    *reinterpret_cast<uint32_t *>(out + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = w;
+  }
+  // scale words of four blocks, for each digit's row
+  constexpr int kWords = FMT == 0 ? 2 : 4;
+  uint32_t words[kWords] = {};
+#pragma unroll
+  for (int b = 0; b < 4 * kWords; ++b)
+    words[b / 4] |= __shfl_sync(0xFFFFFFFFu, byte, b * (8 / kWords)) << (8 * (b % 4));
+  if (lane < kDigits) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      uint32_t w = words[i];
+      if constexpr (FMT == 0) {
+        // 255 stays NaN; a digit whose scale would lie below 2^-127 is 0
+        const uint32_t nan = __vcmpeq4(w, 0xFFFFFFFFu);
+        w = __vsubus4(w, (lane == 0 ? 0u : 3u * lane - 1u) * 0x01010101u) | nan;
+      }
+      *reinterpret_cast<uint4 *>(out + kImageCodes + (i * kDigits + lane) * 16) =
+          make_uint4(w, 0, 0, 0);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- the product
+
+constexpr int kMmaWarps = 6;  // copies, product, four of the epilogue
+constexpr int kMmaThreads = kMmaWarps * 32;
+constexpr int kMaxSlots = 16;
+constexpr int kMmaSmem = 227 * 1024;
+
+struct MmaParams {
+  MoeArgs a;
+  const uint8_t *image;
+  const float *factors;
+  int stages;     // of 256 along K
+  int tiles;      // row tiles of an expert
+  int wrows;      // rows of a tile: 128, 64 or 32 (a part of a 128-row scale tile)
+  int slots;      // stages in flight
+  int bufs;       // accumulators (1 or 2)
+  int w_off, b_off, sfa_off, sfb_off, bar_off, groups_at;  // shared memory
+};
+
+// UP: gate and up rows, h as output; else rows of `hidden`, z as output.  An item
+// is a tile of wrows rows (of each matrix) times a group's tokens; a CTA walks
+// consecutive items, group-major.
+//
+// Shared memory: a ring of stages.  Weight slices of wrows x 128 bytes, one
+// after the other with (128 - wrows) x 128 guard bytes around the ring: the
+// product reads 128 rows with the slice at its place in the 128-row scale tile;
+// what the other rows hold is never read back.  Images: a kilobyte a token, and
+// its scales; a copy to tensor memory takes a word of K of four tokens, 32 rows
+// of 16 bytes, eight of them together.
+// Tensor memory: accumulators [bufs][SEGS][NB][32 columns], then a set of
+// scale columns for each stage in flight, four columns for each 512-byte copy.
+template <int FMT, bool UP, int NB>
+__global__ void __launch_bounds__(kMmaThreads, 1)
+    expert_mma_kernel(const __grid_constant__ CUtensorMap map0,
+                      const __grid_constant__ CUtensorMap map1, const __grid_constant__ MmaParams p) {
+  constexpr int kSegs = UP ? 2 : 1;
+  constexpr int kAtoms = FMT == 0 ? 2 : 4;       // scale tiles (4 blocks) of a stage
+  constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
+  constexpr int kSfaCols = kAtoms * 4;
+  constexpr int kSfb = kImageScales<FMT>;
+  constexpr int kStageImage = kImageCodes + kSfb;
+  extern __shared__ __align__(1024) char smem[];
+  const MoeArgs &a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int kGroup = 4 * NB;  // tokens of a group at most
+  const int slots = p.slots;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + p.bar_off);
+  uint64_t *empty = full + slots;
+  uint64_t *acc_full = empty + slots;   // [2]
+  uint64_t *acc_empty = acc_full + 2;   // [2]
+  uint64_t *done = acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  volatile uint32_t *abort = tmem_slot + 1;
+  if (smem_u32(smem) & 1023u) {  // the 128-byte swizzle needs 1024-byte aligned tiles
+    if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
+    return;
+  }
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < slots; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);
+      mbar_init(smem_u32(&empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&acc_full[i]), 1);
+      mbar_init(smem_u32(&acc_empty[i]), 4);
+    }
+    mbar_init(smem_u32(done), 1);
+    *abort = 0u;
+    fence_barrier_init();
+    prefetch_tmap(&map0);
+    if (UP) prefetch_tmap(&map1);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+  griddep_wait();
+  // (the scratch lies in the ring: the copies follow a barrier and a proxy fence)
+  const Groups g = make_groups<kMmaWarps>(smem + p.groups_at, smem + p.b_off, a.ids,
+                                          a.tokens * a.top_k, a.experts, kGroup, a.status);
+  fence_proxy_async_smem();
+  __syncthreads();
+  const int64_t items = static_cast<int64_t>(g.count) * p.tiles;
+  const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
+  const int end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+  const int rows = UP ? a.inter : a.hidden, k = UP ? a.hidden : a.inter;
+  const int katoms = (k / (FMT == 0 ? 32 : 16) + 3) >> 2;  // scale tiles along K
+  constexpr int acc_cols = kSegs * NB * 32;
+  const uint32_t sf_tmem = tmem + p.bufs * acc_cols;
+  constexpr int sf_cols = (kSegs + NB) * kSfaCols;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------ copies
+    uint32_t it = 0, s = 0, ph = 0;
+    bool ok = true;
+    for (int item = begin; item < end && ok; ++item) {
+      const int grp = item / p.tiles, tile = item - grp * p.tiles;
+      const int e = g.expert[grp], n = g.size[grp];
+      const int row0 = tile * p.wrows;
+      const int64_t scale_bytes = ((rows + 127) >> 7) * static_cast<int64_t>(katoms) * 512;
+      const int64_t scale_off = e * scale_bytes + static_cast<int64_t>(row0 >> 7) * katoms * 512;
+      const uint8_t *sf0 = (UP ? a.gate.scales : a.down.scales) + scale_off;
+      const uint8_t *sf1 = UP ? a.up.scales + scale_off : nullptr;
+      // this lane's token
+      const uint8_t *img = nullptr;
+      if (lane < n) {
+        const int q = g.list[g.begin[grp] + lane];
+        img = p.image + static_cast<int64_t>(UP ? q / a.top_k : q) * p.stages * kImageBytes;
+      }
+      for (int st = 0; st < p.stages; ++st, ++it) {
+        if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, a.status)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = smem_u32(&full[s]);
+        const uint32_t sf_bytes = static_cast<uint32_t>(min(kAtoms, katoms - st * kAtoms)) * 512u;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(fb, kSegs * (p.wrows * 128 + sf_bytes) + n * kStageImage);
+          const uint32_t w = smem_u32(smem + p.w_off) + s * kSegs * p.wrows * 128;
+          const uint32_t sf = smem_u32(smem + p.sfa_off) + s * kSegs * kSfa;
+          tma_load_2d(w, &map0, st * 128, e * rows + row0, fb);
+          bulk_load(sf, sf0 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
+          if constexpr (UP) {
+            tma_load_2d(w + p.wrows * 128, &map1, st * 128, e * rows + row0, fb);
+            bulk_load(sf + kSfa, sf1 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
+          }
+        }
+        __syncwarp();
+        if (lane < n) {
+          bulk_load(smem_u32(smem + p.b_off) + (s * kGroup + lane) * 1024,
+                    img + static_cast<int64_t>(st) * kImageBytes, kImageCodes, fb);
+          bulk_load(smem_u32(smem + p.sfb_off) + (s * kGroup + lane) * kSfb,
+                    img + static_cast<int64_t>(st) * kImageBytes + kImageCodes, kSfb, fb);
+        }
+        __syncwarp();
+        if (++s == static_cast<uint32_t>(slots)) s = 0, ph ^= 1u;
+      }
+    }
+    // no copy may land after the CTA has left
+    const uint32_t inflight = it < static_cast<uint32_t>(slots) ? it : static_cast<uint32_t>(slots);
+    for (uint32_t j = it - inflight; j < it; ++j)
+      mbar_drain(smem_u32(&full[j % slots]), (j / slots) & 1u);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ product
+    uint32_t s = 0, ph = 0, buf = 0, bph = 0;
+    bool ok = true;
+    // One thread issues every product, so a product has to cost it few
+    // instructions: the loops are unrolled and descriptors stepped by constants.
+    constexpr uint32_t idesc0 = mma_idesc<FMT>(128, 32, 0), idesc2 = mma_idesc<FMT>(128, 32, 2);
+    const uint32_t w_ring = smem_u32(smem + p.w_off), b_ring = smem_u32(smem + p.b_off);
+    const uint32_t sfa_ring = smem_u32(smem + p.sfa_off), sfb_ring = smem_u32(smem + p.sfb_off);
+    const uint32_t seg_step = static_cast<uint32_t>(p.wrows * 128) >> 4;
+    for (int item = begin; item < end && ok; ++item) {
+      const int grp = item / p.tiles, tile = item - grp * p.tiles;
+      const int nb = (g.size[grp] + 3) >> 2;
+      const int h_row = tile * p.wrows & 127;
+      ok = mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, a.status);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * acc_cols;
+      for (int st = 0; st < p.stages; ++st) {
+        if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort, a.status)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint32_t sfa_t = sf_tmem + s * sf_cols, sfb_t = sfa_t + kSegs * kSfaCols;
+          const uint64_t sfa = smem_desc_scale_block(sfa_ring + s * kSegs * kSfa);
+          const uint64_t sfb = smem_desc_scale_rows(sfb_ring + s * kGroup * kSfb, kSfb);
+          const int atoms = min(kAtoms, katoms - st * kAtoms);
+          const int steps = min(4, (k - st * kImageK + 63) >> 6);  // of 64 inside K
+#pragma unroll
+          for (int i = 0; i < NB; ++i) {
+            if (i < nb) {
+#pragma unroll
+              for (int j = 0; j < kAtoms; ++j)
+                tc_cp_32x128b_warpx4(sfb_t + i * kSfaCols + j * 4,
+                                     sfb + ((i * 4 * kSfb + j * 128) >> 4));
+            }
+          }
+#pragma unroll
+          for (int m = 0; m < kSegs; ++m) {
+#pragma unroll
+            for (int i = 0; i < kAtoms; ++i) {
+              if (i < atoms)
+                tc_cp_32x128b_warpx4(sfa_t + m * kSfaCols + i * 4,
+                                     sfa + ((m * kSfa + i * 512) >> 4));
+            }
+          }
+          const uint64_t wd =
+              smem_desc_sw128_kmajor(w_ring + s * kSegs * p.wrows * 128 - h_row * 128);
+          const uint64_t bd = smem_desc_sw128_kmajor(b_ring + s * kGroup * 1024);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk) {
+            if (kk < steps) {
+              const int word = FMT == 0 ? kk >> 1 : kk;
+              const uint32_t idesc = FMT == 0 && (kk & 1) ? idesc2 : idesc0;
+#pragma unroll
+              for (int m = 0; m < kSegs; ++m) {
+#pragma unroll
+                for (int i = 0; i < NB; ++i) {
+                  if (i < nb)
+                    tc_mma_block_scaled<FMT>(acc + (m * NB + i) * 32, wd + m * seg_step + 2 * kk,
+                                             bd + i * 256 + 2 * kk, idesc,
+                                             sfa_t + m * kSfaCols + word * 4,
+                                             sfb_t + i * kSfaCols + word * 4,
+                                             kk > 0 || st > 0 ? 1u : 0u);
+                }
+              }
+            }
+          }
+          tc_commit(smem_u32(&empty[s]));
+          if (st == p.stages - 1) tc_commit(smem_u32(&acc_full[buf]));
+        }
+        __syncwarp();
+        if (++s == static_cast<uint32_t>(slots)) s = 0, ph ^= 1u;
+      }
+      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, bph ^= 1u;
+    }
+    // every product issued has finished before the tensor memory goes
+    if (elect_one()) tc_commit(smem_u32(done));
+    __syncwarp();
+    mbar_drain(smem_u32(done), 0u);
+  } else {
+    // ------------------------------------------------------------ epilogue
+    const int q = warp & 3;  // this warp's lane quarter
+    uint32_t buf = 0, bph = 0;
+    const int64_t out_extent = static_cast<int64_t>(a.tokens) * a.top_k * rows;
+    for (int item = begin; item < end; ++item) {
+      const int grp = item / p.tiles, tile = item - grp * p.tiles;
+      const int e = g.expert[grp], n = g.size[grp];
+      const int row0 = tile * p.wrows, h_row = row0 & 127;
+      const int row = (row0 & ~127) + q * 32 + lane;
+      const bool mine = q * 32 >= h_row && q * 32 < h_row + p.wrows && row < rows;
+      const float alpha0 = FMT == 1 ? (UP ? a.gate.ts : a.down.ts)[e] : 1.0f;
+      const float alpha1 = FMT == 1 && UP ? a.up.ts[e] : 1.0f;
+      if (!mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status)) break;
+      tc_fence_after();
+      const uint32_t acc = tmem + buf * acc_cols + (static_cast<uint32_t>(q * 32) << 16);
+      for (int i = 0; i < (n + 3) / 4; ++i) {
+        float sum[kSegs][4];
+#pragma unroll
+        for (int m = 0; m < kSegs; ++m) {
+          uint32_t r[32];
+          tc_ld_32x32b_x32(acc + (m * NB + i) * 32, r);
+          tc_wait_ld();
+          // the digits' sums, the least first
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float t = 0.0f;
+#pragma unroll
+            for (int d = kDigits - 1; d >= 0; --d) {
+              const float v = __uint_as_float(r[j * 8 + d]);
+              if constexpr (FMT == 0)
+                t = __fadd_rn(t, v);
+              else
+                t = __fmaf_rn(v, 1.0f / static_cast<float>(1 << digit_shift(d)), t);
+            }
+            sum[m][j] = t;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = i * 4 + j;
+          if (c >= n || !mine) continue;
+          const int pair = g.list[g.begin[grp] + c];
+          const float f = FMT == 1 ? p.factors[UP ? pair / a.top_k : pair] : 1.0f;
+          float v = FMT == 1 ? sum[0][j] * f * alpha0 : sum[0][j];
+          if constexpr (UP) {
+            const float u = FMT == 1 ? sum[1][j] * f * alpha1 : sum[1][j];
+            const float act = a.gelu ? gelu_f32x2(make_float2(v, v)).x : v / (1.0f + expf(-v));
+            v = act * u;
+          }
+          const int64_t o = static_cast<int64_t>(pair) * rows + row;
+          if (in_bounds(o, 1, out_extent, a.status)) (UP ? a.h : a.z)[o] = v;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
+      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, bph ^= 1u;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int FMT, typename XT>
+cudaError_t launch_split(const MoeArgs &a, const void *x, int64_t ld, int rows, int k,
+                         const int32_t *ids, uint8_t *image, float *factors, cudaStream_t s) {
+  SplitParams p{};
+  p.x = x;
+  p.ld = ld;
+  p.extent = (rows - 1) * ld + k;
+  p.rows = rows;
+  p.k = k;
+  p.stages = (k + kImageK - 1) / kImageK;
+  p.ids = ids;
+  p.experts = a.experts;
+  p.image = image;
+  p.factors = factors;
+  p.status = a.status;
+  return launch_pdl(split_kernel<FMT, XT>, dim3((p.stages + kSplitWarps - 1) / kSplitWarps, rows),
+                    dim3(kSplitWarps * 32), 0, s, p);
+}
+
+template <int FMT, bool UP, int NB>
+cudaError_t launch_mma(const MoeArgs &a, const uint8_t *image, const float *factors, cudaStream_t s) {
+  constexpr int kSegs = UP ? 2 : 1, kAtoms = FMT == 0 ? 2 : 4;
+  const auto kernel = expert_mma_kernel<FMT, UP, NB>;
+  const void *func = reinterpret_cast<const void *>(kernel);
+  if (!kernel_setup_get(func, nullptr)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+    if (e != cudaSuccess) return e;
+    kernel_setup_put(func, 0);
+  }
+  const int rows = UP ? a.inter : a.hidden, k = UP ? a.hidden : a.inter;
+  const int pairs = a.tokens * a.top_k;
+  MmaParams p{};
+  p.a = a;
+  p.image = image;
+  p.factors = factors;
+  p.stages = (k + kImageK - 1) / kImageK;
+  constexpr int kGroup = 4 * NB;
+  const int most = a.experts < pairs ? a.experts : pairs;  // experts with a pair
+  // rows of a tile: whole 128 unless that leaves SMs without an item
+  p.wrows = 128;
+  if (UP) p.wrows = 64;
+  while (p.wrows > 32 && static_cast<int64_t>(most) * ((rows + p.wrows - 1) / p.wrows) < a.num_sms)
+    p.wrows /= 2;
+  if (UP && a.tokens > 8) p.wrows = 128;
+  p.tiles = (rows + p.wrows - 1) / p.wrows;
+  const int guard = (128 - p.wrows) * 128;
+  const int per_slot =
+      kSegs * (p.wrows * 128 + kAtoms * 512) + kGroup * (kImageCodes + kImageScales<FMT>);
+  const int fixed = 2 * guard + 3 * 1024 + 512 + Groups::bytes(pairs);
+  constexpr int sf_cols = (kSegs + NB) * kAtoms * 4, acc = kSegs * NB * 32;
+  int slots = (kMmaSmem - fixed) / per_slot;
+  slots = slots < kMaxSlots ? slots : kMaxSlots;
+  p.bufs = 2 * acc + 4 * sf_cols <= 512 ? 2 : 1;
+  const int tmem_slots = (512 - p.bufs * acc) / sf_cols;
+  p.slots = slots < tmem_slots ? slots : tmem_slots;
+  if (p.slots < 2) return cudaErrorInvalidValue;
+  const auto up1k = [](int v) { return (v + 1023) / 1024 * 1024; };
+  p.w_off = up1k(guard);
+  p.b_off = up1k(p.w_off + p.slots * kSegs * p.wrows * 128 + guard);
+  p.sfa_off = p.b_off + p.slots * kGroup * 1024;
+  p.sfb_off = p.sfa_off + p.slots * kSegs * kAtoms * 512;
+  p.bar_off = p.sfb_off + p.slots * kGroup * kImageScales<FMT>;
+  p.groups_at = p.bar_off + 8 * (2 * p.slots + 5) + 16;
+  const int smem = p.groups_at + Groups::bytes(pairs);
+  // the groups' scratch lies in the images' part of the ring
+  if (smem > kMmaSmem || p.slots * kGroup * 1024 < 2 * kMmaWarps * a.experts)
+    return cudaErrorInvalidValue;
+  CUtensorMap map0, map1;
+  const int64_t stacked = static_cast<int64_t>(a.experts) * rows;
+  if (!encode_codes_window_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, p.wrows) ||
+      !encode_codes_window_map(&map1, UP ? a.up.codes : a.down.codes, stacked, k, p.wrows))
+    return cudaErrorInvalidValue;
+  const int64_t items = static_cast<int64_t>(most + pairs / kGroup) * p.tiles;
+  const int grid = items < a.num_sms ? static_cast<int>(items) : a.num_sms;
+  return launch_pdl(kernel, dim3(grid), dim3(kMmaThreads), smem, s, map0, map1, p);
+}
+
+template <int FMT, bool UP>
+cudaError_t launch_product(const MoeArgs &a, const uint8_t *image, const float *factors,
+                           cudaStream_t s) {
+  if (a.tokens <= 4) return launch_mma<FMT, UP, 1>(a, image, factors, s);
+  if (a.tokens <= 8) return launch_mma<FMT, UP, 2>(a, image, factors, s);
+  return launch_mma<FMT, UP, 3>(a, image, factors, s);
+}
+
+template <int FMT>
+cudaError_t launch_all(const MoeArgs &a, cudaStream_t s) {
+  const int pairs = a.tokens * a.top_k;
+  cudaError_t e = launch_split<FMT, uint16_t>(a, a.x, a.ld_x, a.tokens, a.hidden, nullptr, a.image,
+                                              a.factors, s);
+  if (e == cudaSuccess) e = launch_product<FMT, true>(a, a.image, a.factors, s);
+  uint8_t *himage = a.image + moe_image_bytes(a.tokens, a.hidden);
+  if (e == cudaSuccess)
+    e = launch_split<FMT, float>(a, a.h, a.inter, pairs, a.inter, a.ids, himage, a.factors + a.tokens, s);
+  if (e == cudaSuccess) e = launch_product<FMT, false>(a, himage, a.factors + a.tokens, s);
+  return e;
+}
+
+}  // namespace
+
+size_t moe_image_bytes(int64_t rows, int64_t k) {
+  return static_cast<size_t>(rows) * static_cast<size_t>((k + kImageK - 1) / kImageK) * kImageBytes;
+}
+
+cudaError_t launch_expert_products(const MoeArgs &a, cudaStream_t s) {
+  return a.fmt == 0 ? launch_all<0>(a, s) : launch_all<1>(a, s);
+}
+
+}  // namespace mx

@@ -190,6 +190,9 @@ struct FewMatrix {
 // 64 bytes (128 codes) x box_rows rows, 64-byte swizzle, zeros outside (api.cu).
 // false when it could not be encoded.
 bool encode_few_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k, int box_rows);
+// The same with boxes of 128 bytes (256 codes), 128-byte swizzle.
+bool encode_codes_window_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k,
+                             int box_rows);
 
 // y[t, n] = epilogue(sum_k x[t, k] W[n, k]) for tokens <= kLinearMaxTokens.
 constexpr int kLinearMaxTokens = 32;
@@ -238,11 +241,15 @@ struct MoeArgs {
   int64_t ld_y;
   float *h;            // [tokens * top_k, inter]
   float *z;            // [tokens * top_k, hidden]
-  uint32_t *counters;  // one per kMoeCounterRows rows of hidden
+  uint8_t *image;      // digits of x, then of h (moe_image_bytes)
+  float *factors;      // NVFP4: of the rows of x, then of h
   int num_sms;
   uint32_t *status;
 };
-constexpr int kMoeCounterRows = 32;
+// Bytes of the digits of `rows` rows of k activations.
+size_t moe_image_bytes(int64_t rows, int64_t k);
+// h and z (moe_mma.cu), and then y.
+cudaError_t launch_expert_products(const MoeArgs &a, cudaStream_t s);
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
 
 // Launch with programmatic stream serialization (the kernel itself orders
