@@ -961,7 +961,8 @@ size_t moe_z_bytes(int64_t pairs, int64_t hidden) {
   return round256(static_cast<size_t>(pairs) * static_cast<size_t>(hidden) * sizeof(float));
 }
 size_t moe_images_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k) {
-  return round256(mx::moe_image_bytes(tokens, hidden) + mx::moe_image_bytes(tokens * top_k, inter));
+  return round256(mx::moe_image_bytes(tokens * top_k, hidden) +
+                  mx::moe_image_bytes(tokens * top_k, inter));
 }
 
 int route_check(const char *fn, const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,
@@ -1074,6 +1075,8 @@ int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, c
   a->image = reinterpret_cast<uint8_t *>(a->z) + moe_z_bytes(pairs, moe->hidden);
   a->factors = reinterpret_cast<float *>(
       a->image + moe_images_bytes(tokens, moe->hidden, moe->inter, top_k));
+  a->plan = reinterpret_cast<char *>(a->factors) +
+            round256(static_cast<size_t>(2 * pairs) * sizeof(float));
   Range in[12];
   in[0] = span(x, row_bytes(tokens, moe->hidden, ld_x, 2));
   in[1] = span(ids, static_cast<uint64_t>(pairs) * 4);
@@ -1173,7 +1176,8 @@ MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t int
   const int64_t pairs = tokens * top_k;
   return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) +
          moe_images_bytes(tokens, hidden, inter, top_k) +
-         round256(static_cast<size_t>(tokens + pairs) * sizeof(float));
+         round256(static_cast<size_t>(2 * pairs) * sizeof(float)) +
+         round256(mx::moe_plan_bytes(pairs));
 }
 
 MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,

@@ -15,7 +15,11 @@
 //
 // split_kernel makes the digits (an "image": for a row and 256 elements of K the
 // eight rows of 128 bytes as the product reads them, 128-byte swizzle included,
-// and their scales), expert_mma_kernel streams weights and images.
+// and their scales), expert_mma_kernel streams weights and images.  The images'
+// rows are the (token, slot) pairs sorted by expert, so that a group's lie
+// together and come with two copies a stage.
+#include <cuda_fp16.h>
+
 #include "moe_groups.cuh"
 
 namespace mx {
@@ -24,23 +28,25 @@ namespace {
 constexpr int kDigits = 8;
 constexpr int kImageK = 256;                   // elements of K of a stage
 constexpr int kImageCodes = kDigits * 128;     // bytes of codes
-// Bytes of scales: for each word of four blocks (MXFP4 two, NVFP4 four in a
-// stage) the eight rows' words, 16 bytes apart.
+// Bytes of a group's scales: a scale tile of 128 rows (16 pairs' digits) and four
+// blocks, two (MXFP4) or four (NVFP4) of them a stage.
 template <int FMT>
-constexpr int kImageScales = (FMT == 0 ? 2 : 4) * kDigits * 16;
-constexpr int kImageBytes = kImageCodes + kImageScales<1>;  // of either format
-
+constexpr int kImageScales = (FMT == 0 ? 2 : 4) * 512;
+static_assert(kMoeGroupMax * kDigits == 128, "a group's digits fill a scale tile");
 // Weight of digit p: 2^-kShift[p].
 __host__ __device__ constexpr int digit_shift(int p) { return p == 0 ? 0 : 3 * p - 1; }
 
 struct SplitParams {
   const void *x;        // BF16 or FP32 rows
   int64_t ld, extent;   // row stride, elements from x's base (bounds-checked build)
-  int rows, k, stages;
-  const int32_t *ids;   // a row whose id is outside 0..experts-1 is skipped (null: none is)
-  int experts;
-  uint8_t *image;       // [rows][stages][kImageBytes]
-  float *factors;       // NVFP4: [rows], the power of two of a row
+  int k, stages;
+  const int32_t *ids;   // [pairs]
+  int pairs, experts;
+  int top_k, group;     // pairs of a group at most
+  uint8_t *codes;       // [stages][pairs][kImageCodes], rows by place
+  uint8_t *scales;      // [stages][groups][kImageScales]
+  float *factors;       // NVFP4: [pairs], the power of two of a place
+  char *plan;           // Groups and the places' members (written for x, read for h)
   uint32_t *status;
 };
 
@@ -86,20 +92,37 @@ __device__ __forceinline__ void load8(const SplitParams &p, int r, int at, float
   }
 }
 
-// Row blockIdx.y, stages blockIdx.x * kSplitWarps ..: a warp makes the image of one
-// stage, eight elements a lane.  MXFP4: UE8M0 scales for 32 (four lanes), digit p
+// Row blockIdx.y (x: a token, which goes to the places of its pairs; h: a place),
+// stages blockIdx.x * kSplitWarps ..: a warp makes the image of one stage, eight
+// elements a lane.  MXFP4: UE8M0 scales for 32 (four lanes), digit p
 // with the scale 2^(e - shift p); NVFP4: E4M3 for 16 (two lanes), a power of two
 // relative to the row's factor, the digits' weights left to the reader.  A block
 // that holds an infinity or NaN gets the scale NaN.
 template <int FMT, typename XT>
 __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitParams p) {
   __shared__ float tops[kSplitWarps];
+  constexpr int kPairs = kMoeMaxTokens * kMoeMaxTopK;
+  constexpr bool kGather = sizeof(XT) == 2;  // x: tokens to places
+  __shared__ __align__(16) char groups[kGather ? Groups::bytes(kPairs) : 16];
+  __shared__ __align__(16) char scratch[kGather ? 2 * (kSplitWarps + 2) * kMoeMaxExperts : 16];
+  __shared__ uint16_t places[kGather ? kPairs : 1], members[kGather ? kPairs : 1];
   griddep_launch_dependents();
   griddep_wait();
   const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (p.ids != nullptr) {
-    const int e = p.ids[r];
-    if (e < 0 || e >= p.experts) return;
+  uint16_t *plan_members = reinterpret_cast<uint16_t *>(p.plan + Groups::bytes(p.pairs));
+  if constexpr (kGather) {
+    make_groups<kSplitWarps>(Groups::at(groups, p.pairs), places, members, scratch, p.ids, p.pairs,
+                             p.experts, p.group, p.status);
+    if (blockIdx.x == 0 && r == 0) {
+      for (int i = threadIdx.x; i < Groups::bytes(p.pairs) / 4; i += kSplitWarps * 32)
+        reinterpret_cast<uint32_t *>(p.plan)[i] = reinterpret_cast<const uint32_t *>(groups)[i];
+      for (int i = threadIdx.x; i < p.pairs; i += kSplitWarps * 32) plan_members[i] = members[i];
+    }
+  } else {
+    // the places behind the last group's are empty
+    const Groups g = Groups::at(p.plan, p.pairs);
+    const int n = *g.count;
+    if (n == 0 || r >= g.begin[n - 1] + g.size[n - 1]) return;
   }
   const int stage = blockIdx.x * kSplitWarps + warp;
   float v[8];
@@ -123,7 +146,16 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
     for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, tops[w]);
     // the largest block's scale becomes 2^8, the largest power of two of E4M3
     row_e = max(block_exponent(top) - 8, -118);
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.factors[r] = pow2(row_e);
+    if (blockIdx.x == 0) {
+      if constexpr (kGather) {
+        if (threadIdx.x < static_cast<unsigned>(p.top_k)) {
+          const int at = places[r * p.top_k + threadIdx.x];
+          if (at != 0xFFFF) p.factors[at] = pow2(row_e);
+        }
+      } else if (threadIdx.x == 0) {
+        p.factors[r] = pow2(row_e);
+      }
+    }
   }
   if (stage >= p.stages) return;
   float top = 0.0f;
@@ -148,7 +180,9 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
     e = row_e + j;
     byte = odd ? 0x7Fu : j >= -6 ? static_cast<uint32_t>(j + 7) << 3 : 1u << (j + 9);
   }
-  uint8_t *out = p.image + (static_cast<int64_t>(r) * p.stages + stage) * kImageBytes;
+  // the places of this row
+  const int copies = kGather ? p.top_k : 1;
+  const auto place = [&](int j) { return kGather ? static_cast<int>(places[r * p.top_k + j]) : r; };
   // v 2^-e, in two steps where one power of two would not be a normal number
   const float f0 = pow2(min(-e, 100)), f1 = pow2(-e - min(-e, 100));
 #pragma unroll
@@ -169,7 +203,13 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
     }
     if (FMT == 0 && digit_shift(d) > e + 127) w = 0;  // no scale that small
     // row d of the 8 x 128 byte tile, 16-byte chunk lane / 4, swizzled
-    *reinterpret_cast<uint32_t *>(out + d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4) = w;
+    const int at = d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4;
+    for (int j = 0; j < copies; ++j) {
+      const int to = place(j);
+      if (to != 0xFFFF)
+        *reinterpret_cast<uint32_t *>(
+            p.codes + (static_cast<int64_t>(stage) * p.pairs + to) * kImageCodes + at) = w;
+    }
   }
   // scale words of four blocks, for each digit's row
   constexpr int kWords = FMT == 0 ? 2 : 4;
@@ -186,8 +226,17 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
         const uint32_t nan = __vcmpeq4(w, 0xFFFFFFFFu);
         w = __vsubus4(w, (lane == 0 ? 0u : 3u * lane - 1u) * 0x01010101u) | nan;
       }
-      *reinterpret_cast<uint4 *>(out + kImageCodes + (i * kDigits + lane) * 16) =
-          make_uint4(w, 0, 0, 0);
+      for (int j = 0; j < copies; ++j) {
+        const int to = place(j);
+        if (to == 0xFFFF) continue;
+        // digit rows of a group in the order of a scale tile: row c at c % 32, word c / 32
+        const int member = kGather ? members[to] : plan_members[to];
+        const int m = member % kMoeGroupMax;
+        *reinterpret_cast<uint32_t *>(
+            p.scales +
+            (static_cast<int64_t>(stage) * p.pairs + member / kMoeGroupMax) * kImageScales<FMT> +
+            i * 512 + ((m & 3) * kDigits + lane) * 16 + (m >> 2) * 4) = w;
+      }
     }
   }
 }
@@ -201,7 +250,7 @@ constexpr int kMmaSmem = 227 * 1024;
 
 struct MmaParams {
   MoeArgs a;
-  const uint8_t *image;
+  const uint8_t *image, *image_scales;
   const float *factors;
   int stages;     // of 256 along K
   int tiles;      // row tiles of an expert
@@ -218,11 +267,10 @@ struct MmaParams {
 // Shared memory: a ring of stages.  Weight slices of wrows x 128 bytes, one
 // after the other with (128 - wrows) x 128 guard bytes around the ring: the
 // product reads 128 rows with the slice at its place in the 128-row scale tile;
-// what the other rows hold is never read back.  Images: a kilobyte a token, and
-// its scales; a copy to tensor memory takes a word of K of four tokens, 32 rows
-// of 16 bytes, eight of them together.
+// what the other rows hold is never read back.  Images: a kilobyte a pair, and the
+// group's scale tiles.
 // Tensor memory: accumulators [bufs][SEGS][NB][32 columns], then a set of
-// scale columns for each stage in flight, four columns for each 512-byte copy.
+// scale columns for each stage in flight, four columns for each scale tile.
 template <int FMT, bool UP, int NB>
 __global__ void __launch_bounds__(kMmaThreads, 1)
     expert_mma_kernel(const __grid_constant__ CUtensorMap map0,
@@ -232,7 +280,6 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
   constexpr int kSfaCols = kAtoms * 4;
   constexpr int kSfb = kImageScales<FMT>;
-  constexpr int kStageImage = kImageCodes + kSfb;
   extern __shared__ __align__(1024) char smem[];
   const MoeArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -274,19 +321,19 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
   griddep_wait();
-  // (the scratch lies in the ring: the copies follow a barrier and a proxy fence)
-  const Groups g = make_groups<kMmaWarps>(smem + p.groups_at, smem + p.b_off, a.ids,
-                                          a.tokens * a.top_k, a.experts, kGroup, a.status);
-  fence_proxy_async_smem();
+  const int pairs = a.tokens * a.top_k;
+  for (int i = threadIdx.x; i < Groups::bytes(pairs) / 16; i += kMmaThreads)
+    reinterpret_cast<uint4 *>(smem + p.groups_at)[i] = reinterpret_cast<const uint4 *>(a.plan)[i];
   __syncthreads();
-  const int64_t items = static_cast<int64_t>(g.count) * p.tiles;
+  const Groups g = Groups::at(smem + p.groups_at, pairs);
+  const int64_t items = static_cast<int64_t>(*g.count) * p.tiles;
   const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
   const int end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
   const int rows = UP ? a.inter : a.hidden, k = UP ? a.hidden : a.inter;
   const int katoms = (k / (FMT == 0 ? 32 : 16) + 3) >> 2;  // scale tiles along K
   constexpr int acc_cols = kSegs * NB * 32;
   const uint32_t sf_tmem = tmem + p.bufs * acc_cols;
-  constexpr int sf_cols = (kSegs + NB) * kSfaCols;
+  constexpr int sf_cols = (kSegs + 1) * kSfaCols;
 
   if (warp == 0) {
     // ------------------------------------------------------------ copies
@@ -300,12 +347,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
       const int64_t scale_off = e * scale_bytes + static_cast<int64_t>(row0 >> 7) * katoms * 512;
       const uint8_t *sf0 = (UP ? a.gate.scales : a.down.scales) + scale_off;
       const uint8_t *sf1 = UP ? a.up.scales + scale_off : nullptr;
-      // this lane's token
-      const uint8_t *img = nullptr;
-      if (lane < n) {
-        const int q = g.list[g.begin[grp] + lane];
-        img = p.image + static_cast<int64_t>(UP ? q / a.top_k : q) * p.stages * kImageBytes;
-      }
+      const int64_t place = g.begin[grp];
       for (int st = 0; st < p.stages; ++st, ++it) {
         if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, a.status)) {
           ok = false;
@@ -314,7 +356,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const uint32_t fb = smem_u32(&full[s]);
         const uint32_t sf_bytes = static_cast<uint32_t>(min(kAtoms, katoms - st * kAtoms)) * 512u;
         if (elect_one()) {
-          mbar_arrive_expect_tx(fb, kSegs * (p.wrows * 128 + sf_bytes) + n * kStageImage);
+          mbar_arrive_expect_tx(fb, kSegs * (p.wrows * 128 + sf_bytes) + n * kImageCodes + kSfb);
           const uint32_t w = smem_u32(smem + p.w_off) + s * kSegs * p.wrows * 128;
           const uint32_t sf = smem_u32(smem + p.sfa_off) + s * kSegs * kSfa;
           tma_load_2d(w, &map0, st * 128, e * rows + row0, fb);
@@ -323,13 +365,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
             tma_load_2d(w + p.wrows * 128, &map1, st * 128, e * rows + row0, fb);
             bulk_load(sf + kSfa, sf1 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
           }
-        }
-        __syncwarp();
-        if (lane < n) {
-          bulk_load(smem_u32(smem + p.b_off) + (s * kGroup + lane) * 1024,
-                    img + static_cast<int64_t>(st) * kImageBytes, kImageCodes, fb);
-          bulk_load(smem_u32(smem + p.sfb_off) + (s * kGroup + lane) * kSfb,
-                    img + static_cast<int64_t>(st) * kImageBytes + kImageCodes, kSfb, fb);
+          const int64_t at = static_cast<int64_t>(st) * pairs;
+          bulk_load(smem_u32(smem + p.b_off) + s * kGroup * kImageCodes,
+                    p.image + (at + place) * kImageCodes, n * kImageCodes, fb);
+          bulk_load(smem_u32(smem + p.sfb_off) + s * kSfb, p.image_scales + (at + grp) * kSfb, kSfb,
+                    fb);
         }
         __syncwarp();
         if (++s == static_cast<uint32_t>(slots)) s = 0, ph ^= 1u;
@@ -345,13 +385,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     bool ok = true;
     // One thread issues every product, so a product has to cost it few
     // instructions: the loops are unrolled and descriptors stepped by constants.
-    constexpr uint32_t idesc0 = mma_idesc<FMT>(128, 32, 0), idesc2 = mma_idesc<FMT>(128, 32, 2);
     const uint32_t w_ring = smem_u32(smem + p.w_off), b_ring = smem_u32(smem + p.b_off);
     const uint32_t sfa_ring = smem_u32(smem + p.sfa_off), sfb_ring = smem_u32(smem + p.sfb_off);
     const uint32_t seg_step = static_cast<uint32_t>(p.wrows * 128) >> 4;
     for (int item = begin; item < end && ok; ++item) {
       const int grp = item / p.tiles, tile = item - grp * p.tiles;
-      const int nb = (g.size[grp] + 3) >> 2;
+      // columns: the digits of the group, to a multiple of 16
+      const uint32_t columns = static_cast<uint32_t>(g.size[grp] * kDigits + 15) & ~15u;
+      const uint32_t idesc0 = mma_idesc<FMT>(128, columns, 0);
+      const uint32_t idesc2 = mma_idesc<FMT>(128, columns, 2);
       const int h_row = tile * p.wrows & 127;
       ok = mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, a.status);
       if (!ok) break;
@@ -366,18 +408,12 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         if (elect_one()) {
           const uint32_t sfa_t = sf_tmem + s * sf_cols, sfb_t = sfa_t + kSegs * kSfaCols;
           const uint64_t sfa = smem_desc_scale_block(sfa_ring + s * kSegs * kSfa);
-          const uint64_t sfb = smem_desc_scale_rows(sfb_ring + s * kGroup * kSfb, kSfb);
+          const uint64_t sfb = smem_desc_scale_block(sfb_ring + s * kSfb);
           const int atoms = min(kAtoms, katoms - st * kAtoms);
           const int steps = min(4, (k - st * kImageK + 63) >> 6);  // of 64 inside K
 #pragma unroll
-          for (int i = 0; i < NB; ++i) {
-            if (i < nb) {
-#pragma unroll
-              for (int j = 0; j < kAtoms; ++j)
-                tc_cp_32x128b_warpx4(sfb_t + i * kSfaCols + j * 4,
-                                     sfb + ((i * 4 * kSfb + j * 128) >> 4));
-            }
-          }
+          for (int j = 0; j < kAtoms; ++j)
+            tc_cp_32x128b_warpx4(sfb_t + j * 4, sfb + ((j * 512) >> 4));
 #pragma unroll
           for (int m = 0; m < kSegs; ++m) {
 #pragma unroll
@@ -396,17 +432,10 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
               const int word = FMT == 0 ? kk >> 1 : kk;
               const uint32_t idesc = FMT == 0 && (kk & 1) ? idesc2 : idesc0;
 #pragma unroll
-              for (int m = 0; m < kSegs; ++m) {
-#pragma unroll
-                for (int i = 0; i < NB; ++i) {
-                  if (i < nb)
-                    tc_mma_block_scaled<FMT>(acc + (m * NB + i) * 32, wd + m * seg_step + 2 * kk,
-                                             bd + i * 256 + 2 * kk, idesc,
-                                             sfa_t + m * kSfaCols + word * 4,
-                                             sfb_t + i * kSfaCols + word * 4,
-                                             kk > 0 || st > 0 ? 1u : 0u);
-                }
-              }
+              for (int m = 0; m < kSegs; ++m)
+                tc_mma_block_scaled<FMT>(acc + m * NB * 32, wd + m * seg_step + 2 * kk, bd + 2 * kk,
+                                         idesc, sfa_t + m * kSfaCols + word * 4, sfb_t + word * 4,
+                                         kk > 0 || st > 0 ? 1u : 0u);
             }
           }
           tc_commit(smem_u32(&empty[s]));
@@ -463,15 +492,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         for (int j = 0; j < 4; ++j) {
           const int c = i * 4 + j;
           if (c >= n || !mine) continue;
-          const int pair = g.list[g.begin[grp] + c];
-          const float f = FMT == 1 ? p.factors[UP ? pair / a.top_k : pair] : 1.0f;
+          const int place = g.begin[grp] + c, pair = g.list[place];
+          const float f = FMT == 1 ? p.factors[place] : 1.0f;
           float v = FMT == 1 ? sum[0][j] * f * alpha0 : sum[0][j];
           if constexpr (UP) {
             const float u = FMT == 1 ? sum[1][j] * f * alpha1 : sum[1][j];
             const float act = a.gelu ? gelu_f32x2(make_float2(v, v)).x : v / (1.0f + expf(-v));
             v = act * u;
           }
-          const int64_t o = static_cast<int64_t>(pair) * rows + row;
+          const int64_t o = static_cast<int64_t>(UP ? place : pair) * rows + row;
           if (in_bounds(o, 1, out_extent, a.status)) (UP ? a.h : a.z)[o] = v;
         }
       }
@@ -490,19 +519,37 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   }
 }
 
+// Pairs of a group: the product takes them together, in quarters of 32 columns.
+int group_size(const MoeArgs &a) { return a.tokens <= 4 ? 4 : a.tokens <= 8 ? 8 : 16; }
+
+// The images in the workspace: codes of x, scales of x, codes of h, scales of h.
+struct Images {
+  uint8_t *codes, *scales;
+};
+Images images(const MoeArgs &a, bool of_h) {
+  const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
+  uint8_t *at = a.image + (of_h ? moe_image_bytes(pairs, a.hidden) : 0);
+  const int64_t stages = ((of_h ? a.inter : a.hidden) + kImageK - 1) / kImageK;
+  return Images{at, at + pairs * stages * kImageCodes};
+}
+
 template <int FMT, typename XT>
-cudaError_t launch_split(const MoeArgs &a, const void *x, int64_t ld, int rows, int k,
-                         const int32_t *ids, uint8_t *image, float *factors, cudaStream_t s) {
+cudaError_t launch_split(const MoeArgs &a, const void *x, int64_t ld, int rows, int k, Images out,
+                         float *factors, cudaStream_t s) {
   SplitParams p{};
   p.x = x;
   p.ld = ld;
   p.extent = (rows - 1) * ld + k;
-  p.rows = rows;
   p.k = k;
   p.stages = (k + kImageK - 1) / kImageK;
-  p.ids = ids;
+  p.ids = a.ids;
+  p.pairs = a.tokens * a.top_k;
   p.experts = a.experts;
-  p.image = image;
+  p.top_k = a.top_k;
+  p.group = group_size(a);
+  p.plan = a.plan;
+  p.codes = out.codes;
+  p.scales = out.scales;
   p.factors = factors;
   p.status = a.status;
   return launch_pdl(split_kernel<FMT, XT>, dim3((p.stages + kSplitWarps - 1) / kSplitWarps, rows),
@@ -510,7 +557,7 @@ cudaError_t launch_split(const MoeArgs &a, const void *x, int64_t ld, int rows, 
 }
 
 template <int FMT, bool UP, int NB>
-cudaError_t launch_mma(const MoeArgs &a, const uint8_t *image, const float *factors, cudaStream_t s) {
+cudaError_t launch_mma(const MoeArgs &a, Images image, const float *factors, cudaStream_t s) {
   constexpr int kSegs = UP ? 2 : 1, kAtoms = FMT == 0 ? 2 : 4;
   const auto kernel = expert_mma_kernel<FMT, UP, NB>;
   const void *func = reinterpret_cast<const void *>(kernel);
@@ -524,7 +571,8 @@ cudaError_t launch_mma(const MoeArgs &a, const uint8_t *image, const float *fact
   const int pairs = a.tokens * a.top_k;
   MmaParams p{};
   p.a = a;
-  p.image = image;
+  p.image = image.codes;
+  p.image_scales = image.scales;
   p.factors = factors;
   p.stages = (k + kImageK - 1) / kImageK;
   constexpr int kGroup = 4 * NB;
@@ -538,9 +586,9 @@ cudaError_t launch_mma(const MoeArgs &a, const uint8_t *image, const float *fact
   p.tiles = (rows + p.wrows - 1) / p.wrows;
   const int guard = (128 - p.wrows) * 128;
   const int per_slot =
-      kSegs * (p.wrows * 128 + kAtoms * 512) + kGroup * (kImageCodes + kImageScales<FMT>);
-  const int fixed = 2 * guard + 3 * 1024 + 512 + Groups::bytes(pairs);
-  constexpr int sf_cols = (kSegs + NB) * kAtoms * 4, acc = kSegs * NB * 32;
+      kSegs * (p.wrows * 128 + kAtoms * 512) + kGroup * kImageCodes + kImageScales<FMT>;
+  const int fixed = 2 * guard + 2 * 1024 + 512 + Groups::bytes(pairs);
+  constexpr int sf_cols = (kSegs + 1) * kAtoms * 4, acc = kSegs * NB * 32;
   int slots = (kMmaSmem - fixed) / per_slot;
   slots = slots < kMaxSlots ? slots : kMaxSlots;
   p.bufs = 2 * acc + 4 * sf_cols <= 512 ? 2 : 1;
@@ -552,12 +600,10 @@ cudaError_t launch_mma(const MoeArgs &a, const uint8_t *image, const float *fact
   p.b_off = up1k(p.w_off + p.slots * kSegs * p.wrows * 128 + guard);
   p.sfa_off = p.b_off + p.slots * kGroup * 1024;
   p.sfb_off = p.sfa_off + p.slots * kSegs * kAtoms * 512;
-  p.bar_off = p.sfb_off + p.slots * kGroup * kImageScales<FMT>;
-  p.groups_at = p.bar_off + 8 * (2 * p.slots + 5) + 16;
+  p.bar_off = p.sfb_off + p.slots * kImageScales<FMT>;
+  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + 15) / 16 * 16;
   const int smem = p.groups_at + Groups::bytes(pairs);
-  // the groups' scratch lies in the images' part of the ring
-  if (smem > kMmaSmem || p.slots * kGroup * 1024 < 2 * kMmaWarps * a.experts)
-    return cudaErrorInvalidValue;
+  if (smem > kMmaSmem) return cudaErrorInvalidValue;
   CUtensorMap map0, map1;
   const int64_t stacked = static_cast<int64_t>(a.experts) * rows;
   if (!encode_codes_window_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, p.wrows) ||
@@ -569,30 +615,34 @@ cudaError_t launch_mma(const MoeArgs &a, const uint8_t *image, const float *fact
 }
 
 template <int FMT, bool UP>
-cudaError_t launch_product(const MoeArgs &a, const uint8_t *image, const float *factors,
-                           cudaStream_t s) {
+cudaError_t launch_product(const MoeArgs &a, Images image, const float *factors, cudaStream_t s) {
   if (a.tokens <= 4) return launch_mma<FMT, UP, 1>(a, image, factors, s);
   if (a.tokens <= 8) return launch_mma<FMT, UP, 2>(a, image, factors, s);
-  return launch_mma<FMT, UP, 3>(a, image, factors, s);
+  return launch_mma<FMT, UP, 4>(a, image, factors, s);
 }
 
 template <int FMT>
 cudaError_t launch_all(const MoeArgs &a, cudaStream_t s) {
   const int pairs = a.tokens * a.top_k;
-  cudaError_t e = launch_split<FMT, uint16_t>(a, a.x, a.ld_x, a.tokens, a.hidden, nullptr, a.image,
-                                              a.factors, s);
-  if (e == cudaSuccess) e = launch_product<FMT, true>(a, a.image, a.factors, s);
-  uint8_t *himage = a.image + moe_image_bytes(a.tokens, a.hidden);
+  const Images x = images(a, false), h = images(a, true);
+  cudaError_t e =
+      launch_split<FMT, uint16_t>(a, a.x, a.ld_x, a.tokens, a.hidden, x, a.factors, s);
+  if (e == cudaSuccess) e = launch_product<FMT, true>(a, x, a.factors, s);
   if (e == cudaSuccess)
-    e = launch_split<FMT, float>(a, a.h, a.inter, pairs, a.inter, a.ids, himage, a.factors + a.tokens, s);
-  if (e == cudaSuccess) e = launch_product<FMT, false>(a, himage, a.factors + a.tokens, s);
+    e = launch_split<FMT, float>(a, a.h, a.inter, pairs, a.inter, h, a.factors + pairs, s);
+  if (e == cudaSuccess) e = launch_product<FMT, false>(a, h, a.factors + pairs, s);
   return e;
 }
 
 }  // namespace
 
 size_t moe_image_bytes(int64_t rows, int64_t k) {
-  return static_cast<size_t>(rows) * static_cast<size_t>((k + kImageK - 1) / kImageK) * kImageBytes;
+  return static_cast<size_t>(rows) * static_cast<size_t>((k + kImageK - 1) / kImageK) *
+         (kImageCodes + kImageScales<1>);  // a group's scales for each row: there are no more groups
+}
+
+size_t moe_plan_bytes(int64_t pairs) {
+  return static_cast<size_t>(Groups::bytes(static_cast<int>(pairs))) + static_cast<size_t>(pairs) * 2;
 }
 
 cudaError_t launch_expert_products(const MoeArgs &a, cudaStream_t s) {

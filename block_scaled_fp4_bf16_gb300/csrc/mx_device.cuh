@@ -320,15 +320,6 @@ __device__ __forceinline__ uint64_t smem_desc_scale_block(uint32_t saddr) {
   return d;
 }
 
-// The same with the 8-row groups of 128 bytes `stride` bytes apart.
-__device__ __forceinline__ uint64_t smem_desc_scale_rows(uint32_t saddr, uint32_t stride) {
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((saddr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>((stride >> 4) & 0x3FFFu) << 32;
-  d |= static_cast<uint64_t>(1) << 46;
-  return d;
-}
-
 // Instruction descriptor of the block-scaled MMA with E2M1 A and B, both
 // K-major, M x N, scale-factor byte selector sf_id for A and B.
 template <int FMT>

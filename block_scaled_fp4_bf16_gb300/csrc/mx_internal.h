@@ -217,6 +217,7 @@ cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s);
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;
 constexpr int kMoeMaxTopK = 16;
+constexpr int kMoeGroupMax = 16;  // pairs of an expert that a product takes together
 struct RouteArgs {
   const void *x;
   int64_t ld_x;
@@ -243,11 +244,14 @@ struct MoeArgs {
   float *z;            // [tokens * top_k, hidden]
   uint8_t *image;      // digits of x, then of h (moe_image_bytes)
   float *factors;      // NVFP4: of the rows of x, then of h
+  char *plan;          // the pairs' groups (moe_plan_bytes)
   int num_sms;
   uint32_t *status;
 };
 // Bytes of the digits of `rows` rows of k activations.
 size_t moe_image_bytes(int64_t rows, int64_t k);
+// Bytes of the groups of `pairs` pairs.
+size_t moe_plan_bytes(int64_t pairs);
 // h and z (moe_mma.cu), and then y.
 cudaError_t launch_expert_products(const MoeArgs &a, cudaStream_t s);
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
