@@ -955,10 +955,12 @@ static_assert(MX_MOE_MAX_TOKENS == mx::kMoeMaxTokens && MX_MOE_MAX_EXPERTS == mx
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 size_t moe_h_bytes(int64_t pairs, int64_t inter) {
-  return round256(static_cast<size_t>(pairs) * static_cast<size_t>(inter) * sizeof(float));
+  return round256(static_cast<size_t>(2 * mx::moe_max_parts(pairs) * pairs) *
+                  static_cast<size_t>(inter) * sizeof(float));
 }
 size_t moe_z_bytes(int64_t pairs, int64_t hidden) {
-  return round256(static_cast<size_t>(pairs) * static_cast<size_t>(hidden) * sizeof(float));
+  return round256(static_cast<size_t>(mx::moe_max_parts(pairs) * pairs) *
+                  static_cast<size_t>(hidden) * sizeof(float));
 }
 size_t moe_images_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k) {
   return round256(mx::moe_image_bytes(tokens * top_k, hidden) +
@@ -1088,6 +1090,14 @@ int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, c
   return check_disjoint(fn, out, 2, in, 12);
 }
 
+void moe_device(mx::MoeArgs *a, const DeviceInfo *dev) {
+  a->num_sms = dev->num_sms;
+  a->status = dev->status;
+  const int64_t pairs = static_cast<int64_t>(a->tokens) * a->top_k;
+  a->up_parts = mx::moe_parts(pairs, a->experts, a->inter, a->hidden, dev->num_sms);
+  a->down_parts = mx::moe_parts(pairs, a->experts, a->hidden, a->inter, dev->num_sms);
+}
+
 }  // namespace
 
 MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
@@ -1194,8 +1204,7 @@ MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, cons
   rc = device_info(&dev);
   if (rc != MX_OK) return rc;
   if (tokens == 0) return MX_OK;
-  a.num_sms = dev->num_sms;
-  a.status = dev->status;
+  moe_device(&a, dev);
   return launch_rc(fn, mx::launch_moe_experts(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1235,8 +1244,7 @@ MX_API int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const 
   rc = device_info(&dev);
   if (rc != MX_OK) return rc;
   if (tokens == 0) return MX_OK;
-  a.num_sms = dev->num_sms;
-  a.status = dev->status;
+  moe_device(&a, dev);
   const mx::RouteArgs r{x,      ld_x,        a.tokens, a.hidden, a.experts, top_k, normalize,
                         router, router_bias, ids,      weights,  dev->status};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

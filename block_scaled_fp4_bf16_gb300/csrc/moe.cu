@@ -78,9 +78,16 @@ __global__ void __launch_bounds__(256) combine_kernel(const MoeArgs a) {
     const int p = t * a.top_k + j, e = a.ids[p];
     if (e < 0 || e >= a.experts) continue;
     const float w = a.weights[p];
-    const int64_t o = static_cast<int64_t>(p) * a.hidden + c;
-    if (!in_bounds(o, 2, static_cast<int64_t>(a.tokens) * a.top_k * a.hidden, a.status)) continue;
-    const float2 z = *reinterpret_cast<const float2 *>(a.z + o);
+    float2 z = make_float2(0.0f, 0.0f);
+    for (int i = 0; i < a.down_parts; ++i) {
+      const int64_t o = (static_cast<int64_t>(i) * a.tokens * a.top_k + p) * a.hidden + c;
+      if (!in_bounds(o, 2, static_cast<int64_t>(a.down_parts) * a.tokens * a.top_k * a.hidden,
+                     a.status))
+        continue;
+      const float2 v = *reinterpret_cast<const float2 *>(a.z + o);
+      z.x += v.x;
+      z.y += v.y;
+    }
     y0 = __fmaf_rn(w, z.x, y0);
     y1 = __fmaf_rn(w, z.y, y1);
   }

@@ -37,8 +37,9 @@ static_assert(kMoeGroupMax * kDigits == 128, "a group's digits fill a scale tile
 __host__ __device__ constexpr int digit_shift(int p) { return p == 0 ? 0 : 3 * p - 1; }
 
 struct SplitParams {
-  const void *x;        // BF16 or FP32 rows
+  const void *x;        // x: BF16 rows; h: the partial sums [parts][2][pairs][k]
   int64_t ld, extent;   // row stride, elements from x's base (bounds-checked build)
+  int parts, gelu;      // h
   int k, stages;
   const int32_t *ids;   // [pairs]
   int pairs, experts;
@@ -66,16 +67,26 @@ __device__ __forceinline__ float pow2(int e) {
                    : __uint_as_float(1u << (e + 149));
 }
 
-// Eight consecutive elements of row `r` from k0 + 8 lane (zeros past k).
+// v += eight floats.
+__device__ __forceinline__ void add8(const SplitParams &p, int64_t off, float (&v)[8]) {
+  if (!in_bounds(off, 8, p.extent, p.status)) return;
+  const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + off);
+  const float4 a = src[0], b = src[1];
+  v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
+  v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
+}
+
+// Eight consecutive elements of row r of x, or of h = act(gate) up, from `at`
+// (zeros past k).
 template <typename XT>
 __device__ __forceinline__ void load8(const SplitParams &p, int r, int at, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  const int64_t off = r * p.ld + at;
-  if (at >= p.k || !in_bounds(off, 8, p.extent, p.status)) return;
-  const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + off);
+  if (at >= p.k) return;
   if constexpr (sizeof(XT) == 2) {
-    const uint4 q = src[0];
+    const int64_t off = r * p.ld + at;
+    if (!in_bounds(off, 8, p.extent, p.status)) return;
+    const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + off);
     const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -83,11 +94,18 @@ __device__ __forceinline__ void load8(const SplitParams &p, int r, int at, float
       v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   } else {
+    float u[8] = {};
+    for (int s = 0; s < p.parts; ++s) {
+      add8(p, (static_cast<int64_t>(2 * s) * p.pairs + r) * p.ld + at, v);
+      add8(p, (static_cast<int64_t>(2 * s + 1) * p.pairs + r) * p.ld + at, u);
+    }
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint4 q = src[j];
-      v[4 * j] = __uint_as_float(q.x), v[4 * j + 1] = __uint_as_float(q.y);
-      v[4 * j + 2] = __uint_as_float(q.z), v[4 * j + 3] = __uint_as_float(q.w);
+    for (int i = 0; i < 8; i += 2) {
+      const float2 a = p.gelu ? gelu_f32x2(make_float2(v[i], v[i + 1]))
+                              : make_float2(v[i] / (1.0f + expf(-v[i])),
+                                            v[i + 1] / (1.0f + expf(-v[i + 1])));
+      v[i] = a.x * u[i];
+      v[i + 1] = a.y * u[i + 1];
     }
   }
 }
@@ -129,15 +147,20 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
   load8<XT>(p, r, stage * kImageK + lane * 8, v);
   int row_e = 0;  // NVFP4: exponent of the row's factor
   if constexpr (FMT == 1) {
-    float top = 0.0f;
-    for (int s = warp; s < p.stages; s += kSplitWarps) {
-      float u[8];
-      load8<XT>(p, r, s * kImageK + lane * 8, u);
+    float top = 0.0f;  // of the row's finite elements
+    const auto raise = [&](const float (&u)[8]) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float a = fabsf(u[i]);
         if (a < __uint_as_float(0x7F800000u)) top = fmaxf(top, a);
       }
+    };
+    raise(v);
+    for (int s = warp; s < p.stages; s += kSplitWarps) {
+      if (s == stage) continue;
+      float u[8];
+      load8<XT>(p, r, s * kImageK + lane * 8, u);
+      raise(u);
     }
     top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
     if (lane == 0) tops[warp] = top;
@@ -253,22 +276,22 @@ struct MmaParams {
   const uint8_t *image, *image_scales;
   const float *factors;
   int stages;     // of 256 along K
-  int tiles;      // row tiles of an expert
-  int wrows;      // rows of a tile: 128, 64 or 32 (a part of a 128-row scale tile)
+  int tiles;      // 128-row tiles of an expert
+  int parts;      // ranges of K, each an item with sums of its own
   int slots;      // stages in flight
   int bufs;       // accumulators (1 or 2)
-  int w_off, b_off, sfa_off, sfb_off, bar_off, groups_at;  // shared memory
+  int b_off, sfa_off, sfb_off, bar_off, groups_at;  // shared memory (the weights at 0)
 };
 
-// UP: gate and up rows, h as output; else rows of `hidden`, z as output.  An item
-// is a tile of wrows rows (of each matrix) times a group's tokens; a CTA walks
-// consecutive items, group-major.
+// UP: gate and up rows, h's partial sums as output; else rows of `hidden`, z's.
+// An item is 128 rows (of each matrix) times a group's pairs over one range of
+// K; a CTA walks consecutive items, group-major.  A product reads its 128 weight
+// rows from shared memory in about 100 clocks however few columns it has
+// (measured: 64-row tiles take as long as 128-row ones), so the tiles are whole and a
+// call with few items divides K instead.
 //
-// Shared memory: a ring of stages.  Weight slices of wrows x 128 bytes, one
-// after the other with (128 - wrows) x 128 guard bytes around the ring: the
-// product reads 128 rows with the slice at its place in the 128-row scale tile;
-// what the other rows hold is never read back.  Images: a kilobyte a pair, and the
-// group's scale tiles.
+// Shared memory: a ring of stages: weights (128 rows x 128 bytes of each matrix),
+// images (a kilobyte a pair), scale tiles of the weights and of the group.
 // Tensor memory: accumulators [bufs][SEGS][NB][32 columns], then a set of
 // scale columns for each stage in flight, four columns for each scale tile.
 template <int FMT, bool UP, int NB>
@@ -280,6 +303,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
   constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
   constexpr int kSfaCols = kAtoms * 4;
   constexpr int kSfb = kImageScales<FMT>;
+  constexpr int kTile = 128 * 128;               // bytes of a stage's weights, of one matrix
   extern __shared__ __align__(1024) char smem[];
   const MoeArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -326,11 +350,26 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     reinterpret_cast<uint4 *>(smem + p.groups_at)[i] = reinterpret_cast<const uint4 *>(a.plan)[i];
   __syncthreads();
   const Groups g = Groups::at(smem + p.groups_at, pairs);
-  const int64_t items = static_cast<int64_t>(*g.count) * p.tiles;
+  const int64_t items = static_cast<int64_t>(*g.count) * p.tiles * p.parts;
   const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
   const int end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
   const int rows = UP ? a.inter : a.hidden, k = UP ? a.hidden : a.inter;
   const int katoms = (k / (FMT == 0 ? 32 : 16) + 3) >> 2;  // scale tiles along K
+  const int group_items = p.tiles * p.parts;
+  // an item's group, row tile and range of K
+  struct Item {
+    int grp, tile, part, st0, st1;
+  };
+  const auto item_at = [&](int item) {
+    Item i;
+    i.grp = item / group_items;
+    const int r = item - i.grp * group_items;
+    i.tile = r / p.parts;
+    i.part = r - i.tile * p.parts;
+    i.st0 = p.stages * i.part / p.parts;
+    i.st1 = p.stages * (i.part + 1) / p.parts;
+    return i;
+  };
   constexpr int acc_cols = kSegs * NB * 32;
   const uint32_t sf_tmem = tmem + p.bufs * acc_cols;
   constexpr int sf_cols = (kSegs + 1) * kSfaCols;
@@ -340,15 +379,15 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     uint32_t it = 0, s = 0, ph = 0;
     bool ok = true;
     for (int item = begin; item < end && ok; ++item) {
-      const int grp = item / p.tiles, tile = item - grp * p.tiles;
-      const int e = g.expert[grp], n = g.size[grp];
-      const int row0 = tile * p.wrows;
-      const int64_t scale_bytes = ((rows + 127) >> 7) * static_cast<int64_t>(katoms) * 512;
-      const int64_t scale_off = e * scale_bytes + static_cast<int64_t>(row0 >> 7) * katoms * 512;
+      const Item im = item_at(item);
+      const int grp = im.grp, e = g.expert[grp], n = g.size[grp];
+      const int row0 = im.tile * 128;
+      const int64_t scale_off =
+          (static_cast<int64_t>(e) * p.tiles + im.tile) * static_cast<int64_t>(katoms) * 512;
       const uint8_t *sf0 = (UP ? a.gate.scales : a.down.scales) + scale_off;
       const uint8_t *sf1 = UP ? a.up.scales + scale_off : nullptr;
       const int64_t place = g.begin[grp];
-      for (int st = 0; st < p.stages; ++st, ++it) {
+      for (int st = im.st0; st < im.st1; ++st, ++it) {
         if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, a.status)) {
           ok = false;
           break;
@@ -356,13 +395,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
         const uint32_t fb = smem_u32(&full[s]);
         const uint32_t sf_bytes = static_cast<uint32_t>(min(kAtoms, katoms - st * kAtoms)) * 512u;
         if (elect_one()) {
-          mbar_arrive_expect_tx(fb, kSegs * (p.wrows * 128 + sf_bytes) + n * kImageCodes + kSfb);
-          const uint32_t w = smem_u32(smem + p.w_off) + s * kSegs * p.wrows * 128;
+          mbar_arrive_expect_tx(fb, kSegs * (kTile + sf_bytes) + n * kImageCodes + kSfb);
+          const uint32_t w = smem_u32(smem) + s * kSegs * kTile;
           const uint32_t sf = smem_u32(smem + p.sfa_off) + s * kSegs * kSfa;
           tma_load_2d(w, &map0, st * 128, e * rows + row0, fb);
           bulk_load(sf, sf0 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
           if constexpr (UP) {
-            tma_load_2d(w + p.wrows * 128, &map1, st * 128, e * rows + row0, fb);
+            tma_load_2d(w + kTile, &map1, st * 128, e * rows + row0, fb);
             bulk_load(sf + kSfa, sf1 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
           }
           const int64_t at = static_cast<int64_t>(st) * pairs;
@@ -385,21 +424,20 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     bool ok = true;
     // One thread issues every product, so a product has to cost it few
     // instructions: the loops are unrolled and descriptors stepped by constants.
-    const uint32_t w_ring = smem_u32(smem + p.w_off), b_ring = smem_u32(smem + p.b_off);
+    const uint32_t w_ring = smem_u32(smem), b_ring = smem_u32(smem + p.b_off);
     const uint32_t sfa_ring = smem_u32(smem + p.sfa_off), sfb_ring = smem_u32(smem + p.sfb_off);
-    const uint32_t seg_step = static_cast<uint32_t>(p.wrows * 128) >> 4;
     for (int item = begin; item < end && ok; ++item) {
-      const int grp = item / p.tiles, tile = item - grp * p.tiles;
+      const Item im = item_at(item);
+      const int grp = im.grp;
       // columns: the digits of the group, to a multiple of 16
       const uint32_t columns = static_cast<uint32_t>(g.size[grp] * kDigits + 15) & ~15u;
       const uint32_t idesc0 = mma_idesc<FMT>(128, columns, 0);
       const uint32_t idesc2 = mma_idesc<FMT>(128, columns, 2);
-      const int h_row = tile * p.wrows & 127;
       ok = mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, a.status);
       if (!ok) break;
       tc_fence_after();
       const uint32_t acc = tmem + buf * acc_cols;
-      for (int st = 0; st < p.stages; ++st) {
+      for (int st = im.st0; st < im.st1; ++st) {
         if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort, a.status)) {
           ok = false;
           break;
@@ -423,8 +461,7 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
                                      sfa + ((m * kSfa + i * 512) >> 4));
             }
           }
-          const uint64_t wd =
-              smem_desc_sw128_kmajor(w_ring + s * kSegs * p.wrows * 128 - h_row * 128);
+          const uint64_t wd = smem_desc_sw128_kmajor(w_ring + s * kSegs * kTile);
           const uint64_t bd = smem_desc_sw128_kmajor(b_ring + s * kGroup * 1024);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
@@ -433,13 +470,13 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
               const uint32_t idesc = FMT == 0 && (kk & 1) ? idesc2 : idesc0;
 #pragma unroll
               for (int m = 0; m < kSegs; ++m)
-                tc_mma_block_scaled<FMT>(acc + m * NB * 32, wd + m * seg_step + 2 * kk, bd + 2 * kk,
-                                         idesc, sfa_t + m * kSfaCols + word * 4, sfb_t + word * 4,
-                                         kk > 0 || st > 0 ? 1u : 0u);
+                tc_mma_block_scaled<FMT>(acc + m * NB * 32, wd + m * (kTile >> 4) + 2 * kk,
+                                         bd + 2 * kk, idesc, sfa_t + m * kSfaCols + word * 4,
+                                         sfb_t + word * 4, kk > 0 || st > im.st0 ? 1u : 0u);
             }
           }
           tc_commit(smem_u32(&empty[s]));
-          if (st == p.stages - 1) tc_commit(smem_u32(&acc_full[buf]));
+          if (st == im.st1 - 1) tc_commit(smem_u32(&acc_full[buf]));
         }
         __syncwarp();
         if (++s == static_cast<uint32_t>(slots)) s = 0, ph ^= 1u;
@@ -454,13 +491,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;  // this warp's lane quarter
     uint32_t buf = 0, bph = 0;
-    const int64_t out_extent = static_cast<int64_t>(a.tokens) * a.top_k * rows;
+    const int64_t out_extent = static_cast<int64_t>(p.parts) * kSegs * pairs * rows;
     for (int item = begin; item < end; ++item) {
-      const int grp = item / p.tiles, tile = item - grp * p.tiles;
-      const int e = g.expert[grp], n = g.size[grp];
-      const int row0 = tile * p.wrows, h_row = row0 & 127;
-      const int row = (row0 & ~127) + q * 32 + lane;
-      const bool mine = q * 32 >= h_row && q * 32 < h_row + p.wrows && row < rows;
+      const Item im = item_at(item);
+      const int grp = im.grp, e = g.expert[grp], n = g.size[grp];
+      const int row = im.tile * 128 + q * 32 + lane;
       const float alpha0 = FMT == 1 ? (UP ? a.gate.ts : a.down.ts)[e] : 1.0f;
       const float alpha1 = FMT == 1 && UP ? a.up.ts[e] : 1.0f;
       if (!mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status)) break;
@@ -491,17 +526,16 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = i * 4 + j;
-          if (c >= n || !mine) continue;
+          if (c >= n || row >= rows) continue;
           const int place = g.begin[grp] + c, pair = g.list[place];
           const float f = FMT == 1 ? p.factors[place] : 1.0f;
-          float v = FMT == 1 ? sum[0][j] * f * alpha0 : sum[0][j];
-          if constexpr (UP) {
-            const float u = FMT == 1 ? sum[1][j] * f * alpha1 : sum[1][j];
-            const float act = a.gelu ? gelu_f32x2(make_float2(v, v)).x : v / (1.0f + expf(-v));
-            v = act * u;
+#pragma unroll
+          for (int m = 0; m < kSegs; ++m) {
+            const float v = FMT == 1 ? sum[m][j] * f * (m == 0 ? alpha0 : alpha1) : sum[m][j];
+            const int64_t o = (static_cast<int64_t>(im.part * kSegs + m) * pairs +
+                               (UP ? place : pair)) * rows + row;
+            if (in_bounds(o, 1, out_extent, a.status)) (UP ? a.h : a.z)[o] = v;
           }
-          const int64_t o = static_cast<int64_t>(UP ? place : pair) * rows + row;
-          if (in_bounds(o, 1, out_extent, a.status)) (UP ? a.h : a.z)[o] = v;
         }
       }
       tc_fence_before();
@@ -539,7 +573,10 @@ cudaError_t launch_split(const MoeArgs &a, const void *x, int64_t ld, int rows, 
   SplitParams p{};
   p.x = x;
   p.ld = ld;
-  p.extent = (rows - 1) * ld + k;
+  p.extent = sizeof(XT) == 2 ? (rows - 1) * ld + k
+                             : static_cast<int64_t>(a.up_parts) * 2 * rows * k;
+  p.parts = a.up_parts;
+  p.gelu = a.gelu;
   p.k = k;
   p.stages = (k + kImageK - 1) / kImageK;
   p.ids = a.ids;
@@ -576,18 +613,12 @@ cudaError_t launch_mma(const MoeArgs &a, Images image, const float *factors, cud
   p.factors = factors;
   p.stages = (k + kImageK - 1) / kImageK;
   constexpr int kGroup = 4 * NB;
-  const int most = a.experts < pairs ? a.experts : pairs;  // experts with a pair
-  // rows of a tile: whole 128 unless that leaves SMs without an item
-  p.wrows = 128;
-  if (UP) p.wrows = 64;
-  while (p.wrows > 32 && static_cast<int64_t>(most) * ((rows + p.wrows - 1) / p.wrows) < a.num_sms)
-    p.wrows /= 2;
-  if (UP && a.tokens > 8) p.wrows = 128;
-  p.tiles = (rows + p.wrows - 1) / p.wrows;
-  const int guard = (128 - p.wrows) * 128;
-  const int per_slot =
-      kSegs * (p.wrows * 128 + kAtoms * 512) + kGroup * kImageCodes + kImageScales<FMT>;
-  const int fixed = 2 * guard + 2 * 1024 + 512 + Groups::bytes(pairs);
+  p.tiles = (rows + 127) / 128;
+  p.parts = UP ? a.up_parts : a.down_parts;
+  constexpr int kTile = 128 * 128;
+  constexpr int per_slot =
+      kSegs * (kTile + kAtoms * 512) + kGroup * kImageCodes + kImageScales<FMT>;
+  const int fixed = 512 + Groups::bytes(pairs);
   constexpr int sf_cols = (kSegs + 1) * kAtoms * 4, acc = kSegs * NB * 32;
   int slots = (kMmaSmem - fixed) / per_slot;
   slots = slots < kMaxSlots ? slots : kMaxSlots;
@@ -595,9 +626,7 @@ cudaError_t launch_mma(const MoeArgs &a, Images image, const float *factors, cud
   const int tmem_slots = (512 - p.bufs * acc) / sf_cols;
   p.slots = slots < tmem_slots ? slots : tmem_slots;
   if (p.slots < 2) return cudaErrorInvalidValue;
-  const auto up1k = [](int v) { return (v + 1023) / 1024 * 1024; };
-  p.w_off = up1k(guard);
-  p.b_off = up1k(p.w_off + p.slots * kSegs * p.wrows * 128 + guard);
+  p.b_off = p.slots * kSegs * kTile;
   p.sfa_off = p.b_off + p.slots * kGroup * 1024;
   p.sfb_off = p.sfa_off + p.slots * kSegs * kAtoms * 512;
   p.bar_off = p.sfb_off + p.slots * kImageScales<FMT>;
@@ -606,10 +635,11 @@ cudaError_t launch_mma(const MoeArgs &a, Images image, const float *factors, cud
   if (smem > kMmaSmem) return cudaErrorInvalidValue;
   CUtensorMap map0, map1;
   const int64_t stacked = static_cast<int64_t>(a.experts) * rows;
-  if (!encode_codes_window_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, p.wrows) ||
-      !encode_codes_window_map(&map1, UP ? a.up.codes : a.down.codes, stacked, k, p.wrows))
+  if (!encode_codes_window_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, 128) ||
+      !encode_codes_window_map(&map1, UP ? a.up.codes : a.down.codes, stacked, k, 128))
     return cudaErrorInvalidValue;
-  const int64_t items = static_cast<int64_t>(most + pairs / kGroup) * p.tiles;
+  const int most = a.experts < pairs ? a.experts : pairs;  // experts with a pair
+  const int64_t items = static_cast<int64_t>(most + pairs / kGroup) * p.tiles * p.parts;
   const int grid = items < a.num_sms ? static_cast<int>(items) : a.num_sms;
   return launch_pdl(kernel, dim3(grid), dim3(kMmaThreads), smem, s, map0, map1, p);
 }
@@ -639,6 +669,19 @@ cudaError_t launch_all(const MoeArgs &a, cudaStream_t s) {
 size_t moe_image_bytes(int64_t rows, int64_t k) {
   return static_cast<size_t>(rows) * static_cast<size_t>((k + kImageK - 1) / kImageK) *
          (kImageCodes + kImageScales<1>);  // a group's scales for each row: there are no more groups
+}
+
+// Ranges of K of a product of `rows` rows for `pairs` pairs: so many that a call
+// with few pairs has an item for every SM or nearly (at least 4 stages each), and no
+// more than moe_max_parts(pairs).
+int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms) {
+  const int64_t most = experts < pairs ? experts : pairs;
+  const int64_t items = most * ((rows + 127) / 128), stages = (k + kImageK - 1) / kImageK;
+  int parts = 1;
+  while (2 * parts <= moe_max_parts(pairs) && items * parts * 4 <= num_sms * 3 &&
+         stages >= 8 * parts)
+    parts *= 2;
+  return parts;
 }
 
 size_t moe_plan_bytes(int64_t pairs) {

@@ -240,8 +240,9 @@ struct MoeArgs {
   FewMatrix gate, up, down;
   void *y;
   int64_t ld_y;
-  float *h;            // [tokens * top_k, inter]
-  float *z;            // [tokens * top_k, hidden]
+  int up_parts, down_parts;  // ranges of K of the two products (moe_parts)
+  float *h;            // sums of gate and up rows [up_parts][2][tokens * top_k][inter]
+  float *z;            // [down_parts][tokens * top_k][hidden]
   uint8_t *image;      // digits of x, then of h (moe_image_bytes)
   float *factors;      // NVFP4: of the rows of x, then of h
   char *plan;          // the pairs' groups (moe_plan_bytes)
@@ -250,6 +251,9 @@ struct MoeArgs {
 };
 // Bytes of the digits of `rows` rows of k activations.
 size_t moe_image_bytes(int64_t rows, int64_t k);
+// Ranges of K that a product is divided into, and the most for a number of pairs.
+int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms);
+constexpr int moe_max_parts(int64_t pairs) { return pairs <= 16 ? 4 : pairs <= 64 ? 2 : 1; }
 // Bytes of the groups of `pairs` pairs.
 size_t moe_plan_bytes(int64_t pairs);
 // h and z (moe_mma.cu), and then y.
