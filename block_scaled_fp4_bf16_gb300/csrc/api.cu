@@ -1079,6 +1079,7 @@ int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, c
       a->image + moe_images_bytes(tokens, moe->hidden, moe->inter, top_k));
   a->plan = reinterpret_cast<char *>(a->factors) +
             round256(static_cast<size_t>(2 * pairs) * sizeof(float));
+  a->counts = reinterpret_cast<uint32_t *>(a->plan + round256(mx::moe_plan_bytes(pairs)));
   Range in[12];
   in[0] = span(x, row_bytes(tokens, moe->hidden, ld_x, 2));
   in[1] = span(ids, static_cast<uint64_t>(pairs) * 4);
@@ -1187,7 +1188,7 @@ MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t int
   return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) +
          moe_images_bytes(tokens, hidden, inter, top_k) +
          round256(static_cast<size_t>(2 * pairs) * sizeof(float)) +
-         round256(mx::moe_plan_bytes(pairs));
+         round256(mx::moe_plan_bytes(pairs)) + round256(mx::kMoeCounts * sizeof(uint32_t));
 }
 
 MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,

@@ -65,49 +65,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   }
 }
 
-// ---------------------------------------------------------------- the experts
-
-// y[t] = sum_j w_tj z[t, j], in the order of the slots.
-__global__ void __launch_bounds__(256) combine_kernel(const MoeArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
-  const int t = blockIdx.y, c = (blockIdx.x * 256 + threadIdx.x) * 2;
-  if (c >= a.hidden) return;
-  float y0 = 0.0f, y1 = 0.0f;
-  for (int j = 0; j < a.top_k; ++j) {
-    const int p = t * a.top_k + j, e = a.ids[p];
-    if (e < 0 || e >= a.experts) continue;
-    const float w = a.weights[p];
-    float2 z = make_float2(0.0f, 0.0f);
-    for (int i = 0; i < a.down_parts; ++i) {
-      const int64_t o = (static_cast<int64_t>(i) * a.tokens * a.top_k + p) * a.hidden + c;
-      if (!in_bounds(o, 2, static_cast<int64_t>(a.down_parts) * a.tokens * a.top_k * a.hidden,
-                     a.status))
-        continue;
-      const float2 v = *reinterpret_cast<const float2 *>(a.z + o);
-      z.x += v.x;
-      z.y += v.y;
-    }
-    y0 = __fmaf_rn(w, z.x, y0);
-    y1 = __fmaf_rn(w, z.y, y1);
-  }
-  const int64_t o = t * a.ld_y + c;
-  if (!in_bounds(o, 2, (a.tokens - 1) * a.ld_y + a.hidden, a.status)) return;
-  uint16_t *y = static_cast<uint16_t *>(a.y) + o;
-  y[0] = bf16_bits(y0);
-  y[1] = bf16_bits(y1);
-}
-
 }  // namespace
 
 cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s) {
   return launch_pdl(route_kernel, dim3(a.tokens), dim3(kWarps * 32), 0, s, a);
-}
-
-cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s) {
-  const cudaError_t e = launch_expert_products(a, s);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(combine_kernel, dim3((a.hidden + 511) / 512, a.tokens), dim3(256), 0, s, a);
 }
 
 }  // namespace mx

@@ -13,11 +13,17 @@
 // rate makes the eightfold product cheaper than converting the weights: M = 128,
 // N = 32 (four tokens), K = 64 a step.
 //
-// split_kernel makes the digits (an "image": for a row and 256 elements of K the
-// eight rows of 128 bytes as the product reads them, 128-byte swizzle included,
-// and their scales), expert_mma_kernel streams weights and images.  The images'
-// rows are the (token, slot) pairs sorted by expert, so that a group's lie
-// together and come with two copies a stage.
+// Two launches:
+//   split_kernel    groups the (token, slot) pairs by expert and writes the digits of
+//                   x (an "image": for a row and 256 elements of K the eight rows
+//                   of 128 bytes as the product reads them, 128-byte swizzle
+//                   included, and their scales).  The images' rows are the pairs
+//                   sorted by expert, so a group's lie together.
+//   expert_kernel   one CTA per SM, launched together: the sums of the gate and up
+//                   rows; the digits of h = act(gate) up; the sums of the down rows;
+//                   y.  A grid-wide count separates these, and the copies of the
+//                   down weights run ahead of it: what a kernel boundary would have
+//                   left idle streams weights.
 #include <cuda_fp16.h>
 
 #include "moe_groups.cuh"
@@ -36,19 +42,12 @@ static_assert(kMoeGroupMax * kDigits == 128, "a group's digits fill a scale tile
 // Weight of digit p: 2^-kShift[p].
 __host__ __device__ constexpr int digit_shift(int p) { return p == 0 ? 0 : 3 * p - 1; }
 
-struct SplitParams {
-  const void *x;        // x: BF16 rows; h: the partial sums [parts][2][pairs][k]
-  int64_t ld, extent;   // row stride, elements from x's base (bounds-checked build)
-  int parts, gelu;      // h
-  int k, stages;
-  const int32_t *ids;   // [pairs]
-  int pairs, experts;
-  int top_k, group;     // pairs of a group at most
-  uint8_t *codes;       // [stages][pairs][kImageCodes], rows by place
+// Where digits go.  Rows are places.
+struct Image {
+  uint8_t *codes;       // [stages][pairs][kImageCodes]
   uint8_t *scales;      // [stages][groups][kImageScales]
   float *factors;       // NVFP4: [pairs], the power of two of a place
-  char *plan;           // Groups and the places' members (written for x, read for h)
-  uint32_t *status;
+  int pairs;
 };
 
 constexpr int kSplitWarps = 8;
@@ -67,120 +66,31 @@ __device__ __forceinline__ float pow2(int e) {
                    : __uint_as_float(1u << (e + 149));
 }
 
-// v += eight floats.
-__device__ __forceinline__ void add8(const SplitParams &p, int64_t off, float (&v)[8]) {
-  if (!in_bounds(off, 8, p.extent, p.status)) return;
-  const float4 *src = reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + off);
-  const float4 a = src[0], b = src[1];
-  v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-  v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-}
+// NVFP4: exponent of a row's factor, the largest finite magnitude being `top`: the
+// largest block's scale becomes 2^8, the largest power of two of E4M3.
+__device__ __forceinline__ int row_exponent(float top) { return max(block_exponent(top) - 8, -118); }
 
-// Eight consecutive elements of row r of x, or of h = act(gate) up, from `at`
-// (zeros past k).
-template <typename XT>
-__device__ __forceinline__ void load8(const SplitParams &p, int r, int at, float (&v)[8]) {
+__device__ __forceinline__ void raise_finite(float &top, const float (&v)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-  if (at >= p.k) return;
-  if constexpr (sizeof(XT) == 2) {
-    const int64_t off = r * p.ld + at;
-    if (!in_bounds(off, 8, p.extent, p.status)) return;
-    const uint4 q = *reinterpret_cast<const uint4 *>(static_cast<const XT *>(p.x) + off);
-    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-    }
-  } else {
-    float u[8] = {};
-    for (int s = 0; s < p.parts; ++s) {
-      add8(p, (static_cast<int64_t>(2 * s) * p.pairs + r) * p.ld + at, v);
-      add8(p, (static_cast<int64_t>(2 * s + 1) * p.pairs + r) * p.ld + at, u);
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float2 a = p.gelu ? gelu_f32x2(make_float2(v[i], v[i + 1]))
-                              : make_float2(v[i] / (1.0f + expf(-v[i])),
-                                            v[i + 1] / (1.0f + expf(-v[i + 1])));
-      v[i] = a.x * u[i];
-      v[i + 1] = a.y * u[i + 1];
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float a = fabsf(v[i]);
+    if (a < __uint_as_float(0x7F800000u)) top = fmaxf(top, a);
   }
 }
 
-// Row blockIdx.y (x: a token, which goes to the places of its pairs; h: a place),
-// stages blockIdx.x * kSplitWarps ..: a warp makes the image of one stage, eight
-// elements a lane.  MXFP4: UE8M0 scales for 32 (four lanes), digit p
-// with the scale 2^(e - shift p); NVFP4: E4M3 for 16 (two lanes), a power of two
-// relative to the row's factor, the digits' weights left to the reader.  A block
-// that holds an infinity or NaN gets the scale NaN.
-template <int FMT, typename XT>
-__global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitParams p) {
-  __shared__ float tops[kSplitWarps];
-  constexpr int kPairs = kMoeMaxTokens * kMoeMaxTopK;
-  constexpr bool kGather = sizeof(XT) == 2;  // x: tokens to places
-  __shared__ __align__(16) char groups[kGather ? Groups::bytes(kPairs) : 16];
-  __shared__ __align__(16) char scratch[kGather ? 2 * (kSplitWarps + 2) * kMoeMaxExperts : 16];
-  __shared__ uint16_t places[kGather ? kPairs : 1], members[kGather ? kPairs : 1];
-  griddep_launch_dependents();
-  griddep_wait();
-  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint16_t *plan_members = reinterpret_cast<uint16_t *>(p.plan + Groups::bytes(p.pairs));
-  if constexpr (kGather) {
-    make_groups<kSplitWarps>(Groups::at(groups, p.pairs), places, members, scratch, p.ids, p.pairs,
-                             p.experts, p.group, p.status);
-    if (blockIdx.x == 0 && r == 0) {
-      for (int i = threadIdx.x; i < Groups::bytes(p.pairs) / 4; i += kSplitWarps * 32)
-        reinterpret_cast<uint32_t *>(p.plan)[i] = reinterpret_cast<const uint32_t *>(groups)[i];
-      for (int i = threadIdx.x; i < p.pairs; i += kSplitWarps * 32) plan_members[i] = members[i];
-    }
-  } else {
-    // the places behind the last group's are empty
-    const Groups g = Groups::at(p.plan, p.pairs);
-    const int n = *g.count;
-    if (n == 0 || r >= g.begin[n - 1] + g.size[n - 1]) return;
-  }
-  const int stage = blockIdx.x * kSplitWarps + warp;
-  float v[8];
-  load8<XT>(p, r, stage * kImageK + lane * 8, v);
-  int row_e = 0;  // NVFP4: exponent of the row's factor
-  if constexpr (FMT == 1) {
-    float top = 0.0f;  // of the row's finite elements
-    const auto raise = [&](const float (&u)[8]) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float a = fabsf(u[i]);
-        if (a < __uint_as_float(0x7F800000u)) top = fmaxf(top, a);
-      }
-    };
-    raise(v);
-    for (int s = warp; s < p.stages; s += kSplitWarps) {
-      if (s == stage) continue;
-      float u[8];
-      load8<XT>(p, r, s * kImageK + lane * 8, u);
-      raise(u);
-    }
-    top = __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top)));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, tops[w]);
-    // the largest block's scale becomes 2^8, the largest power of two of E4M3
-    row_e = max(block_exponent(top) - 8, -118);
-    if (blockIdx.x == 0) {
-      if constexpr (kGather) {
-        if (threadIdx.x < static_cast<unsigned>(p.top_k)) {
-          const int at = places[r * p.top_k + threadIdx.x];
-          if (at != 0xFFFF) p.factors[at] = pow2(row_e);
-        }
-      } else if (threadIdx.x == 0) {
-        p.factors[r] = pow2(row_e);
-      }
-    }
-  }
-  if (stage >= p.stages) return;
+__device__ __forceinline__ float warp_max(float v) {  // v >= 0
+  return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
+}
+
+// Whole warp.  The digits of 256 elements (eight a lane, v), written to `copies`
+// places of stage `stage`: place(j) (0xFFFF: none), member(place).  MXFP4: UE8M0
+// scales for 32 (four lanes), digit p with the scale 2^(e - shift p); NVFP4: E4M3
+// for 16 (two lanes), a power of two relative to 2^row_e, the digits' weights left
+// to the reader.  A block that holds an infinity or NaN gets the scale NaN.
+template <int FMT, typename Place, typename Member>
+__device__ __forceinline__ void write_digits(const Image &out, int stage, float (&v)[8], int row_e,
+                                             int copies, const Place &place, const Member &member) {
+  const int lane = threadIdx.x & 31;
   float top = 0.0f;
   uint32_t odd = 0;  // an infinity or NaN here
 #pragma unroll
@@ -203,9 +113,6 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
     e = row_e + j;
     byte = odd ? 0x7Fu : j >= -6 ? static_cast<uint32_t>(j + 7) << 3 : 1u << (j + 9);
   }
-  // the places of this row
-  const int copies = kGather ? p.top_k : 1;
-  const auto place = [&](int j) { return kGather ? static_cast<int>(places[r * p.top_k + j]) : r; };
   // v 2^-e, in two steps where one power of two would not be a normal number
   const float f0 = pow2(min(-e, 100)), f1 = pow2(-e - min(-e, 100));
 #pragma unroll
@@ -231,7 +138,7 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
       const int to = place(j);
       if (to != 0xFFFF)
         *reinterpret_cast<uint32_t *>(
-            p.codes + (static_cast<int64_t>(stage) * p.pairs + to) * kImageCodes + at) = w;
+            out.codes + (static_cast<int64_t>(stage) * out.pairs + to) * kImageCodes + at) = w;
     }
   }
   // scale words of four blocks, for each digit's row
@@ -241,214 +148,286 @@ __global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitPara
   for (int b = 0; b < 4 * kWords; ++b)
     words[b / 4] |= __shfl_sync(0xFFFFFFFFu, byte, b * (8 / kWords)) << (8 * (b % 4));
   if (lane < kDigits) {
+    for (int j = 0; j < copies; ++j) {
+      const int to = place(j);
+      if (to == 0xFFFF) continue;
+      // digit rows of a group in the order of a scale tile: row c at c % 32, word c / 32
+      const int mem = member(to), m = mem % kMoeGroupMax;
+      uint8_t *dst = out.scales +
+                     (static_cast<int64_t>(stage) * out.pairs + mem / kMoeGroupMax) * kImageScales<FMT> +
+                     ((m & 3) * kDigits + lane) * 16 + (m >> 2) * 4;
 #pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      uint32_t w = words[i];
-      if constexpr (FMT == 0) {
-        // 255 stays NaN; a digit whose scale would lie below 2^-127 is 0
-        const uint32_t nan = __vcmpeq4(w, 0xFFFFFFFFu);
-        w = __vsubus4(w, (lane == 0 ? 0u : 3u * lane - 1u) * 0x01010101u) | nan;
-      }
-      for (int j = 0; j < copies; ++j) {
-        const int to = place(j);
-        if (to == 0xFFFF) continue;
-        // digit rows of a group in the order of a scale tile: row c at c % 32, word c / 32
-        const int member = kGather ? members[to] : plan_members[to];
-        const int m = member % kMoeGroupMax;
-        *reinterpret_cast<uint32_t *>(
-            p.scales +
-            (static_cast<int64_t>(stage) * p.pairs + member / kMoeGroupMax) * kImageScales<FMT> +
-            i * 512 + ((m & 3) * kDigits + lane) * 16 + (m >> 2) * 4) = w;
+      for (int i = 0; i < kWords; ++i) {
+        uint32_t w = words[i];
+        if constexpr (FMT == 0) {
+          // 255 stays NaN; a digit whose scale would lie below 2^-127 is 0
+          const uint32_t nan = __vcmpeq4(w, 0xFFFFFFFFu);
+          w = __vsubus4(w, (lane == 0 ? 0u : 3u * lane - 1u) * 0x01010101u) | nan;
+        }
+        *reinterpret_cast<uint32_t *>(dst + i * 512) = w;
       }
     }
   }
 }
 
+struct SplitParams {
+  MoeArgs a;
+  Image image;
+  int stages, group;  // pairs of a group at most
+};
+
+// Eight consecutive elements of token r from `at` (zeros past the end).
+__device__ __forceinline__ void load_x(const MoeArgs &a, int r, int at, float (&v)[8]) {
+  uint4 q = make_uint4(0, 0, 0, 0);
+  const int64_t off = r * a.ld_x + at;
+  if (at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status))
+    q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off);
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// Token blockIdx.y, stages blockIdx.x * kSplitWarps ..: a warp makes the image of
+// one stage and writes it to the places of the token's pairs.  Every CTA makes
+// the groups; the first leaves them in the workspace and clears the counts.
+template <int FMT>
+__global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitParams p) {
+  constexpr int kPairs = kMoeMaxTokens * kMoeMaxTopK;
+  __shared__ float tops[kSplitWarps];
+  __shared__ __align__(16) char groups[Groups::bytes(kPairs)];
+  __shared__ __align__(16) char scratch[2 * (kSplitWarps + 2) * kMoeMaxExperts];
+  __shared__ uint16_t places[kPairs], members[kPairs];
+  griddep_launch_dependents();
+  griddep_wait();
+  const MoeArgs &a = p.a;
+  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pairs = a.tokens * a.top_k, stage = blockIdx.x * kSplitWarps + warp;
+  float v[8];
+  load_x(a, r, stage * kImageK + lane * 8, v);
+  make_groups<kSplitWarps>(Groups::at(groups, pairs), places, members, scratch, a.ids, pairs,
+                           a.experts, p.group, a.status);
+  if (blockIdx.x == 0 && r == 0) {
+    uint16_t *plan_members = reinterpret_cast<uint16_t *>(a.plan + Groups::bytes(pairs));
+    for (int i = threadIdx.x; i < Groups::bytes(pairs) / 4; i += kSplitWarps * 32)
+      reinterpret_cast<uint32_t *>(a.plan)[i] = reinterpret_cast<const uint32_t *>(groups)[i];
+    for (int i = threadIdx.x; i < pairs; i += kSplitWarps * 32) plan_members[i] = members[i];
+    if (threadIdx.x < kMoeCounts) a.counts[threadIdx.x] = 0;
+  }
+  int row_e = 0;
+  if constexpr (FMT == 1) {
+    float top = 0.0f;
+    raise_finite(top, v);
+    for (int s = warp; s < p.stages; s += kSplitWarps) {
+      if (s == stage) continue;
+      float u[8];
+      load_x(a, r, s * kImageK + lane * 8, u);
+      raise_finite(top, u);
+    }
+    top = warp_max(top);
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, tops[w]);
+    row_e = row_exponent(top);
+    if (blockIdx.x == 0 && threadIdx.x < static_cast<unsigned>(a.top_k)) {
+      const int at = places[r * a.top_k + threadIdx.x];
+      if (at != 0xFFFF) p.image.factors[at] = pow2(row_e);
+    }
+  }
+  if (stage >= p.stages) return;
+  write_digits<FMT>(p.image, stage, v, row_e, a.top_k, [&](int j) { return places[r * a.top_k + j]; },
+                    [&](int at) { return members[at]; });
+}
+
 // ---------------------------------------------------------------- the product
 
-constexpr int kMmaWarps = 6;  // copies, product, four of the epilogue
-constexpr int kMmaThreads = kMmaWarps * 32;
+// Warps: copies, product, four of the epilogue (one tensor-memory lane quarter
+// each), and helpers; the last two kinds make the digits of h and y.
+constexpr int kHelpers = 8;
+constexpr int kWorkers = 4 + kHelpers;
+constexpr int kThreads = (2 + kWorkers) * 32;
 constexpr int kMaxSlots = 16;
-constexpr int kMmaSmem = 227 * 1024;
+constexpr int kSmem = 227 * 1024;
+constexpr int kTile = 128 * 128;  // bytes of a stage's weights, of one matrix
 
-struct MmaParams {
+struct ExpertParams {
   MoeArgs a;
-  const uint8_t *image, *image_scales;
-  const float *factors;
-  int stages;     // of 256 along K
-  int tiles;      // 128-row tiles of an expert
-  int parts;      // ranges of K, each an item with sums of its own
+  Image x, h;
   int slots;      // stages in flight
   int bufs;       // accumulators (1 or 2)
   int b_off, sfa_off, sfb_off, bar_off, groups_at;  // shared memory (the weights at 0)
 };
 
-// UP: gate and up rows, h's partial sums as output; else rows of `hidden`, z's.
-// An item is 128 rows (of each matrix) times a group's pairs over one range of
-// K; a CTA walks consecutive items, group-major.  A product reads its 128 weight
-// rows from shared memory in about 100 clocks however few columns it has
-// (measured: 64-row tiles take as long as 128-row ones), so the tiles are whole and a
-// call with few items divides K instead.
-//
-// Shared memory: a ring of stages: weights (128 rows x 128 bytes of each matrix),
-// images (a kilobyte a pair), scale tiles of the weights and of the group.
-// Tensor memory: accumulators [bufs][SEGS][NB][32 columns], then a set of
-// scale columns for each stage in flight, four columns for each scale tile.
-template <int FMT, bool UP, int NB>
-__global__ void __launch_bounds__(kMmaThreads, 1)
-    expert_mma_kernel(const __grid_constant__ CUtensorMap map0,
-                      const __grid_constant__ CUtensorMap map1, const __grid_constant__ MmaParams p) {
-  constexpr int kSegs = UP ? 2 : 1;
-  constexpr int kAtoms = FMT == 0 ? 2 : 4;       // scale tiles (4 blocks) of a stage
-  constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
-  constexpr int kSfaCols = kAtoms * 4;
-  constexpr int kSfb = kImageScales<FMT>;
-  constexpr int kTile = 128 * 128;               // bytes of a stage's weights, of one matrix
-  extern __shared__ __align__(1024) char smem[];
-  const MoeArgs &a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  constexpr int kGroup = 4 * NB;  // tokens of a group at most
-  const int slots = p.slots;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + p.bar_off);
-  uint64_t *empty = full + slots;
-  uint64_t *acc_full = empty + slots;   // [2]
-  uint64_t *acc_empty = acc_full + 2;   // [2]
-  uint64_t *done = acc_empty + 2;
-  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
-  volatile uint32_t *abort = tmem_slot + 1;
-  if (smem_u32(smem) & 1023u) {  // the 128-byte swizzle needs 1024-byte aligned tiles
-    if (threadIdx.x == 0) atomicOr(a.status, kStatusTimeout);
-    return;
-  }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < slots; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
-    }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&acc_full[i]), 1);
-      mbar_init(smem_u32(&acc_empty[i]), 4);
-    }
-    mbar_init(smem_u32(done), 1);
-    *abort = 0u;
-    fence_barrier_init();
-    prefetch_tmap(&map0);
-    if (UP) prefetch_tmap(&map1);
-  }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(tmem_slot), 512);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
-  griddep_launch_dependents();
-  griddep_wait();
-  const int pairs = a.tokens * a.top_k;
-  for (int i = threadIdx.x; i < Groups::bytes(pairs) / 16; i += kMmaThreads)
-    reinterpret_cast<uint4 *>(smem + p.groups_at)[i] = reinterpret_cast<const uint4 *>(a.plan)[i];
-  __syncthreads();
-  const Groups g = Groups::at(smem + p.groups_at, pairs);
-  const int64_t items = static_cast<int64_t>(*g.count) * p.tiles * p.parts;
-  const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
-  const int end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
-  const int rows = UP ? a.inter : a.hidden, k = UP ? a.hidden : a.inter;
-  const int katoms = (k / (FMT == 0 ? 32 : 16) + 3) >> 2;  // scale tiles along K
-  const int group_items = p.tiles * p.parts;
-  // an item's group, row tile and range of K
+// One of the two products: UP: the gate and up rows, K = hidden, partial sums
+// [parts][2][pairs (by place)][inter]; else the down rows, K = inter, [parts][pairs]
+// [hidden].  An item is 128 rows (of each matrix) times a group's pairs over one
+// range of K; a CTA walks consecutive items, group-major.
+template <bool UP>
+struct Product {
+  static constexpr int kSegs = UP ? 2 : 1;
+  int rows, k, stages, tiles, parts, begin, end;
+
   struct Item {
     int grp, tile, part, st0, st1;
   };
-  const auto item_at = [&](int item) {
+  __device__ __forceinline__ Product(const MoeArgs &a, int groups) {
+    rows = UP ? a.inter : a.hidden;
+    k = UP ? a.hidden : a.inter;
+    stages = (k + kImageK - 1) / kImageK;
+    tiles = (rows + 127) / 128;
+    parts = UP ? a.up_parts : a.down_parts;
+    const int64_t items = static_cast<int64_t>(groups) * tiles * parts;
+    begin = static_cast<int>(items * blockIdx.x / gridDim.x);
+    end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+  }
+  __device__ __forceinline__ Item at(int item) const {
     Item i;
-    i.grp = item / group_items;
-    const int r = item - i.grp * group_items;
-    i.tile = r / p.parts;
-    i.part = r - i.tile * p.parts;
-    i.st0 = p.stages * i.part / p.parts;
-    i.st1 = p.stages * (i.part + 1) / p.parts;
+    i.grp = item / (tiles * parts);
+    const int r = item - i.grp * tiles * parts;
+    i.tile = r / parts;
+    i.part = r - i.tile * parts;
+    i.st0 = stages * i.part / parts;
+    i.st1 = stages * (i.part + 1) / parts;
     return i;
-  };
-  constexpr int acc_cols = kSegs * NB * 32;
-  const uint32_t sf_tmem = tmem + p.bufs * acc_cols;
-  constexpr int sf_cols = (kSegs + 1) * kSfaCols;
+  }
+};
 
-  if (warp == 0) {
-    // ------------------------------------------------------------ copies
-    uint32_t it = 0, s = 0, ph = 0;
-    bool ok = true;
-    for (int item = begin; item < end && ok; ++item) {
-      const Item im = item_at(item);
-      const int grp = im.grp, e = g.expert[grp], n = g.size[grp];
-      const int row0 = im.tile * 128;
-      const int64_t scale_off =
-          (static_cast<int64_t>(e) * p.tiles + im.tile) * static_cast<int64_t>(katoms) * 512;
-      const uint8_t *sf0 = (UP ? a.gate.scales : a.down.scales) + scale_off;
-      const uint8_t *sf1 = UP ? a.up.scales + scale_off : nullptr;
-      const int64_t place = g.begin[grp];
-      for (int st = im.st0; st < im.st1; ++st, ++it) {
-        if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, a.status)) {
-          ok = false;
-          break;
-        }
-        const uint32_t fb = smem_u32(&full[s]);
-        const uint32_t sf_bytes = static_cast<uint32_t>(min(kAtoms, katoms - st * kAtoms)) * 512u;
+// A product reads its 128 weight rows from shared memory in about 100 clocks
+// however few columns it has (measured: tiles of 64 rows take as long), so tiles
+// are whole 128 rows and a call with few items divides K instead.
+//
+// Shared memory: a ring of stages (256 of K): weights (128 rows x 128 bytes of each
+// matrix), images (a kilobyte a pair), scale tiles of the weights and of the group.
+// Tensor memory: accumulators [bufs][2][NB][32 columns], then a set of scale
+// columns for each stage in flight, four columns for each scale tile.
+// Every wait is bounded; after one that ran out the CTA's roles leave, its copies
+// and products in flight are waited for, and the status word says so.
+template <int FMT, int NB>
+struct Expert {
+  static constexpr int kGroup = 4 * NB;                 // pairs of a group at most
+  static constexpr int kAtoms = FMT == 0 ? 2 : 4;       // scale tiles (4 blocks) of a stage
+  static constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
+  static constexpr int kSfaCols = kAtoms * 4;
+  static constexpr int kSfb = kImageScales<FMT>;
+  static constexpr int kAccCols = 2 * NB * 32;
+  static constexpr int kSfCols = 3 * kSfaCols;
+
+  const ExpertParams &p;
+  char *smem;
+  uint64_t *full, *empty, *acc_full, *acc_empty;
+  volatile uint32_t *abort;
+  uint32_t tmem;
+  Groups g;
+  int pairs;
+  // the ring's place (copies or product) and the accumulator's (product or epilogue)
+  uint32_t it = 0, s = 0, ph = 0, buf = 0, bph = 0;
+
+  __device__ __forceinline__ void next_slot() {
+    ++it;
+    if (++s == static_cast<uint32_t>(p.slots)) s = 0, ph ^= 1u;
+  }
+  __device__ __forceinline__ void next_buf() {
+    if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, bph ^= 1u;
+  }
+
+  // ---- copies.  Weights of a stage and, if `images`, its images (a stage's barrier
+  // expects the bytes of both).
+  template <bool UP>
+  __device__ __forceinline__ void copy_weights(const Product<UP> &d, const CUtensorMap *m0,
+                                               const CUtensorMap *m1, const typename Product<UP>::Item &im,
+                                               int st) {
+    constexpr int kSegs = Product<UP>::kSegs;
+    const MoeArgs &a = p.a;
+    const int e = g.expert[im.grp], katoms = (d.k / (FMT == 0 ? 32 : 16) + 3) >> 2;
+    const int64_t off = ((static_cast<int64_t>(e) * d.tiles + im.tile) * katoms + st * kAtoms) * 512;
+    const uint32_t bytes = static_cast<uint32_t>(min(kAtoms, katoms - st * kAtoms)) * 512u;
+    const uint32_t fb = smem_u32(&full[s]), w = smem_u32(smem) + s * 2 * kTile;
+    const uint32_t sf = smem_u32(smem + p.sfa_off) + s * 2 * kSfa;
+    const int row = e * d.rows + im.tile * 128;
+    mbar_arrive_expect_tx(fb, kSegs * (kTile + bytes) + g.size[im.grp] * kImageCodes + kSfb);
+    tma_load_2d(w, m0, st * 128, row, fb);
+    bulk_load(sf, (UP ? a.gate.scales : a.down.scales) + off, bytes, fb);
+    if constexpr (UP) {
+      tma_load_2d(w + kTile, m1, st * 128, row, fb);
+      bulk_load(sf + kSfa, a.up.scales + off, bytes, fb);
+    }
+  }
+  __device__ __forceinline__ void copy_images(const Image &im, int grp, int st, uint32_t slot) {
+    const uint32_t fb = smem_u32(&full[slot]);
+    const int64_t at = static_cast<int64_t>(st) * pairs;
+    bulk_load(smem_u32(smem + p.b_off) + slot * kGroup * kImageCodes,
+              im.codes + (at + g.begin[grp]) * kImageCodes, g.size[grp] * kImageCodes, fb);
+    bulk_load(smem_u32(smem + p.sfb_off) + slot * kSfb, im.scales + (at + grp) * kSfb, kSfb, fb);
+  }
+  // The copies of a product.  images: they can be read from the start; else ready()
+  // waits for them (whole warp), and until the ring is full weights run ahead.
+  template <bool UP, typename Ready>
+  __device__ __forceinline__ bool copies(const Product<UP> &d, const CUtensorMap *m0,
+                                         const CUtensorMap *m1, const Image &im, bool images,
+                                         const Ready &ready) {
+    typename Product<UP>::Item cur{}, old{};
+    int late_item = d.begin, late_st = 0, late = 0;  // stages whose images are still to come
+    uint32_t late_slot = s;
+    const auto catch_up = [&]() {
+      if (!ready()) return false;
+      for (; late > 0; --late) {
+        if (elect_one()) copy_images(im, old.grp, late_st, late_slot);
+        __syncwarp();
+        if (++late_slot == static_cast<uint32_t>(p.slots)) late_slot = 0;
+        if (++late_st == old.st1 && ++late_item < d.end) old = d.at(late_item), late_st = old.st0;
+      }
+      images = true;
+      return true;
+    };
+    for (int item = d.begin; item < d.end; ++item) {
+      cur = d.at(item);
+      if (item == d.begin) old = cur, late_st = cur.st0;
+      for (int st = cur.st0; st < cur.st1; ++st) {
+        // (the slots of the first stages come free with the products before them)
+        if (!images && late == p.slots && !catch_up()) return false;
+        if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, p.a.status)) return false;
         if (elect_one()) {
-          mbar_arrive_expect_tx(fb, kSegs * (kTile + sf_bytes) + n * kImageCodes + kSfb);
-          const uint32_t w = smem_u32(smem) + s * kSegs * kTile;
-          const uint32_t sf = smem_u32(smem + p.sfa_off) + s * kSegs * kSfa;
-          tma_load_2d(w, &map0, st * 128, e * rows + row0, fb);
-          bulk_load(sf, sf0 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
-          if constexpr (UP) {
-            tma_load_2d(w + kTile, &map1, st * 128, e * rows + row0, fb);
-            bulk_load(sf + kSfa, sf1 + static_cast<int64_t>(st) * kSfa, sf_bytes, fb);
-          }
-          const int64_t at = static_cast<int64_t>(st) * pairs;
-          bulk_load(smem_u32(smem + p.b_off) + s * kGroup * kImageCodes,
-                    p.image + (at + place) * kImageCodes, n * kImageCodes, fb);
-          bulk_load(smem_u32(smem + p.sfb_off) + s * kSfb, p.image_scales + (at + grp) * kSfb, kSfb,
-                    fb);
+          copy_weights<UP>(d, m0, m1, cur, st);
+          if (images) copy_images(im, cur.grp, st, s);
         }
         __syncwarp();
-        if (++s == static_cast<uint32_t>(slots)) s = 0, ph ^= 1u;
+        if (!images) ++late;
+        next_slot();
       }
     }
-    // no copy may land after the CTA has left
-    const uint32_t inflight = it < static_cast<uint32_t>(slots) ? it : static_cast<uint32_t>(slots);
-    for (uint32_t j = it - inflight; j < it; ++j)
-      mbar_drain(smem_u32(&full[j % slots]), (j / slots) & 1u);
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ product
-    uint32_t s = 0, ph = 0, buf = 0, bph = 0;
-    bool ok = true;
-    // One thread issues every product, so a product has to cost it few
-    // instructions: the loops are unrolled and descriptors stepped by constants.
+    return late == 0 || catch_up();
+  }
+
+  // ---- products.  One thread issues every one, so it has to cost few instructions:
+  // the loops are unrolled and descriptors stepped by constants.
+  template <bool UP>
+  __device__ __forceinline__ bool products(const Product<UP> &d) {
+    constexpr int kSegs = Product<UP>::kSegs;
     const uint32_t w_ring = smem_u32(smem), b_ring = smem_u32(smem + p.b_off);
     const uint32_t sfa_ring = smem_u32(smem + p.sfa_off), sfb_ring = smem_u32(smem + p.sfb_off);
-    for (int item = begin; item < end && ok; ++item) {
-      const Item im = item_at(item);
-      const int grp = im.grp;
+    const uint32_t sf_tmem = tmem + p.bufs * kAccCols;
+    const int katoms = (d.k / (FMT == 0 ? 32 : 16) + 3) >> 2;
+    for (int item = d.begin; item < d.end; ++item) {
+      const typename Product<UP>::Item im = d.at(item);
       // columns: the digits of the group, to a multiple of 16
-      const uint32_t columns = static_cast<uint32_t>(g.size[grp] * kDigits + 15) & ~15u;
+      const uint32_t columns = static_cast<uint32_t>(g.size[im.grp] * kDigits + 15) & ~15u;
       const uint32_t idesc0 = mma_idesc<FMT>(128, columns, 0);
       const uint32_t idesc2 = mma_idesc<FMT>(128, columns, 2);
-      ok = mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, a.status);
-      if (!ok) break;
+      if (!mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, p.a.status)) return false;
       tc_fence_after();
-      const uint32_t acc = tmem + buf * acc_cols;
+      const uint32_t acc = tmem + buf * kAccCols;
       for (int st = im.st0; st < im.st1; ++st) {
-        if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort, a.status)) {
-          ok = false;
-          break;
-        }
+        if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort, p.a.status)) return false;
         tc_fence_after();
         if (elect_one()) {
-          const uint32_t sfa_t = sf_tmem + s * sf_cols, sfb_t = sfa_t + kSegs * kSfaCols;
-          const uint64_t sfa = smem_desc_scale_block(sfa_ring + s * kSegs * kSfa);
+          const uint32_t sfa_t = sf_tmem + s * kSfCols, sfb_t = sfa_t + 2 * kSfaCols;
+          const uint64_t sfa = smem_desc_scale_block(sfa_ring + s * 2 * kSfa);
           const uint64_t sfb = smem_desc_scale_block(sfb_ring + s * kSfb);
           const int atoms = min(kAtoms, katoms - st * kAtoms);
-          const int steps = min(4, (k - st * kImageK + 63) >> 6);  // of 64 inside K
+          const int steps = min(4, (d.k - st * kImageK + 63) >> 6);  // of 64 inside K
 #pragma unroll
           for (int j = 0; j < kAtoms; ++j)
             tc_cp_32x128b_warpx4(sfb_t + j * 4, sfb + ((j * 512) >> 4));
@@ -457,12 +436,11 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
             for (int i = 0; i < kAtoms; ++i) {
               if (i < atoms)
-                tc_cp_32x128b_warpx4(sfa_t + m * kSfaCols + i * 4,
-                                     sfa + ((m * kSfa + i * 512) >> 4));
+                tc_cp_32x128b_warpx4(sfa_t + m * kSfaCols + i * 4, sfa + ((m * kSfa + i * 512) >> 4));
             }
           }
-          const uint64_t wd = smem_desc_sw128_kmajor(w_ring + s * kSegs * kTile);
-          const uint64_t bd = smem_desc_sw128_kmajor(b_ring + s * kGroup * 1024);
+          const uint64_t wd = smem_desc_sw128_kmajor(w_ring + s * 2 * kTile);
+          const uint64_t bd = smem_desc_sw128_kmajor(b_ring + s * kGroup * kImageCodes);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
             if (kk < steps) {
@@ -479,28 +457,28 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           if (st == im.st1 - 1) tc_commit(smem_u32(&acc_full[buf]));
         }
         __syncwarp();
-        if (++s == static_cast<uint32_t>(slots)) s = 0, ph ^= 1u;
+        next_slot();
       }
-      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, bph ^= 1u;
+      next_buf();
     }
-    // every product issued has finished before the tensor memory goes
-    if (elect_one()) tc_commit(smem_u32(done));
-    __syncwarp();
-    mbar_drain(smem_u32(done), 0u);
-  } else {
-    // ------------------------------------------------------------ epilogue
-    const int q = warp & 3;  // this warp's lane quarter
-    uint32_t buf = 0, bph = 0;
-    const int64_t out_extent = static_cast<int64_t>(p.parts) * kSegs * pairs * rows;
-    for (int item = begin; item < end; ++item) {
-      const Item im = item_at(item);
-      const int grp = im.grp, e = g.expert[grp], n = g.size[grp];
-      const int row = im.tile * 128 + q * 32 + lane;
+    return true;
+  }
+
+  // ---- epilogue (a warp per lane quarter): the sums of the digits' columns.
+  template <bool UP>
+  __device__ __forceinline__ void epilogue(const Product<UP> &d, const float *factors) {
+    constexpr int kSegs = Product<UP>::kSegs;
+    const MoeArgs &a = p.a;
+    const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
+    const int64_t extent = static_cast<int64_t>(d.parts) * kSegs * pairs * d.rows;
+    for (int item = d.begin; item < d.end; ++item) {
+      const typename Product<UP>::Item im = d.at(item);
+      const int e = g.expert[im.grp], n = g.size[im.grp], row = im.tile * 128 + q * 32 + lane;
       const float alpha0 = FMT == 1 ? (UP ? a.gate.ts : a.down.ts)[e] : 1.0f;
       const float alpha1 = FMT == 1 && UP ? a.up.ts[e] : 1.0f;
-      if (!mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status)) break;
+      if (!mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status)) return;
       tc_fence_after();
-      const uint32_t acc = tmem + buf * acc_cols + (static_cast<uint32_t>(q * 32) << 16);
+      const uint32_t acc = tmem + buf * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
       for (int i = 0; i < (n + 3) / 4; ++i) {
         float sum[kSegs][4];
 #pragma unroll
@@ -508,17 +486,17 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
           uint32_t r[32];
           tc_ld_32x32b_x32(acc + (m * NB + i) * 32, r);
           tc_wait_ld();
-          // the digits' sums, the least first
+          // the least digit first
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float t = 0.0f;
 #pragma unroll
-            for (int d = kDigits - 1; d >= 0; --d) {
-              const float v = __uint_as_float(r[j * 8 + d]);
+            for (int dg = kDigits - 1; dg >= 0; --dg) {
+              const float v = __uint_as_float(r[j * 8 + dg]);
               if constexpr (FMT == 0)
                 t = __fadd_rn(t, v);
               else
-                t = __fmaf_rn(v, 1.0f / static_cast<float>(1 << digit_shift(d)), t);
+                t = __fmaf_rn(v, 1.0f / static_cast<float>(1 << digit_shift(dg)), t);
             }
             sum[m][j] = t;
           }
@@ -526,142 +504,340 @@ __global__ void __launch_bounds__(kMmaThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = i * 4 + j;
-          if (c >= n || row >= rows) continue;
-          const int place = g.begin[grp] + c, pair = g.list[place];
-          const float f = FMT == 1 ? p.factors[place] : 1.0f;
+          if (c >= n || row >= d.rows) continue;
+          const int place = g.begin[im.grp] + c;
+          const float f = FMT == 1 ? __ldcg(factors + place) : 1.0f;
 #pragma unroll
           for (int m = 0; m < kSegs; ++m) {
             const float v = FMT == 1 ? sum[m][j] * f * (m == 0 ? alpha0 : alpha1) : sum[m][j];
             const int64_t o = (static_cast<int64_t>(im.part * kSegs + m) * pairs +
-                               (UP ? place : pair)) * rows + row;
-            if (in_bounds(o, 1, out_extent, a.status)) (UP ? a.h : a.z)[o] = v;
+                               (UP ? place : g.list[place])) * d.rows + row;
+            if (in_bounds(o, 1, extent, a.status)) (UP ? a.h : a.z)[o] = v;
           }
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
-      if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, bph ^= 1u;
+      next_buf();
     }
+  }
+
+  // ---- the digits of h.  A warp takes a row's stage (MXFP4) or a row (NVFP4, whose
+  // factor needs all of it).
+  __device__ __forceinline__ void load_h(int r, int at, float (&v)[8]) const {
+    const MoeArgs &a = p.a;
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
+    if (at >= a.inter) return;
+    const int64_t part = static_cast<int64_t>(pairs) * a.inter;
+    const int64_t extent = 2 * a.up_parts * part;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
+      if (i >= a.up_parts) break;
+      const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
+      if (!in_bounds(off, 8, extent, a.status) || !in_bounds(off + part, 8, extent, a.status)) continue;
+      const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
+      const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
+      const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
+      v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
+      v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
+      u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
+      u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+      const float2 f = a.gelu ? gelu_f32x2(make_float2(v[i], v[i + 1]))
+                              : make_float2(v[i] / (1.0f + expf(-v[i])),
+                                            v[i + 1] / (1.0f + expf(-v[i + 1])));
+      v[i] = f.x * u[i];
+      v[i + 1] = f.y * u[i + 1];
+    }
+  }
+  __device__ __forceinline__ void split_h(int worker) {
+    const MoeArgs &a = p.a;
+    const int lane = threadIdx.x & 31, groups = *g.count;
+    if (groups == 0) return;
+    const int rows = g.begin[groups - 1] + g.size[groups - 1];
+    const int stages = (a.inter + kImageK - 1) / kImageK;
+    const uint16_t *members = reinterpret_cast<const uint16_t *>(a.plan + Groups::bytes(pairs));
+    const int workers = kWorkers * gridDim.x, first = worker * gridDim.x + blockIdx.x;
+    if constexpr (FMT == 0) {
+      for (int t = first; t < rows * stages; t += workers) {
+        const int r = t / stages, st = t - r * stages;
+        float v[8];
+        load_h(r, st * kImageK + lane * 8, v);
+        const int mem = members[r];
+        write_digits<FMT>(p.h, st, v, 0, 1, [&](int) { return r; }, [&](int) { return mem; });
+      }
+    } else {
+      for (int r = first; r < rows; r += workers) {
+        float top = 0.0f, v[8];
+        for (int st = 0; st < stages; ++st) {
+          load_h(r, st * kImageK + lane * 8, v);
+          raise_finite(top, v);
+        }
+        const int row_e = row_exponent(warp_max(top)), mem = members[r];
+        if (lane == 0) p.h.factors[r] = pow2(row_e);
+        for (int st = 0; st < stages; ++st) {
+          load_h(r, st * kImageK + lane * 8, v);
+          write_digits<FMT>(p.h, st, v, row_e, 1, [&](int) { return r; }, [&](int) { return mem; });
+        }
+      }
+    }
+  }
+
+  // ---- y[t] = sum_j w_tj z[t, j], in the order of the slots; two columns a thread.
+  __device__ __forceinline__ void combine(int worker) {
+    const MoeArgs &a = p.a;
+    const int lane = threadIdx.x & 31, spans = (a.hidden + 63) / 64;
+    const int64_t part = static_cast<int64_t>(pairs) * a.hidden;
+    for (int t = worker * gridDim.x + blockIdx.x; t < a.tokens * spans; t += kWorkers * gridDim.x) {
+      const int token = t / spans, c = (t - token * spans) * 64 + lane * 2;
+      // lane j has slot j's expert and weight
+      int e = -1;
+      float wt = 0.0f;
+      if (lane < a.top_k) e = a.ids[token * a.top_k + lane], wt = a.weights[token * a.top_k + lane];
+      float y0 = 0.0f, y1 = 0.0f;
+      for (int j0 = 0; j0 < a.top_k; j0 += 8) {
+        float2 z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          z[j] = make_float2(0.0f, 0.0f);
+          const int ej = __shfl_sync(0xFFFFFFFFu, e, (j0 + j) & 31);
+          if (j0 + j < a.top_k && ej >= 0 && ej < a.experts && c < a.hidden) {
+            for (int i = 0; i < a.down_parts; ++i) {
+              const int64_t o = i * part + static_cast<int64_t>(token * a.top_k + j0 + j) * a.hidden + c;
+              if (!in_bounds(o, 2, a.down_parts * part, a.status)) continue;
+              const float2 v = __ldcg(reinterpret_cast<const float2 *>(a.z + o));
+              z[j].x += v.x;
+              z[j].y += v.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int ej = __shfl_sync(0xFFFFFFFFu, e, (j0 + j) & 31);
+          const float w = __shfl_sync(0xFFFFFFFFu, wt, (j0 + j) & 31);
+          if (j0 + j < a.top_k && ej >= 0 && ej < a.experts) {
+            y0 = __fmaf_rn(w, z[j].x, y0);
+            y1 = __fmaf_rn(w, z[j].y, y1);
+          }
+        }
+      }
+      if (c >= a.hidden) continue;
+      const int64_t o = token * a.ld_y + c;
+      if (!in_bounds(o, 2, (a.tokens - 1) * a.ld_y + a.hidden, a.status)) continue;
+      uint16_t *y = static_cast<uint16_t *>(a.y) + o;
+      y[0] = bf16_bits(y0);
+      y[1] = bf16_bits(y1);
+    }
+  }
+
+  // ---- the grid-wide counts.  The CTAs are resident together (a cooperative
+  // launch); a wait is bounded all the same.
+  __device__ __forceinline__ bool count_reached(int i) const {
+    const uint64_t t0 = globaltimer_ns();
+    while (true) {
+      uint32_t v;
+      asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(p.a.counts + i) : "memory");
+      if (v >= gridDim.x) return true;
+      if (*abort) return false;
+      if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
+        *abort = 1u;
+        atomicOr(p.a.status, kStatusTimeout);
+        return false;
+      }
+    }
+  }
+  // All workers: what they wrote is counted once for the CTA.
+  __device__ __forceinline__ void add_count(int i) const {
+    asm volatile("fence.proxy.async;" ::: "memory");  // digits are read by bulk copies
+    __threadfence();
+    named_barrier_sync(1, kWorkers * 32);
+    if (threadIdx.x == 64)
+      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.a.counts + i) : "memory");
+  }
+  // All workers: every CTA's count i has come (false: given up).
+  __device__ __forceinline__ bool all_counted(int i, volatile uint32_t *flag) const {
+    if (threadIdx.x == 64) *flag = count_reached(i) ? 1u : 0u;
+    named_barrier_sync(1, kWorkers * 32);
+    const bool ok = *flag != 0u;
+    __threadfence();
+    named_barrier_sync(1, kWorkers * 32);
+    return ok;
+  }
+};
+
+template <int FMT, int NB>
+__global__ void __launch_bounds__(kThreads, 1)
+    expert_kernel(const __grid_constant__ CUtensorMap gate_map,
+                  const __grid_constant__ CUtensorMap up_map,
+                  const __grid_constant__ CUtensorMap down_map,
+                  const __grid_constant__ ExpertParams p) {
+  extern __shared__ __align__(1024) char smem[];
+  const MoeArgs &a = p.a;
+  const int warp = threadIdx.x >> 5;
+  Expert<FMT, NB> x{p, smem};
+  x.full = reinterpret_cast<uint64_t *>(smem + p.bar_off);
+  x.empty = x.full + p.slots;
+  x.acc_full = x.empty + p.slots;   // [2]
+  x.acc_empty = x.acc_full + 2;     // [2]
+  uint64_t *done = x.acc_empty + 2;
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+  x.abort = tmem_slot + 1;
+  volatile uint32_t *flag = tmem_slot + 2;
+  x.pairs = a.tokens * a.top_k;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.slots; ++s) {
+      mbar_init(smem_u32(&x.full[s]), 1);
+      mbar_init(smem_u32(&x.empty[s]), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&x.acc_full[i]), 1);
+      mbar_init(smem_u32(&x.acc_empty[i]), 4);
+    }
+    mbar_init(smem_u32(done), 1);
+    // the 128-byte swizzle needs 1024-byte aligned tiles
+    const bool aligned = (smem_u32(smem) & 1023u) == 0;
+    *x.abort = aligned ? 0u : 1u;
+    if (!aligned) atomicOr(a.status, kStatusTimeout);
+    fence_barrier_init();
+    prefetch_tmap(&gate_map);
+    prefetch_tmap(&up_map);
+    prefetch_tmap(&down_map);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  griddep_launch_dependents();
+  griddep_wait();
+  for (int i = threadIdx.x; i < Groups::bytes(x.pairs) / 16; i += kThreads)
+    reinterpret_cast<uint4 *>(smem + p.groups_at)[i] = reinterpret_cast<const uint4 *>(a.plan)[i];
+  __syncthreads();
+  tc_fence_after();
+  x.tmem = *tmem_slot;
+  x.g = Groups::at(smem + p.groups_at, x.pairs);
+  const Product<true> up(a, *x.g.count);
+  const Product<false> down(a, *x.g.count);
+
+  if (warp == 0) {
+    bool ok = !*x.abort;
+    ok = ok && x.template copies<true>(up, &gate_map, &up_map, p.x, true, [] { return true; });
+    // the digits of h are there when every CTA has counted them
+    ok = ok && x.template copies<false>(down, &down_map, &down_map, p.h, false, [&] {
+      const bool r = x.count_reached(1);
+      asm volatile("fence.proxy.async;" ::: "memory");
+      return __all_sync(0xFFFFFFFFu, r) != 0;
+    });
+    // No copy may land after the CTA has left.  (After an abort a stage may lack
+    // its images: that wait runs out, with no copy left behind it.)
+    const uint32_t slots = static_cast<uint32_t>(p.slots);
+    for (uint32_t j = x.it < slots ? 0u : x.it - slots; j < x.it; ++j)
+      mbar_drain(smem_u32(&x.full[j % slots]), (j / slots) & 1u);
+  } else if (warp == 1) {
+    if (!*x.abort && x.template products<true>(up)) x.template products<false>(down);
+    // every product issued has finished before the tensor memory goes
+    if (elect_one()) tc_commit(smem_u32(done));
+    __syncwarp();
+    mbar_drain(smem_u32(done), 0u);
+  } else {
+    const int worker = warp - 2;
+    if (worker < 4) x.template epilogue<true>(up, p.x.factors);
+    x.add_count(0);
+    if (x.all_counted(0, flag)) x.split_h(worker);
+    x.add_count(1);
+    if (FMT == 1) x.all_counted(1, flag);  // the epilogue reads the factors
+    if (worker < 4) x.template epilogue<false>(down, p.h.factors);
+    x.add_count(2);
+    if (x.all_counted(2, flag)) x.combine(worker);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(x.tmem, 512);
   }
 }
 
-// Pairs of a group: the product takes them together, in quarters of 32 columns.
+// Pairs of a group: a product takes them together, in quarters of 32 columns.
 int group_size(const MoeArgs &a) { return a.tokens <= 4 ? 4 : a.tokens <= 8 ? 8 : 16; }
 
 // The images in the workspace: codes of x, scales of x, codes of h, scales of h.
-struct Images {
-  uint8_t *codes, *scales;
-};
-Images images(const MoeArgs &a, bool of_h) {
+Image image_of(const MoeArgs &a, bool of_h) {
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
   uint8_t *at = a.image + (of_h ? moe_image_bytes(pairs, a.hidden) : 0);
   const int64_t stages = ((of_h ? a.inter : a.hidden) + kImageK - 1) / kImageK;
-  return Images{at, at + pairs * stages * kImageCodes};
+  return Image{at, at + pairs * stages * kImageCodes, a.factors + (of_h ? pairs : 0),
+               static_cast<int>(pairs)};
 }
 
-template <int FMT, typename XT>
-cudaError_t launch_split(const MoeArgs &a, const void *x, int64_t ld, int rows, int k, Images out,
-                         float *factors, cudaStream_t s) {
-  SplitParams p{};
-  p.x = x;
-  p.ld = ld;
-  p.extent = sizeof(XT) == 2 ? (rows - 1) * ld + k
-                             : static_cast<int64_t>(a.up_parts) * 2 * rows * k;
-  p.parts = a.up_parts;
-  p.gelu = a.gelu;
-  p.k = k;
-  p.stages = (k + kImageK - 1) / kImageK;
-  p.ids = a.ids;
-  p.pairs = a.tokens * a.top_k;
-  p.experts = a.experts;
-  p.top_k = a.top_k;
-  p.group = group_size(a);
-  p.plan = a.plan;
-  p.codes = out.codes;
-  p.scales = out.scales;
-  p.factors = factors;
-  p.status = a.status;
-  return launch_pdl(split_kernel<FMT, XT>, dim3((p.stages + kSplitWarps - 1) / kSplitWarps, rows),
-                    dim3(kSplitWarps * 32), 0, s, p);
-}
-
-template <int FMT, bool UP, int NB>
-cudaError_t launch_mma(const MoeArgs &a, Images image, const float *factors, cudaStream_t s) {
-  constexpr int kSegs = UP ? 2 : 1, kAtoms = FMT == 0 ? 2 : 4;
-  const auto kernel = expert_mma_kernel<FMT, UP, NB>;
+template <int FMT, int NB>
+cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
+  using X = Expert<FMT, NB>;
+  const auto kernel = expert_kernel<FMT, NB>;
   const void *func = reinterpret_cast<const void *>(kernel);
   if (!kernel_setup_get(func, nullptr)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kMmaSmem);
+        cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     kernel_setup_put(func, 0);
   }
-  const int rows = UP ? a.inter : a.hidden, k = UP ? a.hidden : a.inter;
   const int pairs = a.tokens * a.top_k;
-  MmaParams p{};
+  ExpertParams p{};
   p.a = a;
-  p.image = image.codes;
-  p.image_scales = image.scales;
-  p.factors = factors;
-  p.stages = (k + kImageK - 1) / kImageK;
-  constexpr int kGroup = 4 * NB;
-  p.tiles = (rows + 127) / 128;
-  p.parts = UP ? a.up_parts : a.down_parts;
-  constexpr int kTile = 128 * 128;
-  constexpr int per_slot =
-      kSegs * (kTile + kAtoms * 512) + kGroup * kImageCodes + kImageScales<FMT>;
-  const int fixed = 512 + Groups::bytes(pairs);
-  constexpr int sf_cols = (kSegs + 1) * kAtoms * 4, acc = kSegs * NB * 32;
-  int slots = (kMmaSmem - fixed) / per_slot;
+  p.x = image_of(a, false);
+  p.h = image_of(a, true);
+  constexpr int per_slot = 2 * (kTile + X::kSfa) + X::kGroup * kImageCodes + X::kSfb;
+  int slots = (kSmem - 512 - Groups::bytes(pairs)) / per_slot;
   slots = slots < kMaxSlots ? slots : kMaxSlots;
-  p.bufs = 2 * acc + 4 * sf_cols <= 512 ? 2 : 1;
-  const int tmem_slots = (512 - p.bufs * acc) / sf_cols;
+  p.bufs = 2 * X::kAccCols + 4 * X::kSfCols <= 512 ? 2 : 1;
+  const int tmem_slots = (512 - p.bufs * X::kAccCols) / X::kSfCols;
   p.slots = slots < tmem_slots ? slots : tmem_slots;
   if (p.slots < 2) return cudaErrorInvalidValue;
-  p.b_off = p.slots * kSegs * kTile;
-  p.sfa_off = p.b_off + p.slots * kGroup * 1024;
-  p.sfb_off = p.sfa_off + p.slots * kSegs * kAtoms * 512;
-  p.bar_off = p.sfb_off + p.slots * kImageScales<FMT>;
+  p.b_off = p.slots * 2 * kTile;
+  p.sfa_off = p.b_off + p.slots * X::kGroup * kImageCodes;
+  p.sfb_off = p.sfa_off + p.slots * 2 * X::kSfa;
+  p.bar_off = p.sfb_off + p.slots * X::kSfb;
   p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + 15) / 16 * 16;
   const int smem = p.groups_at + Groups::bytes(pairs);
-  if (smem > kMmaSmem) return cudaErrorInvalidValue;
-  CUtensorMap map0, map1;
-  const int64_t stacked = static_cast<int64_t>(a.experts) * rows;
-  if (!encode_codes_window_map(&map0, UP ? a.gate.codes : a.down.codes, stacked, k, 128) ||
-      !encode_codes_window_map(&map1, UP ? a.up.codes : a.down.codes, stacked, k, 128))
+  if (smem > kSmem) return cudaErrorInvalidValue;
+  CUtensorMap gate, up, down;
+  const int64_t inner = static_cast<int64_t>(a.experts) * a.inter;
+  if (!encode_codes_window_map(&gate, a.gate.codes, inner, a.hidden, 128) ||
+      !encode_codes_window_map(&up, a.up.codes, inner, a.hidden, 128) ||
+      !encode_codes_window_map(&down, a.down.codes, static_cast<int64_t>(a.experts) * a.hidden,
+                               a.inter, 128))
     return cudaErrorInvalidValue;
-  const int most = a.experts < pairs ? a.experts : pairs;  // experts with a pair
-  const int64_t items = static_cast<int64_t>(most + pairs / kGroup) * p.tiles * p.parts;
-  const int grid = items < a.num_sms ? static_cast<int>(items) : a.num_sms;
-  return launch_pdl(kernel, dim3(grid), dim3(kMmaThreads), smem, s, map0, map1, p);
-}
-
-template <int FMT, bool UP>
-cudaError_t launch_product(const MoeArgs &a, Images image, const float *factors, cudaStream_t s) {
-  if (a.tokens <= 4) return launch_mma<FMT, UP, 1>(a, image, factors, s);
-  if (a.tokens <= 8) return launch_mma<FMT, UP, 2>(a, image, factors, s);
-  return launch_mma<FMT, UP, 4>(a, image, factors, s);
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeCooperative;  // the CTAs wait on one another
+  attr[1].val.cooperative = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(a.num_sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, gate, up, down, p);
 }
 
 template <int FMT>
 cudaError_t launch_all(const MoeArgs &a, cudaStream_t s) {
-  const int pairs = a.tokens * a.top_k;
-  const Images x = images(a, false), h = images(a, true);
-  cudaError_t e =
-      launch_split<FMT, uint16_t>(a, a.x, a.ld_x, a.tokens, a.hidden, x, a.factors, s);
-  if (e == cudaSuccess) e = launch_product<FMT, true>(a, x, a.factors, s);
-  if (e == cudaSuccess)
-    e = launch_split<FMT, float>(a, a.h, a.inter, pairs, a.inter, h, a.factors + pairs, s);
-  if (e == cudaSuccess) e = launch_product<FMT, false>(a, h, a.factors + pairs, s);
-  return e;
+  SplitParams p{a, image_of(a, false), (a.hidden + kImageK - 1) / kImageK, group_size(a)};
+  const cudaError_t e =
+      launch_pdl(split_kernel<FMT>, dim3((p.stages + kSplitWarps - 1) / kSplitWarps, a.tokens),
+                 dim3(kSplitWarps * 32), 0, s, p);
+  if (e != cudaSuccess) return e;
+  if (a.tokens <= 4) return launch_expert_kernel<FMT, 1>(a, s);
+  if (a.tokens <= 8) return launch_expert_kernel<FMT, 2>(a, s);
+  return launch_expert_kernel<FMT, 4>(a, s);
 }
 
 }  // namespace
@@ -688,7 +864,7 @@ size_t moe_plan_bytes(int64_t pairs) {
   return static_cast<size_t>(Groups::bytes(static_cast<int>(pairs))) + static_cast<size_t>(pairs) * 2;
 }
 
-cudaError_t launch_expert_products(const MoeArgs &a, cudaStream_t s) {
+cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s) {
   return a.fmt == 0 ? launch_all<0>(a, s) : launch_all<1>(a, s);
 }
 

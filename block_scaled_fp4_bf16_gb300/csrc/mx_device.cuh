@@ -663,4 +663,15 @@ __device__ __forceinline__ uint32_t cvt_e4m3(float v) {
   return out & 0xFFu;
 }
 
+// Element i of a BF16 array, and a value's BF16 bits (round to nearest even).
+__device__ __forceinline__ float bf16_value(const void *p, int64_t i) {
+  return __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(p)[i]) << 16);
+}
+
+__device__ __forceinline__ uint16_t bf16_bits(float v) {
+  uint32_t out;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(out) : "f"(0.0f), "f"(v));
+  return static_cast<uint16_t>(out & 0xFFFFu);
+}
+
 }  // namespace mx

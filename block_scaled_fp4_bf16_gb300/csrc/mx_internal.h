@@ -246,18 +246,18 @@ struct MoeArgs {
   uint8_t *image;      // digits of x, then of h (moe_image_bytes)
   float *factors;      // NVFP4: of the rows of x, then of h
   char *plan;          // the pairs' groups (moe_plan_bytes)
+  uint32_t *counts;    // kMoeCounts grid-wide counts
   int num_sms;
   uint32_t *status;
 };
 // Bytes of the digits of `rows` rows of k activations.
 size_t moe_image_bytes(int64_t rows, int64_t k);
+constexpr int kMoeCounts = 4;
 // Ranges of K that a product is divided into, and the most for a number of pairs.
 int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms);
 constexpr int moe_max_parts(int64_t pairs) { return pairs <= 16 ? 4 : pairs <= 64 ? 2 : 1; }
 // Bytes of the groups of `pairs` pairs.
 size_t moe_plan_bytes(int64_t pairs);
-// h and z (moe_mma.cu), and then y.
-cudaError_t launch_expert_products(const MoeArgs &a, cudaStream_t s);
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
 
 // Launch with programmatic stream serialization (the kernel itself orders
