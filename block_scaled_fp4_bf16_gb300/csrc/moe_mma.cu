@@ -320,6 +320,7 @@ struct Expert {
   uint64_t *full, *empty, *acc_full, *acc_empty;
   volatile uint32_t *abort;
   uint32_t tmem;
+  float *tops;  // [kWorkers]
   Groups g;
   int pairs;
   // the ring's place (copies or product) and the accumulator's (product or epilogue)
@@ -523,8 +524,8 @@ struct Expert {
     }
   }
 
-  // ---- the digits of h.  A warp takes a row's stage (MXFP4) or a row (NVFP4, whose
-  // factor needs all of it).
+  // ---- the digits of h.  A warp takes a row's stage; NVFP4, whose factor needs all
+  // of a row: the CTA's workers take a row.
   __device__ __forceinline__ void load_h(int r, int at, float (&v)[8]) const {
     const MoeArgs &a = p.a;
     float u[8];
@@ -562,9 +563,8 @@ struct Expert {
     const int rows = g.begin[groups - 1] + g.size[groups - 1];
     const int stages = (a.inter + kImageK - 1) / kImageK;
     const uint16_t *members = reinterpret_cast<const uint16_t *>(a.plan + Groups::bytes(pairs));
-    const int workers = kWorkers * gridDim.x, first = worker * gridDim.x + blockIdx.x;
     if constexpr (FMT == 0) {
-      for (int t = first; t < rows * stages; t += workers) {
+      for (int t = worker * gridDim.x + blockIdx.x; t < rows * stages; t += kWorkers * gridDim.x) {
         const int r = t / stages, st = t - r * stages;
         float v[8];
         load_h(r, st * kImageK + lane * 8, v);
@@ -572,16 +572,25 @@ struct Expert {
         write_digits<FMT>(p.h, st, v, 0, 1, [&](int) { return r; }, [&](int) { return mem; });
       }
     } else {
-      for (int r = first; r < rows; r += workers) {
+      for (int r = blockIdx.x; r < rows; r += gridDim.x) {
         float top = 0.0f, v[8];
-        for (int st = 0; st < stages; ++st) {
-          load_h(r, st * kImageK + lane * 8, v);
-          raise_finite(top, v);
+        load_h(r, worker * kImageK + lane * 8, v);
+        raise_finite(top, v);
+        for (int st = worker + kWorkers; st < stages; st += kWorkers) {
+          float u[8];
+          load_h(r, st * kImageK + lane * 8, u);
+          raise_finite(top, u);
         }
-        const int row_e = row_exponent(warp_max(top)), mem = members[r];
-        if (lane == 0) p.h.factors[r] = pow2(row_e);
-        for (int st = 0; st < stages; ++st) {
-          load_h(r, st * kImageK + lane * 8, v);
+        top = warp_max(top);
+        if (lane == 0) tops[worker] = top;
+        named_barrier_sync(1, kWorkers * 32);
+#pragma unroll
+        for (int w = 0; w < kWorkers; ++w) top = fmaxf(top, tops[w]);
+        named_barrier_sync(1, kWorkers * 32);
+        const int row_e = row_exponent(top), mem = members[r];
+        if (threadIdx.x == 64) p.h.factors[r] = pow2(row_e);
+        for (int st = worker; st < stages; st += kWorkers) {
+          if (st != worker) load_h(r, st * kImageK + lane * 8, v);
           write_digits<FMT>(p.h, st, v, row_e, 1, [&](int) { return r; }, [&](int) { return mem; });
         }
       }
@@ -601,20 +610,23 @@ struct Expert {
       if (lane < a.top_k) e = a.ids[token * a.top_k + lane], wt = a.weights[token * a.top_k + lane];
       float y0 = 0.0f, y1 = 0.0f;
       for (int j0 = 0; j0 < a.top_k; j0 += 8) {
-        float2 z[8];
+        // all loads before any use; an empty slot's are made too and then dropped
+        float2 z[8] = {};
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          z[j] = make_float2(0.0f, 0.0f);
-          const int ej = __shfl_sync(0xFFFFFFFFu, e, (j0 + j) & 31);
-          if (j0 + j < a.top_k && ej >= 0 && ej < a.experts && c < a.hidden) {
-            for (int i = 0; i < a.down_parts; ++i) {
-              const int64_t o = i * part + static_cast<int64_t>(token * a.top_k + j0 + j) * a.hidden + c;
-              if (!in_bounds(o, 2, a.down_parts * part, a.status)) continue;
-              const float2 v = __ldcg(reinterpret_cast<const float2 *>(a.z + o));
-              z[j].x += v.x;
-              z[j].y += v.y;
-            }
+        for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
+          if (i >= a.down_parts) break;
+          float2 v[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int slot = min(j0 + j, a.top_k - 1);
+            const int64_t o = i * part + static_cast<int64_t>(token * a.top_k + slot) * a.hidden +
+                              min(c, a.hidden - 2);
+            v[j] = in_bounds(o, 2, a.down_parts * part, a.status)
+                       ? __ldcg(reinterpret_cast<const float2 *>(a.z + o))
+                       : make_float2(0.0f, 0.0f);
           }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) z[j].x += v[j].x, z[j].y += v[j].y;
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -653,19 +665,18 @@ struct Expert {
   }
   // All workers: what they wrote is counted once for the CTA.
   __device__ __forceinline__ void add_count(int i) const {
-    asm volatile("fence.proxy.async;" ::: "memory");  // digits are read by bulk copies
-    __threadfence();
     named_barrier_sync(1, kWorkers * 32);
-    if (threadIdx.x == 64)
+    if (threadIdx.x == 64) {
+      __threadfence();  // (cumulative: over what the barrier ordered before it)
       asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.a.counts + i) : "memory");
+    }
   }
   // All workers: every CTA's count i has come (false: given up).
   __device__ __forceinline__ bool all_counted(int i, volatile uint32_t *flag) const {
     if (threadIdx.x == 64) *flag = count_reached(i) ? 1u : 0u;
     named_barrier_sync(1, kWorkers * 32);
     const bool ok = *flag != 0u;
-    __threadfence();
-    named_barrier_sync(1, kWorkers * 32);
+    named_barrier_sync(1, kWorkers * 32);  // before the flag is written again
     return ok;
   }
 };
@@ -688,6 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   x.abort = tmem_slot + 1;
   volatile uint32_t *flag = tmem_slot + 2;
+  x.tops = reinterpret_cast<float *>(tmem_slot + 4);
   x.pairs = a.tokens * a.top_k;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.slots; ++s) {
@@ -729,9 +741,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     ok = ok && x.template copies<true>(up, &gate_map, &up_map, p.x, true, [] { return true; });
     // the digits of h are there when every CTA has counted them
     ok = ok && x.template copies<false>(down, &down_map, &down_map, p.h, false, [&] {
-      const bool r = x.count_reached(1);
+      bool r = true;
+      if ((threadIdx.x & 31) == 0) r = x.count_reached(1);
+      r = __all_sync(0xFFFFFFFFu, r) != 0;
       asm volatile("fence.proxy.async;" ::: "memory");
-      return __all_sync(0xFFFFFFFFu, r) != 0;
+      return r;
     });
     // No copy may land after the CTA has left.  (After an abort a stage may lack
     // its images: that wait runs out, with no copy left behind it.)
@@ -749,6 +763,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (worker < 4) x.template epilogue<true>(up, p.x.factors);
     x.add_count(0);
     if (x.all_counted(0, flag)) x.split_h(worker);
+    asm volatile("fence.proxy.async;" ::: "memory");  // the digits are read by bulk copies
     x.add_count(1);
     if (FMT == 1) x.all_counted(1, flag);  // the epilogue reads the factors
     if (worker < 4) x.template epilogue<false>(down, p.h.factors);
@@ -803,7 +818,7 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   p.sfa_off = p.b_off + p.slots * X::kGroup * kImageCodes;
   p.sfb_off = p.sfa_off + p.slots * 2 * X::kSfa;
   p.bar_off = p.sfb_off + p.slots * X::kSfb;
-  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + 15) / 16 * 16;
+  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + kWorkers * 4 + 15) / 16 * 16;
   const int smem = p.groups_at + Groups::bytes(pairs);
   if (smem > kSmem) return cudaErrorInvalidValue;
   CUtensorMap gate, up, down;
