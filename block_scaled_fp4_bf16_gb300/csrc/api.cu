@@ -1077,9 +1077,8 @@ int experts_check(const char *fn, const void *x, int64_t tokens, int64_t ld_x, c
   a->image = reinterpret_cast<uint8_t *>(a->z) + moe_z_bytes(pairs, moe->hidden);
   a->factors = reinterpret_cast<float *>(
       a->image + moe_images_bytes(tokens, moe->hidden, moe->inter, top_k));
-  a->plan = reinterpret_cast<char *>(a->factors) +
-            round256(static_cast<size_t>(2 * pairs) * sizeof(float));
-  a->counts = reinterpret_cast<uint32_t *>(a->plan + round256(mx::moe_plan_bytes(pairs)));
+  a->counts = reinterpret_cast<uint32_t *>(
+      reinterpret_cast<char *>(a->factors) + round256(static_cast<size_t>(2 * pairs) * sizeof(float)));
   Range in[12];
   in[0] = span(x, row_bytes(tokens, moe->hidden, ld_x, 2));
   in[1] = span(ids, static_cast<uint64_t>(pairs) * 4);
@@ -1176,7 +1175,7 @@ MX_API int mx_moe_route_bf16(const void *x, int64_t tokens, int64_t hidden, int6
   if (tokens == 0) return MX_OK;
   const mx::RouteArgs a{x,     ld_x,  static_cast<int>(tokens), static_cast<int>(hidden),
                         static_cast<int>(experts), top_k, normalize, router, bias, ids, weights,
-                        dev->status};
+                        nullptr, dev->status};
   return launch_rc(fn, mx::launch_moe_route(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -1188,7 +1187,7 @@ MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t int
   return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) +
          moe_images_bytes(tokens, hidden, inter, top_k) +
          round256(static_cast<size_t>(2 * pairs) * sizeof(float)) +
-         round256(mx::moe_plan_bytes(pairs)) + round256(mx::kMoeCounts * sizeof(uint32_t));
+         round256(mx::kMoeCounts * sizeof(uint32_t));
 }
 
 MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
@@ -1206,7 +1205,9 @@ MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, cons
   if (rc != MX_OK) return rc;
   if (tokens == 0) return MX_OK;
   moe_device(&a, dev);
-  return launch_rc(fn, mx::launch_moe_experts(a, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = mx::launch_moe_clear(a, s);
+  return launch_rc(fn, e != cudaSuccess ? e : mx::launch_moe_experts(a, s));
 }
 
 MX_API int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const void *router,
@@ -1246,8 +1247,8 @@ MX_API int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const 
   if (rc != MX_OK) return rc;
   if (tokens == 0) return MX_OK;
   moe_device(&a, dev);
-  const mx::RouteArgs r{x,      ld_x,        a.tokens, a.hidden, a.experts, top_k, normalize,
-                        router, router_bias, ids,      weights,  dev->status};
+  const mx::RouteArgs r{x,      ld_x,        a.tokens, a.hidden, a.experts, top_k,     normalize,
+                        router, router_bias, ids,      weights,  a.counts,  dev->status};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   const cudaError_t e = mx::launch_moe_route(r, s);
   return launch_rc(fn, e != cudaSuccess ? e : mx::launch_moe_experts(a, s));

@@ -20,6 +20,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const int t = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  if (a.counts != nullptr && t == 0 && threadIdx.x < kMoeCounts) a.counts[threadIdx.x] = 0;
   for (int e = warp; e < a.experts; e += kWarps) {
     float acc = 0.0f;
     for (int k = lane; k < a.hidden; k += 32)

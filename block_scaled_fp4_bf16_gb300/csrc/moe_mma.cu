@@ -13,17 +13,16 @@
 // rate makes the eightfold product cheaper than converting the weights: M = 128,
 // N = 32 (four tokens), K = 64 a step.
 //
-// Two launches:
-//   split_kernel    groups the (token, slot) pairs by expert and writes the digits of
-//                   x (an "image": for a row and 256 elements of K the eight rows
-//                   of 128 bytes as the product reads them, 128-byte swizzle
-//                   included, and their scales).  The images' rows are the pairs
-//                   sorted by expert, so a group's lie together.
-//   expert_kernel   one CTA per SM, launched together: the sums of the gate and up
-//                   rows; the digits of h = act(gate) up; the sums of the down rows;
-//                   y.  A grid-wide count separates these, and the copies of the
-//                   down weights run ahead of it: what a kernel boundary would have
-//                   left idle streams weights.
+// One launch, one CTA per SM, resident together:
+//   - every CTA groups the (token, slot) pairs by expert;
+//   - the digits of x are written to the workspace (an "image": for a row and 256
+//     elements of K the eight rows of 128 bytes as the product reads them, 128-byte
+//     swizzle included, and their scales; its rows are the pairs sorted by expert, so
+//     a group's lie together);
+//   - the sums of the gate and up rows; the digits of h = act(gate) up; the sums of the
+//     down rows; y.
+// A grid-wide count separates these parts, and the copies of the next weights run
+// ahead of it: where a kernel boundary would leave the memory idle, weights stream.
 #include <cuda_fp16.h>
 
 #include "moe_groups.cuh"
@@ -49,8 +48,6 @@ struct Image {
   float *factors;       // NVFP4: [pairs], the power of two of a place
   int pairs;
 };
-
-constexpr int kSplitWarps = 8;
 
 // Largest e with |v| <= 6 * 2^e for |v| <= top, as small as it can be; top > 0.
 __device__ __forceinline__ int block_exponent(float top) {
@@ -170,78 +167,6 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
   }
 }
 
-struct SplitParams {
-  MoeArgs a;
-  Image image;
-  int stages, group;  // pairs of a group at most
-};
-
-// Eight consecutive elements of token r from `at` (zeros past the end).
-__device__ __forceinline__ void load_x(const MoeArgs &a, int r, int at, float (&v)[8]) {
-  uint4 q = make_uint4(0, 0, 0, 0);
-  const int64_t off = r * a.ld_x + at;
-  if (at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status))
-    q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off);
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
-// Token blockIdx.y, stages blockIdx.x * kSplitWarps ..: a warp makes the image of
-// one stage and writes it to the places of the token's pairs.  Every CTA makes
-// the groups; the first leaves them in the workspace and clears the counts.
-template <int FMT>
-__global__ void __launch_bounds__(kSplitWarps * 32) split_kernel(const SplitParams p) {
-  constexpr int kPairs = kMoeMaxTokens * kMoeMaxTopK;
-  __shared__ float tops[kSplitWarps];
-  __shared__ __align__(16) char groups[Groups::bytes(kPairs)];
-  __shared__ __align__(16) char scratch[2 * (kSplitWarps + 2) * kMoeMaxExperts];
-  __shared__ uint16_t places[kPairs], members[kPairs];
-  griddep_launch_dependents();
-  griddep_wait();
-  const MoeArgs &a = p.a;
-  const int r = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pairs = a.tokens * a.top_k, stage = blockIdx.x * kSplitWarps + warp;
-  float v[8];
-  load_x(a, r, stage * kImageK + lane * 8, v);
-  make_groups<kSplitWarps>(Groups::at(groups, pairs), places, members, scratch, a.ids, pairs,
-                           a.experts, p.group, a.status);
-  if (blockIdx.x == 0 && r == 0) {
-    uint16_t *plan_members = reinterpret_cast<uint16_t *>(a.plan + Groups::bytes(pairs));
-    for (int i = threadIdx.x; i < Groups::bytes(pairs) / 4; i += kSplitWarps * 32)
-      reinterpret_cast<uint32_t *>(a.plan)[i] = reinterpret_cast<const uint32_t *>(groups)[i];
-    for (int i = threadIdx.x; i < pairs; i += kSplitWarps * 32) plan_members[i] = members[i];
-    if (threadIdx.x < kMoeCounts) a.counts[threadIdx.x] = 0;
-  }
-  int row_e = 0;
-  if constexpr (FMT == 1) {
-    float top = 0.0f;
-    raise_finite(top, v);
-    for (int s = warp; s < p.stages; s += kSplitWarps) {
-      if (s == stage) continue;
-      float u[8];
-      load_x(a, r, s * kImageK + lane * 8, u);
-      raise_finite(top, u);
-    }
-    top = warp_max(top);
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSplitWarps; ++w) top = fmaxf(top, tops[w]);
-    row_e = row_exponent(top);
-    if (blockIdx.x == 0 && threadIdx.x < static_cast<unsigned>(a.top_k)) {
-      const int at = places[r * a.top_k + threadIdx.x];
-      if (at != 0xFFFF) p.image.factors[at] = pow2(row_e);
-    }
-  }
-  if (stage >= p.stages) return;
-  write_digits<FMT>(p.image, stage, v, row_e, a.top_k, [&](int j) { return places[r * a.top_k + j]; },
-                    [&](int at) { return members[at]; });
-}
-
 // ---------------------------------------------------------------- the product
 
 // Warps: copies, product, four of the epilogue (one tensor-memory lane quarter
@@ -252,6 +177,10 @@ constexpr int kThreads = (2 + kWorkers) * 32;
 constexpr int kMaxSlots = 16;
 constexpr int kSmem = 227 * 1024;
 constexpr int kTile = 128 * 128;  // bytes of a stage's weights, of one matrix
+// The grid-wide counts: CTAs that have written their part of the digits of x, the up
+// sums, the digits of h, the down sums.
+enum { kCountX, kCountUp, kCountH, kCountDown };
+static_assert(kCountDown < kMoeCounts, "counts");
 
 struct ExpertParams {
   MoeArgs a;
@@ -322,6 +251,7 @@ struct Expert {
   uint32_t tmem;
   float *tops;  // [kWorkers]
   Groups g;
+  uint16_t *places, *members;  // of the pairs, of the places
   int pairs;
   // the ring's place (copies or product) and the accumulator's (product or epilogue)
   uint32_t it = 0, s = 0, ph = 0, buf = 0, bph = 0;
@@ -363,13 +293,13 @@ struct Expert {
               im.codes + (at + g.begin[grp]) * kImageCodes, g.size[grp] * kImageCodes, fb);
     bulk_load(smem_u32(smem + p.sfb_off) + slot * kSfb, im.scales + (at + grp) * kSfb, kSfb, fb);
   }
-  // The copies of a product.  images: they can be read from the start; else ready()
-  // waits for them (whole warp), and until the ring is full weights run ahead.
+  // The copies of a product.  ready() waits for the images (whole warp); until then,
+  // and while the ring has room, weights run ahead.
   template <bool UP, typename Ready>
   __device__ __forceinline__ bool copies(const Product<UP> &d, const CUtensorMap *m0,
-                                         const CUtensorMap *m1, const Image &im, bool images,
-                                         const Ready &ready) {
+                                         const CUtensorMap *m1, const Image &im, const Ready &ready) {
     typename Product<UP>::Item cur{}, old{};
+    bool images = false;
     int late_item = d.begin, late_st = 0, late = 0;  // stages whose images are still to come
     uint32_t late_slot = s;
     const auto catch_up = [&]() {
@@ -524,61 +454,29 @@ struct Expert {
     }
   }
 
-  // ---- the digits of h.  A warp takes a row's stage; NVFP4, whose factor needs all
-  // of a row: the CTA's workers take a row.
-  __device__ __forceinline__ void load_h(int r, int at, float (&v)[8]) const {
-    const MoeArgs &a = p.a;
-    float u[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
-    if (at >= a.inter) return;
-    const int64_t part = static_cast<int64_t>(pairs) * a.inter;
-    const int64_t extent = 2 * a.up_parts * part;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
-      if (i >= a.up_parts) break;
-      const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
-      if (!in_bounds(off, 8, extent, a.status) || !in_bounds(off + part, 8, extent, a.status)) continue;
-      const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
-      const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
-      const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
-      v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
-      v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
-      u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
-      u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-      const float2 f = a.gelu ? gelu_f32x2(make_float2(v[i], v[i + 1]))
-                              : make_float2(v[i] / (1.0f + expf(-v[i])),
-                                            v[i + 1] / (1.0f + expf(-v[i + 1])));
-      v[i] = f.x * u[i];
-      v[i + 1] = f.y * u[i + 1];
-    }
-  }
-  __device__ __forceinline__ void split_h(int worker) {
-    const MoeArgs &a = p.a;
-    const int lane = threadIdx.x & 31, groups = *g.count;
-    if (groups == 0) return;
-    const int rows = g.begin[groups - 1] + g.size[groups - 1];
-    const int stages = (a.inter + kImageK - 1) / kImageK;
-    const uint16_t *members = reinterpret_cast<const uint16_t *>(a.plan + Groups::bytes(pairs));
+  // ---- digits.  A warp takes a row's stage; NVFP4, whose factor needs all of a row:
+  // the CTA's workers take a row.  load(row, at, v): eight elements; copies and
+  // place(row, j): the places that get the row.
+  template <typename Load, typename Place>
+  __device__ __forceinline__ void split(const Image &out, int rows, int stages, int copies,
+                                        const Load &load, const Place &place) {
+    const int worker = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
+    const auto member = [&](int at) { return static_cast<int>(members[at]); };
     if constexpr (FMT == 0) {
       for (int t = worker * gridDim.x + blockIdx.x; t < rows * stages; t += kWorkers * gridDim.x) {
         const int r = t / stages, st = t - r * stages;
         float v[8];
-        load_h(r, st * kImageK + lane * 8, v);
-        const int mem = members[r];
-        write_digits<FMT>(p.h, st, v, 0, 1, [&](int) { return r; }, [&](int) { return mem; });
+        load(r, st * kImageK + lane * 8, v);
+        write_digits<FMT>(out, st, v, 0, copies, [&](int j) { return place(r, j); }, member);
       }
     } else {
       for (int r = blockIdx.x; r < rows; r += gridDim.x) {
         float top = 0.0f, v[8];
-        load_h(r, worker * kImageK + lane * 8, v);
+        load(r, worker * kImageK + lane * 8, v);
         raise_finite(top, v);
         for (int st = worker + kWorkers; st < stages; st += kWorkers) {
           float u[8];
-          load_h(r, st * kImageK + lane * 8, u);
+          load(r, st * kImageK + lane * 8, u);
           raise_finite(top, u);
         }
         top = warp_max(top);
@@ -587,14 +485,70 @@ struct Expert {
 #pragma unroll
         for (int w = 0; w < kWorkers; ++w) top = fmaxf(top, tops[w]);
         named_barrier_sync(1, kWorkers * 32);
-        const int row_e = row_exponent(top), mem = members[r];
-        if (threadIdx.x == 64) p.h.factors[r] = pow2(row_e);
+        const int row_e = row_exponent(top);
+        if (worker == 0 && lane < copies && place(r, lane) != 0xFFFF)
+          out.factors[place(r, lane)] = pow2(row_e);
         for (int st = worker; st < stages; st += kWorkers) {
-          if (st != worker) load_h(r, st * kImageK + lane * 8, v);
-          write_digits<FMT>(p.h, st, v, row_e, 1, [&](int) { return r; }, [&](int) { return mem; });
+          if (st != worker) load(r, st * kImageK + lane * 8, v);
+          write_digits<FMT>(out, st, v, row_e, copies, [&](int j) { return place(r, j); }, member);
         }
       }
     }
+  }
+  __device__ __forceinline__ void split_x() {
+    const MoeArgs &a = p.a;
+    split(p.x, a.tokens, (a.hidden + kImageK - 1) / kImageK, a.top_k,
+          [&](int r, int at, float (&v)[8]) {
+            uint4 q = make_uint4(0, 0, 0, 0);
+            const int64_t off = r * a.ld_x + at;
+            if (at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status))
+              q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off);
+            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v[2 * i] = __uint_as_float(w[i] << 16);
+              v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            }
+          },
+          [&](int r, int j) { return static_cast<int>(places[r * a.top_k + j]); });
+  }
+  // h = act(gate) up, of the partial sums.
+  __device__ __forceinline__ void split_h() {
+    const MoeArgs &a = p.a;
+    const int groups = *g.count;
+    const int rows = groups == 0 ? 0 : g.begin[groups - 1] + g.size[groups - 1];
+    const int64_t part = static_cast<int64_t>(pairs) * a.inter;
+    split(p.h, rows, (a.inter + kImageK - 1) / kImageK, 1,
+          [&](int r, int at, float (&v)[8]) {
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
+            if (at >= a.inter) return;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
+              if (i >= a.up_parts) break;
+              const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
+              if (!in_bounds(off, 8, 2 * a.up_parts * part, a.status) ||
+                  !in_bounds(off + part, 8, 2 * a.up_parts * part, a.status))
+                continue;
+              const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
+              const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
+              const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
+              v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
+              v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
+              u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
+              u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float2 f = a.gelu ? gelu_f32x2(make_float2(v[i], v[i + 1]))
+                                      : make_float2(v[i] / (1.0f + expf(-v[i])),
+                                                    v[i + 1] / (1.0f + expf(-v[i + 1])));
+              v[i] = f.x * u[i];
+              v[i + 1] = f.y * u[i + 1];
+            }
+          },
+          [&](int r, int) { return r; });
   }
 
   // ---- y[t] = sum_j w_tj z[t, j], in the order of the slots; two columns a thread.
@@ -690,7 +644,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) char smem[];
   const MoeArgs &a = p.a;
   const int warp = threadIdx.x >> 5;
-  Expert<FMT, NB> x{p, smem};
+  using X = Expert<FMT, NB>;
+  X x{p, smem};
   x.full = reinterpret_cast<uint64_t *>(smem + p.bar_off);
   x.empty = x.full + p.slots;
   x.acc_full = x.empty + p.slots;   // [2]
@@ -700,6 +655,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   x.abort = tmem_slot + 1;
   volatile uint32_t *flag = tmem_slot + 2;
   x.tops = reinterpret_cast<float *>(tmem_slot + 4);
+  x.g = Groups::at(smem + p.groups_at, a.tokens * a.top_k);
+  x.places = reinterpret_cast<uint16_t *>(smem + p.groups_at + Groups::bytes(a.tokens * a.top_k));
+  x.members = x.places + a.tokens * a.top_k;
   x.pairs = a.tokens * a.top_k;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.slots; ++s) {
@@ -727,26 +685,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   griddep_launch_dependents();
   griddep_wait();
-  for (int i = threadIdx.x; i < Groups::bytes(x.pairs) / 16; i += kThreads)
-    reinterpret_cast<uint4 *>(smem + p.groups_at)[i] = reinterpret_cast<const uint4 *>(a.plan)[i];
+  // (the scratch lies in the ring: a fence and a barrier before the first copy)
+  make_groups<kThreads / 32>(x.g, x.places, x.members, smem, a.ids, x.pairs, a.experts, X::kGroup,
+                             a.status);
+  fence_proxy_async_smem();
   __syncthreads();
   tc_fence_after();
   x.tmem = *tmem_slot;
-  x.g = Groups::at(smem + p.groups_at, x.pairs);
   const Product<true> up(a, *x.g.count);
   const Product<false> down(a, *x.g.count);
 
   if (warp == 0) {
-    bool ok = !*x.abort;
-    ok = ok && x.template copies<true>(up, &gate_map, &up_map, p.x, true, [] { return true; });
-    // the digits of h are there when every CTA has counted them
-    ok = ok && x.template copies<false>(down, &down_map, &down_map, p.h, false, [&] {
+    // the digits are there when every CTA has counted them
+    const auto counted = [&](int i) {
       bool r = true;
-      if ((threadIdx.x & 31) == 0) r = x.count_reached(1);
+      if ((threadIdx.x & 31) == 0) r = x.count_reached(i);
       r = __all_sync(0xFFFFFFFFu, r) != 0;
       asm volatile("fence.proxy.async;" ::: "memory");
       return r;
-    });
+    };
+    if (!*x.abort &&
+        x.template copies<true>(up, &gate_map, &up_map, p.x, [&] { return counted(kCountX); }))
+      x.template copies<false>(down, &down_map, &down_map, p.h, [&] { return counted(kCountH); });
     // No copy may land after the CTA has left.  (After an abort a stage may lack
     // its images: that wait runs out, with no copy left behind it.)
     const uint32_t slots = static_cast<uint32_t>(p.slots);
@@ -759,16 +719,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_drain(smem_u32(done), 0u);
   } else {
-    const int worker = warp - 2;
-    if (worker < 4) x.template epilogue<true>(up, p.x.factors);
-    x.add_count(0);
-    if (x.all_counted(0, flag)) x.split_h(worker);
-    asm volatile("fence.proxy.async;" ::: "memory");  // the digits are read by bulk copies
-    x.add_count(1);
-    if (FMT == 1) x.all_counted(1, flag);  // the epilogue reads the factors
-    if (worker < 4) x.template epilogue<false>(down, p.h.factors);
-    x.add_count(2);
-    if (x.all_counted(2, flag)) x.combine(worker);
+    const bool epilogue = warp < 6;
+    x.split_x();
+    asm volatile("fence.proxy.async;" ::: "memory");  // digits are read by bulk copies
+    x.add_count(kCountX);
+    if (FMT == 1) x.all_counted(kCountX, flag);  // the epilogue reads the factors
+    if (epilogue) x.template epilogue<true>(up, p.x.factors);
+    x.add_count(kCountUp);
+    if (x.all_counted(kCountUp, flag)) x.split_h();
+    asm volatile("fence.proxy.async;" ::: "memory");
+    x.add_count(kCountH);
+    if (FMT == 1) x.all_counted(kCountH, flag);
+    if (epilogue) x.template epilogue<false>(down, p.h.factors);
+    x.add_count(kCountDown);
+    if (x.all_counted(kCountDown, flag)) x.combine(warp - 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -779,8 +743,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Pairs of a group: a product takes them together, in quarters of 32 columns.
-int group_size(const MoeArgs &a) { return a.tokens <= 4 ? 4 : a.tokens <= 8 ? 8 : 16; }
+// Clears the counts (mx_moe_layer_bf16's router does it there).
+__global__ void clear_kernel(uint32_t *counts) {
+  griddep_launch_dependents();
+  griddep_wait();
+  if (threadIdx.x < kMoeCounts) counts[threadIdx.x] = 0;
+}
 
 // The images in the workspace: codes of x, scales of x, codes of h, scales of h.
 Image image_of(const MoeArgs &a, bool of_h) {
@@ -808,7 +776,8 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   p.x = image_of(a, false);
   p.h = image_of(a, true);
   constexpr int per_slot = 2 * (kTile + X::kSfa) + X::kGroup * kImageCodes + X::kSfb;
-  int slots = (kSmem - 512 - Groups::bytes(pairs)) / per_slot;
+  const int groups = Groups::bytes(pairs) + 4 * pairs;
+  int slots = (kSmem - 512 - groups) / per_slot;
   slots = slots < kMaxSlots ? slots : kMaxSlots;
   p.bufs = 2 * X::kAccCols + 4 * X::kSfCols <= 512 ? 2 : 1;
   const int tmem_slots = (512 - p.bufs * X::kAccCols) / X::kSfCols;
@@ -819,8 +788,9 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   p.sfb_off = p.sfa_off + p.slots * 2 * X::kSfa;
   p.bar_off = p.sfb_off + p.slots * X::kSfb;
   p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + kWorkers * 4 + 15) / 16 * 16;
-  const int smem = p.groups_at + Groups::bytes(pairs);
-  if (smem > kSmem) return cudaErrorInvalidValue;
+  const int smem = p.groups_at + groups;
+  // the groups' scratch lies in the weights' part of the ring
+  if (smem > kSmem || p.b_off < 2 * (kThreads / 32 + 2) * a.experts) return cudaErrorInvalidValue;
   CUtensorMap gate, up, down;
   const int64_t inner = static_cast<int64_t>(a.experts) * a.inter;
   if (!encode_codes_window_map(&gate, a.gate.codes, inner, a.hidden, 128) ||
@@ -843,13 +813,9 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, kernel, gate, up, down, p);
 }
 
+// Pairs of a group by the tokens of a call: 4, 8 or 16.
 template <int FMT>
-cudaError_t launch_all(const MoeArgs &a, cudaStream_t s) {
-  SplitParams p{a, image_of(a, false), (a.hidden + kImageK - 1) / kImageK, group_size(a)};
-  const cudaError_t e =
-      launch_pdl(split_kernel<FMT>, dim3((p.stages + kSplitWarps - 1) / kSplitWarps, a.tokens),
-                 dim3(kSplitWarps * 32), 0, s, p);
-  if (e != cudaSuccess) return e;
+cudaError_t launch_fmt(const MoeArgs &a, cudaStream_t s) {
   if (a.tokens <= 4) return launch_expert_kernel<FMT, 1>(a, s);
   if (a.tokens <= 8) return launch_expert_kernel<FMT, 2>(a, s);
   return launch_expert_kernel<FMT, 4>(a, s);
@@ -875,12 +841,12 @@ int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_s
   return parts;
 }
 
-size_t moe_plan_bytes(int64_t pairs) {
-  return static_cast<size_t>(Groups::bytes(static_cast<int>(pairs))) + static_cast<size_t>(pairs) * 2;
+cudaError_t launch_moe_clear(const MoeArgs &a, cudaStream_t s) {
+  return launch_pdl(clear_kernel, dim3(1), dim3(32), 0, s, a.counts);
 }
 
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s) {
-  return a.fmt == 0 ? launch_all<0>(a, s) : launch_all<1>(a, s);
+  return a.fmt == 0 ? launch_fmt<0>(a, s) : launch_fmt<1>(a, s);
 }
 
 }  // namespace mx

@@ -226,6 +226,7 @@ struct RouteArgs {
   const float *bias;
   int32_t *ids;
   float *weights;
+  uint32_t *counts;  // the experts' counts, to be cleared (null: none)
   uint32_t *status;
 };
 cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s);
@@ -245,8 +246,7 @@ struct MoeArgs {
   float *z;            // [down_parts][tokens * top_k][hidden]
   uint8_t *image;      // digits of x, then of h (moe_image_bytes)
   float *factors;      // NVFP4: of the rows of x, then of h
-  char *plan;          // the pairs' groups (moe_plan_bytes)
-  uint32_t *counts;    // kMoeCounts grid-wide counts
+  uint32_t *counts;    // kMoeCounts grid-wide counts, cleared by the launch before
   int num_sms;
   uint32_t *status;
 };
@@ -256,8 +256,7 @@ constexpr int kMoeCounts = 4;
 // Ranges of K that a product is divided into, and the most for a number of pairs.
 int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms);
 constexpr int moe_max_parts(int64_t pairs) { return pairs <= 16 ? 4 : pairs <= 64 ? 2 : 1; }
-// Bytes of the groups of `pairs` pairs.
-size_t moe_plan_bytes(int64_t pairs);
+cudaError_t launch_moe_clear(const MoeArgs &a, cudaStream_t s);  // a.counts
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
 
 // Launch with programmatic stream serialization (the kernel itself orders

@@ -468,14 +468,16 @@ size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int
  * The hidden values act(G x) * U x are kept in binary32 and enter the second
  * product as FP16 times a power of two for each 128 (a rounding of 2^-12,
  * an eighth of the output's own).  y and the workspace must not overlap an
- * input or each other.  Launches two kernels and reads the chosen experts'
- * weights only. */
+ * input or each other.  Reads the chosen experts' weights only.  Launches a
+ * kernel of one warp and one of a CTA per SM, all resident together (a
+ * cooperative launch: it waits for SMs that other streams' kernels hold). */
 int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
                         const float *weights, int top_k, const mx_moe_weights *moe, void *y,
                         int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
 
 /* The whole layer: mx_moe_route_bf16 into ids and weights (outputs), then
- * mx_moe_experts_bf16 of that choice.  Launches three kernels. */
+ * mx_moe_experts_bf16 of that choice.  Launches two kernels, the second with
+ * all its CTAs resident together. */
 int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const void *router,
                       const float *router_bias, int top_k, int normalize,
                       const mx_moe_weights *moe, int32_t *ids, float *weights, void *y,
