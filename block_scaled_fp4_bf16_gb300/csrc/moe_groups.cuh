@@ -42,6 +42,41 @@ template <int W>
 __device__ __forceinline__ void make_groups(const Groups &g, uint16_t *place, uint16_t *member,
                                             char *scratch, const int32_t *ids, int pairs,
                                             int experts, int group, uint32_t *status) {
+  if (pairs <= 32) {
+    // One warp, a pair a lane: its place is the number of pairs before it in the order
+    // (expert, pair), its group the number of groups that begin before it.
+    if (threadIdx.x < 32) {
+      const int lane = threadIdx.x;
+      int e = lane < pairs && in_bounds(lane, 1, pairs, status) ? ids[lane] : -1;
+      if (e < 0 || e >= experts) e = -1;
+      const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
+      const int rank = __popc(same & ((1u << lane) - 1u));
+      const bool first = e >= 0 && rank % group == 0;
+      int at = 0, begins = 0;
+      for (int i = 0; i < pairs; ++i) {
+        const int o = __shfl_sync(0xFFFFFFFFu, e, i);
+        at += o >= 0 && (o < e || (o == e && i < lane)) ? 1 : 0;
+      }
+      for (int i = 0; i < pairs; ++i) {
+        const int o = __shfl_sync(0xFFFFFFFFu, first ? at : -1, i);
+        begins += o >= 0 && o <= at ? 1 : 0;
+      }
+      if (lane < pairs) place[lane] = static_cast<uint16_t>(e >= 0 ? at : 0xFFFF);
+      if (e >= 0) {
+        g.list[at] = static_cast<uint16_t>(lane);
+        member[at] = pack_member(begins - 1, rank % group);
+        if (first) {
+          g.expert[begins - 1] = static_cast<uint16_t>(e);
+          g.begin[begins - 1] = static_cast<uint16_t>(at);
+          g.size[begins - 1] = static_cast<uint16_t>(min(__popc(same) - rank, group));
+        }
+      }
+      const uint32_t starts = __ballot_sync(0xFFFFFFFFu, first);
+      if (lane == 0) *g.count = __popc(starts);
+    }
+    __syncthreads();
+    return;
+  }
   constexpr int kRuns = (kMoeMaxTokens * kMoeMaxTopK + 32 * W - 1) / (32 * W);  // of 32, a warp
   // [W][experts]: a warp's pairs of an expert, then the place of the first of
   // them; and an expert's first place and first group

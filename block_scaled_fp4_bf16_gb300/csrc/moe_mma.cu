@@ -114,6 +114,7 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
   const float f0 = pow2(min(-e, 100)), f1 = pow2(-e - min(-e, 100));
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = odd ? 0.0f : v[i] * f0 * f1;
+  uint32_t digits[kDigits];
 #pragma unroll
   for (int d = 0; d < kDigits; ++d) {
     uint32_t w = 0;
@@ -128,15 +129,7 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
       v[2 * i + 1] = (v[2 * i + 1] - q.y) * up;
       w |= c << (8 * i);
     }
-    if (FMT == 0 && digit_shift(d) > e + 127) w = 0;  // no scale that small
-    // row d of the 8 x 128 byte tile, 16-byte chunk lane / 4, swizzled
-    const int at = d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4;
-    for (int j = 0; j < copies; ++j) {
-      const int to = place(j);
-      if (to != 0xFFFF)
-        *reinterpret_cast<uint32_t *>(
-            out.codes + (static_cast<int64_t>(stage) * out.pairs + to) * kImageCodes + at) = w;
-    }
+    digits[d] = FMT == 0 && digit_shift(d) > e + 127 ? 0u : w;  // (no scale that small)
   }
   // scale words of four blocks, for each digit's row
   constexpr int kWords = FMT == 0 ? 2 : 4;
@@ -144,25 +137,32 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
 #pragma unroll
   for (int b = 0; b < 4 * kWords; ++b)
     words[b / 4] |= __shfl_sync(0xFFFFFFFFu, byte, b * (8 / kWords)) << (8 * (b % 4));
-  if (lane < kDigits) {
-    for (int j = 0; j < copies; ++j) {
-      const int to = place(j);
-      if (to == 0xFFFF) continue;
+  if constexpr (FMT == 0) {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) {
+      // 255 stays NaN; a digit whose scale would lie below 2^-127 is 0
+      const uint32_t nan = __vcmpeq4(words[i], 0xFFFFFFFFu);
+      words[i] = __vsubus4(words[i], ((lane & 7) == 0 ? 0u : 3u * (lane & 7) - 1u) * 0x01010101u) | nan;
+    }
+  }
+  // row d of the 8 x 128 byte tile, 16-byte chunk lane / 4, swizzled
+  uint32_t at[kDigits];
+#pragma unroll
+  for (int d = 0; d < kDigits; ++d) at[d] = d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4;
+  for (int j = 0; j < copies; ++j) {
+    const int to = place(j);
+    if (to == 0xFFFF) continue;
+    uint8_t *codes = out.codes + (static_cast<int64_t>(stage) * out.pairs + to) * kImageCodes;
+#pragma unroll
+    for (int d = 0; d < kDigits; ++d) *reinterpret_cast<uint32_t *>(codes + at[d]) = digits[d];
+    if (lane < kDigits) {
       // digit rows of a group in the order of a scale tile: row c at c % 32, word c / 32
       const int mem = member(to), m = mem % kMoeGroupMax;
       uint8_t *dst = out.scales +
                      (static_cast<int64_t>(stage) * out.pairs + mem / kMoeGroupMax) * kImageScales<FMT> +
                      ((m & 3) * kDigits + lane) * 16 + (m >> 2) * 4;
 #pragma unroll
-      for (int i = 0; i < kWords; ++i) {
-        uint32_t w = words[i];
-        if constexpr (FMT == 0) {
-          // 255 stays NaN; a digit whose scale would lie below 2^-127 is 0
-          const uint32_t nan = __vcmpeq4(w, 0xFFFFFFFFu);
-          w = __vsubus4(w, (lane == 0 ? 0u : 3u * lane - 1u) * 0x01010101u) | nan;
-        }
-        *reinterpret_cast<uint32_t *>(dst + i * 512) = w;
-      }
+      for (int i = 0; i < kWords; ++i) *reinterpret_cast<uint32_t *>(dst + i * 512) = words[i];
     }
   }
 }
