@@ -1,11 +1,24 @@
-// Mixture of experts for a few tokens: the router, and the two products of the
-// chosen experts.
-#include "few_tokens.cuh"
+// The router of a mixture-of-experts layer for a few tokens.
+//
+// logits = x R^T, the k largest of a token and their softmax weights.  The router's
+// weights (2 E H bytes) and a few dependent steps bound it, so the work is spread
+// and joined once: a thread-block cluster takes eight tokens, each of its 16 CTAs a
+// sixteenth of the experts; 16 warps divide K, each product is exact (BF16 times BF16
+// on the 16 x 8 x 16 product, the experts on its 16-row side) and every 32 elements
+// of K are added to binary32 sums; the logits go straight into the shared memory of
+// the CTA that owns the token, and one warp of it chooses.
+#include "mx_device.cuh"
+#include "mx_internal.h"
 
 namespace mx {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kCtas = 16;      // of a cluster
+constexpr int kWarps = 16;     // of a CTA
+constexpr int kTokens = 8;     // of a cluster
+constexpr int kMaxRows = kMoeMaxExperts / kCtas;   // experts of a CTA
+constexpr int kRowTiles = (kMaxRows + 15) / 16;
+constexpr int kLaneExperts = kMoeMaxExperts / 32;  // logits of a lane in the choice
 
 // Order of the logits as unsigned integers: NaN first, then descending.
 __device__ __forceinline__ uint32_t logit_key(float v) {
@@ -14,62 +27,148 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// One CTA per token: the logits by warps, the choice by the first warp.
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 load16(const void *base, int64_t elem, bool valid, int64_t extent,
+                                        uint32_t *status) {
+  if (!valid || !in_bounds(elem, 8, extent, status)) return make_uint4(0, 0, 0, 0);
+  return *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + elem);
+}
+
+// One warp: the choice of token t from its logits.
+__device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *logits) {
+  const int lane = threadIdx.x & 31;
+  float l[kLaneExperts];
+  uint32_t key[kLaneExperts];
+#pragma unroll
+  for (int i = 0; i < kLaneExperts; ++i) {
+    const int e = i * 32 + lane;
+    l[i] = e < a.experts ? logits[e] : -INFINITY;
+    key[i] = e < a.experts ? logit_key(l[i]) : 0u;
+  }
+  const uint32_t least = logit_key(-INFINITY);
+  int id = -1;              // lane j: the j-th choice
+  float chosen = 0.0f, top = 0.0f, sum = 0.0f;
+  for (int j = 0; j < a.top_k; ++j) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < kLaneExperts; ++i) {
+      if (i * 32 >= a.experts) break;
+      if (key[i] > best) best = key[i], at = i;  // (the lowest index of equal ones)
+    }
+    const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, best);
+    if (most <= least) break;  // nothing but -inf is left
+    const uint32_t e = __reduce_min_sync(
+        0xFFFFFFFFu, best == most ? static_cast<uint32_t>(at * 32 + lane) : 0xFFFFFFFFu);
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kLaneExperts; ++i) {
+      if (i * 32 >= a.experts) break;
+      if (static_cast<uint32_t>(i * 32 + lane) == e) key[i] = 0u, v = l[i];
+    }
+    v = __shfl_sync(0xFFFFFFFFu, v, e & 31u);
+    if (j == 0) top = v;
+    if (lane == j) id = static_cast<int>(e), chosen = v;
+  }
+  if (a.normalize) {
+    sum = id >= 0 ? expf(chosen - top) : 0.0f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kLaneExperts; ++i)
+      if (i * 32 + lane < a.experts) sum += expf(l[i] - top);
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+  if (lane < a.top_k) {
+    a.ids[t * a.top_k + lane] = id;
+    a.weights[t * a.top_k + lane] = id < 0 ? 0.0f : expf(chosen - top) / sum;
+  }
+}
+
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
-  __shared__ float logits[kMoeMaxExperts];
+  __shared__ float red[kWarps][kRowTiles][4][32];
+  __shared__ float logits[kMoeMaxExperts];  // of this CTA's token
   griddep_launch_dependents();
   griddep_wait();
-  const int t = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (a.counts != nullptr && t == 0 && threadIdx.x < kMoeCounts) a.counts[threadIdx.x] = 0;
-  for (int e = warp; e < a.experts; e += kWarps) {
-    float acc = 0.0f;
-    for (int k = lane; k < a.hidden; k += 32)
-      acc = __fmaf_rn(bf16_value(a.router, static_cast<int64_t>(e) * a.hidden + k),
-                      bf16_value(a.x, t * a.ld_x + k), acc);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int rank = static_cast<int>(cluster_ctarank()), t0 = static_cast<int>(cluster_id_x()) * kTokens;
+  if (a.counts != nullptr && blockIdx.x == 0 && threadIdx.x < kMoeCounts) a.counts[threadIdx.x] = 0;
+  const int rows = (a.experts + kCtas - 1) / kCtas, row0 = rank * rows;
+  const int n_rows = min(rows, a.experts - row0);  // may be 0 or less
+  const int blocks = a.hidden / 32;
+  const int64_t x_extent = (a.tokens - 1) * a.ld_x + a.hidden;
+  const int64_t r_extent = static_cast<int64_t>(a.experts) * a.hidden;
+  const int64_t x_row = (t0 + g) * a.ld_x + t * 8;
+  const bool x_in = t0 + g < a.tokens;
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(0xFFFFFFFFu, acc, m);
-    if (lane == 0) logits[e] = a.bias ? acc + a.bias[e] : acc;
+  for (int m = 0; m < kRowTiles; ++m) {
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (m * 16 < n_rows) {
+      const int r0 = m * 16 + g, r1 = r0 + 8;
+      const int64_t a_row0 = static_cast<int64_t>(row0 + r0) * a.hidden + t * 8;
+      const int64_t a_row1 = a_row0 + static_cast<int64_t>(8) * a.hidden;
+      // lane t holds elements 8 t .. 8 t + 7 of each 32 of K, of both operands
+#pragma unroll 4
+      for (int b = warp; b < blocks; b += kWarps) {
+        const uint4 p = load16(a.router, a_row0 + b * 32, r0 < n_rows, r_extent, a.status);
+        const uint4 q = load16(a.router, a_row1 + b * 32, r1 < n_rows, r_extent, a.status);
+        const uint4 x = load16(a.x, x_row + b * 32, x_in, x_extent, a.status);
+        float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        mma_bf16(d, p.x, q.x, p.y, q.y, x.x, x.y);
+        mma_bf16(d, p.z, q.z, p.w, q.w, x.z, x.w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] += d[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp][m][i][lane] = acc[i];
   }
   __syncthreads();
-  if (warp != 0) return;
-  float chosen[kMoeMaxTopK];
-  int ids[kMoeMaxTopK];
-  uint32_t taken = 0;  // bit i: this lane's i-th logit is taken
-  for (int j = 0; j < a.top_k; ++j) {
-    uint32_t best = 0, at = 0xFFFFFFFFu;
-    for (int e = lane, i = 0; e < a.experts; e += 32, ++i) {
-      const uint32_t key = logit_key(logits[e]);
-      if (!((taken >> i) & 1u) && key > best) best = key, at = e;
-    }
-    const uint32_t top = __reduce_max_sync(0xFFFFFFFFu, best);
-    const uint32_t id = __reduce_min_sync(0xFFFFFFFFu, best == top ? at : 0xFFFFFFFFu);
-    const bool none = top <= logit_key(-INFINITY);
-    ids[j] = none ? -1 : static_cast<int>(id);
-    chosen[j] = none ? -INFINITY : logits[id];
-    if (!none && (id & 31u) == lane) taken |= 1u << (id / 32);
-  }
-  float sum = 0.0f;
-  if (a.normalize) {
-    for (int j = 0; j < a.top_k; ++j) sum += ids[j] < 0 ? 0.0f : expf(chosen[j] - chosen[0]);
-  } else {
-    for (int e = lane; e < a.experts; e += 32) sum += expf(logits[e] - chosen[0]);
+  // the warps' sums, in their order, to the CTA of the token
+  for (int u = threadIdx.x; u < kRowTiles * 128; u += kWarps * 32) {
+    const int m = u >> 7, i = (u >> 5) & 3, l = u & 31;
+    const int row = m * 16 + (l >> 2) + (i >> 1) * 8, token = (l & 3) * 2 + (i & 1);
+    if (row >= n_rows) continue;
+    float s = red[0][m][i][l];
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, m);
+    for (int w = 1; w < kWarps; ++w) s += red[w][m][i][l];
+    if (a.bias != nullptr && in_bounds(row0 + row, 1, a.experts, a.status)) s += a.bias[row0 + row];
+    st_cluster_f32(mapa_shared(smem_u32(&logits[row0 + row]), static_cast<uint32_t>(token)), s);
   }
-  if (lane < a.top_k) {
-    int id = -1;
-    float l = 0.0f;
-    for (int j = 0; j < a.top_k; ++j)
-      if (j == lane) id = ids[j], l = chosen[j];
-    a.ids[t * a.top_k + lane] = id;
-    a.weights[t * a.top_k + lane] = id < 0 ? 0.0f : expf(l - chosen[0]) / sum;
-  }
+  cluster_sync();
+  if (rank < kTokens && t0 + rank < a.tokens && warp == 0) choose(a, t0 + rank, logits);
 }
 
 }  // namespace
 
 cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s) {
-  return launch_pdl(route_kernel, dim3(a.tokens), dim3(kWarps * 32), 0, s, a);
+  const void *func = reinterpret_cast<const void *>(route_kernel);
+  if (!kernel_setup_get(func, nullptr)) {
+    const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    kernel_setup_put(func, 0);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kCtas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(kCtas * ((a.tokens + kTokens - 1) / kTokens)));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, route_kernel, a);
 }
 
 }  // namespace mx

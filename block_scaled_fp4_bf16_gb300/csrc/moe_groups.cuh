@@ -43,35 +43,36 @@ __device__ __forceinline__ void make_groups(const Groups &g, uint16_t *place, ui
                                             char *scratch, const int32_t *ids, int pairs,
                                             int experts, int group, uint32_t *status) {
   if (pairs <= 32) {
-    // One warp, a pair a lane: its place is the number of pairs before it in the order
+    // A pair a lane: its place is the number of pairs before it in the order
     // (expert, pair), its group the number of groups that begin before it.
+    // (the comparisons of a pair are one vote, the pairs divided among the warps)
+    const int lane = threadIdx.x & 31;
+    int e = lane < pairs && in_bounds(lane, 1, pairs, status) ? ids[lane] : -1;
+    if (e < 0 || e >= experts) e = -1;
+    for (int i = threadIdx.x >> 5; i < pairs; i += W) {
+      const int o = __shfl_sync(0xFFFFFFFFu, e, i);
+      const uint32_t before =
+          __ballot_sync(0xFFFFFFFFu, e >= 0 && (e < o || (e == o && lane < i)));
+      if (lane == 0) place[i] = static_cast<uint16_t>(o >= 0 ? __popc(before) : 0xFFFF);
+    }
+    __syncthreads();
     if (threadIdx.x < 32) {
-      const int lane = threadIdx.x;
-      int e = lane < pairs && in_bounds(lane, 1, pairs, status) ? ids[lane] : -1;
-      if (e < 0 || e >= experts) e = -1;
+      const int at = lane < pairs ? place[lane] : 0xFFFF;
       const uint32_t same = __match_any_sync(0xFFFFFFFFu, e);
       const int rank = __popc(same & ((1u << lane) - 1u));
       const bool first = e >= 0 && rank % group == 0;
-      int at = 0, begins = 0;
-      for (int i = 0; i < pairs; ++i) {
-        const int o = __shfl_sync(0xFFFFFFFFu, e, i);
-        at += o >= 0 && (o < e || (o == e && i < lane)) ? 1 : 0;
-      }
-      for (int i = 0; i < pairs; ++i) {
-        const int o = __shfl_sync(0xFFFFFFFFu, first ? at : -1, i);
-        begins += o >= 0 && o <= at ? 1 : 0;
-      }
-      if (lane < pairs) place[lane] = static_cast<uint16_t>(e >= 0 ? at : 0xFFFF);
+      // the groups in the order of their first places
+      const uint32_t starts = __reduce_or_sync(0xFFFFFFFFu, first ? 1u << at : 0u);
       if (e >= 0) {
+        const int index = __popc(starts & (0xFFFFFFFFu >> (31 - at))) - 1;
         g.list[at] = static_cast<uint16_t>(lane);
-        member[at] = pack_member(begins - 1, rank % group);
+        member[at] = pack_member(index, rank % group);
         if (first) {
-          g.expert[begins - 1] = static_cast<uint16_t>(e);
-          g.begin[begins - 1] = static_cast<uint16_t>(at);
-          g.size[begins - 1] = static_cast<uint16_t>(min(__popc(same) - rank, group));
+          g.expert[index] = static_cast<uint16_t>(e);
+          g.begin[index] = static_cast<uint16_t>(at);
+          g.size[index] = static_cast<uint16_t>(min(__popc(same) - rank, group));
         }
       }
-      const uint32_t starts = __ballot_sync(0xFFFFFFFFu, first);
       if (lane == 0) *g.count = __popc(starts);
     }
     __syncthreads();

@@ -454,20 +454,28 @@ struct Expert {
     }
   }
 
-  // ---- digits.  A warp takes a row's stage; NVFP4, whose factor needs all of a row:
-  // the CTA's workers take a row.  load(row, at, v): eight elements; copies and
-  // place(row, j): the places that get the row.
-  template <typename Load, typename Place>
+  // ---- digits.  A warp takes a row's stage.  NVFP4's factor needs all of a row: the
+  // warp looks through it first (x: top(row) is the largest finite magnitude), or,
+  // where that is costly (h: BY_ROW), the CTA's workers take a row together.
+  // load(row, at, v): eight elements; copies and place(row, j): the places that get
+  // the row.
+  template <bool BY_ROW, typename Load, typename Top, typename Place>
   __device__ __forceinline__ void split(const Image &out, int rows, int stages, int copies,
-                                        const Load &load, const Place &place) {
+                                        const Load &load, const Top &row_top, const Place &place) {
     const int worker = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
     const auto member = [&](int at) { return static_cast<int>(members[at]); };
-    if constexpr (FMT == 0) {
+    if constexpr (FMT == 0 || !BY_ROW) {
       for (int t = worker * gridDim.x + blockIdx.x; t < rows * stages; t += kWorkers * gridDim.x) {
         const int r = t / stages, st = t - r * stages;
         float v[8];
         load(r, st * kImageK + lane * 8, v);
-        write_digits<FMT>(out, st, v, 0, copies, [&](int j) { return place(r, j); }, member);
+        int row_e = 0;
+        if constexpr (FMT == 1) {
+          row_e = row_exponent(row_top(r));
+          if (st == 0 && lane < copies && place(r, lane) != 0xFFFF)
+            out.factors[place(r, lane)] = pow2(row_e);
+        }
+        write_digits<FMT>(out, st, v, row_e, copies, [&](int j) { return place(r, j); }, member);
       }
     } else {
       for (int r = blockIdx.x; r < rows; r += gridDim.x) {
@@ -497,20 +505,46 @@ struct Expert {
   }
   __device__ __forceinline__ void split_x() {
     const MoeArgs &a = p.a;
-    split(p.x, a.tokens, (a.hidden + kImageK - 1) / kImageK, a.top_k,
-          [&](int r, int at, float (&v)[8]) {
-            uint4 q = make_uint4(0, 0, 0, 0);
-            const int64_t off = r * a.ld_x + at;
-            if (at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status))
-              q = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off);
-            const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+    const int lane = threadIdx.x & 31;
+    const auto load = [&](int r, int at) {
+      const int64_t off = r * a.ld_x + at;
+      return at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status)
+                 ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off)
+                 : make_uint4(0, 0, 0, 0);
+    };
+    split<false>(
+        p.x, a.tokens, (a.hidden + kImageK - 1) / kImageK, a.top_k,
+        [&](int r, int at, float (&v)[8]) {
+          const uint4 q = load(r, at);
+          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              v[2 * i] = __uint_as_float(w[i] << 16);
-              v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+          }
+        },
+        [&](int r) {
+          // eight loads in flight; magnitudes compare as integers, a magnitude of
+          // 0x7F80 or more is no number and counts as 0
+          uint32_t top = 0;
+          for (int at = 0; at < a.hidden; at += 8 * kImageK) {
+            uint4 q[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) q[i] = load(r, at + i * kImageK + lane * 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t m = w[j] & 0x7FFF7FFFu;
+                top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7F807F80u));
+              }
             }
-          },
-          [&](int r, int j) { return static_cast<int>(places[r * a.top_k + j]); });
+          }
+          top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+          return __uint_as_float(top << 16);
+        },
+        [&](int r, int j) { return static_cast<int>(places[r * a.top_k + j]); });
   }
   // h = act(gate) up, of the partial sums.
   __device__ __forceinline__ void split_h() {
@@ -518,7 +552,7 @@ struct Expert {
     const int groups = *g.count;
     const int rows = groups == 0 ? 0 : g.begin[groups - 1] + g.size[groups - 1];
     const int64_t part = static_cast<int64_t>(pairs) * a.inter;
-    split(p.h, rows, (a.inter + kImageK - 1) / kImageK, 1,
+    split<true>(p.h, rows, (a.inter + kImageK - 1) / kImageK, 1,
           [&](int r, int at, float (&v)[8]) {
             float u[8];
 #pragma unroll
@@ -548,7 +582,7 @@ struct Expert {
               v[i + 1] = f.y * u[i + 1];
             }
           },
-          [&](int r, int) { return r; });
+          [](int) { return 0.0f; }, [&](int r, int) { return r; });
   }
 
   // ---- y[t] = sum_j w_tj z[t, j], in the order of the slots; two columns a thread.
@@ -701,7 +735,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool r = true;
       if ((threadIdx.x & 31) == 0) r = x.count_reached(i);
       r = __all_sync(0xFFFFFFFFu, r) != 0;
-      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("fence.proxy.async;" ::: "memory");  // bulk copies read what was counted
       return r;
     };
     if (!*x.abort &&
@@ -721,13 +755,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     const bool epilogue = warp < 6;
     x.split_x();
-    asm volatile("fence.proxy.async;" ::: "memory");  // digits are read by bulk copies
     x.add_count(kCountX);
     if (FMT == 1) x.all_counted(kCountX, flag);  // the epilogue reads the factors
     if (epilogue) x.template epilogue<true>(up, p.x.factors);
     x.add_count(kCountUp);
     if (x.all_counted(kCountUp, flag)) x.split_h();
-    asm volatile("fence.proxy.async;" ::: "memory");
     x.add_count(kCountH);
     if (FMT == 1) x.all_counted(kCountH, flag);
     if (epilogue) x.template epilogue<false>(down, p.h.factors);
