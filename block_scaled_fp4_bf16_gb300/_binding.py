@@ -92,6 +92,8 @@ class MXError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libmxfp4.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -186,10 +188,28 @@ def _nbytes(x) -> int:
     return x.numel() * x.element_size()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """torch's current stream as an integer: the direct query where this torch has
+    it (0.2 us), else the public one, which makes a Stream object (1.5 us)."""
+    global _current_stream
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is not None and device is not None:
+        torch.cuda.current_stream()  # initialises CUDA
+        _current_stream = lambda: raw(device())  # noqa: E731
+    else:
+        _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -1335,18 +1335,6 @@ std::mutex g_setup_mutex;
 std::vector<SetupRecord> g_setup;  // one per kernel instance and context: a few dozen
 }  // namespace
 
-bool encode_few_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k, int box_rows) {
-  EncodeTiledFn fn = encode_fn();
-  if (fn == nullptr) return false;
-  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(k / 2), static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(k / 2)};
-  const cuuint32_t box[2] = {64u, static_cast<cuuint32_t>(box_rows)};
-  const cuuint32_t estr[2] = {1u, 1u};
-  return fn(tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 bool encode_codes_window_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k,
                              int box_rows) {
   return encode_codes_map(tm, codes, rows, k, box_rows) == MX_OK;

@@ -1,17 +1,5 @@
-// The experts' products on the FP4 tensor cores, activations as sums of FP4.
-//
-// The weights' bytes bound these products, so no instruction should touch a
-// weight: codes and scales go from memory to the block-scaled FP4 product as
-// they lie.  For that the activations have to be FP4 too, without losing their
-// digits: a value is written as a sum of eight E2M1 digits,
-//     x = 2^e (q_0 + 2^-2 q_1 + 2^-5 q_2 + ... + 2^-20 q_7),   e for its block,
-// each digit the rounding of what the ones before it left (what is left after
-// q_0 is at most 1 of 6, after every other at most 1/2 of 4, so eight digits
-// reach 2^-21 of the block's scale: a BF16 value is exact unless its last bit
-// lies below that).  The digits of a token are eight rows of the product's
-// narrow operand, and the epilogue adds their eight sums in binary32.  The FP4
-// rate makes the eightfold product cheaper than converting the weights: M = 128,
-// N = 32 (four tokens), K = 64 a step.
+// The experts' products on the FP4 tensor cores, activations as sums of FP4
+// (fp4_digits.cuh); M = 128 weight rows, N = the digits of a group's up to 16 pairs.
 //
 // One launch, one CTA per SM, resident together:
 //   - every CTA groups the (token, slot) pairs by expert;
@@ -23,149 +11,11 @@
 //     down rows; y.
 // A grid-wide count separates these parts, and the copies of the next weights run
 // ahead of it: where a kernel boundary would leave the memory idle, weights stream.
-#include <cuda_fp16.h>
-
+#include "fp4_digits.cuh"
 #include "moe_groups.cuh"
 
 namespace mx {
 namespace {
-
-constexpr int kDigits = 8;
-constexpr int kImageK = 256;                   // elements of K of a stage
-constexpr int kImageCodes = kDigits * 128;     // bytes of codes
-// Bytes of a group's scales: a scale tile of 128 rows (16 pairs' digits) and four
-// blocks, two (MXFP4) or four (NVFP4) of them a stage.
-template <int FMT>
-constexpr int kImageScales = (FMT == 0 ? 2 : 4) * 512;
-static_assert(kMoeGroupMax * kDigits == 128, "a group's digits fill a scale tile");
-// Weight of digit p: 2^-kShift[p].
-__host__ __device__ constexpr int digit_shift(int p) { return p == 0 ? 0 : 3 * p - 1; }
-
-// Where digits go.  Rows are places.
-struct Image {
-  uint8_t *codes;       // [stages][pairs][kImageCodes]
-  uint8_t *scales;      // [stages][groups][kImageScales]
-  float *factors;       // NVFP4: [pairs], the power of two of a place
-  int pairs;
-};
-
-// Largest e with |v| <= 6 * 2^e for |v| <= top, as small as it can be; top > 0.
-__device__ __forceinline__ int block_exponent(float top) {
-  const uint32_t u = __float_as_uint(top);
-  if (u < 0x00800000u) return -127;  // subnormal: 2^-126 at most
-  const int e = static_cast<int>(u >> 23) - 127;
-  return (u & 0x007FFFFFu) > 0x00400000u ? e - 1 : e - 2;
-}
-
-// 2^e for -149 <= e <= 127.
-__device__ __forceinline__ float pow2(int e) {
-  return e >= -126 ? __uint_as_float(static_cast<uint32_t>(e + 127) << 23)
-                   : __uint_as_float(1u << (e + 149));
-}
-
-// NVFP4: exponent of a row's factor, the largest finite magnitude being `top`: the
-// largest block's scale becomes 2^8, the largest power of two of E4M3.
-__device__ __forceinline__ int row_exponent(float top) { return max(block_exponent(top) - 8, -118); }
-
-__device__ __forceinline__ void raise_finite(float &top, const float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a = fabsf(v[i]);
-    if (a < __uint_as_float(0x7F800000u)) top = fmaxf(top, a);
-  }
-}
-
-__device__ __forceinline__ float warp_max(float v) {  // v >= 0
-  return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
-}
-
-// Whole warp.  The digits of 256 elements (eight a lane, v), written to `copies`
-// places of stage `stage`: place(j) (0xFFFF: none), member(place).  MXFP4: UE8M0
-// scales for 32 (four lanes), digit p with the scale 2^(e - shift p); NVFP4: E4M3
-// for 16 (two lanes), a power of two relative to 2^row_e, the digits' weights left
-// to the reader.  A block that holds an infinity or NaN gets the scale NaN.
-template <int FMT, typename Place, typename Member>
-__device__ __forceinline__ void write_digits(const Image &out, int stage, float (&v)[8], int row_e,
-                                             int copies, const Place &place, const Member &member) {
-  const int lane = threadIdx.x & 31;
-  float top = 0.0f;
-  uint32_t odd = 0;  // an infinity or NaN here
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top = fmaxf(top, fabsf(v[i]));
-    odd |= (__float_as_uint(v[i]) & 0x7F800000u) == 0x7F800000u;
-  }
-#pragma unroll
-  for (int m = 1; m < (FMT == 0 ? 4 : 2); m <<= 1) {
-    top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, m));
-    odd |= __shfl_xor_sync(0xFFFFFFFFu, odd, m);
-  }
-  int e = block_exponent(top);
-  uint32_t byte;
-  if constexpr (FMT == 0) {
-    e = max(e, -127);
-    byte = odd ? 255u : static_cast<uint32_t>(e + 127);
-  } else {
-    const int j = min(max(e - row_e, -9), 8);  // 2^-9 is E4M3's least
-    e = row_e + j;
-    byte = odd ? 0x7Fu : j >= -6 ? static_cast<uint32_t>(j + 7) << 3 : 1u << (j + 9);
-  }
-  // v 2^-e, in two steps where one power of two would not be a normal number
-  const float f0 = pow2(min(-e, 100)), f1 = pow2(-e - min(-e, 100));
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = odd ? 0.0f : v[i] * f0 * f1;
-  uint32_t digits[kDigits];
-#pragma unroll
-  for (int d = 0; d < kDigits; ++d) {
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t c = cvt_e2m1x2(v[2 * i], v[2 * i + 1]);
-      uint32_t h;
-      asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(c));
-      const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-      const float up = d == 0 ? 4.0f : 8.0f;
-      v[2 * i] = (v[2 * i] - q.x) * up;
-      v[2 * i + 1] = (v[2 * i + 1] - q.y) * up;
-      w |= c << (8 * i);
-    }
-    digits[d] = FMT == 0 && digit_shift(d) > e + 127 ? 0u : w;  // (no scale that small)
-  }
-  // scale words of four blocks, for each digit's row
-  constexpr int kWords = FMT == 0 ? 2 : 4;
-  uint32_t words[kWords] = {};
-#pragma unroll
-  for (int b = 0; b < 4 * kWords; ++b)
-    words[b / 4] |= __shfl_sync(0xFFFFFFFFu, byte, b * (8 / kWords)) << (8 * (b % 4));
-  if constexpr (FMT == 0) {
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) {
-      // 255 stays NaN; a digit whose scale would lie below 2^-127 is 0
-      const uint32_t nan = __vcmpeq4(words[i], 0xFFFFFFFFu);
-      words[i] = __vsubus4(words[i], ((lane & 7) == 0 ? 0u : 3u * (lane & 7) - 1u) * 0x01010101u) | nan;
-    }
-  }
-  // row d of the 8 x 128 byte tile, 16-byte chunk lane / 4, swizzled
-  uint32_t at[kDigits];
-#pragma unroll
-  for (int d = 0; d < kDigits; ++d) at[d] = d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4;
-  for (int j = 0; j < copies; ++j) {
-    const int to = place(j);
-    if (to == 0xFFFF) continue;
-    uint8_t *codes = out.codes + (static_cast<int64_t>(stage) * out.pairs + to) * kImageCodes;
-#pragma unroll
-    for (int d = 0; d < kDigits; ++d) *reinterpret_cast<uint32_t *>(codes + at[d]) = digits[d];
-    if (lane < kDigits) {
-      // digit rows of a group in the order of a scale tile: row c at c % 32, word c / 32
-      const int mem = member(to), m = mem % kMoeGroupMax;
-      uint8_t *dst = out.scales +
-                     (static_cast<int64_t>(stage) * out.pairs + mem / kMoeGroupMax) * kImageScales<FMT> +
-                     ((m & 3) * kDigits + lane) * 16 + (m >> 2) * 4;
-#pragma unroll
-      for (int i = 0; i < kWords; ++i) *reinterpret_cast<uint32_t *>(dst + i * 512) = words[i];
-    }
-  }
-}
 
 // ---------------------------------------------------------------- the product
 
@@ -634,39 +484,6 @@ struct Expert {
       y[1] = bf16_bits(y1);
     }
   }
-
-  // ---- the grid-wide counts.  The CTAs are resident together (a cooperative
-  // launch); a wait is bounded all the same.
-  __device__ __forceinline__ bool count_reached(int i) const {
-    const uint64_t t0 = globaltimer_ns();
-    while (true) {
-      uint32_t v;
-      asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(p.a.counts + i) : "memory");
-      if (v >= gridDim.x) return true;
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
-        *abort = 1u;
-        atomicOr(p.a.status, kStatusTimeout);
-        return false;
-      }
-    }
-  }
-  // All workers: what they wrote is counted once for the CTA.
-  __device__ __forceinline__ void add_count(int i) const {
-    named_barrier_sync(1, kWorkers * 32);
-    if (threadIdx.x == 64) {
-      __threadfence();  // (cumulative: over what the barrier ordered before it)
-      asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(p.a.counts + i) : "memory");
-    }
-  }
-  // All workers: every CTA's count i has come (false: given up).
-  __device__ __forceinline__ bool all_counted(int i, volatile uint32_t *flag) const {
-    if (threadIdx.x == 64) *flag = count_reached(i) ? 1u : 0u;
-    named_barrier_sync(1, kWorkers * 32);
-    const bool ok = *flag != 0u;
-    named_barrier_sync(1, kWorkers * 32);  // before the flag is written again
-    return ok;
-  }
 };
 
 template <int FMT, int NB>
@@ -733,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the digits are there when every CTA has counted them
     const auto counted = [&](int i) {
       bool r = true;
-      if ((threadIdx.x & 31) == 0) r = x.count_reached(i);
+      if ((threadIdx.x & 31) == 0) r = count_reached(a.counts + i, gridDim.x, x.abort, a.status);
       r = __all_sync(0xFFFFFFFFu, r) != 0;
       asm volatile("fence.proxy.async;" ::: "memory");  // bulk copies read what was counted
       return r;
@@ -753,18 +570,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     mbar_drain(smem_u32(done), 0u);
   } else {
-    const bool epilogue = warp < 6;
+    const bool epilogue = warp < 6, leader = threadIdx.x == 64;
+    const auto add = [&](int i) { add_count(a.counts + i, kWorkers * 32, leader); };
+    const auto wait = [&](int i) {
+      return all_counted(a.counts + i, kWorkers * 32, leader, flag, x.abort, a.status);
+    };
     x.split_x();
-    x.add_count(kCountX);
-    if (FMT == 1) x.all_counted(kCountX, flag);  // the epilogue reads the factors
+    add(kCountX);
+    if (FMT == 1) wait(kCountX);  // the epilogue reads the factors
     if (epilogue) x.template epilogue<true>(up, p.x.factors);
-    x.add_count(kCountUp);
-    if (x.all_counted(kCountUp, flag)) x.split_h();
-    x.add_count(kCountH);
-    if (FMT == 1) x.all_counted(kCountH, flag);
+    add(kCountUp);
+    if (wait(kCountUp)) x.split_h();
+    add(kCountH);
+    if (FMT == 1) wait(kCountH);
     if (epilogue) x.template epilogue<false>(down, p.h.factors);
-    x.add_count(kCountDown);
-    if (x.all_counted(kCountDown, flag)) x.combine(warp - 2);
+    add(kCountDown);
+    if (wait(kCountDown)) x.combine(warp - 2);
   }
   tc_fence_before();
   __syncthreads();
@@ -788,7 +609,7 @@ Image image_of(const MoeArgs &a, bool of_h) {
   uint8_t *at = a.image + (of_h ? moe_image_bytes(pairs, a.hidden) : 0);
   const int64_t stages = ((of_h ? a.inter : a.hidden) + kImageK - 1) / kImageK;
   return Image{at, at + pairs * stages * kImageCodes, a.factors + (of_h ? pairs : 0),
-               static_cast<int>(pairs)};
+               static_cast<int>(pairs), static_cast<int>(pairs)};
 }
 
 template <int FMT, int NB>

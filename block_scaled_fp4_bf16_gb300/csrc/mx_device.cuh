@@ -674,4 +674,19 @@ __device__ __forceinline__ uint16_t bf16_bits(float v) {
   return static_cast<uint16_t>(out & 0xFFFFu);
 }
 
+// Stores output (row, token) of mx_linear_bf16 after its epilogue; v: alpha times the
+// sum.  Each term is one binary32 operation, then one rounding to the output type.
+__device__ __forceinline__ void put_linear(const LinearArgs &a, int64_t row, int token, float v) {
+  const int64_t at = token * a.ld_y + row;
+  if (!in_bounds(at, 1, (a.tokens - 1) * a.ld_y + a.n, a.status)) return;
+  if (a.beta != 0.0f)
+    v = __fmaf_rn(a.beta, a.out_fp32 ? static_cast<const float *>(a.y)[at] : bf16_value(a.y, at), v);
+  if (a.bias != nullptr) v = __fadd_rn(v, a.bias[row]);
+  if (a.gelu) v = gelu_f32x2(make_float2(v, v)).x;
+  if (a.out_fp32)
+    static_cast<float *>(a.y)[at] = v;
+  else
+    static_cast<uint16_t *>(a.y)[at] = bf16_bits(v);
+}
+
 }  // namespace mx

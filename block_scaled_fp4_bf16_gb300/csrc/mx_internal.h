@@ -186,11 +186,9 @@ struct FewMatrix {
   const float *ts;  // NVFP4: one per matrix; MXFP4: null
 };
 
-// Tensor map of a stack of packed code matrices as [rows, k / 2] bytes: boxes of
-// 64 bytes (128 codes) x box_rows rows, 64-byte swizzle, zeros outside (api.cu).
-// false when it could not be encoded.
-bool encode_few_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k, int box_rows);
-// The same with boxes of 128 bytes (256 codes), 128-byte swizzle.
+// Tensor map of a stack of packed code matrices as [rows, k / 2] bytes: boxes of 128
+// bytes (256 codes) x box_rows rows, 128-byte swizzle, zeros outside (api.cu).  false
+// when it could not be encoded.
 bool encode_codes_window_map(CUtensorMap *tm, const void *codes, int64_t rows, int64_t k,
                              int box_rows);
 
