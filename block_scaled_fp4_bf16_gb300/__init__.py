@@ -19,7 +19,8 @@ from ._binding import (  # noqa: F401
     mx_quantize_bf16_2d, nvfp4_quantize_bf16_sr, MX_PHILOX_MAX_ROUNDS, nvfp4_quantize_bf16_2d,
     mx_gemm_epilogue, mxfp4_gemm_ex, nvfp4_gemm_ex, mx_calibrate_mma, MX_MMA_MXF4,
     MX_MMA_MXF4NVF4_2X, MX_MMA_MXF4NVF4_4X, MX_CALIBRATE_MAX_STEPS, MX_ERR_DEVICE_BOUNDS,
-    MX_BUILD_BOUNDS_CHECK, mx_build_flags, mx_fp4_transpose, mx_linear_bf16, MX_LINEAR_MAX_TOKENS,
+    MX_BUILD_BOUNDS_CHECK, mx_build_flags, mx_fp4_transpose, mx_linear_bf16, mx_linear_workspace_bytes,
+    MX_LINEAR_MAX_TOKENS,
     mx_moe_route_bf16, mx_moe_experts_bf16, mx_moe_layer_bf16, mx_moe_workspace_bytes,
     mx_moe_matrix, mx_moe_weights, moe_weights, MX_ACT_SILU, MX_ACT_GELU, MX_MOE_MAX_TOKENS,
     MX_MOE_MAX_EXPERTS, MX_MOE_MAX_TOP_K)

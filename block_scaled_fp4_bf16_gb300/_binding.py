@@ -9,6 +9,7 @@ on first use; if it is missing the call raises (there is no fallback path).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -152,6 +153,11 @@ def lib() -> ctypes.CDLL:
                                                   i32, vp]
         L.mx_linear_bf16.restype = i32
         L.mx_linear_bf16.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, i64, vp, i64, i32, ep, vp]
+        L.mx_linear_workspace_bytes.restype = sz
+        L.mx_linear_workspace_bytes.argtypes = [i64, i64, i64, i32]
+        L.mx_linear_bf16_workspace.restype = i32
+        L.mx_linear_bf16_workspace.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, i64, vp, i64,
+                                               i32, ep, vp, sz, vp]
         L.mx_moe_route_bf16.restype = i32
         L.mx_moe_route_bf16.argtypes = [vp, i64, i64, i64, vp, i64, vp, i32, i32, vp, vp, vp]
         L.mx_moe_workspace_bytes.restype = sz
@@ -374,9 +380,32 @@ def mxfp4_gemm_static_workspace(a_codes, a_scales, b_codes, b_scales, d, m, n, k
         out_dtype, split_k, _stream(stream)))
 
 
+@functools.lru_cache(maxsize=1024)
+def mx_linear_workspace_bytes(tokens: int, k: int, n: int, fmt: int) -> int:
+    return lib().mx_linear_workspace_bytes(tokens, k, n, fmt)
+
+
 def mx_linear_bf16(x, tokens, k, ld_x, fmt, w_codes, w_scales, w_tensor_scale, n, y, ld_y,
-                   out_dtype=MX_OUT_BF16, bias=None, beta=0.0, gelu=False, stream=None):
-    """y = act(x W^T + beta * y_in + bias) for a few BF16 rows and an FP4 weight."""
+                   out_dtype=MX_OUT_BF16, bias=None, beta=0.0, gelu=False, stream=None,
+                   workspace=None, workspace_bytes=None):
+    """y = act(x W^T + beta * y_in + bias) for a few BF16 rows and an FP4 weight.
+
+    With a workspace (mx_linear_workspace_bytes) it is mx_linear_bf16_workspace.  None:
+    on the current stream one is taken from torch's allocator, which keeps it in the
+    order of that stream and of a graph capture; with another stream, or with addresses
+    for tensors, the call does without."""
+    if workspace is None and stream is None and hasattr(x, "new_empty"):
+        need = mx_linear_workspace_bytes(tokens, k, n, fmt)
+        if need:
+            workspace = x.new_empty(need // x.element_size())
+            workspace_bytes = need
+    if workspace is not None:
+        if workspace_bytes is None:
+            workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
+        return _check("mx_linear_bf16_workspace", lib().mx_linear_bf16_workspace(
+            _ptr(x), tokens, k, ld_x, fmt, _ptr(w_codes), _ptr(w_scales), _ptr(w_tensor_scale), n,
+            _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _ptr(workspace),
+            workspace_bytes, _stream(stream)))
     return _check("mx_linear_bf16", lib().mx_linear_bf16(
         _ptr(x), tokens, k, ld_x, fmt, _ptr(w_codes), _ptr(w_scales), _ptr(w_tensor_scale), n,
         _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _stream(stream)))

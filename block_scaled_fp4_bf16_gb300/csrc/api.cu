@@ -1100,12 +1100,13 @@ void moe_device(mx::MoeArgs *a, const DeviceInfo *dev) {
 
 }  // namespace
 
-MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
-                          const void *w_codes, const void *w_scales, const float *w_tensor_scale,
-                          int64_t n, void *y, int64_t ld_y, int out_dtype,
-                          const mx_gemm_epilogue *epilogue, void *stream) {
-  clear_detail();
-  const char *fn = "mx_linear_bf16";
+namespace {
+
+// The arguments of a linear call; workspace_used: the bytes that the call writes there.
+int linear_check(const char *fn, const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
+                 const void *w_codes, const void *w_scales, const float *w_tensor_scale, int64_t n,
+                 void *y, int64_t ld_y, int out_dtype, const mx_gemm_epilogue *epilogue,
+                 const void *workspace, size_t workspace_used, mx::LinearArgs *out_args) {
   if (!valid_format(format))
     return fail(MX_ERR_INVALID_ARG, "%s: format %d (MX_FMT_MXFP4 = 0 or MX_FMT_NVFP4 = 1)", fn,
                 format);
@@ -1128,7 +1129,8 @@ MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x
     return fail(MX_ERR_INVALID_ARG, "%s: epilogue gelu = %d (0 or 1)", fn, epilogue->gelu);
   if (epilogue && epilogue->bias && !aligned16(epilogue->bias))
     return fail(MX_ERR_ALIGNMENT, "%s: bias is not 16-byte aligned", fn);
-  mx::LinearArgs a{};
+  mx::LinearArgs &a = *out_args;
+  a = mx::LinearArgs{};
   a.x = x;
   a.ld_x = ld_x;
   a.tokens = static_cast<int>(tokens);
@@ -1149,16 +1151,63 @@ MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x
   in[0] = span(x, row_bytes(tokens, k, ld_x, 2));
   in[1] = span(a.bias, static_cast<uint64_t>(n) * sizeof(float));
   matrix_ranges(a.w, format, 1, n, k, in + 2);
-  const Range out[1] = {span(y, row_bytes(tokens, n, ld_y, a.out_fp32 ? 4 : 2))};
-  rc = check_disjoint(fn, out, 1, in, 5);
-  if (rc != MX_OK) return rc;
+  const Range out[2] = {span(y, row_bytes(tokens, n, ld_y, a.out_fp32 ? 4 : 2)),
+                        span(workspace, workspace ? workspace_used : 0)};
+  return check_disjoint(fn, out, workspace ? 2 : 1, in, 5);
+}
+
+int linear_run(const char *fn, mx::LinearArgs *a, void *workspace, void *stream) {
   DeviceInfo *dev = nullptr;
-  rc = device_info(&dev);
+  const int rc = device_info(&dev);
   if (rc != MX_OK) return rc;
-  if (tokens == 0) return MX_OK;
-  a.num_sms = dev->num_sms;
-  a.status = dev->status;
-  return launch_rc(fn, mx::launch_linear(a, static_cast<cudaStream_t>(stream)));
+  if (a->tokens == 0) return MX_OK;
+  a->num_sms = dev->num_sms;
+  a->status = dev->status;
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  return launch_rc(fn, workspace ? mx::launch_linear_mma(*a, workspace, s) : mx::launch_linear(*a, s));
+}
+
+}  // namespace
+
+MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
+                          const void *w_codes, const void *w_scales, const float *w_tensor_scale,
+                          int64_t n, void *y, int64_t ld_y, int out_dtype,
+                          const mx_gemm_epilogue *epilogue, void *stream) {
+  clear_detail();
+  const char *fn = "mx_linear_bf16";
+  mx::LinearArgs a;
+  const int rc = linear_check(fn, x, tokens, k, ld_x, format, w_codes, w_scales, w_tensor_scale, n,
+                              y, ld_y, out_dtype, epilogue, nullptr, 0, &a);
+  return rc != MX_OK ? rc : linear_run(fn, &a, nullptr, stream);
+}
+
+MX_API size_t mx_linear_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int format) {
+  if (!valid_format(format) || tokens < 1 || tokens > MX_LINEAR_MAX_TOKENS || k <= 0 || k % 32 != 0 ||
+      n <= 0 || n % 32 != 0 || k >= (int64_t(1) << 31) || n >= (int64_t(1) << 31))
+    return 0;
+  const int fmt = format == MX_FMT_MXFP4 ? 0 : 1;
+  return mx::linear_mma_better(tokens, n, k) ? mx::linear_workspace_bytes(fmt, tokens, n, k) : 0;
+}
+
+MX_API int mx_linear_bf16_workspace(const void *x, int64_t tokens, int64_t k, int64_t ld_x,
+                                    int format, const void *w_codes, const void *w_scales,
+                                    const float *w_tensor_scale, int64_t n, void *y, int64_t ld_y,
+                                    int out_dtype, const mx_gemm_epilogue *epilogue,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+  clear_detail();
+  const char *fn = "mx_linear_bf16_workspace";
+  const size_t need = mx_linear_workspace_bytes(tokens, k, n, format);
+  if (need == 0) workspace = nullptr;
+  mx::LinearArgs a;
+  int rc = linear_check(fn, x, tokens, k, ld_x, format, w_codes, w_scales, w_tensor_scale, n, y,
+                        ld_y, out_dtype, epilogue, workspace, need, &a);
+  if (rc != MX_OK) return rc;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need))
+    return fail(MX_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes, got %zu%s", fn, need,
+                workspace ? workspace_bytes : size_t(0), workspace ? "" : " (null)");
+  if (!aligned16(workspace))
+    return fail(MX_ERR_ALIGNMENT, "%s: workspace is not 16-byte aligned", fn);
+  return linear_run(fn, &a, workspace, stream);
 }
 
 MX_API int mx_moe_route_bf16(const void *x, int64_t tokens, int64_t hidden, int64_t ld_x,

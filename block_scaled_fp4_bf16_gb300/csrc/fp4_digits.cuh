@@ -1,5 +1,5 @@
 // Activations as sums of FP4, for products of a few tokens on the FP4 tensor cores
-// (moe_mma.cu).
+// (moe_mma.cu, linear_mma.cu).
 //
 // The weights' bytes bound such products, so no instruction should touch a
 // weight: codes and scales go from memory to the block-scaled FP4 product as
@@ -73,10 +73,9 @@ __device__ __forceinline__ float warp_max(float v) {  // v >= 0
 
 // Whole warp.  The digits of 256 elements (eight a lane, v), written to `copies`
 // places of stage `stage`: place(j) (0xFFFF: none), member(place) (its scale tile *
-// kTileRows + its row there).  MXFP4: UE8M0
-// scales for 32 (four lanes), digit p with the scale 2^(e - shift p); NVFP4: E4M3
-// for 16 (two lanes), a power of two relative to 2^row_e, the digits' weights left
-// to the reader.  A block that holds an infinity or NaN gets the scale NaN.
+// kTileRows + its row there).  MXFP4: UE8M0 scales for 32 (four lanes), digit p with
+// the scale 2^(e - shift p); NVFP4: E4M3 for 16 (two lanes), a power of two relative
+// to 2^row_e, the digits' weights left to the reader.  A block that holds an infinity or NaN gets the scale NaN.
 template <int FMT, typename Place, typename Member>
 __device__ __forceinline__ void write_digits(const Image &out, int stage, float (&v)[8], int row_e,
                                              int copies, const Place &place, const Member &member) {

@@ -1,6 +1,8 @@
 // mx_linear_bf16: a few BF16 rows times an FP4 weight.
 //
-// y[t, n] = sum_k W[n, k] x[t, k] for up to 8 NT tokens.
+// y[t, n] = sum_k W[n, k] x[t, k] for up to 8 NT tokens.  Two kernels; the rule that
+// chooses (launch_linear) has both sides' times.  This one is for the smaller calls,
+// where a launch and one pass of dependent steps are what counts:
 //   - an item is R = 16 MT weight rows; the CTA's warps divide K, each walks its range
 //     in stages of 128 that come by cp.async into a ring of its own, over the end
 //     of one item into the next; the warps meet only to add their sums;
@@ -12,7 +14,7 @@
 //   - activations become FP16 times a power of two for each (token, 128): BF16
 //     values keep all their bits unless they lie 2^-31 below the largest of the 128.
 // It issues about 2.5 instructions a code, which bounds it at 4.2 TB/s of weights for
-// up to 8 tokens.
+// up to 8 tokens; linear_mma.cu leaves the weights to the tensor cores.
 #include <cuda_fp16.h>
 
 #include "mx_device.cuh"
@@ -390,8 +392,10 @@ cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
     kernel_setup_put(func, 0);
   }
   const LinearParams p{a, static_cast<int>((a.n + 16 * MT - 1) / (16 * MT))};
-  const size_t smem = W * MT * NT * 512 +
-                      static_cast<size_t>(W) * S * stage_bytes<FMT, MT>(a.tokens);
+  size_t smem = W * MT * NT * 512 + static_cast<size_t>(W) * S * stage_bytes<FMT, MT>(a.tokens);
+  // One CTA an SM: two on one, launched while the kernel before it still holds the
+  // others, share what one SM can do (1 x 4096 x 8192: 11.9 us, so 8.0).
+  if (smem <= kMaxSmem / 2) smem = kMaxSmem / 2 + 1024;
   const int grid = p.tiles < a.num_sms ? p.tiles : a.num_sms;
   return launch_pdl(kernel, dim3(grid), dim3(W * 32), smem, s, p);
 }
@@ -407,6 +411,19 @@ cudaError_t launch_fmt(const LinearArgs &a, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Which is the faster, by the number of weights (us, this kernel / linear_mma.cu's;
+// a token's digits cost the latter little, its two launches about 9 us):
+//                      4096 x 4096   8192 x 4096   8192 x 8192   28672 x 8192
+//   MXFP4   8 tokens:   4.9 / 11.2    8.7 / 13.0   15.1 / 15.1    31.9 / 25.2
+//          16 tokens:   6.6 / 13.3   12.0 / 14.9   21.3 / 16.6    45.1 / 26.3
+//          32 tokens:  12.2 / 17.7   23.2 / 18.0   43.5 / 20.8   126.1 / 33.0
+//   NVFP4   8 tokens:   5.2 / 11.5    9.4 / 13.3   16.5 / 15.3    36.1 / 26.5
+//          32 tokens:  11.9 / 18.7   22.6 / 18.9   42.1 / 22.1   122.0 / 35.2
+bool linear_mma_better(int64_t tokens, int64_t n, int64_t k) {
+  const int64_t least = tokens <= 8 ? 64 : tokens <= 16 ? 48 : 28;
+  return n * k >= least << 20;
+}
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s) {
   return a.fmt == 0 ? launch_fmt<0>(a, s) : launch_fmt<1>(a, s);

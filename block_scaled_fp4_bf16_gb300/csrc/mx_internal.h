@@ -211,6 +211,12 @@ struct LinearArgs {
   uint32_t *status;
 };
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s);
+// The two kernels for weights of many bytes (linear_mma.cu), their workspace, and
+// whether they are the faster (linear.cu).
+constexpr int kLinearCtas = 160;  // most CTAs of the product (one per SM)
+bool linear_mma_better(int64_t tokens, int64_t n, int64_t k);
+size_t linear_workspace_bytes(int fmt, int64_t tokens, int64_t n, int64_t k);
+cudaError_t launch_linear_mma(const LinearArgs &a, void *workspace, cudaStream_t s);
 
 constexpr int kMoeMaxTokens = 64;
 constexpr int kMoeMaxExperts = 512;

@@ -401,11 +401,29 @@ int nvfp4_gemm_ex(const void *a_codes, const void *a_scales, const void *b_codes
  *   epilogue: as for mxfp4_gemm_ex (NULL: none; beta * y_in reads y);
  *   tokens 0..MX_LINEAR_MAX_TOKENS (0 launches nothing), k % 32 == 0,
  *   n % 32 == 0.  y must not overlap an input (MX_ERR_INVALID_ARG).
- * Launches one kernel and needs no workspace. */
+ * Launches one kernel and needs no workspace; for weights of many bytes
+ * mx_linear_bf16_workspace is the faster call. */
 int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
                    const void *w_codes, const void *w_scales, const float *w_tensor_scale,
                    int64_t n, void *y, int64_t ld_y, int out_dtype,
                    const mx_gemm_epilogue *epilogue, void *stream);
+
+/* Workspace of mx_linear_bf16_workspace: 0 where one pass without it is the
+ * faster (small weights), and for sizes that the call refuses. */
+size_t mx_linear_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int format);
+
+/* The same product by the faster of two ways.  Where mx_linear_workspace_bytes
+ * is 0 it is mx_linear_bf16 (workspace ignored, may be NULL).  Else x is written
+ * to the workspace as sums of FP4 numbers, which the FP4 tensor cores multiply
+ * with the weights as they lie: two launches.
+ *   workspace: mx_linear_workspace_bytes(...) bytes, 16-byte aligned, its
+ *       contents arbitrary before and after; one call at a time may use it.
+ *       MX_ERR_WORKSPACE when it is missing or too small. */
+int mx_linear_bf16_workspace(const void *x, int64_t tokens, int64_t k, int64_t ld_x, int format,
+                             const void *w_codes, const void *w_scales,
+                             const float *w_tensor_scale, int64_t n, void *y, int64_t ld_y,
+                             int out_dtype, const mx_gemm_epilogue *epilogue, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /* ---- mixture of experts, a few tokens ----------------------------------- */
 #define MX_MOE_MAX_TOKENS 64

@@ -149,6 +149,30 @@ def test_experts_and_layer(lib):
     ])
 
 
+def test_linear_workspace(lib):
+    """A size that takes a workspace: its refusals, and those of the plain call."""
+    ok = dict(LINEAR, k=8192, ldx=8192, n=28672, ldy=28672, x=FAKE, c=FAKE + 256 * MB, s=FAKE + 512 * MB,
+              y=FAKE + 16 * MB, bias=FAKE + 32 * MB, ws=FAKE + 64 * MB, wsb=None)
+    need = mx.mx_linear_workspace_bytes(4, 8192, 28672, 0)
+    assert need > 0
+
+    def call(a):
+        ep = mx.mx_gemm_epilogue(a["bias"], a["beta"], a["gelu"])
+        return lib.mx_linear_bf16_workspace(
+            a["x"], a["t"], a["k"], a["ldx"], a["fmt"], a["c"], a["s"], a["ts"], a["n"], a["y"], a["ldy"],
+            a["out"], ctypes.byref(ep), a["ws"], need if a["wsb"] is None else a["wsb"], None)
+    codes_of(call, ok, [
+        (dict(ws=None), mx.MX_ERR_WORKSPACE), (dict(wsb=need - 1), mx.MX_ERR_WORKSPACE),
+        (dict(ws=FAKE + 64 * MB + 8), mx.MX_ERR_ALIGNMENT),
+        (dict(ws=FAKE + 256 * MB), mx.MX_ERR_INVALID_ARG),          # over the codes
+        (dict(ws=FAKE), mx.MX_ERR_INVALID_ARG),                     # over x
+        (dict(ws=FAKE + 16 * MB), mx.MX_ERR_INVALID_ARG),           # over y
+        (dict(x=None), mx.MX_ERR_INVALID_ARG), (dict(t=33), mx.MX_ERR_UNSUPPORTED_SHAPE),
+        (dict(k=8200), mx.MX_ERR_UNSUPPORTED_SHAPE), (dict(fmt=3), mx.MX_ERR_INVALID_ARG),
+        (dict(out=2), mx.MX_ERR_UNSUPPORTED_FEATURE),
+    ])
+
+
 def test_messages_name_the_call(lib):
     lib.mx_linear_bf16(None, 1, 32, 32, 0, None, None, None, 32, None, 32, 0, None, None)
     assert "mx_linear_bf16" in mx.mx_last_error_string() and "x is null" in mx.mx_last_error_string()
