@@ -1236,7 +1236,7 @@ MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t int
   return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) +
          moe_images_bytes(tokens, hidden, inter, top_k) +
          round256(static_cast<size_t>(2 * pairs) * sizeof(float)) +
-         round256(mx::kMoeCounts * sizeof(uint32_t));
+         round256(static_cast<size_t>(mx::moe_counts(static_cast<int>(pairs))) * sizeof(uint32_t));
 }
 
 MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,

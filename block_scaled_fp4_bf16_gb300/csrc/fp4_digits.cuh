@@ -71,14 +71,23 @@ __device__ __forceinline__ float warp_max(float v) {  // v >= 0
   return __uint_as_float(__reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v)));
 }
 
-// Whole warp.  The digits of 256 elements (eight a lane, v), written to `copies`
-// places of stage `stage`: place(j) (0xFFFF: none), member(place) (its scale tile *
-// kTileRows + its row there).  MXFP4: UE8M0 scales for 32 (four lanes), digit p with
-// the scale 2^(e - shift p); NVFP4: E4M3 for 16 (two lanes), a power of two relative
-// to 2^row_e, the digits' weights left to the reader.  A block that holds an infinity or NaN gets the scale NaN.
-template <int FMT, typename Place, typename Member>
-__device__ __forceinline__ void write_digits(const Image &out, int stage, float (&v)[8], int row_e,
-                                             int copies, const Place &place, const Member &member) {
+// Whole warp.  The digits of 256 elements (eight a lane), written to `copies` places
+// of an image's stage (`codes`, `scales`): places[j] (0xFFFF: none), or `place` where
+// places is null; members[place] (null: place) is its scale tile * kTileRows + its row
+// there.  MXFP4: UE8M0 scales for 32 (four lanes), digit p with the scale
+// 2^(e - shift p); NVFP4: E4M3 for 16 (two lanes), a power of two relative to 2^row_e,
+// the digits' weights left to the reader.  A block that holds an infinity or NaN gets
+// the scale NaN.
+//
+// Not inlined, and the digits a loop: instructions that run for the first time are
+// fetched behind the weights that stream meanwhile (unrolled, 8 KB of code: 4 us).
+// Kernels call it once with no copies before there is such a stream (warm_digits).
+template <int FMT>
+__device__ __noinline__ void write_digits(uint8_t *codes, uint8_t *scales, float v0, float v1,
+                                          float v2, float v3, float v4, float v5, float v6,
+                                          float v7, int row_e, int copies, const uint16_t *places,
+                                          int place, const uint16_t *members) {
+  float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
   const int lane = threadIdx.x & 31;
   float top = 0.0f;
   uint32_t odd = 0;  // an infinity or NaN here
@@ -106,9 +115,10 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
   const float f0 = pow2(min(-e, 100)), f1 = pow2(-e - min(-e, 100));
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = odd ? 0.0f : v[i] * f0 * f1;
-  uint32_t digits[kDigits];
-#pragma unroll
+  uint32_t digits[kDigits] = {};
+#pragma unroll 1
   for (int d = 0; d < kDigits; ++d) {
+    const float up = d == 0 ? 4.0f : 8.0f;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -116,12 +126,14 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
       uint32_t h;
       asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(c));
       const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-      const float up = d == 0 ? 4.0f : 8.0f;
       v[2 * i] = (v[2 * i] - q.x) * up;
       v[2 * i + 1] = (v[2 * i + 1] - q.y) * up;
       w |= c << (8 * i);
     }
-    digits[d] = FMT == 0 && digit_shift(d) > e + 127 ? 0u : w;  // (no scale that small)
+    if (FMT == 0 && digit_shift(d) > e + 127) w = 0;  // (no scale that small)
+#pragma unroll
+    for (int i = 0; i + 1 < kDigits; ++i) digits[i] = digits[i + 1];
+    digits[kDigits - 1] = w;
   }
   // scale words of four blocks, for each digit's row
   constexpr int kWords = FMT == 0 ? 2 : 4;
@@ -141,17 +153,17 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
   uint32_t at[kDigits];
 #pragma unroll
   for (int d = 0; d < kDigits; ++d) at[d] = d * 128 + (((lane >> 2) ^ d) << 4) + (lane & 3) * 4;
+#pragma unroll 1
   for (int j = 0; j < copies; ++j) {
-    const int to = place(j);
+    const int to = places != nullptr ? places[j] : place;
     if (to == 0xFFFF) continue;
-    uint8_t *codes = out.codes + (static_cast<int64_t>(stage) * out.rows + to) * kImageCodes;
+    uint8_t *c = codes + static_cast<int64_t>(to) * kImageCodes;
 #pragma unroll
-    for (int d = 0; d < kDigits; ++d) *reinterpret_cast<uint32_t *>(codes + at[d]) = digits[d];
+    for (int d = 0; d < kDigits; ++d) *reinterpret_cast<uint32_t *>(c + at[d]) = digits[d];
     if (lane < kDigits) {
       // digit rows of a group in the order of a scale tile: row c at c % 32, word c / 32
-      const int mem = member(to), m = mem % kTileRows;
-      uint8_t *dst = out.scales +
-                     (static_cast<int64_t>(stage) * out.tiles + mem / kTileRows) * kImageScales<FMT> +
+      const int mem = members != nullptr ? members[to] : to, m = mem % kTileRows;
+      uint8_t *dst = scales + (mem / kTileRows) * kImageScales<FMT> +
                      ((m & 3) * kDigits + lane) * 16 + (m >> 2) * 4;
 #pragma unroll
       for (int i = 0; i < kWords; ++i) *reinterpret_cast<uint32_t *>(dst + i * 512) = words[i];
@@ -159,18 +171,45 @@ __device__ __forceinline__ void write_digits(const Image &out, int stage, float 
   }
 }
 
+// The digits of v for `copies` places of stage `stage`.
+template <int FMT>
+__device__ __forceinline__ void write_digits(const Image &out, int stage, const float (&v)[8],
+                                             int row_e, int copies, const uint16_t *places,
+                                             int place, const uint16_t *members) {
+  write_digits<FMT>(out.codes + static_cast<int64_t>(stage) * out.rows * kImageCodes,
+                    out.scales + static_cast<int64_t>(stage) * out.tiles * kImageScales<FMT>, v[0],
+                    v[1], v[2], v[3], v[4], v[5], v[6], v[7], row_e, copies, places, place, members);
+}
+template <int FMT>
+__device__ __forceinline__ void warm_digits(const Image &out) {
+  const float v[8] = {};
+  write_digits<FMT>(out, 0, v, 0, 0, nullptr, 0, nullptr);
+}
+
 // ---------------------------------------------------------------- grid-wide counts
 // Kernels whose CTAs are resident together (a cooperative launch) count the CTAs
 // that have finished a part; a wait for the count is bounded all the same.
 
-// One thread.  False when the wait ran out (abort is raised then) or abort was up.
+__device__ __forceinline__ uint32_t load_acquire(const uint32_t *count) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
+  return v;
+}
+
+// Adds one after all that this thread has seen done (and what a barrier ordered before).
+__device__ __forceinline__ void release_add(uint32_t *count) {
+  __threadfence();
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
+}
+
+// One thread, or a whole warp together (a warp of which one lane waits comes out
+// diverged, and every shuffle after it then takes 330 clocks: measured, 4 us in
+// write_digits).  False when the wait ran out (abort is raised then) or abort was up.
 __device__ __forceinline__ bool count_reached(const uint32_t *count, uint32_t target,
                                               volatile uint32_t *abort, uint32_t *status) {
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    uint32_t v;
-    asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(v) : "l"(count) : "memory");
-    if (v >= target) return true;
+    if (load_acquire(count) >= target) return true;
     if (*abort) return false;
     if (globaltimer_ns() - t0 > kWaitTimeoutNs) {
       *abort = 1u;
@@ -184,21 +223,19 @@ __device__ __forceinline__ bool count_reached(const uint32_t *count, uint32_t ta
 // wrote is counted once.
 __device__ __forceinline__ void add_count(uint32_t *count, int threads, bool leader) {
   named_barrier_sync(1, threads);
-  if (leader) {
-    __threadfence();  // (cumulative: over what the barrier ordered before it)
-    asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(count) : "memory");
-  }
+  if (leader) release_add(count);
 }
 
-// The same threads: every CTA has counted (false: given up).
+// The same threads: every CTA has counted (false: given up).  The leader's warp looks.
 __device__ __forceinline__ bool all_counted(const uint32_t *count, int threads, bool leader,
                                             volatile uint32_t *flag, volatile uint32_t *abort,
                                             uint32_t *status) {
-  if (leader) *flag = count_reached(count, gridDim.x, abort, status) ? 1u : 0u;
+  if (__any_sync(0xFFFFFFFFu, leader)) {
+    const bool ok = __all_sync(0xFFFFFFFFu, count_reached(count, gridDim.x, abort, status));
+    if (leader) *flag = ok ? 1u : 0u;
+  }
   named_barrier_sync(1, threads);
-  const bool ok = *flag != 0u;
-  named_barrier_sync(1, threads);  // before the flag is written again
-  return ok;
+  return *flag != 0u;
 }
 
 }  // namespace mx

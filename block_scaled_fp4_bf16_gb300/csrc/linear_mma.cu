@@ -44,6 +44,7 @@ __global__ void __launch_bounds__(kDigitWarps<FMT> * 32) digits_kernel(const __g
   __shared__ uint32_t tops[kDigitWarps<FMT>];
   const LinearArgs &a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y;
+  warm_digits<FMT>(p.x);
   griddep_wait();
   // After the wait: what the product copies before its own wait is then older than this
   // kernel.
@@ -95,7 +96,7 @@ __global__ void __launch_bounds__(kDigitWarps<FMT> * 32) digits_kernel(const __g
     v[2 * i] = __uint_as_float(w[i] << 16);
     v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
   }
-  write_digits<FMT>(p.x, st, v, row_e, 1, [&](int) { return t; }, [](int at) { return at; });
+  write_digits<FMT>(p.x, st, v, row_e, 1, nullptr, t, nullptr);
 }
 
 // ---------------------------------------------------------------- the product
@@ -354,11 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool finish = whole;
       float v[kMine] = {};
       if (two) {
-        if (leader) {
-          uint32_t n;
-          asm volatile("ld.acquire.gpu.u32 %0, [%1];" : "=r"(n) : "l"(p.counts + tile) : "memory");
-          last[word] = n;
-        }
+        if (leader) last[word] = load_acquire(p.counts + tile);
         named_barrier_sync(1, kEpilogue * 32);
         finish = last[word] != 0;
         if (finish) {

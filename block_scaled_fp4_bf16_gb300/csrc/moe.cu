@@ -99,7 +99,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteArgs a) {
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank()), t0 = static_cast<int>(cluster_id_x()) * kTokens;
-  if (a.counts != nullptr && blockIdx.x == 0 && threadIdx.x < kMoeCounts) a.counts[threadIdx.x] = 0;
+  if (a.counts != nullptr && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < moe_counts(a.tokens * a.top_k); i += blockDim.x) a.counts[i] = 0;
   const int rows = (a.experts + kCtas - 1) / kCtas, row0 = rank * rows;
   const int n_rows = min(rows, a.experts - row0);  // may be 0 or less
   const int blocks = a.hidden / 32;

@@ -26,11 +26,11 @@ constexpr int kWorkers = 4 + kHelpers;
 constexpr int kThreads = (2 + kWorkers) * 32;
 constexpr int kMaxSlots = 16;
 constexpr int kSmem = 227 * 1024;
+enum { kKnown, kLook, kWait };
 constexpr int kTile = 128 * 128;  // bytes of a stage's weights, of one matrix
-// The grid-wide counts: CTAs that have written their part of the digits of x, the up
-// sums, the digits of h, the down sums.
-enum { kCountX, kCountUp, kCountH, kCountDown };
-static_assert(kCountDown < kMoeCounts, "counts");
+// The counts: CTAs that have written their part of the digits of x, of the down sums;
+// then, for each group, items of its up sums, and its digits of h (tasks of them).
+enum { kCountX, kCountDown, kCountGroups };
 
 struct ExpertParams {
   MoeArgs a;
@@ -43,11 +43,13 @@ struct ExpertParams {
 // One of the two products: UP: the gate and up rows, K = hidden, partial sums
 // [parts][2][pairs (by place)][inter]; else the down rows, K = inter, [parts][pairs]
 // [hidden].  An item is 128 rows (of each matrix) times a group's pairs over one
-// range of K; a CTA walks consecutive items, group-major.
+// range of K.  The items, group-major, go round the CTAs, the down items from where
+// the up items end: a group is done early, and its digits of h made, while the up
+// sums of the later ones run.
 template <bool UP>
 struct Product {
   static constexpr int kSegs = UP ? 2 : 1;
-  int rows, k, stages, tiles, parts, begin, end;
+  int rows, k, stages, tiles, parts, begin, end, step;
 
   struct Item {
     int grp, tile, part, st0, st1;
@@ -58,9 +60,10 @@ struct Product {
     stages = (k + kImageK - 1) / kImageK;
     tiles = (rows + 127) / 128;
     parts = UP ? a.up_parts : a.down_parts;
-    const int64_t items = static_cast<int64_t>(groups) * tiles * parts;
-    begin = static_cast<int>(items * blockIdx.x / gridDim.x);
-    end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+    end = groups * tiles * parts;
+    step = gridDim.x;
+    const int before = UP ? 0 : groups * ((a.inter + 127) / 128) * a.up_parts % step;
+    begin = (static_cast<int>(blockIdx.x) - before + step) % step;
   }
   __device__ __forceinline__ Item at(int item) const {
     Item i;
@@ -73,6 +76,12 @@ struct Product {
     return i;
   }
 };
+
+// Not inlined, and called once before weights stream: as write_digits.
+__device__ __noinline__ float2 act(float2 v, int gelu) {
+  return gelu ? gelu_f32x2(v)
+              : make_float2(v.x / (1.0f + expf(-v.x)), v.y / (1.0f + expf(-v.y)));
+}
 
 // A product reads its 128 weight rows from shared memory in about 100 clocks
 // however few columns it has (measured: tiles of 64 rows take as long), so tiles
@@ -99,7 +108,7 @@ struct Expert {
   uint64_t *full, *empty, *acc_full, *acc_empty;
   volatile uint32_t *abort;
   uint32_t tmem;
-  float *tops;  // [kWorkers]
+  float *tops;  // [kHelpers]
   Groups g;
   uint16_t *places, *members;  // of the pairs, of the places
   int pairs;
@@ -143,43 +152,47 @@ struct Expert {
               im.codes + (at + g.begin[grp]) * kImageCodes, g.size[grp] * kImageCodes, fb);
     bulk_load(smem_u32(smem + p.sfb_off) + slot * kSfb, im.scales + (at + grp) * kSfb, kSfb, fb);
   }
-  // The copies of a product.  ready() waits for the images (whole warp); until then,
-  // and while the ring has room, weights run ahead.
+  // The copies of a product.  ready(group, how): whether the group's images are there;
+  // kKnown: as far as that is known without a look, kLook, kWait (whole warp; < 0:
+  // given up).  Until they are, and while the ring has room, weights run ahead.
   template <bool UP, typename Ready>
   __device__ __forceinline__ bool copies(const Product<UP> &d, const CUtensorMap *m0,
                                          const CUtensorMap *m1, const Image &im, const Ready &ready) {
-    typename Product<UP>::Item cur{}, old{};
-    bool images = false;
-    int late_item = d.begin, late_st = 0, late = 0;  // stages whose images are still to come
+    if (d.begin >= d.end) return true;
+    typename Product<UP>::Item cur{}, old = d.at(d.begin);
+    int late_item = d.begin, late_st = old.st0, late = 0;  // stages whose images are still to come
     uint32_t late_slot = s;
-    const auto catch_up = [&]() {
-      if (!ready()) return false;
-      for (; late > 0; --late) {
-        if (elect_one()) copy_images(im, old.grp, late_st, late_slot);
-        __syncwarp();
-        if (++late_slot == static_cast<uint32_t>(p.slots)) late_slot = 0;
-        if (++late_st == old.st1 && ++late_item < d.end) old = d.at(late_item), late_st = old.st0;
+    const auto catch_up = [&](int how) {
+      while (late > 0) {
+        const int there = ready(old.grp, how);
+        if (there <= 0) return there == 0;
+        const int n = min(late, old.st1 - late_st);
+        for (int i = 0; i < n; ++i) {
+          if (elect_one()) copy_images(im, old.grp, late_st, late_slot);
+          __syncwarp();
+          if (++late_slot == static_cast<uint32_t>(p.slots)) late_slot = 0;
+          ++late_st;
+        }
+        late -= n;
+        if (late_st == old.st1 && (late_item += d.step) < d.end) old = d.at(late_item), late_st = old.st0;
       }
-      images = true;
       return true;
     };
-    for (int item = d.begin; item < d.end; ++item) {
+    for (int item = d.begin; item < d.end; item += d.step) {
       cur = d.at(item);
-      if (item == d.begin) old = cur, late_st = cur.st0;
+      if (item != d.begin && !catch_up(kLook)) return false;
       for (int st = cur.st0; st < cur.st1; ++st) {
         // (the slots of the first stages come free with the products before them)
-        if (!images && late == p.slots && !catch_up()) return false;
+        if (late == p.slots && !catch_up(kWait)) return false;
         if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, p.a.status)) return false;
-        if (elect_one()) {
-          copy_weights<UP>(d, m0, m1, cur, st);
-          if (images) copy_images(im, cur.grp, st, s);
-        }
+        if (elect_one()) copy_weights<UP>(d, m0, m1, cur, st);
         __syncwarp();
-        if (!images) ++late;
+        ++late;
         next_slot();
+        if (!catch_up(kKnown)) return false;
       }
     }
-    return late == 0 || catch_up();
+    return catch_up(kWait);
   }
 
   // ---- products.  One thread issues every one, so it has to cost few instructions:
@@ -191,7 +204,7 @@ struct Expert {
     const uint32_t sfa_ring = smem_u32(smem + p.sfa_off), sfb_ring = smem_u32(smem + p.sfb_off);
     const uint32_t sf_tmem = tmem + p.bufs * kAccCols;
     const int katoms = (d.k / (FMT == 0 ? 32 : 16) + 3) >> 2;
-    for (int item = d.begin; item < d.end; ++item) {
+    for (int item = d.begin; item < d.end; item += d.step) {
       const typename Product<UP>::Item im = d.at(item);
       // columns: the digits of the group, to a multiple of 16
       const uint32_t columns = static_cast<uint32_t>(g.size[im.grp] * kDigits + 15) & ~15u;
@@ -252,15 +265,17 @@ struct Expert {
     const MoeArgs &a = p.a;
     const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int64_t extent = static_cast<int64_t>(d.parts) * kSegs * pairs * d.rows;
-    for (int item = d.begin; item < d.end; ++item) {
+    bool ok = true;
+    for (int item = d.begin; item < d.end; item += d.step) {
       const typename Product<UP>::Item im = d.at(item);
       const int e = g.expert[im.grp], n = g.size[im.grp], row = im.tile * 128 + q * 32 + lane;
       const float alpha0 = FMT == 1 ? (UP ? a.gate.ts : a.down.ts)[e] : 1.0f;
       const float alpha1 = FMT == 1 && UP ? a.up.ts[e] : 1.0f;
-      if (!mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status)) return;
+      // (a warp that gives up still meets the others below; nothing is counted then)
+      ok = ok && mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status);
       tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
-      for (int i = 0; i < (n + 3) / 4; ++i) {
+      for (int i = 0; ok && i < (n + 3) / 4; ++i) {
         float sum[kSegs][4];
 #pragma unroll
         for (int m = 0; m < kSegs; ++m) {
@@ -301,138 +316,178 @@ struct Expert {
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&acc_empty[buf]));
       next_buf();
+      if constexpr (UP) {
+        named_barrier_sync(2, 128);
+        if (threadIdx.x == 64 && !*abort) release_add(up_counts() + im.grp);
+      }
     }
   }
 
-  // ---- digits.  A warp takes a row's stage.  NVFP4's factor needs all of a row: the
-  // warp looks through it first (x: top(row) is the largest finite magnitude), or,
-  // where that is costly (h: BY_ROW), the CTA's workers take a row together.
-  // load(row, at, v): eight elements; copies and place(row, j): the places that get
-  // the row.
-  template <bool BY_ROW, typename Load, typename Top, typename Place>
-  __device__ __forceinline__ void split(const Image &out, int rows, int stages, int copies,
-                                        const Load &load, const Top &row_top, const Place &place) {
-    const int worker = (threadIdx.x >> 5) - 2, lane = threadIdx.x & 31;
-    const auto member = [&](int at) { return static_cast<int>(members[at]); };
-    if constexpr (FMT == 0 || !BY_ROW) {
-      for (int t = worker * gridDim.x + blockIdx.x; t < rows * stages; t += kWorkers * gridDim.x) {
+  // ---- digits of x.  A warp takes a token's stage; NVFP4's factor needs all of the
+  // token: the warp looks through it first.
+  __device__ __forceinline__ uint4 load_x(int r, int at) const {
+    const MoeArgs &a = p.a;
+    const int64_t off = r * a.ld_x + at;
+    return at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status)
+               ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off)
+               : make_uint4(0, 0, 0, 0);
+  }
+  // The largest finite magnitude of a token.
+  __device__ __noinline__ float x_top(int r) const {
+    // eight loads in flight; magnitudes compare as integers, a magnitude of 0x7F80 or
+    // more is no number and counts as 0
+    uint32_t top = 0;
+    for (int at = (threadIdx.x & 31) * 8; at < p.a.hidden; at += 8 * kImageK) {
+      uint4 q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = load_x(r, at + i * kImageK);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t m = w[j] & 0x7FFF7FFFu;
+          top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7F807F80u));
+        }
+      }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+    return __uint_as_float(top << 16);
+  }
+  // A warp's first task is loaded before the groups are made and weights stream.
+  int x_stages, x_task;
+  uint4 x_first;
+  float x_first_top;
+  __device__ __forceinline__ void fetch_x() {
+    const MoeArgs &a = p.a;
+    x_stages = (a.hidden + kImageK - 1) / kImageK;
+    x_task = (static_cast<int>(threadIdx.x >> 5) - 2) * static_cast<int>(gridDim.x) +
+             static_cast<int>(blockIdx.x);
+    x_first_top = 0.0f;
+    if (x_task < 0 || x_task >= a.tokens * x_stages) return;
+    const int r = x_task / x_stages;
+    x_first = load_x(r, (x_task - r * x_stages) * kImageK + (threadIdx.x & 31) * 8);
+    if (FMT == 1) x_first_top = x_top(r);
+  }
+  __device__ __forceinline__ void split_x() {
+    const MoeArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    uint4 q = x_first;
+    float top = x_first_top;
+    for (int t = x_task; t < a.tokens * x_stages; t += kWorkers * gridDim.x) {
+      const int r = t / x_stages, st = t - r * x_stages;
+      if (t != x_task) {
+        q = load_x(r, st * kImageK + lane * 8);
+        if (FMT == 1) top = x_top(r);
+      }
+      const uint16_t *to = places + r * a.top_k;
+      const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(w[i] << 16);
+        v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      }
+      int row_e = 0;
+      if constexpr (FMT == 1) {
+        row_e = row_exponent(top);
+        if (st == 0 && lane < a.top_k && to[lane] != 0xFFFF) p.x.factors[to[lane]] = pow2(row_e);
+      }
+      write_digits<FMT>(p.x, st, v, row_e, a.top_k, to, 0, members);
+    }
+  }
+  // ---- digits of h = act(gate) up, of the partial sums, by the helpers: a group's as
+  // soon as its sums are there.  MXFP4: a warp takes a place's stage; NVFP4, whose
+  // factor needs all of a place: the CTA's helpers take a place together.
+  __device__ __forceinline__ uint32_t *up_counts() const { return p.a.counts + kCountGroups; }
+  __device__ __forceinline__ uint32_t *h_counts() const { return up_counts() + pairs; }
+  __device__ __forceinline__ int h_tasks(int grp) const {  // what h_counts()[grp] reaches
+    return FMT == 0 ? g.size[grp] * ((p.a.inter + kImageK - 1) / kImageK) : g.size[grp];
+  }
+  __device__ __forceinline__ void split_h(const Product<true> &up, volatile uint32_t *flag) {
+    const MoeArgs &a = p.a;
+    const int lane = threadIdx.x & 31, helper = (threadIdx.x >> 5) - 6;
+    const int groups = *g.count, stages = (a.inter + kImageK - 1) / kImageK;
+    const int rows = groups == 0 ? 0 : g.begin[groups - 1] + g.size[groups - 1];
+    const int64_t part = static_cast<int64_t>(pairs) * a.inter;
+    const auto load = [&](int r, int at, float (&v)[8]) {
+                  float u[8];
+      #pragma unroll
+                  for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
+                  if (at >= a.inter) return;
+      #pragma unroll
+                  for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
+                    if (i >= a.up_parts) break;
+                    const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
+                    if (!in_bounds(off, 8, 2 * a.up_parts * part, a.status) ||
+                        !in_bounds(off + part, 8, 2 * a.up_parts * part, a.status))
+                      continue;
+                    const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
+                    const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
+                    const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
+                    v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
+                    v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
+                    u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
+                    u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
+                  }
+      #pragma unroll
+                  for (int i = 0; i < 8; i += 2) {
+                    const float2 f = act(make_float2(v[i], v[i + 1]), a.gelu);
+                    v[i] = f.x * u[i];
+                    v[i + 1] = f.y * u[i + 1];
+                  }
+    };
+    int grp = 0;
+    const auto group_of = [&](int r) {  // (places only grow)
+      while (r >= g.begin[grp] + g.size[grp]) ++grp;
+    };
+    const auto summed = [&]() {
+      return count_reached(up_counts() + grp, up.tiles * up.parts, abort, a.status);
+    };
+    if constexpr (FMT == 0) {
+      for (int t = helper * gridDim.x + blockIdx.x; t < rows * stages; t += kHelpers * gridDim.x) {
         const int r = t / stages, st = t - r * stages;
+        group_of(r);
+        if (!__all_sync(0xFFFFFFFFu, summed())) return;
         float v[8];
         load(r, st * kImageK + lane * 8, v);
-        int row_e = 0;
-        if constexpr (FMT == 1) {
-          row_e = row_exponent(row_top(r));
-          if (st == 0 && lane < copies && place(r, lane) != 0xFFFF)
-            out.factors[place(r, lane)] = pow2(row_e);
-        }
-        write_digits<FMT>(out, st, v, row_e, copies, [&](int j) { return place(r, j); }, member);
+        write_digits<FMT>(p.h, st, v, 0, 1, nullptr, r, members);
+        __syncwarp();
+        if (lane == 0) release_add(h_counts() + grp);
       }
     } else {
+      const bool leader = helper == 0 && lane == 0;
       for (int r = blockIdx.x; r < rows; r += gridDim.x) {
+        group_of(r);
+        if (helper == 0) {
+          const bool ok = __all_sync(0xFFFFFFFFu, summed());
+          if (leader) *flag = ok ? 1u : 0u;
+        }
+        named_barrier_sync(3, kHelpers * 32);
+        if (*flag == 0u) return;
         float top = 0.0f, v[8];
-        load(r, worker * kImageK + lane * 8, v);
+        load(r, helper * kImageK + lane * 8, v);
         raise_finite(top, v);
-        for (int st = worker + kWorkers; st < stages; st += kWorkers) {
+        for (int st = helper + kHelpers; st < stages; st += kHelpers) {
           float u[8];
           load(r, st * kImageK + lane * 8, u);
           raise_finite(top, u);
         }
         top = warp_max(top);
-        if (lane == 0) tops[worker] = top;
-        named_barrier_sync(1, kWorkers * 32);
+        if (lane == 0) tops[helper] = top;
+        named_barrier_sync(3, kHelpers * 32);
 #pragma unroll
-        for (int w = 0; w < kWorkers; ++w) top = fmaxf(top, tops[w]);
-        named_barrier_sync(1, kWorkers * 32);
+        for (int w = 0; w < kHelpers; ++w) top = fmaxf(top, tops[w]);
         const int row_e = row_exponent(top);
-        if (worker == 0 && lane < copies && place(r, lane) != 0xFFFF)
-          out.factors[place(r, lane)] = pow2(row_e);
-        for (int st = worker; st < stages; st += kWorkers) {
-          if (st != worker) load(r, st * kImageK + lane * 8, v);
-          write_digits<FMT>(out, st, v, row_e, copies, [&](int j) { return place(r, j); }, member);
+        if (leader) p.h.factors[r] = pow2(row_e);
+        for (int st = helper; st < stages; st += kHelpers) {
+          if (st != helper) load(r, st * kImageK + lane * 8, v);
+          write_digits<FMT>(p.h, st, v, row_e, 1, nullptr, r, members);
         }
+        named_barrier_sync(3, kHelpers * 32);  // (the next place's flag and tops too)
+        if (leader) release_add(h_counts() + grp);
       }
     }
-  }
-  __device__ __forceinline__ void split_x() {
-    const MoeArgs &a = p.a;
-    const int lane = threadIdx.x & 31;
-    const auto load = [&](int r, int at) {
-      const int64_t off = r * a.ld_x + at;
-      return at < a.hidden && in_bounds(off, 8, (a.tokens - 1) * a.ld_x + a.hidden, a.status)
-                 ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off)
-                 : make_uint4(0, 0, 0, 0);
-    };
-    split<false>(
-        p.x, a.tokens, (a.hidden + kImageK - 1) / kImageK, a.top_k,
-        [&](int r, int at, float (&v)[8]) {
-          const uint4 q = load(r, at);
-          const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-          }
-        },
-        [&](int r) {
-          // eight loads in flight; magnitudes compare as integers, a magnitude of
-          // 0x7F80 or more is no number and counts as 0
-          uint32_t top = 0;
-          for (int at = 0; at < a.hidden; at += 8 * kImageK) {
-            uint4 q[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = load(r, at + i * kImageK + lane * 8);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const uint32_t m = w[j] & 0x7FFF7FFFu;
-                top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7F807F80u));
-              }
-            }
-          }
-          top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
-          return __uint_as_float(top << 16);
-        },
-        [&](int r, int j) { return static_cast<int>(places[r * a.top_k + j]); });
-  }
-  // h = act(gate) up, of the partial sums.
-  __device__ __forceinline__ void split_h() {
-    const MoeArgs &a = p.a;
-    const int groups = *g.count;
-    const int rows = groups == 0 ? 0 : g.begin[groups - 1] + g.size[groups - 1];
-    const int64_t part = static_cast<int64_t>(pairs) * a.inter;
-    split<true>(p.h, rows, (a.inter + kImageK - 1) / kImageK, 1,
-          [&](int r, int at, float (&v)[8]) {
-            float u[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
-            if (at >= a.inter) return;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
-              if (i >= a.up_parts) break;
-              const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
-              if (!in_bounds(off, 8, 2 * a.up_parts * part, a.status) ||
-                  !in_bounds(off + part, 8, 2 * a.up_parts * part, a.status))
-                continue;
-              const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
-              const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
-              const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
-              v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
-              v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
-              u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
-              u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-              const float2 f = a.gelu ? gelu_f32x2(make_float2(v[i], v[i + 1]))
-                                      : make_float2(v[i] / (1.0f + expf(-v[i])),
-                                                    v[i + 1] / (1.0f + expf(-v[i + 1])));
-              v[i] = f.x * u[i];
-              v[i + 1] = f.y * u[i + 1];
-            }
-          },
-          [](int) { return 0.0f; }, [&](int r, int) { return r; });
   }
 
   // ---- y[t] = sum_j w_tj z[t, j], in the order of the slots; two columns a thread.
@@ -535,7 +590,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   griddep_launch_dependents();
+  if (warp >= 2) {
+    warm_digits<FMT>(p.x);
+    // (the result is used, so that the call stays)
+    if (act(make_float2(0.0f, 0.0f), a.gelu).x != 0.0f) atomicOr(a.status, kStatusTimeout);
+  }
   griddep_wait();
+  x.fetch_x();
   // (the scratch lies in the ring: a fence and a barrier before the first copy)
   make_groups<kThreads / 32>(x.g, x.places, x.members, smem, a.ids, x.pairs, a.experts, X::kGroup,
                              a.status);
@@ -547,17 +608,37 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Product<false> down(a, *x.g.count);
 
   if (warp == 0) {
-    // the digits are there when every CTA has counted them
-    const auto counted = [&](int i) {
-      bool r = true;
-      if ((threadIdx.x & 31) == 0) r = count_reached(a.counts + i, gridDim.x, x.abort, a.status);
-      r = __all_sync(0xFFFFFFFFu, r) != 0;
-      asm volatile("fence.proxy.async;" ::: "memory");  // bulk copies read what was counted
-      return r;
+    // the digits of x are there when every CTA has counted them
+    int x_there = 0;
+    const auto x_ready = [&](int, int how) {
+      if (x_there == 0 && how == kWait) {
+        const bool r = count_reached(a.counts + kCountX, gridDim.x, x.abort, a.status);
+        x_there = __all_sync(0xFFFFFFFFu, r) != 0 ? 1 : -1;
+        asm volatile("fence.proxy.async;" ::: "memory");  // bulk copies read what was counted
+      }
+      return x_there;
     };
-    if (!*x.abort &&
-        x.template copies<true>(up, &gate_map, &up_map, p.x, [&] { return counted(kCountX); }))
-      x.template copies<false>(down, &down_map, &down_map, p.h, [&] { return counted(kCountH); });
+    // those of h, of a group; a look takes in the 32 groups from it on
+    int from = 0;
+    uint32_t there = 0;
+    const auto h_ready = [&](int grp, int how) {
+      if (grp - from < 32 && (there >> (grp - from)) & 1u) return 1;
+      if (how == kKnown) return 0;
+      from = grp;
+      if (how == kWait) {
+        const bool r = count_reached(x.h_counts() + grp, x.h_tasks(grp), x.abort, a.status);
+        if (!__all_sync(0xFFFFFFFFu, r)) return -1;
+      }
+      const int look = grp + static_cast<int>(threadIdx.x & 31);
+      bool r = false;
+      if (look < *x.g.count)
+        r = load_acquire(x.h_counts() + look) >= static_cast<uint32_t>(x.h_tasks(look));
+      there = __ballot_sync(0xFFFFFFFFu, r);
+      asm volatile("fence.proxy.async;" ::: "memory");
+      return static_cast<int>(there & 1u);
+    };
+    if (!*x.abort && x.template copies<true>(up, &gate_map, &up_map, p.x, x_ready))
+      x.template copies<false>(down, &down_map, &down_map, p.h, h_ready);
     // No copy may land after the CTA has left.  (After an abort a stage may lack
     // its images: that wait runs out, with no copy left behind it.)
     const uint32_t slots = static_cast<uint32_t>(p.slots);
@@ -577,13 +658,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     x.split_x();
     add(kCountX);
-    if (FMT == 1) wait(kCountX);  // the epilogue reads the factors
-    if (epilogue) x.template epilogue<true>(up, p.x.factors);
-    add(kCountUp);
-    if (wait(kCountUp)) x.split_h();
-    add(kCountH);
-    if (FMT == 1) wait(kCountH);
-    if (epilogue) x.template epilogue<false>(down, p.h.factors);
+    if (epilogue) {
+      // (the factors it reads were counted before the products that it waits for)
+      x.template epilogue<true>(up, p.x.factors);
+      x.template epilogue<false>(down, p.h.factors);
+    } else {
+      x.split_h(up, flag);
+    }
     add(kCountDown);
     if (wait(kCountDown)) x.combine(warp - 2);
   }
@@ -597,10 +678,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Clears the counts (mx_moe_layer_bf16's router does it there).
-__global__ void clear_kernel(uint32_t *counts) {
+__global__ void __launch_bounds__(256) clear_kernel(uint32_t *counts, int n) {
   griddep_launch_dependents();
   griddep_wait();
-  if (threadIdx.x < kMoeCounts) counts[threadIdx.x] = 0;
+  for (int i = threadIdx.x; i < n; i += 256) counts[i] = 0;
 }
 
 // The images in the workspace: codes of x, scales of x, codes of h, scales of h.
@@ -640,7 +721,7 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   p.sfa_off = p.b_off + p.slots * X::kGroup * kImageCodes;
   p.sfb_off = p.sfa_off + p.slots * 2 * X::kSfa;
   p.bar_off = p.sfb_off + p.slots * X::kSfb;
-  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + kWorkers * 4 + 15) / 16 * 16;
+  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + kHelpers * 4 + 15) / 16 * 16;
   const int smem = p.groups_at + groups;
   // the groups' scratch lies in the weights' part of the ring
   if (smem > kSmem || p.b_off < 2 * (kThreads / 32 + 2) * a.experts) return cudaErrorInvalidValue;
@@ -695,7 +776,8 @@ int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_s
 }
 
 cudaError_t launch_moe_clear(const MoeArgs &a, cudaStream_t s) {
-  return launch_pdl(clear_kernel, dim3(1), dim3(32), 0, s, a.counts);
+  return launch_pdl(clear_kernel, dim3(1), dim3(256), 0, s, a.counts,
+                    moe_counts(a.tokens * a.top_k));
 }
 
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s) {

@@ -250,13 +250,14 @@ struct MoeArgs {
   float *z;            // [down_parts][tokens * top_k][hidden]
   uint8_t *image;      // digits of x, then of h (moe_image_bytes)
   float *factors;      // NVFP4: of the rows of x, then of h
-  uint32_t *counts;    // kMoeCounts grid-wide counts, cleared by the launch before
+  uint32_t *counts;    // moe_counts(tokens * top_k), cleared by the launch before
   int num_sms;
   uint32_t *status;
 };
 // Bytes of the digits of `rows` rows of k activations.
 size_t moe_image_bytes(int64_t rows, int64_t k);
-constexpr int kMoeCounts = 4;
+// Grid-wide counts, and those of the groups (moe_mma.cu).
+constexpr int moe_counts(int pairs) { return 2 + 2 * pairs; }
 // Ranges of K that a product is divided into, and the most for a number of pairs.
 int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms);
 constexpr int moe_max_parts(int64_t pairs) { return pairs <= 16 ? 4 : pairs <= 64 ? 2 : 1; }
