@@ -101,7 +101,16 @@ struct Expert {
   static constexpr int kSfaCols = kAtoms * 4;
   static constexpr int kSfb = kImageScales<FMT>;
   static constexpr int kAccCols = 2 * NB * 32;
-  static constexpr int kSfCols = 3 * kSfaCols;
+  static constexpr int kSfCols = 4 * kSfaCols;
+
+  // Stages in a slot: two for the down product where the images and the second
+  // stage's scales of the group fit one slot's room for images, for it has half the
+  // weights of the up product in a stage and would have half as many bytes in flight
+  // (8 x 4096 x 2048 NVFP4 of 64: 76.9 us with one, 69.5 so).
+  template <bool UP>
+  __device__ __forceinline__ int span(int grp) const {
+    return !UP && 2 * g.size[grp] * kImageCodes + kSfb <= kGroup * kImageCodes ? 2 : 1;
+  }
 
   const ExpertParams &p;
   char *smem;
@@ -123,34 +132,41 @@ struct Expert {
     if (++buf == static_cast<uint32_t>(p.bufs)) buf = 0, bph ^= 1u;
   }
 
-  // ---- copies.  Weights of a stage and, if `images`, its images (a stage's barrier
-  // expects the bytes of both).
+  // ---- copies of n stages into a slot, whose barrier expects the bytes of both kinds.
+  // The second stage (of the down product) takes the place of the second matrix.
   template <bool UP>
   __device__ __forceinline__ void copy_weights(const Product<UP> &d, const CUtensorMap *m0,
-                                               const CUtensorMap *m1, const typename Product<UP>::Item &im,
-                                               int st) {
-    constexpr int kSegs = Product<UP>::kSegs;
+                                               const CUtensorMap *m1,
+                                               const typename Product<UP>::Item &im, int st, int n) {
     const MoeArgs &a = p.a;
     const int e = g.expert[im.grp], katoms = (d.k / (FMT == 0 ? 32 : 16) + 3) >> 2;
     const int64_t off = ((static_cast<int64_t>(e) * d.tiles + im.tile) * katoms + st * kAtoms) * 512;
-    const uint32_t bytes = static_cast<uint32_t>(min(kAtoms, katoms - st * kAtoms)) * 512u;
     const uint32_t fb = smem_u32(&full[s]), w = smem_u32(smem) + s * 2 * kTile;
     const uint32_t sf = smem_u32(smem + p.sfa_off) + s * 2 * kSfa;
     const int row = e * d.rows + im.tile * 128;
-    mbar_arrive_expect_tx(fb, kSegs * (kTile + bytes) + g.size[im.grp] * kImageCodes + kSfb);
+    // bytes of scales, of one matrix; those of the second stage follow the first's
+    const uint32_t bytes = static_cast<uint32_t>(min(n * kAtoms, katoms - st * kAtoms)) * 512u;
+    mbar_arrive_expect_tx(fb, (UP ? 2 : n) * kTile + (UP ? 2 : 1) * bytes +
+                                  n * (g.size[im.grp] * kImageCodes + kSfb));
     tma_load_2d(w, m0, st * 128, row, fb);
     bulk_load(sf, (UP ? a.gate.scales : a.down.scales) + off, bytes, fb);
     if constexpr (UP) {
       tma_load_2d(w + kTile, m1, st * 128, row, fb);
       bulk_load(sf + kSfa, a.up.scales + off, bytes, fb);
+    } else if (n == 2) {
+      tma_load_2d(w + kTile, m0, (st + 1) * 128, row, fb);
     }
   }
-  __device__ __forceinline__ void copy_images(const Image &im, int grp, int st, uint32_t slot) {
-    const uint32_t fb = smem_u32(&full[slot]);
+  __device__ __forceinline__ void copy_images(const Image &im, int grp, int st, uint32_t slot, int n) {
+    const uint32_t fb = smem_u32(&full[slot]), size = g.size[grp] * kImageCodes;
+    const uint32_t b = smem_u32(smem + p.b_off) + slot * kGroup * kImageCodes;
     const int64_t at = static_cast<int64_t>(st) * pairs;
-    bulk_load(smem_u32(smem + p.b_off) + slot * kGroup * kImageCodes,
-              im.codes + (at + g.begin[grp]) * kImageCodes, g.size[grp] * kImageCodes, fb);
+    bulk_load(b, im.codes + (at + g.begin[grp]) * kImageCodes, size, fb);
     bulk_load(smem_u32(smem + p.sfb_off) + slot * kSfb, im.scales + (at + grp) * kSfb, kSfb, fb);
+    if (n == 2) {
+      bulk_load(b + size, im.codes + (at + pairs + g.begin[grp]) * kImageCodes, size, fb);
+      bulk_load(b + 2 * size, im.scales + (at + pairs + grp) * kSfb, kSfb, fb);
+    }
   }
   // The copies of a product.  ready(group, how): whether the group's images are there;
   // kKnown: as far as that is known without a look, kLook, kWait (whole warp; < 0:
@@ -160,32 +176,31 @@ struct Expert {
                                          const CUtensorMap *m1, const Image &im, const Ready &ready) {
     if (d.begin >= d.end) return true;
     typename Product<UP>::Item cur{}, old = d.at(d.begin);
-    int late_item = d.begin, late_st = old.st0, late = 0;  // stages whose images are still to come
+    int late_item = d.begin, late_st = old.st0, late = 0;  // slots whose images are still to come
     uint32_t late_slot = s;
     const auto catch_up = [&](int how) {
       while (late > 0) {
         const int there = ready(old.grp, how);
         if (there <= 0) return there == 0;
-        const int n = min(late, old.st1 - late_st);
-        for (int i = 0; i < n; ++i) {
-          if (elect_one()) copy_images(im, old.grp, late_st, late_slot);
+        const int by = span<UP>(old.grp);
+        for (; late > 0 && late_st < old.st1; --late, late_st += by) {
+          if (elect_one()) copy_images(im, old.grp, late_st, late_slot, min(by, old.st1 - late_st));
           __syncwarp();
           if (++late_slot == static_cast<uint32_t>(p.slots)) late_slot = 0;
-          ++late_st;
         }
-        late -= n;
-        if (late_st == old.st1 && (late_item += d.step) < d.end) old = d.at(late_item), late_st = old.st0;
+        if (late_st >= old.st1 && (late_item += d.step) < d.end) old = d.at(late_item), late_st = old.st0;
       }
       return true;
     };
     for (int item = d.begin; item < d.end; item += d.step) {
       cur = d.at(item);
       if (item != d.begin && !catch_up(kLook)) return false;
-      for (int st = cur.st0; st < cur.st1; ++st) {
+      const int by = span<UP>(cur.grp);
+      for (int st = cur.st0; st < cur.st1; st += by) {
         // (the slots of the first stages come free with the products before them)
         if (late == p.slots && !catch_up(kWait)) return false;
         if (!mbar_wait_warp(smem_u32(&empty[s]), ph ^ 1u, abort, p.a.status)) return false;
-        if (elect_one()) copy_weights<UP>(d, m0, m1, cur, st);
+        if (elect_one()) copy_weights<UP>(d, m0, m1, cur, st, min(by, cur.st1 - st));
         __syncwarp();
         ++late;
         next_slot();
@@ -199,7 +214,6 @@ struct Expert {
   // the loops are unrolled and descriptors stepped by constants.
   template <bool UP>
   __device__ __forceinline__ bool products(const Product<UP> &d) {
-    constexpr int kSegs = Product<UP>::kSegs;
     const uint32_t w_ring = smem_u32(smem), b_ring = smem_u32(smem + p.b_off);
     const uint32_t sfa_ring = smem_u32(smem + p.sfa_off), sfb_ring = smem_u32(smem + p.sfb_off);
     const uint32_t sf_tmem = tmem + p.bufs * kAccCols;
@@ -213,42 +227,69 @@ struct Expert {
       if (!mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, p.a.status)) return false;
       tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols;
-      for (int st = im.st0; st < im.st1; ++st) {
+      const int by = span<UP>(im.grp), size = g.size[im.grp] * kImageCodes;
+      for (int st = im.st0; st < im.st1; st += by) {
         if (!mbar_wait_warp(smem_u32(&full[s]), ph, abort, p.a.status)) return false;
         tc_fence_after();
         if (elect_one()) {
+          const uint32_t b = b_ring + s * kGroup * kImageCodes;
           const uint32_t sfa_t = sf_tmem + s * kSfCols, sfb_t = sfa_t + 2 * kSfaCols;
           const uint64_t sfa = smem_desc_scale_block(sfa_ring + s * 2 * kSfa);
-          const uint64_t sfb = smem_desc_scale_block(sfb_ring + s * kSfb);
-          const int atoms = min(kAtoms, katoms - st * kAtoms);
-          const int steps = min(4, (d.k - st * kImageK + 63) >> 6);  // of 64 inside K
+          const uint64_t wd = smem_desc_sw128_kmajor(w_ring + s * 2 * kTile);
+          const int last = min(by, im.st1 - st) - 1;  // of the slot's stages
+          // h: the second matrix (UP), or the second stage, whose digits are its own
+          const auto scales = [&](int h) {
+            const uint64_t sfb =
+                smem_desc_scale_block(h == 0 ? sfb_ring + s * kSfb : b + 2 * size);
+            const int atoms = min(kAtoms, katoms - (UP ? st : st + h) * kAtoms);
+            if (!UP || h == 0) {
 #pragma unroll
-          for (int j = 0; j < kAtoms; ++j)
-            tc_cp_32x128b_warpx4(sfb_t + j * 4, sfb + ((j * 512) >> 4));
-#pragma unroll
-          for (int m = 0; m < kSegs; ++m) {
+              for (int j = 0; j < kAtoms; ++j)
+                tc_cp_32x128b_warpx4(sfb_t + h * kSfaCols + j * 4, sfb + ((j * 512) >> 4));
+            }
 #pragma unroll
             for (int i = 0; i < kAtoms; ++i) {
               if (i < atoms)
-                tc_cp_32x128b_warpx4(sfa_t + m * kSfaCols + i * 4, sfa + ((m * kSfa + i * 512) >> 4));
+                tc_cp_32x128b_warpx4(sfa_t + h * kSfaCols + i * 4, sfa + ((h * kSfa + i * 512) >> 4));
             }
-          }
-          const uint64_t wd = smem_desc_sw128_kmajor(w_ring + s * 2 * kTile);
-          const uint64_t bd = smem_desc_sw128_kmajor(b_ring + s * kGroup * kImageCodes);
+          };
+          const auto multiply = [&](int h, int kk, uint64_t bd) {
+            const int word = FMT == 0 ? kk >> 1 : kk;
+            tc_mma_block_scaled<FMT>(
+                acc + (UP ? h * NB * 32 : 0), wd + h * (kTile >> 4) + 2 * kk, bd + 2 * kk,
+                FMT == 0 && (kk & 1) ? idesc2 : idesc0, sfa_t + h * kSfaCols + word * 4,
+                sfb_t + (UP ? 0 : h * kSfaCols) + word * 4,
+                kk > 0 || st > im.st0 || (!UP && h > 0) ? 1u : 0u);
+          };
+          const auto steps = [&](int stage) { return min(4, (d.k - stage * kImageK + 63) >> 6); };
+          const uint64_t bd = smem_desc_sw128_kmajor(b);
+          scales(0);
+          if constexpr (UP) {
+            scales(1);
+            const int n = steps(st);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            if (kk < steps) {
-              const int word = FMT == 0 ? kk >> 1 : kk;
-              const uint32_t idesc = FMT == 0 && (kk & 1) ? idesc2 : idesc0;
+            for (int kk = 0; kk < 4; ++kk) {
+              if (kk < n) {
+                multiply(0, kk, bd);
+                multiply(1, kk, bd);
+              }
+            }
+          } else {
+            if (last > 0) scales(1);
+            const int n = steps(st);
 #pragma unroll
-              for (int m = 0; m < kSegs; ++m)
-                tc_mma_block_scaled<FMT>(acc + m * NB * 32, wd + m * (kTile >> 4) + 2 * kk,
-                                         bd + 2 * kk, idesc, sfa_t + m * kSfaCols + word * 4,
-                                         sfb_t + word * 4, kk > 0 || st > im.st0 ? 1u : 0u);
+            for (int kk = 0; kk < 4; ++kk)
+              if (kk < n) multiply(0, kk, bd);
+            if (last > 0) {
+              const uint64_t bd1 = smem_desc_sw128_kmajor(b + size);
+              const int n1 = steps(st + 1);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                if (kk < n1) multiply(1, kk, bd1);
             }
           }
           tc_commit(smem_u32(&empty[s]));
-          if (st == im.st1 - 1) tc_commit(smem_u32(&acc_full[buf]));
+          if (st + last == im.st1 - 1) tc_commit(smem_u32(&acc_full[buf]));
         }
         __syncwarp();
         next_slot();
@@ -411,31 +452,31 @@ struct Expert {
     const int rows = groups == 0 ? 0 : g.begin[groups - 1] + g.size[groups - 1];
     const int64_t part = static_cast<int64_t>(pairs) * a.inter;
     const auto load = [&](int r, int at, float (&v)[8]) {
-                  float u[8];
-      #pragma unroll
-                  for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
-                  if (at >= a.inter) return;
-      #pragma unroll
-                  for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
-                    if (i >= a.up_parts) break;
-                    const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
-                    if (!in_bounds(off, 8, 2 * a.up_parts * part, a.status) ||
-                        !in_bounds(off + part, 8, 2 * a.up_parts * part, a.status))
-                      continue;
-                    const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
-                    const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
-                    const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
-                    v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
-                    v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
-                    u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
-                    u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
-                  }
-      #pragma unroll
-                  for (int i = 0; i < 8; i += 2) {
-                    const float2 f = act(make_float2(v[i], v[i + 1]), a.gelu);
-                    v[i] = f.x * u[i];
-                    v[i + 1] = f.y * u[i + 1];
-                  }
+      float u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = u[i] = 0.0f;
+      if (at >= a.inter) return;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {  // (moe_max_parts is 4)
+        if (i >= a.up_parts) break;
+        const int64_t off = 2 * i * part + static_cast<int64_t>(r) * a.inter + at;
+        if (!in_bounds(off, 8, 2 * a.up_parts * part, a.status) ||
+            !in_bounds(off + part, 8, 2 * a.up_parts * part, a.status))
+          continue;
+        const float4 *s0 = reinterpret_cast<const float4 *>(a.h + off);
+        const float4 *s1 = reinterpret_cast<const float4 *>(a.h + off + part);
+        const float4 a0 = __ldcg(s0), a1 = __ldcg(s0 + 1), b0 = __ldcg(s1), b1 = __ldcg(s1 + 1);
+        v[0] += a0.x, v[1] += a0.y, v[2] += a0.z, v[3] += a0.w;
+        v[4] += a1.x, v[5] += a1.y, v[6] += a1.z, v[7] += a1.w;
+        u[0] += b0.x, u[1] += b0.y, u[2] += b0.z, u[3] += b0.w;
+        u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float2 f = act(make_float2(v[i], v[i + 1]), a.gelu);
+        v[i] = f.x * u[i];
+        v[i + 1] = f.y * u[i + 1];
+      }
     };
     int grp = 0;
     const auto group_of = [&](int r) {  // (places only grow)
