@@ -384,11 +384,20 @@ int nvfp4_gemm_ex(const void *a_codes, const void *a_scales, const void *b_codes
  * counterpart; they are this library's own addition.
  *
  * Numerics.  A weight is code * block scale (* tensor scale), each factor
- * exact.  An activation enters the products as FP16 times one power of two for
- * each (token, 128 consecutive elements): a BF16 value is held exactly unless
- * it is below 2^-31 of the largest of its 128, and then to within 2^-40 of
- * that largest.  Sums are binary32.  Infinities and NaN in x reach the outputs
- * of their token.  A UE8M0 scale byte of 255 is NaN. */
+ * exact.  Sums are binary32; their order does not depend on the run.
+ *   mx_linear_bf16 multiplies FP16: an activation enters as FP16 times one
+ *   power of two for each (token, 128 consecutive elements), a BF16 value
+ *   exactly unless it is below 2^-31 of the largest of its 128, and then to
+ *   within 2^-40 of that largest.
+ *   mx_linear_bf16_workspace (where it takes a workspace) and the experts
+ *   multiply FP4: an activation enters as the sum of eight FP4 digits under
+ *   the format's own block scales, a BF16 value exactly unless it is below
+ *   2^-13 of the largest of its block (32 or 16 elements), and always to
+ *   within 2^-22 of that largest (NVFP4: or 2^-39 of the token's largest;
+ *   MXFP4: or 2^-126).
+ * Infinities and NaN in x reach the outputs of their token and no others; in
+ * the experts' products they make all of them NaN.  A UE8M0 scale byte of 255
+ * is NaN. */
 
 /* Most rows of x that mx_linear_bf16 takes. */
 #define MX_LINEAR_MAX_TOKENS 32
@@ -469,9 +478,10 @@ typedef struct mx_moe_weights {
   mx_moe_matrix down; /* per expert [hidden, inter] */
 } mx_moe_weights;
 
-/* Workspace bytes of the two calls below: the hidden values and the weighted
- * outputs of every (token, slot) pair in binary32, and counters.  0 for
- * invalid arguments.  Nothing in it needs to start at any value. */
+/* Workspace bytes of the two calls below: the sums of the gate, up and down
+ * rows for every (token, slot) pair in binary32, the digits of x and of the
+ * hidden values, and counters.  0 for invalid arguments.  Nothing in it needs
+ * to start at any value; one call at a time may use it. */
 size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k);
 
 /* y[t] = sum_j weights[t, j] D_e (act(G_e x_t) * U_e x_t), e = ids[t, j].
@@ -483,10 +493,9 @@ size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int
  *   y: out BF16 [tokens, hidden], row stride ld_y (>= hidden);
  *   hidden % 32 == 0, inter % 32 == 0; tokens 0..MX_MOE_MAX_TOKENS;
  *   workspace: mx_moe_workspace_bytes(...) bytes, 16-byte aligned.
- * The hidden values act(G x) * U x are kept in binary32 and enter the second
- * product as FP16 times a power of two for each 128 (a rounding of 2^-12,
- * an eighth of the output's own).  y and the workspace must not overlap an
- * input or each other.  Reads the chosen experts' weights only.  Launches a
+ * The hidden values act(G x) * U x are computed in binary32 and enter the
+ * second product as eight FP4 digits (to within 2^-22 of the largest of their
+ * block).  y and the workspace must not overlap an input or each other.  Reads the chosen experts' weights only.  Launches a
  * kernel of one warp and one of a CTA per SM, all resident together (a
  * cooperative launch: it waits for SMs that other streams' kernels hold). */
 int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,

@@ -12,7 +12,7 @@ Tolerances, with S = sum_k |x||w|:
 * BF16 out: the same plus one BF16 ulp.
 * experts: the hidden value h = act(g) u carries dh = 1.13 E_g |u| + |act g| E_u
   + (E_g E_u) + 2^-20 |h| (silu and gelu have slope below 1.13), and enters the
-  second product as FP16, 2^-12 relative: z carries sum |w_d| (dh + 2^-12 |h|) +
+  second product to within 2^-12 relative: z carries sum |w_d| (dh + 2^-12 |h|) +
   1e-5 sum |w_d||h| + the 2^-39 term; y the weighted sum of the z's, 2^-20 of
   their absolute sum, and one BF16 ulp.
 * route: ids equal where the choice is exact or the gap to the next logit is
