@@ -32,6 +32,7 @@ struct Params {
   float *parts;      // [CTA][first or last tile of its share][tokens][128]
   uint32_t *counts;  // [tiles]: CTAs that have written their sums
   int tiles, stages;
+  int each, more;                             // units of a CTA (Share)
   int slots, b_bytes;                         // stages in flight; bytes of a stage's digits
   int b_off, sfa_off, sfb_off, bar_off;       // shared memory (the weights at 0)
 };
@@ -148,14 +149,14 @@ __device__ __noinline__ float nonfinite_sum(const LinearArgs &a, int64_t row, in
   return any ? sum : v;
 }
 
-// A CTA's share of the units, and who shares a tile.
+// A CTA's share of the units (the first `more` CTAs have one more than `each`), and
+// who shares a tile.
 struct Share {
-  int64_t units;
-  __device__ __forceinline__ int begin(int cta) const {
-    return static_cast<int>(units * cta / gridDim.x);
-  }
-  __device__ __forceinline__ int owner(int64_t unit) const {
-    return static_cast<int>(((unit + 1) * gridDim.x - 1) / units);
+  int each, more;
+  __device__ __forceinline__ int begin(int cta) const { return cta * each + min(cta, more); }
+  __device__ __forceinline__ int owner(int unit) const {
+    const int first = more * (each + 1);
+    return unit < first ? unit / (each + 1) : more + (unit - first) / each;
   }
 };
 
@@ -187,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
   volatile uint32_t *abort = tmem_slot + 1;
   volatile uint32_t *last = tmem_slot + 2;  // [first or last tile][before, after its sums]
-  const Share share{static_cast<int64_t>(p.tiles) * p.stages};
+  const Share share{p.each, p.more};
   const int begin = share.begin(blockIdx.x), end = share.begin(blockIdx.x + 1);
   const int katoms = static_cast<int>((a.k / (FMT == 0 ? 32 : 16) + 3) >> 2);
   const uint32_t slots = static_cast<uint32_t>(p.slots);
@@ -207,21 +208,24 @@ __global__ void __launch_bounds__(kThreads, 1)
               a.tokens * kImageCodes, fb);
     bulk_load(smem_u32(smem + p.sfb_off) + s * S::kSfb, p.x.scales + st * S::kSfb, S::kSfb, fb);
   };
-  const int ahead = min(p.slots, end - begin);  // weights copied before the digits are there
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < p.slots; ++s) {
-      mbar_init(smem_u32(&full[s]), 1);
-      mbar_init(smem_u32(&empty[s]), 1);
+  const int ahead = min(p.slots, end - begin);  // stages copied before the first wait
+  if (warp == 0) {
+    if (elect_one()) {
+      for (int s = 0; s < p.slots; ++s) {
+        mbar_init(smem_u32(&full[s]), 1);
+        mbar_init(smem_u32(&empty[s]), 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(smem_u32(&acc_full[i]), 1);
+        mbar_init(smem_u32(&acc_empty[i]), kEpilogue);
+      }
+      mbar_init(smem_u32(done), 1);
+      *abort = 0u;
+      fence_barrier_init();
+      // the weights before the digits are there
+      for (int i = 0; i < ahead; ++i) weights(begin + i, i);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&acc_full[i]), 1);
-      mbar_init(smem_u32(&acc_empty[i]), kEpilogue);
-    }
-    mbar_init(smem_u32(done), 1);
-    *abort = 0u;
-    fence_barrier_init();
-    prefetch_tmap(&map);
-    for (int i = 0; i < ahead; ++i) weights(begin + i, i);
+    __syncwarp();
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     griddep_wait();
-    asm volatile("fence.proxy.async;" ::: "memory");  // bulk copies read what kernels wrote
+    asm volatile("fence.proxy.async;" ::: "memory");
     if (elect_one())
       for (int i = 0; i < ahead; ++i) digits(begin + i, i);
     __syncwarp();
@@ -330,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int st1 = min(p.stages, st0 + end - unit);
       const bool whole = st0 == 0 && st1 == p.stages;
       const int64_t at = static_cast<int64_t>(tile) * 128 + row;
-      const int64_t first = static_cast<int64_t>(tile) * p.stages;
+      const int first = tile * p.stages;
       const int c0 = whole ? blockIdx.x : share.owner(first);
       const int c1 = whole ? blockIdx.x : share.owner(first + p.stages - 1);
       const int word = unit == begin ? 0 : 2;
@@ -473,9 +477,15 @@ cudaError_t launch_product(Params p, cudaStream_t s) {
   if (smem > kSmem) return cudaErrorInvalidValue;
   CUtensorMap map;
   if (!encode_codes_window_map(&map, a.w.codes, a.n, a.k, 128)) return cudaErrorInvalidValue;
-  const int64_t units = static_cast<int64_t>(p.tiles) * p.stages;
-  int64_t ctas = a.num_sms < kLinearCtas ? a.num_sms : kLinearCtas;
+  const int units = p.tiles * p.stages;
+  int ctas = a.num_sms < kLinearCtas ? a.num_sms : kLinearCtas;
+  // With many tokens every end of a share costs an epilogue of 2 us: tiles divided
+  // evenly where that leaves few SMs idle (32 x 8192 x 8192 NVFP4: 22.1 us, so 20.1; 8 x
+  // 8192 x 28672, bound by the weights, 30.7 us and would take 33.3).
+  if (const int even = ctas / p.tiles * p.tiles; NB == 8 && even * 5 >= ctas * 4) ctas = even;
   if (ctas > units) ctas = units;
+  p.each = units / ctas;
+  p.more = units % ctas;
   return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, s, map, p);
 }
 
@@ -487,7 +497,7 @@ cudaError_t launch_fmt(const Params &p, cudaStream_t s) {
   cudaError_t e;
   if (FMT == 1 && p.a.tokens > 16) {
     // Launched early, so many CTAs crowd on the SMs that the kernel before it leaves
-    // first and hold up the product's there (32 x 8192 x 8192: 27.9 us, so 22.1).
+    // first and hold up the product's there (32 x 8192 x 8192: 27.9 us; so 22.1).
     digits_kernel<FMT><<<grid, block, 0, s>>>(p);
     e = cudaGetLastError();
   } else {
