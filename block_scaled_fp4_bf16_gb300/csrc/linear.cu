@@ -1,8 +1,8 @@
 // mx_linear_bf16: a few BF16 rows times an FP4 weight.
 //
 // y[t, n] = sum_k W[n, k] x[t, k] for up to 8 NT tokens.  Two kernels; the rule that
-// chooses (launch_linear) has both sides' times.  This one is for the smaller calls,
-// where a launch and one pass of dependent steps are what counts:
+// chooses (linear_mma_better) has both sides' times.  This one is for the smaller
+// calls, where a launch and one pass of dependent steps are what counts:
 //   - an item is R = 16 MT weight rows; the CTA's warps divide K, each walks its range
 //     in stages of 128 that come by cp.async into a ring of its own, over the end
 //     of one item into the next; the warps meet only to add their sums;
@@ -13,8 +13,10 @@
 //     E4M3 scales of NVFP4 to the FP16 weights (code * scale has 6 bits: exact);
 //   - activations become FP16 times a power of two for each (token, 128): BF16
 //     values keep all their bits unless they lie 2^-31 below the largest of the 128.
-// It issues about 2.5 instructions a code, which bounds it at 4.2 TB/s of weights for
-// up to 8 tokens; linear_mma.cu leaves the weights to the tensor cores.
+// It issues about 2.5 instructions a code, which bounds it at 4 TB/s of weights
+// for up to 8 tokens (28672 x 8192: 30 us); linear_mma.cu leaves the weights to the
+// tensor cores.  At 8 x 4096 x 4096 (4.9 us; its bytes 1.4) latency bounds it: a launch,
+// two rounds of copies from memory, the join of the warps.
 #include <cuda_fp16.h>
 
 #include "mx_device.cuh"

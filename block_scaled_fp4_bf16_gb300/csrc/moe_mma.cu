@@ -6,11 +6,18 @@
 //   - the digits of x are written to the workspace (an "image": for a row and 256
 //     elements of K the eight rows of 128 bytes as the product reads them, 128-byte
 //     swizzle included, and their scales; its rows are the pairs sorted by expert, so
-//     a group's lie together);
-//   - the sums of the gate and up rows; the digits of h = act(gate) up; the sums of the
-//     down rows; y.
-// A grid-wide count separates these parts, and the copies of the next weights run
-// ahead of it: where a kernel boundary would leave the memory idle, weights stream.
+//     a group's lie together); a grid-wide count says that they are there;
+//   - the sums of the gate and up rows; group by group, as its sums are complete, the
+//     digits of h = act(gate) up; the sums of the down rows;
+//   - after a second grid-wide count, y.
+// The copies of weights run ahead of the counts: where a kernel boundary would leave
+// the memory idle, weights stream.  (With grid-wide counts around the digits of h too:
+// 64 x 4096 x 2048 of 64 173 us and 8 x 4096 x 2048 NVFP4 82 us; so 165 and 77.)
+//
+// Bound: at many pairs the weights' bytes (64 x 4096 x 2048 of 64 MXFP4 155 us, 5.5 TB/s
+// of them; 8 x 4096 x 2048, 26 of 64 experts chosen, NVFP4 70 us, 5.4 TB/s); at few the
+// chain of dependent steps (1 x 2048 x 1024 of 64 20 us: digits of x 4, up sums 4, digits of h
+// 3, down sums 3, y 2, the rest launches; the weights alone are 4 us).
 #include "fp4_digits.cuh"
 #include "moe_groups.cuh"
 
