@@ -1224,8 +1224,8 @@ MX_API int mx_moe_route_bf16(const void *x, int64_t tokens, int64_t hidden, int6
   if (tokens == 0) return MX_OK;
   const mx::RouteArgs a{x,     ld_x,  static_cast<int>(tokens), static_cast<int>(hidden),
                         static_cast<int>(experts), top_k, normalize, router, bias, ids, weights,
-                        nullptr, dev->status};
-  return launch_rc(fn, mx::launch_moe_route(a, static_cast<cudaStream_t>(stream)));
+                        dev->status};
+  return launch_rc(fn, mx::launch_moe_route(a, nullptr, static_cast<cudaStream_t>(stream)));
 }
 
 MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k) {
@@ -1255,7 +1255,7 @@ MX_API int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, cons
   if (tokens == 0) return MX_OK;
   moe_device(&a, dev);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = mx::launch_moe_clear(a, s);
+  const cudaError_t e = mx::launch_moe_prepare(a, s);
   return launch_rc(fn, e != cudaSuccess ? e : mx::launch_moe_experts(a, s));
 }
 
@@ -1297,9 +1297,9 @@ MX_API int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const 
   if (tokens == 0) return MX_OK;
   moe_device(&a, dev);
   const mx::RouteArgs r{x,      ld_x,        a.tokens, a.hidden, a.experts, top_k,     normalize,
-                        router, router_bias, ids,      weights,  a.counts,  dev->status};
+                        router, router_bias, ids,      weights,  dev->status};
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = mx::launch_moe_route(r, s);
+  const cudaError_t e = mx::launch_moe_route(r, &a, s);
   return launch_rc(fn, e != cudaSuccess ? e : mx::launch_moe_experts(a, s));
 }
 

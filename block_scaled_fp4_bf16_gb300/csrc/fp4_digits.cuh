@@ -188,6 +188,79 @@ __device__ __forceinline__ void warm_digits(const Image &out) {
   write_digits<FMT>(out, 0, v, 0, 0, nullptr, 0, nullptr);
 }
 
+// Warps of a CTA that makes digits of x.
+template <int FMT>
+constexpr int kDigitWarps = FMT == 0 ? 4 : 8;
+
+// The CTA's W warps: the digits of token t, stages group * W and on, one a warp, places
+// by token.  NVFP4's factor needs the token's largest magnitude, which the CTA looks for
+// together (tops: W words of shared memory).
+template <int FMT, int W>
+__device__ __forceinline__ void token_digits(const Image &out, const void *x, int64_t ld_x,
+                                             int tokens, int64_t k, int t, int group,
+                                             uint32_t *tops, uint32_t *status) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t extent = (tokens - 1) * ld_x + k;
+  const auto load = [&](int64_t at) {
+    const int64_t off = t * ld_x + at;
+    return at < k && in_bounds(off, 8, extent, status)
+               ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(x) + off)
+               : make_uint4(0, 0, 0, 0);
+  };
+  // (its own part first: later loads queue behind the next kernel's first weights)
+  const int st = group * W + warp;
+  const uint4 q = load(static_cast<int64_t>(st) * kImageK + lane * 8);
+  int row_e = 0;
+  if constexpr (FMT == 1) {
+    // magnitudes compare as integers; one of 0x7F80 or more is no number and counts as 0
+    uint32_t top = 0;
+    for (int64_t at = threadIdx.x * 8; at < k; at += 8 * W * kImageK) {
+      uint4 u[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) u[i] = load(at + i * W * kImageK);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t m = w[j] & 0x7FFF7FFFu;
+          top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7F807F80u));
+        }
+      }
+    }
+    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < W; ++w) top = max(top, tops[w]);
+    __syncthreads();  // (before another call writes them)
+    row_e = row_exponent(__uint_as_float(top << 16));
+    if (group == 0 && threadIdx.x == 0) out.factors[t] = pow2(row_e);
+  }
+  if (static_cast<int64_t>(st) * kImageK >= k) return;
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+  write_digits<FMT>(out, st, v, row_e, 1, nullptr, t, nullptr);
+}
+
+// The images in the experts' workspace: codes of x, scales of x, codes of h, scales of
+// h.  Rows are pairs sorted by expert; of x, for so few tokens that all of them fit any
+// group, the tokens (moe_by_token).
+inline Image moe_image_of(const MoeArgs &a, bool of_h) {
+  const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
+  const bool by_token = !of_h && moe_by_token(a.tokens);
+  const int64_t rows = by_token ? a.tokens : pairs;
+  uint8_t *at = a.image + (of_h ? moe_image_bytes(pairs, a.hidden) : 0);
+  const int64_t stages = ((of_h ? a.inter : a.hidden) + kImageK - 1) / kImageK;
+  return Image{at, at + rows * stages * kImageCodes, a.factors + (of_h ? pairs : 0),
+               static_cast<int>(rows), by_token ? 1 : static_cast<int>(pairs)};
+}
+
 // ---------------------------------------------------------------- grid-wide counts
 // Kernels whose CTAs are resident together (a cooperative launch) count the CTAs
 // that have finished a part; a wait for the count is bounded all the same.

@@ -23,8 +23,6 @@ constexpr int kThreads = (2 + kEpilogue) * 32;
 constexpr int kSmem = 227 * 1024;
 constexpr int kMaxSlots = 12;
 constexpr int kTile = 128 * 128;  // bytes of a stage's weights
-template <int FMT>
-constexpr int kDigitWarps = FMT == 0 ? 4 : 8;
 
 struct Params {
   LinearArgs a;
@@ -37,67 +35,19 @@ struct Params {
   int b_off, sfa_off, sfb_off, bar_off;       // shared memory (the weights at 0)
 };
 
-// ---------------------------------------------------------------- digits of x
-// A warp takes 256 elements of a token; NVFP4's factor needs the token's largest
-// magnitude, which the CTA looks for together.
 template <int FMT>
 __global__ void __launch_bounds__(kDigitWarps<FMT> * 32) digits_kernel(const __grid_constant__ Params p) {
   __shared__ uint32_t tops[kDigitWarps<FMT>];
-  const LinearArgs &a = p.a;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y;
   warm_digits<FMT>(p.x);
   griddep_wait();
-  // After the wait: what the product copies before its own wait is then older than this
-  // kernel.
-  griddep_launch_dependents();
+  griddep_launch_dependents();  // after the wait: what the product copies before its own
+                                // wait is then older than this kernel
   const int cta = blockIdx.y * gridDim.x + blockIdx.x;
   for (int i = cta * blockDim.x + threadIdx.x; i < p.tiles; i += gridDim.x * gridDim.y * blockDim.x)
     p.counts[i] = 0;
-  const int64_t extent = (a.tokens - 1) * a.ld_x + a.k;
-  const auto load = [&](int64_t at) {
-    const int64_t off = t * a.ld_x + at;
-    return at < a.k && in_bounds(off, 8, extent, a.status)
-               ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off)
-               : make_uint4(0, 0, 0, 0);
-  };
-  // (its own part first: later loads queue behind the product's first weights)
-  const int st = blockIdx.x * kDigitWarps<FMT> + warp;
-  const uint4 q = load(static_cast<int64_t>(st) * kImageK + lane * 8);
-  int row_e = 0;
-  if constexpr (FMT == 1) {
-    // magnitudes compare as integers; one of 0x7F80 or more is no number and counts as 0
-    uint32_t top = 0;
-    for (int64_t at = threadIdx.x * 8; at < a.k; at += 8 * kDigitWarps<FMT> * kImageK) {
-      uint4 u[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) u[i] = load(at + i * kDigitWarps<FMT> * kImageK);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t m = w[j] & 0x7FFF7FFFu;
-          top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7F807F80u));
-        }
-      }
-    }
-    top = __reduce_max_sync(0xFFFFFFFFu, max(top & 0xFFFFu, top >> 16));
-    if (lane == 0) tops[warp] = top;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kDigitWarps<FMT>; ++w) top = max(top, tops[w]);
-    row_e = row_exponent(__uint_as_float(top << 16));
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.x.factors[t] = pow2(row_e);
-  }
-  if (st >= p.stages) return;
-  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-  write_digits<FMT>(p.x, st, v, row_e, 1, nullptr, t, nullptr);
+  const LinearArgs &a = p.a;
+  token_digits<FMT, kDigitWarps<FMT>>(p.x, a.x, a.ld_x, a.tokens, a.k, blockIdx.y, blockIdx.x, tops,
+                                      a.status);
 }
 
 // ---------------------------------------------------------------- the product

@@ -9,6 +9,7 @@
 // the CTA that owns the token, and one warp of it chooses.  Registers leave room for two
 // CTAs an SM: with one, seven clusters of 16 are resident and the eighth (64 tokens)
 // runs after them (64 x 8192 of 256: 14.9 us, so 11.0; 1 x 2048 of 64: 3.6 us, latency).
+#include "fp4_digits.cuh"
 #include "mx_device.cuh"
 #include "mx_internal.h"
 
@@ -95,15 +96,33 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32, 2) route_kernel(const RouteArgs a) {
+// What the experts' kernel that follows needs (fmt: -1 no digits).
+struct Next {
+  Image x;
+  int fmt;
+  uint32_t *counts;
+  int n_counts;
+};
+
+template <int FMT>
+__device__ __forceinline__ void next_digits(const RouteArgs &a, const Next &next, int worker,
+                                            int workers, uint32_t *tops) {
+  const int groups = (a.hidden + kWarps * kImageK - 1) / (kWarps * kImageK);
+  for (int i = worker; i < a.tokens * groups; i += workers)
+    token_digits<FMT, kWarps>(next.x, a.x, a.ld_x, a.tokens, a.hidden, i / groups, i % groups, tops,
+                              a.status);
+}
+
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ Next next) {
   __shared__ float red[kWarps][kRowTiles][4][32];
   __shared__ float logits[kMoeMaxExperts];  // of this CTA's token
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(cluster_ctarank()), t0 = static_cast<int>(cluster_id_x()) * kTokens;
-  if (a.counts != nullptr && blockIdx.x == 0)
-    for (int i = threadIdx.x; i < moe_counts(a.tokens * a.top_k); i += blockDim.x) a.counts[i] = 0;
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i < next.n_counts; i += blockDim.x) next.counts[i] = 0;
   const int rows = (a.experts + kCtas - 1) / kCtas, row0 = rank * rows;
   const int n_rows = min(rows, a.experts - row0);  // may be 0 or less
   const int blocks = a.hidden / 32;
@@ -154,12 +173,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2) route_kernel(const RouteArgs a
     st_cluster_f32(mapa_shared(smem_u32(&logits[row0 + row]), static_cast<uint32_t>(token)), s);
   }
   cluster_sync();
-  if (rank < kTokens && t0 + rank < a.tokens && warp == 0) choose(a, t0 + rank, logits);
+  if (rank < kTokens) {
+    if (t0 + rank < a.tokens && warp == 0) choose(a, t0 + rank, logits);
+  } else if (next.fmt >= 0) {
+    // (one cluster) the other CTAs make the digits of x meanwhile
+    uint32_t *tops = reinterpret_cast<uint32_t *>(logits);
+    if (next.fmt == 0)
+      next_digits<0>(a, next, rank - kTokens, kCtas - kTokens, tops);
+    else
+      next_digits<1>(a, next, rank - kTokens, kCtas - kTokens, tops);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s) {
+cudaError_t launch_moe_route(const RouteArgs &a, const MoeArgs *experts, cudaStream_t s) {
+  Next next{};
+  next.fmt = -1;
+  if (experts != nullptr) {
+    next.counts = experts->counts;
+    next.n_counts = moe_counts(a.tokens * a.top_k);
+    if (moe_by_token(a.tokens)) {
+      static_assert(!moe_by_token(kTokens + 1), "one cluster");
+      next.x = moe_image_of(*experts, false);
+      next.fmt = experts->fmt;
+    }
+  }
   const void *func = reinterpret_cast<const void *>(route_kernel);
   if (!kernel_setup_get(func, nullptr)) {
     const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
@@ -179,7 +218,7 @@ cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, route_kernel, a);
+  return cudaLaunchKernelEx(&cfg, route_kernel, a, next);
 }
 
 }  // namespace mx

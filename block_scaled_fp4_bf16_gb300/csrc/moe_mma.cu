@@ -103,6 +103,10 @@ __device__ __noinline__ float2 act(float2 v, int gelu) {
 template <int FMT, int NB>
 struct Expert {
   static constexpr int kGroup = 4 * NB;                 // pairs of a group at most
+  // The up product multiplies the digits of all tokens with any group's weights (its time
+  // does not depend on so few columns), and the epilogue takes the group's: the digits of x
+  // need no order then and are made before this kernel.
+  static constexpr bool kByToken = moe_by_token(kGroup);
   static constexpr int kAtoms = FMT == 0 ? 2 : 4;       // scale tiles (4 blocks) of a stage
   static constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
   static constexpr int kSfaCols = kAtoms * 4;
@@ -154,7 +158,7 @@ struct Expert {
     // bytes of scales, of one matrix; those of the second stage follow the first's
     const uint32_t bytes = static_cast<uint32_t>(min(n * kAtoms, katoms - st * kAtoms)) * 512u;
     mbar_arrive_expect_tx(fb, (UP ? 2 : n) * kTile + (UP ? 2 : 1) * bytes +
-                                  n * (g.size[im.grp] * kImageCodes + kSfb));
+                                  n * (images<UP>(im.grp) * kImageCodes + kSfb));
     tma_load_2d(w, m0, st * 128, row, fb);
     bulk_load(sf, (UP ? a.gate.scales : a.down.scales) + off, bytes, fb);
     if constexpr (UP) {
@@ -164,9 +168,20 @@ struct Expert {
       tma_load_2d(w + kTile, m0, (st + 1) * 128, row, fb);
     }
   }
+  template <bool UP>
+  __device__ __forceinline__ int images(int grp) const {  // rows of images of a stage
+    return UP && kByToken ? p.a.tokens : g.size[grp];
+  }
+  template <bool UP>
   __device__ __forceinline__ void copy_images(const Image &im, int grp, int st, uint32_t slot, int n) {
-    const uint32_t fb = smem_u32(&full[slot]), size = g.size[grp] * kImageCodes;
+    const uint32_t fb = smem_u32(&full[slot]), size = images<UP>(grp) * kImageCodes;
     const uint32_t b = smem_u32(smem + p.b_off) + slot * kGroup * kImageCodes;
+    if (UP && kByToken) {
+      bulk_load(b, im.codes + static_cast<int64_t>(st) * size, size, fb);
+      bulk_load(smem_u32(smem + p.sfb_off) + slot * kSfb, im.scales + static_cast<int64_t>(st) * kSfb,
+                kSfb, fb);
+      return;
+    }
     const int64_t at = static_cast<int64_t>(st) * pairs;
     bulk_load(b, im.codes + (at + g.begin[grp]) * kImageCodes, size, fb);
     bulk_load(smem_u32(smem + p.sfb_off) + slot * kSfb, im.scales + (at + grp) * kSfb, kSfb, fb);
@@ -191,7 +206,7 @@ struct Expert {
         if (there <= 0) return there == 0;
         const int by = span<UP>(old.grp);
         for (; late > 0 && late_st < old.st1; --late, late_st += by) {
-          if (elect_one()) copy_images(im, old.grp, late_st, late_slot, min(by, old.st1 - late_st));
+          if (elect_one()) copy_images<UP>(im, old.grp, late_st, late_slot, min(by, old.st1 - late_st));
           __syncwarp();
           if (++late_slot == static_cast<uint32_t>(p.slots)) late_slot = 0;
         }
@@ -227,8 +242,8 @@ struct Expert {
     const int katoms = (d.k / (FMT == 0 ? 32 : 16) + 3) >> 2;
     for (int item = d.begin; item < d.end; item += d.step) {
       const typename Product<UP>::Item im = d.at(item);
-      // columns: the digits of the group, to a multiple of 16
-      const uint32_t columns = static_cast<uint32_t>(g.size[im.grp] * kDigits + 15) & ~15u;
+      // columns: the digits, to a multiple of 16
+      const uint32_t columns = static_cast<uint32_t>(images<UP>(im.grp) * kDigits + 15) & ~15u;
       const uint32_t idesc0 = mma_idesc<FMT>(128, columns, 0);
       const uint32_t idesc2 = mma_idesc<FMT>(128, columns, 2);
       if (!mbar_wait_warp(smem_u32(&acc_empty[buf]), bph ^ 1u, abort, p.a.status)) return false;
@@ -350,10 +365,14 @@ struct Expert {
           const int c = i * 4 + j;
           if (c >= n || row >= d.rows) continue;
           const int place = g.begin[im.grp] + c;
-          const float f = FMT == 1 ? __ldcg(factors + place) : 1.0f;
+          const bool by_token = UP && kByToken;
+          const int at = by_token ? g.list[place] / a.top_k : place;
+          const float f = FMT == 1 ? __ldcg(factors + at) : 1.0f;
 #pragma unroll
           for (int m = 0; m < kSegs; ++m) {
-            const float v = FMT == 1 ? sum[m][j] * f * (m == 0 ? alpha0 : alpha1) : sum[m][j];
+            float v = sum[m][j];
+            if (by_token) v = at == 0 ? sum[m][0] : at == 1 ? sum[m][1] : at == 2 ? sum[m][2] : sum[m][3];
+            if (FMT == 1) v *= f * (m == 0 ? alpha0 : alpha1);
             const int64_t o = (static_cast<int64_t>(im.part * kSegs + m) * pairs +
                                (UP ? place : g.list[place])) * d.rows + row;
             if (in_bounds(o, 1, extent, a.status)) (UP ? a.h : a.z)[o] = v;
@@ -644,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (act(make_float2(0.0f, 0.0f), a.gelu).x != 0.0f) atomicOr(a.status, kStatusTimeout);
   }
   griddep_wait();
-  x.fetch_x();
+  if constexpr (!X::kByToken) x.fetch_x();
   // (the scratch lies in the ring: a fence and a barrier before the first copy)
   make_groups<kThreads / 32>(x.g, x.places, x.members, smem, a.ids, x.pairs, a.experts, X::kGroup,
                              a.status);
@@ -657,7 +676,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     // the digits of x are there when every CTA has counted them
-    int x_there = 0;
+    int x_there = X::kByToken ? 1 : 0;
+    if (X::kByToken) asm volatile("fence.proxy.async;" ::: "memory");
     const auto x_ready = [&](int, int how) {
       if (x_there == 0 && how == kWait) {
         const bool r = count_reached(a.counts + kCountX, gridDim.x, x.abort, a.status);
@@ -704,8 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const auto wait = [&](int i) {
       return all_counted(a.counts + i, kWorkers * 32, leader, flag, x.abort, a.status);
     };
-    x.split_x();
-    add(kCountX);
+    if constexpr (!X::kByToken) {
+      x.split_x();
+      add(kCountX);
+    }
     if (epilogue) {
       // (the factors it reads were counted before the products that it waits for)
       x.template epilogue<true>(up, p.x.factors);
@@ -725,20 +747,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// Clears the counts (mx_moe_layer_bf16's router does it there).
-__global__ void __launch_bounds__(256) clear_kernel(uint32_t *counts, int n) {
+// What mx_moe_layer_bf16's router does there.
+template <int FMT>
+__global__ void __launch_bounds__(kDigitWarps<FMT> * 32)
+    prepare_kernel(const __grid_constant__ MoeArgs a, const __grid_constant__ Image x, int n_counts,
+                   int by_token) {
+  __shared__ uint32_t tops[kDigitWarps<FMT>];
   griddep_launch_dependents();
+  if (by_token) warm_digits<FMT>(x);
   griddep_wait();
-  for (int i = threadIdx.x; i < n; i += 256) counts[i] = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < n_counts; i += kDigitWarps<FMT> * 32) a.counts[i] = 0;
+  if (by_token)
+    token_digits<FMT, kDigitWarps<FMT>>(x, a.x, a.ld_x, a.tokens, a.hidden, blockIdx.y, blockIdx.x,
+                                        tops, a.status);
 }
 
-// The images in the workspace: codes of x, scales of x, codes of h, scales of h.
-Image image_of(const MoeArgs &a, bool of_h) {
-  const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
-  uint8_t *at = a.image + (of_h ? moe_image_bytes(pairs, a.hidden) : 0);
-  const int64_t stages = ((of_h ? a.inter : a.hidden) + kImageK - 1) / kImageK;
-  return Image{at, at + pairs * stages * kImageCodes, a.factors + (of_h ? pairs : 0),
-               static_cast<int>(pairs), static_cast<int>(pairs)};
+template <int FMT>
+cudaError_t launch_prepare(const MoeArgs &a, cudaStream_t s) {
+  const bool by_token = moe_by_token(a.tokens);
+  constexpr int k = kDigitWarps<FMT> * kImageK;
+  const dim3 grid(by_token ? static_cast<unsigned>((a.hidden + k - 1) / k) : 1u,
+                  by_token ? static_cast<unsigned>(a.tokens) : 1u);
+  return launch_pdl(prepare_kernel<FMT>, grid, dim3(kDigitWarps<FMT> * 32), 0, s, a,
+                    moe_image_of(a, false), moe_counts(a.tokens * a.top_k), by_token ? 1 : 0);
 }
 
 template <int FMT, int NB>
@@ -755,8 +787,8 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   const int pairs = a.tokens * a.top_k;
   ExpertParams p{};
   p.a = a;
-  p.x = image_of(a, false);
-  p.h = image_of(a, true);
+  p.x = moe_image_of(a, false);
+  p.h = moe_image_of(a, true);
   constexpr int per_slot = 2 * (kTile + X::kSfa) + X::kGroup * kImageCodes + X::kSfb;
   const int groups = Groups::bytes(pairs) + 4 * pairs;
   int slots = (kSmem - 512 - groups) / per_slot;
@@ -823,9 +855,8 @@ int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_s
   return parts;
 }
 
-cudaError_t launch_moe_clear(const MoeArgs &a, cudaStream_t s) {
-  return launch_pdl(clear_kernel, dim3(1), dim3(256), 0, s, a.counts,
-                    moe_counts(a.tokens * a.top_k));
+cudaError_t launch_moe_prepare(const MoeArgs &a, cudaStream_t s) {
+  return a.fmt == 0 ? launch_prepare<0>(a, s) : launch_prepare<1>(a, s);
 }
 
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s) {

@@ -230,10 +230,11 @@ struct RouteArgs {
   const float *bias;
   int32_t *ids;
   float *weights;
-  uint32_t *counts;  // the experts' counts, to be cleared (null: none)
   uint32_t *status;
 };
-cudaError_t launch_moe_route(const RouteArgs &a, cudaStream_t s);
+// next: the experts' call that follows (null: none), for which it does launch_moe_prepare.
+struct MoeArgs;
+cudaError_t launch_moe_route(const RouteArgs &a, const MoeArgs *next, cudaStream_t s);
 
 struct MoeArgs {
   const void *x;
@@ -261,7 +262,11 @@ constexpr int moe_counts(int pairs) { return 2 + 2 * pairs; }
 // Ranges of K that a product is divided into, and the most for a number of pairs.
 int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms);
 constexpr int moe_max_parts(int64_t pairs) { return pairs <= 16 ? 4 : pairs <= 64 ? 2 : 1; }
-cudaError_t launch_moe_clear(const MoeArgs &a, cudaStream_t s);  // a.counts
+// Whether the digits of x are made by the launch before the experts' kernel, in the
+// order of the tokens (4: the tokens of a group at most then).
+constexpr bool moe_by_token(int tokens) { return tokens <= 4; }
+// Clears a.counts, and makes the digits of x if moe_by_token.
+cudaError_t launch_moe_prepare(const MoeArgs &a, cudaStream_t s);
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
 
 // Launch with programmatic stream serialization (the kernel itself orders
