@@ -253,7 +253,7 @@ __device__ __forceinline__ void token_digits(const Image &out, const void *x, in
 // group, the tokens (moe_by_token).
 inline Image moe_image_of(const MoeArgs &a, bool of_h) {
   const int64_t pairs = static_cast<int64_t>(a.tokens) * a.top_k;
-  const bool by_token = !of_h && moe_by_token(a.tokens);
+  const bool by_token = !of_h && moe_by_token(a.fmt, a.tokens);
   const int64_t rows = by_token ? a.tokens : pairs;
   uint8_t *at = a.image + (of_h ? moe_image_bytes(pairs, a.hidden) : 0);
   const int64_t stages = ((of_h ? a.inter : a.hidden) + kImageK - 1) / kImageK;

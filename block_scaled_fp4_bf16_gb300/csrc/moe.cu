@@ -96,22 +96,14 @@ __device__ __forceinline__ void choose(const RouteArgs &a, int t, const float *l
   }
 }
 
-// What the experts' kernel that follows needs (fmt: -1 no digits).
+// What the experts' kernel that follows needs (digits: of x, of the one format that
+// moe_by_token has).
 struct Next {
   Image x;
-  int fmt;
+  int digits;
   uint32_t *counts;
   int n_counts;
 };
-
-template <int FMT>
-__device__ __forceinline__ void next_digits(const RouteArgs &a, const Next &next, int worker,
-                                            int workers, uint32_t *tops) {
-  const int groups = (a.hidden + kWarps * kImageK - 1) / (kWarps * kImageK);
-  for (int i = worker; i < a.tokens * groups; i += workers)
-    token_digits<FMT, kWarps>(next.x, a.x, a.ld_x, a.tokens, a.hidden, i / groups, i % groups, tops,
-                              a.status);
-}
 
 __global__ void __launch_bounds__(kWarps * 32, 2)
     route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ Next next) {
@@ -175,13 +167,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   cluster_sync();
   if (rank < kTokens) {
     if (t0 + rank < a.tokens && warp == 0) choose(a, t0 + rank, logits);
-  } else if (next.fmt >= 0) {
+  } else if (next.digits) {
     // (one cluster) the other CTAs make the digits of x meanwhile
-    uint32_t *tops = reinterpret_cast<uint32_t *>(logits);
-    if (next.fmt == 0)
-      next_digits<0>(a, next, rank - kTokens, kCtas - kTokens, tops);
-    else
-      next_digits<1>(a, next, rank - kTokens, kCtas - kTokens, tops);
+    static_assert(!moe_by_token(1, 1), "MXFP4");
+    const int groups = (a.hidden + kWarps * kImageK - 1) / (kWarps * kImageK);
+    for (int i = rank - kTokens; i < a.tokens * groups; i += kCtas - kTokens)
+      token_digits<0, kWarps>(next.x, a.x, a.ld_x, a.tokens, a.hidden, i / groups, i % groups, nullptr,
+                              a.status);
   }
 }
 
@@ -189,14 +181,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 
 cudaError_t launch_moe_route(const RouteArgs &a, const MoeArgs *experts, cudaStream_t s) {
   Next next{};
-  next.fmt = -1;
   if (experts != nullptr) {
     next.counts = experts->counts;
     next.n_counts = moe_counts(a.tokens * a.top_k);
-    if (moe_by_token(a.tokens)) {
-      static_assert(!moe_by_token(kTokens + 1), "one cluster");
+    if (moe_by_token(experts->fmt, a.tokens)) {
+      static_assert(!moe_by_token(0, kTokens + 1), "one cluster");
       next.x = moe_image_of(*experts, false);
-      next.fmt = experts->fmt;
+      next.digits = 1;
     }
   }
   const void *func = reinterpret_cast<const void *>(route_kernel);

@@ -106,7 +106,7 @@ struct Expert {
   // The up product multiplies the digits of all tokens with any group's weights (its time
   // does not depend on so few columns), and the epilogue takes the group's: the digits of x
   // need no order then and are made before this kernel.
-  static constexpr bool kByToken = moe_by_token(kGroup);
+  static constexpr bool kByToken = moe_by_token(FMT, kGroup);
   static constexpr int kAtoms = FMT == 0 ? 2 : 4;       // scale tiles (4 blocks) of a stage
   static constexpr int kSfa = kAtoms * 512;             // bytes, of one matrix
   static constexpr int kSfaCols = kAtoms * 4;
@@ -325,6 +325,7 @@ struct Expert {
   template <bool UP>
   __device__ __forceinline__ void epilogue(const Product<UP> &d, const float *factors) {
     constexpr int kSegs = Product<UP>::kSegs;
+    constexpr bool by_token = UP && kByToken;
     const MoeArgs &a = p.a;
     const int q = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
     const int64_t extent = static_cast<int64_t>(d.parts) * kSegs * pairs * d.rows;
@@ -338,7 +339,16 @@ struct Expert {
       ok = ok && mbar_wait_warp(smem_u32(&acc_full[buf]), bph, abort, a.status);
       tc_fence_after();
       const uint32_t acc = tmem + buf * kAccCols + (static_cast<uint32_t>(q * 32) << 16);
-      for (int i = 0; ok && i < (n + 3) / 4; ++i) {
+      // lane c has column block c's factor
+      float factor = 1.0f;
+      if (FMT == 1 && ok && lane < images<UP>(im.grp))
+        factor = __ldcg(factors + (by_token ? lane : g.begin[im.grp] + lane));
+      const auto put = [&](int m, int place, float v) {
+        const int64_t o = (static_cast<int64_t>(im.part * kSegs + m) * pairs +
+                           (UP ? place : g.list[place])) * d.rows + row;
+        if (in_bounds(o, 1, extent, a.status)) (UP ? a.h : a.z)[o] = v;
+      };
+      for (int i = 0; ok && i < (images<UP>(im.grp) + 3) / 4; ++i) {
         float sum[kSegs][4];
 #pragma unroll
         for (int m = 0; m < kSegs; ++m) {
@@ -357,25 +367,26 @@ struct Expert {
               else
                 t = __fmaf_rn(v, 1.0f / static_cast<float>(1 << digit_shift(dg)), t);
             }
+            if (FMT == 1) t *= __shfl_sync(0xFFFFFFFFu, factor, i * 4 + j) * (m == 0 ? alpha0 : alpha1);
             sum[m][j] = t;
           }
         }
+        if (row >= d.rows) continue;
+        if constexpr (by_token) {
+          for (int c = 0; c < n; ++c) {
+            const int place = g.begin[im.grp] + c, t = g.list[place] / a.top_k;
+            if (t >> 2 != i) continue;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int c = i * 4 + j;
-          if (c >= n || row >= d.rows) continue;
-          const int place = g.begin[im.grp] + c;
-          const bool by_token = UP && kByToken;
-          const int at = by_token ? g.list[place] / a.top_k : place;
-          const float f = FMT == 1 ? __ldcg(factors + at) : 1.0f;
+            for (int m = 0; m < kSegs; ++m)
+              put(m, place, (t & 2) != 0 ? (t & 1) != 0 ? sum[m][3] : sum[m][2]
+                                         : (t & 1) != 0 ? sum[m][1] : sum[m][0]);
+          }
+        } else {
 #pragma unroll
-          for (int m = 0; m < kSegs; ++m) {
-            float v = sum[m][j];
-            if (by_token) v = at == 0 ? sum[m][0] : at == 1 ? sum[m][1] : at == 2 ? sum[m][2] : sum[m][3];
-            if (FMT == 1) v *= f * (m == 0 ? alpha0 : alpha1);
-            const int64_t o = (static_cast<int64_t>(im.part * kSegs + m) * pairs +
-                               (UP ? place : g.list[place])) * d.rows + row;
-            if (in_bounds(o, 1, extent, a.status)) (UP ? a.h : a.z)[o] = v;
+          for (int j = 0; j < 4; ++j) {
+            if (i * 4 + j >= n) break;
+#pragma unroll
+            for (int m = 0; m < kSegs; ++m) put(m, g.begin[im.grp] + i * 4 + j, sum[m][j]);
           }
         }
       }
@@ -754,18 +765,19 @@ __global__ void __launch_bounds__(kDigitWarps<FMT> * 32)
                    int by_token) {
   __shared__ uint32_t tops[kDigitWarps<FMT>];
   griddep_launch_dependents();
-  if (by_token) warm_digits<FMT>(x);
+  constexpr bool some = moe_by_token(FMT, 1);
+  if (some && by_token) warm_digits<FMT>(x);
   griddep_wait();
   if (blockIdx.x == 0 && blockIdx.y == 0)
     for (int i = threadIdx.x; i < n_counts; i += kDigitWarps<FMT> * 32) a.counts[i] = 0;
-  if (by_token)
+  if (some && by_token)
     token_digits<FMT, kDigitWarps<FMT>>(x, a.x, a.ld_x, a.tokens, a.hidden, blockIdx.y, blockIdx.x,
                                         tops, a.status);
 }
 
 template <int FMT>
 cudaError_t launch_prepare(const MoeArgs &a, cudaStream_t s) {
-  const bool by_token = moe_by_token(a.tokens);
+  const bool by_token = moe_by_token(FMT, a.tokens);
   constexpr int k = kDigitWarps<FMT> * kImageK;
   const dim3 grid(by_token ? static_cast<unsigned>((a.hidden + k - 1) / k) : 1u,
                   by_token ? static_cast<unsigned>(a.tokens) : 1u);

@@ -263,8 +263,11 @@ constexpr int moe_counts(int pairs) { return 2 + 2 * pairs; }
 int moe_parts(int64_t pairs, int64_t experts, int64_t rows, int64_t k, int num_sms);
 constexpr int moe_max_parts(int64_t pairs) { return pairs <= 16 ? 4 : pairs <= 64 ? 2 : 1; }
 // Whether the digits of x are made by the launch before the experts' kernel, in the
-// order of the tokens (4: the tokens of a group at most then).
-constexpr bool moe_by_token(int tokens) { return tokens <= 4; }
+// order of the tokens: MXFP4 and few tokens (us, so and in that kernel: 4 x 2048 x 1024 of
+// 64 27.8 / 29.8, 1 x 8192 x 4096 of 8 29.3 / 32.4; but 8 x 4096 x 2048 76.1 / 71.3, where
+// all tokens' digits cost more than a group's, and NVFP4, whose factor takes that launch
+// 2 us, 4 x 4096 x 2048 of 8 35.7 / 32.2).
+constexpr bool moe_by_token(int fmt, int tokens) { return fmt == 0 && tokens <= 4; }
 // Clears a.counts, and makes the digits of x if moe_by_token.
 cudaError_t launch_moe_prepare(const MoeArgs &a, cudaStream_t s);
 cudaError_t launch_moe_experts(const MoeArgs &a, cudaStream_t s);
