@@ -6,6 +6,9 @@
 //   - an item is R = 16 MT weight rows; the CTA's warps divide K, each walks its range
 //     in stages of 128 that come by cp.async into a ring of its own, over the end
 //     of one item into the next; the warps meet only to add their sums;
+//   - with fewer items than SMs the CTAs of a cluster divide K and add their sums
+//     through each other's shared memory (1 x 1024 x 8192: 7.3 us, so 4.8; 13 x 1312 x
+//     25408 NVFP4 31.7 us, so 14.5);
 //   - E2M1 becomes FP16 by the conversion instruction, two codes at once, and
 //     multiplies on the 16 x 8 x 16 FP16 product with binary32 sums, the weights on
 //     its 16-row side (measured: 90 codes a clock per SM converted, 128 multiplied);
@@ -303,9 +306,20 @@ __device__ __forceinline__ void stage_product(uint32_t st, int count, float (&to
   }
 }
 
+constexpr int kMaxCtas = 8;  // of a cluster
+
+// CTAs of a cluster for `tiles` tiles: at least two stages a warp.
+int cluster_ctas(int warps, int64_t tiles, int64_t k, int num_sms) {
+  const int64_t stages = (k + kStageK - 1) / kStageK;
+  int64_t c = num_sms / tiles;
+  if (c > stages / (2 * warps)) c = stages / (2 * warps);
+  return static_cast<int>(c < 1 ? 1 : c > kMaxCtas ? kMaxCtas : c);
+}
+
 struct LinearParams {
   LinearArgs a;
   int tiles;  // row tiles of 16 MT rows
+  int ctas;   // of a cluster
 };
 
 // Persistent over row tiles: tile blockIdx.x, + gridDim.x, ...  Each of the W
@@ -321,17 +335,20 @@ __global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p)
   float4 *red = reinterpret_cast<float4 *>(smem);
   const uint32_t ring = smem_u32(smem) + W * kUnits * 16 + warp * S * stage_size;
   const int all = static_cast<int>((a.k + kStageK - 1) / kStageK);
-  const int s_begin = static_cast<int>(static_cast<int64_t>(all) * warp / W);
-  const int s_end = static_cast<int>(static_cast<int64_t>(all) * (warp + 1) / W);
+  const int rank = p.ctas > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int first_tile = blockIdx.x / p.ctas, tile_step = gridDim.x / p.ctas;
+  const int share = rank * W + warp, shares = p.ctas * W;  // of K
+  const int s_begin = static_cast<int>(static_cast<int64_t>(all) * share / shares);
+  const int s_end = static_cast<int>(static_cast<int64_t>(all) * (share + 1) / shares);
 
   // the copies' place: tile and stage, ahead of the product's
-  int ptile = blockIdx.x, ps = s_begin, pslot = 0;
+  int ptile = first_tile, ps = s_begin, pslot = 0;
   const auto issue = [&]() {
     if (s_begin < s_end && ptile < p.tiles) {
       const uint32_t dst = ring + pslot * stage_size;
       load_weights<FMT, MT>(dst, a, static_cast<int64_t>(ptile) * R, ps);
       load_x(dst + R * (64 + (FMT == 0 ? 4 : 8)), a, ps);
-      if (++ps == s_end) ps = s_begin, ptile += gridDim.x;
+      if (++ps == s_end) ps = s_begin, ptile += tile_step;
       if (++pslot == S) pslot = 0;
     }
     cp_async_commit();
@@ -342,7 +359,7 @@ __global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p)
   for (int i = 0; i < S - 1; ++i) issue();
   const float alpha = FMT == 1 ? *a.w.ts : 1.0f;
   int slot = 0;
-  for (int tile = blockIdx.x; tile < p.tiles; tile += gridDim.x) {
+  for (int tile = first_tile; tile < p.tiles; tile += tile_step) {
     float total[MT][NT][4] = {};
     for (int s = s_begin; s < s_end; ++s) {
       cp_async_wait<S - 2>();
@@ -361,12 +378,20 @@ __global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p)
             make_float4(total[m][n][0], total[m][n][1], total[m][n][2], total[m][n][3]);
     }
     __syncthreads();
-    for (int u = threadIdx.x; u < kUnits; u += W * 32) {
-      float4 v = red[u];
+    if (p.ctas > 1) cluster_sync();
+    // (of a cluster each CTA takes a part of the outputs)
+    for (int u = threadIdx.x * p.ctas + rank; u < kUnits; u += W * 32 * p.ctas) {
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c = 0; c < p.ctas; ++c) {
+        float4 o[W];
 #pragma unroll
-      for (int w = 1; w < W; ++w) {
-        const float4 o = red[w * kUnits + u];
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+        for (int w = 0; w < W; ++w) {
+          const float4 *from = red + w * kUnits + u;
+          o[w] = p.ctas > 1 ? ld_cluster_f32x4(mapa_shared(smem_u32(from), static_cast<uint32_t>(c)))
+                            : *from;
+        }
+#pragma unroll
+        for (int w = 0; w < W; ++w) v.x += o[w].x, v.y += o[w].y, v.z += o[w].z, v.w += o[w].w;
       }
       const int ul = u & 31, mn = u >> 5;
       const int64_t row0 = static_cast<int64_t>(tile) * R + (mn / NT) * 16 + (ul >> 2);
@@ -379,7 +404,10 @@ __global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p)
         if (row < a.n && col < a.tokens) put_linear(a, row, col, FMT == 1 ? f[i] * alpha : f[i]);
       }
     }
-    __syncthreads();
+    if (p.ctas > 1)
+      cluster_sync();
+    else
+      __syncthreads();
   }
 }
 
@@ -393,38 +421,80 @@ cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kernel_setup_put(func, 0);
   }
-  const LinearParams p{a, static_cast<int>((a.n + 16 * MT - 1) / (16 * MT))};
   size_t smem = W * MT * NT * 512 + static_cast<size_t>(W) * S * stage_bytes<FMT, MT>(a.tokens);
   // One CTA an SM: two on one, launched while the kernel before it still holds the
   // others, share what one SM can do (1 x 4096 x 8192: 11.9 us, so 8.0).
   if (smem <= kMaxSmem / 2) smem = kMaxSmem / 2 + 1024;
-  const int grid = p.tiles < a.num_sms ? p.tiles : a.num_sms;
-  return launch_pdl(kernel, dim3(grid), dim3(W * 32), smem, s, p);
+  LinearParams p{a, static_cast<int>((a.n + 16 * MT - 1) / (16 * MT)), 1};
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.blockDim = dim3(W * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  // Fewer tiles than SMs: the CTAs of a cluster divide K, so many as leave every tile a
+  // cluster at once (a cluster lies within a part of the GPU: fewer fit than SMs / CTAs).
+  for (p.ctas = cluster_ctas(W, p.tiles, a.k, a.num_sms); p.ctas > 1; --p.ctas) {
+    static const char keys[kMaxCtas + 1] = {};  // their addresses name the instance and count
+    int fit = 0;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.ctas);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.ctas));
+    cfg.numAttrs = 2;
+    if (!kernel_setup_get(&keys[p.ctas], &fit)) {
+      // (the most shared memory the instance can ask for, so that the answer holds)
+      cfg.dynamicSmemBytes = kMaxSmem;
+      const cudaError_t e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
+      if (e != cudaSuccess) return e;
+      cfg.dynamicSmemBytes = smem;
+      kernel_setup_put(&keys[p.ctas], fit);
+    }
+    if (fit >= p.tiles) break;
+  }
+  const int clusters = p.tiles < a.num_sms ? p.tiles : a.num_sms;
+  cfg.gridDim = dim3(static_cast<unsigned>(clusters * p.ctas));
+  cfg.numAttrs = p.ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-// Rows of an item and depth of the rings: 64 rows where every SM gets one, else 32
-// (measured, MXFP4: 1 x 28672 x 8192 29.8 us; 8 x 4096 x 4096 4.8 us).
+// Rows of an item: 64 where every SM gets one, else 32.
+bool tall_items(int64_t tokens, int64_t n, int num_sms) {
+  return tokens <= 16 && n >= 64 * static_cast<int64_t>(num_sms);
+}
+
+// Warps and depth of the rings: what shared memory holds.
 template <int FMT>
 cudaError_t launch_fmt(const LinearArgs &a, cudaStream_t s) {
-  const bool small = a.n < 64 * static_cast<int64_t>(a.num_sms);
-  if (a.tokens <= 8) return small ? launch<FMT, 2, 1, 8, 4>(a, s) : launch<FMT, 4, 1, 8, 3>(a, s);
-  if (a.tokens <= 16) return small ? launch<FMT, 2, 2, 8, 3>(a, s) : launch<FMT, 4, 2, 8, 2>(a, s);
+  const bool tall = tall_items(a.tokens, a.n, a.num_sms);
+  if (a.tokens <= 8) return tall ? launch<FMT, 4, 1, 8, 3>(a, s) : launch<FMT, 2, 1, 8, 4>(a, s);
+  if (a.tokens <= 16) return tall ? launch<FMT, 4, 2, 8, 2>(a, s) : launch<FMT, 2, 2, 8, 3>(a, s);
   return launch<FMT, 2, 4, 6, 2>(a, s);
 }
 
 }  // namespace
 
-// Which is the faster, by the number of weights (us, this kernel / linear_mma.cu's;
-// a token's digits cost the latter little, its two launches about 9 us):
-//                      4096 x 4096   8192 x 4096   8192 x 8192   28672 x 8192
-//   MXFP4   8 tokens:   4.9 / 11.2    8.7 / 13.0   15.1 / 15.1    31.9 / 25.2
-//          16 tokens:   6.6 / 13.3   12.0 / 14.9   21.3 / 16.6    45.1 / 26.3
-//          32 tokens:  12.2 / 17.7   23.2 / 18.0   43.5 / 20.8   126.1 / 33.0
-//   NVFP4   8 tokens:   5.2 / 11.5    9.4 / 13.3   16.5 / 15.3    36.1 / 26.5
-//          32 tokens:  11.9 / 18.7   22.6 / 18.9   42.1 / 22.1   122.0 / 35.2
+// Which is the faster, by the weights that an SM's share of this kernel's grid has (with
+// the rows and SMs that the last round of items leaves idle), times the 152 SMs: it takes
+// 0.2 us for 2^20 of them up to 8 tokens, 0.3 up to 16, 0.55 above; linear_mma.cu's two
+// launches take 9 to 12 us and then 6 TB/s.  Measured (us, this kernel / that one):
+//                      4096 x 4096   8192 x 4096   8192 x 8192   28672 x 8192   3360 x 19552
+//   (2^20 weights            19            38            76            228            91)
+//   MXFP4   8 tokens:   4.9 /  9.9    8.7 / 13.0   15.1 / 15.1    31.9 / 25.4    17.6 / 14.3
+//          16 tokens:   6.6 / 11.8   12.0 / 14.9   21.3 / 16.6    45.1 / 26.7
+//          32 tokens:  12.4 / 14.8   23.2 / 18.0   43.5 / 20.1   126.1 / 32.8
+//   NVFP4   8 tokens:   5.2 / 10.8    9.4 / 13.3   16.5 / 15.3    36.1 / 27.3    19.1 / 15.7
+//          32 tokens:  12.1 / 14.7   22.6 / 18.9   42.1 / 20.0   122.0 / 35.8
 bool linear_mma_better(int64_t tokens, int64_t n, int64_t k) {
-  const int64_t least = tokens <= 8 ? 64 : tokens <= 16 ? 48 : 28;
-  return n * k >= least << 20;
+  constexpr int kSms = 152;
+  const int64_t rows = tall_items(tokens, n, kSms) ? 64 : 32, tiles = (n + rows - 1) / rows;
+  const int64_t ctas = cluster_ctas(tokens <= 16 ? 8 : 6, tiles, k, kSms);
+  const int64_t rounds = ctas > 1 ? 1 : (tiles + kSms - 1) / kSms;
+  const int64_t least = tokens <= 8 ? 72 : tokens <= 16 ? 50 : 28;
+  return rounds * rows * kSms * k / ctas >= least << 20;
 }
 
 cudaError_t launch_linear(const LinearArgs &a, cudaStream_t s) {

@@ -3,7 +3,8 @@ against the formula in binary64, on a sample of the rows.
 
 Tolerance, FP32 out: E = 1e-5 sum_k |x||w| (the accumulation bound of the GEMM tests)
 + 2^-22 sum over blocks (32 of K for MXFP4, 16 for NVFP4) of (max |x| of the block)
-(sum |w|) (what eight FP4 digits lose of an element far below its block's largest)
+(sum |w|) (what eight FP4 digits lose of an element far below its block's largest; the
+sizes without a workspace lose less)
 + 2^-39 (max |x| of the token) (sum |w|) (NVFP4: the least E4M3 scale).  BF16 out:
 plus one BF16 ulp.  With an epilogue as in the tests of the smaller sizes.
 """
@@ -52,8 +53,7 @@ def run(bits, w, out_fp32=True, ld_x=None, ld_y=None, bias=None, beta=0.0, gelu_
     if y_in is not None:
         y[:, :w.n] = y_in
     need = mx.mx_linear_workspace_bytes(t, k, w.n, w.fmt)
-    assert need > 0, "a size for the other kernel"
-    ws = guarded(need, torch.uint8, 0xA5)
+    ws = guarded(max(need, 1), torch.uint8, 0xA5)  # (unused where need is 0)
     mx.mx_linear_bf16(strided(bits, ld_x), t, k, ld_x, w.fmt, w.codes, w.scales, w.ts, w.n, y, ld_y,
                       mx.MX_OUT_FP32 if out_fp32 else mx.MX_OUT_BF16, bias, beta, gelu_on, workspace=ws)
     torch.cuda.synchronize()
@@ -78,8 +78,16 @@ def reference(bits, w):
     return x @ v.T, tol
 
 
-SIZES = [(1, 8224, 8224), (4, 2336, 28768), (5, 65568, 1056), (8, 2097152 + 32, 32), (9, 1600, 31520),
-         (16, 12320, 4128), (17, 1056, 27872), (31, 8224, 3616), (32, 96, 309600)]
+# with a workspace (the first nine), and without it
+SIZES = [(1, 8224, 8224), (4, 2464, 28768), (5, 75808, 1056), (8, 2424832 + 32, 32), (9, 2496, 31520),
+         (16, 12320, 4128), (17, 1056, 27872), (31, 8224, 3616), (32, 96, 309600),
+         (4, 2336, 28768), (5, 65568, 1056), (8, 2097152 + 32, 32), (9, 1600, 31520), (13, 1312, 25408),
+         (32, 96, 16384), (7, 32, 12320)]
+
+
+def test_which_sizes_take_a_workspace():
+    assert all(mx.mx_linear_workspace_bytes(t, k, n, fmt) > 0 for t, n, k in SIZES[:9] for fmt in FMTS)
+    assert all(mx.mx_linear_workspace_bytes(t, k, n, fmt) == 0 for t, n, k in SIZES[9:] for fmt in FMTS)
 
 
 @pytest.mark.parametrize("fmt", FMTS)
