@@ -181,11 +181,7 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(x):
     """Device address of a tensor / int / None (NULL)."""
-    if x is None:
-        return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    return x if x is None or isinstance(x, int) else x.data_ptr()
 
 
 def _nbytes(x) -> int:
@@ -394,21 +390,21 @@ def mx_linear_bf16(x, tokens, k, ld_x, fmt, w_codes, w_scales, w_tensor_scale, n
     on the current stream one is taken from torch's allocator, which keeps it in the
     order of that stream and of a graph capture; with another stream, or with addresses
     for tensors, the call does without."""
-    if workspace is None and stream is None and hasattr(x, "new_empty"):
+    if workspace is None and stream is None:
         need = mx_linear_workspace_bytes(tokens, k, n, fmt)
-        if need:
+        if need and hasattr(x, "new_empty"):
             workspace = x.new_empty(need // x.element_size())
             workspace_bytes = need
-    if workspace is not None:
-        if workspace_bytes is None:
-            workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
-        return _check("mx_linear_bf16_workspace", lib().mx_linear_bf16_workspace(
+    if workspace is None:
+        return _check("mx_linear_bf16", lib().mx_linear_bf16(
             _ptr(x), tokens, k, ld_x, fmt, _ptr(w_codes), _ptr(w_scales), _ptr(w_tensor_scale), n,
-            _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _ptr(workspace),
-            workspace_bytes, _stream(stream)))
-    return _check("mx_linear_bf16", lib().mx_linear_bf16(
+            _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _stream(stream)))
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
+    return _check("mx_linear_bf16_workspace", lib().mx_linear_bf16_workspace(
         _ptr(x), tokens, k, ld_x, fmt, _ptr(w_codes), _ptr(w_scales), _ptr(w_tensor_scale), n,
-        _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _stream(stream)))
+        _ptr(y), ld_y, out_dtype, _epilogue(bias, beta, gelu), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
 
 
 def mx_moe_route_bf16(x, tokens, hidden, ld_x, router, experts, bias, top_k, normalize, ids,
