@@ -15,6 +15,7 @@
 #include <mutex>
 #include <vector>
 
+#include "few_tokens.h"
 #include "mx_internal.h"
 #include "mxfp4.h"
 

@@ -16,8 +16,7 @@
 
 #include <cuda_fp16.h>
 
-#include "mx_device.cuh"
-#include "mx_internal.h"
+#include "few_tokens.cuh"
 
 namespace mx {
 

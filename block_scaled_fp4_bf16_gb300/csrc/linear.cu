@@ -22,8 +22,7 @@
 // two rounds of copies from memory, the join of the warps.
 #include <cuda_fp16.h>
 
-#include "mx_device.cuh"
-#include "mx_internal.h"
+#include "few_tokens.cuh"
 
 namespace mx {
 namespace {

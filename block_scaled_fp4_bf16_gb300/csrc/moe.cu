@@ -10,8 +10,6 @@
 // CTAs an SM: with one, seven clusters of 16 are resident and the eighth (64 tokens)
 // runs after them (64 x 8192 of 256: 14.9 us, so 11.0; 1 x 2048 of 64: 3.6 us, latency).
 #include "fp4_digits.cuh"
-#include "mx_device.cuh"
-#include "mx_internal.h"
 
 namespace mx {
 namespace {

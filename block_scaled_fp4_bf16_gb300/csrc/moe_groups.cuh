@@ -1,8 +1,7 @@
 // The grouping of a mixture-of-experts call's (token, slot) pairs by expert.
 #pragma once
 
-#include "mx_device.cuh"
-#include "mx_internal.h"
+#include "few_tokens.cuh"
 
 namespace mx {
 
