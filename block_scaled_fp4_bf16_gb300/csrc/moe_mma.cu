@@ -128,7 +128,7 @@ struct Expert {
   uint64_t *full, *empty, *acc_full, *acc_empty;
   volatile uint32_t *abort;
   uint32_t tmem;
-  float *tops;  // [kHelpers]
+  float *tops;  // [kWorkers]
   Groups g;
   uint16_t *places, *members;  // of the pairs, of the places
   int pairs;
@@ -402,7 +402,9 @@ struct Expert {
   }
 
   // ---- digits of x.  A warp takes a token's stage; NVFP4's factor needs all of the
-  // token: the warp looks through it first.
+  // token: the warp looks through it first, or all the CTA's workers where only one of
+  // them has a task (8 x 4096 x 2048 of 64 71.1 us, so 70.2; 1 x 8192 x 4096 of 8 40.3, so
+  // 39.1).
   __device__ __forceinline__ uint4 load_x(int r, int at) const {
     const MoeArgs &a = p.a;
     const int64_t off = r * a.ld_x + at;
@@ -410,15 +412,17 @@ struct Expert {
                ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(a.x) + off)
                : make_uint4(0, 0, 0, 0);
   }
-  // The largest finite magnitude of a token.
-  __device__ __noinline__ float x_top(int r) const {
+  // The largest finite magnitude of a token; `warps` warps look, this one as number `warp`
+  // (its part only).
+  __device__ __noinline__ float x_top(int r, int warp, int warps) const {
     // eight loads in flight; magnitudes compare as integers, a magnitude of 0x7F80 or
     // more is no number and counts as 0
     uint32_t top = 0;
-    for (int at = (threadIdx.x & 31) * 8; at < p.a.hidden; at += 8 * kImageK) {
+    const int lane_at = (threadIdx.x & 31) * 8;
+    for (int st = warp; st * kImageK < p.a.hidden; st += 8 * warps) {
       uint4 q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) q[i] = load_x(r, at + i * kImageK);
+      for (int i = 0; i < 8; ++i) q[i] = load_x(r, (st + i * warps) * kImageK + lane_at);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
@@ -442,10 +446,21 @@ struct Expert {
     x_task = (static_cast<int>(threadIdx.x >> 5) - 2) * static_cast<int>(gridDim.x) +
              static_cast<int>(blockIdx.x);
     x_first_top = 0.0f;
-    if (x_task < 0 || x_task >= a.tokens * x_stages) return;
-    const int r = x_task / x_stages;
-    x_first = load_x(r, (x_task - r * x_stages) * kImageK + (threadIdx.x & 31) * 8);
-    if (FMT == 1) x_first_top = x_top(r);
+    const int tasks = a.tokens * x_stages, worker = static_cast<int>(threadIdx.x >> 5) - 2;
+    if (worker < 0) return;
+    const bool together = FMT == 1 && tasks <= static_cast<int>(gridDim.x);
+    if (x_task < tasks) {
+      const int r = x_task / x_stages;
+      x_first = load_x(r, (x_task - r * x_stages) * kImageK + (threadIdx.x & 31) * 8);
+      if (FMT == 1 && !together) x_first_top = x_top(r, 0, 1);
+    }
+    if (together && static_cast<int>(blockIdx.x) < tasks) {
+      const float top = x_top(static_cast<int>(blockIdx.x) / x_stages, worker, kWorkers);
+      if ((threadIdx.x & 31) == 0) tops[worker] = top;
+      named_barrier_sync(1, kWorkers * 32);
+#pragma unroll
+      for (int w = 0; w < kWorkers; ++w) x_first_top = fmaxf(x_first_top, tops[w]);
+    }
   }
   __device__ __forceinline__ void split_x() {
     const MoeArgs &a = p.a;
@@ -456,7 +471,7 @@ struct Expert {
       const int r = t / x_stages, st = t - r * x_stages;
       if (t != x_task) {
         q = load_x(r, st * kImageK + lane * 8);
-        if (FMT == 1) top = x_top(r);
+        if (FMT == 1) top = x_top(r, 0, 1);
       }
       const uint16_t *to = places + r * a.top_k;
       const uint32_t w[4] = {q.x, q.y, q.z, q.w};
@@ -813,7 +828,7 @@ cudaError_t launch_expert_kernel(const MoeArgs &a, cudaStream_t s) {
   p.sfa_off = p.b_off + p.slots * X::kGroup * kImageCodes;
   p.sfb_off = p.sfa_off + p.slots * 2 * X::kSfa;
   p.bar_off = p.sfb_off + p.slots * X::kSfb;
-  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + kHelpers * 4 + 15) / 16 * 16;
+  p.groups_at = (p.bar_off + 8 * (2 * p.slots + 5) + 16 + kWorkers * 4 + 15) / 16 * 16;
   const int smem = p.groups_at + groups;
   // the groups' scratch lies in the weights' part of the ring
   if (smem > kSmem || p.b_off < 2 * (kThreads / 32 + 2) * a.experts) return cudaErrorInvalidValue;
