@@ -84,10 +84,13 @@ struct Product {
   }
 };
 
-// Not inlined, and called once before weights stream: as write_digits.
-__device__ __noinline__ float2 act(float2 v, int gelu) {
-  return gelu ? gelu_f32x2(v)
-              : make_float2(v.x / (1.0f + expf(-v.x)), v.y / (1.0f + expf(-v.y)));
+// Not inlined, and called once before weights stream: as write_digits.  (The quotient
+// of silu within 2 units of the last place, far below the digits of h.)
+__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + expf(-v)); }
+__device__ __noinline__ float4 act(float4 v, int gelu) {
+  if (!gelu) return make_float4(silu(v.x), silu(v.y), silu(v.z), silu(v.w));
+  const float2 lo = gelu_f32x2(make_float2(v.x, v.y)), hi = gelu_f32x2(make_float2(v.z, v.w));
+  return make_float4(lo.x, lo.y, hi.x, hi.y);
 }
 
 // A product reads its 128 weight rows from shared memory in about 100 clocks
@@ -524,10 +527,12 @@ struct Expert {
         u[4] += b1.x, u[5] += b1.y, u[6] += b1.z, u[7] += b1.w;
       }
 #pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const float2 f = act(make_float2(v[i], v[i + 1]), a.gelu);
+      for (int i = 0; i < 8; i += 4) {
+        const float4 f = act(make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]), a.gelu);
         v[i] = f.x * u[i];
         v[i + 1] = f.y * u[i + 1];
+        v[i + 2] = f.z * u[i + 2];
+        v[i + 3] = f.w * u[i + 3];
       }
     };
     int grp = 0;
@@ -686,7 +691,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 2) {
     warm_digits<FMT>(p.x);
     // (the result is used, so that the call stays)
-    if (act(make_float2(0.0f, 0.0f), a.gelu).x != 0.0f) atomicOr(a.status, kStatusTimeout);
+    if (act(make_float4(0.0f, 0.0f, 0.0f, 0.0f), a.gelu).x != 0.0f)
+      atomicOr(a.status, kStatusTimeout);
   }
   griddep_wait();
   if constexpr (!X::kByToken) x.fetch_x();
