@@ -355,11 +355,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (finish) continue;
       // the last of the tile's CTAs adds the sums of all
       named_barrier_sync(1, kEpilogue * 32);
-      if (leader) {
-        __threadfence();  // (cumulative: over what the barrier ordered before it)
-        last[word + 1] = *abort == 0 && atomicAdd(p.counts + tile, 1u) == static_cast<uint32_t>(c1 - c0);
-        __threadfence();
-      }
+      if (leader)
+        last[word + 1] = *abort == 0 &&
+                         acquire_release_add(p.counts + tile) == static_cast<uint32_t>(c1 - c0);
       named_barrier_sync(1, kEpilogue * 32);
       if (last[word + 1] == 0) continue;
 #pragma unroll
