@@ -285,7 +285,8 @@ __device__ __forceinline__ uint32_t acquire_release_add(uint32_t *count) {
 
 // One thread, or a whole warp together (a warp of which one lane waits comes out
 // diverged, and every shuffle after it then takes 330 clocks: measured, 4 us of a
-// write_digits; experts 1 x 2048 x 1024 of 64 25.3 us, so 20.7).  False when the wait ran out (abort is raised then) or abort was up.
+// write_digits; experts 1 x 2048 x 1024 of 64 25.3 us, so 20.7).  False when the wait
+// ran out (abort is raised then) or abort was up.
 __device__ __forceinline__ bool count_reached(const uint32_t *count, uint32_t target,
                                               volatile uint32_t *abort, uint32_t *status) {
   const uint64_t t0 = globaltimer_ns();

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (warp == 0) {
     griddep_wait();
-    asm volatile("fence.proxy.async;" ::: "memory");
+    asm volatile("fence.proxy.async.global;" ::: "memory");
     if (elect_one())
       for (int i = 0; i < ahead; ++i) digits(begin + i, i);
     __syncwarp();

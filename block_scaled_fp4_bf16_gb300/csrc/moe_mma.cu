@@ -709,12 +709,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     // the digits of x are there when every CTA has counted them
     int x_there = X::kByToken ? 1 : 0;
-    if (X::kByToken) asm volatile("fence.proxy.async;" ::: "memory");
+    if (X::kByToken) asm volatile("fence.proxy.async.global;" ::: "memory");
     const auto x_ready = [&](int, int how) {
       if (x_there == 0 && how == kWait) {
         const bool r = count_reached(a.counts + kCountX, gridDim.x, x.abort, a.status);
         x_there = __all_sync(0xFFFFFFFFu, r) != 0 ? 1 : -1;
-        asm volatile("fence.proxy.async;" ::: "memory");  // bulk copies read what was counted
+        asm volatile("fence.proxy.async.global;" ::: "memory");  // bulk copies read what was counted
       }
       return x_there;
     };
@@ -734,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (look < *x.g.count)
         r = load_acquire(x.h_counts() + look) >= static_cast<uint32_t>(x.h_tasks(look));
       there = __ballot_sync(0xFFFFFFFFu, r);
-      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("fence.proxy.async.global;" ::: "memory");
       return static_cast<int>(there & 1u);
     };
     if (!*x.abort && x.template copies<true>(up, &gate_map, &up_map, p.x, x_ready))
