@@ -725,15 +725,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (grp - from < 32 && (there >> (grp - from)) & 1u) return 1;
       if (how == kKnown) return 0;
       from = grp;
-      if (how == kWait) {
-        const bool r = count_reached(x.h_counts() + grp, x.h_tasks(grp), x.abort, a.status);
-        if (!__all_sync(0xFFFFFFFFu, r)) return -1;
-      }
       const int look = grp + static_cast<int>(threadIdx.x & 31);
-      bool r = false;
-      if (look < *x.g.count)
-        r = load_acquire(x.h_counts() + look) >= static_cast<uint32_t>(x.h_tasks(look));
-      there = __ballot_sync(0xFFFFFFFFu, r);
+      const uint64_t t0 = globaltimer_ns();
+      while (true) {
+        there = __ballot_sync(0xFFFFFFFFu, look < *x.g.count &&
+                                               load_acquire(x.h_counts() + look) >=
+                                                   static_cast<uint32_t>(x.h_tasks(look)));
+        if (how != kWait || (there & 1u) != 0) break;
+        const bool late = globaltimer_ns() - t0 > kWaitTimeoutNs;
+        if (!__any_sync(0xFFFFFFFFu, late || *x.abort != 0)) continue;
+        if (late) {
+          *x.abort = 1u;
+          atomicOr(a.status, kStatusTimeout);
+        }
+        __syncwarp();
+        return -1;
+      }
       asm volatile("fence.proxy.async.global;" ::: "memory");
       return static_cast<int>(there & 1u);
     };
