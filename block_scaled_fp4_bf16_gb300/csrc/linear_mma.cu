@@ -8,10 +8,10 @@
 // last of them to arrive, which adds the sums of all in the order of K: the result
 // does not depend on the order of arrival, and no CTA waits for another.
 //
-// Bound by the weights' bytes: 1 to 8 x 28672 x 8192 MXFP4 25.5 us, 4.9 TB/s of them
-// over the whole call (its parts: 2 us until the first copies are under way, 20 to
-// 22 us of streaming, 2 us of epilogue); 16 rows 26.9 us, 32 rows 32.9 us, where each
-// SM reads twice as many bytes of digits from L2 as of weights.  NVFP4 26.8, 35.2 us.
+// Bound by the weights' bytes: 1 to 8 x 28672 x 8192 MXFP4 25.0 us, 5 TB/s of them over
+// the whole call (its parts: 2 us until the first copies are under way, 20 to 22 us of
+// streaming, 2 us of epilogue); 16 rows 26.5 us, 32 rows 32.9 us, where each SM reads
+// twice as many bytes of digits from L2 as of weights.  NVFP4 26.2, 28.1, 35.9 us.
 #include "fp4_digits.cuh"
 
 namespace mx {

@@ -15,9 +15,9 @@
 // 64 x 4096 x 2048 of 64 173 us and 8 x 4096 x 2048 NVFP4 82 us; so 165 and 77.)
 //
 // Bound: at many pairs the weights' bytes (64 x 4096 x 2048 of 64 MXFP4 155 us, 5.5 TB/s
-// of them; 8 x 4096 x 2048, 26 of 64 experts chosen, NVFP4 70 us, 5.4 TB/s); at few the
-// chain of dependent steps (1 x 2048 x 1024 of 64 20 us: digits of x 4, up sums 4, digits of h
-// 3, down sums 3, y 2, the rest launches; the weights alone are 4 us).
+// of them; 8 x 4096 x 2048, 26 of 64 experts chosen, NVFP4 68 us, 5.5 TB/s); at few the
+// chain of dependent steps (1 x 2048 x 1024 of 64 17 us: the launch before with x's digits 3,
+// up sums 5, digits of h 3, down sums 2, y 2, the rest launches; the weights alone are 4).
 #include "fp4_digits.cuh"
 #include "moe_groups.cuh"
 
