@@ -76,7 +76,8 @@ __device__ __noinline__ float nonfinite_sum(const LinearArgs &a, int64_t row, in
   bool any = false;
   for (int64_t k0 = 0; k0 < a.k; k0 += kBlock) {
     const int64_t block = k0 / kBlock;
-    const int64_t at = ((row >> 7) * tiles + (block >> 2)) * 512 + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (block & 3);
+    const int64_t at = ((row >> 7) * tiles + (block >> 2)) * 512 + (row & 31) * 16 +
+                       ((row >> 5) & 3) * 4 + (block & 3);
     if (!in_bounds(at, 1, ((a.n + 127) >> 7) * tiles * 512, a.status)) continue;
     const uint32_t byte = a.w.scales[at];
     float scale;

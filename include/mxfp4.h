@@ -495,9 +495,10 @@ size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int
  *   workspace: mx_moe_workspace_bytes(...) bytes, 16-byte aligned.
  * The hidden values act(G x) * U x are computed in binary32 and enter the
  * second product as eight FP4 digits (to within 2^-22 of the largest of their
- * block).  y and the workspace must not overlap an input or each other.  Reads the chosen experts' weights only.  Launches a
- * small kernel and one of a CTA per SM, all resident together (a cooperative
- * launch: it waits for SMs that other streams' kernels hold). */
+ * block).  y and the workspace must not overlap an input or each other.  Reads
+ * the chosen experts' weights only.  Launches a small kernel and one of a CTA
+ * per SM, all resident together (a cooperative launch: it waits for SMs that
+ * other streams' kernels hold). */
 int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
                         const float *weights, int top_k, const mx_moe_weights *moe, void *y,
                         int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
