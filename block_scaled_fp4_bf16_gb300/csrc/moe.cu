@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     route_kernel(const __grid_constant__ RouteArgs a, const __grid_constant__ Next next) {
   __shared__ float red[kWarps][kRowTiles][4][32];
   __shared__ float logits[kMoeMaxExperts];  // of this CTA's token
+  cluster_arrive_relaxed();
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -151,7 +152,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     for (int i = 0; i < 4; ++i) red[warp][m][i][lane] = acc[i];
   }
   __syncthreads();
-  // the warps' sums, in their order, to the CTA of the token
+  // the warps' sums, in their order, to the CTA of the token, which has begun by then
+  cluster_wait();
   for (int u = threadIdx.x; u < kRowTiles * 128; u += kWarps * 32) {
     const int m = u >> 7, i = (u >> 5) & 3, l = u & 31;
     const int row = m * 16 + (l >> 2) + (i >> 1) * 8, token = (l & 3) * 2 + (i & 1);

@@ -368,6 +368,15 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The two halves of a barrier that orders no memory: after cluster_wait every CTA of the
+// cluster has begun, which an access to its shared memory needs.  All threads of all CTAs.
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Store to shared memory of another CTA of the cluster (cluster_addr from
 // mapa_shared).
 __device__ __forceinline__ void st_cluster_f32(uint32_t cluster_addr, float v) {
