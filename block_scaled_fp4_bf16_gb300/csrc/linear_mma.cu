@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (in_bounds(o, 1, parts_extent, a.status)) p.parts[o] = u;
           }
         }
+        __syncwarp();  // (an output may have taken some lanes through nonfinite_sum)
       }
       tc_fence_before();
       __syncwarp();
@@ -370,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 #pragma unroll
       for (int i = 0; i < kMine; ++i) put(v[i], i);
+      __syncwarp();
     }
   }
   tc_fence_before();

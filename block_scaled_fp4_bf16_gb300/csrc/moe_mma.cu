@@ -374,8 +374,7 @@ struct Expert {
             sum[m][j] = t;
           }
         }
-        if (row >= d.rows) continue;
-        if constexpr (by_token) {
+        if (by_token && row < d.rows) {
           for (int c = 0; c < n; ++c) {
             const int place = g.begin[im.grp] + c, t = g.list[place] / a.top_k;
             if (t >> 2 != i) continue;
@@ -384,7 +383,7 @@ struct Expert {
               put(m, place, (t & 2) != 0 ? (t & 1) != 0 ? sum[m][3] : sum[m][2]
                                          : (t & 1) != 0 ? sum[m][1] : sum[m][0]);
           }
-        } else {
+        } else if (row < d.rows) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             if (i * 4 + j >= n) break;
@@ -392,6 +391,7 @@ struct Expert {
             for (int m = 0; m < kSegs; ++m) put(m, g.begin[im.grp] + i * 4 + j, sum[m][j]);
           }
         }
+        __syncwarp();  // (rows past the last have no outputs)
       }
       tc_fence_before();
       __syncwarp();

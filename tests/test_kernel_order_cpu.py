@@ -45,3 +45,34 @@ def test_a_cluster_has_begun_before_its_shared_memory_is_used(name):
         found += 1
         assert BARRIER.search(k[:first.start()]), f"{name}: no cluster barrier before {first.group(1)}"
     assert found > 0
+
+
+def loops(text):
+    """The braces' contents of the `for` loops of a text that have braces."""
+    for m in re.finditer(r"\bfor \(", text):
+        depth, i = 1, m.end()
+        while depth:
+            depth += {"(": 1, ")": -1}.get(text[i], 0)
+            i += 1
+        if text[i:].lstrip().startswith("{"):
+            yield body(text, i)
+
+
+@pytest.mark.parametrize("name", ["linear_mma.cu", "moe_mma.cu"])
+def test_a_warp_is_whole_again_before_it_reads_tensor_memory(name):
+    """tcgen05.ld is for whole warps: the loop that has one and then writes outputs, of which
+    lanes may have none or more to do, ends with __syncwarp()."""
+    def reads_and_writes(loop):
+        at = loop.find("tc_ld_32x32b_x32(")
+        return at >= 0 and re.search(r"\bput\(", loop[at:]) is not None
+
+    found = [x for x in loops(source(name)) if reads_and_writes(x)]
+    inner = [x for x in found if not any(reads_and_writes(y) for y in loops(x[1:]))]
+    assert len(inner) == 1
+    assert inner[0][:-1].rstrip().endswith("__syncwarp();"), f"{name}: a loop over tcgen05.ld"
+
+
+def test_a_warp_is_whole_again_before_the_next_tile():
+    text = source("linear_mma.cu")
+    ends = [m.end() for m in re.finditer(r"put\(v\[i\], i\);\s*", text)]
+    assert ends and all(text[e:].startswith("__syncwarp();") for e in ends)
