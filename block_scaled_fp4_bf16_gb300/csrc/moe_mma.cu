@@ -741,6 +741,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         return -1;
       }
+      // (a vote orders no memory: what each lane acquired, for the lane that copies)
+      __syncwarp();
       asm volatile("fence.proxy.async.global;" ::: "memory");
       return static_cast<int>(there & 1u);
     };

@@ -76,3 +76,13 @@ def test_a_warp_is_whole_again_before_the_next_tile():
     text = source("linear_mma.cu")
     ends = [m.end() for m in re.finditer(r"put\(v\[i\], i\);\s*", text)]
     assert ends and all(text[e:].startswith("__syncwarp();") for e in ends)
+
+
+def test_what_the_lanes_acquired_is_there_for_the_lane_that_copies():
+    """Each lane acquires the count of another group and one lane then issues the copies of
+    any: only __syncwarp() between orders the one after the others (a vote does not)."""
+    text = source("moe_mma.cu")
+    look = body(text, text.index("const auto h_ready"))
+    assert "load_acquire(" in look and "__ballot_sync(" in look
+    last = look.rindex("fence.proxy.async.global")
+    assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"$", look[:last])
