@@ -12,10 +12,13 @@
 //   - E2M1 becomes FP16 by the conversion instruction, two codes at once, and
 //     multiplies on the 16 x 8 x 16 FP16 product with binary32 sums, the weights on
 //     its 16-row side (measured: 90 codes a clock per SM converted, 128 multiplied);
-//   - MXFP4 scales apply to the sum of a 32-block (any UE8M0 power of two), the
-//     E4M3 scales of NVFP4 to the FP16 weights (code * scale has 6 bits: exact);
+//   - MXFP4 scales apply to the sum of a 32-block, the E4M3 scales of NVFP4 to the FP16
+//     weights (code * scale has 6 bits: exact);
 //   - activations become FP16 times a power of two for each (token, 128): BF16
 //     values keep all their bits unless they lie 2^-31 below the largest of the 128.
+//     The sums of a block are then up to 2^22.6, with which a UE8M0 scale above 2^104
+//     overflows, as may the whole sum before a small tensor scale: an output that is not
+//     finite is summed again with more range (wide_sum).
 // It issues about 2.5 instructions a code, which bounds it at 4 TB/s of weights
 // for up to 8 tokens (28672 x 8192: 30 us); linear_mma.cu leaves the weights to the
 // tensor cores.  At 8 x 4096 x 4096 (4.9 us; its bytes 1.4) latency bounds it: a launch,
@@ -324,7 +327,7 @@ struct LinearParams {
 // Persistent over row tiles: tile blockIdx.x, + gridDim.x, ...  Each of the W
 // warps takes its share of K in every tile.
 template <int FMT, int MT, int NT, int W, int S>
-__global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(W * 32, 1) linear_kernel(const __grid_constant__ LinearParams p) {
   extern __shared__ __align__(128) char smem[];
   constexpr int R = 16 * MT, kUnits = MT * NT * 32;
   const LinearArgs &a = p.a;
@@ -400,9 +403,13 @@ __global__ void __launch_bounds__(W * 32, 1) linear_kernel(const LinearParams p)
       for (int i = 0; i < 4; ++i) {
         const int64_t row = row0 + (i >> 1) * 8;
         const int col = col0 + (i & 1);
-        if (row < a.n && col < a.tokens) put_linear(a, row, col, FMT == 1 ? f[i] * alpha : f[i]);
+        if (row >= a.n || col >= a.tokens) continue;
+        float o = FMT == 1 ? f[i] * alpha : f[i];
+        if (!(fabsf(o) < __uint_as_float(0x7F800000u))) o = wide_sum<FMT>(a, row, col);
+        put_linear(a, row, col, o);
       }
     }
+    __syncwarp();  // (an output may have taken some lanes through wide_sum)
     if (p.ctas > 1)
       cluster_sync();
     else
