@@ -52,54 +52,6 @@ __global__ void __launch_bounds__(kDigitWarps<FMT> * 32) digits_kernel(const __g
 
 // ---------------------------------------------------------------- the product
 
-__device__ __forceinline__ float from_e2m1(uint32_t code) {
-  uint32_t h;
-  asm("{\n .reg .b8 t;\n cvt.u8.u32 t, %1;\n cvt.rn.f16x2.e2m1x2 %0, t;\n}\n" : "=r"(h) : "r"(code));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-}
-__device__ __forceinline__ float from_e4m3(uint32_t byte) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(byte)));
-  return __half2float(__ushort_as_half(static_cast<unsigned short>(h & 0xFFFFu)));
-}
-
-// Output (row, token) of an x that holds infinities or NaN, whose digits are NaN as a
-// whole: the sum of those elements' terms, to which the finite ones add nothing, and
-// NaN if a scale of the row is NaN.  v if x holds none.  It walks all of x, for such
-// outputs only.
-template <int FMT>
-__device__ __noinline__ float nonfinite_sum(const LinearArgs &a, int64_t row, int t, float v) {
-  constexpr int kBlock = FMT == 0 ? 32 : 16;
-  const int tiles = static_cast<int>((a.k / kBlock + 3) >> 2);
-  const float ts = FMT == 1 ? *a.w.ts : 1.0f;
-  float sum = 0.0f;
-  bool any = false;
-  for (int64_t k0 = 0; k0 < a.k; k0 += kBlock) {
-    const int64_t block = k0 / kBlock;
-    const int64_t at = ((row >> 7) * tiles + (block >> 2)) * 512 + (row & 31) * 16 +
-                       ((row >> 5) & 3) * 4 + (block & 3);
-    if (!in_bounds(at, 1, ((a.n + 127) >> 7) * tiles * 512, a.status)) continue;
-    const uint32_t byte = a.w.scales[at];
-    float scale;
-    if constexpr (FMT == 0)
-      scale = byte == 255u ? __uint_as_float(0x7FC00000u) : pow2(static_cast<int>(byte) - 127);
-    else
-      scale = from_e4m3(byte);
-    if (scale != scale) sum = scale;
-    for (int i = 0; i < kBlock; ++i) {
-      const int64_t off = t * a.ld_x + k0 + i;
-      if (!in_bounds(off, 1, (a.tokens - 1) * a.ld_x + a.k, a.status)) continue;
-      const float x = bf16_value(a.x, off);
-      if ((__float_as_uint(x) & 0x7F800000u) != 0x7F800000u) continue;
-      any = true;
-      const int64_t c = row * (a.k >> 1) + ((k0 + i) >> 1);
-      if (!in_bounds(c, 1, a.n * (a.k >> 1), a.status)) continue;
-      sum += x * (from_e2m1((a.w.codes[c] >> (4 * (i & 1))) & 15u) * scale * ts);
-    }
-  }
-  return any ? sum : v;
-}
-
 // A CTA's share of the units (the first `more` CTAs have one more than `each`), and
 // who shares a tile.
 struct Share {
@@ -301,7 +253,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const auto put = [&](float v, int i) {
         if (token(i) >= a.tokens || at >= a.n) return;
         if (FMT == 1) v *= alpha;
-        if (v != v) v = nonfinite_sum<FMT>(a, at, token(i), v);
+        // (a block that holds an infinity or NaN has digits that are NaN as a whole)
+        if (!(fabsf(v) < __uint_as_float(0x7F800000u))) v = wide_sum<FMT>(a, at, token(i));
         put_linear(a, at, token(i), v);
       };
       // Of two CTAs the second to arrive, if it is clear before its own sums are there,
@@ -348,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (in_bounds(o, 1, parts_extent, a.status)) p.parts[o] = u;
           }
         }
-        __syncwarp();  // (an output may have taken some lanes through nonfinite_sum)
+        __syncwarp();  // (an output may have taken some lanes through wide_sum)
       }
       tc_fence_before();
       __syncwarp();

@@ -7,12 +7,15 @@ form may lose), from the formula in binary64.
 """
 import numpy as np
 import pytest
+import torch
 
+import block_scaled_fp4_bf16_gb300 as mx
 import oracle
 from block_scaled_fp4_bf16_gb300 import synth
 from tests.gpu_helpers import bf16_bits_to_f64
 from tests.test_gpu_few_tokens import (FMTS, MX, NV, Weight, assert_close, linear_ref, run_linear, ulp,
                                        x_bits)
+from tests.test_gpu_linear_workspace import Wide, pick, reference, run
 
 pytestmark = pytest.mark.gpu
 
@@ -79,3 +82,46 @@ def test_results_beyond_the_range_stay_infinite(fmt):
     bits[1] = BIG | 0x8000
     got = run_linear(bits, w)
     assert (got[0] == np.inf).all() and (got[1] == -np.inf).all()
+
+
+# with a workspace: one, two, four and eight columns of digits' blocks; two and more CTAs a tile
+WIDE = [(4, 2464, 28768), (8, 8224, 8224), (16, 12320, 4128), (20, 8224, 8224)]
+
+
+@pytest.mark.parametrize("tokens,n,k", WIDE)
+def test_large_block_scales_with_a_workspace(tokens, n, k):
+    assert mx.mx_linear_workspace_bytes(tokens, k, n, MX) > 0
+    w = Wide(n, k, MX, 441, 110, 254)
+    bits = scaled(x_bits(tokens, k, 442), [(-20, -60, -100)[t % 3] for t in range(tokens)])
+    ref, tol = reference(bits, w)
+    assert np.abs(ref).max() < 1e38
+    assert_close(pick(run(bits, w), w), ref, tol, "fp32")
+
+
+@pytest.mark.parametrize("tokens,n,k", WIDE)
+def test_large_activations_under_a_small_tensor_scale_with_a_workspace(tokens, n, k):
+    assert mx.mx_linear_workspace_bytes(tokens, k, n, NV) > 0
+    w, bits = Wide(n, k, NV, 451, 0x20, 0x7E), x_bits(tokens, k, 452)
+    w.ts.fill_(2.0 ** -30)
+    clean = run(bits, w)
+    bits[0] = BIG | (bits[0] & 0x8000)
+    ref, tol = reference(bits, w)
+    assert np.abs(ref).max() < 1e38
+    got = run(bits, w)
+    assert_close(pick(got, w), ref, tol, "largest")
+    assert torch.equal(got[1:], clean[1:])
+    assert_close(pick(run(bits, w, out_fp32=False), w), ref, tol + ulp(ref), "bf16")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_infinities_with_a_workspace_whose_weights_are_next_to_nothing(fmt):
+    """inf times the least weight other than zero is inf, and times zero NaN."""
+    t, n, k = 3, 8224, 8224
+    w, bits = Wide(n, k, fmt, 461, *((0, 0) if fmt == MX else (1, 1))), x_bits(t, k, 462)
+    if fmt == NV:
+        w.ts.fill_(2.0 ** -140)
+    bits[1, 100] = 0x7F80
+    got, v = pick(run(bits, w), w), w.value()
+    zero = v[:, 100] == 0
+    assert np.isnan(got[1][zero]).all() and (got[1][~zero] == np.sign(v[~zero, 100]) * np.inf).all()
+    assert np.isfinite(got[[0, 2]]).all()
