@@ -84,9 +84,15 @@ struct Product {
   }
 };
 
-// Not inlined, and called once before weights stream: as write_digits.  (The quotient
-// of silu within 2 units of the last place, far below the digits of h.)
-__device__ __forceinline__ float silu(float v) { return __fdividef(v, 1.0f + expf(-v)); }
+// v / (1 + exp(-v)) by the exponential of -|v|, which cannot overflow: a divisor of 1 to 2,
+// where the quotient is within 2 units of the last place (by exp(-v) it is 0 where that
+// passes 2^126, v below -87.3).  Relative error below 2^-21, where v exp(v) is subnormal
+// 2^-149 |v| besides.
+__device__ __forceinline__ float silu(float v) {
+  const float e = expf(-fabsf(v));
+  return __fdividef(v >= 0.0f ? v : v * e, 1.0f + e);
+}
+// Not inlined, and called once before weights stream: as write_digits.
 __device__ __noinline__ float4 act(float4 v, int gelu) {
   if (!gelu) return make_float4(silu(v.x), silu(v.y), silu(v.z), silu(v.w));
   const float2 lo = gelu_f32x2(make_float2(v.x, v.y)), hi = gelu_f32x2(make_float2(v.z, v.w));
