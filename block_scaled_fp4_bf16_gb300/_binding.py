@@ -388,11 +388,11 @@ def mx_linear_bf16(x, tokens, k, ld_x, fmt, w_codes, w_scales, w_tensor_scale, n
 
     With a workspace (mx_linear_workspace_bytes) it is mx_linear_bf16_workspace.  None:
     on the current stream one is taken from torch's allocator, which keeps it in the
-    order of that stream and of a graph capture; with another stream, or with addresses
-    for tensors, the call does without."""
+    order of that stream and of a graph capture; with another stream, or with an address
+    or a tensor in host memory for x, the call does without."""
     if workspace is None and stream is None:
         need = mx_linear_workspace_bytes(tokens, k, n, fmt)
-        if need and hasattr(x, "new_empty"):
+        if need and getattr(x, "is_cuda", False):
             workspace = x.new_empty(need // x.element_size())
             workspace_bytes = need
     if workspace is None:
