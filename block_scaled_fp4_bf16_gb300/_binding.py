@@ -376,6 +376,18 @@ def mxfp4_gemm_static_workspace(a_codes, a_scales, b_codes, b_scales, d, m, n, k
         out_dtype, split_k, _stream(stream)))
 
 
+def _empty_on(stream, x, numel):
+    """x.new_empty(numel), allocated on the given stream (None: the current one)."""
+    if stream is None:
+        return x.new_empty(numel)
+    import torch
+    if isinstance(stream, int):
+        # (1 is the default stream's other handle; torch has it as 0)
+        stream = torch.cuda.ExternalStream(0 if stream == 1 else stream, device=x.device)
+    with torch.cuda.stream(stream):
+        return x.new_empty(numel)
+
+
 @functools.lru_cache(maxsize=1024)
 def mx_linear_workspace_bytes(tokens: int, k: int, n: int, fmt: int) -> int:
     return lib().mx_linear_workspace_bytes(tokens, k, n, fmt)
@@ -387,13 +399,13 @@ def mx_linear_bf16(x, tokens, k, ld_x, fmt, w_codes, w_scales, w_tensor_scale, n
     """y = act(x W^T + beta * y_in + bias) for a few BF16 rows and an FP4 weight.
 
     With a workspace (mx_linear_workspace_bytes) it is mx_linear_bf16_workspace.  None:
-    on the current stream one is taken from torch's allocator, which keeps it in the
-    order of that stream and of a graph capture; with another stream, or with an address
-    or a tensor in host memory for x, the call does without."""
-    if workspace is None and stream is None:
+    one is taken from torch's allocator on the call's stream, which keeps it in the order
+    of that stream and of a graph capture; with an address or a tensor in host memory for
+    x the call does without."""
+    if workspace is None:
         need = mx_linear_workspace_bytes(tokens, k, n, fmt)
         if need and getattr(x, "is_cuda", False):
-            workspace = x.new_empty(need // x.element_size())
+            workspace = _empty_on(stream, x, need // x.element_size())
             workspace_bytes = need
     if workspace is None:
         return _check("mx_linear_bf16", lib().mx_linear_bf16(
