@@ -906,6 +906,11 @@ int few_check_x(const char *fn, const void *x, int64_t tokens, int64_t max_token
   return MX_OK;
 }
 
+// Scale blocks of a matrix [rows, k], its rows in whole tiles: 2^31 or more.
+bool too_many_blocks(int format, int64_t rows, int64_t k) {
+  return (rows + 127) / 128 * 128 * (k / block_of(format)) >= (int64_t(1) << 31);
+}
+
 // A stack of `count` FP4 matrices [rows, k] (rows, k already checked).
 int few_check_matrix(const char *fn, const char *name, int format, const void *codes,
                      const void *scales, const float *ts, int64_t rows, int64_t k) {
@@ -919,7 +924,7 @@ int few_check_matrix(const char *fn, const char *name, int format, const void *c
                 !aligned16(codes) ? "codes are not 16-byte aligned"
                 : !aligned16(scales) ? "scales are not 16-byte aligned"
                                      : "tensor scale is not 4-byte aligned");
-  if ((rows + 127) / 128 * 128 * (k / block_of(format)) >= (int64_t(1) << 31))
+  if (too_many_blocks(format, rows, k))
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: %s [%lld, %lld] has 2^31 or more scale blocks", fn,
                 name, static_cast<long long>(rows), static_cast<long long>(k));
   return MX_OK;
@@ -1184,7 +1189,8 @@ MX_API int mx_linear_bf16(const void *x, int64_t tokens, int64_t k, int64_t ld_x
 
 MX_API size_t mx_linear_workspace_bytes(int64_t tokens, int64_t k, int64_t n, int format) {
   if (!valid_format(format) || tokens < 1 || tokens > MX_LINEAR_MAX_TOKENS || k <= 0 || k % 32 != 0 ||
-      n <= 0 || n % 32 != 0 || k >= (int64_t(1) << 31) || n >= (int64_t(1) << 31))
+      n <= 0 || n % 32 != 0 || k >= (int64_t(1) << 31) || n >= (int64_t(1) << 31) ||
+      too_many_blocks(format, n, k))
     return 0;
   const int fmt = format == MX_FMT_MXFP4 ? 0 : 1;
   return mx::linear_mma_better(tokens, n, k) ? mx::linear_workspace_bytes(fmt, tokens, n, k) : 0;
@@ -1231,7 +1237,8 @@ MX_API int mx_moe_route_bf16(const void *x, int64_t tokens, int64_t hidden, int6
 
 MX_API size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int top_k) {
   if (tokens < 1 || tokens > MX_MOE_MAX_TOKENS || top_k < 1 || top_k > MX_MOE_MAX_TOP_K ||
-      hidden <= 0 || inter <= 0 || hidden >= (int64_t(1) << 31) || inter >= (int64_t(1) << 31))
+      hidden <= 0 || inter <= 0 || hidden % 32 != 0 || inter % 32 != 0 ||
+      hidden >= (int64_t(1) << 31) || inter >= (int64_t(1) << 31))
     return 0;
   const int64_t pairs = tokens * top_k;
   return moe_h_bytes(pairs, inter) + moe_z_bytes(pairs, hidden) +
