@@ -74,7 +74,11 @@ class Decoder:
         self.logits = new(tokens, model.vocab, dtype=torch.float32)
         self.moe_workspace = new(mx.mx_moe_workspace_bytes(tokens, model.hidden, model.inter, model.top_k),
                                  dtype=torch.uint8)
-        need = mx.mx_linear_workspace_bytes(tokens, model.hidden, model.vocab, model.fmt)
+        # (the projection's calls take up to MX_LINEAR_MAX_TOKENS rows, one after the other)
+        self.parts = [slice(i, min(i + mx.MX_LINEAR_MAX_TOKENS, tokens))
+                      for i in range(0, tokens, mx.MX_LINEAR_MAX_TOKENS)]
+        need = max(mx.mx_linear_workspace_bytes(p.stop - p.start, model.hidden, model.vocab, model.fmt)
+                   for p in self.parts)
         self.head_workspace = new(need, dtype=torch.uint8) if need else None
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
@@ -95,8 +99,10 @@ class Decoder:
                                  self.weights, self.y, m.hidden, self.moe_workspace)
             x = x + self.y
         codes, scales, ts = m.head
-        mx.mx_linear_bf16(m.norm(x), t, m.hidden, m.hidden, m.fmt, codes, scales, ts, m.vocab, self.logits,
-                          m.vocab, mx.MX_OUT_FP32, workspace=self.head_workspace)
+        x = m.norm(x)
+        for p in self.parts:
+            mx.mx_linear_bf16(x[p], p.stop - p.start, m.hidden, m.hidden, m.fmt, codes, scales, ts, m.vocab,
+                              self.logits[p], m.vocab, mx.MX_OUT_FP32, workspace=self.head_workspace)
         self.ids.copy_(self.logits.argmax(1))
 
     def decode(self, first, steps):
