@@ -697,8 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 2) {
     warm_digits<FMT>(p.x);
     // (the result is used, so that the call stays)
-    if (act(make_float4(0.0f, 0.0f, 0.0f, 0.0f), a.gelu).x != 0.0f)
-      atomicOr(a.status, kStatusTimeout);
+    asm volatile("" ::"f"(act(make_float4(0.0f, 0.0f, 0.0f, 0.0f), a.gelu).x));
   }
   griddep_wait();
   if constexpr (!X::kByToken) x.fetch_x();

@@ -86,3 +86,12 @@ def test_what_the_lanes_acquired_is_there_for_the_lane_that_copies():
     assert "load_acquire(" in look and "__ballot_sync(" in look
     last = look.rindex("fence.proxy.async.global")
     assert re.search(r"__syncwarp\(\);\s*asm volatile\(\"$", look[:last])
+
+
+def test_a_timeout_is_reported_for_waits_and_misplaced_memory_only():
+    """kStatusTimeout reaches the caller as MX_ERR_DEVICE_TIMEOUT: in the experts' kernel it
+    stands behind the waits' limits and the shared memory's alignment."""
+    text = source("moe_mma.cu")
+    for m in re.finditer(r"atomicOr\([^;]*kStatusTimeout\)", text):
+        before = text[:m.start()].rstrip()
+        assert before.endswith("if (!aligned)") or before.endswith("*x.abort = 1u;"), before[-80:]
