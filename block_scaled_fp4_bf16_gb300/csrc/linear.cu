@@ -398,16 +398,24 @@ __global__ void __launch_bounds__(W * 32, 1) linear_kernel(const __grid_constant
       const int ul = u & 31, mn = u >> 5;
       const int64_t row0 = static_cast<int64_t>(tile) * R + (mn / NT) * 16 + (ul >> 2);
       const int col0 = (mn % NT) * 8 + (ul & 3) * 2;
-      const float f[4] = {v.x, v.y, v.z, v.w};
+      float f[4] = {v.x, v.y, v.z, v.w};
+      const auto in = [&](int i) { return row0 + (i >> 1) * 8 < a.n && col0 + (i & 1) < a.tokens; };
+      bool finite = true;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t row = row0 + (i >> 1) * 8;
-        const int col = col0 + (i & 1);
-        if (row >= a.n || col >= a.tokens) continue;
-        float o = FMT == 1 ? f[i] * alpha : f[i];
-        if (!(fabsf(o) < __uint_as_float(0x7F800000u))) o = wide_sum<FMT>(a, row, col);
-        put_linear(a, row, col, o);
+        if (FMT == 1) f[i] *= alpha;
+        finite = finite && fabsf(f[i]) < __uint_as_float(0x7F800000u);
       }
+      if (!finite) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (in(i) && !(fabsf(f[i]) < __uint_as_float(0x7F800000u)))
+            f[i] = wide_sum<FMT>(a, row0 + (i >> 1) * 8, col0 + (i & 1));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (in(i)) put_linear(a, row0 + (i >> 1) * 8, col0 + (i & 1), f[i]);
     }
     __syncwarp();  // (an output may have taken some lanes through wide_sum)
     if (p.ctas > 1)
