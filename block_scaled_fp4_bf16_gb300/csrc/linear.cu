@@ -7,8 +7,8 @@
 //     in stages of 128 that come by cp.async into a ring of its own, over the end
 //     of one item into the next; the warps meet only to add their sums;
 //   - with fewer items than SMs the CTAs of a cluster divide K and add their sums
-//     through each other's shared memory (1 x 1024 x 8192: 7.3 us, so 4.8; 13 x 1312 x
-//     25408 NVFP4 31.7 us, so 14.5);
+//     through each other's shared memory (1 x 1024 x 8192: 7.3 us, so 4.9; 13 x 1312 x
+//     25408 NVFP4 31.7 us, so 14.7);
 //   - E2M1 becomes FP16 by the conversion instruction, two codes at once, and
 //     multiplies on the 16 x 8 x 16 FP16 product with binary32 sums, the weights on
 //     its 16-row side (measured: 90 codes a clock per SM converted, 128 multiplied);
@@ -20,9 +20,11 @@
 //     overflows, as may the whole sum before a small tensor scale: an output that is not
 //     finite is summed again with more range (wide_sum).
 // It issues about 2.5 instructions a code, which bounds it at 4 TB/s of weights
-// for up to 8 tokens (28672 x 8192: 30 us); linear_mma.cu leaves the weights to the
-// tensor cores.  At 8 x 4096 x 4096 (4.9 us; its bytes 1.4) latency bounds it: a launch,
-// two rounds of copies from memory, the join of the warps.
+// for up to 8 tokens (8 x 28672 x 8192: 32 us); linear_mma.cu leaves the weights to the
+// tensor cores.  At 8 x 4096 x 4096 (5.0 us; its bytes 1.4) latency bounds it: a launch,
+// two rounds of copies from memory, the join of the warps.  Above 16 tokens instructions do
+// (32 x 4096 x 4096: 12.8 us): every item of 32 rows converts all of x again, as many
+// elements as weights, and shared memory holds two stages a warp.
 #include <cuda_fp16.h>
 
 #include "few_tokens.cuh"
@@ -437,7 +439,7 @@ cudaError_t launch(const LinearArgs &a, cudaStream_t s) {
   }
   size_t smem = W * MT * NT * 512 + static_cast<size_t>(W) * S * stage_bytes<FMT, MT>(a.tokens);
   // One CTA an SM: two on one, launched while the kernel before it still holds the
-  // others, share what one SM can do (1 x 4096 x 8192: 11.9 us, so 8.0).
+  // others, share what one SM can do (1 x 4096 x 8192: 11.9 us, so 8.1).
   if (smem <= kMaxSmem / 2) smem = kMaxSmem / 2 + 1024;
   LinearParams p{a, static_cast<int>((a.n + 16 * MT - 1) / (16 * MT)), 1};
   cudaLaunchConfig_t cfg = {};
@@ -497,11 +499,14 @@ cudaError_t launch_fmt(const LinearArgs &a, cudaStream_t s) {
 // launches take 9 to 12 us and then 6 TB/s.  Measured (us, this kernel / that one):
 //                      4096 x 4096   8192 x 4096   8192 x 8192   28672 x 8192   3360 x 19552
 //   (2^20 weights            19            38            76            228            91)
-//   MXFP4   8 tokens:   4.9 /  9.9    8.7 / 13.0   15.1 / 15.1    31.9 / 25.4    17.6 / 14.3
-//          16 tokens:   6.6 / 11.8   12.0 / 14.9   21.3 / 16.6    45.1 / 26.7
-//          32 tokens:  12.4 / 14.8   23.2 / 18.0   43.5 / 20.1   126.1 / 32.8
-//   NVFP4   8 tokens:   5.2 / 10.8    9.4 / 13.3   16.5 / 15.3    36.1 / 27.3    19.1 / 15.7
-//          32 tokens:  12.1 / 14.7   22.6 / 18.9   42.1 / 20.0   122.0 / 35.8
+//   MXFP4   8 tokens:   5.0 /  9.9    9.0 / 13.0   15.2 / 13.9    32.5 / 24.6    17.8 / 13.3
+//          16 tokens:   6.7 / 11.8   12.2 / 14.9   21.3 / 15.5    45.9 / 26.0    24.6 / 14.8
+//          32 tokens:  12.8 / 14.8   24.5 / 15.6   44.5 / 20.0   130.5 / 32.9    50.8 / 22.9
+//   NVFP4   8 tokens:   5.4 / 10.8    9.8 / 13.3   16.8 / 14.4    36.4 / 26.3    19.7 / 14.2
+//          32 tokens:  12.4 / 14.7   23.6 / 15.5   42.9 / 19.4   125.4 / 36.1    49.0 / 26.7
+// The workspace's size follows from it, so it asks no device: it assumes 152 SMs, and that
+// as many clusters of the CTAs wanted are resident as there are tiles (launch() takes fewer
+// CTAs where they are not).
 bool linear_mma_better(int64_t tokens, int64_t n, int64_t k) {
   constexpr int kSms = 152;
   const int64_t rows = tall_items(tokens, n, kSms) ? 64 : 32, tiles = (n + rows - 1) / rows;

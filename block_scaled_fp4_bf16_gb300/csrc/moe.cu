@@ -8,7 +8,7 @@
 // of K are added to binary32 sums; the logits go straight into the shared memory of
 // the CTA that owns the token, and one warp of it chooses.  Registers leave room for two
 // CTAs an SM: with one, seven clusters of 16 are resident and the eighth (64 tokens)
-// runs after them (64 x 8192 of 256: 14.9 us, so 11.0; 1 x 2048 of 64: 3.6 us, latency).
+// runs after them (64 x 8192 of 256: 14.9 us, so 11.0; 1 x 2048 of 64: 3.4 us, latency).
 #include "fp4_digits.cuh"
 
 namespace mx {

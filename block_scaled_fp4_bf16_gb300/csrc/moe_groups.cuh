@@ -7,9 +7,8 @@ namespace mx {
 
 // The pairs sorted by expert (an expert's in ascending order), divided into groups
 // of up to a given size of one expert.  A pair's place is its index in the list.
-// The arrays lie one after the other (bytes(pairs) in all, 16-byte aligned), in
-// shared memory or, as split_kernel leaves them for the later kernels, in the
-// workspace.
+// The arrays lie one after the other (bytes(pairs) in all, 16-byte aligned) in shared
+// memory; every CTA makes its own.
 struct Groups {
   uint16_t *list;    // pairs
   uint16_t *expert;  // of a group
@@ -35,7 +34,7 @@ __device__ __forceinline__ uint16_t pack_member(int group, int index) {
 }
 
 // Whole CTA of W warps.  Fills g; place[pair]: its place (0xFFFF: an empty slot);
-// member[place]: pack_member.  scratch: 4 * W * experts bytes.
+// member[place]: pack_member.  scratch: 2 * (W + 2) * experts bytes.
 // Every CTA that does this gets the same groups.
 template <int W>
 __device__ __forceinline__ void make_groups(const Groups &g, uint16_t *place, uint16_t *member,

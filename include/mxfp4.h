@@ -397,7 +397,12 @@ int nvfp4_gemm_ex(const void *a_codes, const void *a_scales, const void *b_codes
  *   MXFP4: or 2^-126).
  * Infinities and NaN in x reach the outputs of their token and no others; in
  * the experts' products they make all of them NaN.  A UE8M0 scale byte of 255
- * is NaN. */
+ * is NaN.
+ *   mx_linear_bf16 and mx_linear_bf16_workspace: a sum that is infinite or NaN
+ *   in the kernels' units (block scales above 2^104; activations near BF16's
+ *   largest under a small tensor scale; infinities and NaN themselves) is taken
+ *   again term by term with more range, so it is infinite or NaN where the
+ *   formula's is.  Such outputs are slow: one of 4096 of K takes 100 us. */
 
 /* Most rows of x that mx_linear_bf16 takes. */
 #define MX_LINEAR_MAX_TOKENS 32
@@ -497,8 +502,9 @@ size_t mx_moe_workspace_bytes(int64_t tokens, int64_t hidden, int64_t inter, int
  * second product as eight FP4 digits (to within 2^-22 of the largest of their
  * block).  y and the workspace must not overlap an input or each other.  Reads
  * the chosen experts' weights only.  Launches a small kernel and one of a CTA
- * per SM, all resident together (a cooperative launch: it waits for SMs that
- * other streams' kernels hold). */
+ * per SM of the device, all resident together (a cooperative launch: it waits
+ * for SMs that other streams' kernels hold; a context that has been given only
+ * some of the SMs gets the runtime's error). */
 int mx_moe_experts_bf16(const void *x, int64_t tokens, int64_t ld_x, const int32_t *ids,
                         const float *weights, int top_k, const mx_moe_weights *moe, void *y,
                         int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
