@@ -582,6 +582,8 @@ __device__ __forceinline__ float2 mul_f32x2(float2 a, float2 b) {
 // MUFU reciprocal and one exponential per value.  Two values at a time: their
 // multiplies and FMAs are packed pairs; the reciprocal, the exponential and
 // the final select stay per value.
+// From |y| = 15 on Phi(-|y|) is 0 in binary32; past 64 the result is taken as y or
+// -0 outright, because a^2 is infinite from 2^64 on and l then -inf.
 __device__ __forceinline__ float2 gelu_f32x2(float2 y) {
   const auto two = [](float v) { return make_float2(v, v); };
   const float2 a = make_float2(fabsf(y.x), fabsf(y.y));
@@ -608,8 +610,11 @@ __device__ __forceinline__ float2 gelu_f32x2(float2 y) {
   ex = fma_f32x2(ex, r, ex);                         // exp(arg + r)
   const float2 phi = mul_f32x2(t, ex);  // Phi(-|y|)
   const float2 yp = mul_f32x2(y, phi);
-  return make_float2(y.x > 0.0f ? __fsub_rn(y.x, yp.x) : yp.x,
-                     y.y > 0.0f ? __fsub_rn(y.y, yp.y) : yp.y);
+  const auto pick = [](float v, float vp) {
+    const float g = v > 0.0f ? __fsub_rn(v, vp) : vp;
+    return fabsf(v) > 64.0f ? fmaxf(v, -0.0f) : g;
+  };
+  return make_float2(pick(y.x, yp.x), pick(y.y, yp.y));
 }
 
 // GEMM epilogue of N consecutive outputs of one row (N = 4 or 8; idx = the

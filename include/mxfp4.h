@@ -349,8 +349,8 @@ int nvfp4_gemm(const void *a_codes, const void *a_scales, const void *b_codes,
  * them to mxfp4_gemm / nvfp4_gemm as one optional epilogue:
  *   D[i, j] = act(alpha * sum_k A[i, k] B[j, k] + beta * D_in[i, j] + bias[j])
  * with act = GELU(y) = y * Phi(y) (Phi the standard normal CDF, the erf form
- * of GELU) when gelu == 1, the identity when gelu == 0; alpha = 1 for MXFP4
- * and s_tA * s_tB for NVFP4.  Each term is one binary32 operation on the
+ * of GELU; inf for inf, 0 for -inf) when gelu == 1, the identity when gelu == 0;
+ * alpha = 1 for MXFP4 and s_tA * s_tB for NVFP4.  Each term is one binary32 operation on the
  * FP32 accumulator, in the order written (beta * D_in by one FMA); the
  * result is then rounded once to the output type.  D_in is the content of D
  * before the call, in the output type; with beta == 0 it is not read (D is
