@@ -23,4 +23,8 @@ from ._binding import (  # noqa: F401
     MX_LINEAR_MAX_TOKENS,
     mx_moe_route_bf16, mx_moe_experts_bf16, mx_moe_layer_bf16, mx_moe_workspace_bytes,
     mx_moe_matrix, mx_moe_weights, moe_weights, MX_ACT_SILU, MX_ACT_GELU, MX_MOE_MAX_TOKENS,
-    MX_MOE_MAX_EXPERTS, MX_MOE_MAX_TOP_K)
+    MX_MOE_MAX_EXPERTS, MX_MOE_MAX_TOP_K, MX_ERR_DEVICE_INDEX,
+    mx_qk_norm, qk_norm, mx_qk_norm_rope_bf16, mx_qk_norm_rope_backward_bf16,
+    mx_qk_norm_rope_backward_workspace_bytes, MX_CACHE_BLOCK, mx_kv_cache, kv_cache,
+    mx_kv_append_bf16, mx_attention_bf16, mx_attention_workspace_bytes, MX_ATTENTION_MAX_QUERY,
+    MX_ATTENTION_MAX_SEQUENCES, mx_sample, MX_SAMPLE_MAX_VOCAB)

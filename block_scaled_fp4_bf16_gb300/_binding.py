@@ -30,6 +30,7 @@ MX_ERR_WORKSPACE = -7
 MX_ERR_CUDA = -8
 MX_ERR_DEVICE_TIMEOUT = -9
 MX_ERR_DEVICE_BOUNDS = -10
+MX_ERR_DEVICE_INDEX = -11
 
 MX_FMT_MXFP4 = 0
 MX_FMT_NVFP4 = 1
@@ -52,6 +53,10 @@ MX_MOE_MAX_EXPERTS = 512
 MX_MOE_MAX_TOP_K = 16
 MX_ACT_SILU = 0
 MX_ACT_GELU = 1
+MX_CACHE_BLOCK = 32
+MX_ATTENTION_MAX_QUERY = 16
+MX_ATTENTION_MAX_SEQUENCES = 4096
+MX_SAMPLE_MAX_VOCAB = 262144
 
 _lock = threading.Lock()
 _lib = None
@@ -80,6 +85,23 @@ class mx_moe_weights(ctypes.Structure):
     _fields_ = [("format", ctypes.c_int), ("activation", ctypes.c_int),
                 ("experts", ctypes.c_int64), ("hidden", ctypes.c_int64), ("inter", ctypes.c_int64),
                 ("gate", mx_moe_matrix), ("up", mx_moe_matrix), ("down", mx_moe_matrix)]
+
+
+class mx_qk_norm(ctypes.Structure):
+    """include/mxfp4.h: norm and rotation of a layer's queries and keys (see qk_norm)."""
+    _fields_ = [("q_heads", ctypes.c_int64), ("k_heads", ctypes.c_int64),
+                ("head_dim", ctypes.c_int64), ("rotary_dim", ctypes.c_int64),
+                ("interleaved", ctypes.c_int), ("eps", ctypes.c_float),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("inv_freq", ctypes.c_void_p)]
+
+
+class mx_kv_cache(ctypes.Structure):
+    """include/mxfp4.h: a paged cache of keys and values (see kv_cache)."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_codes", ctypes.c_void_p), ("v_scales", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_tokens", ctypes.c_int64),
+                ("kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
 
 
 class MXError(RuntimeError):
@@ -168,6 +190,23 @@ def lib() -> ctypes.CDLL:
         L.mx_moe_layer_bf16.restype = i32
         L.mx_moe_layer_bf16.argtypes = [vp, i64, i64, vp, vp, i32, i32, mw, vp, vp, vp, i64, vp, sz,
                                         vp]
+        nm, kc, f32 = ctypes.POINTER(mx_qk_norm), ctypes.POINTER(mx_kv_cache), ctypes.c_float
+        L.mx_qk_norm_rope_bf16.restype = i32
+        L.mx_qk_norm_rope_bf16.argtypes = [vp, i64, vp, i64, i64, vp, nm, vp, i64, vp, i64, vp]
+        L.mx_qk_norm_rope_backward_workspace_bytes.restype = sz
+        L.mx_qk_norm_rope_backward_workspace_bytes.argtypes = [i64, nm]
+        L.mx_qk_norm_rope_backward_bf16.restype = i32
+        L.mx_qk_norm_rope_backward_bf16.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i64, vp, nm, vp,
+                                                    i64, vp, i64, vp, vp, vp, sz, vp]
+        L.mx_kv_append_bf16.restype = i32
+        L.mx_kv_append_bf16.argtypes = [vp, i64, vp, i64, i64, vp, vp, i64, vp, i64, kc, vp]
+        L.mx_attention_workspace_bytes.restype = sz
+        L.mx_attention_workspace_bytes.argtypes = [i64, i64, i64, kc]
+        L.mx_attention_bf16.restype = i32
+        L.mx_attention_bf16.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, kc, f32, i64, vp, i64, vp,
+                                        vp, sz, vp]
+        L.mx_sample.restype = i32
+        L.mx_sample.argtypes = [vp, i64, i64, i64, i32, vp, vp, vp, vp, vp, vp, vp, vp]
         L.mx_device_status.restype = i32
         L.mx_device_status.argtypes = [vp]
         L.mx_selftest_wait_timeout.restype = i32
@@ -459,6 +498,84 @@ def mx_moe_layer_bf16(x, tokens, ld_x, router, router_bias, top_k, normalize, mo
         _ptr(x), tokens, ld_x, _ptr(router), _ptr(router_bias), top_k, int(normalize), moe,
         _ptr(ids), _ptr(weights), _ptr(y), ld_y, _ptr(workspace), workspace_bytes,
         _stream(stream)))
+
+
+def qk_norm(q_heads, k_heads, head_dim, q_weight, k_weight, inv_freq, rotary_dim=None,
+            interleaved=False, eps=1e-6):
+    """The descriptor of a layer's norm and rotation of queries and keys.  rotary_dim None:
+    2 * inv_freq.numel(), all rotating channels.  It is made once and keeps the tensors alive."""
+    if rotary_dim is None:
+        rotary_dim = 0 if inv_freq is None else 2 * inv_freq.numel()
+    n = mx_qk_norm(q_heads, k_heads, head_dim, rotary_dim, int(interleaved), eps, _ptr(q_weight),
+                   _ptr(k_weight), _ptr(inv_freq))
+    n.tensors = (q_weight, k_weight, inv_freq)
+    return n
+
+
+def mx_qk_norm_rope_bf16(q, ld_q, k, ld_k, tokens, positions, norm, q_out, ld_q_out, k_out, ld_k_out,
+                         stream=None):
+    """norm: an mx_qk_norm (qk_norm); q_out may be q, k_out may be k."""
+    return _check("mx_qk_norm_rope_bf16", lib().mx_qk_norm_rope_bf16(
+        _ptr(q), ld_q, _ptr(k), ld_k, tokens, _ptr(positions), norm, _ptr(q_out), ld_q_out,
+        _ptr(k_out), ld_k_out, _stream(stream)))
+
+
+def mx_qk_norm_rope_backward_workspace_bytes(tokens: int, norm) -> int:
+    return lib().mx_qk_norm_rope_backward_workspace_bytes(tokens, norm)
+
+
+def mx_qk_norm_rope_backward_bf16(q, ld_q, k, ld_k, dq_out, ld_dq_out, dk_out, ld_dk_out, tokens,
+                                  positions, norm, dq, ld_dq, dk, ld_dk, dq_weight=None,
+                                  dk_weight=None, workspace=None, workspace_bytes=None, stream=None):
+    """Gradients of mx_qk_norm_rope_bf16 (q, k: its inputs)."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
+    return _check("mx_qk_norm_rope_backward_bf16", lib().mx_qk_norm_rope_backward_bf16(
+        _ptr(q), ld_q, _ptr(k), ld_k, _ptr(dq_out), ld_dq_out, _ptr(dk_out), ld_dk_out, tokens,
+        _ptr(positions), norm, _ptr(dq), ld_dq, _ptr(dk), ld_dk, _ptr(dq_weight), _ptr(dk_weight),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def kv_cache(k_codes, k_scales, v_codes, v_scales, pages, page_tokens, kv_heads, head_dim):
+    """The descriptor of a layer's cache: codes [pages, kv_heads, page_tokens, head_dim] and
+    scales [pages, kv_heads, page_tokens / MX_CACHE_BLOCK], one byte each.  It is made once and
+    keeps the tensors alive."""
+    c = mx_kv_cache(_ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), pages, page_tokens,
+                    kv_heads, head_dim)
+    c.tensors = (k_codes, k_scales, v_codes, v_scales)
+    return c
+
+
+def mx_kv_append_bf16(k, ld_k, v, ld_v, tokens, starts, page_table, max_pages, lengths, sequences,
+                      cache, stream=None):
+    """cache: an mx_kv_cache (kv_cache); lengths hold the new tokens already."""
+    return _check("mx_kv_append_bf16", lib().mx_kv_append_bf16(
+        _ptr(k), ld_k, _ptr(v), ld_v, tokens, _ptr(starts), _ptr(page_table), max_pages,
+        _ptr(lengths), sequences, cache, _stream(stream)))
+
+
+def mx_attention_workspace_bytes(sequences: int, q_tokens: int, q_heads: int, cache) -> int:
+    return lib().mx_attention_workspace_bytes(sequences, q_tokens, q_heads, cache)
+
+
+def mx_attention_bf16(q, ld_q, q_heads, sequences, q_tokens, page_table, max_pages, lengths, cache,
+                      scale, window, out, ld_out, lse=None, workspace=None, workspace_bytes=None,
+                      stream=None):
+    """cache: an mx_kv_cache (kv_cache) that holds the query tokens too; window 0: none."""
+    if workspace_bytes is None:
+        workspace_bytes = _nbytes(workspace) if not isinstance(workspace, int) else 0
+    return _check("mx_attention_bf16", lib().mx_attention_bf16(
+        _ptr(q), ld_q, q_heads, sequences, q_tokens, _ptr(page_table), max_pages, _ptr(lengths), cache,
+        scale, window, _ptr(out), ld_out, _ptr(lse), _ptr(workspace), workspace_bytes,
+        _stream(stream)))
+
+
+def mx_sample(logits, rows, vocab, ld, dtype, temperature, top_k, top_p, min_p, uniform, ids,
+              probability=None, stream=None):
+    """temperature, top_k, top_p, min_p: one a row, or None."""
+    return _check("mx_sample", lib().mx_sample(
+        _ptr(logits), rows, vocab, ld, dtype, _ptr(temperature), _ptr(top_k), _ptr(top_p),
+        _ptr(min_p), _ptr(uniform), _ptr(ids), _ptr(probability), _stream(stream)))
 
 
 def mx_device_status(stream=None) -> int:

@@ -21,9 +21,9 @@ OUT_DIR = os.path.join(PKG, "_build_bounds" if BOUNDS_CHECK else "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libmxfp4.so")
 SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "gemm_pair.cu", "gemm_swap.cu", "static_ws.cu",
            "calibrate.cu", "transpose.cu", "linear.cu", "linear_mma.cu", "moe.cu",
-           "moe_mma.cu"]
+           "moe_mma.cu", "qk_rope.cu", "kv_append.cu", "attention.cu", "sample.cu"]
 HEADERS = ["mx_device.cuh", "mx_internal.h", "few_tokens.h", "few_tokens.cuh", "fp4_digits.cuh",
-           "moe_groups.cuh"]
+           "moe_groups.cuh", "decode.h", "kv_cache.cuh"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + [

@@ -12,9 +12,11 @@
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
+#include <cstring>
 #include <mutex>
 #include <vector>
 
+#include "decode.h"
 #include "few_tokens.h"
 #include "mx_internal.h"
 #include "mxfp4.h"
@@ -29,6 +31,13 @@ namespace {
 thread_local char t_detail[256] = "";
 
 void clear_detail() { t_detail[0] = '\0'; }
+
+// Leaves the detail as it was (for checks in calls that return no status).
+struct KeepDetail {
+  char was[sizeof t_detail];
+  KeepDetail() { memcpy(was, t_detail, sizeof was); }
+  ~KeepDetail() { memcpy(t_detail, was, sizeof was); }
+};
 
 __attribute__((format(printf, 2, 3))) int fail(int code, const char *fmt, ...) {
   va_list ap;
@@ -396,6 +405,7 @@ MX_API const char *mx_error_string(int code) {
     case MX_ERR_CUDA: return "CUDA runtime, driver or launch error";
     case MX_ERR_DEVICE_TIMEOUT: return "a bounded device-side wait ran out";
     case MX_ERR_DEVICE_BOUNDS: return "bounds-checked build: a kernel access outside its buffer";
+    case MX_ERR_DEVICE_INDEX: return "a page, length or row number in device memory is out of range";
     default: return "unknown status code";
   }
 }
@@ -1311,6 +1321,468 @@ MX_API int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const 
   return launch_rc(fn, e != cudaSuccess ? e : mx::launch_moe_experts(a, s));
 }
 
+// ---- the rest of a decoding step
+
+namespace {
+
+// A strided block of rows in device memory.
+struct Rows {
+  const char *name;
+  const void *p;
+  int64_t rows, cols, ld;
+};
+
+// Do two blocks of 2-byte elements share an element?  Blocks of one stride may lie in each
+// other's gaps; otherwise their whole ranges count.
+bool rows_overlap(const Rows &a, const Rows &b) {
+  const Range ra = span(a.p, row_bytes(a.rows, a.cols, a.ld, 2)), rb = span(b.p, row_bytes(b.rows, b.cols, b.ld, 2));
+  if (!a.p || !b.p || !overlap(ra, rb)) return false;
+  if (a.ld != b.ld) return true;
+  const uint64_t pitch = static_cast<uint64_t>(a.ld) * 2, wa = static_cast<uint64_t>(a.cols) * 2,
+                 wb = static_cast<uint64_t>(b.cols) * 2;
+  const uint64_t d = rb.lo >= ra.lo ? (rb.lo - ra.lo) % pitch : (pitch - (ra.lo - rb.lo) % pitch) % pitch;
+  return d < wa || d + wb > pitch;
+}
+
+// A block of `heads` heads: present iff there are heads, aligned, its stride wide enough.
+int rows_check(const char *fn, const Rows &r) {
+  if (r.cols == 0) {
+    if (r.p) return fail(MX_ERR_INVALID_ARG, "%s: %s must be null: it has no heads", fn, r.name);
+    return MX_OK;
+  }
+  if (!r.p) return fail(MX_ERR_INVALID_ARG, "%s: %s is null", fn, r.name);
+  if (r.ld < r.cols || r.ld >= (int64_t(1) << 31))
+    return fail(MX_ERR_INVALID_ARG, "%s: row stride %lld of %s (%lld .. 2^31 - 1)", fn,
+                static_cast<long long>(r.ld), r.name, static_cast<long long>(r.cols));
+  if (!aligned16(r.p) || r.ld % 8 != 0)
+    return fail(MX_ERR_ALIGNMENT, "%s: %s %s", fn, r.name,
+                !aligned16(r.p) ? "is not 16-byte aligned"
+                                : "has a row stride that is not a multiple of 8 elements (16 bytes)");
+  return MX_OK;
+}
+
+int qk_norm_check(const char *fn, const mx_qk_norm *n, int64_t tokens) {
+  if (!n) return fail(MX_ERR_INVALID_ARG, "%s: the norm's descriptor is null", fn);
+  if (tokens < 0 || tokens >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: tokens = %lld (0 .. 2^31 - 1)", fn, static_cast<long long>(tokens));
+  if (n->q_heads < 0 || n->k_heads < 0 || n->q_heads > 65535 || n->k_heads > 65535 || n->q_heads + n->k_heads == 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: %lld query and %lld key heads (0..65535, one at least)", fn,
+                static_cast<long long>(n->q_heads), static_cast<long long>(n->k_heads));
+  if (n->head_dim < 16 || n->head_dim > mx::kRopeMaxDim || n->head_dim % 16 != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: head_dim = %lld (a multiple of 16, 16..%d)", fn,
+                static_cast<long long>(n->head_dim), mx::kRopeMaxDim);
+  if (n->rotary_dim < 0 || n->rotary_dim > n->head_dim || n->rotary_dim % 16 != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: rotary_dim = %lld (a multiple of 16, 0..head_dim)", fn,
+                static_cast<long long>(n->rotary_dim));
+  if (n->interleaved != 0 && n->interleaved != 1)
+    return fail(MX_ERR_INVALID_ARG, "%s: interleaved = %d (0 or 1)", fn, n->interleaved);
+  if (!(n->eps >= 0.0f) || n->eps > 3.0e38f)
+    return fail(MX_ERR_INVALID_ARG, "%s: eps = %g (0 or more, finite)", fn, static_cast<double>(n->eps));
+  if ((n->rotary_dim > 0) != (n->inv_freq != nullptr))
+    return fail(MX_ERR_INVALID_ARG, "%s: inv_freq %s", fn,
+                n->inv_freq ? "must be null when rotary_dim is 0" : "is null");
+  if (!aligned16(n->q_weight) || !aligned16(n->k_weight))
+    return fail(MX_ERR_ALIGNMENT, "%s: %s is not 16-byte aligned", fn, aligned16(n->q_weight) ? "k_weight" : "q_weight");
+  if (!aligned4(n->inv_freq)) return fail(MX_ERR_ALIGNMENT, "%s: inv_freq is not 4-byte aligned", fn);
+  return MX_OK;
+}
+
+// Outputs (and plain ranges among them) against inputs and one another.
+int rows_disjoint(const char *fn, const Rows *out, int nout, const Rows *in, int nin, const Range *small_out,
+                  int nsmall_out, const Range *small_in, int nsmall_in, bool in_place) {
+  auto range = [](const Rows &r) { return span(r.p, row_bytes(r.rows, r.cols, r.ld, 2)); };
+  for (int o = 0; o < nout; ++o) {
+    for (int i = 0; i < nin; ++i) {
+      if (in_place && i == o && out[o].p == in[i].p && out[o].ld == in[i].ld) continue;
+      if (rows_overlap(out[o], in[i]))
+        return fail(MX_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out[o].name, in[i].name);
+    }
+    for (int p = o + 1; p < nout; ++p)
+      if (rows_overlap(out[o], out[p]))
+        return fail(MX_ERR_INVALID_ARG, "%s: %s overlaps %s", fn, out[o].name, out[p].name);
+    for (int i = 0; i < nsmall_in; ++i)
+      if (overlap(range(out[o]), small_in[i]))
+        return fail(MX_ERR_INVALID_ARG, "%s: %s overlaps an input", fn, out[o].name);
+    for (int p = 0; p < nsmall_out; ++p)
+      if (overlap(range(out[o]), small_out[p]))
+        return fail(MX_ERR_INVALID_ARG, "%s: %s overlaps another output or the workspace", fn, out[o].name);
+  }
+  for (int p = 0; p < nsmall_out; ++p)
+    for (int i = 0; i < nin; ++i)
+      if (overlap(small_out[p], range(in[i])))
+        return fail(MX_ERR_INVALID_ARG, "%s: an output or the workspace overlaps %s", fn, in[i].name);
+  return check_disjoint(fn, small_out, nsmall_out, small_in, nsmall_in);
+}
+
+mx::Heads heads_of(const void *x, int64_t ld, const void *dy, int64_t ld_dy, void *y, int64_t ld_y,
+                   const void *weight, float *dweight, int64_t heads) {
+  mx::Heads h;
+  h.x = static_cast<const uint16_t *>(x);
+  h.ld = ld;
+  h.dy = static_cast<const uint16_t *>(dy);
+  h.ld_dy = ld_dy;
+  h.y = static_cast<uint16_t *>(y);
+  h.ld_y = ld_y;
+  h.weight = static_cast<const uint16_t *>(weight);
+  h.dweight = dweight;
+  h.heads = static_cast<int>(heads);
+  return h;
+}
+
+void rope_args(mx::RopeArgs *a, int64_t tokens, const int32_t *positions, const mx_qk_norm *norm,
+               const DeviceInfo *dev) {
+  a->tokens = tokens;
+  a->positions = positions;
+  a->inv_freq = norm->inv_freq;
+  a->head_dim = static_cast<int>(norm->head_dim);
+  a->rotary_dim = static_cast<int>(norm->rotary_dim);
+  a->interleaved = norm->interleaved;
+  a->eps = norm->eps;
+  a->partials = nullptr;
+  a->num_sms = dev->num_sms;
+  a->status = dev->status;
+}
+
+int positions_check(const char *fn, const int32_t *positions) {
+  if (!positions) return fail(MX_ERR_INVALID_ARG, "%s: positions is null", fn);
+  if (!aligned4(positions)) return fail(MX_ERR_ALIGNMENT, "%s: positions is not 4-byte aligned", fn);
+  return MX_OK;
+}
+
+void norm_ranges(const mx_qk_norm *n, const int32_t *positions, int64_t tokens, Range *out) {
+  out[0] = span(positions, static_cast<uint64_t>(tokens) * 4);
+  out[1] = span(n->inv_freq, static_cast<uint64_t>(n->rotary_dim / 2) * 4);
+  out[2] = span(n->q_weight, static_cast<uint64_t>(n->head_dim) * 2);
+  out[3] = span(n->k_weight, static_cast<uint64_t>(n->head_dim) * 2);
+}
+
+}  // namespace
+
+MX_API int mx_qk_norm_rope_bf16(const void *q, int64_t ld_q, const void *k, int64_t ld_k, int64_t tokens,
+                                const int32_t *positions, const mx_qk_norm *norm, void *q_out,
+                                int64_t ld_q_out, void *k_out, int64_t ld_k_out, void *stream) {
+  clear_detail();
+  const char *fn = "mx_qk_norm_rope_bf16";
+  int rc = qk_norm_check(fn, norm, tokens);
+  if (rc == MX_OK) rc = positions_check(fn, positions);
+  if (rc != MX_OK) return rc;
+  const int64_t qc = norm->q_heads * norm->head_dim, kc = norm->k_heads * norm->head_dim;
+  const Rows in[2] = {{"q", q, tokens, qc, ld_q}, {"k", k, tokens, kc, ld_k}};
+  const Rows out[2] = {{"q_out", q_out, tokens, qc, ld_q_out}, {"k_out", k_out, tokens, kc, ld_k_out}};
+  for (int i = 0; i < 2 && rc == MX_OK; ++i) rc = rows_check(fn, in[i]);
+  for (int i = 0; i < 2 && rc == MX_OK; ++i) rc = rows_check(fn, out[i]);
+  if (rc != MX_OK) return rc;
+  Range small[4];
+  norm_ranges(norm, positions, tokens, small);
+  rc = rows_disjoint(fn, out, 2, in, 2, nullptr, 0, small, 4, true);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0) return MX_OK;
+  mx::RopeArgs a;
+  rope_args(&a, tokens, positions, norm, dev);
+  a.part[0] = heads_of(q, ld_q, nullptr, 0, q_out, ld_q_out, norm->q_weight, nullptr, norm->q_heads);
+  a.part[1] = heads_of(k, ld_k, nullptr, 0, k_out, ld_k_out, norm->k_weight, nullptr, norm->k_heads);
+  return launch_rc(fn, mx::launch_qk_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+MX_API size_t mx_qk_norm_rope_backward_workspace_bytes(int64_t tokens, const mx_qk_norm *norm) {
+  const KeepDetail keep;
+  if (qk_norm_check("mx_qk_norm_rope_backward_workspace_bytes", norm, tokens) != MX_OK) return 0;
+  return static_cast<size_t>(mx::kRopeBackCtas) * 2 * static_cast<size_t>(norm->head_dim) * sizeof(float);
+}
+
+MX_API int mx_qk_norm_rope_backward_bf16(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                         const void *dq_out, int64_t ld_dq_out, const void *dk_out,
+                                         int64_t ld_dk_out, int64_t tokens, const int32_t *positions,
+                                         const mx_qk_norm *norm, void *dq, int64_t ld_dq, void *dk,
+                                         int64_t ld_dk, float *dq_weight, float *dk_weight,
+                                         void *workspace, size_t workspace_bytes, void *stream) {
+  const char *fn = "mx_qk_norm_rope_backward_bf16";
+  clear_detail();
+  const size_t need = mx_qk_norm_rope_backward_workspace_bytes(tokens, norm);
+  int rc = qk_norm_check(fn, norm, tokens);
+  if (rc == MX_OK) rc = positions_check(fn, positions);
+  if (rc != MX_OK) return rc;
+  const int64_t qc = norm->q_heads * norm->head_dim, kc = norm->k_heads * norm->head_dim;
+  const Rows in[4] = {{"q", q, tokens, qc, ld_q},
+                      {"k", k, tokens, kc, ld_k},
+                      {"dq_out", dq_out, tokens, qc, ld_dq_out},
+                      {"dk_out", dk_out, tokens, kc, ld_dk_out}};
+  const Rows out[2] = {{"dq", dq, tokens, qc, ld_dq}, {"dk", dk, tokens, kc, ld_dk}};
+  for (int i = 0; i < 4 && rc == MX_OK; ++i) rc = rows_check(fn, in[i]);
+  for (int i = 0; i < 2 && rc == MX_OK; ++i) rc = rows_check(fn, out[i]);
+  if (rc != MX_OK) return rc;
+  if ((dq_weight && !norm->q_weight) || (dk_weight && !norm->k_weight))
+    return fail(MX_ERR_INVALID_ARG, "%s: %s must be null: there is no such weight", fn,
+                dq_weight && !norm->q_weight ? "dq_weight" : "dk_weight");
+  if (!aligned4(dq_weight) || !aligned4(dk_weight))
+    return fail(MX_ERR_ALIGNMENT, "%s: %s is not 4-byte aligned", fn, aligned4(dq_weight) ? "dk_weight" : "dq_weight");
+  const bool weights = dq_weight || dk_weight;
+  if (weights) {
+    if (!workspace || workspace_bytes < need)
+      return fail(MX_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes, got %zu%s", fn, need,
+                  workspace ? workspace_bytes : size_t(0), workspace ? "" : " (null)");
+    if (!aligned16(workspace)) return fail(MX_ERR_ALIGNMENT, "%s: workspace is not 16-byte aligned", fn);
+  }
+  Range small_in[4];
+  norm_ranges(norm, positions, tokens, small_in);
+  const uint64_t dw = static_cast<uint64_t>(norm->head_dim) * 4;
+  const Range small_out[3] = {span(dq_weight, dw), span(dk_weight, dw), span(weights ? workspace : nullptr, need)};
+  rc = rows_disjoint(fn, out, 2, in, 4, small_out, 3, small_in, 4, false);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0 && !weights) return MX_OK;
+  mx::RopeArgs a;
+  rope_args(&a, tokens, positions, norm, dev);
+  a.part[0] = heads_of(q, ld_q, dq_out, ld_dq_out, dq, ld_dq, norm->q_weight, dq_weight, norm->q_heads);
+  a.part[1] = heads_of(k, ld_k, dk_out, ld_dk_out, dk, ld_dk, norm->k_weight, dk_weight, norm->k_heads);
+  if (weights) a.partials = static_cast<float *>(workspace);
+  return launch_rc(fn, mx::launch_qk_rope_backward(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+static_assert(MX_CACHE_BLOCK == mx::kCacheBlock && MX_ATTENTION_MAX_QUERY == mx::kAttentionMaxQuery &&
+                  MX_ATTENTION_MAX_SEQUENCES == mx::kAttentionMaxSequences &&
+                  MX_SAMPLE_MAX_VOCAB == mx::kSampleMaxVocab,
+              "limits of the decoding step");
+
+int cache_shape_check(const char *fn, const mx_kv_cache *c) {
+  if (!c) return fail(MX_ERR_INVALID_ARG, "%s: the cache's descriptor is null", fn);
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: head_dim = %lld (64, 128 or 256)", fn,
+                static_cast<long long>(c->head_dim));
+  if (c->kv_heads < 1 || c->kv_heads > 1024)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: kv_heads = %lld (1..1024)", fn, static_cast<long long>(c->kv_heads));
+  if (c->page_tokens < MX_CACHE_BLOCK || c->page_tokens > (1 << 20) || c->page_tokens % MX_CACHE_BLOCK != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: page_tokens = %lld (a multiple of %d up to 2^20)", fn,
+                static_cast<long long>(c->page_tokens), MX_CACHE_BLOCK);
+  if (c->pages < 1 || c->pages >= (int64_t(1) << 31))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: pages = %lld (1 .. 2^31 - 1)", fn, static_cast<long long>(c->pages));
+  return MX_OK;
+}
+
+// The cache, the page table and the lengths; fills the kernels' view and the six ranges
+// (codes and scales of keys and values, page table, lengths).
+int cache_check(const char *fn, const mx_kv_cache *c, const int32_t *page_table, int64_t max_pages,
+                const int32_t *lengths, int64_t sequences, int64_t most, mx::CacheArgs *a, Range *ranges) {
+  const int rc = cache_shape_check(fn, c);
+  if (rc != MX_OK) return rc;
+  if (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales)
+    return fail(MX_ERR_INVALID_ARG, "%s: the cache's codes or scales are null", fn);
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales))
+    return fail(MX_ERR_ALIGNMENT, "%s: the cache's codes or scales are not 16-byte aligned", fn);
+  if (!page_table || !lengths)
+    return fail(MX_ERR_INVALID_ARG, "%s: %s is null", fn, !page_table ? "page_table" : "lengths");
+  if (!aligned4(page_table) || !aligned4(lengths))
+    return fail(MX_ERR_ALIGNMENT, "%s: %s is not 4-byte aligned", fn, !aligned4(page_table) ? "page_table" : "lengths");
+  if (sequences < 0 || sequences > most)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: sequences = %lld (0..%lld)", fn, static_cast<long long>(sequences),
+                static_cast<long long>(most));
+  if (max_pages < 1 || max_pages > (int64_t(1) << 24))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: max_pages = %lld (1 .. 2^24)", fn, static_cast<long long>(max_pages));
+  a->codes[0] = static_cast<uint8_t *>(c->k_codes);
+  a->codes[1] = static_cast<uint8_t *>(c->v_codes);
+  a->scales[0] = static_cast<uint8_t *>(c->k_scales);
+  a->scales[1] = static_cast<uint8_t *>(c->v_scales);
+  a->pages = c->pages;
+  a->page_tokens = static_cast<int>(c->page_tokens);
+  a->heads = static_cast<int>(c->kv_heads);
+  a->head_dim = static_cast<int>(c->head_dim);
+  a->table = page_table;
+  a->max_pages = max_pages;
+  a->lengths = lengths;
+  a->sequences = static_cast<int>(sequences);
+  a->status = nullptr;
+  const uint64_t rows = static_cast<uint64_t>(c->pages) * static_cast<uint64_t>(c->kv_heads);
+  const uint64_t codes = rows * static_cast<uint64_t>(c->page_tokens * c->head_dim);
+  const uint64_t scales = rows * static_cast<uint64_t>(c->page_tokens / MX_CACHE_BLOCK);
+  ranges[0] = span(c->k_codes, codes);
+  ranges[1] = span(c->k_scales, scales);
+  ranges[2] = span(c->v_codes, codes);
+  ranges[3] = span(c->v_scales, scales);
+  ranges[4] = span(page_table, static_cast<uint64_t>(sequences) * static_cast<uint64_t>(max_pages) * 4);
+  ranges[5] = span(lengths, static_cast<uint64_t>(sequences) * 4);
+  return MX_OK;
+}
+
+}  // namespace
+
+MX_API int mx_kv_append_bf16(const void *k, int64_t ld_k, const void *v, int64_t ld_v, int64_t tokens,
+                             const int32_t *starts, const int32_t *page_table, int64_t max_pages,
+                             const int32_t *lengths, int64_t sequences, const mx_kv_cache *cache,
+                             void *stream) {
+  clear_detail();
+  const char *fn = "mx_kv_append_bf16";
+  mx::AppendArgs a;
+  Range ranges[6];
+  int rc = cache_check(fn, cache, page_table, max_pages, lengths, sequences, 65535, &a.c, ranges);
+  if (rc != MX_OK) return rc;
+  if (tokens < 0 || tokens > (int64_t(1) << 30))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: tokens = %lld (0 .. 2^30)", fn, static_cast<long long>(tokens));
+  if (!starts && sequences > 0 && tokens % sequences != 0)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: %lld tokens for %lld sequences without starts", fn,
+                static_cast<long long>(tokens), static_cast<long long>(sequences));
+  const int64_t cols = cache->kv_heads * cache->head_dim;
+  const Rows in[2] = {{"k", k, tokens, cols, ld_k}, {"v", v, tokens, cols, ld_v}};
+  for (int i = 0; i < 2 && rc == MX_OK; ++i) rc = rows_check(fn, in[i]);
+  if (rc != MX_OK) return rc;
+  if (!aligned4(starts)) return fail(MX_ERR_ALIGNMENT, "%s: starts is not 4-byte aligned", fn);
+  const Range inputs[5] = {span(k, row_bytes(tokens, cols, ld_k, 2)), span(v, row_bytes(tokens, cols, ld_v, 2)),
+                           ranges[4], ranges[5], span(starts, static_cast<uint64_t>(sequences + 1) * 4)};
+  rc = check_disjoint(fn, ranges, 4, inputs, 5);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (tokens == 0 || sequences == 0) return MX_OK;
+  a.c.status = dev->status;
+  a.x[0] = static_cast<const uint16_t *>(k);
+  a.x[1] = static_cast<const uint16_t *>(v);
+  a.ld[0] = ld_k;
+  a.ld[1] = ld_v;
+  a.tokens = tokens;
+  a.starts = starts;
+  return launch_rc(fn, mx::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+int attention_shape_check(const char *fn, int64_t sequences, int64_t q_tokens, int64_t q_heads,
+                          const mx_kv_cache *cache) {
+  const int rc = cache_shape_check(fn, cache);
+  if (rc != MX_OK) return rc;
+  if (sequences < 0 || sequences > MX_ATTENTION_MAX_SEQUENCES)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: sequences = %lld (0..%d)", fn, static_cast<long long>(sequences),
+                MX_ATTENTION_MAX_SEQUENCES);
+  if (q_tokens < 1 || q_tokens > MX_ATTENTION_MAX_QUERY)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: q_tokens = %lld (1..%d)", fn, static_cast<long long>(q_tokens),
+                MX_ATTENTION_MAX_QUERY);
+  if (q_heads < cache->kv_heads || q_heads % cache->kv_heads != 0 ||
+      q_heads / cache->kv_heads > mx::kAttentionMaxGroup)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: q_heads = %lld (a multiple of kv_heads = %lld, at most %d times)", fn,
+                static_cast<long long>(q_heads), static_cast<long long>(cache->kv_heads), mx::kAttentionMaxGroup);
+  return MX_OK;
+}
+
+}  // namespace
+
+MX_API size_t mx_attention_workspace_bytes(int64_t sequences, int64_t q_tokens, int64_t q_heads,
+                                           const mx_kv_cache *cache) {
+  const KeepDetail keep;
+  if (attention_shape_check("mx_attention_workspace_bytes", sequences, q_tokens, q_heads, cache) != MX_OK) return 0;
+  return mx::attention_workspace_bytes(sequences, q_heads / cache->kv_heads * q_tokens,
+                                       static_cast<int>(cache->head_dim));
+}
+
+MX_API int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64_t sequences,
+                             int64_t q_tokens, const int32_t *page_table, int64_t max_pages,
+                             const int32_t *lengths, const mx_kv_cache *cache, float scale,
+                             int64_t window, void *out, int64_t ld_out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream) {
+  const char *fn = "mx_attention_bf16";
+  clear_detail();
+  const size_t need = mx_attention_workspace_bytes(sequences, q_tokens, q_heads, cache);
+  int rc = attention_shape_check(fn, sequences, q_tokens, q_heads, cache);
+  if (rc != MX_OK) return rc;
+  mx::AttentionArgs a;
+  Range ranges[6];
+  rc = cache_check(fn, cache, page_table, max_pages, lengths, sequences, MX_ATTENTION_MAX_SEQUENCES, &a.c, ranges);
+  if (rc != MX_OK) return rc;
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f))
+    return fail(MX_ERR_INVALID_ARG, "%s: scale = %g (finite)", fn, static_cast<double>(scale));
+  if (window < 0 || window >= (int64_t(1) << 31))
+    return fail(MX_ERR_INVALID_ARG, "%s: window = %lld (0 .. 2^31 - 1)", fn, static_cast<long long>(window));
+  const int64_t rows = sequences * q_tokens, cols = q_heads * cache->head_dim;
+  const Rows in{"q", q, rows, cols, ld_q}, o{"out", out, rows, cols, ld_out};
+  rc = rows_check(fn, in);
+  if (rc == MX_OK) rc = rows_check(fn, o);
+  if (rc != MX_OK) return rc;
+  if (!aligned4(lse)) return fail(MX_ERR_ALIGNMENT, "%s: lse is not 4-byte aligned", fn);
+  if (!workspace || workspace_bytes < need)
+    return fail(MX_ERR_WORKSPACE, "%s: needs a workspace of %zu bytes, got %zu%s", fn, need,
+                workspace ? workspace_bytes : size_t(0), workspace ? "" : " (null)");
+  if (!aligned16(workspace)) return fail(MX_ERR_ALIGNMENT, "%s: workspace is not 16-byte aligned", fn);
+  const Range outputs[2] = {span(lse, static_cast<uint64_t>(rows * q_heads) * 4), span(workspace, need)};
+  rc = rows_disjoint(fn, &o, 1, &in, 1, outputs, 2, ranges, 6, false);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (sequences == 0) return MX_OK;
+  a.c.status = dev->status;
+  a.q = static_cast<const uint16_t *>(q);
+  a.ld_q = ld_q;
+  a.q_heads = static_cast<int>(q_heads);
+  a.q_tokens = static_cast<int>(q_tokens);
+  a.scale = scale;
+  a.window = window;
+  a.out = static_cast<uint16_t *>(out);
+  a.ld_out = ld_out;
+  a.lse = lse;
+  a.workspace = workspace;
+  a.num_sms = dev->num_sms;
+  return launch_rc(fn, mx::launch_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+MX_API int mx_sample(const void *logits, int64_t rows, int64_t vocab, int64_t ld, int dtype,
+                     const float *temperature, const int32_t *top_k, const float *top_p,
+                     const float *min_p, const float *uniform, int32_t *ids, float *probability,
+                     void *stream) {
+  clear_detail();
+  const char *fn = "mx_sample";
+  if (!logits || !uniform || !ids)
+    return fail(MX_ERR_INVALID_ARG, "%s: %s is null", fn, !logits ? "logits" : !uniform ? "uniform" : "ids");
+  if (dtype != MX_OUT_BF16 && dtype != MX_OUT_FP32)
+    return fail(MX_ERR_UNSUPPORTED_FEATURE, "%s: dtype %d (MX_OUT_BF16 = 0 or MX_OUT_FP32 = 1)", fn, dtype);
+  if (rows < 0 || rows > (1 << 20))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: rows = %lld (0 .. 2^20)", fn, static_cast<long long>(rows));
+  if (vocab < 1 || vocab > MX_SAMPLE_MAX_VOCAB)
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: vocab = %lld (1..%d)", fn, static_cast<long long>(vocab),
+                MX_SAMPLE_MAX_VOCAB);
+  if (ld < vocab || ld >= (int64_t(1) << 40))
+    return fail(MX_ERR_INVALID_ARG, "%s: ld = %lld (>= vocab = %lld, below 2^40)", fn, static_cast<long long>(ld),
+                static_cast<long long>(vocab));
+  if (!aligned16(logits)) return fail(MX_ERR_ALIGNMENT, "%s: logits is not 16-byte aligned", fn);
+  const struct {
+    const char *name;
+    const void *p;
+  } small[7] = {{"temperature", temperature}, {"top_k", top_k}, {"top_p", top_p}, {"min_p", min_p},
+                {"uniform", uniform},         {"ids", ids},     {"probability", probability}};
+  for (const auto &v : small)
+    if (!aligned4(v.p)) return fail(MX_ERR_ALIGNMENT, "%s: %s is not 4-byte aligned", fn, v.name);
+  const uint64_t n = static_cast<uint64_t>(rows) * 4;
+  const Range in[6] = {span(logits, row_bytes(rows, vocab, ld, dtype == MX_OUT_FP32 ? 4 : 2)),
+                       span(temperature, n), span(top_k, n), span(top_p, n), span(min_p, n), span(uniform, n)};
+  const Range out[2] = {span(ids, n), span(probability, n)};
+  int rc = check_disjoint(fn, out, 2, in, 6);
+  if (rc != MX_OK) return rc;
+  DeviceInfo *dev = nullptr;
+  rc = device_info(&dev);
+  if (rc != MX_OK) return rc;
+  if (rows == 0) return MX_OK;
+  mx::SampleArgs a;
+  a.logits = logits;
+  a.ld = ld;
+  a.rows = static_cast<int>(rows);
+  a.vocab = static_cast<int>(vocab);
+  a.fp32 = dtype == MX_OUT_FP32;
+  a.temperature = temperature;
+  a.top_k = top_k;
+  a.top_p = top_p;
+  a.min_p = min_p;
+  a.uniform = uniform;
+  a.ids = ids;
+  a.probability = probability;
+  a.num_sms = dev->num_sms;
+  a.status = dev->status;
+  return launch_rc(fn, mx::launch_sample(a, static_cast<cudaStream_t>(stream)));
+}
+
 MX_API int mx_device_status(void *stream) {
   clear_detail();
   DeviceInfo *dev = nullptr;
@@ -1333,6 +1805,10 @@ MX_API int mx_device_status(void *stream) {
     return fail(MX_ERR_DEVICE_BOUNDS,
                 "mx_device_status: a kernel of the bounds-checked build skipped an access outside "
                 "its buffer");
+  if (word & mx::kStatusIndexBit)
+    return fail(MX_ERR_DEVICE_INDEX,
+                "mx_device_status: a page, length or row number in device memory was out of range; "
+                "what it names was left out");
   return MX_OK;
 }
 

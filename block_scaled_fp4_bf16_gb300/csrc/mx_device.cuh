@@ -15,6 +15,8 @@ namespace mx {
 constexpr uint32_t kStatusTimeout = kStatusTimeoutBit;
 // Bit recorded by the bounds-checked build for an access outside its buffer.
 constexpr uint32_t kStatusBounds = kStatusBoundsBit;
+// Bit recorded for an index in device memory that is out of range.
+constexpr uint32_t kStatusIndex = kStatusIndexBit;
 // Longest a kernel waits on one barrier phase before it gives up.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 // Bound on the clean-up waits after an abort.

@@ -1,0 +1,399 @@
+// RMS norm of each query and key head and the rotation by position, and its gradients.
+//
+// Forward: s = mean(x^2), r = (s + eps)^-1/2, n = x r w; a pair (a, b) of channels with
+// angle phi becomes (a cos - b sin, b cos + a sin).  Backward: with g the pair's gradient
+// turned back, dw = sum g x r, dx = r (g w - x r mean(g w x r)).
+//
+// Both read each element once and write it once.  A group of LANES lanes takes a head, 16
+// channels a lane (two 16-byte loads), so that the mean is a few shuffles, and a lane
+// holds both channels of its eight pairs in either order of the channels; a warp takes 32 /
+// LANES heads at a time and goes through the heads of a token with the sines and cosines
+// in registers: they are computed once for a token and slice of its heads, not once a head.
+#include "decode.h"
+#include "mx_device.cuh"
+
+namespace mx {
+namespace {
+
+constexpr int kWarps = 8;
+
+// f / 2 pi modulo 1, in units of 2^-64: the phase of a position is then one 64-bit
+// product, exact modulo a turn.
+__device__ __forceinline__ uint64_t turns_of(float f) {
+  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;  // 2^64 / 2 pi
+  const uint32_t b = __float_as_uint(f);
+  const int be = static_cast<int>((b >> 23) & 255u);
+  const uint64_t m = (b & 0x7FFFFFu) | (be ? 0x800000u : 0u);
+  const int e = (be ? be : 1) - 150;  // |f| = m 2^e
+  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+  uint64_t t;
+  if (e >= 0)
+    t = e < 64 ? lo << e : 0;
+  else if (e > -64)
+    t = (lo >> -e) | (hi << (64 + e));
+  else
+    t = e > -128 ? hi >> (-e - 64) : 0;
+  return (b >> 31) ? 0 - t : t;
+}
+
+// The 16 channels of lane j of a head: two chunks of 8 that begin at these channels.  The
+// lane's pairs are 8 j .. 8 j + 7: (chunk 0, chunk 1) element by element, or neighbours.
+struct Chunks {
+  int at[2];
+  bool in, turns;
+};
+
+__device__ __forceinline__ Chunks chunks_of(int j, const RopeArgs &a) {
+  Chunks c;
+  c.in = 16 * j < a.head_dim;
+  c.turns = 16 * j < a.rotary_dim;
+  if (c.turns && !a.interleaved)
+    c.at[0] = 8 * j, c.at[1] = 8 * j + a.rotary_dim / 2;
+  else
+    c.at[0] = 16 * j, c.at[1] = 16 * j + 8;
+  return c;
+}
+
+__device__ __forceinline__ void unpack(const uint4 &q, float *v) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack(const float *v) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A lane's 16 channels of a row that begins at element `row` (zeros if !in).
+struct Row {
+  uint4 q[2];
+};
+__device__ __forceinline__ Row load_row(const uint16_t *p, int64_t row, const Chunks &c, bool in,
+                                        int64_t extent, uint32_t *status) {
+  Row r;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r.q[i] = in && in_bounds(row + c.at[i], 8, extent, status)
+                 ? *reinterpret_cast<const uint4 *>(p + row + c.at[i])
+                 : make_uint4(0, 0, 0, 0);
+  return r;
+}
+
+__device__ __forceinline__ void store_row(uint16_t *p, int64_t row, const Chunks &c, bool in,
+                                          const float *v, int64_t extent, uint32_t *status) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (in && in_bounds(row + c.at[i], 8, extent, status))
+      *reinterpret_cast<uint4 *>(p + row + c.at[i]) = pack(v + 8 * i);
+}
+
+template <int LANES>
+__device__ __forceinline__ float head_sum(float v) {
+#pragma unroll
+  for (int m = LANES / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  return v;
+}
+
+// Sine and cosine of the lane's eight pairs at a position.
+struct Angles {
+  float sin[8], cos[8];
+};
+__device__ __forceinline__ void angles_of(Angles &t, const uint64_t *turns, int position) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    // (the upper 32 bits as a signed fraction of a turn: half turns in [-1, 1))
+    const uint64_t phase = turns[i] * static_cast<uint64_t>(static_cast<int64_t>(position));
+    const float half = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
+    sincospif(half, &t.sin[i], &t.cos[i]);
+  }
+}
+
+// Turns the lane's pairs, by the angle (SIGN 1) or back (-1).
+template <int SIGN>
+__device__ __forceinline__ void turn(float *v, const Angles &t, bool interleaved) {
+  auto pair = [&](float &x, float &y, int i) {
+    const float a = x, b = y, s = SIGN * t.sin[i];
+    x = a * t.cos[i] - b * s;
+    y = b * t.cos[i] + a * s;
+  };
+  if (interleaved) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pair(v[2 * i], v[2 * i + 1], i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) pair(v[i], v[8 + i], i);
+  }
+}
+
+__device__ __forceinline__ void load_turns(uint64_t *turns, const RopeArgs &a, const Chunks &c, int j) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    turns[i] = c.turns && in_bounds(8 * j + i, 1, a.rotary_dim / 2, a.status)
+                   ? turns_of(a.inv_freq[8 * j + i])
+                   : 0;
+}
+
+// A warp's share: `slices` of the groups of heads of each token, tokens and slices shared
+// out evenly over the warps of the grid.
+struct Share {
+  int groups[2];  // of queries and keys, 32 / LANES heads each
+  int slices, per_slice;
+};
+
+template <int LANES>
+__global__ void __launch_bounds__(kWarps * 32)
+    rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
+  constexpr int kHeads = 32 / LANES, kBatch = 4;
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LANES;
+  const Chunks c = chunks_of(j, a);
+  uint64_t turns[8];
+  load_turns(turns, a, c, j);
+  const int total = share.groups[0] + share.groups[1];
+  const int64_t items = a.tokens * share.slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += stride) {
+    const int64_t token = item / share.slices;
+    const int first = static_cast<int>(item % share.slices) * share.per_slice;
+    const int last = min(first + share.per_slice, total);
+    Angles t;
+    if (in_bounds(token, 1, a.tokens, a.status)) angles_of(t, turns, a.positions[token]);
+    for (int g0 = first; g0 < last; g0 += kBatch) {
+      Row x[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int g = g0 + i, k = g >= share.groups[0];
+        const Heads &p = a.part[k];
+        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
+        x[i] = load_row(p.x, token * p.ld + head * a.head_dim, c, c.in && g < last && head < p.heads,
+                        (a.tokens - 1) * p.ld + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int g = g0 + i, k = g >= share.groups[0];
+        if (g >= last) break;
+        const Heads &p = a.part[k];
+        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
+        float v[16];
+        unpack(x[i].q[0], v);
+        unpack(x[i].q[1], v + 8);
+        if (p.weight != nullptr) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum += v[e] * v[e];
+          const float r = 1.0f / sqrtf(head_sum<LANES>(sum) / static_cast<float>(a.head_dim) + a.eps);
+          float w[16];
+          const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
+          unpack(wr.q[0], w);
+          unpack(wr.q[1], w + 8);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
+        }
+        if (c.turns) turn<1>(v, t, a.interleaved);
+        store_row(p.y, token * p.ld_y + head * a.head_dim, c, c.in && head < p.heads, v,
+                  (a.tokens - 1) * p.ld_y + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
+      }
+    }
+  }
+}
+
+// The gradients of the inputs, and each CTA's sums of those of the weights.  The order of
+// the sums follows from the sizes and the number of SMs alone: a warp's tokens in order,
+// then the lanes, then the warps, then (backward_sum_kernel) the CTAs.
+template <int LANES>
+__global__ void __launch_bounds__(kWarps * 32)
+    rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
+  constexpr int kHeads = 32 / LANES, kBatch = 2;
+  __shared__ float sums[kWarps][2][kRopeMaxDim];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LANES;
+  const Chunks c = chunks_of(j, a);
+  uint64_t turns[8];
+  load_turns(turns, a, c, j);
+  const int total = share.groups[0] + share.groups[1];
+  const int64_t items = a.tokens * share.slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  float dw[2][16] = {};
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += stride) {
+    const int64_t token = item / share.slices;
+    const int first = static_cast<int>(item % share.slices) * share.per_slice;
+    const int last = min(first + share.per_slice, total);
+    Angles t;
+    if (in_bounds(token, 1, a.tokens, a.status)) angles_of(t, turns, a.positions[token]);
+    for (int g0 = first; g0 < last; g0 += kBatch) {
+      Row x[kBatch], dy[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int g = g0 + i, k = g >= share.groups[0];
+        const Heads &p = a.part[k];
+        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
+        const bool in = c.in && g < last && head < p.heads;
+        const int64_t cols = static_cast<int64_t>(p.heads) * a.head_dim;
+        // (without a norm the inputs are not read)
+        x[i] = load_row(p.x, token * p.ld + head * a.head_dim, c, in && p.weight != nullptr,
+                        (a.tokens - 1) * p.ld + cols, a.status);
+        dy[i] = load_row(p.dy, token * p.ld_dy + head * a.head_dim, c, in,
+                         (a.tokens - 1) * p.ld_dy + cols, a.status);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int g = g0 + i, k = g >= share.groups[0];
+        if (g >= last) break;
+        const Heads &p = a.part[k];
+        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
+        float v[16];
+        unpack(dy[i].q[0], v);
+        unpack(dy[i].q[1], v + 8);
+        if (c.turns) turn<-1>(v, t, a.interleaved);
+        if (p.weight != nullptr) {
+          float n[16], w[16];
+          unpack(x[i].q[0], n);
+          unpack(x[i].q[1], n + 8);
+          const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
+          unpack(wr.q[0], w);
+          unpack(wr.q[1], w + 8);
+          float sum = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) sum += n[e] * n[e];
+          const float r = 1.0f / sqrtf(head_sum<LANES>(sum) / static_cast<float>(a.head_dim) + a.eps);
+          float dot = 0.0f;
+          const bool in = c.in && head < p.heads;  // (others' x is 0, but r may be infinite)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            n[e] = in ? n[e] * r : 0.0f;
+            const float s = v[e] * n[e];
+            if (k == 0)
+              dw[0][e] += s;
+            else
+              dw[1][e] += s;
+            v[e] *= w[e];
+            dot += v[e] * n[e];
+          }
+          dot = head_sum<LANES>(dot) / static_cast<float>(a.head_dim);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = r * (v[e] - n[e] * dot);
+        }
+        store_row(p.y, token * p.ld_y + head * a.head_dim, c, c.in && head < p.heads, v,
+                  (a.tokens - 1) * p.ld_y + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
+      }
+    }
+  }
+  if (a.partials == nullptr) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      float s = dw[k][e];
+#pragma unroll
+      for (int m = 16; m >= LANES; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+      if (lane < LANES && c.in) sums[warp][k][c.at[e >> 3] + (e & 7)] = s;
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * a.head_dim; i += kWarps * 32) {
+    const int k = i >= a.head_dim, d = i - k * a.head_dim;
+    float s = sums[0][k][d];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) s += sums[w][k][d];
+    a.partials[static_cast<int64_t>(blockIdx.x) * 2 * a.head_dim + i] = s;
+  }
+}
+
+// dweight[d] = the CTAs' sums, in their order within each of 8 warps: a CTA takes 32
+// columns of the 2 head_dim.
+__global__ void __launch_bounds__(kWarps * 32)
+    backward_sum_kernel(const __grid_constant__ RopeArgs a, int ctas) {
+  __shared__ float sums[kWarps][32];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int i = blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (i < 2 * a.head_dim) {
+#pragma unroll 8
+    for (int p = warp; p < ctas; p += kWarps) s += a.partials[static_cast<int64_t>(p) * 2 * a.head_dim + i];
+  }
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (warp != 0 || i >= 2 * a.head_dim) return;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) s += sums[w][lane];
+  const int k = i >= a.head_dim;
+  float *out = a.part[k].dweight;
+  if (out != nullptr) out[i - k * a.head_dim] = s;
+}
+
+int lanes_of(int head_dim) {
+  int lanes = 1;
+  while (16 * lanes < head_dim) lanes *= 2;
+  return lanes;
+}
+
+// Each warp gets a whole token where there are enough of them, otherwise a slice.
+Share share_of(const RopeArgs &a, int lanes, int batch, int64_t warps) {
+  const int heads = 32 / lanes;
+  Share s;
+  for (int k = 0; k < 2; ++k) s.groups[k] = (a.part[k].heads + heads - 1) / heads;
+  const int total = s.groups[0] + s.groups[1];
+  const int most = (total + batch - 1) / batch;
+  int64_t slices = warps / (a.tokens > 0 ? a.tokens : 1);
+  slices = slices < 1 ? 1 : slices > most ? most : slices;
+  s.per_slice = static_cast<int>((total + slices - 1) / slices);
+  s.slices = (total + s.per_slice - 1) / s.per_slice;
+  return s;
+}
+
+template <int LANES>
+cudaError_t forward(const RopeArgs &a, cudaStream_t s) {
+  const int64_t warps = static_cast<int64_t>(a.num_sms) * 4 * kWarps;
+  // few tokens: one group of heads a warp
+  const Share share = share_of(a, LANES, 1, warps);
+  const int64_t ctas = (a.tokens * share.slices + kWarps - 1) / kWarps;
+  const int64_t most = static_cast<int64_t>(a.num_sms) * 4;
+  return launch_pdl(rope_kernel<LANES>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
+                    dim3(kWarps * 32), 0, s, a, share);
+}
+
+template <int LANES>
+cudaError_t backward(const RopeArgs &a, cudaStream_t s) {
+  int64_t most = static_cast<int64_t>(a.num_sms) * 2;
+  if (most > kRopeBackCtas) most = kRopeBackCtas;
+  const Share share = share_of(a, LANES, 1, most * kWarps);
+  int64_t ctas = (a.tokens * share.slices + kWarps - 1) / kWarps;
+  ctas = ctas < 1 ? 1 : ctas < most ? ctas : most;
+  const cudaError_t e = launch_pdl(rope_backward_kernel<LANES>, dim3(static_cast<unsigned>(ctas)),
+                                   dim3(kWarps * 32), 0, s, a, share);
+  if (e != cudaSuccess || a.partials == nullptr) return e;
+  return launch_pdl(backward_sum_kernel, dim3((2 * a.head_dim + 31) / 32), dim3(kWarps * 32), 0, s, a,
+                    static_cast<int>(ctas));
+}
+
+}  // namespace
+
+cudaError_t launch_qk_rope(const RopeArgs &a, cudaStream_t s) {
+  switch (lanes_of(a.head_dim)) {
+    case 1: return forward<1>(a, s);
+    case 2: return forward<2>(a, s);
+    case 4: return forward<4>(a, s);
+    case 8: return forward<8>(a, s);
+    default: return forward<16>(a, s);
+  }
+}
+
+cudaError_t launch_qk_rope_backward(const RopeArgs &a, cudaStream_t s) {
+  switch (lanes_of(a.head_dim)) {
+    case 1: return backward<1>(a, s);
+    case 2: return backward<2>(a, s);
+    case 4: return backward<4>(a, s);
+    case 8: return backward<8>(a, s);
+    default: return backward<16>(a, s);
+  }
+}
+
+}  // namespace mx

@@ -66,6 +66,8 @@ extern "C" {
 #define MX_ERR_DEVICE_TIMEOUT (-9)      /* a bounded device-side wait ran out     */
 #define MX_ERR_DEVICE_BOUNDS (-10)      /* bounds-checked build: an access outside
                                            its buffer was found and skipped     */
+#define MX_ERR_DEVICE_INDEX (-11)       /* a page, length or row number in device
+                                           memory was out of range; skipped      */
 
 /* ---- enums ----------------------------------------------------------- */
 #define MX_FMT_MXFP4 0    /* UE8M0 scale per 32 elements                      */
@@ -517,6 +519,174 @@ int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const void *r
                       const mx_moe_weights *moe, int32_t *ids, float *weights, void *y,
                       int64_t ld_y, void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- the rest of a decoding step -------------------------------------------
+ * Between the products of a few tokens a decoding step norms and rotates its
+ * queries and keys, stores keys and values, attends to what is stored and, at
+ * its end, chooses a token.  The pages have no counterpart; these calls are this
+ * library's own addition.  Arithmetic is binary32 unless said otherwise, and no
+ * result depends on the run. */
+
+/* The norm and rotation of a layer's queries and keys (host memory, read before
+ * a call returns). */
+typedef struct mx_qk_norm {
+  int64_t q_heads, k_heads; /* 0 or more each, one of them at least 1            */
+  int64_t head_dim;         /* a multiple of 16, 16..256                         */
+  int64_t rotary_dim;       /* leading channels that rotate: a multiple of 16,
+                               0..head_dim                                       */
+  int interleaved;          /* channel i turns with i + rotary_dim / 2 (0), or
+                               channels 2i and 2i + 1 with one another (1)       */
+  float eps;                /* >= 0                                              */
+  const void *q_weight;     /* device BF16 [head_dim]; NULL: queries are not normed */
+  const void *k_weight;     /* the same for keys                                 */
+  const float *inv_freq;    /* device FP32 [rotary_dim / 2]; NULL if rotary_dim = 0 */
+} mx_qk_norm;
+
+/* For each token and head x [head_dim]: n = x w / sqrt(mean(x^2) + eps) (x itself
+ * without a weight), then for each pair (a, b) of rotating channels and its
+ * angle phi = positions[token] * inv_freq[i]
+ *   a' = a cos phi - b sin phi,  b' = b cos phi + a sin phi;
+ * one rounding to BF16.  phi is reduced exactly (to 2^-32 of a turn) for any
+ * position and |inv_freq| up to 2^16.
+ *   q: BF16 [tokens, q_heads, head_dim], token stride ld_q (>= q_heads * head_dim,
+ *      % 8 == 0); k, q_out, k_out likewise.  q and q_out (k and k_out) are NULL
+ *      when there are no such heads.
+ *   positions: device int32 [tokens].
+ *   tokens 0..2^31 - 1 (0 launches nothing).
+ * q_out may be q itself (with the same stride), k_out may be k; apart from that
+ * outputs overlap neither inputs nor one another.  Rows of one stride may lie in
+ * each other's gaps (a fused projection's output).  Launches one kernel. */
+int mx_qk_norm_rope_bf16(const void *q, int64_t ld_q, const void *k, int64_t ld_k, int64_t tokens,
+                         const int32_t *positions, const mx_qk_norm *norm, void *q_out,
+                         int64_t ld_q_out, void *k_out, int64_t ld_k_out, void *stream);
+
+/* Workspace bytes of the gradients (0 for invalid arguments). */
+size_t mx_qk_norm_rope_backward_workspace_bytes(int64_t tokens, const mx_qk_norm *norm);
+
+/* The gradients of mx_qk_norm_rope_bf16 from those of its outputs (dq_out, dk_out).
+ *   q, k, positions, norm: as in the forward call (the inputs, not the outputs);
+ *   dq, dk: out BF16, shaped as q and k;
+ *   dq_weight, dk_weight: out FP32 [head_dim], sums over tokens and heads in a fixed
+ *      order; NULL where there is no weight, and also accepted where there is one.
+ * With no tokens dq_weight and dk_weight are set to zero.  No output overlaps an
+ * input or another output.  workspace: mx_qk_norm_rope_backward_workspace_bytes(...)
+ * bytes, 16-byte aligned, contents arbitrary; one call at a time may use it.
+ * Launches two kernels (one if neither dq_weight nor dk_weight is given). */
+int mx_qk_norm_rope_backward_bf16(const void *q, int64_t ld_q, const void *k, int64_t ld_k,
+                                  const void *dq_out, int64_t ld_dq_out, const void *dk_out,
+                                  int64_t ld_dk_out, int64_t tokens, const int32_t *positions,
+                                  const mx_qk_norm *norm, void *dq, int64_t ld_dq, void *dk,
+                                  int64_t ld_dk, float *dq_weight, float *dk_weight,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/* Tokens of a scale of the cache. */
+#define MX_CACHE_BLOCK 32
+
+/* A cache of keys and values of one layer in pages (host memory, read before a
+ * call returns).  Keys and values are E4M3 codes with one UE8M0 scale for each
+ * MX_CACHE_BLOCK tokens of a page and head: value = code * 2^(scale - 127).
+ * Page p, head h, token t of the page, channel d:
+ *   code  at ((p * kv_heads + h) * page_tokens + t) * head_dim + d,
+ *   scale at (p * kv_heads + h) * (page_tokens / 32) + t / 32.
+ * A sequence's token i is token i % page_tokens of the page page_table[i / page_tokens].
+ * Nothing needs to start at any value. */
+typedef struct mx_kv_cache {
+  void *k_codes, *k_scales, *v_codes, *v_scales; /* device */
+  int64_t pages;       /* of the pool                                           */
+  int64_t page_tokens; /* a multiple of 32, up to 2^20                          */
+  int64_t kv_heads;    /* 1..1024                                               */
+  int64_t head_dim;    /* 64, 128 or 256                                        */
+} mx_kv_cache;
+
+/* Stores new keys and values.  Sequence b has n_b new tokens, rows
+ * starts[b] .. starts[b + 1] - 1 of k and v; they are its last ones: positions
+ * lengths[b] - n_b .. lengths[b] - 1.  (Rows whose position would be negative, as
+ * in a slot of the batch with length 0, are not stored.)
+ *   k, v: BF16 [tokens, kv_heads, head_dim], token strides ld_k, ld_v (>= kv_heads *
+ *      head_dim, % 8 == 0);
+ *   starts: device int32 [sequences + 1], not descending, from 0 to at most tokens; NULL:
+ *      tokens / sequences new ones for each (tokens % sequences == 0);
+ *   page_table: device int32 [sequences, max_pages]; lengths: device int32 [sequences];
+ *   sequences 0..65535, tokens 0..2^30, max_pages 1..2^24.
+ * Scale of a block of 32 tokens: 2^e with the least e such that the largest
+ * finite magnitude among its new tokens is at most 448 * 2^e (-127 if that is 0),
+ * and at least that of the tokens it already holds; those are rounded again, from
+ * their codes, if e grows.  Codes are rounded to nearest even; infinities and NaN
+ * become NaN.  What a block holds behind the sequence's end is left as it is.
+ * A page that sequences go on in must belong to one of them.  Rows whose page is
+ * not 0..pages - 1, or that max_pages does not reach, are left out, and
+ * mx_device_status then returns MX_ERR_DEVICE_INDEX; likewise sequences whose
+ * starts are out of order or range.  Launches one kernel. */
+int mx_kv_append_bf16(const void *k, int64_t ld_k, const void *v, int64_t ld_v, int64_t tokens,
+                      const int32_t *starts, const int32_t *page_table, int64_t max_pages,
+                      const int32_t *lengths, int64_t sequences, const mx_kv_cache *cache,
+                      void *stream);
+
+/* Most query tokens of a sequence and sequences that mx_attention_bf16 takes. */
+#define MX_ATTENTION_MAX_QUERY 16
+#define MX_ATTENTION_MAX_SEQUENCES 4096
+
+/* Workspace bytes of mx_attention_bf16 (0 for invalid arguments). */
+size_t mx_attention_workspace_bytes(int64_t sequences, int64_t q_tokens, int64_t q_heads,
+                                    const mx_kv_cache *cache);
+
+/* Attention of the last q_tokens tokens of each sequence over its cached tokens.
+ * Query i of sequence b (row b * q_tokens + i) is at position p = lengths[b] -
+ * q_tokens + i and sees the cached positions t with t <= p, and t > p - window if
+ * window is not 0.  Its head h reads the cache's head h / (q_heads / kv_heads):
+ *   out = sum_t softmax_t(scale * q . k_t) v_t,  lse = log sum_t exp(scale * q . k_t).
+ * A row that sees nothing (length 0, p < 0) gets 0 and -inf.  NaN that a row does
+ * not see does not reach it.
+ *   q, out: BF16 [sequences * q_tokens, q_heads, head_dim], row strides ld_q, ld_out
+ *      (>= q_heads * head_dim, % 8 == 0); lse: FP32 [sequences * q_tokens, q_heads] or NULL;
+ *   page_table, max_pages, lengths: as in mx_kv_append_bf16, with the new tokens stored;
+ *   q_heads a multiple of kv_heads, at most 64 times as many; q_tokens
+ *      1..MX_ATTENTION_MAX_QUERY; sequences 0..MX_ATTENTION_MAX_SEQUENCES; scale finite;
+ *      window 0..2^31 - 1.
+ * Tokens on a page that is not 0..pages - 1 are not seen, a length above max_pages *
+ * page_tokens counts as that, one below 0 as 0; mx_device_status then returns
+ * MX_ERR_DEVICE_INDEX.  Products are FP16 with binary32 sums: codes are exact in
+ * FP16, q is under a power of two of its row and head (exact above 2^-29 of their
+ * largest), the weights of a block of 32 tokens are rounded to FP16 relative to the
+ * block's largest.  No output overlaps an input or the workspace
+ * (mx_attention_workspace_bytes(...) bytes, 16-byte aligned, contents arbitrary; one
+ * call at a time may use it).  Launches two kernels. */
+int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64_t sequences,
+                      int64_t q_tokens, const int32_t *page_table, int64_t max_pages,
+                      const int32_t *lengths, const mx_kv_cache *cache, float scale,
+                      int64_t window, void *out, int64_t ld_out, float *lse, void *workspace,
+                      size_t workspace_bytes, void *stream);
+
+/* Most logits of a row that mx_sample takes. */
+#define MX_SAMPLE_MAX_VOCAB 262144
+
+/* One token for each row of logits.  With the logits in descending order (equal
+ * ones: the lowest index first), l_0 the largest and w_j = exp((l_j - l_0) /
+ * temperature), a row keeps
+ *   the first top_k (top_k <= 0 or > vocab: all), of these
+ *   the fewest whose w add up to at least top_p times the sum of all of these
+ *      (top_p >= 1: all; always the first), and of these
+ *   those with w_j >= min_p (min_p <= 0: all; the first is always kept);
+ * ids is the first kept token, by index, up to which the kept w (in the order of
+ * the indexes) add up to more than uniform times their sum, and probability its
+ * w over that sum.  temperature <= 0 takes the largest logit, probability 1.
+ * The w are computed to 2^-40 and summed as 64-bit integers of 2^-44: w below
+ * 2^-45 count as 0.  Temperatures below 2^-100 count as that.
+ * Logits of -inf are never chosen; +inf ones share the row.  A row with nothing
+ * above -inf, or with a NaN among its logits, temperature, top_p, min_p or
+ * uniform, gets id -1, probability 0.
+ *   logits: FP32 or BF16 (dtype MX_OUT_FP32 or MX_OUT_BF16) [rows, vocab], row
+ *      stride ld (>= vocab, any);
+ *   temperature, top_p, min_p: device FP32 [rows], top_k: device int32 [rows]; NULL: 1,
+ *      all, all, all;  uniform: device FP32 [rows] in [0, 1) (values outside count as the
+ *      nearest inside);
+ *   ids: out int32 [rows]; probability: out FP32 [rows] or NULL;
+ *   rows 0..2^20, vocab 1..MX_SAMPLE_MAX_VOCAB.
+ * The outputs overlap neither an input nor each other.  Launches one kernel. */
+int mx_sample(const void *logits, int64_t rows, int64_t vocab, int64_t ld, int dtype,
+              const float *temperature, const int32_t *top_k, const float *top_p,
+              const float *min_p, const float *uniform, int32_t *ids, float *probability,
+              void *stream);
+
 /* Size of the fixed device scratch array of mxfp4_gemm_static_workspace. */
 #define MX_STATIC_WORKSPACE_BYTES (16u << 20) /* 16 MiB */
 
@@ -544,7 +714,8 @@ int mxfp4_gemm_static_workspace(const void *a_codes, const void *a_scales, const
 /* Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns MX_OK, MX_ERR_DEVICE_TIMEOUT when a kernel's
  * bounded wait (on a TMA or tensor-core completion barrier) ran out and the
- * kernel abandoned its work, or MX_ERR_CUDA. */
+ * kernel abandoned its work, MX_ERR_DEVICE_INDEX when a call met a page, length
+ * or row number out of range in device memory, or MX_ERR_CUDA. */
 int mx_device_status(void *stream);
 
 /* Self-test of the bounded device wait: launches one CTA that waits on a
