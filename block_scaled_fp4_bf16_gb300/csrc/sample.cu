@@ -1,9 +1,11 @@
 // One token for each row of logits: temperature, top-k, top-p, min-p, one uniform number.
 //
 // What a row keeps is a prefix of its logits in descending order, so nothing is sorted: the
-// threshold is a logit (and, among equal ones, an index), found by counting or by adding up
-// weights on one side of it.  A thread-block cluster takes a row; each of its CTAs reads a
-// contiguous slice once into shared memory, in which all further passes run.
+// threshold is a logit (and, among equal ones, an index).  A thread-block cluster takes a
+// row; each of its CTAs reads a contiguous slice once into shared memory, in which all
+// further passes run.  A threshold takes three steps: counts (top-k) or weights (top-p) of
+// bins of equal width in the exponent, the bin where the wanted sum is reached, and that
+// bin's few logits, sorted by one CTA.
 //
 // Borders are what can go wrong: with weights to binary32 the sums at a border of 10^5 tokens
 // are off by more than the uniform numbers' spacing.  So a weight is computed to 2^-40 (pairs
@@ -19,6 +21,11 @@ constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMaxCtas = 8;
 constexpr int kUnit = 44;  // weights are in units of 2^-44
 constexpr int kTable = 256;
+constexpr int kBins = 512;     // the last one: weights that are 0
+constexpr float kSpan = 46.0f; // powers of two that the others cover
+constexpr int kList = 1024;    // logits of a bin that are sorted
+constexpr int kLimb = 15;      // bits of a weight that one 32-bit sum takes of a CTA's 2^15
+constexpr int kLimbs = 3;
 
 // Order of logits as unsigned integers (no NaN among them).
 __device__ __forceinline__ uint32_t logit_key(float v) {
@@ -93,24 +100,56 @@ __device__ __forceinline__ uint64_t part_of(float f, uint64_t n) {
   return shift < 128 ? hi >> (shift - 64) : 0;
 }
 
-struct Slots {
-  uint64_t sum[2][kMaxCtas];
-};
-
 __device__ __forceinline__ void st_cluster_u64(uint32_t addr, uint64_t v) {
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t add_cluster_u32(uint32_t addr, uint32_t n) {
+  uint32_t v;
+  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(addr), "r"(n) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ uint64_t warp_total(uint64_t v) {
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+  return v;
+}
+__device__ __forceinline__ uint64_t warp_upto(uint64_t v, int lane) {  // the sum of the lanes up to this one
+#pragma unroll
+  for (int m = 1; m < 32; m <<= 1) {
+    const uint64_t up = __shfl_up_sync(0xFFFFFFFFu, v, m);
+    if (lane >= m) v += up;
+  }
+  return v;
+}
+
+struct Shared {
+  float2 table[kTable];
+  uint32_t bins[1 + kLimbs][kBins];  // counts; weights in limbs of kLimb bits
+  uint64_t list[kList];              // of the cluster's first CTA: (key, ~index)
+  uint64_t slots[2][kMaxCtas];       // every CTA's number
+  uint64_t sums[2][kWarps];
+  uint64_t found[2];                 // what a search found
+  Scale scale;
+  uint32_t listed[4];                // entries, of each use of the list
+  int piece;
+};
 
 template <bool FP32>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
     sample_kernel(const __grid_constant__ SampleArgs a, int ctas, int slice) {
-  extern __shared__ uint32_t keys[];  // of this CTA's slice
-  __shared__ float2 table[kTable];
-  __shared__ Slots slots;
-  __shared__ uint64_t warp_sums[2][kWarps];
-  __shared__ Scale shared_scale;
+  extern __shared__ __align__(16) uint32_t keys[];  // of this CTA's slice
+  __shared__ Shared sh;
   cluster_arrive_relaxed();
   griddep_launch_dependents();
+  if (threadIdx.x < kTable) sh.table[threadIdx.x] = table_entry(threadIdx.x);
+  for (int i = threadIdx.x; i < (1 + kLimbs) * kBins; i += kThreads) (&sh.bins[0][0])[i] = 0;
+  if (threadIdx.x < 4) sh.listed[threadIdx.x] = 0;
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank()), row = static_cast<int>(cluster_id_x());
@@ -125,26 +164,42 @@ __global__ void __launch_bounds__(kThreads)
   int top_k = a.top_k != nullptr && in_bounds(row, 1, a.rows, a.status) ? a.top_k[row] : 0;
   if (top_k <= 0 || top_k > a.vocab) top_k = a.vocab;
 
-  if (threadIdx.x < kTable) table[threadIdx.x] = table_entry(threadIdx.x);
-  // the slice; the largest logit, and the lowest index that has it
+  // the slice, four logits a lane at a time; the largest, and the lowest index that has it
   uint64_t best = 0;
   bool nan = temperature != temperature || top_p != top_p || min_p != min_p || uniform != uniform;
-  for (int i = from + lane; i < from + segment; i += 32) {
+  const bool fours = (static_cast<int64_t>(row) * a.ld) % 4 == 0;
+#pragma unroll 4
+  for (int i = from + lane * 4; i < from + segment; i += 128) {
     const int at = base + i;
-    if (at >= a.vocab) {
-      keys[i] = 0;
-      continue;
-    }
     const int64_t e = row * a.ld + at;
-    float v = 0.0f;
-    if (in_bounds(e, 1, extent, a.status))
-      v = FP32 ? static_cast<const float *>(a.logits)[e]
-               : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.logits)[e]) << 16);
-    nan |= v != v;
-    const uint32_t k = logit_key(v);
-    keys[i] = k;
-    const uint64_t mine = static_cast<uint64_t>(k) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at));
-    best = mine > best ? mine : best;
+    float v[4];
+    if (fours && at + 4 <= a.vocab && in_bounds(e, 4, extent, a.status)) {
+      if constexpr (FP32) {
+        const float4 x = *reinterpret_cast<const float4 *>(static_cast<const float *>(a.logits) + e);
+        v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+      } else {
+        const uint2 x = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.logits) + e);
+        v[0] = __uint_as_float(x.x << 16), v[1] = __uint_as_float(x.x & 0xFFFF0000u);
+        v[2] = __uint_as_float(x.y << 16), v[3] = __uint_as_float(x.y & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        v[j] = -INFINITY;
+        if (at + j < a.vocab && in_bounds(e + j, 1, extent, a.status))
+          v[j] = FP32 ? static_cast<const float *>(a.logits)[e + j]
+                      : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.logits)[e + j]) << 16);
+      }
+    }
+    uint32_t k[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      nan |= v[j] != v[j];
+      k[j] = logit_key(v[j]);
+      const uint64_t mine = static_cast<uint64_t>(k[j]) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at + j));
+      best = mine > best ? mine : best;
+    }
+    *reinterpret_cast<uint4 *>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
   }
   if (nan) best = ~0ull;
 #pragma unroll
@@ -152,7 +207,7 @@ __global__ void __launch_bounds__(kThreads)
     const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, m);
     best = other > best ? other : best;
   }
-  if (lane == 0) warp_sums[0][warp] = best;
+  if (lane == 0) sh.sums[0][warp] = best;
   cluster_wait();
   __syncthreads();
 
@@ -160,33 +215,15 @@ __global__ void __launch_bounds__(kThreads)
   // only after the barrier that follows the reads of its last use.
   int turn = 0;
   auto share = [&](uint64_t v) {  // v: of thread 0
-    if (threadIdx.x == 0)
-      for (int r = 0; r < ctas; ++r)
-        st_cluster_u64(mapa_shared(smem_u32(&slots.sum[turn][rank]), static_cast<uint32_t>(r)), v);
+    if (threadIdx.x < ctas) st_cluster_u64(mapa_shared(smem_u32(&sh.slots[turn][rank]), threadIdx.x), v);
     cluster_sync();
     turn ^= 1;
     return turn ^ 1;
   };
-  int sums_turn = 1;
-  auto total_of = [&](uint64_t v) {  // the sum of v over the cluster's threads
-#pragma unroll
-    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
-    if (lane == 0) warp_sums[sums_turn][warp] = v;
-    __syncthreads();
-    uint64_t s = 0;
-    if (threadIdx.x == 0)
-      for (int w = 0; w < kWarps; ++w) s += warp_sums[sums_turn][w];
-    sums_turn ^= 1;
-    const int set = share(s);
-    s = 0;
-    for (int r = 0; r < ctas; ++r) s += slots.sum[set][r];
-    return s;
-  };
-
   {
-    for (int w = 0; w < kWarps; ++w) best = warp_sums[0][w] > best ? warp_sums[0][w] : best;
+    for (int w = 0; w < kWarps; ++w) best = sh.sums[0][w] > best ? sh.sums[0][w] : best;
     const int set = share(best);
-    for (int r = 0; r < ctas; ++r) best = slots.sum[set][r] > best ? slots.sum[set][r] : best;
+    for (int r = 0; r < ctas; ++r) best = sh.slots[set][r] > best ? sh.slots[set][r] : best;
   }
   const uint32_t top_key = static_cast<uint32_t>(best >> 32);
   const float top = key_logit(top_key);
@@ -201,144 +238,342 @@ __global__ void __launch_bounds__(kThreads)
   }
   if (threadIdx.x == 0) {
     const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 0x1p-100f));
-    shared_scale.top = top;
-    shared_scale.hi = static_cast<float>(c);
-    shared_scale.lo = static_cast<float>(c - static_cast<double>(shared_scale.hi));
+    sh.scale.top = top;
+    sh.scale.hi = static_cast<float>(c);
+    sh.scale.lo = static_cast<float>(c - static_cast<double>(sh.scale.hi));
   }
   __syncthreads();
-  const Scale scale = shared_scale;
+  const Scale scale = sh.scale;
   const uint32_t least = logit_key(-INFINITY);
 
   // kept: keys above `key`, and of those equal to it the ones up to index `last`
-  struct Limit {
-    uint32_t key;
-    int last;
+  uint32_t limit_key = least;
+  int limit_last = -1;
+  auto kept = [&](uint32_t k, int i) { return k > limit_key || (k == limit_key && base + i <= limit_last); };
+  auto weight = [&](uint32_t k) { return weight_of(key_logit(k), scale, sh.table); };
+
+  // Bins of equal width in the exponent, in descending order of the logits (a logit's bin is a
+  // monotonous function of it, in binary32 too).
+  const float per_bin = scale.hi * ((kBins - 1) / kSpan);
+  auto place_of = [&](uint32_t k) {
+    const float x = k == top_key ? 0.0f : (top - key_logit(k)) * per_bin;
+    return x < static_cast<float>(kBins - 1) ? x : static_cast<float>(kBins - 1);
   };
-  Limit limit{least, -1};
-  auto kept = [&](uint32_t k, int i) { return k > limit.key || (k == limit.key && base + i <= limit.last); };
-  auto weight = [&](uint32_t k) { return weight_of(key_logit(k), scale, table); };
-  auto count_above = [&](uint32_t key) {
-    uint64_t n = 0;
-    for (int i = from + lane; i < from + segment; i += 32) n += keys[i] > key;
-    return total_of(n);
+  auto bin_of = [&](uint32_t k) { return static_cast<int>(place_of(k)); };
+  // the same within a bin (binary32 has 15 bits and more left there)
+  auto bin_within = [&](uint32_t k, int bin) {
+    return static_cast<int>((place_of(k) - static_cast<float>(bin)) * static_cast<float>(kBins));
   };
-  auto mass_above = [&](uint32_t key) {
-    uint64_t n = 0;
-    for (int i = from + lane; i < from + segment; i += 32)
-      if (keys[i] > key && kept(keys[i], i)) n += weight(keys[i]);
-    return total_of(n);
-  };
-  // the index of the n-th of those equal to `key`
-  auto nth_equal = [&](uint32_t key, uint64_t n) {
-    int lo = -1, hi = a.vocab - 1;  // not enough up to lo, enough up to hi
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      uint64_t c = 0;
-      for (int i = from + lane; i < from + segment; i += 32) c += keys[i] == key && base + i <= mid;
-      if (total_of(c) >= n)
-        hi = mid;
-      else
-        lo = mid;
+  auto add_weight = [&](int bin, uint64_t w) {
+#pragma unroll
+    for (int l = 0; l < kLimbs; ++l) {
+      const uint32_t limb = static_cast<uint32_t>(w >> (kLimb * l)) & ((1u << kLimb) - 1);
+      if (limb != 0) atomicAdd(&sh.bins[1 + l][bin], limb);
     }
-    return hi;
+  };
+  // The cluster's sum of one bin: of the counts, or of the weights.
+  auto bin_total = [&](int bin, bool weights) {
+    uint64_t n = 0;
+    for (int r = 0; r < ctas; ++r) {
+      if (weights) {
+#pragma unroll
+        for (int l = 0; l < kLimbs; ++l)
+          n += static_cast<uint64_t>(ld_cluster_u32(mapa_shared(smem_u32(&sh.bins[1 + l][bin]), r))) << (kLimb * l);
+      } else {
+        n += ld_cluster_u32(mapa_shared(smem_u32(&sh.bins[0][bin]), r));
+      }
+    }
+    return n;
+  };
+  // Totals of the bins up to and with each thread's (a bin a thread), and of all.
+  static_assert(kBins == kThreads && kList == 2 * kThreads, "a bin, two entries a thread");
+  auto scan = [&](uint64_t mine, uint64_t &all) {
+    uint64_t upto = warp_upto(mine, lane);
+    if (lane == 31) sh.sums[1][warp] = upto;
+    __syncthreads();
+    all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) upto += sh.sums[1][w];
+      all += sh.sums[1][w];
+    }
+    return upto;
+  };
+
+  // The bin (in sh.piece) where the sum reaches `want`, and what is wanted of it (in found[1]).
+  auto find_bin = [&](uint64_t mine, uint64_t upto, uint64_t want) {
+    __syncthreads();
+    if (upto - mine < want && want <= upto) sh.piece = threadIdx.x, sh.found[1] = want - (upto - mine);
+    __syncthreads();
+  };
+
+  // The limit such that the kept of the logits in `bin` with the greatest (key, ~index) are the
+  // fewest whose number (weights) comes to at least `want`, which the whole bin does.
+  int uses = 0;
+  auto cut = [&](int bin, uint64_t want, bool weights) {
+    int within = -1;  // a bin of the bin, if not -1
+    auto belongs = [&](uint32_t k, int i) {
+      return k > least && bin_of(k) == bin && (within < 0 || bin_within(k, bin) == within) && kept(k, i);
+    };
+    // how many there are; up to kList of them in the first CTA's list
+    auto gather = [&] {
+      const uint32_t list_at = mapa_shared(smem_u32(sh.list), 0), listed_at = mapa_shared(smem_u32(&sh.listed[uses++]), 0);
+      for (int i0 = from; i0 < from + segment; i0 += 32) {
+        const int i = i0 + lane;
+        const uint32_t k = keys[i];
+        const bool in = belongs(k, i);
+        const uint32_t which = __ballot_sync(0xFFFFFFFFu, in);
+        if (which == 0) continue;
+        uint32_t to = lane == 0 ? add_cluster_u32(listed_at, __popc(which)) : 0;
+        to = __shfl_sync(0xFFFFFFFFu, to, 0) + __popc(which & ((1u << lane) - 1));
+        if (in && to < kList)
+          st_cluster_u64(list_at + to * 8, static_cast<uint64_t>(k) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(base + i)));
+      }
+      cluster_sync();
+      return ld_cluster_u32(listed_at);
+    };
+    uint32_t n = gather();
+    if (n > kList) {  // divide the bin, too (all CTAs have read the bins: they are past a barrier)
+      for (int i = threadIdx.x; i < kLimbs * kBins; i += kThreads)
+        if (weights)
+          sh.bins[1 + i / kBins][i % kBins] = 0;
+        else
+          sh.bins[0][i % kBins] = 0;
+      __syncthreads();
+      for (int i = from + lane; i < from + segment; i += 32) {
+        const uint32_t k = keys[i];
+        if (!belongs(k, i)) continue;
+        if (weights)
+          add_weight(bin_within(k, bin), weight(k));
+        else
+          atomicAdd(&sh.bins[0][bin_within(k, bin)], 1u);
+      }
+      cluster_sync();
+      const uint64_t mine = bin_total(threadIdx.x, weights);
+      uint64_t all;
+      const uint64_t upto = scan(mine, all);
+      find_bin(mine, upto, want);
+      within = sh.piece;
+      want = sh.found[1];
+      n = gather();
+    }
+    if (n <= kList) {
+      if (rank == 0) {
+        // sorted in descending order (bitonic, of the next power of two), then added up
+        uint32_t p = 2;
+        while (p < n) p *= 2;
+        for (uint32_t i = n + threadIdx.x; i < p; i += kThreads) sh.list[i] = 0;
+        for (uint32_t size = 2; size <= p; size *= 2)
+          for (uint32_t step = size / 2; step > 0; step /= 2) {
+            __syncthreads();
+            if (threadIdx.x < p / 2) {
+              const uint32_t i = 2 * threadIdx.x - (threadIdx.x & (step - 1)), j = i + step;
+              const uint64_t x = sh.list[i], y = sh.list[j];
+              if ((x < y) == ((i & size) == 0)) sh.list[i] = y, sh.list[j] = x;
+            }
+          }
+        __syncthreads();
+        uint64_t entry[2], own[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const uint32_t i = 2 * threadIdx.x + e;
+          entry[e] = i < n ? sh.list[i] : 0;
+          own[e] = i >= n ? 0 : weights ? weight(static_cast<uint32_t>(entry[e] >> 32)) : 1;
+        }
+        uint64_t all;
+        uint64_t before = scan(own[0] + own[1], all) - own[0] - own[1];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (before < want && before + own[e] >= want)
+            for (int r = 0; r < ctas; ++r) st_cluster_u64(mapa_shared(smem_u32(&sh.found[0]), r), entry[e]);
+          before += own[e];
+        }
+      }
+      cluster_sync();
+      limit_key = static_cast<uint32_t>(sh.found[0] >> 32);
+      limit_last = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(sh.found[0]));
+      return;
+    }
+    // Too many (equal logits, mostly): halve the range of keys, then find the index among those equal.
+    auto total_of = [&](uint64_t v) {
+      v = warp_total(v);
+      __syncthreads();
+      if (lane == 0) sh.sums[0][warp] = v;
+      __syncthreads();
+      uint64_t s = 0;
+      for (int w = 0; w < kWarps; ++w) s += sh.sums[0][w];
+      const int set = share(s);
+      s = 0;
+      for (int r = 0; r < ctas; ++r) s += sh.slots[set][r];
+      return s;
+    };
+    auto above = [&](uint32_t key) {  // of the bin's kept ones with greater keys
+      uint64_t v = 0;
+      for (int i = from + lane; i < from + segment; i += 32) {
+        const uint32_t k = keys[i];
+        if (k > key && belongs(k, i)) v += weights ? weight(k) : 1;
+      }
+      return total_of(v);
+    };
+    uint32_t high = 0, low = 0xFFFFFFFFu;
+    for (int i = from + lane; i < from + segment; i += 32) {
+      const uint32_t k = keys[i];
+      if (belongs(k, i)) high = max(high, k), low = min(low, k);
+    }
+    high = __reduce_max_sync(0xFFFFFFFFu, high);
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    __syncthreads();
+    if (lane == 0) sh.sums[0][warp] = static_cast<uint64_t>(high) << 32 | (0xFFFFFFFFu - low);
+    __syncthreads();
+    {
+      uint32_t inverse = 0;
+      high = 0;
+      for (int w = 0; w < kWarps; ++w) {
+        high = max(high, static_cast<uint32_t>(sh.sums[0][w] >> 32));
+        inverse = max(inverse, static_cast<uint32_t>(sh.sums[0][w]));
+      }
+      const int set = share(static_cast<uint64_t>(high) << 32 | inverse);
+      for (int r = 0; r < ctas; ++r) {
+        high = max(high, static_cast<uint32_t>(sh.slots[set][r] >> 32));
+        inverse = max(inverse, static_cast<uint32_t>(sh.slots[set][r]));
+      }
+      low = 0xFFFFFFFFu - inverse;
+    }
+    while (low < high) {  // the least key with less than `want` above it
+      const uint32_t mid = low + (high - low) / 2;
+      if (above(mid) >= want)
+        low = mid + 1;
+      else
+        high = mid;
+    }
+    uint64_t rest = want - above(low);  // of those equal to it
+    if (weights) {
+      const uint64_t each = weight(low);
+      rest = (rest + each - 1) / each;
+    }
+    uint64_t mine = 0;
+    for (int i = from + lane; i < from + segment; i += 32) mine += keys[i] == low;
+    mine = warp_total(mine);
+    __syncthreads();
+    if (lane == 0) sh.sums[0][warp] = mine;
+    __syncthreads();
+    uint64_t sum = 0, before = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh.sums[0][w];
+      sum += sh.sums[0][w];
+    }
+    const int set = share(sum);
+    for (int r = 0; r < rank; ++r) before += sh.slots[set][r];
+    if (before < rest && rest <= before + mine) {
+      for (int i0 = from; i0 < from + segment; i0 += 32) {
+        const uint32_t which = __ballot_sync(0xFFFFFFFFu, keys[i0 + lane] == low);
+        if (before + __popc(which) < rest) {
+          before += __popc(which);
+          continue;
+        }
+        const int bit = static_cast<int>(__fns(which, 0, static_cast<int>(rest - before)));
+        if (lane < ctas) st_cluster_u64(mapa_shared(smem_u32(&sh.found[0]), lane), static_cast<uint64_t>(base + i0 + bit));
+        break;
+      }
+    }
+    cluster_sync();
+    limit_key = low;
+    limit_last = static_cast<int>(sh.found[0]);
   };
 
   if (top_k < a.vocab) {
-    // the largest key with fewer than top_k above it that is a logit's: the k-th logit
-    uint32_t lo = least, hi = top_key;  // the k-th is in lo .. hi
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (count_above(mid) >= static_cast<uint64_t>(top_k))
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    if (lo > least) {
-      const uint64_t above = count_above(lo);
-      limit.last = nth_equal(lo, static_cast<uint64_t>(top_k) - above);
-      limit.key = lo;
-    }
+    for (int i = from + lane; i < from + segment; i += 32)
+      if (keys[i] > least) atomicAdd(&sh.bins[0][bin_of(keys[i])], 1u);
+    cluster_sync();
+    const uint64_t mine = bin_total(threadIdx.x, false);
+    uint64_t all;
+    const uint64_t upto = scan(mine, all);
+    if (threadIdx.x == 0) sh.piece = kBins - 1;
+    find_bin(mine, upto, static_cast<uint64_t>(top_k));
+    // (the k-th in the last bin, or less than k in all: what is cut off weighs nothing)
+    if (sh.piece < kBins - 1) cut(sh.piece, sh.found[1], false);
   }
   if (top_p < 1.0f) {
-    const uint64_t all = mass_above(0);
+    for (int i = from + lane; i < from + segment; i += 32) {
+      const uint32_t k = keys[i];
+      if (k <= least || !kept(k, i)) continue;
+      add_weight(bin_of(k), weight(k));
+    }
+    cluster_sync();
+    const uint64_t mine = bin_total(threadIdx.x, true);
+    uint64_t all;
+    const uint64_t upto = scan(mine, all);
     uint64_t want = part_of(top_p, all);  // the least whole number that is not below top_p * all
-    // (exact but where top_p * all is whole: then one less would do)
     {
       const uint32_t b = __float_as_uint(top_p);
       const uint64_t m = (b & 0x7FFFFFu) | ((b >> 23) ? 0x800000u : 0u);
       const int shift = 150 - max(static_cast<int>(b >> 23), 1);
-      const uint64_t lo = m * all;
-      const bool whole = top_p <= 0.0f || (shift < 64 && (lo & ((1ull << shift) - 1)) == 0);
+      const bool whole = top_p <= 0.0f || (shift < 64 && ((m * all) & ((1ull << shift) - 1)) == 0);
       if (!whole) ++want;
     }
     if (want < 1) want = 1;
-    uint32_t lo = limit.key, hi = top_key;
-    while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (mass_above(mid) >= want)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    const uint64_t above = mass_above(lo), each = weight(lo);
-    if (each > 0 && above < want) {
-      const uint64_t n = (want - above + each - 1) / each;
-      const int last = nth_equal(lo, n);
-      if (lo > limit.key || last < limit.last) limit.last = last;
-      limit.key = lo;
-    }
+    find_bin(mine, upto, want);
+    cut(sh.piece, sh.found[1], true);
   }
   const uint64_t floor_weight =
-      min_p > 0.0f ? static_cast<uint64_t>(ceil(fmin(static_cast<double>(min_p), 1.0) * static_cast<double>(1ull << kUnit)))
-                   : 1;
+      min_p > 0.0f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.0f) * static_cast<float>(1ull << kUnit))) : 1;
+  auto final_weight = [&](int i) -> uint64_t {
+    const uint32_t k = keys[i];
+    if (k <= least || !kept(k, i)) return 0;
+    const uint64_t w = weight(k);
+    return w >= floor_weight ? w : 0;
+  };
 
-  // the kept weights in the order of the indexes: warps' segments, then the one that has it
+  // the kept weights in the order of the indexes: by warps' segments, then within the one that
+  // has the place, by all the CTA's warps
   uint64_t mine = 0;
-  for (int i = from + lane; i < from + segment; i += 32)
-    if (keys[i] > least && kept(keys[i], i)) {
-      const uint64_t w = weight(keys[i]);
-      if (w >= floor_weight) mine += w;
-    }
-#pragma unroll
-  for (int m = 16; m > 0; m >>= 1) mine += __shfl_xor_sync(0xFFFFFFFFu, mine, m);
-  if (lane == 0) warp_sums[sums_turn][warp] = mine;
+  for (int i = from + lane; i < from + segment; i += 32) mine += final_weight(i);
+  mine = warp_total(mine);
+  __syncthreads();
+  if (lane == 0) sh.sums[0][warp] = mine;
   __syncthreads();
   uint64_t sum = 0, before = 0;
   for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_sums[sums_turn][w];
-    sum += warp_sums[sums_turn][w];
+    if (w < warp) before += sh.sums[0][w];
+    sum += sh.sums[0][w];
   }
   const int set = share(sum);
-  uint64_t all = 0;
+  uint64_t all = 0, cta_before = 0;
   for (int r = 0; r < ctas; ++r) {
-    if (r < rank) before += slots.sum[set][r];
-    all += slots.sum[set][r];
+    if (r < rank) cta_before += sh.slots[set][r];
+    all += sh.slots[set][r];
   }
   const uint64_t target = part_of(uniform, all);  // the first place whose sum is above it
-  if (before <= target && target < before + mine) {
-    for (int i0 = from; i0 < from + segment; i0 += 32) {
-      const int i = i0 + lane;
-      uint64_t w = 0;
-      if (keys[i] > least && kept(keys[i], i)) {
-        w = weight(keys[i]);
-        if (w < floor_weight) w = 0;
-      }
-      uint64_t upto = w;
-#pragma unroll
-      for (int m = 1; m < 32; m <<= 1) {
-        const uint64_t up = __shfl_up_sync(0xFFFFFFFFu, upto, m);
-        if (lane >= m) upto += up;
-      }
-      const uint32_t over = __ballot_sync(0xFFFFFFFFu, before + upto > target);
-      if (over != 0) {
-        if (lane == __ffs(over) - 1 && in_bounds(row, 1, a.rows, a.status)) {
-          a.ids[row] = base + i;
-          if (a.probability != nullptr)
-            a.probability[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(all));
+  if (cta_before <= target && target < cta_before + sum) {  // (one CTA's)
+    before += cta_before;
+    if (before <= target && target < before + mine && lane == 0) sh.piece = warp, sh.found[1] = before;
+    __syncthreads();
+    const int begin = sh.piece * segment;
+    before = sh.found[1];
+    // pieces of the segment, in order, a warp each
+    const int length = (segment / 32 + kWarps - 1) / kWarps * 32;
+    const int p0 = min(begin + warp * length, begin + segment), p1 = min(p0 + length, begin + segment);
+    uint64_t part = 0;
+    for (int i = p0 + lane; i < p1; i += 32) part += final_weight(i);
+    part = warp_total(part);
+    __syncthreads();
+    if (lane == 0) sh.sums[0][warp] = part;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) before += sh.sums[0][w];
+    if (before <= target && target < before + part) {
+      for (int i0 = p0; i0 < p1; i0 += 32) {
+        const uint64_t w = final_weight(i0 + lane);
+        const uint64_t upto = before + warp_upto(w, lane);
+        const uint32_t over = __ballot_sync(0xFFFFFFFFu, upto > target);
+        if (over != 0) {
+          if (lane == __ffs(over) - 1 && in_bounds(row, 1, a.rows, a.status)) {
+            a.ids[row] = base + i0 + lane;
+            if (a.probability != nullptr)
+              a.probability[row] = static_cast<float>(static_cast<double>(w) / static_cast<double>(all));
+          }
+          break;
         }
-        break;
+        before = __shfl_sync(0xFFFFFFFFu, upto, 31);
       }
-      before += __shfl_sync(0xFFFFFFFFu, upto, 31);
     }
   }
   cluster_sync();  // (no CTA ends while another may still write to it)
@@ -348,8 +583,9 @@ template <bool FP32>
 cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
   int ctas = 1;
   while (ctas < kMaxCtas && ctas * 4096 < a.vocab) ctas *= 2;
+  constexpr int kStep = kWarps * 128;  // a warp's segment is a multiple of 128
   const int per = (a.vocab + ctas - 1) / ctas;
-  const int slice = (per + kThreads - 1) / kThreads * kThreads;
+  const int slice = (per + kStep - 1) / kStep * kStep;
   const void *func = reinterpret_cast<const void *>(sample_kernel<FP32>);
   if (!kernel_setup_get(func, nullptr)) {
     const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
