@@ -9,7 +9,7 @@
 //
 // Borders are what can go wrong: with weights to binary32 the sums at a border of 10^5 tokens
 // are off by more than the uniform numbers' spacing.  So a weight is computed to 2^-40 (pairs
-// of binary32 numbers) and becomes a 64-bit integer in units of 2^-44: sums are then exact, in
+// of binary32 numbers) and becomes a 64-bit integer in units of 2^-43: sums are then exact, in
 // any order, and every comparison is one of integers.
 #include "decode.h"
 #include "mx_device.cuh"
@@ -18,18 +18,18 @@ namespace mx {
 namespace {
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kMaxCtas = 8;
-constexpr int kUnit = 44;  // weights are in units of 2^-44
+constexpr int kMaxCtas = 16;
+constexpr int kUnit = 43;  // weights are in units of 2^-43
 constexpr int kTable = 256;
-constexpr int kBins = 512;     // the last one: weights that are 0
-constexpr float kSpan = 46.0f; // powers of two that the others cover
+constexpr int kBins = 1024;    // the last one: weights that are 0
+constexpr float kSpan = 45.0f; // powers of two that the others cover
 constexpr int kList = 1024;    // logits of a bin that are sorted
 constexpr int kLimb = 15;      // bits of a weight that one 32-bit sum takes of a CTA's 2^15
 constexpr int kLimbs = 3;
 
-// Order of logits as unsigned integers (no NaN among them).
+// Order of logits as unsigned integers (no NaN, no -0 among them).
 __device__ __forceinline__ uint32_t logit_key(float v) {
-  const uint32_t u = __float_as_uint(v == 0.0f ? 0.0f : v);  // (-0 equals 0)
+  const uint32_t u = __float_as_uint(v);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 __device__ __forceinline__ float key_logit(uint32_t k) {
@@ -57,7 +57,7 @@ struct Scale {
   float top, hi, lo;
 };
 
-// round(2^44 exp((l - top) / temperature)), l <= top; 0 below 2^-45.
+// round(2^43 exp((l - top) / temperature)), l <= top; 0 below 2^-44.
 __device__ __forceinline__ uint64_t weight_of(float l, const Scale &c, const float2 *table) {
   if (l == c.top) return 1ull << kUnit;
   // l - top, exactly, as d + e
@@ -66,11 +66,12 @@ __device__ __forceinline__ uint64_t weight_of(float l, const Scale &c, const flo
   const float p = d * c.hi;
   if (!(p > -46.0f)) return 0;
   const float pe = fmaf(d, c.hi, -p) + fmaf(d, c.lo, e * c.hi);
-  // 2^(p + pe) = 2^(k / 256) 2^r
-  const float kf = rintf(p * 256.0f);
-  const int k = static_cast<int>(kf);
-  const float r = fmaf(kf, -0x1p-8f, p);
-  // y = r ln 2 as yh + yl, then e^y - 1 as q + ql
+  // 2^(p + pe) = 2^(k / 256) 2^r, k to the nearest: the sum with 1.5 * 2^23 ends in it (the
+  // conversion instructions have an eighth of an addition's rate)
+  const float kb = fmaf(p, 256.0f, 0x1.8p23f);
+  const int k = __float_as_int(kb) - 0x4B400000;
+  const float r = fmaf(kb - 0x1.8p23f, -0x1p-8f, p);
+  // y = r ln 2 as yh + yl, then e^y - 1 as qh + qe
   const float yh = r * 0x1.62e43p-1f;
   const float yl = fmaf(r, 0x1.62e43p-1f, -yh) + fmaf(r, -0x1.05c61p-29f, pe * 0x1.62e43p-1f);
   const float ql = fmaf(yl, yh, yl) + yh * yh * fmaf(yh, fmaf(yh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f);
@@ -80,11 +81,14 @@ __device__ __forceinline__ uint64_t weight_of(float l, const Scale &c, const flo
   const float m = t.x * qh;
   const float ml = fmaf(t.x, qh, -m) + fmaf(t.x, qe, fmaf(t.y, qh, t.y));
   const float s = t.x + m;
-  const float sl = (m - (s - t.x)) + ml;  // the value is s + sl, s in [0.99, 2), |sl| < 2^-22
-  const int64_t fixed = (static_cast<int64_t>(static_cast<int32_t>(s * 0x1p24f)) << 28) +
-                        static_cast<int64_t>(__float2int_rn(sl * 0x1p52f));  // units of 2^-52
-  const int shift = 52 - kUnit - (k >> 8);  // 8 .. 55
-  return static_cast<uint64_t>((fixed + (1ll << (shift - 1))) >> shift);
+  // s + sl in units of 2^-43, s in [0.99, 2.01): s + 4 is a multiple of 2^-21, what is left, below
+  // 2^-21 with sl, and 1.5 * 2^-20 one of 2^-43
+  const float high = s + 4.0f;
+  const float low = (s - (high - 4.0f)) + ((m - (s - t.x)) + ml) + 0x1.8p-20f;
+  const int64_t fixed = (static_cast<int64_t>(__float_as_int(high) - 0x40800000) << (kUnit - 21)) +
+                        (__float_as_int(low) - 0x35C00000);
+  const int shift = -(k >> 8);  // 0 .. 46
+  return static_cast<uint64_t>((fixed + ((1ll << shift) >> 1)) >> shift);
 }
 
 // floor(f * n) for f in [0, 1) (the nearest inside, if it is outside) and n < 2^63.
@@ -128,6 +132,12 @@ __device__ __forceinline__ uint64_t warp_upto(uint64_t v, int lane) {  // the su
   return v;
 }
 
+// A logit and its index as one number, in the order of a row: greater logits, then lower
+// indexes, are greater.
+__device__ __forceinline__ uint64_t entry_of(float l, int index) {
+  return static_cast<uint64_t>(logit_key(l)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(index));
+}
+
 struct Shared {
   float2 table[kTable];
   uint32_t bins[1 + kLimbs][kBins];  // counts; weights in limbs of kLimb bits
@@ -143,7 +153,7 @@ struct Shared {
 template <bool FP32>
 __global__ void __launch_bounds__(kThreads, 2)
     sample_kernel(const __grid_constant__ SampleArgs a, int ctas, int slice) {
-  extern __shared__ __align__(16) uint32_t keys[];  // of this CTA's slice
+  extern __shared__ __align__(16) float logits[];  // this CTA's slice
   __shared__ Shared sh;
   cluster_arrive_relaxed();
   griddep_launch_dependents();
@@ -165,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (top_k <= 0 || top_k > a.vocab) top_k = a.vocab;
 
   // the slice, four logits a lane at a time; the largest, and the lowest index that has it
-  uint64_t best = 0;
+  float high = -INFINITY;
+  int high_at = 0;
   bool nan = temperature != temperature || top_p != top_p || min_p != min_p || uniform != uniform;
   const bool fours = (static_cast<int64_t>(row) * a.ld) % 4 == 0;
 #pragma unroll 4
@@ -191,17 +202,15 @@ __global__ void __launch_bounds__(kThreads, 2)
                       : __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(a.logits)[e + j]) << 16);
       }
     }
-    uint32_t k[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       nan |= v[j] != v[j];
-      k[j] = logit_key(v[j]);
-      const uint64_t mine = static_cast<uint64_t>(k[j]) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(at + j));
-      best = mine > best ? mine : best;
+      v[j] += 0.0f;  // (-0 equals 0)
+      if (v[j] > high) high = v[j], high_at = at + j;  // (the lowest index of equal ones)
     }
-    *reinterpret_cast<uint4 *>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+    *reinterpret_cast<float4 *>(logits + i) = make_float4(v[0], v[1], v[2], v[3]);
   }
-  if (nan) best = ~0ull;
+  uint64_t best = nan ? ~0ull : entry_of(high, high_at);
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) {
     const uint64_t other = __shfl_xor_sync(0xFFFFFFFFu, best, m);
@@ -225,8 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int set = share(best);
     for (int r = 0; r < ctas; ++r) best = sh.slots[set][r] > best ? sh.slots[set][r] : best;
   }
-  const uint32_t top_key = static_cast<uint32_t>(best >> 32);
-  const float top = key_logit(top_key);
+  const float top = key_logit(static_cast<uint32_t>(best >> 32));
   const bool none = best == ~0ull || top == -INFINITY;
   if (none || temperature <= 0.0f) {
     if (rank == 0 && threadIdx.x == 0 && in_bounds(row, 1, a.rows, a.status)) {
@@ -244,25 +252,34 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   __syncthreads();
   const Scale scale = sh.scale;
-  const uint32_t least = logit_key(-INFINITY);
 
-  // kept: keys above `key`, and of those equal to it the ones up to index `last`
-  uint32_t limit_key = least;
+  // kept: logits above `limit`, and of those equal to it the ones up to index `last`
+  float limit = -INFINITY;
   int limit_last = -1;
-  auto kept = [&](uint32_t k, int i) { return k > limit_key || (k == limit_key && base + i <= limit_last); };
-  auto weight = [&](uint32_t k) { return weight_of(key_logit(k), scale, sh.table); };
+  auto kept = [&](float l, int i) { return l > limit || (l == limit && base + i <= limit_last); };
+  auto weight = [&](float l) { return weight_of(l, scale, sh.table); };
+  // f(logit, place in the slice) for each of the warp's segment
+  auto each = [&](auto &&f) {
+#pragma unroll 2
+    for (int i = from + lane * 4; i < from + segment; i += 128) {
+      const float4 v = *reinterpret_cast<const float4 *>(logits + i);
+      f(v.x, i), f(v.y, i + 1), f(v.z, i + 2), f(v.w, i + 3);
+    }
+  };
 
   // Bins of equal width in the exponent, in descending order of the logits (a logit's bin is a
   // monotonous function of it, in binary32 too).
   const float per_bin = scale.hi * ((kBins - 1) / kSpan);
-  auto place_of = [&](uint32_t k) {
-    const float x = k == top_key ? 0.0f : (top - key_logit(k)) * per_bin;
+  auto place_of = [&](float l) {
+    const float x = l == top ? 0.0f : (top - l) * per_bin;
     return x < static_cast<float>(kBins - 1) ? x : static_cast<float>(kBins - 1);
   };
-  auto bin_of = [&](uint32_t k) { return static_cast<int>(place_of(k)); };
-  // the same within a bin (binary32 has 15 bits and more left there)
-  auto bin_within = [&](uint32_t k, int bin) {
-    return static_cast<int>((place_of(k) - static_cast<float>(bin)) * static_cast<float>(kBins));
+  // (to the nearest whole number: the sum with 2^23 ends in it)
+  auto bin_of = [&](float l) { return __float_as_int(place_of(l) + 0x1p23f) - 0x4B000000; };
+  // the same within a bin (binary32 has 14 bits and more left there)
+  auto bin_within = [&](float l, int bin) {
+    const float x = (place_of(l) - static_cast<float>(bin) + 0.5f) * static_cast<float>(kBins - 1);
+    return __float_as_int(x + 0x1p23f) - 0x4B000000;
   };
   auto add_weight = [&](int bin, uint64_t w) {
 #pragma unroll
@@ -285,8 +302,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     return n;
   };
-  // Totals of the bins up to and with each thread's (a bin a thread), and of all.
-  static_assert(kBins == kThreads && kList == 2 * kThreads, "a bin, two entries a thread");
+  // Sums up to and with each thread's, and of all.
   auto scan = [&](uint64_t mine, uint64_t &all) {
     uint64_t upto = warp_upto(mine, lane);
     if (lane == 31) sh.sums[1][warp] = upto;
@@ -298,36 +314,52 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     return upto;
   };
-
-  // The bin (in sh.piece) where the sum reaches `want`, and what is wanted of it (in found[1]).
-  auto find_bin = [&](uint64_t mine, uint64_t upto, uint64_t want) {
+  // A thread has two neighbouring bins, or entries of the list.
+  static_assert(kBins == 2 * kThreads && kList == 2 * kThreads, "two a thread");
+  struct Two {
+    uint64_t of[2], before;
+  };
+  auto scan_bins = [&](bool weights, uint64_t &all) {
+    Two t;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) t.of[e] = bin_total(2 * threadIdx.x + e, weights);
+    t.before = scan(t.of[0] + t.of[1], all) - t.of[0] - t.of[1];
+    return t;
+  };
+  // The bin (in sh.piece) where the sum reaches `want`, and what is wanted of it (in found[1]);
+  // the last bin if none does.
+  auto find_bin = [&](const Two &t, uint64_t want) {
     __syncthreads();
-    if (upto - mine < want && want <= upto) sh.piece = threadIdx.x, sh.found[1] = want - (upto - mine);
+    if (threadIdx.x == 0) sh.piece = kBins - 1;
+    __syncthreads();
+    uint64_t before = t.before;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if (before < want && want <= before + t.of[e]) sh.piece = 2 * threadIdx.x + e, sh.found[1] = want - before;
+      before += t.of[e];
+    }
     __syncthreads();
   };
 
-  // The limit such that the kept of the logits in `bin` with the greatest (key, ~index) are the
-  // fewest whose number (weights) comes to at least `want`, which the whole bin does.
+  // The limit such that the first in order of the kept logits in `bin` are the fewest whose
+  // number (weights) comes to at least `want`, which the whole bin does.
   int uses = 0;
   auto cut = [&](int bin, uint64_t want, bool weights) {
     int within = -1;  // a bin of the bin, if not -1
-    auto belongs = [&](uint32_t k, int i) {
-      return k > least && bin_of(k) == bin && (within < 0 || bin_within(k, bin) == within) && kept(k, i);
+    auto belongs = [&](float l, int i) {
+      return kept(l, i) && bin_of(l) == bin && (within < 0 || bin_within(l, bin) == within);
     };
     // how many there are; up to kList of them in the first CTA's list
     auto gather = [&] {
       const uint32_t list_at = mapa_shared(smem_u32(sh.list), 0), listed_at = mapa_shared(smem_u32(&sh.listed[uses++]), 0);
-      for (int i0 = from; i0 < from + segment; i0 += 32) {
-        const int i = i0 + lane;
-        const uint32_t k = keys[i];
-        const bool in = belongs(k, i);
+      each([&](float l, int i) {
+        const bool in = belongs(l, i);
         const uint32_t which = __ballot_sync(0xFFFFFFFFu, in);
-        if (which == 0) continue;
+        if (which == 0) return;
         uint32_t to = lane == 0 ? add_cluster_u32(listed_at, __popc(which)) : 0;
         to = __shfl_sync(0xFFFFFFFFu, to, 0) + __popc(which & ((1u << lane) - 1));
-        if (in && to < kList)
-          st_cluster_u64(list_at + to * 8, static_cast<uint64_t>(k) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(base + i)));
-      }
+        if (in && to < kList) st_cluster_u64(list_at + to * 8, entry_of(l, base + i));
+      });
       cluster_sync();
       return ld_cluster_u32(listed_at);
     };
@@ -339,19 +371,16 @@ __global__ void __launch_bounds__(kThreads, 2)
         else
           sh.bins[0][i % kBins] = 0;
       __syncthreads();
-      for (int i = from + lane; i < from + segment; i += 32) {
-        const uint32_t k = keys[i];
-        if (!belongs(k, i)) continue;
+      each([&](float l, int i) {
+        if (!belongs(l, i)) return;
         if (weights)
-          add_weight(bin_within(k, bin), weight(k));
+          add_weight(bin_within(l, bin), weight(l));
         else
-          atomicAdd(&sh.bins[0][bin_within(k, bin)], 1u);
-      }
+          atomicAdd(&sh.bins[0][bin_within(l, bin)], 1u);
+      });
       cluster_sync();
-      const uint64_t mine = bin_total(threadIdx.x, weights);
       uint64_t all;
-      const uint64_t upto = scan(mine, all);
-      find_bin(mine, upto, want);
+      find_bin(scan_bins(weights, all), want);
       within = sh.piece;
       want = sh.found[1];
       n = gather();
@@ -377,7 +406,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int e = 0; e < 2; ++e) {
           const uint32_t i = 2 * threadIdx.x + e;
           entry[e] = i < n ? sh.list[i] : 0;
-          own[e] = i >= n ? 0 : weights ? weight(static_cast<uint32_t>(entry[e] >> 32)) : 1;
+          own[e] = i >= n ? 0 : weights ? weight(key_logit(static_cast<uint32_t>(entry[e] >> 32))) : 1;
         }
         uint64_t all;
         uint64_t before = scan(own[0] + own[1], all) - own[0] - own[1];
@@ -389,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
       }
       cluster_sync();
-      limit_key = static_cast<uint32_t>(sh.found[0] >> 32);
+      limit = key_logit(static_cast<uint32_t>(sh.found[0] >> 32));
       limit_last = static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(sh.found[0]));
       return;
     }
@@ -408,17 +437,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     };
     auto above = [&](uint32_t key) {  // of the bin's kept ones with greater keys
       uint64_t v = 0;
-      for (int i = from + lane; i < from + segment; i += 32) {
-        const uint32_t k = keys[i];
-        if (k > key && belongs(k, i)) v += weights ? weight(k) : 1;
-      }
+      const float border = key_logit(key);
+      each([&](float l, int i) {
+        if (l > border && belongs(l, i)) v += weights ? weight(l) : 1;
+      });
       return total_of(v);
     };
     uint32_t high = 0, low = 0xFFFFFFFFu;
-    for (int i = from + lane; i < from + segment; i += 32) {
-      const uint32_t k = keys[i];
-      if (belongs(k, i)) high = max(high, k), low = min(low, k);
-    }
+    each([&](float l, int i) {
+      if (belongs(l, i)) high = max(high, logit_key(l)), low = min(low, logit_key(l));
+    });
     high = __reduce_max_sync(0xFFFFFFFFu, high);
     low = __reduce_min_sync(0xFFFFFFFFu, low);
     __syncthreads();
@@ -446,12 +474,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         high = mid;
     }
     uint64_t rest = want - above(low);  // of those equal to it
+    const float border = key_logit(low);
     if (weights) {
-      const uint64_t each = weight(low);
-      rest = (rest + each - 1) / each;
+      const uint64_t one = weight(border);
+      rest = (rest + one - 1) / one;
     }
     uint64_t mine = 0;
-    for (int i = from + lane; i < from + segment; i += 32) mine += keys[i] == low;
+    each([&](float l, int) { mine += l == border; });
     mine = warp_total(mine);
     __syncthreads();
     if (lane == 0) sh.sums[0][warp] = mine;
@@ -465,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int r = 0; r < rank; ++r) before += sh.slots[set][r];
     if (before < rest && rest <= before + mine) {
       for (int i0 = from; i0 < from + segment; i0 += 32) {
-        const uint32_t which = __ballot_sync(0xFFFFFFFFu, keys[i0 + lane] == low);
+        const uint32_t which = __ballot_sync(0xFFFFFFFFu, logits[i0 + lane] == border);
         if (before + __popc(which) < rest) {
           before += __popc(which);
           continue;
@@ -476,32 +505,27 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     cluster_sync();
-    limit_key = low;
+    limit = border;
     limit_last = static_cast<int>(sh.found[0]);
   };
 
   if (top_k < a.vocab) {
-    for (int i = from + lane; i < from + segment; i += 32)
-      if (keys[i] > least) atomicAdd(&sh.bins[0][bin_of(keys[i])], 1u);
+    each([&](float l, int) {
+      if (l > -INFINITY) atomicAdd(&sh.bins[0][bin_of(l)], 1u);
+    });
     cluster_sync();
-    const uint64_t mine = bin_total(threadIdx.x, false);
     uint64_t all;
-    const uint64_t upto = scan(mine, all);
-    if (threadIdx.x == 0) sh.piece = kBins - 1;
-    find_bin(mine, upto, static_cast<uint64_t>(top_k));
+    find_bin(scan_bins(false, all), static_cast<uint64_t>(top_k));
     // (the k-th in the last bin, or less than k in all: what is cut off weighs nothing)
     if (sh.piece < kBins - 1) cut(sh.piece, sh.found[1], false);
   }
   if (top_p < 1.0f) {
-    for (int i = from + lane; i < from + segment; i += 32) {
-      const uint32_t k = keys[i];
-      if (k <= least || !kept(k, i)) continue;
-      add_weight(bin_of(k), weight(k));
-    }
+    each([&](float l, int i) {
+      if (kept(l, i)) add_weight(bin_of(l), weight(l));
+    });
     cluster_sync();
-    const uint64_t mine = bin_total(threadIdx.x, true);
     uint64_t all;
-    const uint64_t upto = scan(mine, all);
+    const Two bins = scan_bins(true, all);
     uint64_t want = part_of(top_p, all);  // the least whole number that is not below top_p * all
     {
       const uint32_t b = __float_as_uint(top_p);
@@ -511,22 +535,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!whole) ++want;
     }
     if (want < 1) want = 1;
-    find_bin(mine, upto, want);
+    find_bin(bins, want);
     cut(sh.piece, sh.found[1], true);
   }
   const uint64_t floor_weight =
       min_p > 0.0f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.0f) * static_cast<float>(1ull << kUnit))) : 1;
-  auto final_weight = [&](int i) -> uint64_t {
-    const uint32_t k = keys[i];
-    if (k <= least || !kept(k, i)) return 0;
-    const uint64_t w = weight(k);
+  auto final_weight = [&](float l, int i) -> uint64_t {
+    if (!kept(l, i)) return 0;
+    const uint64_t w = weight(l);
     return w >= floor_weight ? w : 0;
   };
 
   // the kept weights in the order of the indexes: by warps' segments, then within the one that
   // has the place, by all the CTA's warps
   uint64_t mine = 0;
-  for (int i = from + lane; i < from + segment; i += 32) mine += final_weight(i);
+  each([&](float l, int i) { mine += final_weight(l, i); });
   mine = warp_total(mine);
   __syncthreads();
   if (lane == 0) sh.sums[0][warp] = mine;
@@ -553,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int length = (segment / 32 + kWarps - 1) / kWarps * 32;
     const int p0 = min(begin + warp * length, begin + segment), p1 = min(p0 + length, begin + segment);
     uint64_t part = 0;
-    for (int i = p0 + lane; i < p1; i += 32) part += final_weight(i);
+    for (int i = p0 + lane; i < p1; i += 32) part += final_weight(logits[i], i);
     part = warp_total(part);
     __syncthreads();
     if (lane == 0) sh.sums[0][warp] = part;
@@ -561,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int w = 0; w < warp; ++w) before += sh.sums[0][w];
     if (before <= target && target < before + part) {
       for (int i0 = p0; i0 < p1; i0 += 32) {
-        const uint64_t w = final_weight(i0 + lane);
+        const uint64_t w = final_weight(logits[i0 + lane], i0 + lane);
         const uint64_t upto = before + warp_upto(w, lane);
         const uint32_t over = __ballot_sync(0xFFFFFFFFu, upto > target);
         if (over != 0) {
@@ -582,15 +605,19 @@ __global__ void __launch_bounds__(kThreads, 2)
 template <bool FP32>
 cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
   int ctas = 1;
-  while (ctas < kMaxCtas && ctas * 4096 < a.vocab) ctas *= 2;
+  while (ctas < 8 && ctas * 4096 < a.vocab) ctas *= 2;
+  // (few rows: more CTAs a row than may be taken for granted)
+  if (static_cast<int64_t>(a.rows) * ctas * 2 <= a.num_sms && ctas == 8 && a.vocab > 32768) ctas = kMaxCtas;
   constexpr int kStep = kWarps * 128;  // a warp's segment is a multiple of 128
   const int per = (a.vocab + ctas - 1) / ctas;
   const int slice = (per + kStep - 1) / kStep * kStep;
   const void *func = reinterpret_cast<const void *>(sample_kernel<FP32>);
   if (!kernel_setup_get(func, nullptr)) {
     const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kSampleMaxVocab / kMaxCtas * static_cast<int>(sizeof(uint32_t)));
+                                               kSampleMaxVocab / 8 * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) return e;
+    const cudaError_t n = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (n != cudaSuccess) return n;
     kernel_setup_put(func, 0);
   }
   cudaLaunchConfig_t cfg = {};
@@ -603,7 +630,7 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
   attr[1].val.clusterDim.z = 1;
   cfg.gridDim = dim3(static_cast<unsigned>(ctas) * static_cast<unsigned>(a.rows));
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(slice) * sizeof(uint32_t);
+  cfg.dynamicSmemBytes = static_cast<size_t>(slice) * sizeof(float);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
