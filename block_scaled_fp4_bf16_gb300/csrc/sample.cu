@@ -5,7 +5,7 @@
 // row; each of its CTAs reads a contiguous slice once into shared memory, in which all
 // further passes run.  A threshold takes three steps: counts (top-k) or weights (top-p) of
 // bins of equal width in the exponent, the bin where the wanted sum is reached, and that
-// bin's few logits, sorted by one CTA.
+// bin's few logits, compared with one another by one CTA.
 //
 // Borders are what can go wrong: with weights to binary32 the sums at a border of 10^5 tokens
 // are off by more than the uniform numbers' spacing.  So a weight is computed to 2^-40 (pairs
@@ -23,7 +23,7 @@ constexpr int kUnit = 43;  // weights are in units of 2^-43
 constexpr int kTable = 256;
 constexpr int kBins = 1024;    // the last one: weights that are 0
 constexpr float kSpan = 45.0f; // powers of two that the others cover
-constexpr int kList = 1024;    // logits of a bin that are sorted
+constexpr int kList = 1024;    // logits of a bin that one CTA takes
 constexpr int kLimb = 15;      // bits of a weight that one 32-bit sum takes of a CTA's 2^15
 constexpr int kLimbs = 3;
 
@@ -59,12 +59,10 @@ struct Scale {
 
 // round(2^43 exp((l - top) / temperature)), l <= top; 0 below 2^-44.
 __device__ __forceinline__ uint64_t weight_of(float l, const Scale &c, const float2 *table) {
-  if (l == c.top) return 1ull << kUnit;
   // l - top, exactly, as d + e
   const float d = l - c.top, b = d - l;
   const float e = (l - (d - b)) + (-c.top - b);
-  const float p = d * c.hi;
-  if (!(p > -46.0f)) return 0;
+  const float exponent = d * c.hi, p = fmaxf(exponent, -46.0f);  // (-46 for NaN, too)
   const float pe = fmaf(d, c.hi, -p) + fmaf(d, c.lo, e * c.hi);
   // 2^(p + pe) = 2^(k / 256) 2^r, k to the nearest: the sum with 1.5 * 2^23 ends in it (the
   // conversion instructions have an eighth of an addition's rate)
@@ -88,7 +86,9 @@ __device__ __forceinline__ uint64_t weight_of(float l, const Scale &c, const flo
   const int64_t fixed = (static_cast<int64_t>(__float_as_int(high) - 0x40800000) << (kUnit - 21)) +
                         (__float_as_int(low) - 0x35C00000);
   const int shift = -(k >> 8);  // 0 .. 46
-  return static_cast<uint64_t>((fixed + ((1ll << shift) >> 1)) >> shift);
+  const uint64_t w = static_cast<uint64_t>((fixed + ((1ll << shift) >> 1)) >> shift);
+  // (no branch before: four of these run side by side.  An infinite top's difference is NaN.)
+  return l == c.top ? 1ull << kUnit : exponent > -46.0f ? w : 0;
 }
 
 // floor(f * n) for f in [0, 1) (the nearest inside, if it is outside) and n < 2^63.
@@ -112,12 +112,6 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t add_cluster_u32(uint32_t addr, uint32_t n) {
-  uint32_t v;
-  asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(v) : "r"(addr), "r"(n) : "memory");
-  return v;
-}
-
 __device__ __forceinline__ uint64_t warp_total(uint64_t v) {
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
@@ -144,9 +138,9 @@ struct Shared {
   uint64_t list[kList];              // of the cluster's first CTA: (key, ~index)
   uint64_t slots[2][kMaxCtas];       // every CTA's number
   uint64_t sums[2][kWarps];
+  uint64_t totals[kBins];            // of the cluster's bins
   uint64_t found[2];                 // what a search found
-  Scale scale;
-  uint32_t listed[4];                // entries, of each use of the list
+  uint32_t listed;                   // entries of a list
   int piece;
 };
 
@@ -159,7 +153,6 @@ __global__ void __launch_bounds__(kThreads, 2)
   griddep_launch_dependents();
   if (threadIdx.x < kTable) sh.table[threadIdx.x] = table_entry(threadIdx.x);
   for (int i = threadIdx.x; i < (1 + kLimbs) * kBins; i += kThreads) (&sh.bins[0][0])[i] = 0;
-  if (threadIdx.x < 4) sh.listed[threadIdx.x] = 0;
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank()), row = static_cast<int>(cluster_id_x());
@@ -244,14 +237,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     cluster_sync();  // (no CTA ends while another may still write to it)
     return;
   }
-  if (threadIdx.x == 0) {
-    const double c = 1.4426950408889634074 / static_cast<double>(fmaxf(temperature, 0x1p-100f));
-    sh.scale.top = top;
-    sh.scale.hi = static_cast<float>(c);
-    sh.scale.lo = static_cast<float>(c - static_cast<double>(sh.scale.hi));
+  Scale scale;
+  scale.top = top;
+  {
+    // log2(e) / temperature as hi + lo
+    const float t = fminf(fmaxf(temperature, 0x1p-100f), 0x1p100f);
+    scale.hi = 0x1.715476p+0f / t;
+    scale.lo = (fmaf(-scale.hi, t, 0x1.715476p+0f) + 0x1.4ae0cp-26f) / t;
   }
-  __syncthreads();
-  const Scale scale = sh.scale;
 
   // kept: logits above `limit`, and of those equal to it the ones up to index `last`
   float limit = -INFINITY;
@@ -264,6 +257,23 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = from + lane * 4; i < from + segment; i += 128) {
       const float4 v = *reinterpret_cast<const float4 *>(logits + i);
       f(v.x, i), f(v.y, i + 1), f(v.z, i + 2), f(v.w, i + 3);
+    }
+  };
+  // f(weight, logit): the same with the weights of those that are kept (0 for the others), four
+  // computed at once; a warp goes past four by 32 of which it keeps none
+  auto each_weight = [&](auto &&f) {
+    for (int i = from + lane * 4; i < from + segment; i += 128) {
+      const float4 x = *reinterpret_cast<const float4 *>(logits + i);
+      const float v[4] = {x.x, x.y, x.z, x.w};
+      bool in[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) in[j] = kept(v[j], i + j);
+      if (!__any_sync(0xFFFFFFFFu, in[0] || in[1] || in[2] || in[3])) continue;
+      uint64_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) w[j] = weight(v[j]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) f(in[j] ? w[j] : 0, v[j]);
     }
   };
 
@@ -281,26 +291,17 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float x = (place_of(l) - static_cast<float>(bin) + 0.5f) * static_cast<float>(kBins - 1);
     return __float_as_int(x + 0x1p23f) - 0x4B000000;
   };
+  auto clear_bins = [&] {
+    __syncthreads();
+    for (int i = threadIdx.x; i < (1 + kLimbs) * kBins; i += kThreads) (&sh.bins[0][0])[i] = 0;
+    __syncthreads();
+  };
   auto add_weight = [&](int bin, uint64_t w) {
 #pragma unroll
     for (int l = 0; l < kLimbs; ++l) {
       const uint32_t limb = static_cast<uint32_t>(w >> (kLimb * l)) & ((1u << kLimb) - 1);
       if (limb != 0) atomicAdd(&sh.bins[1 + l][bin], limb);
     }
-  };
-  // The cluster's sum of one bin: of the counts, or of the weights.
-  auto bin_total = [&](int bin, bool weights) {
-    uint64_t n = 0;
-    for (int r = 0; r < ctas; ++r) {
-      if (weights) {
-#pragma unroll
-        for (int l = 0; l < kLimbs; ++l)
-          n += static_cast<uint64_t>(ld_cluster_u32(mapa_shared(smem_u32(&sh.bins[1 + l][bin]), r))) << (kLimb * l);
-      } else {
-        n += ld_cluster_u32(mapa_shared(smem_u32(&sh.bins[0][bin]), r));
-      }
-    }
-    return n;
   };
   // Sums up to and with each thread's, and of all.
   auto scan = [&](uint64_t mine, uint64_t &all) {
@@ -319,10 +320,33 @@ __global__ void __launch_bounds__(kThreads, 2)
   struct Two {
     uint64_t of[2], before;
   };
+  // The cluster's sums of the bins: a CTA adds up its share of them and sends the sums to all.
   auto scan_bins = [&](bool weights, uint64_t &all) {
+    cluster_sync();
+    const int own = kBins / ctas;  // bins of this CTA; a thread adds up two numbers
+    uint64_t n[2] = {};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int item = threadIdx.x + e * kThreads, source = item / own, from_bin = rank * own + item % own;
+      if (weights) {
+#pragma unroll
+        for (int l = 0; l < kLimbs; ++l)
+          n[e] += static_cast<uint64_t>(ld_cluster_u32(mapa_shared(smem_u32(&sh.bins[1 + l][from_bin]), source))) << (kLimb * l);
+      } else {
+        n[e] = ld_cluster_u32(mapa_shared(smem_u32(&sh.bins[0][from_bin]), source));
+      }
+      sh.list[item] = n[e];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < own; i += kThreads) {
+      uint64_t total = 0;
+      for (int r = 0; r < ctas; ++r) total += sh.list[r * own + i];
+      for (int r = 0; r < ctas; ++r) st_cluster_u64(mapa_shared(smem_u32(&sh.totals[rank * own + i]), r), total);
+    }
+    cluster_sync();
     Two t;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) t.of[e] = bin_total(2 * threadIdx.x + e, weights);
+    for (int e = 0; e < 2; ++e) t.of[e] = sh.totals[2 * threadIdx.x + e];
     t.before = scan(t.of[0] + t.of[1], all) - t.of[0] - t.of[1];
     return t;
   };
@@ -343,34 +367,42 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // The limit such that the first in order of the kept logits in `bin` are the fewest whose
   // number (weights) comes to at least `want`, which the whole bin does.
-  int uses = 0;
   auto cut = [&](int bin, uint64_t want, bool weights) {
     int within = -1;  // a bin of the bin, if not -1
     auto belongs = [&](float l, int i) {
       return kept(l, i) && bin_of(l) == bin && (within < 0 || bin_within(l, bin) == within);
     };
-    // how many there are; up to kList of them in the first CTA's list
+    // how many there are; if not above kList, all of them in the first CTA's list (each CTA's own
+    // come to its bins' memory first: nobody reads those any more)
+    uint64_t *const mine = reinterpret_cast<uint64_t *>(&sh.bins[0][0]);
+    static_assert(sizeof(sh.bins) >= kList * sizeof(uint64_t), "a list in the bins' place");
     auto gather = [&] {
-      const uint32_t list_at = mapa_shared(smem_u32(sh.list), 0), listed_at = mapa_shared(smem_u32(&sh.listed[uses++]), 0);
+      if (threadIdx.x == 0) sh.listed = 0;
+      __syncthreads();
       each([&](float l, int i) {
-        const bool in = belongs(l, i);
-        const uint32_t which = __ballot_sync(0xFFFFFFFFu, in);
-        if (which == 0) return;
-        uint32_t to = lane == 0 ? add_cluster_u32(listed_at, __popc(which)) : 0;
-        to = __shfl_sync(0xFFFFFFFFu, to, 0) + __popc(which & ((1u << lane) - 1));
-        if (in && to < kList) st_cluster_u64(list_at + to * 8, entry_of(l, base + i));
+        if (!belongs(l, i)) return;
+        const uint32_t to = atomicAdd(&sh.listed, 1u);
+        if (to < kList) mine[to] = entry_of(l, base + i);
       });
-      cluster_sync();
-      return ld_cluster_u32(listed_at);
+      __syncthreads();
+      const uint32_t here = sh.listed;
+      const int set = share(here);
+      uint32_t before = 0, n = 0;
+      for (int r = 0; r < ctas; ++r) {
+        const uint32_t there = static_cast<uint32_t>(sh.slots[set][r]);
+        if (r < rank) before += there;
+        n += there;
+      }
+      if (n <= kList) {
+        for (uint32_t i = threadIdx.x; i < here; i += kThreads)
+          st_cluster_u64(mapa_shared(smem_u32(&sh.list[before + i]), 0), mine[i]);
+        cluster_sync();
+      }
+      return n;
     };
     uint32_t n = gather();
-    if (n > kList) {  // divide the bin, too (all CTAs have read the bins: they are past a barrier)
-      for (int i = threadIdx.x; i < kLimbs * kBins; i += kThreads)
-        if (weights)
-          sh.bins[1 + i / kBins][i % kBins] = 0;
-        else
-          sh.bins[0][i % kBins] = 0;
-      __syncthreads();
+    if (n > kList) {  // divide the bin, too
+      clear_bins();
       each([&](float l, int i) {
         if (!belongs(l, i)) return;
         if (weights)
@@ -378,7 +410,6 @@ __global__ void __launch_bounds__(kThreads, 2)
         else
           atomicAdd(&sh.bins[0][bin_within(l, bin)], 1u);
       });
-      cluster_sync();
       uint64_t all;
       find_bin(scan_bins(weights, all), want);
       within = sh.piece;
@@ -387,34 +418,47 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (n <= kList) {
       if (rank == 0) {
-        // sorted in descending order (bitonic, of the next power of two), then added up
-        uint32_t p = 2;
-        while (p < n) p *= 2;
-        for (uint32_t i = n + threadIdx.x; i < p; i += kThreads) sh.list[i] = 0;
-        for (uint32_t size = 2; size <= p; size *= 2)
-          for (uint32_t step = size / 2; step > 0; step /= 2) {
-            __syncthreads();
-            if (threadIdx.x < p / 2) {
-              const uint32_t i = 2 * threadIdx.x - (threadIdx.x & (step - 1)), j = i + step;
-              const uint64_t x = sh.list[i], y = sh.list[j];
-              if ((x < y) == ((i & size) == 0)) sh.list[i] = y, sh.list[j] = x;
-            }
+        // This CTA finds the one with which the sum is reached: by bins once more, now among the
+        // entries, and in the bin found one by one.  `mine` takes the entries of that bin, its
+        // second half their weights.
+        auto within_of = [&](uint64_t entry) {
+          const float l = key_logit(static_cast<uint32_t>(entry >> 32));
+          if (within < 0) return bin_within(l, bin);
+          const float x = (place_of(l) - static_cast<float>(bin) + 0.5f) * static_cast<float>(kBins - 1);
+          return __float_as_int((x - static_cast<float>(within) + 0.5f) * static_cast<float>(kBins - 1) + 0x1p23f) - 0x4B000000;
+        };
+        auto size_of = [&](uint64_t entry) {
+          return weights ? weight(key_logit(static_cast<uint32_t>(entry >> 32))) : 1ull;
+        };
+        for (int i = threadIdx.x; i < kBins; i += kThreads) sh.totals[i] = 0;
+        if (threadIdx.x == 0) sh.listed = 0;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+          atomicAdd(reinterpret_cast<unsigned long long *>(&sh.totals[within_of(sh.list[i])]), size_of(sh.list[i]));
+        __syncthreads();
+        Two t;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) t.of[e] = sh.totals[2 * threadIdx.x + e];
+        uint64_t all;
+        t.before = scan(t.of[0] + t.of[1], all) - t.of[0] - t.of[1];
+        find_bin(t, want);
+        const int third = sh.piece;
+        const uint64_t rest = sh.found[1];
+        uint64_t *const sizes = mine + kList;
+        static_assert(sizeof(sh.bins) >= 2 * kList * sizeof(uint64_t), "entries and weights in the bins' place");
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+          if (within_of(sh.list[i]) == third) {
+            const uint32_t to = atomicAdd(&sh.listed, 1u);
+            mine[to] = sh.list[i];
+            sizes[to] = size_of(sh.list[i]);
           }
         __syncthreads();
-        uint64_t entry[2], own[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint32_t i = 2 * threadIdx.x + e;
-          entry[e] = i < n ? sh.list[i] : 0;
-          own[e] = i >= n ? 0 : weights ? weight(key_logit(static_cast<uint32_t>(entry[e] >> 32))) : 1;
-        }
-        uint64_t all;
-        uint64_t before = scan(own[0] + own[1], all) - own[0] - own[1];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (before < want && before + own[e] >= want)
-            for (int r = 0; r < ctas; ++r) st_cluster_u64(mapa_shared(smem_u32(&sh.found[0]), r), entry[e]);
-          before += own[e];
+        const uint32_t m = sh.listed;
+        for (uint32_t i = threadIdx.x; i < m; i += kThreads) {
+          uint64_t before = 0;
+          for (uint32_t j = 0; j < m; ++j) before += mine[j] > mine[i] ? sizes[j] : 0;
+          if (before < rest && rest <= before + sizes[i])
+            for (int r = 0; r < ctas; ++r) st_cluster_u64(mapa_shared(smem_u32(&sh.found[0]), r), mine[i]);
         }
       }
       cluster_sync();
@@ -479,11 +523,11 @@ __global__ void __launch_bounds__(kThreads, 2)
       const uint64_t one = weight(border);
       rest = (rest + one - 1) / one;
     }
-    uint64_t mine = 0;
-    each([&](float l, int) { mine += l == border; });
-    mine = warp_total(mine);
+    uint64_t equal = 0;
+    each([&](float l, int) { equal += l == border; });
+    equal = warp_total(equal);
     __syncthreads();
-    if (lane == 0) sh.sums[0][warp] = mine;
+    if (lane == 0) sh.sums[0][warp] = equal;
     __syncthreads();
     uint64_t sum = 0, before = 0;
     for (int w = 0; w < kWarps; ++w) {
@@ -492,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     const int set = share(sum);
     for (int r = 0; r < rank; ++r) before += sh.slots[set][r];
-    if (before < rest && rest <= before + mine) {
+    if (before < rest && rest <= before + equal) {
       for (int i0 = from; i0 < from + segment; i0 += 32) {
         const uint32_t which = __ballot_sync(0xFFFFFFFFu, logits[i0 + lane] == border);
         if (before + __popc(which) < rest) {
@@ -513,17 +557,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     each([&](float l, int) {
       if (l > -INFINITY) atomicAdd(&sh.bins[0][bin_of(l)], 1u);
     });
-    cluster_sync();
     uint64_t all;
     find_bin(scan_bins(false, all), static_cast<uint64_t>(top_k));
     // (the k-th in the last bin, or less than k in all: what is cut off weighs nothing)
     if (sh.piece < kBins - 1) cut(sh.piece, sh.found[1], false);
   }
   if (top_p < 1.0f) {
-    each([&](float l, int i) {
-      if (kept(l, i)) add_weight(bin_of(l), weight(l));
+    if (top_k < a.vocab) clear_bins();
+    each_weight([&](uint64_t w, float l) {
+      if (w != 0) add_weight(bin_of(l), w);
     });
-    cluster_sync();
     uint64_t all;
     const Two bins = scan_bins(true, all);
     uint64_t want = part_of(top_p, all);  // the least whole number that is not below top_p * all
@@ -549,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the kept weights in the order of the indexes: by warps' segments, then within the one that
   // has the place, by all the CTA's warps
   uint64_t mine = 0;
-  each([&](float l, int i) { mine += final_weight(l, i); });
+  each_weight([&](uint64_t w, float) { mine += w >= floor_weight ? w : 0; });
   mine = warp_total(mine);
   __syncthreads();
   if (lane == 0) sh.sums[0][warp] = mine;

@@ -670,7 +670,7 @@ int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64_t sequ
  * the indexes) add up to more than uniform times their sum, and probability its
  * w over that sum.  temperature <= 0 takes the largest logit, probability 1.
  * The w are computed to 2^-40 and summed as 64-bit integers of 2^-43: w below
- * 2^-44 count as 0.  Temperatures below 2^-100 count as that.
+ * 2^-44 count as 0.  Temperatures below 2^-100 or above 2^100 count as those.
  * Logits of -inf are never chosen; +inf ones share the row.  A row with nothing
  * above -inf, or with a NaN among its logits, temperature, top_p, min_p or
  * uniform, gets id -1, probability 0.
