@@ -2,25 +2,29 @@
 //
 //   s_t = scale * 2^(ek) q . kcode_t,   out = sum_t softmax(s)_t 2^(ev) vcode_t
 //
-// The cache's bytes bound it: each is read once for the up to 16 (query token, head) rows
-// that share a key head, as the 16-row side of FP16 products (16 x 8 x 16, binary32 sums).
+// The cache's bytes bound it: each is read once for the up to 32 (query token, head) rows
+// that share a key head.  Keys, and values transposed, are the 16-row side of FP16 products
+// (16 x 8 x 16, binary32 sums) and the rows its 8 columns, so that the conversion of codes,
+// which costs more than the products, is done once for all rows and few rows waste little.
 // E4M3 is exact in FP16; q enters under a power of two of its row.
 //
 // Every warp is a worker of its own: the blocks of 32 tokens of all (row tile, sequence,
 // key head) together are shared out evenly and in order over the workers, so that uneven
 // lengths and few sequences fill the GPU alike.  A worker streams its blocks through its own
 // ring of shared memory (cp.async, no barrier wider than the warp) and keeps queries, sums
-// and the softmax's running maximum in registers.  Weights of a block are taken relative to
-// the block's own maximum and its sum joins the running one with one binary32 factor, which
-// also carries the block's scale: no ratio between blocks' scales or weights is ever rounded
-// to FP16.  What a worker leaves unfinished goes to the workspace; a second, small launch
-// joins such parts in their order.
+// and the softmax's state in registers.  A row has two running maxima: of its logits, to
+// which its sum of weights is relative, and of logit + value scale (both as powers of two), to
+// which the FP16 weights are: a weight is rounded relative to the largest contribution to the
+// output, however far the blocks' scales lie apart.  What a worker leaves unfinished goes to
+// the workspace; its CTA joins the parts of its workers, and a second, small launch those of
+// the CTAs, in their order.
 //
-// Layouts: the order of channels in a product is free, so lane (g, c) = (lane / 4, lane % 4)
-// takes 16 consecutive bytes of key g as four k-steps, and the queries are laid out to match;
-// the order of columns is free as well, so a lane takes 16 consecutive channels of its two
-// tokens' values and owns 32 consecutive channels of the output.  16-byte pieces of a row are
-// exchanged by the row's number (exclusive or), which leaves every load free of conflicts.
+// Layouts: the order of channels in a product is free, so lane (g, t) = (lane / 4, lane % 4)
+// takes 16 consecutive bytes of keys g and g + 8 as four k-steps, and the queries are laid out
+// to match; the order of the output's channels is free as well, so a lane takes 16 consecutive
+// channels of its two tokens' values and owns 16 consecutive channels of two rows' output.
+// 16-byte pieces of a row are exchanged by the row's number (exclusive or), which leaves every
+// load free of conflicts.
 #include <cuda_fp16.h>
 
 #include "kv_cache.cuh"
@@ -28,35 +32,42 @@
 namespace mx {
 namespace {
 
-constexpr int kTile = 16;  // rows of a product
 constexpr int kMaxSms = 160;
+constexpr int kMaxWarps = 16;
 constexpr int kJoinThreads = 128;
+constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14: 2^-28 of it is still exact to 2^-11
 
-template <int DIM>
+// NT: columns of the products in eights, the rows of a tile.
+template <int DIM, int NT>
 struct Shape {
-  static constexpr int kWarps = DIM == 64 ? 16 : DIM == 128 ? 8 : 4;
-  static constexpr int kStages = DIM == 256 ? 2 : 3;
-  static constexpr int kRing = 2 * kCacheBlock * DIM * kStages;  // bytes of a warp: keys, values
-  static constexpr int kSteps = DIM / 16;                        // k-steps of q . k
-  static constexpr int kChunks = DIM / 64;                       // 16-byte pieces of a key a lane reads
-  static constexpr int kRun = DIM == 64 ? 8 : 16;                // channels of a value a lane reads at once
+  static constexpr int kRows = 8 * NT;
+  // registers: DIM / 8 * NT sums and, in registers or shared memory, half as many for queries
+  static constexpr int kWarps = DIM == 64 ? (NT == 4 ? 12 : 16) : DIM == 128 ? (NT == 4 ? 8 : 12) : (NT == 1 ? 6 : 4);
+  static constexpr int kStages = DIM == 64 ? (NT == 4 ? 4 : 3) : 2;
+  static constexpr int kBlockBytes = 2 * kCacheBlock * DIM;  // keys, values
+  static constexpr int kRing = kBlockBytes * kStages;
+  static constexpr int kSteps = DIM / 16;    // k-steps of q . k
+  static constexpr int kChunks = DIM / 64;   // 16-byte pieces of a key that a lane reads
+  static constexpr int kRun = DIM == 64 ? 8 : 16;  // channels of a value that a lane reads at once
   static constexpr int kRuns = DIM / 8 / kRun;
-  static constexpr bool kQueriesInShared = DIM == 256;           // (registers: the sums take 128)
-  static constexpr int kQueryBytes = kQueriesInShared ? kSteps * 512 : 0;
+  static constexpr bool kQueriesInShared = DIM * NT >= 512;
+  static constexpr int kQueryBytes = kQueriesInShared ? NT * kSteps * 256 : 0;
 };
 
-// What the two launches share: `first` holds the blocks before each sequence (one tile, one head).
+// What the launches share: `first` holds the blocks before each sequence (one tile, one head).
 struct Plan {
-  int64_t *first;  // [sequences + 1]
-  float *parts;    // two for each worker: sums [rows][DIM], maximum [rows], weight [rows]
+  int64_t *first;   // [sequences + 1]
+  float *parts;     // two for each worker, then two for each CTA (part_floats)
+  float *cta_parts;
   int tiles, rows, group;  // rows: of all tiles of a (sequence, key head)
   int part_rows;           // rows of a part
-  int workers;
+  int workers, per_cta;
+  int blocks_per_page;
 };
 
-// Numbers of a part: 16-byte stores need its length in fours.
+// Numbers of a part: sums [rows][dim], then each row's two maxima and its weight.
 __host__ __device__ constexpr int64_t part_floats(int64_t rows, int dim) {
-  return rows * dim + (2 * rows + 3) / 4 * 4;
+  return rows * dim + (3 * rows + 3) / 4 * 4;
 }
 
 // Shares of `total` blocks: worker p has [begin(p), begin(p + 1)).
@@ -70,17 +81,24 @@ struct Shares {
 };
 
 // The first token that any query of a sequence of this length sees.
-__device__ __forceinline__ int64_t first_seen(const AttentionArgs &a, int64_t length) {
+__device__ __forceinline__ int first_seen(const AttentionArgs &a, int length) {
   if (a.window == 0) return 0;
   const int64_t t = length - a.q_tokens - a.window + 1;
-  return t > 0 ? t : 0;
+  return t > 0 ? static_cast<int>(t) : 0;
 }
-__device__ __forceinline__ int64_t blocks_of(const AttentionArgs &a, int64_t length) {
-  return (length + kCacheBlock - 1) / kCacheBlock - first_seen(a, length) / kCacheBlock;
+__device__ __forceinline__ int blocks_of(const AttentionArgs &a, int length) {
+  return static_cast<int>((static_cast<int64_t>(length) + kCacheBlock - 1) / kCacheBlock) -
+         first_seen(a, length) / kCacheBlock;
+}
+__device__ __forceinline__ int length_of(const AttentionArgs &a, int b) {
+  return static_cast<int>(cache_length(a.c, b));  // (lengths are 32-bit numbers)
 }
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -117,11 +135,19 @@ __device__ __forceinline__ void half4_of(uint32_t codes, uint32_t &lo, uint32_t 
       : "r"(codes));
 }
 
-__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8 x 8 matrix of FP16, two of a row in a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -136,23 +162,32 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return h;
 }
 
-// Any NaN code among the four bytes?
-__device__ __forceinline__ bool any_nan(uint32_t codes) {
-  return (((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  uint32_t h;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(hi), "f"(lo));
+  return h;
 }
+
+// 0x80 in each byte that is a NaN code.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t codes) {
+  return ((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
+// 0 for -inf: a maximum that numbers are taken relative to.
+__device__ __forceinline__ float base_of_max(float v) { return v == -INFINITY ? 0.0f : v; }
 
 // Sequence, key head, tile and block of a place in the order of all blocks.
 struct Place {
   int b, h, tile;
-  int64_t block, blocks;  // of the sequence: from its first seen one
+  int block, blocks;  // of the sequence: from its first seen one
 };
 
 __device__ __forceinline__ Place place_of(int64_t f, const int64_t *first, const CacheArgs &c) {
   Place p;
   const int64_t per_tile = first[c.sequences] * c.heads;
   p.tile = static_cast<int>(f / per_tile);
-  f %= per_tile;
-  int lo = 0, hi = c.sequences;  // the last b with first[b] * heads <= f (and blocks of its own)
+  f -= p.tile * per_tile;
+  int lo = 0, hi = c.sequences;  // the last b with first[b] * heads <= f (it has blocks of its own)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (first[mid] * c.heads <= f)
@@ -161,36 +196,106 @@ __device__ __forceinline__ Place place_of(int64_t f, const int64_t *first, const
       hi = mid;
   }
   p.b = lo;
-  p.blocks = first[lo + 1] - first[lo];
+  p.blocks = static_cast<int>(first[lo + 1] - first[lo]);
   f -= first[lo] * c.heads;
   p.h = static_cast<int>(f / p.blocks);
-  p.block = f % p.blocks;
+  p.block = static_cast<int>(f - static_cast<int64_t>(p.h) * p.blocks);
   return p;
 }
 
-__device__ __forceinline__ void advance(Place &p, const int64_t *first, const CacheArgs &c) {
-  if (++p.block < p.blocks) return;
+// The next place; true if it is in another (tile, sequence, head).
+__device__ __forceinline__ bool advance(Place &p, const int64_t *first, const CacheArgs &c) {
+  if (++p.block < p.blocks) return false;
   p.block = 0;
-  if (++p.h < c.heads) return;
+  if (++p.h < c.heads) return true;
   p.h = 0;
   do {
     if (++p.b == c.sequences) p.b = 0, ++p.tile;
-    p.blocks = first[p.b + 1] - first[p.b];
+    p.blocks = static_cast<int>(first[p.b + 1] - first[p.b]);
   } while (p.blocks == 0);
+  return true;
 }
 
-// One row's queries: a power of two 2^-shift brings its largest to 2^14 .. 2^15.
+// The power of two that brings a row's largest (as binary32 bits) to 2^14 .. 2^15 is 2^-shift.
 __device__ __forceinline__ int query_shift(uint32_t largest) {
   const int e = static_cast<int>(largest >> 23);
   return e == 0 || e == 255 ? 0 : e - 127 - 14;
 }
 
-template <int DIM>
-__global__ void __launch_bounds__(Shape<DIM>::kWarps * 32, 1)
+// Writes four channels of a finished row, and its log-sum-exp with the first.
+__device__ __forceinline__ void finish(const AttentionArgs &a, const Plan &plan, int b, int h, int row, int d, int dim,
+                                       const float (&v)[4], float top, float ref, float weight) {
+  const int64_t o_row = static_cast<int64_t>(b) * a.q_tokens + row / plan.group;
+  const int64_t head = static_cast<int64_t>(h) * plan.group + row % plan.group;
+  // (two factors: together they may leave binary32's range where the result does not)
+  const float f1 = weight == 0.0f ? 0.0f : exp2f(-kLift) / weight, f2 = exp2f(base_of_max(ref) - base_of_max(top));
+  const int64_t to = o_row * a.ld_out + head * dim + d;
+  const int64_t extent = (static_cast<int64_t>(a.c.sequences) * a.q_tokens - 1) * a.ld_out +
+                         static_cast<int64_t>(a.q_heads) * dim;
+  if (in_bounds(to, 4, extent, a.c.status))
+    *reinterpret_cast<uint2 *>(a.out + to) =
+        make_uint2(bf16x2_bits(v[0] * f1 * f2, v[1] * f1 * f2), bf16x2_bits(v[2] * f1 * f2, v[3] * f1 * f2));
+  if (a.lse != nullptr && d == 0)
+    a.lse[o_row * a.q_heads + head] = weight == 0.0f ? -INFINITY : (top + log2f(weight)) * 0.6931471805599453f;
+}
+
+// The sum of the parts part(0) .. part(n - 1) of a row, four channels from d on.
+struct Joined {
+  float v[4], top, ref, weight;
+};
+template <typename Part>
+__device__ __forceinline__ Joined join(int n, const Part &part, int part_rows, int row, int d, int dim) {
+  Joined j{{0.0f, 0.0f, 0.0f, 0.0f}, -INFINITY, -INFINITY, 0.0f};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float *p = part(i), *state = p + static_cast<int64_t>(part_rows) * dim;
+    const float top = state[row], ref = state[part_rows + row], weight = state[2 * part_rows + row];
+    const float4 v = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(row) * dim + d);
+    const float now = fmaxf(j.top, top), now_ref = fmaxf(j.ref, ref);
+    const float b = base_of_max(now), b_ref = base_of_max(now_ref);
+    j.weight = j.weight * exp2_approx(j.top - b) + weight * exp2_approx(top - b);
+    const float keep = exp2_approx(j.ref - b_ref), add = exp2_approx(ref - b_ref);
+    j.v[0] = j.v[0] * keep + v.x * add;
+    j.v[1] = j.v[1] * keep + v.y * add;
+    j.v[2] = j.v[2] * keep + v.z * add;
+    j.v[3] = j.v[3] * keep + v.w * add;
+    j.top = now;
+    j.ref = now_ref;
+  }
+  return j;
+}
+
+__device__ __forceinline__ void put_part(float *part, int part_rows, int row, int d, int dim, const Joined &j) {
+  *reinterpret_cast<float4 *>(part + static_cast<int64_t>(row) * dim + d) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
+  if (d == 0) {
+    float *state = part + static_cast<int64_t>(part_rows) * dim;
+    state[row] = j.top;
+    state[part_rows + row] = j.ref;
+    state[2 * part_rows + row] = j.weight;
+  }
+}
+
+// A worker's parts: 0 goes on with a (tile, sequence, head) that another began, 1 begins one.
+struct PartInfo {
+  int valid, ends;  // ends: the (tile, sequence, head) does
+  int tile, b, h;
+};
+// Parts of one (tile, sequence, head) by neighbouring workers of a CTA.
+struct Chain {
+  int warp, count;      // the first worker, the number of workers
+  int begins, ends;
+  int tile, b, h;
+};
+
+template <int DIM, int NT>
+__global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     attention_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan) {
-  using S = Shape<DIM>;
+  using S = Shape<DIM, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t warp_sum[S::kWarps];
+  __shared__ PartInfo infos[S::kWarps][2];
+  __shared__ Chain chains[S::kWarps + 1];
+  __shared__ int n_chains;
   griddep_launch_dependents();
   griddep_wait();
   const CacheArgs &c = a.c;
@@ -202,7 +307,7 @@ __global__ void __launch_bounds__(Shape<DIM>::kWarps * 32, 1)
     int64_t before = 0;
     for (int b0 = 0; b0 < c.sequences; b0 += S::kWarps * 32) {
       const int b = b0 + threadIdx.x;
-      const int64_t n = b < c.sequences ? blocks_of(a, cache_length(c, b)) : 0;
+      const int64_t n = b < c.sequences ? blocks_of(a, length_of(a, b)) : 0;
       int64_t sum = n;
 #pragma unroll
       for (int m = 1; m < 32; m <<= 1) {
@@ -221,6 +326,7 @@ __global__ void __launch_bounds__(Shape<DIM>::kWarps * 32, 1)
       __syncthreads();
     }
     if (threadIdx.x == 0) first[c.sequences] = before;
+    if (threadIdx.x < 2 * S::kWarps) infos[threadIdx.x >> 1][threadIdx.x & 1].valid = 0;
     __syncthreads();
     if (blockIdx.x == 0)
       for (int b = threadIdx.x; b <= c.sequences; b += S::kWarps * 32) plan.first[b] = first[b];
@@ -229,491 +335,537 @@ __global__ void __launch_bounds__(Shape<DIM>::kWarps * 32, 1)
   const Shares shares(total, plan.workers);
   const int worker = blockIdx.x * S::kWarps + warp;
   const int64_t begin = shares.begin(worker), end = shares.begin(worker + 1);
-  if (begin >= end) return;
 
-  const uint32_t ring = smem_u32(smem) + warp * S::kRing;
-  [[maybe_unused]] const uint32_t query_at = smem_u32(smem) + S::kWarps * S::kRing + warp * S::kQueryBytes;
-  const int64_t code_extent = c.pages * c.heads * static_cast<int64_t>(c.page_tokens) * DIM;
-  const int64_t scale_extent = c.pages * c.heads * static_cast<int64_t>(c.page_tokens / kCacheBlock);
+  if (begin < end) {
+    const uint32_t ring = smem_u32(smem) + warp * S::kRing;
+    [[maybe_unused]] const uint32_t query_at = smem_u32(smem) + S::kWarps * S::kRing + warp * S::kQueryBytes;
+    const int64_t block_extent = c.pages * c.heads * static_cast<int64_t>(plan.blocks_per_page);
 
-  // ---- copies, kStages - 1 blocks ahead.  next_*: the block to be copied next.
-  Place next = place_of(begin, first, c);
-  int64_t next_at = begin;
-  int64_t next_length = cache_length(c, next.b), next_start = first_seen(a, next_length);
-  int64_t next_block = next_start / kCacheBlock + next.block;
-  int64_t next_page = cache_page(c, next.b, next_block * kCacheBlock);
-  int64_t base_of[S::kStages];  // first token's place in the pool of the blocks in the ring, -1: no page
+    // ---- copies, kStages - 1 blocks ahead.  next_*: the block to be copied next.
+    Place next = place_of(begin, first, c);
+    Place at = next;
+    int64_t left = end - begin;  // blocks still to be copied
+    int next_length = 0, next_start = 0, next_page_index = 0, next_in_page = 0, next_page = 0;
+    auto load_page = [&] {
+      const int64_t i = static_cast<int64_t>(next.b) * c.max_pages + next_page_index;
+      next_page = in_bounds(i, 1, c.sequences * c.max_pages, c.status) ? c.table[i] : -1;
+    };
+    auto locate = [&] {
+      next_length = length_of(a, next.b);
+      next_start = first_seen(a, next_length);
+      const int block = next_start / kCacheBlock + next.block;
+      next_page_index = block / plan.blocks_per_page;
+      next_in_page = block - next_page_index * plan.blocks_per_page;
+      load_page();
+    };
+    locate();
+    struct Ahead {
+      bool held;        // on a page of the pool
+      int key_scale, value_scale;
+    };
+    Ahead ahead[S::kStages];  // of the blocks in the ring
 #pragma unroll
-  for (int i = 0; i < S::kStages; ++i) base_of[i] = -1;
-  auto copy_next = [&](int stage, int64_t &base) {
-    if (next_at < end) {
-      const int64_t t0 = next_block * kCacheBlock;
-      base = next_page < 0 ? -1 : (next_page * c.heads + next.h) * c.page_tokens + t0 % c.page_tokens;
-      const int64_t from = base < 0 ? 0 : base * DIM;
-      const uint32_t dst = ring + stage * (2 * kCacheBlock * DIM);
+    for (int i = 0; i < S::kStages; ++i) ahead[i] = Ahead{false, 0, 0};
+    // a lane's pieces of a row pair, quad or so: their places repeat every eight rows
+    constexpr int kRowsAtOnce = 512 / DIM, kPieces = DIM / 16, kTurn = 8 / kRowsAtOnce > 0 ? 8 / kRowsAtOnce : 1;
+    uint32_t to[kTurn];
 #pragma unroll
-      for (int i = 0; i < kCacheBlock * DIM / 512; ++i) {
-        const int u = i * 32 + lane, row = u / (DIM / 16), chunk = u % (DIM / 16);
-        // rows that no query sees come as zeros: whatever lies there, NaN among it, stays out
-        const bool in = base >= 0 && t0 + row < next_length && t0 + row >= next_start &&
-                        in_bounds(from + u * 16, 16, code_extent, c.status);
-        cp_async16(dst + place<DIM>(row, chunk), c.codes[0] + from + u * 16, in);
-        cp_async16(dst + kCacheBlock * DIM + place<DIM>(row, chunk), c.codes[1] + from + u * 16, in);
-      }
-      if (++next_at < end) {
-        const int b = next.b;
-        advance(next, first, c);
-        if (next.b != b) {
-          next_length = cache_length(c, next.b);
-          next_start = first_seen(a, next_length);
-        }
-        next_block = next_start / kCacheBlock + next.block;
-        next_page = cache_page(c, next.b, next_block * kCacheBlock);
-      }
-    }
-    cp_async_commit();
-  };
+    for (int i = 0; i < kTurn; ++i)
+      to[i] = place<DIM>(i * kRowsAtOnce + lane / kPieces, lane % kPieces) - i * 512;
+    auto copy_next = [&](int stage, Ahead &x) {
+      if (left > 0) {
+        x.held = next_page >= 0 && next_page < c.pages;
+        if (!x.held && lane == 0) atomicOr(c.status, kStatusIndex);
+        const int64_t block = x.held ? (static_cast<int64_t>(next_page) * c.heads + next.h) * plan.blocks_per_page + next_in_page : 0;
+        const int t0 = (next_start / kCacheBlock + next.block) * kCacheBlock;
+        const uint8_t *const from_k = c.codes[0] + block * (kCacheBlock * DIM) + lane * 16;
+        const uint8_t *const from_v = c.codes[1] + block * (kCacheBlock * DIM) + lane * 16;
+        const uint32_t dst = ring + stage * S::kBlockBytes;
+        if (x.held && t0 >= next_start && t0 + kCacheBlock <= next_length && in_bounds(block, 1, block_extent, c.status)) {
 #pragma unroll
-  for (int i = 0; i < S::kStages - 1; ++i) copy_next(i, base_of[i]);
-
-  // ---- the blocks, one after the other
-  Place at = place_of(begin, first, c);
-  float out[DIM / 8][4];
-  float top[2], weight[2];       // running maximum (in powers of two) and sum, rows g and g + 8
-  float factor[2];               // of a logit: scale, log2(e) and the row's power of two
-  [[maybe_unused]] uint32_t query[S::kQueriesInShared ? 1 : S::kSteps][4];
-  int64_t length = 0, start = 0;
-  bool from_start = false, fresh = true;
-  int stage = 0;
-  for (int64_t f = begin; f < end; ++f) {
-    if (fresh) {  // a new (tile, sequence, head): its queries
-      fresh = false;
-      from_start = at.block == 0;
-      length = cache_length(c, at.b);
-      start = first_seen(a, length);
+          for (int i = 0; i < kCacheBlock * DIM / 512; ++i) {
+            cp_async16(dst + to[i % kTurn] + i * 512, from_k + i * 512);
+            cp_async16(dst + kCacheBlock * DIM + to[i % kTurn] + i * 512, from_v + i * 512);
+          }
+        } else {
+          // rows that no query sees come as zeros: whatever lies there, NaN among it, stays out
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        top[r] = -INFINITY;
-        weight[r] = 0.0f;
-        const int row = at.tile * kTile + g + 8 * r;
-        const int64_t q_row = static_cast<int64_t>(at.b) * a.q_tokens + row / plan.group;
-        const int64_t q_at = q_row * a.ld_q + (static_cast<int64_t>(at.h) * plan.group + row % plan.group) * DIM;
-        const int64_t extent = (static_cast<int64_t>(c.sequences) * a.q_tokens - 1) * a.ld_q +
-                               static_cast<int64_t>(a.q_heads) * DIM;
-        uint4 raw[S::kChunks][2];
-        uint32_t largest = 0;
-#pragma unroll
-        for (int i = 0; i < S::kChunks; ++i) {
-          const int chunk = DIM == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int64_t e = q_at + chunk * 16 + k * 8;
-            raw[i][k] = row < plan.rows && in_bounds(e, 8, extent, c.status)
-                            ? *reinterpret_cast<const uint4 *>(a.q + e)
-                            : make_uint4(0, 0, 0, 0);
-            const uint32_t w[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
-#pragma unroll
-            for (int u = 0; u < 4; ++u) largest = max(largest, max((w[u] & 0x7FFFu) << 16, w[u] & 0x7FFF0000u));
+          for (int i = 0; i < kCacheBlock * DIM / 512; ++i) {
+            const int token = t0 + i * kRowsAtOnce + lane / kPieces;
+            const bool in = x.held && token < next_length && token >= next_start && in_bounds(block, 1, block_extent, c.status);
+            cp_async16(dst + to[i % kTurn] + i * 512, from_k + i * 512, in);
+            cp_async16(dst + kCacheBlock * DIM + to[i % kTurn] + i * 512, from_v + i * 512, in);
           }
         }
-        largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, 1));
-        largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, 2));
-        const int shift = query_shift(largest);
-        const float f1 = exp2_int(-shift / 2), f2 = exp2_int(-shift - -shift / 2);
-        // (back in two steps, for the ends of binary32's range)
-        factor[r] = a.scale * 1.4426950408889634f * exp2_int(shift / 2) * exp2_int(shift - shift / 2);
+        if (in_bounds(block, 1, block_extent, c.status)) {
+          x.key_scale = c.scales[0][block];
+          x.value_scale = c.scales[1][block];
+        }
+        if (--left > 0) {
+          if (!advance(next, first, c)) {
+            if (++next_in_page == plan.blocks_per_page) {
+              next_in_page = 0;
+              ++next_page_index;
+              load_page();
+            }
+          } else {
+            locate();
+          }
+        }
+      }
+      cp_async_commit();
+    };
 #pragma unroll
-        for (int i = 0; i < S::kChunks; ++i)
+    for (int i = 0; i < S::kStages - 1; ++i) copy_next(i, ahead[i]);
+
+    // ---- the blocks, one after the other
+    float out[NT][DIM / 16][4];  // [..][..][2 e + r]: channels 2 i + e of the lane's, rows 2 t + r
+    float top[NT][2], ref[NT][2], weight[NT][2];
+    float factor[NT][2];         // of a logit: scale, log2(e) and the row's power of two
+    [[maybe_unused]] uint32_t query[S::kQueriesInShared ? 1 : NT][S::kQueriesInShared ? 1 : S::kSteps][2];
+    int length = 0, start = 0;
+    bool from_start = false, fresh = true;
+    int stage = 0;
+    for (int64_t f = begin; f < end; ++f) {
+      if (fresh) {  // a new (tile, sequence, head): its queries
+        fresh = false;
+        from_start = at.block == 0;
+        length = length_of(a, at.b);
+        start = first_seen(a, length);
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const uint4 &v = raw[i][u >> 1];
-            const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
-            const uint32_t h0 = half2_bits(__uint_as_float(w0 << 16) * f1 * f2, __uint_as_float(w0 & 0xFFFF0000u) * f1 * f2);
-            const uint32_t h1 = half2_bits(__uint_as_float(w1 << 16) * f1 * f2, __uint_as_float(w1 & 0xFFFF0000u) * f1 * f2);
+        for (int nt = 0; nt < NT; ++nt) {
+          const int row = at.tile * S::kRows + nt * 8 + g;
+          const int64_t q_row = static_cast<int64_t>(at.b) * a.q_tokens + row / plan.group;
+          const int64_t q_at = q_row * a.ld_q + (static_cast<int64_t>(at.h) * plan.group + row % plan.group) * DIM;
+          const int64_t extent = (static_cast<int64_t>(c.sequences) * a.q_tokens - 1) * a.ld_q +
+                                 static_cast<int64_t>(a.q_heads) * DIM;
+          uint4 raw[S::kChunks][2];
+          uint32_t largest = 0;
+#pragma unroll
+          for (int i = 0; i < S::kChunks; ++i) {
+            const int chunk = DIM == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const int64_t e = q_at + chunk * 16 + k * 8;
+              raw[i][k] = row < plan.rows && in_bounds(e, 8, extent, c.status)
+                              ? *reinterpret_cast<const uint4 *>(a.q + e)
+                              : make_uint4(0, 0, 0, 0);
+              const uint32_t w[4] = {raw[i][k].x, raw[i][k].y, raw[i][k].z, raw[i][k].w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) largest = max(largest, max((w[u] & 0x7FFFu) << 16, w[u] & 0x7FFF0000u));
+            }
+          }
+          largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, 1));
+          largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, 2));
+          const int shift = query_shift(largest);
+          const float f1 = exp2_int(-shift / 2), f2 = exp2_int(-shift - -shift / 2);
+          // (back in two steps, for the ends of binary32's range)
+          const float mine = a.scale * 1.4426950408889634f * exp2_int(shift / 2) * exp2_int(shift - shift / 2);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            factor[nt][r] = __shfl_sync(0xFFFFFFFFu, mine, (2 * t + r) * 4);
+            top[nt][r] = ref[nt][r] = -INFINITY;
+            weight[nt][r] = 0.0f;
+          }
+#pragma unroll
+          for (int i = 0; i < S::kChunks; ++i)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 &v = raw[i][u >> 1];
+              const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
+              const uint32_t h0 = half2_bits(__uint_as_float(w0 << 16) * f1 * f2, __uint_as_float(w0 & 0xFFFF0000u) * f1 * f2);
+              const uint32_t h1 = half2_bits(__uint_as_float(w1 << 16) * f1 * f2, __uint_as_float(w1 & 0xFFFF0000u) * f1 * f2);
+              if constexpr (S::kQueriesInShared) {
+                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(query_at + (nt * S::kSteps + i * 4 + u) * 256 + lane * 8),
+                             "r"(h0), "r"(h1)
+                             : "memory");
+              } else {
+                query[nt][i * 4 + u][0] = h0;
+                query[nt][i * 4 + u][1] = h1;
+              }
+            }
+#pragma unroll
+          for (int i = 0; i < DIM / 16; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) out[nt][i][k] = 0.0f;
+        }
+      }
+
+      cp_async_wait<S::kStages - 2>();
+      __syncwarp();  // the lanes' copies are there for all, and the stage before this one is read
+      const Ahead here = ahead[0];
+#pragma unroll
+      for (int i = 0; i + 1 < S::kStages; ++i) ahead[i] = ahead[i + 1];
+      copy_next(stage == 0 ? S::kStages - 1 : stage - 1, ahead[S::kStages - 2]);
+      const uint32_t keys = ring + stage * S::kBlockBytes, values = keys + kCacheBlock * DIM;
+
+      // logits: s[nt][j][2 e + r] of token 16 j + 8 e + g and row 2 t + r of eight
+      float s[NT][2][4] = {};
+#pragma unroll
+      for (int i = 0; i < S::kChunks; ++i) {
+        const int chunk = DIM == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
+        uint4 k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = lds128(keys + place<DIM>(8 * j + g, chunk));
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint32_t q[NT][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
             if constexpr (S::kQueriesInShared) {
-              const uint32_t to = query_at + (i * 4 + u) * 512 + lane * 16 + r * 4;
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to), "r"(h0) : "memory");
-              asm volatile("st.shared.u32 [%0], %1;" ::"r"(to + 8), "r"(h1) : "memory");
+              const uint2 v = lds64(query_at + (nt * S::kSteps + i * 4 + u) * 256 + lane * 8);
+              q[nt][0] = v.x, q[nt][1] = v.y;
             } else {
-              query[i * 4 + u][r] = h0;
-              query[i * 4 + u][2 + r] = h1;
+              q[nt][0] = query[nt][i * 4 + u][0], q[nt][1] = query[nt][i * 4 + u][1];
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint4 &k0 = k[2 * j], &k1 = k[2 * j + 1];
+            uint32_t a0, a1, a2, a3;
+            half4_of(u == 0 ? k0.x : u == 1 ? k0.y : u == 2 ? k0.z : k0.w, a0, a2);
+            half4_of(u == 0 ? k1.x : u == 1 ? k1.y : u == 2 ? k1.z : k1.w, a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt][j], a0, a1, a2, a3, q[nt][0], q[nt][1]);
+          }
+        }
+      }
+
+      const int t0 = (start / kCacheBlock + at.block) * kCacheBlock;
+      const int position = length - a.q_tokens;  // of the first query
+      // do all rows see all of the block?
+      const bool whole = here.held && t0 + kCacheBlock - 1 <= position &&
+                         (a.window == 0 || static_cast<int64_t>(t0) >= length - a.window);
+      const float key_scale = here.key_scale == 0 ? 0x1p-127f : __int_as_float(here.key_scale << 23);
+      const float value_exp = static_cast<float>(here.value_scale - 127);
+      float most[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float scaled = factor[nt][r];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][i >> 1][2 * (i & 1) + r] *= scaled * key_scale;
+        }
+      if (!whole) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int p = position + (at.tile * S::kRows + nt * 8 + 2 * t + r) / plan.group;
+            const int64_t low = a.window == 0 ? 0 : p - a.window + 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int token = t0 + 8 * i + g;
+              if (!(here.held && token <= p && token < length && token >= low))
+                s[nt][i >> 1][2 * (i & 1) + r] = -INFINITY;
             }
           }
       }
+      bool grows = false;
 #pragma unroll
-      for (int i = 0; i < DIM / 8; ++i)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) out[i][k] = 0.0f;
-    }
-
-    cp_async_wait<S::kStages - 2>();
-    __syncwarp();  // the lanes' copies are there for all, and the stage before this one is read
-    const int64_t base = base_of[0];
-#pragma unroll
-    for (int i = 0; i + 1 < S::kStages; ++i) base_of[i] = base_of[i + 1];
-    const int free_stage = stage == 0 ? S::kStages - 1 : stage - 1;
-    copy_next(free_stage, base_of[S::kStages - 2]);
-    const bool held = base >= 0 && in_bounds(base / kCacheBlock, 1, scale_extent, c.status);
-    const int key_exp = held ? c.scales[0][base / kCacheBlock] - 127 : 0;
-    const int value_exp = held ? c.scales[1][base / kCacheBlock] - 127 : 0;
-    const uint32_t keys = ring + stage * (2 * kCacheBlock * DIM), values = keys + kCacheBlock * DIM;
-
-    // logits: s[j][0, 1] of row g and tokens 8 j + 2 t, + 1; s[j][2, 3] of row g + 8
-    float s[4][4] = {};
-#pragma unroll
-    for (int i = 0; i < S::kChunks; ++i) {
-      const int chunk = DIM == 64 ? t : 8 * (i >> 1) + 2 * t + (i & 1);
-      uint4 k[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) k[j] = lds128(keys + place<DIM>(8 * j + g, chunk));
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        uint32_t q[4];
-        if constexpr (S::kQueriesInShared) {
-          const uint4 v = lds128(query_at + (i * 4 + u) * 512 + lane * 16);
-          q[0] = v.x, q[1] = v.y, q[2] = v.z, q[3] = v.w;
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) q[e] = query[i * 4 + u][e];
+        for (int r = 0; r < 2; ++r) {
+          float m = fmaxf(fmaxf(s[nt][0][r], s[nt][0][2 + r]), fmaxf(s[nt][1][r], s[nt][1][2 + r]));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 4));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
+          m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+          most[nt][r] = m;
+          grows |= m > top[nt][r] || m + value_exp > ref[nt][r];
         }
+      if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t b0, b1;
-          half4_of(u == 0 ? k[j].x : u == 1 ? k[j].y : u == 2 ? k[j].z : k[j].w, b0, b1);
-          mma_f16(s[j], q, b0, b1);
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float now = fmaxf(top[nt][r], most[nt][r]), now_ref = fmaxf(ref[nt][r], most[nt][r] + value_exp);
+            weight[nt][r] *= exp2_approx(top[nt][r] - base_of_max(now));
+            const float keep = exp2_approx(ref[nt][r] - base_of_max(now_ref));
+            top[nt][r] = now;
+            ref[nt][r] = now_ref;
+#pragma unroll
+            for (int i = 0; i < DIM / 16; ++i) {
+              out[nt][i][r] *= keep;
+              out[nt][i][2 + r] *= keep;
+            }
+          }
       }
-    }
-
-    const int64_t t0 = (start / kCacheBlock + at.block) * kCacheBlock;
-    const int64_t here = length - a.q_tokens;  // position of the first query
-    // do all rows see all of the block?
-    const bool whole = held && t0 + kCacheBlock - 1 <= here &&
-                       (a.window == 0 || t0 > here + a.q_tokens - 1 - a.window);
-    uint32_t seen[2] = {0xFFu, 0xFFu};  // bit 2 j + k: the lane's token 8 j + 2 t + k
-    if (!whole) {
+      // weights: in binary32 for their sum, in FP16 relative to the largest contribution
+      uint32_t p[NT][4];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = at.tile * kTile + g + 8 * r;
-        const int64_t p = here + row / plan.group;
-        seen[r] = 0;
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[2][4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int64_t token = t0 + 8 * (i >> 1) + 2 * t + (i & 1);
-          if (held && token <= p && token < length && (a.window == 0 || token > p - a.window)) seen[r] |= 1u << i;
-        }
-      }
-    }
-    // weights relative to the block's maximum, and the factors that join the block
-    const float key_scale = exp2_int(key_exp), value_scale = exp2_int(value_exp);
-    float keep[2], join[2];
-    uint32_t p[4][2];
+        for (int r = 0; r < 2; ++r) {
+          const float base = base_of_max(top[nt][r]), lift = value_exp + kLift - base_of_max(ref[nt][r]);
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float l[8], most = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        l[i] = s[i >> 1][2 * r + (i & 1)] * factor[r] * key_scale;
-        if (!whole && !(seen[r] >> i & 1)) l[i] = -INFINITY;
-        most = fmaxf(most, l[i]);
-      }
-      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 1));
-      most = fmaxf(most, __shfl_xor_sync(0xFFFFFFFFu, most, 2));
-      const float ref = most == -INFINITY ? 0.0f : most;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        l[i] = exp2_approx(l[i] - ref);
-        sum += l[i];
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) p[j][r] = half2_bits(l[2 * j], l[2 * j + 1]);
-      const float now = fmaxf(top[r], most), now_ref = now == -INFINITY ? 0.0f : now;
-      keep[r] = exp2_approx(top[r] - now_ref);
-      join[r] = exp2_approx(most - now_ref);
-      weight[r] = weight[r] * keep[r] + sum * join[r];
-      join[r] *= value_scale;
-      top[r] = now;
-    }
-
-#pragma unroll
-    for (int run = 0; run < S::kRuns; ++run) {
-      // the lane's tokens 16 j + 2 t, + 1 (b0) and + 8, + 9 (b1)
-      constexpr int kWords = S::kRun / 4;
-      uint32_t v[2][4][kWords];
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int row = 16 * j + 2 * t + (k & 1) + 8 * (k >> 1);
-          if constexpr (DIM == 64) {
-            const uint2 x = lds64(values + place<DIM>(row, g >> 1) + (g & 1) * 8);
-            v[j][k][0] = x.x, v[j][k][1] = x.y;
-          } else {
-            const uint4 x = lds128(values + place<DIM>(row, 8 * run + g));
-            v[j][k][0] = x.x, v[j][k][1] = x.y, v[j][k][2] = x.z, v[j][k][3] = x.w;
+          for (int i = 0; i < 4; ++i) {
+            const float l = s[nt][i >> 1][2 * (i & 1) + r];
+            weight[nt][r] += exp2_approx(l - base);
+            w[r][i] = exp2_approx(l + lift);
           }
         }
-      if (!whole) {
-        // A NaN is for the rows that see it only: they get it by themselves, the product a
-        // zero (0 * NaN would bring it to all).  With one query token no row differs.
-        bool nan = false;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[nt][i] = transpose8(half2_bits(w[0][i], w[1][i]));
+      }
+
+#pragma unroll
+      for (int run = 0; run < S::kRuns; ++run) {
+        // the lane's tokens 16 j + 2 t, + 1 and + 8, + 9
+        constexpr int kWords = S::kRun / 4;
+        uint32_t v[2][4][kWords];
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int w = 0; w < kWords; ++w) nan |= any_nan(v[j][k][w]);
-        if (__any_sync(0xFFFFFFFFu, nan)) {
-          // the lane's values belong to columns g; its sums to columns 2 t, 2 t + 1 of rows g, g + 8
-          for (int row = 0; row < kCacheBlock; ++row) {
-            const int64_t token = t0 + row;
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              for (int e = 0; e < S::kRun; ++e) {
-                const int col = (2 * t + k) * S::kRun + e;  // within the run
-                uint32_t code;
-                const uint32_t addr = values + place<DIM>(row, 8 * run + col / 16) + col % 16;
-                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(addr));
-                if ((code & 0x7Fu) != 0x7Fu) continue;
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                  const int64_t pos = here + (at.tile * kTile + g + 8 * r) / plan.group;
-                  if (held && token <= pos && token < length && (a.window == 0 || token > pos - a.window)) {
-#pragma unroll
-                    for (int x = 0; x < S::kRun; ++x)
-                      if (x == e) out[run * S::kRun + x][2 * r + k] = NAN;
-                  }
-                }
-              }
+          for (int k = 0; k < 4; ++k) {
+            const int row = 16 * j + 2 * t + (k & 1) + 8 * (k >> 1);
+            if constexpr (DIM == 64) {
+              const uint2 x = lds64(values + place<DIM>(row, g >> 1) + (g & 1) * 8);
+              v[j][k][0] = x.x, v[j][k][1] = x.y;
+            } else {
+              const uint4 x = lds128(values + place<DIM>(row, 8 * run + g));
+              v[j][k][0] = x.x, v[j][k][1] = x.y, v[j][k][2] = x.z, v[j][k][3] = x.w;
+            }
           }
+        if (!whole) {
+          // A NaN is for the rows that see it only: they get it by themselves, the product a
+          // zero (0 * NaN would bring it to all).
+          uint32_t nan = 0;
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int k = 0; k < 4; ++k)
 #pragma unroll
-              for (int w = 0; w < kWords; ++w) {
-                const uint32_t high = ((v[j][k][w] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                v[j][k][w] &= ~((high >> 7) * 0xFFu);
+              for (int w = 0; w < kWords; ++w) nan |= nan_codes(v[j][k][w]);
+          if (__any_sync(0xFFFFFFFFu, nan != 0)) {
+            for (int row = 0; row < kCacheBlock; ++row) {
+              const int token = t0 + row;
+#pragma unroll
+              for (int e = 0; e < S::kRun; ++e) {  // the lane's channels of the output
+                const int col = g * S::kRun + e;
+                uint32_t code;
+                const uint32_t addr = values + place<DIM>(row, 8 * run + col / 16) + col % 16;
+                asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(addr));
+                if ((code & 0x7Fu) != 0x7Fu) continue;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int r = 0; r < 2; ++r) {
+                    const int q = position + (at.tile * S::kRows + nt * 8 + 2 * t + r) / plan.group;
+                    const int64_t low = a.window == 0 ? 0 : q - a.window + 1;
+                    if (here.held && token <= q && token < length && token >= low)
+                      out[nt][(run * S::kRun + e) / 2][2 * (e & 1) + r] = NAN;
+                  }
               }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) v[j][k][w] &= ~((nan_codes(v[j][k][w]) >> 7) * 0xFFu);
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          // the same channel of two neighbouring tokens, for four channels
+          uint32_t b[4][2][2];  // [channel][j][tokens 2 t, + 1 / + 8, + 9]
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t lo = __byte_perm(v[j][2 * k][w], v[j][2 * k + 1][w], 0x5140);
+              const uint32_t hi = __byte_perm(v[j][2 * k][w], v[j][2 * k + 1][w], 0x7362);
+              half4_of(lo, b[0][j][k], b[1][j][k]);
+              half4_of(hi, b[2][j][k], b[3][j][k]);
+            }
+#pragma unroll
+          for (int e = 0; e < 4; e += 2)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16(out[nt][(run * S::kRun + 4 * w + e) / 2], b[e][j][0], b[e + 1][j][0], b[e][j][1], b[e + 1][j][1],
+                        p[nt][2 * j], p[nt][2 * j + 1]);
         }
       }
-#pragma unroll
-      for (int w = 0; w < kWords; ++w) {
-        // the same channel of two neighbouring tokens, for four channels
-        uint32_t b[4][2][2];  // [channel][j][b0, b1]
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t lo = __byte_perm(v[j][2 * k][w], v[j][2 * k + 1][w], 0x5140);
-            const uint32_t hi = __byte_perm(v[j][2 * k][w], v[j][2 * k + 1][w], 0x7362);
-            half4_of(lo, b[0][j][k], b[1][j][k]);
-            half4_of(hi, b[2][j][k], b[3][j][k]);
-          }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float part[4] = {};
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t pa[4] = {p[2 * j][0], p[2 * j][1], p[2 * j + 1][0], p[2 * j + 1][1]};
-            mma_f16(part, pa, b[e][j][0], b[e][j][1]);
-          }
-          float(&o)[4] = out[run * S::kRun + 4 * w + e];
-          o[0] = o[0] * keep[0] + part[0] * join[0];
-          o[1] = o[1] * keep[0] + part[1] * join[0];
-          o[2] = o[2] * keep[1] + part[2] * join[1];
-          o[3] = o[3] * keep[1] + part[3] * join[1];
-        }
-      }
-    }
-    stage = stage + 1 == S::kStages ? 0 : stage + 1;
+      stage = stage + 1 == S::kStages ? 0 : stage + 1;
 
-    // ---- the end of a (tile, sequence, head), or of the worker's share
-    const bool last = at.block + 1 == at.blocks;
-    if (last || f + 1 == end) {
-      fresh = true;
+      // ---- the end of a (tile, sequence, head), or of the worker's share
+      const bool last = at.block + 1 == at.blocks;
+      if (last || f + 1 == end) {
+        fresh = true;
+        const bool whole_row = from_start && last;
+        float *part = plan.parts + (static_cast<int64_t>(worker) * 2 + from_start) * part_floats(plan.part_rows, DIM);
+        if (!whole_row && lane == 0) infos[warp][from_start] = PartInfo{1, last, at.tile, at.b, at.h};
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        float l = weight[r];
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
-        l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
-        const int row = at.tile * kTile + g + 8 * r;
-        if (row >= plan.rows) continue;
-        if (from_start && last) {
-          const int64_t o_row = static_cast<int64_t>(at.b) * a.q_tokens + row / plan.group;
-          const int64_t head = static_cast<int64_t>(at.h) * plan.group + row % plan.group;
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          const int64_t extent = (static_cast<int64_t>(c.sequences) * a.q_tokens - 1) * a.ld_out +
-                                 static_cast<int64_t>(a.q_heads) * DIM;
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int run = 0; run < S::kRuns; ++run)
+          for (int r = 0; r < 2; ++r) {
+            Joined j;
+            j.weight = weight[nt][r];
+            j.weight += __shfl_xor_sync(0xFFFFFFFFu, j.weight, 4);
+            j.weight += __shfl_xor_sync(0xFFFFFFFFu, j.weight, 8);
+            j.weight += __shfl_xor_sync(0xFFFFFFFFu, j.weight, 16);
+            j.top = top[nt][r];
+            j.ref = ref[nt][r];
+            const int pr = nt * 8 + 2 * t + r, row = at.tile * S::kRows + pr;
+            if (row >= plan.rows) continue;
 #pragma unroll
-            for (int k = 0; k < 2; ++k)
+            for (int run = 0; run < S::kRuns; ++run)
 #pragma unroll
-              for (int e = 0; e < S::kRun; e += 8) {
-                uint32_t w[4];
+              for (int e = 0; e < S::kRun; e += 4) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u)
-                  asm("cvt.rn.bf16x2.f32 %0, %1, %2;"
-                      : "=r"(w[u])
-                      : "f"(out[run * S::kRun + e + 2 * u + 1][2 * r + k] * inv),
-                        "f"(out[run * S::kRun + e + 2 * u][2 * r + k] * inv));
-                const int64_t to = o_row * a.ld_out + head * DIM + run * 128 + (2 * t + k) * S::kRun + e;
-                if (in_bounds(to, 8, extent, c.status))
-                  *reinterpret_cast<uint4 *>(a.out + to) = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int k = 0; k < 4; ++k) j.v[k] = out[nt][(run * S::kRun + e + k) / 2][2 * (k & 1) + r];
+                const int d = run * 128 + g * S::kRun + e;
+                if (whole_row)
+                  finish(a, plan, at.b, at.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
+                else
+                  put_part(part, plan.part_rows, pr, d, DIM, j);
               }
-          if (a.lse != nullptr && t == 0)
-            a.lse[o_row * a.q_heads + head] = l == 0.0f ? -INFINITY : (top[r] + log2f(l)) * 0.6931471805599453f;
-        } else {
-          float *part = plan.parts + (static_cast<int64_t>(worker) * 2 + from_start) * part_floats(plan.part_rows, DIM);
-          const int pr = g + 8 * r;
-#pragma unroll
-          for (int run = 0; run < S::kRuns; ++run)
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-              for (int e = 0; e < S::kRun; e += 4)
-                *reinterpret_cast<float4 *>(part + pr * DIM + run * 128 + (2 * t + k) * S::kRun + e) =
-                    make_float4(out[run * S::kRun + e][2 * r + k], out[run * S::kRun + e + 1][2 * r + k],
-                                out[run * S::kRun + e + 2][2 * r + k], out[run * S::kRun + e + 3][2 * r + k]);
-          if (t == 0) {
-            part[plan.part_rows * DIM + pr] = top[r];
-            part[plan.part_rows * (DIM + 1) + pr] = l;
           }
-        }
       }
+      if (f + 1 < end) advance(at, first, c);
     }
-    if (f + 1 < end) advance(at, first, c);
+    cp_async_wait<0>();
   }
-  cp_async_wait<0>();
+
+  // ---- the workers' parts: chains of one (tile, sequence, head) by neighbouring workers
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int n = 0;
+    for (int w = 0; w < S::kWarps; ++w) {
+      const PartInfo &head = infos[w][0], &tail = infos[w][1];
+      if (head.valid) {
+        if (w == 0) chains[n++] = Chain{0, 0, 0, 0, head.tile, head.b, head.h};
+        ++chains[n - 1].count;
+        chains[n - 1].ends = head.ends;
+      }
+      if (tail.valid) chains[n++] = Chain{w, 1, 1, 0, tail.tile, tail.b, tail.h};
+    }
+    n_chains = n;
+  }
+  __syncthreads();
+  const int per_chain = plan.part_rows * (DIM / 4);
+  for (int i = threadIdx.x; i < n_chains * per_chain; i += S::kWarps * 32) {
+    const Chain &chain = chains[i / per_chain];
+    const int pr = i % per_chain / (DIM / 4), d = i % (DIM / 4) * 4, row = chain.tile * S::kRows + pr;
+    if (row >= plan.rows) continue;
+    const auto part = [&](int k) {
+      const int64_t w = static_cast<int64_t>(blockIdx.x) * S::kWarps + chain.warp + k;
+      return plan.parts + (w * 2 + (k == 0 && chain.begins)) * part_floats(plan.part_rows, DIM);
+    };
+    const Joined j = join(chain.count, part, plan.part_rows, pr, d, DIM);
+    if (chain.begins && chain.ends)
+      finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
+    else
+      put_part(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
+               plan.part_rows, pr, d, DIM, j);
+  }
 }
 
-// Joins the parts of one row of a (sequence, key head) that several workers share, in their
-// order; a row of a sequence without blocks gets 0.
+// Joins the parts of one row of a (sequence, key head) that several CTAs share, in their
+// order; a row of a sequence without blocks gets 0.  A warp takes every fourth part.
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads)
-    join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan) {
-  constexpr int kWarps = kJoinThreads / 32, kPer = DIM / 32;
-  __shared__ float sums[kWarps][DIM];
-  __shared__ float tops[kWarps], weights[kWarps];
+    join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan, int tile_rows) {
+  constexpr int kGroups = kJoinThreads / (DIM / 4);
+  __shared__ __align__(16) float parts[kGroups][DIM + 4];
   griddep_launch_dependents();
   griddep_wait();
   const CacheArgs &c = a.c;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = blockIdx.x % plan.rows, h = blockIdx.y, b = blockIdx.x / plan.rows;
-  const int tile = row / kTile, pr = row % kTile;
-  const int64_t o_row = static_cast<int64_t>(b) * a.q_tokens + row / plan.group;
-  const int64_t head = static_cast<int64_t>(h) * plan.group + row % plan.group;
+  const int tile = row / tile_rows, pr = row % tile_rows;
   const int64_t f0 = plan.first[b], blocks = plan.first[b + 1] - f0, per_tile = plan.first[c.sequences] * c.heads;
   int64_t p0 = 0, p1 = -1;
-  int64_t begin = 0;
   if (blocks > 0) {
     const Shares shares(per_tile * plan.tiles, plan.workers);
-    begin = tile * per_tile + f0 * c.heads + h * blocks;
-    p0 = shares.owner(begin);
-    p1 = shares.owner(begin + blocks - 1);
-    if (p0 == p1) return;  // the worker has finished it
+    const int64_t begin = tile * per_tile + f0 * c.heads + h * blocks;
+    p0 = shares.owner(begin) / plan.per_cta;
+    p1 = shares.owner(begin + blocks - 1) / plan.per_cta;
+    if (p0 == p1) return;  // the CTA has finished it
   }
-  float sum[kPer] = {}, top = -INFINITY, weight = 0.0f;
-  for (int64_t p = p0 + warp; p <= p1; p += kWarps) {
-    // (the first worker's part begins the row, the others' go on with it)
-    const float *part = plan.parts + (p * 2 + (p == p0)) * part_floats(plan.part_rows, DIM);
-    const float m = part[plan.part_rows * DIM + pr], l = part[plan.part_rows * (DIM + 1) + pr];
-    float v[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) v[i] = part[pr * DIM + i * 32 + lane];
-    const float now = fmaxf(top, m), ref = now == -INFINITY ? 0.0f : now;
-    const float keep = exp2f(top - ref), join = exp2f(m - ref);
-    weight = weight * keep + l * join;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sum[i] = sum[i] * keep + v[i] * join;
-    top = now;
-  }
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) sums[warp][i * 32 + lane] = sum[i];
-  if (lane == 0) tops[warp] = top, weights[warp] = weight;
+  const int group = threadIdx.x / (DIM / 4), d = threadIdx.x % (DIM / 4) * 4;
+  const int n = static_cast<int>(p1 - p0 + 1), mine = n > group ? (n - group + kGroups - 1) / kGroups : 0;
+  // (the first CTA's part begins the row, the others' go on with it)
+  const auto part = [&](int k) {
+    const int64_t p = p0 + group + static_cast<int64_t>(k) * kGroups;
+    return plan.cta_parts + (p * 2 + (p == p0)) * part_floats(plan.part_rows, DIM);
+  };
+  Joined j = join(mine, part, plan.part_rows, pr, d, DIM);
+  put_part(parts[group], 1, 0, d, DIM, j);
   __syncthreads();
-  float most = tops[0];
-#pragma unroll
-  for (int w = 1; w < kWarps; ++w) most = fmaxf(most, tops[w]);
-  const float ref = most == -INFINITY ? 0.0f : most;
-  float total = 0.0f, f[kWarps];
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    f[w] = exp2f(tops[w] - ref);
-    total += weights[w] * f[w];
-  }
-  const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-  const int64_t extent = (static_cast<int64_t>(c.sequences) * a.q_tokens - 1) * a.ld_out +
-                         static_cast<int64_t>(a.q_heads) * DIM;
-  for (int d = threadIdx.x * 2; d < DIM; d += kJoinThreads * 2) {
-    float lo = 0.0f, hi = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) lo += sums[w][d] * f[w], hi += sums[w][d + 1] * f[w];
-    uint32_t bits;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(bits) : "f"(hi * inv), "f"(lo * inv));
-    const int64_t to = o_row * a.ld_out + head * DIM + d;
-    if (in_bounds(to, 2, extent, c.status)) *reinterpret_cast<uint32_t *>(a.out + to) = bits;
-  }
-  if (a.lse != nullptr && threadIdx.x == 0)
-    a.lse[o_row * a.q_heads + head] = total == 0.0f ? -INFINITY : (most + log2f(total)) * 0.6931471805599453f;
+  if (group != 0) return;
+  j = join(kGroups, [&](int k) { return parts[k]; }, 1, 0, d, DIM);
+  finish(a, plan, b, h, row, d, DIM, j.v, j.top, j.ref, j.weight);
 }
 
 constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int DIM>
-size_t parts_bytes(int64_t rows) {
-  const int64_t part_rows = rows < kTile ? rows : kTile;
-  return static_cast<size_t>(kMaxSms) * Shape<DIM>::kWarps * 2 * static_cast<size_t>(part_floats(part_rows, DIM)) * sizeof(float);
+// The rows of a tile: registers allow 32, or 16 of 256 channels.
+int tile_rows_of(int64_t rows, int dim) { return rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32; }
+int64_t part_rows_of(int64_t rows, int dim) {
+  const int64_t most = tile_rows_of(rows, dim);
+  return rows < most ? rows : most;
 }
 
-template <int DIM>
+template <int DIM, int NT>
 cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
-  using S = Shape<DIM>;
+  using S = Shape<DIM, NT>;
+  static_assert(S::kWarps <= kMaxWarps, "workspace");
   Plan plan;
   plan.group = a.q_heads / a.c.heads;
   plan.rows = plan.group * a.q_tokens;
-  plan.tiles = (plan.rows + kTile - 1) / kTile;
-  plan.part_rows = plan.rows < kTile ? plan.rows : kTile;
-  plan.first = static_cast<int64_t *>(a.workspace);
-  plan.parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) +
-                                         round256((static_cast<size_t>(a.c.sequences) + 1) * sizeof(int64_t)));
+  plan.tiles = (plan.rows + S::kRows - 1) / S::kRows;
+  plan.part_rows = static_cast<int>(part_rows_of(plan.rows, DIM));
+  plan.blocks_per_page = a.c.page_tokens / kCacheBlock;
   const int ctas = a.num_sms < kMaxSms ? a.num_sms : kMaxSms;
+  plan.per_cta = S::kWarps;
   plan.workers = ctas * S::kWarps;
-  const size_t smem = static_cast<size_t>(S::kWarps) * (S::kRing + S::kQueryBytes) +
-                      (static_cast<size_t>(a.c.sequences) + 1) * sizeof(int64_t);
-  const void *func = reinterpret_cast<const void *>(attention_kernel<DIM>);
+  plan.first = static_cast<int64_t *>(a.workspace);
+  plan.cta_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) +
+                                             round256((static_cast<size_t>(a.c.sequences) + 1) * sizeof(int64_t)));
+  plan.parts = plan.cta_parts + 2 * ctas * part_floats(plan.part_rows, DIM);
+  constexpr size_t kFixed = static_cast<size_t>(S::kWarps) * (S::kRing + S::kQueryBytes);
+  const size_t smem = kFixed + (static_cast<size_t>(a.c.sequences) + 1) * sizeof(int64_t);
+  const void *func = reinterpret_cast<const void *>(attention_kernel<DIM, NT>);
   if (!kernel_setup_get(func, nullptr)) {
-    const size_t most = static_cast<size_t>(S::kWarps) * (S::kRing + S::kQueryBytes) +
-                        (kAttentionMaxSequences + 1) * sizeof(int64_t);
-    const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+    constexpr size_t kMost = kFixed + (kAttentionMaxSequences + 1) * sizeof(int64_t);
+    static_assert(kMost + 2048 <= 227 * 1024, "shared memory");
+    const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
     if (e != cudaSuccess) return e;
     kernel_setup_put(func, 0);
   }
-  const cudaError_t e = launch_pdl(attention_kernel<DIM>, dim3(static_cast<unsigned>(ctas)), dim3(S::kWarps * 32),
+  const cudaError_t e = launch_pdl(attention_kernel<DIM, NT>, dim3(static_cast<unsigned>(ctas)), dim3(S::kWarps * 32),
                                    smem, s, a, plan);
   if (e != cudaSuccess) return e;
   return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(a.c.sequences) * plan.rows, a.c.heads),
-                    dim3(kJoinThreads), 0, s, a, plan);
+                    dim3(kJoinThreads), 0, s, a, plan, S::kRows);
+}
+
+template <int DIM>
+cudaError_t launch_rows(const AttentionArgs &a, cudaStream_t s) {
+  const int rows = tile_rows_of(static_cast<int64_t>(a.q_heads / a.c.heads) * a.q_tokens, DIM);
+  if (rows == 8) return launch<DIM, 1>(a, s);
+  if constexpr (DIM < 256)
+    if (rows == 32) return launch<DIM, 4>(a, s);
+  return launch<DIM, 2>(a, s);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t sequences, int64_t rows, int head_dim) {
-  const size_t first = round256((static_cast<size_t>(sequences) + 1) * sizeof(int64_t));
-  switch (head_dim) {
-    case 64: return first + parts_bytes<64>(rows);
-    case 128: return first + parts_bytes<128>(rows);
-    default: return first + parts_bytes<256>(rows);
-  }
+  const int64_t parts = 2 * kMaxSms * (1 + kMaxWarps);
+  return round256((static_cast<size_t>(sequences) + 1) * sizeof(int64_t)) +
+         static_cast<size_t>(parts * part_floats(part_rows_of(rows, head_dim), head_dim)) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t s) {
   switch (a.c.head_dim) {
-    case 64: return launch<64>(a, s);
-    case 128: return launch<128>(a, s);
-    default: return launch<256>(a, s);
+    case 64: return launch_rows<64>(a, s);
+    case 128: return launch_rows<128>(a, s);
+    default: return launch_rows<256>(a, s);
   }
 }
 

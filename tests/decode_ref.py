@@ -162,8 +162,10 @@ def attention(cache, q, lengths, q_tokens, q_heads, scale, window):
 
     Bound of out before its own rounding: a logit is off by at most dl = (dim + 8) 2^-24 scale
     sum |q||k| (binary32 sums) + 2^-21 (|logit| + 1) (its scaling and the exponential), a weight
-    by 2 dl (its own and its sum's) + 2^-11 (FP16) + 2^-18 (sums over tokens), and by 2^-25 of the
-    block's largest weight (FP16 below 2^-14); of lse dl + 2^-18."""
+    by 2 dl (its own and its sum's) + 2^-11 (FP16) + 2^-18 + tokens 2^-27 (sums over 16 tokens at a
+    time, 2^-23 each).  FP16 weights are lifted so that the row's largest weight * value scale
+    comes to at least 2^13: those below 2^-14 are off by up to 2^-25, 2^-38 of that largest, times the
+    value's code; of lse dl + 2^-18."""
     group = q_heads // cache.heads
     rows = q.shape[0]
     out, lse = np.zeros((rows, q_heads, cache.dim)), np.full((rows, q_heads), -np.inf)
@@ -175,6 +177,11 @@ def attention(cache, q, lengths, q_tokens, q_heads, scale, window):
         k, ok = cache.values(0, b, length)
         v, _ = cache.values(1, b, length)
         t = np.arange(length)
+        unit = np.zeros((length, cache.heads))  # scale of each value
+        for x in range(length):
+            page, off = cache.table[b, x // cache.page_tokens], x % cache.page_tokens
+            if ok[x]:
+                unit[x] = 2.0 ** (cache.scales[1][page, :, off // BLOCK].astype(np.float64) - 127)
         for i in range(q_tokens):
             p = length - q_tokens + i
             see = ok & (t <= p)
@@ -194,12 +201,10 @@ def attention(cache, q, lengths, q_tokens, q_heads, scale, window):
                 lse[r, h] = top + np.log(total)
                 dl = ((cache.dim + 8) * 2.0 ** -24 * abs(scale) * (np.abs(kk) @ np.abs(x)) +
                       2.0 ** -21 * (np.abs(l) + 1)).max()
-                small = np.zeros(cache.dim)
-                blocks = t[see] // BLOCK
-                for blk in np.unique(blocks):
-                    m = blocks == blk
-                    small += w[m].max() * np.abs(vv[m]).sum(0)
-                e_out[r, h] = (2 * dl + 2.0 ** -11 + 2.0 ** -18) * (w @ np.abs(vv)) / total + 2.0 ** -25 * small / total
+                u = unit[see, h // group]
+                small = 2.0 ** -38 * (w * u).max() * (np.abs(vv) / u[:, None]).sum(0)
+                rel = 2 * dl + 2.0 ** -11 + 2.0 ** -18 + len(w) * 2.0 ** -27
+                e_out[r, h] = (rel * (w @ np.abs(vv)) + small) / total
                 e_lse[r, h] = dl + 2.0 ** -18
     return out, lse, e_out, e_lse
 
