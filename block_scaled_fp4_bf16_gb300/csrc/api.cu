@@ -1675,8 +1675,7 @@ MX_API size_t mx_attention_workspace_bytes(int64_t sequences, int64_t q_tokens, 
                                            const mx_kv_cache *cache) {
   const KeepDetail keep;
   if (attention_shape_check("mx_attention_workspace_bytes", sequences, q_tokens, q_heads, cache) != MX_OK) return 0;
-  return mx::attention_workspace_bytes(sequences, q_heads / cache->kv_heads * q_tokens,
-                                       static_cast<int>(cache->head_dim));
+  return mx::attention_workspace_bytes(q_heads / cache->kv_heads * q_tokens, static_cast<int>(cache->head_dim));
 }
 
 MX_API int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64_t sequences,

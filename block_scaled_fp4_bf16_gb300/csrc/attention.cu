@@ -34,7 +34,8 @@ namespace {
 
 constexpr int kMaxSms = 160;
 constexpr int kMaxWarps = 16;
-constexpr int kJoinThreads = 128;
+constexpr int64_t kMostBlocks = int64_t(1) << 31;  // of all sequences
+constexpr int kJoinThreads = 256;
 constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14: 2^-28 of it is still exact to 2^-11
 
 // NT: columns of the products in eights, the rows of a tile.
@@ -42,8 +43,8 @@ template <int DIM, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   // registers: DIM / 8 * NT sums and, in registers or shared memory, half as many for queries
-  static constexpr int kWarps = DIM == 64 ? (NT == 4 ? 12 : 16) : DIM == 128 ? (NT == 4 ? 8 : 12) : (NT == 1 ? 6 : 4);
-  static constexpr int kStages = DIM == 64 ? (NT == 4 ? 4 : 3) : 2;
+  static constexpr int kWarps = DIM == 64 ? (NT == 1 ? 16 : NT == 2 ? 12 : 8) : DIM == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 6 : 4);
+  static constexpr int kStages = DIM == 64 ? (NT == 1 ? 3 : 4) : DIM == 128 && NT == 2 ? 3 : 2;
   static constexpr int kBlockBytes = 2 * kCacheBlock * DIM;  // keys, values
   static constexpr int kRing = kBlockBytes * kStages;
   static constexpr int kSteps = DIM / 16;    // k-steps of q . k
@@ -54,10 +55,15 @@ struct Shape {
   static constexpr int kQueryBytes = kQueriesInShared ? NT * kSteps * 256 : 0;
 };
 
-// What the launches share: `first` holds the blocks before each sequence (one tile, one head).
+// A (tile, sequence, head) that a CTA begins and others go on with: the last of them (-1: none).
+struct Split {
+  int last_cta, tile, b, h;
+};
+
+// What the two launches share.
 struct Plan {
-  int64_t *first;   // [sequences + 1]
-  float *parts;     // two for each worker, then two for each CTA (part_floats)
+  Split *splits;         // of each CTA
+  float *parts;          // two for each worker and two for each CTA (part_floats)
   float *cta_parts;
   int tiles, rows, group;  // rows: of all tiles of a (sequence, key head)
   int part_rows;           // rows of a part
@@ -182,29 +188,29 @@ struct Place {
   int block, blocks;  // of the sequence: from its first seen one
 };
 
-__device__ __forceinline__ Place place_of(int64_t f, const int64_t *first, const CacheArgs &c) {
+__device__ __forceinline__ Place place_of(int64_t f, const uint32_t *first, const CacheArgs &c) {
   Place p;
-  const int64_t per_tile = first[c.sequences] * c.heads;
+  const int64_t per_tile = static_cast<int64_t>(first[c.sequences]) * c.heads;
   p.tile = static_cast<int>(f / per_tile);
   f -= p.tile * per_tile;
   int lo = 0, hi = c.sequences;  // the last b with first[b] * heads <= f (it has blocks of its own)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (first[mid] * c.heads <= f)
+    if (static_cast<int64_t>(first[mid]) * c.heads <= f)
       lo = mid;
     else
       hi = mid;
   }
   p.b = lo;
   p.blocks = static_cast<int>(first[lo + 1] - first[lo]);
-  f -= first[lo] * c.heads;
+  f -= static_cast<int64_t>(first[lo]) * c.heads;
   p.h = static_cast<int>(f / p.blocks);
   p.block = static_cast<int>(f - static_cast<int64_t>(p.h) * p.blocks);
   return p;
 }
 
 // The next place; true if it is in another (tile, sequence, head).
-__device__ __forceinline__ bool advance(Place &p, const int64_t *first, const CacheArgs &c) {
+__device__ __forceinline__ bool advance(Place &p, const uint32_t *first, const CacheArgs &c) {
   if (++p.block < p.blocks) return false;
   p.block = 0;
   if (++p.h < c.heads) return true;
@@ -239,18 +245,27 @@ __device__ __forceinline__ void finish(const AttentionArgs &a, const Plan &plan,
     a.lse[o_row * a.q_heads + head] = weight == 0.0f ? -INFINITY : (top + log2f(weight)) * 0.6931471805599453f;
 }
 
+// A part: sums [rows][dim]; each row's two maxima and its weight, `rows` apart.
+struct Part {
+  float *sums, *state;
+  int rows;
+};
+__device__ __forceinline__ Part part_at(float *p, int rows, int dim) {
+  return Part{p, p + static_cast<int64_t>(rows) * dim, rows};
+}
+
 // The sum of the parts part(0) .. part(n - 1) of a row, four channels from d on.
 struct Joined {
   float v[4], top, ref, weight;
 };
-template <typename Part>
-__device__ __forceinline__ Joined join(int n, const Part &part, int part_rows, int row, int d, int dim) {
+template <typename PartOf>
+__device__ __forceinline__ Joined join(int n, const PartOf &part, int row, int d, int dim) {
   Joined j{{0.0f, 0.0f, 0.0f, 0.0f}, -INFINITY, -INFINITY, 0.0f};
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
-    const float *p = part(i), *state = p + static_cast<int64_t>(part_rows) * dim;
-    const float top = state[row], ref = state[part_rows + row], weight = state[2 * part_rows + row];
-    const float4 v = *reinterpret_cast<const float4 *>(p + static_cast<int64_t>(row) * dim + d);
+    const Part p = part(i);
+    const float top = p.state[row], ref = p.state[p.rows + row], weight = p.state[2 * p.rows + row];
+    const float4 v = *reinterpret_cast<const float4 *>(p.sums + row * dim + d);
     const float now = fmaxf(j.top, top), now_ref = fmaxf(j.ref, ref);
     const float b = base_of_max(now), b_ref = base_of_max(now_ref);
     j.weight = j.weight * exp2_approx(j.top - b) + weight * exp2_approx(top - b);
@@ -265,26 +280,26 @@ __device__ __forceinline__ Joined join(int n, const Part &part, int part_rows, i
   return j;
 }
 
-__device__ __forceinline__ void put_part(float *part, int part_rows, int row, int d, int dim, const Joined &j) {
-  *reinterpret_cast<float4 *>(part + static_cast<int64_t>(row) * dim + d) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
+__device__ __forceinline__ void put_part(const Part &p, int row, int d, int dim, const Joined &j) {
+  *reinterpret_cast<float4 *>(p.sums + row * dim + d) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
   if (d == 0) {
-    float *state = part + static_cast<int64_t>(part_rows) * dim;
-    state[row] = j.top;
-    state[part_rows + row] = j.ref;
-    state[2 * part_rows + row] = j.weight;
+    p.state[row] = j.top;
+    p.state[p.rows + row] = j.ref;
+    p.state[2 * p.rows + row] = j.weight;
   }
 }
 
 // A worker's parts: 0 goes on with a (tile, sequence, head) that another began, 1 begins one.
 struct PartInfo {
   int valid, ends;  // ends: the (tile, sequence, head) does
-  int tile, b, h;
+  int here;         // in the worker's shared memory (the last one of its share)
+  int tile, b, h, blocks;
 };
 // Parts of one (tile, sequence, head) by neighbouring workers of a CTA.
 struct Chain {
   int warp, count;      // the first worker, the number of workers
   int begins, ends;
-  int tile, b, h;
+  int tile, b, h, blocks;
 };
 
 template <int DIM, int NT>
@@ -296,11 +311,12 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
   __shared__ PartInfo infos[S::kWarps][2];
   __shared__ Chain chains[S::kWarps + 1];
   __shared__ int n_chains;
+  __shared__ float states[S::kWarps][3 * S::kRows];
   griddep_launch_dependents();
   griddep_wait();
   const CacheArgs &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  int64_t *const first = reinterpret_cast<int64_t *>(smem + S::kWarps * (S::kRing + S::kQueryBytes));
+  uint32_t *const first = reinterpret_cast<uint32_t *>(smem + S::kWarps * (S::kRing + S::kQueryBytes));
 
   // blocks before each sequence
   {
@@ -321,17 +337,28 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
         if (w < warp) sum += warp_sum[w];
         all += warp_sum[w];
       }
-      if (b < c.sequences) first[b] = before + sum - n;
+      if (b < c.sequences) first[b] = static_cast<uint32_t>(before + sum - n);
       before += all;
       __syncthreads();
     }
-    if (threadIdx.x == 0) first[c.sequences] = before;
+    if (threadIdx.x == 0) first[c.sequences] = static_cast<uint32_t>(before);
+    if (before > kMostBlocks) {  // (uniform) nothing is seen
+      if (threadIdx.x == 0) atomicOr(c.status, kStatusIndex);
+      for (int b = threadIdx.x; b <= c.sequences; b += S::kWarps * 32) first[b] = 0;
+    }
     if (threadIdx.x < 2 * S::kWarps) infos[threadIdx.x >> 1][threadIdx.x & 1].valid = 0;
     __syncthreads();
-    if (blockIdx.x == 0)
-      for (int b = threadIdx.x; b <= c.sequences; b += S::kWarps * 32) plan.first[b] = first[b];
   }
-  const int64_t total = first[c.sequences] * c.heads * plan.tiles;
+  // sequences without blocks: rows of 0
+  for (int b = blockIdx.x; b < c.sequences; b += gridDim.x) {
+    if (first[b] != first[b + 1]) continue;
+    for (int i = threadIdx.x; i < c.heads * plan.rows * (DIM / 4); i += S::kWarps * 32) {
+      const float zero[4] = {};
+      const int row = i / (DIM / 4) % plan.rows, h = i / (DIM / 4) / plan.rows;
+      finish(a, plan, b, h, row, i % (DIM / 4) * 4, DIM, zero, -INFINITY, -INFINITY, 0.0f);
+    }
+  }
+  const int64_t total = static_cast<int64_t>(first[c.sequences]) * c.heads * plan.tiles;
   const Shares shares(total, plan.workers);
   const int worker = blockIdx.x * S::kWarps + warp;
   const int64_t begin = shares.begin(worker), end = shares.begin(worker + 1);
@@ -697,8 +724,17 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
       if (last || f + 1 == end) {
         fresh = true;
         const bool whole_row = from_start && last;
-        float *part = plan.parts + (static_cast<int64_t>(worker) * 2 + from_start) * part_floats(plan.part_rows, DIM);
-        if (!whole_row && lane == 0) infos[warp][from_start] = PartInfo{1, last, at.tile, at.b, at.h};
+        // (the last part of a share takes the place of the ring, an earlier one goes to memory)
+        const bool in_ring = f + 1 == end;
+        Part part = part_at(plan.parts + (static_cast<int64_t>(worker) * 2 + from_start) * part_floats(plan.part_rows, DIM),
+                            plan.part_rows, DIM);
+        if (in_ring) {
+          part = Part{reinterpret_cast<float *>(smem + warp * S::kRing), states[warp], S::kRows};
+          cp_async_wait<0>();
+          __syncwarp();
+        }
+        if (!whole_row && lane == 0)
+          infos[warp][from_start] = PartInfo{1, last, in_ring, at.tile, at.b, at.h, at.blocks};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -722,29 +758,39 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
                 if (whole_row)
                   finish(a, plan, at.b, at.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
                 else
-                  put_part(part, plan.part_rows, pr, d, DIM, j);
+                  put_part(part, pr, d, DIM, j);
               }
           }
       }
       if (f + 1 < end) advance(at, first, c);
     }
-    cp_async_wait<0>();
   }
 
   // ---- the workers' parts: chains of one (tile, sequence, head) by neighbouring workers
   __syncthreads();
-  if (threadIdx.x == 0) {
-    int n = 0;
-    for (int w = 0; w < S::kWarps; ++w) {
-      const PartInfo &head = infos[w][0], &tail = infos[w][1];
-      if (head.valid) {
-        if (w == 0) chains[n++] = Chain{0, 0, 0, 0, head.tile, head.b, head.h};
-        ++chains[n - 1].count;
-        chains[n - 1].ends = head.ends;
-      }
-      if (tail.valid) chains[n++] = Chain{w, 1, 1, 0, tail.tile, tail.b, tail.h};
+  static_assert(S::kRing >= S::kRows * DIM * 4, "a part in the ring's place");
+  if (warp == 0) {
+    // lane w: the chain that worker w begins; a chain that goes on from the CTA before is w = 0's too
+    const bool in = lane < S::kWarps;
+    const PartInfo head = in ? infos[lane][0] : PartInfo{}, tail = in ? infos[lane][1] : PartInfo{};
+    const uint32_t heads = __ballot_sync(0xFFFFFFFFu, in && head.valid), tails = __ballot_sync(0xFFFFFFFFu, in && tail.valid);
+    const int goes_on = heads & 1u;
+    // workers after w that go on with its chain: up to the first that begins one itself
+    const auto after = [&](int w) {
+      const int run = __ffs(static_cast<int>(~(heads >> (w + 1)))) - 1, tail_at = __ffs(static_cast<int>(tails >> (w + 1)));
+      return tail_at > 0 && tail_at < run ? tail_at : run;
+    };
+    if (in && tail.valid) {
+      const int n = after(lane);
+      chains[goes_on + __popc(tails & ((1u << lane) - 1))] =
+          Chain{lane, 1 + n, 1, n > 0 ? infos[lane + n][0].ends : 0, tail.tile, tail.b, tail.h, tail.blocks};
     }
-    n_chains = n;
+    if (lane == 0 && goes_on) {
+      // (if worker 0 has a tail, too, the next workers go on with that one)
+      const int n = tail.valid ? 0 : after(0);
+      chains[0] = Chain{0, 1 + n, 0, infos[n][0].ends, head.tile, head.b, head.h, head.blocks};
+    }
+    if (lane == 0) n_chains = goes_on + __popc(tails);
   }
   __syncthreads();
   const int per_chain = plan.part_rows * (DIM / 4);
@@ -753,55 +799,62 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     const int pr = i % per_chain / (DIM / 4), d = i % (DIM / 4) * 4, row = chain.tile * S::kRows + pr;
     if (row >= plan.rows) continue;
     const auto part = [&](int k) {
-      const int64_t w = static_cast<int64_t>(blockIdx.x) * S::kWarps + chain.warp + k;
-      return plan.parts + (w * 2 + (k == 0 && chain.begins)) * part_floats(plan.part_rows, DIM);
+      const int w = chain.warp + k, slot = k == 0 && chain.begins;
+      if (infos[w][slot].here) return Part{reinterpret_cast<float *>(smem + w * S::kRing), states[w], S::kRows};
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * S::kWarps + w) * 2 + slot;
+      return part_at(plan.parts + at * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
     };
-    const Joined j = join(chain.count, part, plan.part_rows, pr, d, DIM);
+    const Joined j = join(chain.count, part, pr, d, DIM);
     if (chain.begins && chain.ends)
       finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
     else
-      put_part(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
-               plan.part_rows, pr, d, DIM, j);
+      put_part(part_at(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
+                       plan.part_rows, DIM),
+               pr, d, DIM, j);
+  }
+  if (threadIdx.x == 0) {
+    Split split{-1, 0, 0, 0};
+    if (n_chains > 0 && chains[n_chains - 1].begins && !chains[n_chains - 1].ends) {
+      const Chain &chain = chains[n_chains - 1];
+      const int64_t f0 = chain.tile * (total / plan.tiles) + static_cast<int64_t>(first[chain.b]) * c.heads + static_cast<int64_t>(chain.h) * chain.blocks;
+      split = Split{static_cast<int>(shares.owner(f0 + chain.blocks - 1) / S::kWarps), chain.tile, chain.b, chain.h};
+    }
+    plan.splits[blockIdx.x] = split;
   }
 }
 
-// Joins the parts of one row of a (sequence, key head) that several CTAs share, in their
-// order; a row of a sequence without blocks gets 0.  A warp takes every fourth part.
+// Joins the CTAs' parts of a row: CTA (x, y) row y of what CTA x of the launch before began and
+// left unfinished.  Groups of DIM / 4 threads take every so many-th part.
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan, int tile_rows) {
   constexpr int kGroups = kJoinThreads / (DIM / 4);
-  __shared__ __align__(16) float parts[kGroups][DIM + 4];
+  __shared__ __align__(16) float sums[kGroups][DIM];
+  __shared__ float states[kGroups][3];
   griddep_launch_dependents();
   griddep_wait();
-  const CacheArgs &c = a.c;
-  const int row = blockIdx.x % plan.rows, h = blockIdx.y, b = blockIdx.x / plan.rows;
-  const int tile = row / tile_rows, pr = row % tile_rows;
-  const int64_t f0 = plan.first[b], blocks = plan.first[b + 1] - f0, per_tile = plan.first[c.sequences] * c.heads;
-  int64_t p0 = 0, p1 = -1;
-  if (blocks > 0) {
-    const Shares shares(per_tile * plan.tiles, plan.workers);
-    const int64_t begin = tile * per_tile + f0 * c.heads + h * blocks;
-    p0 = shares.owner(begin) / plan.per_cta;
-    p1 = shares.owner(begin + blocks - 1) / plan.per_cta;
-    if (p0 == p1) return;  // the CTA has finished it
-  }
+  const int p0 = blockIdx.x, pr = blockIdx.y;
+  const Split split = plan.splits[p0];
+  if (split.last_cta < 0) return;
+  const int row = split.tile * tile_rows + pr;
+  if (row >= plan.rows) return;
   const int group = threadIdx.x / (DIM / 4), d = threadIdx.x % (DIM / 4) * 4;
-  const int n = static_cast<int>(p1 - p0 + 1), mine = n > group ? (n - group + kGroups - 1) / kGroups : 0;
+  const int n = split.last_cta - p0 + 1, mine = n > group ? (n - group + kGroups - 1) / kGroups : 0;
   // (the first CTA's part begins the row, the others' go on with it)
   const auto part = [&](int k) {
     const int64_t p = p0 + group + static_cast<int64_t>(k) * kGroups;
-    return plan.cta_parts + (p * 2 + (p == p0)) * part_floats(plan.part_rows, DIM);
+    return part_at(plan.cta_parts + (p * 2 + (p == p0)) * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
   };
-  Joined j = join(mine, part, plan.part_rows, pr, d, DIM);
-  put_part(parts[group], 1, 0, d, DIM, j);
+  Joined j = join(mine, part, pr, d, DIM);
+  put_part(Part{sums[group], states[group], 1}, 0, d, DIM, j);
   __syncthreads();
   if (group != 0) return;
-  j = join(kGroups, [&](int k) { return parts[k]; }, 1, 0, d, DIM);
-  finish(a, plan, b, h, row, d, DIM, j.v, j.top, j.ref, j.weight);
+  j = join(min(n, kGroups), [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, DIM);
+  finish(a, plan, split.b, split.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
 }
 
-constexpr size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+constexpr size_t kSplitBytes = kMaxSms * sizeof(Split);
+static_assert(kSplitBytes % 16 == 0, "alignment of the parts");
 
 // The rows of a tile: registers allow 32, or 16 of 256 channels.
 int tile_rows_of(int64_t rows, int dim) { return rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32; }
@@ -823,16 +876,15 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   const int ctas = a.num_sms < kMaxSms ? a.num_sms : kMaxSms;
   plan.per_cta = S::kWarps;
   plan.workers = ctas * S::kWarps;
-  plan.first = static_cast<int64_t *>(a.workspace);
-  plan.cta_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) +
-                                             round256((static_cast<size_t>(a.c.sequences) + 1) * sizeof(int64_t)));
+  plan.splits = static_cast<Split *>(a.workspace);
+  plan.cta_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kSplitBytes);
   plan.parts = plan.cta_parts + 2 * ctas * part_floats(plan.part_rows, DIM);
   constexpr size_t kFixed = static_cast<size_t>(S::kWarps) * (S::kRing + S::kQueryBytes);
-  const size_t smem = kFixed + (static_cast<size_t>(a.c.sequences) + 1) * sizeof(int64_t);
+  const size_t smem = kFixed + (static_cast<size_t>(a.c.sequences) + 1) * sizeof(uint32_t);
   const void *func = reinterpret_cast<const void *>(attention_kernel<DIM, NT>);
   if (!kernel_setup_get(func, nullptr)) {
-    constexpr size_t kMost = kFixed + (kAttentionMaxSequences + 1) * sizeof(int64_t);
-    static_assert(kMost + 2048 <= 227 * 1024, "shared memory");
+    constexpr size_t kMost = kFixed + (kAttentionMaxSequences + 1) * sizeof(uint32_t);
+    static_assert(kMost + 8192 <= 227 * 1024, "shared memory");
     const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kMost));
     if (e != cudaSuccess) return e;
     kernel_setup_put(func, 0);
@@ -840,8 +892,8 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   const cudaError_t e = launch_pdl(attention_kernel<DIM, NT>, dim3(static_cast<unsigned>(ctas)), dim3(S::kWarps * 32),
                                    smem, s, a, plan);
   if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(a.c.sequences) * plan.rows, a.c.heads),
-                    dim3(kJoinThreads), 0, s, a, plan, S::kRows);
+  return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(ctas), plan.part_rows), dim3(kJoinThreads), 0, s, a,
+                    plan, S::kRows);
 }
 
 template <int DIM>
@@ -855,10 +907,9 @@ cudaError_t launch_rows(const AttentionArgs &a, cudaStream_t s) {
 
 }  // namespace
 
-size_t attention_workspace_bytes(int64_t sequences, int64_t rows, int head_dim) {
+size_t attention_workspace_bytes(int64_t rows, int head_dim) {
   const int64_t parts = 2 * kMaxSms * (1 + kMaxWarps);
-  return round256((static_cast<size_t>(sequences) + 1) * sizeof(int64_t)) +
-         static_cast<size_t>(parts * part_floats(part_rows_of(rows, head_dim), head_dim)) * sizeof(float);
+  return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows, head_dim), head_dim)) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t s) {

@@ -75,7 +75,8 @@ struct AttentionArgs {
   void *workspace;
   int num_sms;
 };
-size_t attention_workspace_bytes(int64_t sequences, int64_t rows, int head_dim);
+// rows: of a (sequence, key head)
+size_t attention_workspace_bytes(int64_t rows, int head_dim);
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t s);
 
 constexpr int kSampleMaxVocab = 262144;

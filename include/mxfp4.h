@@ -643,8 +643,9 @@ size_t mx_attention_workspace_bytes(int64_t sequences, int64_t q_tokens, int64_t
  *      1..MX_ATTENTION_MAX_QUERY; sequences 0..MX_ATTENTION_MAX_SEQUENCES; scale finite;
  *      window 0..2^31 - 1.
  * Tokens on a page that is not 0..pages - 1 are not seen, a length above max_pages *
- * page_tokens counts as that, one below 0 as 0; mx_device_status then returns
- * MX_ERR_DEVICE_INDEX.  Products are FP16 with binary32 sums: codes are exact in
+ * page_tokens counts as that, one below 0 as 0, and of lengths that come to more than
+ * 2^36 together nothing is seen; mx_device_status then returns MX_ERR_DEVICE_INDEX.
+ * Products are FP16 with binary32 sums: codes are exact in
  * FP16, q is under a power of two of its row and head (exact above 2^-29 of their
  * largest), the weights of a block of 32 tokens are rounded to FP16 relative to the
  * block's largest.  No output overlaps an input or the workspace
