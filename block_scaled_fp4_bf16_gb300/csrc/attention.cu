@@ -2,7 +2,7 @@
 //
 //   s_t = scale * 2^(ek) q . kcode_t,   out = sum_t softmax(s)_t 2^(ev) vcode_t
 //
-// The cache's bytes bound it: each is read once for the up to 32 (query token, head) rows
+// The cache's bytes bound it: each is read once for the up to 16 (query token, head) rows
 // that share a key head.  Keys, and values transposed, are the 16-row side of FP16 products
 // (16 x 8 x 16, binary32 sums) and the rows its 8 columns, so that the conversion of codes,
 // which costs more than the products, is done once for all rows and few rows waste little.
@@ -35,7 +35,7 @@ namespace {
 constexpr int kMaxSms = 160;
 constexpr int kMaxWarps = 16;
 constexpr int64_t kMostBlocks = int64_t(1) << 31;  // of all sequences
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 128;
 constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14: 2^-28 of it is still exact to 2^-11
 
 // NT: columns of the products in eights, the rows of a tile.
@@ -43,7 +43,7 @@ template <int DIM, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   // registers: DIM / 8 * NT sums and, in registers or shared memory, half as many for queries
-  static constexpr int kWarps = DIM == 64 ? (NT == 1 ? 16 : NT == 2 ? 12 : 8) : DIM == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 6 : 4);
+  static constexpr int kWarps = DIM == 64 ? (NT == 1 ? 16 : 12) : DIM == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 6 : 4);
   static constexpr int kStages = DIM == 64 ? (NT == 1 ? 3 : 4) : DIM == 128 && NT == 2 ? 3 : 2;
   static constexpr int kBlockBytes = 2 * kCacheBlock * DIM;  // keys, values
   static constexpr int kRing = kBlockBytes * kStages;
@@ -228,19 +228,27 @@ __device__ __forceinline__ int query_shift(uint32_t largest) {
   return e == 0 || e == 255 ? 0 : e - 127 - 14;
 }
 
+// What turns a row's sums into its output: two factors, which together may leave binary32's
+// range where the result does not.
+struct Factors {
+  float by_weight, by_scale;
+};
+__device__ __forceinline__ Factors factors_of(float top, float ref, float weight) {
+  return Factors{weight == 0.0f ? 0.0f : exp2f(-kLift) / weight, exp2f(base_of_max(ref) - base_of_max(top))};
+}
+
 // Writes four channels of a finished row, and its log-sum-exp with the first.
 __device__ __forceinline__ void finish(const AttentionArgs &a, const Plan &plan, int b, int h, int row, int d, int dim,
-                                       const float (&v)[4], float top, float ref, float weight) {
+                                       const float (&v)[4], const Factors &f, float top, float weight) {
   const int64_t o_row = static_cast<int64_t>(b) * a.q_tokens + row / plan.group;
   const int64_t head = static_cast<int64_t>(h) * plan.group + row % plan.group;
-  // (two factors: together they may leave binary32's range where the result does not)
-  const float f1 = weight == 0.0f ? 0.0f : exp2f(-kLift) / weight, f2 = exp2f(base_of_max(ref) - base_of_max(top));
   const int64_t to = o_row * a.ld_out + head * dim + d;
   const int64_t extent = (static_cast<int64_t>(a.c.sequences) * a.q_tokens - 1) * a.ld_out +
                          static_cast<int64_t>(a.q_heads) * dim;
   if (in_bounds(to, 4, extent, a.c.status))
     *reinterpret_cast<uint2 *>(a.out + to) =
-        make_uint2(bf16x2_bits(v[0] * f1 * f2, v[1] * f1 * f2), bf16x2_bits(v[2] * f1 * f2, v[3] * f1 * f2));
+        make_uint2(bf16x2_bits(v[0] * f.by_weight * f.by_scale, v[1] * f.by_weight * f.by_scale),
+                   bf16x2_bits(v[2] * f.by_weight * f.by_scale, v[3] * f.by_weight * f.by_scale));
   if (a.lse != nullptr && d == 0)
     a.lse[o_row * a.q_heads + head] = weight == 0.0f ? -INFINITY : (top + log2f(weight)) * 0.6931471805599453f;
 }
@@ -292,8 +300,8 @@ __device__ __forceinline__ void put_part(const Part &p, int row, int d, int dim,
 // A worker's parts: 0 goes on with a (tile, sequence, head) that another began, 1 begins one.
 struct PartInfo {
   int valid, ends;  // ends: the (tile, sequence, head) does
-  int here;         // in the worker's shared memory (the last one of its share)
   int tile, b, h, blocks;
+  Part part;        // in the worker's shared memory (the last one of its share) or the workspace
 };
 // Parts of one (tile, sequence, head) by neighbouring workers of a CTA.
 struct Chain {
@@ -355,7 +363,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     for (int i = threadIdx.x; i < c.heads * plan.rows * (DIM / 4); i += S::kWarps * 32) {
       const float zero[4] = {};
       const int row = i / (DIM / 4) % plan.rows, h = i / (DIM / 4) / plan.rows;
-      finish(a, plan, b, h, row, i % (DIM / 4) * 4, DIM, zero, -INFINITY, -INFINITY, 0.0f);
+      finish(a, plan, b, h, row, i % (DIM / 4) * 4, DIM, zero, Factors{0.0f, 0.0f}, -INFINITY, 0.0f);
     }
   }
   const int64_t total = static_cast<int64_t>(first[c.sequences]) * c.heads * plan.tiles;
@@ -734,7 +742,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
           __syncwarp();
         }
         if (!whole_row && lane == 0)
-          infos[warp][from_start] = PartInfo{1, last, in_ring, at.tile, at.b, at.h, at.blocks};
+          infos[warp][from_start] = PartInfo{1, last, at.tile, at.b, at.h, at.blocks, part};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -748,6 +756,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
             j.ref = ref[nt][r];
             const int pr = nt * 8 + 2 * t + r, row = at.tile * S::kRows + pr;
             if (row >= plan.rows) continue;
+            const Factors factors = factors_of(j.top, j.ref, j.weight);
 #pragma unroll
             for (int run = 0; run < S::kRuns; ++run)
 #pragma unroll
@@ -756,7 +765,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
                 for (int k = 0; k < 4; ++k) j.v[k] = out[nt][(run * S::kRun + e + k) / 2][2 * (k & 1) + r];
                 const int d = run * 128 + g * S::kRun + e;
                 if (whole_row)
-                  finish(a, plan, at.b, at.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
+                  finish(a, plan, at.b, at.h, row, d, DIM, j.v, factors, j.top, j.weight);
                 else
                   put_part(part, pr, d, DIM, j);
               }
@@ -793,26 +802,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     if (lane == 0) n_chains = goes_on + __popc(tails);
   }
   __syncthreads();
-  const int per_chain = plan.part_rows * (DIM / 4);
-  for (int i = threadIdx.x; i < n_chains * per_chain; i += S::kWarps * 32) {
-    const Chain &chain = chains[i / per_chain];
-    const int pr = i % per_chain / (DIM / 4), d = i % (DIM / 4) * 4, row = chain.tile * S::kRows + pr;
-    if (row >= plan.rows) continue;
-    const auto part = [&](int k) {
-      const int w = chain.warp + k, slot = k == 0 && chain.begins;
-      if (infos[w][slot].here) return Part{reinterpret_cast<float *>(smem + w * S::kRing), states[w], S::kRows};
-      const int64_t at = (static_cast<int64_t>(blockIdx.x) * S::kWarps + w) * 2 + slot;
-      return part_at(plan.parts + at * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
-    };
-    const Joined j = join(chain.count, part, pr, d, DIM);
-    if (chain.begins && chain.ends)
-      finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
-    else
-      put_part(part_at(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
-                       plan.part_rows, DIM),
-               pr, d, DIM, j);
-  }
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == S::kWarps * 32 - 1) {
     Split split{-1, 0, 0, 0};
     if (n_chains > 0 && chains[n_chains - 1].begins && !chains[n_chains - 1].ends) {
       const Chain &chain = chains[n_chains - 1];
@@ -821,15 +811,30 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     }
     plan.splits[blockIdx.x] = split;
   }
+  const int per_chain = plan.part_rows * (DIM / 4);
+  for (int i = threadIdx.x; i < n_chains * per_chain; i += S::kWarps * 32) {
+    const Chain &chain = chains[i / per_chain];
+    const int pr = i % per_chain / (DIM / 4), d = i % (DIM / 4) * 4, row = chain.tile * S::kRows + pr;
+    if (row >= plan.rows) continue;
+    const auto part = [&](int k) { return infos[chain.warp + k][k == 0 && chain.begins].part; };
+    const Joined j = join(chain.count, part, pr, d, DIM);
+    if (chain.begins && chain.ends)
+      finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, factors_of(j.top, j.ref, j.weight), j.top, j.weight);
+    else
+      put_part(part_at(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
+                       plan.part_rows, DIM),
+               pr, d, DIM, j);
+  }
 }
 
-// Joins the CTAs' parts of a row: CTA (x, y) row y of what CTA x of the launch before began and
-// left unfinished.  Groups of DIM / 4 threads take every so many-th part.
+// Joins the CTAs' parts of a row: CTA (x, y, z) channels 64 z .. 64 z + 63 of row y of what CTA x
+// of the launch before began and left unfinished.  Groups of 16 threads take every so many-th
+// part.
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads)
     join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan, int tile_rows) {
-  constexpr int kGroups = kJoinThreads / (DIM / 4);
-  __shared__ __align__(16) float sums[kGroups][DIM];
+  constexpr int kSlice = 64, kGroups = kJoinThreads / (kSlice / 4);
+  __shared__ __align__(16) float sums[kGroups][kSlice];
   __shared__ float states[kGroups][3];
   griddep_launch_dependents();
   griddep_wait();
@@ -838,30 +843,29 @@ __global__ void __launch_bounds__(kJoinThreads)
   if (split.last_cta < 0) return;
   const int row = split.tile * tile_rows + pr;
   if (row >= plan.rows) return;
-  const int group = threadIdx.x / (DIM / 4), d = threadIdx.x % (DIM / 4) * 4;
+  const int group = threadIdx.x / (kSlice / 4), d = threadIdx.x % (kSlice / 4) * 4;
   const int n = split.last_cta - p0 + 1, mine = n > group ? (n - group + kGroups - 1) / kGroups : 0;
   // (the first CTA's part begins the row, the others' go on with it)
   const auto part = [&](int k) {
     const int64_t p = p0 + group + static_cast<int64_t>(k) * kGroups;
     return part_at(plan.cta_parts + (p * 2 + (p == p0)) * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
   };
-  Joined j = join(mine, part, pr, d, DIM);
-  put_part(Part{sums[group], states[group], 1}, 0, d, DIM, j);
+  Joined j = join(mine, part, pr, blockIdx.z * kSlice + d, DIM);
+  put_part(Part{sums[group], states[group], 1}, 0, d, kSlice, j);
   __syncthreads();
   if (group != 0) return;
-  j = join(min(n, kGroups), [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, DIM);
-  finish(a, plan, split.b, split.h, row, d, DIM, j.v, j.top, j.ref, j.weight);
+  j = join(min(n, kGroups), [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, kSlice);
+  finish(a, plan, split.b, split.h, row, blockIdx.z * kSlice + d, DIM, j.v, factors_of(j.top, j.ref, j.weight), j.top,
+         j.weight);
 }
 
 constexpr size_t kSplitBytes = kMaxSms * sizeof(Split);
 static_assert(kSplitBytes % 16 == 0, "alignment of the parts");
 
-// The rows of a tile: registers allow 32, or 16 of 256 channels.
-int tile_rows_of(int64_t rows, int dim) { return rows <= 8 ? 8 : rows <= 16 || dim == 256 ? 16 : 32; }
-int64_t part_rows_of(int64_t rows, int dim) {
-  const int64_t most = tile_rows_of(rows, dim);
-  return rows < most ? rows : most;
-}
+// The rows of a tile: 8 where they do, else 16 (32 were slower than two tiles of 16, for lack of
+// registers: 16 x 4 x 8192 of 64/8 heads 99 us against 82, 7 x 4 x 5000 of 28/4 17.0 against 12.6).
+int tile_rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
+int64_t part_rows_of(int64_t rows) { return rows < tile_rows_of(rows) ? rows : tile_rows_of(rows); }
 
 template <int DIM, int NT>
 cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
@@ -871,7 +875,7 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   plan.group = a.q_heads / a.c.heads;
   plan.rows = plan.group * a.q_tokens;
   plan.tiles = (plan.rows + S::kRows - 1) / S::kRows;
-  plan.part_rows = static_cast<int>(part_rows_of(plan.rows, DIM));
+  plan.part_rows = static_cast<int>(part_rows_of(plan.rows));
   plan.blocks_per_page = a.c.page_tokens / kCacheBlock;
   const int ctas = a.num_sms < kMaxSms ? a.num_sms : kMaxSms;
   plan.per_cta = S::kWarps;
@@ -892,24 +896,21 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   const cudaError_t e = launch_pdl(attention_kernel<DIM, NT>, dim3(static_cast<unsigned>(ctas)), dim3(S::kWarps * 32),
                                    smem, s, a, plan);
   if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(ctas), plan.part_rows), dim3(kJoinThreads), 0, s, a,
+  return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(ctas), plan.part_rows, DIM / 64), dim3(kJoinThreads), 0, s, a,
                     plan, S::kRows);
 }
 
 template <int DIM>
 cudaError_t launch_rows(const AttentionArgs &a, cudaStream_t s) {
-  const int rows = tile_rows_of(static_cast<int64_t>(a.q_heads / a.c.heads) * a.q_tokens, DIM);
-  if (rows == 8) return launch<DIM, 1>(a, s);
-  if constexpr (DIM < 256)
-    if (rows == 32) return launch<DIM, 4>(a, s);
-  return launch<DIM, 2>(a, s);
+  const int64_t rows = static_cast<int64_t>(a.q_heads / a.c.heads) * a.q_tokens;
+  return tile_rows_of(rows) == 8 ? launch<DIM, 1>(a, s) : launch<DIM, 2>(a, s);
 }
 
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t rows, int head_dim) {
   const int64_t parts = 2 * kMaxSms * (1 + kMaxWarps);
-  return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows, head_dim), head_dim)) * sizeof(float);
+  return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows), head_dim)) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t s) {

@@ -101,6 +101,12 @@ __device__ __forceinline__ float head_sum(float v) {
   return v;
 }
 
+// The frequencies of all pairs as turns, in shared memory (in registers they would cost a
+// quarter of the warps).
+__device__ __forceinline__ void load_turns(uint64_t *turns, const RopeArgs &a) {
+  for (int i = threadIdx.x; i < a.rotary_dim / 2; i += kWarps * 32) turns[i] = turns_of(a.inv_freq[i]);
+}
+
 // Sine and cosine of the lane's eight pairs at a position.
 struct Angles {
   float sin[8], cos[8];
@@ -132,176 +138,184 @@ __device__ __forceinline__ void turn(float *v, const Angles &t, bool interleaved
   }
 }
 
-__device__ __forceinline__ void load_turns(uint64_t *turns, const RopeArgs &a, const Chunks &c, int j) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    turns[i] = c.turns && in_bounds(8 * j + i, 1, a.rotary_dim / 2, a.status)
-                   ? turns_of(a.inv_freq[8 * j + i])
-                   : 0;
-}
-
-// A warp's share: `slices` of the groups of heads of each token, tokens and slices shared
-// out evenly over the warps of the grid.
+// A warp's items: (token, slice of the groups of heads), in the order of the tokens.
 struct Share {
   int groups[2];  // of queries and keys, 32 / LANES heads each
-  int slices, per_slice;
+  int slices[2], per_slice[2];
 };
+struct Item {
+  int64_t token;
+  int first, last;  // groups
+};
+__device__ __forceinline__ Item item_of(int64_t i, int slices, int per_slice, int groups) {
+  Item t;
+  if (slices == 1) {
+    t = Item{i, 0, groups};
+  } else {  // (there are slices only where tokens are few)
+    const int n = static_cast<int>(i), token = n / slices, first = (n - token * slices) * per_slice;
+    t = Item{token, first, min(first + per_slice, groups)};
+  }
+  return t;
+}
 
+// The reciprocal norm of a head, from its lane's 16 channels.
 template <int LANES>
-__global__ void __launch_bounds__(kWarps * 32)
+__device__ __forceinline__ float reciprocal_norm(const float *v, const RopeArgs &a, float per_dim) {
+  float sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 16; ++e) sum += v[e] * v[e];
+  return rsqrtf(head_sum<LANES>(sum) * per_dim + a.eps);
+}
+
+// Queries and keys count as one row of heads: groups of the queries', then of the keys'.
+template <int LANES>
+__global__ void __launch_bounds__(kWarps * 32, 3)
     rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
   constexpr int kHeads = 32 / LANES, kBatch = 4;
+  __shared__ uint64_t turns[kRopeMaxDim / 2];
   griddep_launch_dependents();
   griddep_wait();
+  load_turns(turns, a);
+  __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LANES;
   const Chunks c = chunks_of(j, a);
-  uint64_t turns[8];
-  load_turns(turns, a, c, j);
+  const float per_dim = 1.0f / static_cast<float>(a.head_dim);
   const int total = share.groups[0] + share.groups[1];
-  const int64_t items = a.tokens * share.slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += stride) {
-    const int64_t token = item / share.slices;
-    const int first = static_cast<int>(item % share.slices) * share.per_slice;
-    const int last = min(first + share.per_slice, total);
+  const int64_t items = a.tokens * share.slices[0], stride = static_cast<int64_t>(gridDim.x) * kWarps;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < items; i += stride) {
+    const Item item = item_of(i, share.slices[0], share.per_slice[0], total);
     Angles t;
-    if (in_bounds(token, 1, a.tokens, a.status)) angles_of(t, turns, a.positions[token]);
-    for (int g0 = first; g0 < last; g0 += kBatch) {
+    bool turned = false;
+    for (int g0 = item.first; g0 < item.last; g0 += kBatch) {
       Row x[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int g = g0 + i, k = g >= share.groups[0];
+      for (int b = 0; b < kBatch; ++b) {
+        const int g = g0 + b, k = g >= share.groups[0];
         const Heads &p = a.part[k];
         const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
-        x[i] = load_row(p.x, token * p.ld + head * a.head_dim, c, c.in && g < last && head < p.heads,
+        x[b] = load_row(p.x, item.token * p.ld + head * a.head_dim, c, c.in && g < item.last && head < p.heads,
                         (a.tokens - 1) * p.ld + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
       }
+      if (!turned) {  // (while the first heads are on their way)
+        turned = true;
+        if (c.turns && in_bounds(item.token, 1, a.tokens, a.status)) angles_of(t, turns + 8 * j, a.positions[item.token]);
+      }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int g = g0 + i, k = g >= share.groups[0];
-        if (g >= last) break;
+      for (int b = 0; b < kBatch; ++b) {
+        const int g = g0 + b, k = g >= share.groups[0];
+        if (g >= item.last) break;
         const Heads &p = a.part[k];
         const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
         float v[16];
-        unpack(x[i].q[0], v);
-        unpack(x[i].q[1], v + 8);
+        unpack(x[b].q[0], v);
+        unpack(x[b].q[1], v + 8);
         if (p.weight != nullptr) {
-          float sum = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sum += v[e] * v[e];
-          const float r = 1.0f / sqrtf(head_sum<LANES>(sum) / static_cast<float>(a.head_dim) + a.eps);
-          float w[16];
           const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
+          const float r = reciprocal_norm<LANES>(v, a, per_dim);
+          float w[16];
           unpack(wr.q[0], w);
           unpack(wr.q[1], w + 8);
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
         }
         if (c.turns) turn<1>(v, t, a.interleaved);
-        store_row(p.y, token * p.ld_y + head * a.head_dim, c, c.in && head < p.heads, v,
+        store_row(p.y, item.token * p.ld_y + head * a.head_dim, c, c.in && head < p.heads, v,
                   (a.tokens - 1) * p.ld_y + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
       }
     }
   }
 }
 
-// The gradients of the inputs, and each CTA's sums of those of the weights.  The order of
-// the sums follows from the sizes and the number of SMs alone: a warp's tokens in order,
-// then the lanes, then the warps, then (backward_sum_kernel) the CTAs.
+// The gradients of the inputs, and each CTA's sums of those of the weights: of the queries,
+// then of the keys (one part's sums in registers at a time).  The order of the sums follows
+// from the sizes and the number of SMs alone: a warp's tokens in order, then the lanes, then
+// the warps, then (backward_sum_kernel) the CTAs.
 template <int LANES>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
   constexpr int kHeads = 32 / LANES, kBatch = 2;
-  __shared__ float sums[kWarps][2][kRopeMaxDim];
+  __shared__ uint64_t turns[kRopeMaxDim / 2];
+  __shared__ float sums[kWarps][kRopeMaxDim];
   griddep_launch_dependents();
   griddep_wait();
+  load_turns(turns, a);
+  __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LANES;
   const Chunks c = chunks_of(j, a);
-  uint64_t turns[8];
-  load_turns(turns, a, c, j);
-  const int total = share.groups[0] + share.groups[1];
-  const int64_t items = a.tokens * share.slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
-  float dw[2][16] = {};
-  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kWarps + warp; item < items; item += stride) {
-    const int64_t token = item / share.slices;
-    const int first = static_cast<int>(item % share.slices) * share.per_slice;
-    const int last = min(first + share.per_slice, total);
-    Angles t;
-    if (in_bounds(token, 1, a.tokens, a.status)) angles_of(t, turns, a.positions[token]);
-    for (int g0 = first; g0 < last; g0 += kBatch) {
-      Row x[kBatch], dy[kBatch];
+  const float per_dim = 1.0f / static_cast<float>(a.head_dim);
+  for (int k = 0; k < 2; ++k) {
+    const Heads &p = a.part[k];
+    const int64_t cols = static_cast<int64_t>(p.heads) * a.head_dim, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    const int64_t items = p.heads > 0 ? a.tokens * share.slices[k] : 0;
+    float dw[16] = {};
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < items; i += stride) {
+      const Item item = item_of(i, share.slices[k], share.per_slice[k], share.groups[k]);
+      Angles t;
+      bool turned = false;
+      for (int g0 = item.first; g0 < item.last; g0 += kBatch) {
+        Row x[kBatch], dy[kBatch];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int g = g0 + i, k = g >= share.groups[0];
-        const Heads &p = a.part[k];
-        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
-        const bool in = c.in && g < last && head < p.heads;
-        const int64_t cols = static_cast<int64_t>(p.heads) * a.head_dim;
-        // (without a norm the inputs are not read)
-        x[i] = load_row(p.x, token * p.ld + head * a.head_dim, c, in && p.weight != nullptr,
-                        (a.tokens - 1) * p.ld + cols, a.status);
-        dy[i] = load_row(p.dy, token * p.ld_dy + head * a.head_dim, c, in,
-                         (a.tokens - 1) * p.ld_dy + cols, a.status);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int g = g0 + i, k = g >= share.groups[0];
-        if (g >= last) break;
-        const Heads &p = a.part[k];
-        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
-        float v[16];
-        unpack(dy[i].q[0], v);
-        unpack(dy[i].q[1], v + 8);
-        if (c.turns) turn<-1>(v, t, a.interleaved);
-        if (p.weight != nullptr) {
-          float n[16], w[16];
-          unpack(x[i].q[0], n);
-          unpack(x[i].q[1], n + 8);
-          const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
-          unpack(wr.q[0], w);
-          unpack(wr.q[1], w + 8);
-          float sum = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 16; ++e) sum += n[e] * n[e];
-          const float r = 1.0f / sqrtf(head_sum<LANES>(sum) / static_cast<float>(a.head_dim) + a.eps);
-          float dot = 0.0f;
-          const bool in = c.in && head < p.heads;  // (others' x is 0, but r may be infinite)
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            n[e] = in ? n[e] * r : 0.0f;
-            const float s = v[e] * n[e];
-            if (k == 0)
-              dw[0][e] += s;
-            else
-              dw[1][e] += s;
-            v[e] *= w[e];
-            dot += v[e] * n[e];
-          }
-          dot = head_sum<LANES>(dot) / static_cast<float>(a.head_dim);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = r * (v[e] - n[e] * dot);
+        for (int b = 0; b < kBatch; ++b) {
+          const int head = (g0 + b) * kHeads + lane / LANES;
+          const bool in = c.in && g0 + b < item.last && head < p.heads;
+          // (without a norm the inputs are not read)
+          x[b] = load_row(p.x, item.token * p.ld + head * a.head_dim, c, in && p.weight != nullptr,
+                          (a.tokens - 1) * p.ld + cols, a.status);
+          dy[b] = load_row(p.dy, item.token * p.ld_dy + head * a.head_dim, c, in, (a.tokens - 1) * p.ld_dy + cols, a.status);
         }
-        store_row(p.y, token * p.ld_y + head * a.head_dim, c, c.in && head < p.heads, v,
-                  (a.tokens - 1) * p.ld_y + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
+        if (!turned) {  // (while the first heads are on their way)
+          turned = true;
+          if (c.turns && in_bounds(item.token, 1, a.tokens, a.status)) angles_of(t, turns + 8 * j, a.positions[item.token]);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          if (g0 + b >= item.last) break;
+          const int head = (g0 + b) * kHeads + lane / LANES;
+          const bool in = c.in && head < p.heads;
+          float v[16];
+          unpack(dy[b].q[0], v);
+          unpack(dy[b].q[1], v + 8);
+          if (c.turns) turn<-1>(v, t, a.interleaved);
+          if (p.weight != nullptr) {
+            const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
+            float n[16], w[16];
+            unpack(x[b].q[0], n);
+            unpack(x[b].q[1], n + 8);
+            const float r = reciprocal_norm<LANES>(n, a, per_dim);
+            unpack(wr.q[0], w);
+            unpack(wr.q[1], w + 8);
+            float dot = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              n[e] = in ? n[e] * r : 0.0f;  // (others' x is 0, but r may be infinite)
+              dw[e] += v[e] * n[e];
+              v[e] *= w[e];
+              dot += v[e] * n[e];
+            }
+            dot = head_sum<LANES>(dot) * per_dim;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = r * (v[e] - n[e] * dot);
+          }
+          store_row(p.y, item.token * p.ld_y + head * a.head_dim, c, in, v, (a.tokens - 1) * p.ld_y + cols, a.status);
+        }
       }
     }
-  }
-  if (a.partials == nullptr) return;
-#pragma unroll
-  for (int k = 0; k < 2; ++k)
+    if (a.partials == nullptr) continue;
+    __syncthreads();  // (the queries' sums are read)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
-      float s = dw[k][e];
+      float s = dw[e];
 #pragma unroll
       for (int m = 16; m >= LANES; m >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-      if (lane < LANES && c.in) sums[warp][k][c.at[e >> 3] + (e & 7)] = s;
+      if (lane < LANES && c.in) sums[warp][c.at[e >> 3] + (e & 7)] = s;
     }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 2 * a.head_dim; i += kWarps * 32) {
-    const int k = i >= a.head_dim, d = i - k * a.head_dim;
-    float s = sums[0][k][d];
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.head_dim; d += kWarps * 32) {
+      float s = sums[0][d];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) s += sums[w][k][d];
-    a.partials[static_cast<int64_t>(blockIdx.x) * 2 * a.head_dim + i] = s;
+      for (int w = 1; w < kWarps; ++w) s += sums[w][d];
+      a.partials[(static_cast<int64_t>(blockIdx.x) * 2 + k) * a.head_dim + d] = s;
+    }
   }
 }
 
@@ -335,27 +349,29 @@ int lanes_of(int head_dim) {
   return lanes;
 }
 
-// Each warp gets a whole token where there are enough of them, otherwise a slice.
-Share share_of(const RopeArgs &a, int lanes, int batch, int64_t warps) {
+// Each warp gets a whole token where there are enough of them, otherwise a slice of its groups.
+void slice(int64_t tokens, int groups, int64_t warps, int *slices, int *per_slice) {
+  int64_t n = warps / (tokens > 0 ? tokens : 1);
+  n = n < 1 ? 1 : n > groups ? groups : n;
+  if (n < 1) n = 1;  // (no heads)
+  *per_slice = static_cast<int>((groups + n - 1) / n);
+  *slices = *per_slice > 0 ? (groups + *per_slice - 1) / *per_slice : 1;
+}
+
+Share share_of(const RopeArgs &a, int lanes, int64_t warps, bool together) {
   const int heads = 32 / lanes;
   Share s;
   for (int k = 0; k < 2; ++k) s.groups[k] = (a.part[k].heads + heads - 1) / heads;
-  const int total = s.groups[0] + s.groups[1];
-  const int most = (total + batch - 1) / batch;
-  int64_t slices = warps / (a.tokens > 0 ? a.tokens : 1);
-  slices = slices < 1 ? 1 : slices > most ? most : slices;
-  s.per_slice = static_cast<int>((total + slices - 1) / slices);
-  s.slices = (total + s.per_slice - 1) / s.per_slice;
+  for (int k = 0; k < 2; ++k)
+    slice(a.tokens, together ? s.groups[0] + s.groups[1] : s.groups[k], warps, &s.slices[k], &s.per_slice[k]);
   return s;
 }
 
 template <int LANES>
 cudaError_t forward(const RopeArgs &a, cudaStream_t s) {
-  const int64_t warps = static_cast<int64_t>(a.num_sms) * 4 * kWarps;
-  // few tokens: one group of heads a warp
-  const Share share = share_of(a, LANES, 1, warps);
-  const int64_t ctas = (a.tokens * share.slices + kWarps - 1) / kWarps;
-  const int64_t most = static_cast<int64_t>(a.num_sms) * 4;
+  const int64_t most = static_cast<int64_t>(a.num_sms) * 3;
+  const Share share = share_of(a, LANES, most * kWarps, true);
+  const int64_t ctas = (a.tokens * share.slices[0] + kWarps - 1) / kWarps;
   return launch_pdl(rope_kernel<LANES>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
                     dim3(kWarps * 32), 0, s, a, share);
 }
@@ -364,8 +380,9 @@ template <int LANES>
 cudaError_t backward(const RopeArgs &a, cudaStream_t s) {
   int64_t most = static_cast<int64_t>(a.num_sms) * 2;
   if (most > kRopeBackCtas) most = kRopeBackCtas;
-  const Share share = share_of(a, LANES, 1, most * kWarps);
-  int64_t ctas = (a.tokens * share.slices + kWarps - 1) / kWarps;
+  const Share share = share_of(a, LANES, most * kWarps, false);
+  const int64_t slices = share.slices[0] > share.slices[1] ? share.slices[0] : share.slices[1];
+  int64_t ctas = (a.tokens * slices + kWarps - 1) / kWarps;
   ctas = ctas < 1 ? 1 : ctas < most ? ctas : most;
   const cudaError_t e = launch_pdl(rope_backward_kernel<LANES>, dim3(static_cast<unsigned>(ctas)),
                                    dim3(kWarps * 32), 0, s, a, share);
