@@ -5,11 +5,12 @@
 // exponent, so that when a later token raises e, rounding the held codes again loses
 // nothing but what falls below 2^-6 of the new range.
 //
-// A CTA takes the new tokens of one block of 32 of one sequence, for one head of the keys or
-// the values: it reads each value once, holds it in registers (8 channels a lane) while the
-// largest magnitude goes through shared memory, and writes its codes.  Bandwidth bounds a
-// prompt; one token each is bound by the chain lengths, page, scale, which is read in
-// parallel with the values.
+// A CTA takes the new tokens of one block of 32 of one sequence, for one head, half of it the
+// keys and half the values: it reads each once, holds it in registers (8 channels a lane)
+// while the largest magnitude goes through shared memory, and writes its codes.  What a value
+// costs bounds a prompt (the largest of two at a time, one factor, no test for infinities
+// where the block has none), the chain starts and lengths, page, scale a single token; the
+// values are read beside it.
 #include <cuda_fp16.h>
 
 #include "kv_cache.cuh"
@@ -17,43 +18,44 @@
 namespace mx {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kHalf = 128;  // threads of keys or values
+constexpr int kThreads = 2 * kHalf;
 
-// The least e with amax <= 448 * 2^e, -127 .. 127 (-127 for 0).
-__device__ __forceinline__ int block_exponent(float amax) {
-  const uint32_t b = __float_as_uint(amax);
-  const int e = static_cast<int>(b >> 23);  // 448 = 1.75 * 2^8
-  if (e == 0) return -127;                  // (below 2^-126: less than 448 * 2^-127)
-  const int up = (b & 0x7FFFFFu) > 0x600000u;
+// The least e with amax <= 448 * 2^e, -127 .. 120 (-127 for 0).
+__device__ __forceinline__ int block_exponent(uint32_t amax) {
+  const int e = static_cast<int>(amax >> 23);  // 448 = 1.75 * 2^8
+  if (e == 0) return -127;                     // (below 2^-126: less than 448 * 2^-127)
+  const int up = (amax & 0x7FFFFFu) > 0x600000u;
   return max(e - 127 - 8 + up, -127);
 }
 
-// The block of a slot: sequence, first position, number of tokens, row of the first.
-struct Slot {
-  int sequence;
-  int64_t position, row;
-  int count;
-};
+// The larger of each of two unsigned 16-bit numbers.
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
 
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kLanes = DIM / 8, kRows = kThreads / kLanes, kPasses = kCacheBlock / kRows;
-  __shared__ int found;
+  constexpr int kLanes = DIM / 8, kRows = kHalf / kLanes, kPasses = kCacheBlock / kRows;
+  __shared__ int found;  // the sequence
   __shared__ uint32_t largest[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
   const CacheArgs &c = a.c;
-  const int which = blockIdx.y & 1, head = blockIdx.y >> 1;
+  const int which = threadIdx.x / kHalf, thread = threadIdx.x % kHalf, head = blockIdx.y;
   // Slots of sequence b begin at starts[b] / 32 + 2 b, which leaves room for any place
   // of its tokens in their blocks.
   int b = 0;
-  int64_t row0 = 0, n = 0, index = 0;
+  int64_t row0 = 0, n = 0, index = 0, stated = 0;
   if (a.starts == nullptr) {
     n = a.tokens / c.sequences;
-    const int64_t per = (n + kCacheBlock - 2) / kCacheBlock + 1;
-    b = static_cast<int>(blockIdx.x / per);
-    index = blockIdx.x % per;
+    const int per = static_cast<int>((n + kCacheBlock - 2) / kCacheBlock + 1);
+    b = static_cast<int>(blockIdx.x) / per;
+    index = static_cast<int>(blockIdx.x) % per;
     row0 = b * n;
+    stated = c.lengths[b];
   } else {
     if (threadIdx.x == 0) found = 0x7FFFFFFF;
     __syncthreads();
@@ -64,6 +66,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         if (slot == 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndex);
         continue;
       }
+      // (starts in order make a slot that of one sequence; out of order, the first one takes it)
       if (slot >= s0 / kCacheBlock + 2 * static_cast<int64_t>(i) &&
           slot < s1 / kCacheBlock + 2 * static_cast<int64_t>(i) + 2)
         atomicMin(&found, i);
@@ -73,50 +76,71 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (b == 0x7FFFFFFF) return;
     row0 = a.starts[b];
     n = a.starts[b + 1] - row0;
+    stated = c.lengths[b];
     index = slot - (row0 / kCacheBlock + 2 * static_cast<int64_t>(b));
   }
   // positions first .. first + n - 1, of which those from 0 on are stored
-  const int64_t stated = c.lengths[b], length = cache_length(c, b);
+  const int64_t length = cache_length(c, b);
   const int64_t first = stated - n, begin = first > 0 ? first : 0;
   const int64_t block0 = (begin / kCacheBlock + index) * kCacheBlock;
   const int64_t from = begin > block0 ? begin : block0;
   const int64_t to = length < block0 + kCacheBlock ? length : block0 + kCacheBlock;
   if (from >= to) return;
+  const int held = static_cast<int>(from - block0), count = static_cast<int>(to - from);
+
+  const int lane = thread % kLanes, sub = thread / kLanes;
+  const int64_t rows = row0 + (from - first);
+  const int64_t extent = (a.tokens - 1) * a.ld[which] + static_cast<int64_t>(c.heads) * DIM;
+  const int64_t x_at = (rows + sub) * a.ld[which] + head * DIM + lane * 8;
+  uint4 x[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    x[i] = make_uint4(0, 0, 0, 0);
+    const int64_t at = x_at + i * kRows * a.ld[which];
+    if (i * kRows + sub < count && in_bounds(at, 8, extent, c.status))
+      x[i] = *reinterpret_cast<const uint4 *>(a.x[which] + at);
+  }
   const int64_t page = cache_page(c, b, block0);
   if (page < 0) return;
-  const int64_t base = (page * c.heads + head) * c.page_tokens + block0 % c.page_tokens;
-  const int held = static_cast<int>(from - block0), count = static_cast<int>(to - from);
+  const int in_page = static_cast<int>(block0 % c.page_tokens);
+  const int64_t base = (page * c.heads + head) * c.page_tokens + in_page;
   uint8_t *scale = c.scales[which] + base / kCacheBlock;
   const int64_t scales = c.pages * c.heads * (c.page_tokens / kCacheBlock);
   const int before = held > 0 && in_bounds(base / kCacheBlock, 1, scales, c.status) ? *scale - 127 : -127;
 
-  const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
-  const int64_t rows = row0 + (from - first);
-  const int64_t extent = (a.tokens - 1) * a.ld[which] + static_cast<int64_t>(c.heads) * DIM;
-  uint4 x[kPasses];
-  uint32_t amax = 0;
+  // magnitudes are ordered as the bits without the sign: two at a time
+  uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
-    const int r = i * kRows + sub;
-    const int64_t at = (rows + r) * a.ld[which] + head * DIM + lane * 8;
-    x[i] = make_uint4(0, 0, 0, 0);
-    if (r < count && in_bounds(at, 8, extent, c.status))
-      x[i] = *reinterpret_cast<const uint4 *>(a.x[which] + at);
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t lo = (w[k] & 0x7FFFu) << 16, hi = w[k] & 0x7FFF0000u;
-      amax = max(amax, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
-    }
+    most = max_u16x2(most, max_u16x2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu));
+    most = max_u16x2(most, max_u16x2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
   }
-  amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-  if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = amax;
-  __syncthreads();
+  uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(most & 0xFFFFu, most >> 16)) << 16;
+  auto across = [&] {  // the largest of the half's warps
+    if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = amax;
+    named_barrier_sync(1 + which, kHalf);
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) amax = max(amax, largest[w]);
-  const int e = max(block_exponent(__uint_as_float(amax)), before);
-  // 2^-e in two factors: e goes up to 120 and down to -127
-  const float f1 = exp2_int(-e / 2), f2 = exp2_int(-e - -e / 2);
+    for (int w = 0; w < kHalf / 32; ++w) amax = max(amax, largest[which * (kHalf / 32) + w]);
+  };
+  across();
+  const bool wild = amax >= 0x7F800000u;  // infinities or NaN: the scale goes by the others
+  if (wild) {
+    amax = 0;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t lo = (w[k] & 0x7FFFu) << 16, hi = w[k] & 0x7FFF0000u;
+        amax = max(amax, max(lo < 0x7F800000u ? lo : 0u, hi < 0x7F800000u ? hi : 0u));
+      }
+    }
+    amax = __reduce_max_sync(0xFFFFFFFFu, amax);
+    named_barrier_sync(1 + which, kHalf);  // (the others have read the first ones)
+    across();
+  }
+  const int e = max(block_exponent(amax), before);
+  const float f = exp2_int(-e);
   uint8_t *codes = c.codes[which] + base * DIM;
   const int64_t code_extent = c.pages * c.heads * c.page_tokens * DIM - base * DIM;
 #pragma unroll
@@ -127,13 +151,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     uint16_t out[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float lo = __uint_as_float(w[k] << 16) * f1 * f2, hi = __uint_as_float(w[k] & 0xFFFF0000u) * f1 * f2;
-      // an infinity is NaN in E4M3 (the conversion would make it 448)
-      if (fabsf(lo) == INFINITY) lo = NAN;
-      if (fabsf(hi) == INFINITY) hi = NAN;
+      float lo = __uint_as_float(w[k] << 16) * f, hi = __uint_as_float(w[k] & 0xFFFF0000u) * f;
+      if (wild) {  // (the conversion would make an infinity 448)
+        if (fabsf(lo) == INFINITY) lo = NAN;
+        if (fabsf(hi) == INFINITY) hi = NAN;
+      }
       asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(out[k]) : "f"(hi), "f"(lo));
     }
-    const int64_t at = static_cast<int64_t>(held + r) * DIM + lane * 8;
+    const int at = (held + r) * DIM + lane * 8;
     if (in_bounds(at, 8, code_extent, c.status))
       *reinterpret_cast<uint2 *>(codes + at) =
           make_uint2(out[0] | static_cast<uint32_t>(out[1]) << 16, out[2] | static_cast<uint32_t>(out[3]) << 16);
@@ -141,7 +166,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   if (e > before && held > 0) {
     // what the block holds, rounded again under the new scale
     const float g = exp2_int(max(before - e, -149));
-    for (int i = threadIdx.x; i < held * (DIM / 4); i += kThreads) {
+    for (int i = thread; i < held * (DIM / 4); i += kHalf) {
       if (!in_bounds(static_cast<int64_t>(i) * 4, 4, code_extent, c.status)) continue;
       uint32_t *p = reinterpret_cast<uint32_t *>(codes) + i;
       const float2 lo = e4m3x2_value(*p & 0xFFFFu), hi = e4m3x2_value(*p >> 16);
@@ -152,8 +177,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       *p = (*p & nan) | ((l | static_cast<uint32_t>(h) << 16) & ~nan);
     }
   }
-  if (threadIdx.x == 0 && in_bounds(base / kCacheBlock, 1, scales, c.status))
-    *scale = static_cast<uint8_t>(e + 127);
+  if (thread == 0 && in_bounds(base / kCacheBlock, 1, scales, c.status)) *scale = static_cast<uint8_t>(e + 127);
 }
 
 template <int DIM>
@@ -165,8 +189,8 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
   } else {
     slots = a.tokens / kCacheBlock + 2 * static_cast<int64_t>(a.c.sequences);
   }
-  return launch_pdl(append_kernel<DIM>, dim3(static_cast<unsigned>(slots), 2 * a.c.heads), dim3(kThreads),
-                    0, s, a);
+  return launch_pdl(append_kernel<DIM>, dim3(static_cast<unsigned>(slots), a.c.heads), dim3(kThreads), 0,
+                    s, a);
 }
 
 }  // namespace

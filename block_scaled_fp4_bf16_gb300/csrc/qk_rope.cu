@@ -9,6 +9,8 @@
 // holds both channels of its eight pairs in either order of the channels; a warp takes 32 /
 // LANES heads at a time and goes through the heads of a token with the sines and cosines
 // in registers: they are computed once for a token and slice of its heads, not once a head.
+#include <type_traits>
+
 #include "decode.h"
 #include "mx_device.cuh"
 
@@ -69,6 +71,30 @@ __device__ __forceinline__ uint4 pack(const float *v) {
   for (int i = 0; i < 4; ++i)
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
   return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A part's weight in shared memory, in the lanes' order: lane j's 16 channels, four at a time.
+struct Weights {
+  float4 of[4][16];  // [four][lane j]
+};
+__device__ __forceinline__ void load_weights(Weights &w, const uint16_t *weight, const RopeArgs &a) {
+  for (int i = threadIdx.x; i < 64 && weight != nullptr; i += kWarps * 32) {
+    const int j = i >> 2, four = i & 3;
+    const Chunks c = chunks_of(j, a);
+    const int at = c.at[four >> 1] + 4 * (four & 1);
+    if (!c.in || !in_bounds(at, 4, a.head_dim, a.status)) continue;
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(static_cast<uint32_t>(weight[at + e]) << 16);
+    w.of[four][j] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+__device__ __forceinline__ void weights_of(float *w, const Weights &s, int j) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = s.of[i][j];
+    w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+  }
 }
 
 // A lane's 16 channels of a row that begins at element `row` (zeros if !in).
@@ -169,60 +195,75 @@ __device__ __forceinline__ float reciprocal_norm(const float *v, const RopeArgs 
 
 // Queries and keys count as one row of heads: groups of the queries', then of the keys'.
 template <int LANES>
-__global__ void __launch_bounds__(kWarps * 32, 3)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     rope_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
-  constexpr int kHeads = 32 / LANES, kBatch = 4;
+  constexpr int kHeads = 32 / LANES, kBatch = 2;
   __shared__ uint64_t turns[kRopeMaxDim / 2];
+  __shared__ Weights weights[2];
   griddep_launch_dependents();
   griddep_wait();
   load_turns(turns, a);
+  load_weights(weights[0], a.part[0].weight, a);
+  load_weights(weights[1], a.part[1].weight, a);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LANES;
   const Chunks c = chunks_of(j, a);
   const float per_dim = 1.0f / static_cast<float>(a.head_dim);
-  const int total = share.groups[0] + share.groups[1];
   const int64_t items = a.tokens * share.slices[0], stride = static_cast<int64_t>(gridDim.x) * kWarps;
   for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < items; i += stride) {
-    const Item item = item_of(i, share.slices[0], share.per_slice[0], total);
+    const Item item = item_of(i, share.slices[0], share.per_slice[0], share.groups[0] + share.groups[1]);
     Angles t;
     bool turned = false;
-    for (int g0 = item.first; g0 < item.last; g0 += kBatch) {
-      Row x[kBatch];
+    // groups first .. last - 1 of a part (K: queries or keys, so that its fields are constants)
+    auto part = [&](auto which, int first, int last) {
+      constexpr int K = decltype(which)::value;
+      if (first >= last) return;
+      const Heads &p = a.part[K];
+      const int64_t cols = static_cast<int64_t>(p.heads) * a.head_dim;
+      const int step = kHeads * a.head_dim, own = lane / LANES * a.head_dim;
+      const int64_t x_at = item.token * p.ld + own, y_at = item.token * p.ld_y + own;
+      Row x[2][kBatch];  // a batch, and the next one on its way
+      auto load = [&](Row(&to)[kBatch], int g0) {
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int g = g0 + b, k = g >= share.groups[0];
-        const Heads &p = a.part[k];
-        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
-        x[b] = load_row(p.x, item.token * p.ld + head * a.head_dim, c, c.in && g < item.last && head < p.heads,
-                        (a.tokens - 1) * p.ld + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
-      }
+        for (int b = 0; b < kBatch; ++b)
+          to[b] = load_row(p.x, x_at + static_cast<int64_t>(g0 + b) * step, c,
+                           c.in && g0 + b < last && (g0 + b) * kHeads + lane / LANES < p.heads,
+                           (a.tokens - 1) * p.ld + cols, a.status);
+      };
+      auto turn_batch = [&](const Row(&of)[kBatch], int g0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          if (g0 + b >= last) break;
+          float v[16];
+          unpack(of[b].q[0], v);
+          unpack(of[b].q[1], v + 8);
+          if (p.weight != nullptr) {
+            const float r = reciprocal_norm<LANES>(v, a, per_dim);
+            float w[16];
+            weights_of(w, weights[K], j);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
+          }
+          if (c.turns) turn<1>(v, t, a.interleaved);
+          store_row(p.y, y_at + static_cast<int64_t>(g0 + b) * step, c,
+                    c.in && (g0 + b) * kHeads + lane / LANES < p.heads, v, (a.tokens - 1) * p.ld_y + cols, a.status);
+        }
+      };
+      load(x[0], first);
       if (!turned) {  // (while the first heads are on their way)
         turned = true;
         if (c.turns && in_bounds(item.token, 1, a.tokens, a.status)) angles_of(t, turns + 8 * j, a.positions[item.token]);
       }
-#pragma unroll
-      for (int b = 0; b < kBatch; ++b) {
-        const int g = g0 + b, k = g >= share.groups[0];
-        if (g >= item.last) break;
-        const Heads &p = a.part[k];
-        const int head = (g - (k ? share.groups[0] : 0)) * kHeads + lane / LANES;
-        float v[16];
-        unpack(x[b].q[0], v);
-        unpack(x[b].q[1], v + 8);
-        if (p.weight != nullptr) {
-          const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
-          const float r = reciprocal_norm<LANES>(v, a, per_dim);
-          float w[16];
-          unpack(wr.q[0], w);
-          unpack(wr.q[1], w + 8);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = v[e] * r * w[e];
-        }
-        if (c.turns) turn<1>(v, t, a.interleaved);
-        store_row(p.y, item.token * p.ld_y + head * a.head_dim, c, c.in && head < p.heads, v,
-                  (a.tokens - 1) * p.ld_y + static_cast<int64_t>(p.heads) * a.head_dim, a.status);
+      for (int g0 = first; g0 < last; g0 += 2 * kBatch) {
+        if (g0 + kBatch < last) load(x[1], g0 + kBatch);
+        turn_batch(x[0], g0);
+        if (g0 + kBatch >= last) break;
+        if (g0 + 2 * kBatch < last) load(x[0], g0 + 2 * kBatch);
+        turn_batch(x[1], g0 + kBatch);
       }
-    }
+    };
+    part(std::integral_constant<int, 0>(), item.first, min(item.last, share.groups[0]));
+    part(std::integral_constant<int, 1>(), max(item.first - share.groups[0], 0), item.last - share.groups[0]);
   }
 }
 
@@ -235,21 +276,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
   constexpr int kHeads = 32 / LANES, kBatch = 2;
   __shared__ uint64_t turns[kRopeMaxDim / 2];
+  __shared__ Weights weights[2];
   __shared__ float sums[kWarps][kRopeMaxDim];
   griddep_launch_dependents();
   griddep_wait();
   load_turns(turns, a);
+  load_weights(weights[0], a.part[0].weight, a);
+  load_weights(weights[1], a.part[1].weight, a);
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, j = lane % LANES;
   const Chunks c = chunks_of(j, a);
   const float per_dim = 1.0f / static_cast<float>(a.head_dim);
-  for (int k = 0; k < 2; ++k) {
+  auto part = [&](auto which) {
+    constexpr int k = decltype(which)::value;
     const Heads &p = a.part[k];
     const int64_t cols = static_cast<int64_t>(p.heads) * a.head_dim, stride = static_cast<int64_t>(gridDim.x) * kWarps;
     const int64_t items = p.heads > 0 ? a.tokens * share.slices[k] : 0;
     float dw[16] = {};
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + warp; i < items; i += stride) {
       const Item item = item_of(i, share.slices[k], share.per_slice[k], share.groups[k]);
+      const int step = kHeads * a.head_dim, own = lane / LANES * a.head_dim;
+      const int64_t x_at = item.token * p.ld + own, dy_at = item.token * p.ld_dy + own, y_at = item.token * p.ld_y + own;
       Angles t;
       bool turned = false;
       for (int g0 = item.first; g0 < item.last; g0 += kBatch) {
@@ -259,9 +306,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           const int head = (g0 + b) * kHeads + lane / LANES;
           const bool in = c.in && g0 + b < item.last && head < p.heads;
           // (without a norm the inputs are not read)
-          x[b] = load_row(p.x, item.token * p.ld + head * a.head_dim, c, in && p.weight != nullptr,
-                          (a.tokens - 1) * p.ld + cols, a.status);
-          dy[b] = load_row(p.dy, item.token * p.ld_dy + head * a.head_dim, c, in, (a.tokens - 1) * p.ld_dy + cols, a.status);
+          const int64_t at = static_cast<int64_t>(g0 + b) * step;
+          x[b] = load_row(p.x, x_at + at, c, in && p.weight != nullptr, (a.tokens - 1) * p.ld + cols, a.status);
+          dy[b] = load_row(p.dy, dy_at + at, c, in, (a.tokens - 1) * p.ld_dy + cols, a.status);
         }
         if (!turned) {  // (while the first heads are on their way)
           turned = true;
@@ -277,13 +324,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
           unpack(dy[b].q[1], v + 8);
           if (c.turns) turn<-1>(v, t, a.interleaved);
           if (p.weight != nullptr) {
-            const Row wr = load_row(p.weight, 0, c, c.in, a.head_dim, a.status);
             float n[16], w[16];
             unpack(x[b].q[0], n);
             unpack(x[b].q[1], n + 8);
             const float r = reciprocal_norm<LANES>(n, a, per_dim);
-            unpack(wr.q[0], w);
-            unpack(wr.q[1], w + 8);
+            weights_of(w, weights[k], j);
             float dot = 0.0f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
@@ -296,11 +341,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = r * (v[e] - n[e] * dot);
           }
-          store_row(p.y, item.token * p.ld_y + head * a.head_dim, c, in, v, (a.tokens - 1) * p.ld_y + cols, a.status);
+          store_row(p.y, y_at + static_cast<int64_t>(g0 + b) * step, c, in, v, (a.tokens - 1) * p.ld_y + cols, a.status);
         }
       }
     }
-    if (a.partials == nullptr) continue;
+    if (a.partials == nullptr) return;
     __syncthreads();  // (the queries' sums are read)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
@@ -316,7 +361,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       for (int w = 1; w < kWarps; ++w) s += sums[w][d];
       a.partials[(static_cast<int64_t>(blockIdx.x) * 2 + k) * a.head_dim + d] = s;
     }
-  }
+  };
+  part(std::integral_constant<int, 0>());
+  part(std::integral_constant<int, 1>());
 }
 
 // dweight[d] = the CTAs' sums, in their order within each of 8 warps: a CTA takes 32
@@ -349,13 +396,19 @@ int lanes_of(int head_dim) {
   return lanes;
 }
 
-// Each warp gets a whole token where there are enough of them, otherwise a slice of its groups.
+// Slices of a token's groups of heads: those with which the busiest warp has the least to do,
+// an item's angles counted as one group (8192 tokens of 18 groups on 3648 warps: whole tokens
+// leave most warps with two and some with three).
 void slice(int64_t tokens, int groups, int64_t warps, int *slices, int *per_slice) {
-  int64_t n = warps / (tokens > 0 ? tokens : 1);
-  n = n < 1 ? 1 : n > groups ? groups : n;
-  if (n < 1) n = 1;  // (no heads)
-  *per_slice = static_cast<int>((groups + n - 1) / n);
-  *slices = *per_slice > 0 ? (groups + *per_slice - 1) / *per_slice : 1;
+  *slices = 1;
+  *per_slice = groups;
+  int64_t least = INT64_MAX;
+  for (int p = groups; p >= 1; --p) {
+    const int n = (groups + p - 1) / p;
+    if (n > 1 && tokens * n >= (int64_t(1) << 31)) break;  // (the kernel divides 32-bit numbers)
+    const int64_t cost = (tokens * n + warps - 1) / warps * (p + 1);
+    if (cost < least) least = cost, *slices = n, *per_slice = p;
+  }
 }
 
 Share share_of(const RopeArgs &a, int lanes, int64_t warps, bool together) {
@@ -369,7 +422,7 @@ Share share_of(const RopeArgs &a, int lanes, int64_t warps, bool together) {
 
 template <int LANES>
 cudaError_t forward(const RopeArgs &a, cudaStream_t s) {
-  const int64_t most = static_cast<int64_t>(a.num_sms) * 3;
+  const int64_t most = static_cast<int64_t>(a.num_sms) * 2;
   const Share share = share_of(a, LANES, most * kWarps, true);
   const int64_t ctas = (a.tokens * share.slices[0] + kWarps - 1) / kWarps;
   return launch_pdl(rope_kernel<LANES>, dim3(static_cast<unsigned>(ctas < most ? ctas : most)),
