@@ -5,12 +5,13 @@
 // exponent, so that when a later token raises e, rounding the held codes again loses
 // nothing but what falls below 2^-6 of the new range.
 //
-// A CTA takes the new tokens of one block of 32 of one sequence, for one head, half of it the
-// keys and half the values: it reads each once, holds it in registers (8 channels a lane)
-// while the largest magnitude goes through shared memory, and writes its codes.  What a value
-// costs bounds a prompt (the largest of two at a time, one factor, no test for infinities
-// where the block has none), the chain starts and lengths, page, scale a single token; the
-// values are read beside it.
+// A CTA takes the new tokens of one block of 32 of one sequence, for as many heads as come to
+// 256 channels (one head a CTA: 23 us for 16384 x 8 x 128, 35 for 16 x 64, where this takes 19 and
+// 20).  A unit of its threads has the keys or the values of a head: it reads each once, holds
+// it in registers (8 channels a lane) while the largest magnitude goes across its warps, and
+// writes its codes.  What a value costs bounds a prompt (so the largest of two at a time, one
+// factor, no test for infinities where the block has none), the chain starts and lengths,
+// page, scale a single token; the values are read beside it.
 #include <cuda_fp16.h>
 
 #include "kv_cache.cuh"
@@ -18,8 +19,7 @@
 namespace mx {
 namespace {
 
-constexpr int kHalf = 128;  // threads of keys or values
-constexpr int kThreads = 2 * kHalf;
+constexpr int kThreads = 256;
 
 // The least e with amax <= 448 * 2^e, -127 .. 120 (-127 for 0).
 __device__ __forceinline__ int block_exponent(uint32_t amax) {
@@ -38,13 +38,15 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
-  constexpr int kLanes = DIM / 8, kRows = kHalf / kLanes, kPasses = kCacheBlock / kRows;
+  constexpr int kLanes = DIM / 8, kRows = 4, kPasses = kCacheBlock / kRows;
+  constexpr int kUnit = kLanes * kRows, kUnits = kThreads / kUnit;  // a unit: keys or values of a head
   __shared__ int found;  // the sequence
   __shared__ uint32_t largest[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
   const CacheArgs &c = a.c;
-  const int which = threadIdx.x / kHalf, thread = threadIdx.x % kHalf, head = blockIdx.y;
+  const int unit = threadIdx.x / kUnit, thread = threadIdx.x % kUnit;
+  const int which = unit & 1, head = blockIdx.y * (kUnits / 2) + (unit >> 1);
   // Slots of sequence b begin at starts[b] / 32 + 2 b, which leaves room for any place
   // of its tokens in their blocks.
   int b = 0;
@@ -79,6 +81,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     stated = c.lengths[b];
     index = slot - (row0 / kCacheBlock + 2 * static_cast<int64_t>(b));
   }
+  if (head >= c.heads) return;
   // positions first .. first + n - 1, of which those from 0 on are stored
   const int64_t length = cache_length(c, b);
   const int64_t first = stated - n, begin = first > 0 ? first : 0;
@@ -116,11 +119,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     most = max_u16x2(most, max_u16x2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu));
   }
   uint32_t amax = __reduce_max_sync(0xFFFFFFFFu, max(most & 0xFFFFu, most >> 16)) << 16;
-  auto across = [&] {  // the largest of the half's warps
-    if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = amax;
-    named_barrier_sync(1 + which, kHalf);
+  auto across = [&] {  // the largest of the unit's warps
+    if constexpr (kUnit > 32) {
+      if ((threadIdx.x & 31) == 0) largest[threadIdx.x >> 5] = amax;
+      named_barrier_sync(1 + unit, kUnit);
 #pragma unroll
-    for (int w = 0; w < kHalf / 32; ++w) amax = max(amax, largest[which * (kHalf / 32) + w]);
+      for (int w = 0; w < kUnit / 32; ++w) amax = max(amax, largest[unit * (kUnit / 32) + w]);
+    }
   };
   across();
   const bool wild = amax >= 0x7F800000u;  // infinities or NaN: the scale goes by the others
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       }
     }
     amax = __reduce_max_sync(0xFFFFFFFFu, amax);
-    named_barrier_sync(1 + which, kHalf);  // (the others have read the first ones)
+    if constexpr (kUnit > 32) named_barrier_sync(1 + unit, kUnit);  // (the others have read the first ones)
     across();
   }
   const int e = max(block_exponent(amax), before);
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   if (e > before && held > 0) {
     // what the block holds, rounded again under the new scale
     const float g = exp2_int(max(before - e, -149));
-    for (int i = thread; i < held * (DIM / 4); i += kHalf) {
+    for (int i = thread; i < held * (DIM / 4); i += kUnit) {
       if (!in_bounds(static_cast<int64_t>(i) * 4, 4, code_extent, c.status)) continue;
       uint32_t *p = reinterpret_cast<uint32_t *>(codes) + i;
       const float2 lo = e4m3x2_value(*p & 0xFFFFu), hi = e4m3x2_value(*p >> 16);
@@ -189,8 +194,9 @@ cudaError_t launch(const AppendArgs &a, cudaStream_t s) {
   } else {
     slots = a.tokens / kCacheBlock + 2 * static_cast<int64_t>(a.c.sequences);
   }
-  return launch_pdl(append_kernel<DIM>, dim3(static_cast<unsigned>(slots), a.c.heads), dim3(kThreads), 0,
-                    s, a);
+  constexpr int kHeads = kThreads / (DIM / 2) / 2;  // of a CTA
+  return launch_pdl(append_kernel<DIM>, dim3(static_cast<unsigned>(slots), (a.c.heads + kHeads - 1) / kHeads),
+                    dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

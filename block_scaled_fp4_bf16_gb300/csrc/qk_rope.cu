@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 template <int LANES>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {
-  constexpr int kHeads = 32 / LANES, kBatch = 2;
+  constexpr int kHeads = 32 / LANES;
   __shared__ uint64_t turns[kRopeMaxDim / 2];
   __shared__ Weights weights[2];
   __shared__ float sums[kWarps][kRopeMaxDim];
@@ -298,51 +298,49 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       const int step = kHeads * a.head_dim, own = lane / LANES * a.head_dim;
       const int64_t x_at = item.token * p.ld + own, dy_at = item.token * p.ld_dy + own, y_at = item.token * p.ld_y + own;
       Angles t;
-      bool turned = false;
-      for (int g0 = item.first; g0 < item.last; g0 += kBatch) {
-        Row x[kBatch], dy[kBatch];
+      Row x[2], dy[2];  // of a group, and of the next one, on its way
+      auto load = [&](int to, int g) {
+        const bool in = c.in && g * kHeads + lane / LANES < p.heads;
+        const int64_t at = static_cast<int64_t>(g) * step;
+        // (without a norm the inputs are not read)
+        x[to] = load_row(p.x, x_at + at, c, in && p.weight != nullptr, (a.tokens - 1) * p.ld + cols, a.status);
+        dy[to] = load_row(p.dy, dy_at + at, c, in, (a.tokens - 1) * p.ld_dy + cols, a.status);
+      };
+      auto back = [&](int of, int g) {
+        const bool in = c.in && g * kHeads + lane / LANES < p.heads;
+        float v[16];
+        unpack(dy[of].q[0], v);
+        unpack(dy[of].q[1], v + 8);
+        if (c.turns) turn<-1>(v, t, a.interleaved);
+        if (p.weight != nullptr) {
+          float n[16], w[16];
+          unpack(x[of].q[0], n);
+          unpack(x[of].q[1], n + 8);
+          const float r = reciprocal_norm<LANES>(n, a, per_dim);
+          weights_of(w, weights[k], j);
+          float dot = 0.0f;
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          const int head = (g0 + b) * kHeads + lane / LANES;
-          const bool in = c.in && g0 + b < item.last && head < p.heads;
-          // (without a norm the inputs are not read)
-          const int64_t at = static_cast<int64_t>(g0 + b) * step;
-          x[b] = load_row(p.x, x_at + at, c, in && p.weight != nullptr, (a.tokens - 1) * p.ld + cols, a.status);
-          dy[b] = load_row(p.dy, dy_at + at, c, in, (a.tokens - 1) * p.ld_dy + cols, a.status);
-        }
-        if (!turned) {  // (while the first heads are on their way)
-          turned = true;
-          if (c.turns && in_bounds(item.token, 1, a.tokens, a.status)) angles_of(t, turns + 8 * j, a.positions[item.token]);
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-          if (g0 + b >= item.last) break;
-          const int head = (g0 + b) * kHeads + lane / LANES;
-          const bool in = c.in && head < p.heads;
-          float v[16];
-          unpack(dy[b].q[0], v);
-          unpack(dy[b].q[1], v + 8);
-          if (c.turns) turn<-1>(v, t, a.interleaved);
-          if (p.weight != nullptr) {
-            float n[16], w[16];
-            unpack(x[b].q[0], n);
-            unpack(x[b].q[1], n + 8);
-            const float r = reciprocal_norm<LANES>(n, a, per_dim);
-            weights_of(w, weights[k], j);
-            float dot = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              n[e] = in ? n[e] * r : 0.0f;  // (others' x is 0, but r may be infinite)
-              dw[e] += v[e] * n[e];
-              v[e] *= w[e];
-              dot += v[e] * n[e];
-            }
-            dot = head_sum<LANES>(dot) * per_dim;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = r * (v[e] - n[e] * dot);
+          for (int e = 0; e < 16; ++e) {
+            n[e] = in ? n[e] * r : 0.0f;  // (others' x is 0, but r may be infinite)
+            dw[e] += v[e] * n[e];
+            v[e] *= w[e];
+            dot += v[e] * n[e];
           }
-          store_row(p.y, y_at + static_cast<int64_t>(g0 + b) * step, c, in, v, (a.tokens - 1) * p.ld_y + cols, a.status);
+          dot = head_sum<LANES>(dot) * per_dim;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = r * (v[e] - n[e] * dot);
         }
+        store_row(p.y, y_at + static_cast<int64_t>(g) * step, c, in, v, (a.tokens - 1) * p.ld_y + cols, a.status);
+      };
+      if (item.first >= item.last) continue;
+      load(0, item.first);
+      if (c.turns && in_bounds(item.token, 1, a.tokens, a.status)) angles_of(t, turns + 8 * j, a.positions[item.token]);
+      for (int g = item.first; g < item.last; g += 2) {
+        if (g + 1 < item.last) load(1, g + 1);
+        back(0, g);
+        if (g + 1 >= item.last) break;
+        if (g + 2 < item.last) load(0, g + 2);
+        back(1, g + 1);
       }
     }
     if (a.partials == nullptr) return;
@@ -366,29 +364,34 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   part(std::integral_constant<int, 1>());
 }
 
-// dweight[d] = the CTAs' sums, in their order within each of 8 warps: a CTA takes 32
-// columns of the 2 head_dim.
-__global__ void __launch_bounds__(kWarps * 32)
+// dweight[d] = the CTAs' sums, in their order within each of 32 warps (so that all are read at
+// once): a CTA takes 32 columns of the 2 head_dim.
+constexpr int kSumWarps = 32;
+__global__ void __launch_bounds__(kSumWarps * 32)
     backward_sum_kernel(const __grid_constant__ RopeArgs a, int ctas) {
-  __shared__ float sums[kWarps][32];
+  __shared__ float sums[kSumWarps][32];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int i = blockIdx.x * 32 + lane;
   float s = 0.0f;
   if (i < 2 * a.head_dim) {
-#pragma unroll 8
-    for (int p = warp; p < ctas; p += kWarps) s += a.partials[static_cast<int64_t>(p) * 2 * a.head_dim + i];
+#pragma unroll
+    for (int k = 0; k < kRopeBackCtas / kSumWarps; ++k) {
+      const int p = k * kSumWarps + warp;
+      if (p < ctas) s += a.partials[static_cast<int64_t>(p) * 2 * a.head_dim + i];
+    }
   }
   sums[warp][lane] = s;
   __syncthreads();
   if (warp != 0 || i >= 2 * a.head_dim) return;
 #pragma unroll
-  for (int w = 1; w < kWarps; ++w) s += sums[w][lane];
+  for (int w = 1; w < kSumWarps; ++w) s += sums[w][lane];
   const int k = i >= a.head_dim;
   float *out = a.part[k].dweight;
   if (out != nullptr) out[i - k * a.head_dim] = s;
 }
+static_assert(kRopeBackCtas % kSumWarps == 0, "all partials are summed");
 
 int lanes_of(int head_dim) {
   int lanes = 1;
@@ -440,7 +443,7 @@ cudaError_t backward(const RopeArgs &a, cudaStream_t s) {
   const cudaError_t e = launch_pdl(rope_backward_kernel<LANES>, dim3(static_cast<unsigned>(ctas)),
                                    dim3(kWarps * 32), 0, s, a, share);
   if (e != cudaSuccess || a.partials == nullptr) return e;
-  return launch_pdl(backward_sum_kernel, dim3((2 * a.head_dim + 31) / 32), dim3(kWarps * 32), 0, s, a,
+  return launch_pdl(backward_sum_kernel, dim3((2 * a.head_dim + 31) / 32), dim3(kSumWarps * 32), 0, s, a,
                     static_cast<int>(ctas));
 }
 
