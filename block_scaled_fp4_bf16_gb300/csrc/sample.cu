@@ -57,38 +57,54 @@ struct Scale {
   float top, hi, lo;
 };
 
-// round(2^43 exp((l - top) / temperature)), l <= top; 0 below 2^-44.
-__device__ __forceinline__ uint64_t weight_of(float l, const Scale &c, const float2 *table) {
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ float2 minus(float2 a, float2 b) { return fma_f32x2(b, both(-1.0f), a); }
+
+// round(2^43 exp((l - top) / temperature)) of two logits l <= top (finite), 0 below 2^-44 and
+// where !in.  Two at a time: a weight is some forty binary32 operations, which come in pairs.
+__device__ __forceinline__ void weights_of(float2 l, const Scale &c, const float2 *table, const bool (&in)[2],
+                                           uint64_t (&w)[2]) {
   // l - top, exactly, as d + e
-  const float d = l - c.top, b = d - l;
-  const float e = (l - (d - b)) + (-c.top - b);
-  const float exponent = d * c.hi, p = fmaxf(exponent, -46.0f);  // (-46 for NaN, too)
-  const float pe = fmaf(d, c.hi, -p) + fmaf(d, c.lo, e * c.hi);
-  // 2^(p + pe) = 2^(k / 256) 2^r, k to the nearest: the sum with 1.5 * 2^23 ends in it (the
+  const float2 top = both(-c.top), b = minus(add_f32x2(l, top), l);
+  float2 d = add_f32x2(l, top), e = add_f32x2(minus(l, minus(d, b)), minus(top, b));
+  // -(l - top) / temperature in powers of two, and what its rounding leaves; a weight that is 0
+  // goes on as 1, which is dropped at the end (no infinity or NaN on the way)
+  float2 p = mul_f32x2(d, both(-c.hi));
+  const bool some[2] = {in[0] && p.x < 46.0f, in[1] && p.y < 46.0f};
+  d = make_float2(some[0] ? d.x : 0.0f, some[1] ? d.y : 0.0f);
+  e = make_float2(some[0] ? e.x : 0.0f, some[1] ? e.y : 0.0f);
+  p = make_float2(some[0] ? p.x : 0.0f, some[1] ? p.y : 0.0f);
+  const float2 pe = fma_f32x2(d, both(c.lo), fma_f32x2(e, both(c.hi), fma_f32x2(d, both(c.hi), p)));
+  // 2^(pe - p) = 2^(k / 256) 2^-r, k to the nearest: the sum with 1.5 * 2^23 ends in it (the
   // conversion instructions have an eighth of an addition's rate)
-  const float kb = fmaf(p, 256.0f, 0x1.8p23f);
-  const int k = __float_as_int(kb) - 0x4B400000;
-  const float r = fmaf(kb - 0x1.8p23f, -0x1p-8f, p);
-  // y = r ln 2 as yh + yl, then e^y - 1 as qh + qe
-  const float yh = r * 0x1.62e43p-1f;
-  const float yl = fmaf(r, 0x1.62e43p-1f, -yh) + fmaf(r, -0x1.05c61p-29f, pe * 0x1.62e43p-1f);
-  const float ql = fmaf(yl, yh, yl) + yh * yh * fmaf(yh, fmaf(yh, 1.0f / 24.0f, 1.0f / 6.0f), 0.5f);
-  const float qh = yh + ql, qe = ql - (qh - yh);
-  // times the table's entry
-  const float2 t = table[k & (kTable - 1)];
-  const float m = t.x * qh;
-  const float ml = fmaf(t.x, qh, -m) + fmaf(t.x, qe, fmaf(t.y, qh, t.y));
-  const float s = t.x + m;
-  // s + sl in units of 2^-43, s in [0.99, 2.01): s + 4 is a multiple of 2^-21, what is left, below
-  // 2^-21 with sl, and 1.5 * 2^-20 one of 2^-43
-  const float high = s + 4.0f;
-  const float low = (s - (high - 4.0f)) + ((m - (s - t.x)) + ml) + 0x1.8p-20f;
-  const int64_t fixed = (static_cast<int64_t>(__float_as_int(high) - 0x40800000) << (kUnit - 21)) +
-                        (__float_as_int(low) - 0x35C00000);
-  const int shift = -(k >> 8);  // 0 .. 46
-  const uint64_t w = static_cast<uint64_t>((fixed + ((1ll << shift) >> 1)) >> shift);
-  // (no branch before: four of these run side by side.  An infinite top's difference is NaN.)
-  return l == c.top ? 1ull << kUnit : exponent > -46.0f ? w : 0;
+  const float2 kb = fma_f32x2(p, both(-256.0f), both(0x1.8p23f));
+  const float2 r = fma_f32x2(add_f32x2(kb, both(-0x1.8p23f)), both(0x1p-8f), p);
+  // y = pe ln 2 - r ln 2 as yh + yl, then e^y - 1 as qh + qe
+  constexpr float kLn2 = 0x1.62e43p-1f, kLn2Low = -0x1.05c61p-29f;
+  const float2 yh = mul_f32x2(r, both(-kLn2)), ny = mul_f32x2(r, both(kLn2));
+  const float2 yl = fma_f32x2(pe, both(kLn2), fma_f32x2(r, both(-kLn2Low), fma_f32x2(r, both(-kLn2), ny)));
+  const float2 c2 = fma_f32x2(ny, fma_f32x2(ny, both(1.0f / 24.0f), both(-1.0f / 6.0f)), both(0.5f));
+  const float2 ql = fma_f32x2(yl, yh, fma_f32x2(mul_f32x2(ny, ny), c2, yl));
+  const float2 qh = add_f32x2(yh, ql), qe = minus(ql, minus(qh, yh));
+  // times the table's entry: s + sl, s in [0.99, 2.01), |sl| < 2^-22
+  const uint32_t k0 = __float_as_uint(kb.x), k1 = __float_as_uint(kb.y);
+  const float2 t0 = table[k0 & (kTable - 1)], t1 = table[k1 & (kTable - 1)];
+  const float2 th = make_float2(t0.x, t1.x), tl = make_float2(t0.y, t1.y);
+  const float2 m = mul_f32x2(th, qh), me = fma_f32x2(th, qh, mul_f32x2(m, both(-1.0f)));
+  const float2 s = add_f32x2(th, m);
+  const float2 sl = add_f32x2(minus(m, minus(s, th)), add_f32x2(fma_f32x2(th, qe, fma_f32x2(tl, qh, tl)), me));
+  // times 2^(k / 256, rounded down)
+  const float2 f = make_float2(some[0] ? __uint_as_float((k0 >> 8 << 23) + 0x3F800000u) : 0.0f,
+                               some[1] ? __uint_as_float((k1 >> 8 << 23) + 0x3F800000u) : 0.0f);
+  const float2 v = mul_f32x2(s, f), vl = mul_f32x2(sl, f);
+  // in units of 2^-43: v + 4 is a multiple of 2^-21, what is left, below 2^-21 with vl, and
+  // 1.5 * 2^-20 one of 2^-43
+  const float2 high = add_f32x2(v, both(4.0f));
+  const float2 low = add_f32x2(add_f32x2(minus(v, add_f32x2(high, both(-4.0f))), vl), both(0x1.8p-20f));
+  w[0] = (static_cast<uint64_t>(__float_as_uint(high.x) - 0x40800000u) << (kUnit - 21)) +
+         static_cast<int64_t>(__float_as_int(low.x) - 0x35C00000);
+  w[1] = (static_cast<uint64_t>(__float_as_uint(high.y) - 0x40800000u) << (kUnit - 21)) +
+         static_cast<int64_t>(__float_as_int(low.y) - 0x35C00000);
 }
 
 // floor(f * n) for f in [0, 1) (the nearest inside, if it is outside) and n < 2^63.
@@ -250,7 +266,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   float limit = -INFINITY;
   int limit_last = -1;
   auto kept = [&](float l, int i) { return l > limit || (l == limit && base + i <= limit_last); };
-  auto weight = [&](float l) { return weight_of(l, scale, sh.table); };
+  const bool endless = top == INFINITY;  // (then those equal to it have all the weight)
+  auto weight = [&](float l) {
+    uint64_t w[2];
+    const bool in[2] = {true, false};
+    weights_of(both(l), scale, sh.table, in, w);
+    return endless ? (l == top ? 1ull << kUnit : 0) : w[0];
+  };
   // f(logit, place in the slice) for each of the warp's segment
   auto each = [&](auto &&f) {
 #pragma unroll 2
@@ -260,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
   };
   // f(weight, logit): the same with the weights of those that are kept (0 for the others), four
-  // computed at once; a warp goes past four by 32 of which it keeps none
+  // computed side by side; a warp goes past four by 32 of which it keeps none
   auto each_weight = [&](auto &&f) {
     for (int i = from + lane * 4; i < from + segment; i += 128) {
       const float4 x = *reinterpret_cast<const float4 *>(logits + i);
@@ -269,11 +291,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int j = 0; j < 4; ++j) in[j] = kept(v[j], i + j);
       if (!__any_sync(0xFFFFFFFFu, in[0] || in[1] || in[2] || in[3])) continue;
-      uint64_t w[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) w[j] = weight(v[j]);
+      for (int j = 0; j < 4; j += 2) {
+        uint64_t w[2];
+        const bool pair[2] = {in[j], in[j + 1]};
+        weights_of(make_float2(v[j], v[j + 1]), scale, sh.table, pair, w);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) f(in[j] ? w[j] : 0, v[j]);
+        for (int k = 0; k < 2; ++k)
+          f(endless ? (v[j + k] == top && pair[k] ? 1ull << kUnit : 0) : w[k], v[j + k]);
+      }
     }
   };
 
