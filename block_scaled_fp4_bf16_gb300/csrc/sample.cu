@@ -21,8 +21,11 @@ constexpr int kWarps = 16, kThreads = kWarps * 32;
 constexpr int kMaxCtas = 16;
 constexpr int kUnit = 43;  // weights are in units of 2^-43
 constexpr int kTable = 256;
-constexpr int kBins = 1024;    // the last one: weights that are 0
-constexpr float kSpan = 45.0f; // powers of two that the others cover
+constexpr int kBins = 1024;    // the last one: all lower logits
+// Powers of two that the other bins cover: first those where a threshold lies mostly (then few
+// logits need an atomic addition), else all weights above 0.
+constexpr float kSpan = 16.0f, kWholeSpan = 45.0f;
+constexpr int kFew = 64;       // entries that are compared with one another at once
 constexpr int kList = 1024;    // logits of a bin that one CTA takes
 constexpr int kLimb = 15;      // bits of a weight that one 32-bit sum takes of a CTA's 2^15
 constexpr int kLimbs = 3;
@@ -305,13 +308,20 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   // Bins of equal width in the exponent, in descending order of the logits (a logit's bin is a
   // monotonous function of it, in binary32 too).
-  const float per_bin = scale.hi * ((kBins - 1) / kSpan);
+  float per_bin = 0.0f;
+  auto set_span = [&](float span) { per_bin = scale.hi * ((kBins - 1) / span); };
+  const float narrow = scale.hi * ((kBins - 1) / kSpan);
   auto place_of = [&](float l) {
     const float x = l == top ? 0.0f : (top - l) * per_bin;
     return x < static_cast<float>(kBins - 1) ? x : static_cast<float>(kBins - 1);
   };
   // (to the nearest whole number: the sum with 2^23 ends in it)
   auto bin_of = [&](float l) { return __float_as_int(place_of(l) + 0x1p23f) - 0x4B000000; };
+  // Logits below are in the last bin (with room for the roundings; others may be, too).
+  auto far_end = [&] {
+    const float width = static_cast<float>(kBins) / per_bin;
+    return top - width - (fabsf(top) + width) * 0x1p-20f;
+  };
   // the same within a bin (binary32 has 14 bits and more left there)
   auto bin_within = [&](float l, int bin) {
     const float x = (place_of(l) - static_cast<float>(bin) + 0.5f) * static_cast<float>(kBins - 1);
@@ -395,7 +405,12 @@ __global__ void __launch_bounds__(kThreads, 2)
   // number (weights) comes to at least `want`, which the whole bin does.
   auto cut = [&](int bin, uint64_t want, bool weights) {
     int within = -1;  // a bin of the bin, if not -1
+    // logits outside of these are in other bins (with room for the roundings; NaN lets all through)
+    const float slack = (fabsf(top) + static_cast<float>(bin + 1) / per_bin) * 0x1p-20f;
+    const float low_end = top - (static_cast<float>(bin) + 0.5f) / per_bin - slack;
+    const float high_end = top - (static_cast<float>(bin) - 0.5f) / per_bin + slack;
     auto belongs = [&](float l, int i) {
+      if (l < low_end || l > high_end) return false;
       return kept(l, i) && bin_of(l) == bin && (within < 0 || bin_within(l, bin) == within);
     };
     // how many there are; if not above kList, all of them in the first CTA's list (each CTA's own
@@ -456,28 +471,36 @@ __global__ void __launch_bounds__(kThreads, 2)
         auto size_of = [&](uint64_t entry) {
           return weights ? weight(key_logit(static_cast<uint32_t>(entry >> 32))) : 1ull;
         };
-        for (int i = threadIdx.x; i < kBins; i += kThreads) sh.totals[i] = 0;
-        if (threadIdx.x == 0) sh.listed = 0;
-        __syncthreads();
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads)
-          atomicAdd(reinterpret_cast<unsigned long long *>(&sh.totals[within_of(sh.list[i])]), size_of(sh.list[i]));
-        __syncthreads();
-        Two t;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) t.of[e] = sh.totals[2 * threadIdx.x + e];
-        uint64_t all;
-        t.before = scan(t.of[0] + t.of[1], all) - t.of[0] - t.of[1];
-        find_bin(t, want);
-        const int third = sh.piece;
-        const uint64_t rest = sh.found[1];
         uint64_t *const sizes = mine + kList;
         static_assert(sizeof(sh.bins) >= 2 * kList * sizeof(uint64_t), "entries and weights in the bins' place");
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads)
-          if (within_of(sh.list[i]) == third) {
-            const uint32_t to = atomicAdd(&sh.listed, 1u);
-            mine[to] = sh.list[i];
-            sizes[to] = size_of(sh.list[i]);
+        if (threadIdx.x == 0) sh.listed = n <= kFew ? n : 0;
+        uint64_t rest = want;
+        if (n <= kFew) {
+          if (threadIdx.x < n) {
+            mine[threadIdx.x] = sh.list[threadIdx.x];
+            sizes[threadIdx.x] = size_of(sh.list[threadIdx.x]);
           }
+        } else {
+          for (int i = threadIdx.x; i < kBins; i += kThreads) sh.totals[i] = 0;
+          __syncthreads();
+          for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sh.totals[within_of(sh.list[i])]), size_of(sh.list[i]));
+          __syncthreads();
+          Two t;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) t.of[e] = sh.totals[2 * threadIdx.x + e];
+          uint64_t all;
+          t.before = scan(t.of[0] + t.of[1], all) - t.of[0] - t.of[1];
+          find_bin(t, want);
+          const int third = sh.piece;
+          rest = sh.found[1];
+          for (uint32_t i = threadIdx.x; i < n; i += kThreads)
+            if (within_of(sh.list[i]) == third) {
+              const uint32_t to = atomicAdd(&sh.listed, 1u);
+              mine[to] = sh.list[i];
+              sizes[to] = size_of(sh.list[i]);
+            }
+        }
         __syncthreads();
         const uint32_t m = sh.listed;
         for (uint32_t i = threadIdx.x; i < m; i += kThreads) {
@@ -579,32 +602,60 @@ __global__ void __launch_bounds__(kThreads, 2)
     limit_last = static_cast<int>(sh.found[0]);
   };
 
+  bool dirty = false;
   if (top_k < a.vocab) {
-    each([&](float l, int) {
-      if (l > -INFINITY) atomicAdd(&sh.bins[0][bin_of(l)], 1u);
-    });
-    uint64_t all;
-    find_bin(scan_bins(false, all), static_cast<uint64_t>(top_k));
+    set_span(kSpan);
+    for (;;) {
+      if (dirty) clear_bins();
+      dirty = true;
+      uint32_t others = 0;
+      each([&](float l, int) {
+        const int bin = l < far_end() ? kBins - 1 : bin_of(l);
+        if (bin < kBins - 1)
+          atomicAdd(&sh.bins[0][bin], 1u);
+        else
+          others += l > -INFINITY;
+      });
+      others = __reduce_add_sync(0xFFFFFFFFu, others);
+      if (lane == 0) atomicAdd(&sh.bins[0][kBins - 1], others);
+      uint64_t all;
+      const Two bins = scan_bins(false, all);
+      find_bin(bins, static_cast<uint64_t>(top_k));
+      if (sh.piece < kBins - 1 || per_bin != narrow || all <= static_cast<uint64_t>(top_k)) break;
+      set_span(kWholeSpan);
+    }
     // (the k-th in the last bin, or less than k in all: what is cut off weighs nothing)
     if (sh.piece < kBins - 1) cut(sh.piece, sh.found[1], false);
   }
   if (top_p < 1.0f) {
-    if (top_k < a.vocab) clear_bins();
-    each_weight([&](uint64_t w, float l) {
-      if (w != 0) add_weight(bin_of(l), w);
-    });
-    uint64_t all;
-    const Two bins = scan_bins(true, all);
-    uint64_t want = part_of(top_p, all);  // the least whole number that is not below top_p * all
-    {
+    set_span(kSpan);
+    uint64_t all = 0, want = 0;
+    for (;;) {
+      if (dirty) clear_bins();
+      dirty = true;
+      uint64_t others = 0;
+      each_weight([&](uint64_t w, float l) {
+        if (w == 0) return;
+        const int bin = l < far_end() ? kBins - 1 : bin_of(l);
+        if (bin < kBins - 1)
+          add_weight(bin, w);
+        else
+          others += w;
+      });
+      others = warp_total(others);
+      if (lane == 0 && others != 0) add_weight(kBins - 1, others);
+      const Two bins = scan_bins(true, all);
+      want = part_of(top_p, all);  // the least whole number that is not below top_p * all
       const uint32_t b = __float_as_uint(top_p);
       const uint64_t m = (b & 0x7FFFFFu) | ((b >> 23) ? 0x800000u : 0u);
       const int shift = 150 - max(static_cast<int>(b >> 23), 1);
       const bool whole = top_p <= 0.0f || (shift < 64 && ((m * all) & ((1ull << shift) - 1)) == 0);
       if (!whole) ++want;
+      if (want < 1) want = 1;
+      find_bin(bins, want);
+      if (sh.piece < kBins - 1 || per_bin != narrow) break;
+      set_span(kWholeSpan);
     }
-    if (want < 1) want = 1;
-    find_bin(bins, want);
     cut(sh.piece, sh.found[1], true);
   }
   const uint64_t floor_weight =
@@ -618,7 +669,41 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the kept weights in the order of the indexes: by warps' segments, then within the one that
   // has the place, by all the CTA's warps
   uint64_t mine = 0;
-  each_weight([&](uint64_t w, float) { mine += w >= floor_weight ? w : 0; });
+  if (limit == -INFINITY) {
+    each_weight([&](uint64_t w, float) { mine += w >= floor_weight ? w : 0; });
+  } else {
+    // those that are kept side by side (in the bins' place), so that the rest cost no weights
+    __syncthreads();
+    float *const dense = reinterpret_cast<float *>(&sh.bins[0][0]) + warp * 256;
+    static_assert(sizeof(sh.bins) >= kWarps * 256 * sizeof(float), "each warp's kept logits in the bins' place");
+    int n = 0;
+    auto take = [&](int first, int count) {
+      __syncwarp();
+      const bool in[2] = {2 * lane < count, 2 * lane + 1 < count};
+      const float2 l = make_float2(in[0] ? dense[first + 2 * lane] : top, in[1] ? dense[first + 2 * lane + 1] : top);
+      uint64_t w[2];
+      weights_of(l, scale, sh.table, in, w);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (endless) w[e] = in[e] && (e == 0 ? l.x : l.y) == top ? 1ull << kUnit : 0;
+        mine += w[e] >= floor_weight ? w[e] : 0;
+      }
+      __syncwarp();
+    };
+    for (int i = from + lane * 4; i < from + segment; i += 128) {
+      const float4 x = *reinterpret_cast<const float4 *>(logits + i);
+      const float v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool in = kept(v[j], i + j);
+        const uint32_t which = __ballot_sync(0xFFFFFFFFu, in);
+        if (in) dense[n + __popc(which & ((1u << lane) - 1))] = v[j];
+        n += __popc(which);
+      }
+      while (n >= 64) n -= 64, take(n, 64);
+    }
+    if (n > 0) take(0, n);
+  }
   mine = warp_total(mine);
   __syncthreads();
   if (lane == 0) sh.sums[0][warp] = mine;
