@@ -61,7 +61,14 @@ struct Scale {
 };
 
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ float2 minus(float2 a, float2 b) { return fma_f32x2(b, both(-1.0f), a); }
+__device__ __forceinline__ float2 minus(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
+      " sub.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
 
 // round(2^43 exp((l - top) / temperature)) of two logits l <= top (finite), 0 below 2^-44 and
 // where !in.  Two at a time: a weight is some forty binary32 operations, which come in pairs.
@@ -758,10 +765,14 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <bool FP32>
 cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
+  // The CTAs of a row: at least 4096 logits each; 16 (more than may be taken for granted) for few
+  // rows, and where rows fill the GPU as few as hold a row in 16384 logits each (what a CTA
+  // does besides its logits takes 8 us; 256 x 32000: eight a row 73 us, two MANYROWS).
   int ctas = 1;
   while (ctas < 8 && ctas * 4096 < a.vocab) ctas *= 2;
-  // (few rows: more CTAs a row than may be taken for granted)
-  if (static_cast<int64_t>(a.rows) * ctas * 2 <= a.num_sms && ctas == 8 && a.vocab > 32768) ctas = kMaxCtas;
+  const int64_t rows = a.rows;
+  if (rows * ctas * 2 <= a.num_sms && ctas == 8 && a.vocab > 32768) ctas = kMaxCtas;
+  while (ctas > 1 && rows * ctas > 2 * a.num_sms && (a.vocab + ctas / 2 - 1) / (ctas / 2) <= 16384) ctas /= 2;
   constexpr int kStep = kWarps * 128;  // a warp's segment is a multiple of 128
   const int per = (a.vocab + ctas - 1) / ctas;
   const int slice = (per + kStep - 1) / kStep * kStep;
