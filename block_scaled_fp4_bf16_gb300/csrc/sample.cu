@@ -767,7 +767,7 @@ template <bool FP32>
 cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
   // The CTAs of a row: at least 4096 logits each; 16 (more than may be taken for granted) for few
   // rows, and where rows fill the GPU as few as hold a row in 16384 logits each (what a CTA
-  // does besides its logits takes 8 us; 256 x 32000: eight a row 73 us, two MANYROWS).
+  // does besides its logits takes 8 us; 256 x 32000: eight a row 73 us, two 41).
   int ctas = 1;
   while (ctas < 8 && ctas * 4096 < a.vocab) ctas *= 2;
   const int64_t rows = a.rows;
