@@ -351,7 +351,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     }
     if (threadIdx.x == 0) first[c.sequences] = static_cast<uint32_t>(before);
     if (before > kMostBlocks) {  // (uniform) nothing is seen
-      if (threadIdx.x == 0) atomicOr(c.status, kStatusIndex);
+      if (threadIdx.x == 0) atomicOr(c.status, kStatusIndexBit);
       for (int b = threadIdx.x; b <= c.sequences; b += S::kWarps * 32) first[b] = 0;
     }
     if (threadIdx.x < 2 * S::kWarps) infos[threadIdx.x >> 1][threadIdx.x & 1].valid = 0;
@@ -410,7 +410,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     auto copy_next = [&](int stage, Ahead &x) {
       if (left > 0) {
         x.held = next_page >= 0 && next_page < c.pages;
-        if (!x.held && lane == 0) atomicOr(c.status, kStatusIndex);
+        if (!x.held && lane == 0) atomicOr(c.status, kStatusIndexBit);
         const int64_t block = x.held ? (static_cast<int64_t>(next_page) * c.heads + next.h) * plan.blocks_per_page + next_in_page : 0;
         const int t0 = (next_start / kCacheBlock + next.block) * kCacheBlock;
         const uint8_t *const from_k = c.codes[0] + block * (kCacheBlock * DIM) + lane * 16;

@@ -6,6 +6,10 @@
 
 namespace mx {
 
+// Bit of the device status word set when a page, length or row number in device memory was
+// out of range (and was skipped).
+constexpr uint32_t kStatusIndexBit = 4u;
+
 // Queries or keys of a layer: rows of heads, with the norm's weight.
 struct Heads {
   const uint16_t *x;   // BF16 [tokens, heads, head_dim], row stride ld

@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     for (int i = threadIdx.x; i < c.sequences; i += kThreads) {
       const int64_t s0 = a.starts[i], s1 = a.starts[i + 1];
       if (s0 < 0 || s1 < s0 || s1 > a.tokens) {
-        if (slot == 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndex);
+        if (slot == 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndexBit);
         continue;
       }
       // (starts in order make a slot that of one sequence; out of order, the first one takes it)

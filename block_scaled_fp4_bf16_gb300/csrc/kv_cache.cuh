@@ -11,7 +11,7 @@ __device__ __forceinline__ int64_t cache_length(const CacheArgs &c, int b) {
   const int64_t n = in_bounds(b, 1, c.sequences, c.status) ? c.lengths[b] : 0;
   const int64_t most = c.max_pages * c.page_tokens;
   if (n < 0 || n > most) {
-    atomicOr(c.status, kStatusIndex);
+    atomicOr(c.status, kStatusIndexBit);
     return n < 0 ? 0 : most;
   }
   return n;
@@ -24,7 +24,7 @@ __device__ __forceinline__ int64_t cache_page(const CacheArgs &c, int b, int64_t
   if (!in_bounds(at, 1, c.sequences * c.max_pages, c.status)) return -1;
   const int64_t page = c.table[at];
   if (page >= 0 && page < c.pages) return page;
-  atomicOr(c.status, kStatusIndex);
+  atomicOr(c.status, kStatusIndexBit);
   return -1;
 }
 

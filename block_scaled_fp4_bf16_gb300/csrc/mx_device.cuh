@@ -15,8 +15,6 @@ namespace mx {
 constexpr uint32_t kStatusTimeout = kStatusTimeoutBit;
 // Bit recorded by the bounds-checked build for an access outside its buffer.
 constexpr uint32_t kStatusBounds = kStatusBoundsBit;
-// Bit recorded for an index in device memory that is out of range.
-constexpr uint32_t kStatusIndex = kStatusIndexBit;
 // Longest a kernel waits on one barrier phase before it gives up.
 constexpr uint64_t kWaitTimeoutNs = 2000000000ull;
 // Bound on the clean-up waits after an abort.
@@ -552,15 +550,6 @@ __device__ __forceinline__ float2 fma_f32x2(float2 a, float2 b, float2 c) {
       " mov.b64 rc, {%6, %7};\n fma.rn.f32x2 rd, ra, rb, rc;\n mov.b64 {%0, %1}, rd;\n}\n"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
-__device__ __forceinline__ float2 add_f32x2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 ra, rb, rd;\n mov.b64 ra, {%2, %3};\n mov.b64 rb, {%4, %5};\n"
-      " add.rn.f32x2 rd, ra, rb;\n mov.b64 {%0, %1}, rd;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
 

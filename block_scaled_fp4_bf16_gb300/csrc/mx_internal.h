@@ -40,9 +40,6 @@ constexpr uint32_t kStatusTimeoutBit = 1u;
 // Bit set by the library built with -DMX_BOUNDS_CHECK when a kernel found a
 // global access outside its buffer (and skipped it).
 constexpr uint32_t kStatusBoundsBit = 2u;
-// Bit set when a page, length or row number in device memory was out of range
-// (and was skipped).
-constexpr uint32_t kStatusIndexBit = 4u;
 
 struct QuantizeArgs {
   const void *x;
