@@ -33,7 +33,6 @@ namespace mx {
 namespace {
 
 constexpr int kMaxSms = 160;
-constexpr int kMaxWarps = 16;
 constexpr int64_t kMostBlocks = int64_t(1) << 31;  // of all sequences
 constexpr int kJoinThreads = 128;
 constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14: 2^-28 of it is still exact to 2^-11
@@ -870,7 +869,6 @@ int64_t part_rows_of(int64_t rows) { return rows < tile_rows_of(rows) ? rows : t
 template <int DIM, int NT>
 cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   using S = Shape<DIM, NT>;
-  static_assert(S::kWarps <= kMaxWarps, "workspace");
   Plan plan;
   plan.group = a.q_heads / a.c.heads;
   plan.rows = plan.group * a.q_tokens;
@@ -909,7 +907,11 @@ cudaError_t launch_rows(const AttentionArgs &a, cudaStream_t s) {
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t rows, int head_dim) {
-  const int64_t parts = 2 * kMaxSms * (1 + kMaxWarps);
+  const int nt = tile_rows_of(rows) / 8;
+  const int warps = head_dim == 64    ? (nt == 1 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps)
+                    : head_dim == 128 ? (nt == 1 ? Shape<128, 1>::kWarps : Shape<128, 2>::kWarps)
+                                      : (nt == 1 ? Shape<256, 1>::kWarps : Shape<256, 2>::kWarps);
+  const int64_t parts = 2 * kMaxSms * (1 + warps);  // of the CTAs and of their warps
   return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows), head_dim)) * sizeof(float);
 }
 

@@ -588,7 +588,8 @@ int mx_qk_norm_rope_backward_bf16(const void *q, int64_t ld_q, const void *k, in
  *   code  at ((p * kv_heads + h) * page_tokens + t) * head_dim + d,
  *   scale at (p * kv_heads + h) * (page_tokens / 32) + t / 32.
  * A sequence's token i is token i % page_tokens of the page page_table[i / page_tokens].
- * Nothing needs to start at any value. */
+ * Nothing needs to start at any value.  Scale bytes are 0..254 (255, NaN in UE8M0, is never
+ * written; a row that sees one gets unspecified numbers). */
 typedef struct mx_kv_cache {
   void *k_codes, *k_scales, *v_codes, *v_scales; /* device */
   int64_t pages;       /* of the pool                                           */
@@ -645,10 +646,11 @@ size_t mx_attention_workspace_bytes(int64_t sequences, int64_t q_tokens, int64_t
  * Tokens on a page that is not 0..pages - 1 are not seen, a length above max_pages *
  * page_tokens counts as that, one below 0 as 0, and of lengths that come to more than
  * 2^36 together nothing is seen; mx_device_status then returns MX_ERR_DEVICE_INDEX.
- * Products are FP16 with binary32 sums: codes are exact in
- * FP16, q is under a power of two of its row and head (exact above 2^-29 of their
- * largest), the weights of a block of 32 tokens are rounded to FP16 relative to the
- * block's largest.  No output overlaps an input or the workspace
+ * Products are FP16 with binary32 sums: codes are exact in FP16, q is under a power of
+ * two of its row and head (exact above 2^-29 of their largest), and the weights are
+ * rounded to FP16 relative to the row's largest weight times value scale (2^-11
+ * relative, 2^-38 of that largest where they are below 2^-27 of it); their sum is not
+ * rounded.  No output overlaps an input or the workspace
  * (mx_attention_workspace_bytes(...) bytes, 16-byte aligned, contents arbitrary; one
  * call at a time may use it).  Launches two kernels. */
 int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64_t sequences,
