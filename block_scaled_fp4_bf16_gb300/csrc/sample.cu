@@ -78,10 +78,22 @@ __device__ __forceinline__ float2 minus(float2 a, float2 b) {
   return d;
 }
 
+// A weight as two binary32 numbers whose bits count units: those of `high` above 4.0's units of
+// 2^-21, those of `low` above kLowBase's units of 2^-43.  Sums of weights add the bits up.
+struct Raw {
+  float2 high, low;  // of two weights
+};
+constexpr uint32_t kHighBase = 0x40800000u, kLowBase = 0x35C00000u;  // 4.0, 1.5 * 2^-20
+__device__ __forceinline__ uint64_t units_of(uint32_t high, uint32_t low) {
+  return (static_cast<uint64_t>(high) << (kUnit - 21)) + static_cast<int64_t>(static_cast<int32_t>(low));
+}
+__device__ __forceinline__ uint64_t units_of(float high, float low) {
+  return units_of(__float_as_uint(high) - kHighBase, __float_as_uint(low) - kLowBase);
+}
+
 // round(2^43 exp((l - top) / temperature)) of two logits l <= top (finite), 0 below 2^-44 and
 // where !in.  Two at a time: a weight is some forty binary32 operations, which come in pairs.
-__device__ __forceinline__ void weights_of(float2 l, const Scale &c, const float2 *table, const bool (&in)[2],
-                                           uint64_t (&w)[2]) {
+__device__ __forceinline__ Raw weights_of(float2 l, const Scale &c, const float2 *table, const bool (&in)[2]) {
   // l - top, exactly, as d + e
   const float2 top = both(-c.top), b = minus(add_f32x2(l, top), l);
   float2 d = add_f32x2(l, top), e = add_f32x2(minus(l, minus(d, b)), minus(top, b));
@@ -117,13 +129,23 @@ __device__ __forceinline__ void weights_of(float2 l, const Scale &c, const float
   const float2 v = mul_f32x2(s, f), vl = mul_f32x2(sl, f);
   // in units of 2^-43: v + 4 is a multiple of 2^-21, what is left, below 2^-21 with vl, and
   // 1.5 * 2^-20 one of 2^-43
-  const float2 high = add_f32x2(v, both(4.0f));
-  const float2 low = add_f32x2(add_f32x2(minus(v, add_f32x2(high, both(-4.0f))), vl), both(0x1.8p-20f));
-  w[0] = (static_cast<uint64_t>(__float_as_uint(high.x) - 0x40800000u) << (kUnit - 21)) +
-         static_cast<int64_t>(__float_as_int(low.x) - 0x35C00000);
-  w[1] = (static_cast<uint64_t>(__float_as_uint(high.y) - 0x40800000u) << (kUnit - 21)) +
-         static_cast<int64_t>(__float_as_int(low.y) - 0x35C00000);
+  Raw w;
+  w.high = add_f32x2(v, both(4.0f));
+  w.low = add_f32x2(add_f32x2(minus(v, add_f32x2(w.high, both(-4.0f))), vl), both(0x1.8p-20f));
+  return w;
 }
+
+// The sum of a thread's weights: at most 64 (its part of a slice), so that 32 bits hold the
+// sums of either part's units.
+struct RawSum {
+  uint32_t high = 0, low = 0, count = 0;
+  __device__ void add(float h, float l) {
+    high += __float_as_uint(h);
+    low += __float_as_uint(l);
+    ++count;
+  }
+  __device__ uint64_t total() const { return units_of(high - count * kHighBase, low - count * kLowBase); }
+};
 
 // floor(f * n) for f in [0, 1) (the nearest inside, if it is outside) and n < 2^63.
 __device__ __forceinline__ uint64_t part_of(float f, uint64_t n) {
@@ -285,11 +307,11 @@ __global__ void __launch_bounds__(kThreads, 2)
   int limit_last = -1;
   auto kept = [&](float l, int i) { return l > limit || (l == limit && base + i <= limit_last); };
   const bool endless = top == INFINITY;  // (then those equal to it have all the weight)
-  auto weight = [&](float l) {
-    uint64_t w[2];
+  auto weight = [&](float l) -> uint64_t {
+    if (endless) return l == top ? 1ull << kUnit : 0;
     const bool in[2] = {true, false};
-    weights_of(both(l), scale, sh.table, in, w);
-    return endless ? (l == top ? 1ull << kUnit : 0) : w[0];
+    const Raw w = weights_of(both(l), scale, sh.table, in);
+    return units_of(w.high.x, w.low.x);
   };
   // f(logit, place in the slice) for each of the warp's segment
   auto each = [&](auto &&f) {
@@ -299,8 +321,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       f(v.x, i), f(v.y, i + 1), f(v.z, i + 2), f(v.w, i + 3);
     }
   };
-  // f(weight, logit): the same with the weights of those that are kept (0 for the others), four
-  // computed side by side; a warp goes past four by 32 of which it keeps none
+  // f(high, low, logit): the same with the weights (Raw) of those that are kept (0 for the others),
+  // four computed side by side; a warp goes past four by 32 of which it keeps none.  (top finite)
   auto each_weight = [&](auto &&f) {
     for (int i = from + lane * 4; i < from + segment; i += 128) {
       const float4 x = *reinterpret_cast<const float4 *>(logits + i);
@@ -311,12 +333,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!__any_sync(0xFFFFFFFFu, in[0] || in[1] || in[2] || in[3])) continue;
 #pragma unroll
       for (int j = 0; j < 4; j += 2) {
-        uint64_t w[2];
         const bool pair[2] = {in[j], in[j + 1]};
-        weights_of(make_float2(v[j], v[j + 1]), scale, sh.table, pair, w);
-#pragma unroll
-        for (int k = 0; k < 2; ++k)
-          f(endless ? (v[j + k] == top && pair[k] ? 1ull << kUnit : 0) : w[k], v[j + k]);
+        const Raw w = weights_of(make_float2(v[j], v[j + 1]), scale, sh.table, pair);
+        f(w.high.x, w.low.x, v[j]);
+        f(w.high.y, w.low.y, v[j + 1]);
       }
     }
   };
@@ -624,8 +644,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (dirty) clear_bins();
       dirty = true;
       uint32_t others = 0;
+      const float far = far_end();
       each([&](float l, int) {
-        const int bin = l < far_end() ? kBins - 1 : bin_of(l);
+        const int bin = l < far ? kBins - 1 : bin_of(l);
         if (bin < kBins - 1)
           atomicAdd(&sh.bins[0][bin], 1u);
         else
@@ -649,14 +670,22 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (dirty) clear_bins();
       dirty = true;
       uint64_t others = 0;
-      each_weight([&](uint64_t w, float l) {
-        if (w == 0) return;
-        const int bin = l < far_end() ? kBins - 1 : bin_of(l);
-        if (bin < kBins - 1)
-          add_weight(bin, w);
-        else
-          others += w;
-      });
+      if (endless) {
+        each([&](float l, int i) {
+          if (kept(l, i) && l == top) add_weight(0, 1ull << kUnit);
+        });
+      } else {
+        RawSum sum;
+        const float far = far_end();
+        each_weight([&](float high, float low, float l) {
+          const int bin = l < far ? kBins - 1 : bin_of(l);
+          if (bin < kBins - 1)
+            add_weight(bin, units_of(high, low));
+          else
+            sum.add(high, low);
+        });
+        others = sum.total();
+      }
       others = warp_total(others);
       if (lane == 0 && others != 0) add_weight(kBins - 1, others);
       const Two bins = scan_bins(true, all);
@@ -684,8 +713,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   // the kept weights in the order of the indexes: by warps' segments, then within the one that
   // has the place, by all the CTA's warps
   uint64_t mine = 0;
-  if (limit == -INFINITY) {
-    each_weight([&](uint64_t w, float) { mine += w >= floor_weight ? w : 0; });
+  RawSum kept_sum;
+  auto take_weight = [&](float high, float low) {
+    if (floor_weight <= 1)
+      kept_sum.add(high, low);
+    else if (units_of(high, low) >= floor_weight)
+      mine += units_of(high, low);
+  };
+  if (endless) {
+    each([&](float l, int i) { mine += final_weight(l, i); });
+  } else if (limit == -INFINITY) {
+    each_weight([&](float high, float low, float) { take_weight(high, low); });
   } else {
     // those that are kept side by side (in the bins' place), so that the rest cost no weights
     __syncthreads();
@@ -696,13 +734,9 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       const bool in[2] = {2 * lane < count, 2 * lane + 1 < count};
       const float2 l = make_float2(in[0] ? dense[first + 2 * lane] : top, in[1] ? dense[first + 2 * lane + 1] : top);
-      uint64_t w[2];
-      weights_of(l, scale, sh.table, in, w);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (endless) w[e] = in[e] && (e == 0 ? l.x : l.y) == top ? 1ull << kUnit : 0;
-        mine += w[e] >= floor_weight ? w[e] : 0;
-      }
+      const Raw w = weights_of(l, scale, sh.table, in);
+      take_weight(w.high.x, w.low.x);
+      take_weight(w.high.y, w.low.y);
       __syncwarp();
     };
     for (int i = from + lane * 4; i < from + segment; i += 128) {
@@ -719,7 +753,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     }
     if (n > 0) take(0, n);
   }
-  mine = warp_total(mine);
+  mine = warp_total(mine + kept_sum.total());
   __syncthreads();
   if (lane == 0) sh.sums[0][warp] = mine;
   __syncthreads();
