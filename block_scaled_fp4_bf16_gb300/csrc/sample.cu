@@ -357,9 +357,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float width = static_cast<float>(kBins) / per_bin;
     return top - width - (fabsf(top) + width) * 0x1p-20f;
   };
-  // the same within a bin (binary32 has 14 bits and more left there)
-  auto bin_within = [&](float l, int bin) {
-    const float x = (place_of(l) - static_cast<float>(bin) + 0.5f) * static_cast<float>(kBins - 1);
+  // the same within a range of bins (binary32 has 14 bits and more left there)
+  auto bin_within = [&](float l, int from_bin, int to_bin) {
+    const float x = (place_of(l) - static_cast<float>(from_bin) + 0.5f) *
+                    (static_cast<float>(kBins - 1) / static_cast<float>(to_bin - from_bin + 1));
     return __float_as_int(x + 0x1p23f) - 0x4B000000;
   };
   auto clear_bins = [&] {
@@ -436,17 +437,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
   };
 
-  // The limit such that the first in order of the kept logits in `bin` are the fewest whose
-  // number (weights) comes to at least `want`, which the whole bin does.
-  auto cut = [&](int bin, uint64_t want, bool weights) {
-    int within = -1;  // a bin of the bin, if not -1
+  // The limit such that the first in order of the kept logits in the bins first_bin .. last_bin
+  // are the fewest whose number (weights) comes to at least `want`, which all of them do.
+  auto cut = [&](int first_bin, int last_bin, uint64_t want, bool weights) {
+    int within = -1;  // a bin of the range, if not -1
     // logits outside of these are in other bins (with room for the roundings; NaN lets all through)
-    const float slack = (fabsf(top) + static_cast<float>(bin + 1) / per_bin) * 0x1p-20f;
-    const float low_end = top - (static_cast<float>(bin) + 0.5f) / per_bin - slack;
-    const float high_end = top - (static_cast<float>(bin) - 0.5f) / per_bin + slack;
+    const float slack = (fabsf(top) + static_cast<float>(last_bin + 1) / per_bin) * 0x1p-20f;
+    const float low_end = top - (static_cast<float>(last_bin) + 0.5f) / per_bin - slack;
+    const float high_end = top - (static_cast<float>(first_bin) - 0.5f) / per_bin + slack;
     auto belongs = [&](float l, int i) {
-      if (l < low_end || l > high_end) return false;
-      return kept(l, i) && bin_of(l) == bin && (within < 0 || bin_within(l, bin) == within);
+      if (l < low_end || l > high_end || !kept(l, i)) return false;
+      const int bin = bin_of(l);
+      return bin >= first_bin && bin <= last_bin && (within < 0 || bin_within(l, first_bin, last_bin) == within);
     };
     // how many there are; if not above kList, all of them in the first CTA's list (each CTA's own
     // come to its bins' memory first: nobody reads those any more)
@@ -477,14 +479,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       return n;
     };
     uint32_t n = gather();
-    if (n > kList) {  // divide the bin, too
+    if (n > kList) {  // divide the range, too
       clear_bins();
       each([&](float l, int i) {
         if (!belongs(l, i)) return;
         if (weights)
-          add_weight(bin_within(l, bin), weight(l));
+          add_weight(bin_within(l, first_bin, last_bin), weight(l));
         else
-          atomicAdd(&sh.bins[0][bin_within(l, bin)], 1u);
+          atomicAdd(&sh.bins[0][bin_within(l, first_bin, last_bin)], 1u);
       });
       uint64_t all;
       find_bin(scan_bins(weights, all), want);
@@ -499,8 +501,9 @@ __global__ void __launch_bounds__(kThreads, 2)
         // second half their weights.
         auto within_of = [&](uint64_t entry) {
           const float l = key_logit(static_cast<uint32_t>(entry >> 32));
-          if (within < 0) return bin_within(l, bin);
-          const float x = (place_of(l) - static_cast<float>(bin) + 0.5f) * static_cast<float>(kBins - 1);
+          if (within < 0) return bin_within(l, first_bin, last_bin);
+          const float x = (place_of(l) - static_cast<float>(first_bin) + 0.5f) *
+                          (static_cast<float>(kBins - 1) / static_cast<float>(last_bin - first_bin + 1));
           return __float_as_int((x - static_cast<float>(within) + 0.5f) * static_cast<float>(kBins - 1) + 0x1p23f) - 0x4B000000;
         };
         auto size_of = [&](uint64_t entry) {
@@ -639,29 +642,40 @@ __global__ void __launch_bounds__(kThreads, 2)
 
   bool dirty = false;
   if (top_k < a.vocab) {
-    set_span(kSpan);
-    for (;;) {
-      if (dirty) clear_bins();
-      dirty = true;
-      uint32_t others = 0;
-      const float far = far_end();
-      each([&](float l, int) {
-        const int bin = l < far ? kBins - 1 : bin_of(l);
-        if (bin < kBins - 1)
-          atomicAdd(&sh.bins[0][bin], 1u);
-        else
-          others += l > -INFINITY;
-      });
-      others = __reduce_add_sync(0xFFFFFFFFu, others);
-      if (lane == 0) atomicAdd(&sh.bins[0][kBins - 1], others);
-      uint64_t all;
-      const Two bins = scan_bins(false, all);
-      find_bin(bins, static_cast<uint64_t>(top_k));
-      if (sh.piece < kBins - 1 || per_bin != narrow || all <= static_cast<uint64_t>(top_k)) break;
-      set_span(kWholeSpan);
+    // The threads' largest logits first: the k-th of them is no larger than the k-th of all, and
+    // not much lower where k is well below their number, so that few logits are left above it.
+    set_span(kWholeSpan);
+    dirty = true;
+    if (high > -INFINITY) atomicAdd(&sh.bins[0][bin_of(high)], 1u);
+    uint64_t threads;
+    find_bin(scan_bins(false, threads), static_cast<uint64_t>(top_k));
+    if (sh.piece < kBins - 1) {
+      cut(0, sh.piece, static_cast<uint64_t>(top_k), false);
+    } else {
+      set_span(kSpan);
+      for (;;) {
+        if (dirty) clear_bins();
+        dirty = true;
+        uint32_t others = 0;
+        const float far = far_end();
+        each([&](float l, int) {
+          const int bin = l < far ? kBins - 1 : bin_of(l);
+          if (bin < kBins - 1)
+            atomicAdd(&sh.bins[0][bin], 1u);
+          else
+            others += l > -INFINITY;
+        });
+        others = __reduce_add_sync(0xFFFFFFFFu, others);
+        if (lane == 0) atomicAdd(&sh.bins[0][kBins - 1], others);
+        uint64_t all;
+        const Two bins = scan_bins(false, all);
+        find_bin(bins, static_cast<uint64_t>(top_k));
+        if (sh.piece < kBins - 1 || per_bin != narrow || all <= static_cast<uint64_t>(top_k)) break;
+        set_span(kWholeSpan);
+      }
+      // (the k-th in the last bin, or less than k in all: what is cut off weighs nothing)
+      if (sh.piece < kBins - 1) cut(sh.piece, sh.piece, sh.found[1], false);
     }
-    // (the k-th in the last bin, or less than k in all: what is cut off weighs nothing)
-    if (sh.piece < kBins - 1) cut(sh.piece, sh.found[1], false);
   }
   if (top_p < 1.0f) {
     set_span(kSpan);
@@ -700,7 +714,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (sh.piece < kBins - 1 || per_bin != narrow) break;
       set_span(kWholeSpan);
     }
-    cut(sh.piece, sh.found[1], true);
+    cut(sh.piece, sh.piece, sh.found[1], true);
   }
   const uint64_t floor_weight =
       min_p > 0.0f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.0f) * static_cast<float>(1ull << kUnit))) : 1;
@@ -742,6 +756,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int i = from + lane * 4; i < from + segment; i += 128) {
       const float4 x = *reinterpret_cast<const float4 *>(logits + i);
       const float v[4] = {x.x, x.y, x.z, x.w};
+      if (!__any_sync(0xFFFFFFFFu, fmaxf(fmaxf(v[0], v[1]), fmaxf(v[2], v[3])) >= limit)) continue;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const bool in = kept(v[j], i + j);
