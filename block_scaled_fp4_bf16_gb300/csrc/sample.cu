@@ -202,7 +202,7 @@ struct Shared {
 
 template <bool FP32>
 __global__ void __launch_bounds__(kThreads, 2)
-    sample_kernel(const __grid_constant__ SampleArgs a, int ctas, int slice) {
+    sample_kernel(const __grid_constant__ SampleArgs a, int ctas, int slice, int sort_rows) {
   extern __shared__ __align__(16) float logits[];  // this CTA's slice
   __shared__ Shared sh;
   cluster_arrive_relaxed();
@@ -211,7 +211,28 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int i = threadIdx.x; i < (1 + kLimbs) * kBins; i += kThreads) (&sh.bins[0][0])[i] = 0;
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = static_cast<int>(cluster_ctarank()), row = static_cast<int>(cluster_id_x());
+  const int rank = static_cast<int>(cluster_ctarank());
+  int row = static_cast<int>(cluster_id_x());
+  if (sort_rows) {
+    // Rows with top-p take twice as long as the others: where not all rows run at once, they
+    // begin first.  This cluster's row is the one of its number in that order.
+    const int i = threadIdx.x;
+    const bool in = i < a.rows, slow = in && a.top_p[i] < 1.0f && (a.temperature == nullptr || a.temperature[i] > 0.0f);
+    const uint32_t slows = __ballot_sync(0xFFFFFFFFu, slow), others = __ballot_sync(0xFFFFFFFFu, in && !slow);
+    if (lane == 0) sh.sums[0][warp] = static_cast<uint64_t>(__popc(slows)) << 32 | static_cast<uint32_t>(__popc(others));
+    __syncthreads();
+    uint64_t before = 0, all = 0;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) before += sh.sums[0][w];
+      all += sh.sums[0][w];
+    }
+    const uint32_t below = (1u << lane) - 1;
+    const int place = slow ? static_cast<int>(before >> 32) + __popc(slows & below)
+                           : static_cast<int>((all >> 32) + static_cast<uint32_t>(before)) + __popc(others & below);
+    if (in && place == row) sh.piece = i;
+    __syncthreads();
+    row = sh.piece;
+  }
   const int base = rank * slice, segment = slice / kWarps, from = warp * segment;
   const int64_t extent = static_cast<int64_t>(a.rows - 1) * a.ld + a.vocab;
 
@@ -856,7 +877,8 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, sample_kernel<FP32>, a, ctas, slice);
+  const int sort_rows = a.top_p != nullptr && rows <= kThreads && rows * ctas > 2 * a.num_sms;
+  return cudaLaunchKernelEx(&cfg, sample_kernel<FP32>, a, ctas, slice, sort_rows);
 }
 
 }  // namespace

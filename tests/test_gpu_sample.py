@@ -68,6 +68,19 @@ def test_many_rows():
         top_p=rng.choice([1.0, 0.9, 0.3], rows), min_p=rng.choice([0.0, 0.05], rows), uniform=uniforms(rows))
 
 
+@pytest.mark.parametrize("rows,vocab", [(100, 40001), (512, 16001), (513, 16001)])
+def test_rows_that_do_not_all_run_at_once(rows, vocab):
+    """Rows with top-p begin first; each row's answer stays its own."""
+    rng = np.random.default_rng(rows)
+    x = normal(rows, vocab, seed=rows)
+    x[7, 3], x[9] = np.nan, -np.inf
+    t = rng.choice([0.0, 0.6, 1.2], rows)
+    t[11] = np.nan
+    run(x, temperature=t, top_k=rng.choice([0, 30, 3000], rows), top_p=rng.choice([1.0, 0.9, 0.4], rows),
+        min_p=rng.choice([0.0, 0.03], rows), uniform=uniforms(rows, rows))
+    run(x[:, :vocab], top_p=rng.choice([1.0, 0.7], rows), uniform=uniforms(rows, rows + 1))
+
+
 @pytest.mark.parametrize("uniform", [0.0, 2.0 ** -30, 0.5, 1 - 2.0 ** -24, 1.0, 2.0, -1.0])
 def test_ends_of_the_uniform_numbers(uniform):
     x = np.concatenate([normal(3, 5001, seed=6), np.full((1, 5001), 0.25)])
