@@ -2,10 +2,12 @@
 //
 //   s_t = scale * 2^(ek) q . kcode_t,   out = sum_t softmax(s)_t 2^(ev) vcode_t
 //
-// The cache's bytes bound it: each is read once for the up to 16 (query token, head) rows
-// that share a key head.  Keys, and values transposed, are the 16-row side of FP16 products
-// (16 x 8 x 16, binary32 sums) and the rows its 8 columns, so that the conversion of codes,
-// which costs more than the products, is done once for all rows and few rows waste little.
+// The cache's bytes bound it: each is read once for the 8 (query token, head) rows that share
+// a key head (16 of 64 channels; more rows make more tiles, which find it in L2).  Keys, and
+// values transposed, are the 16-row side of FP16 products (16 x 8 x 16, binary32 sums) and the
+// rows its 8 columns, so that the conversion of codes, which costs more than the products, is
+// done once for all rows and few rows waste little (the rows on the 16-row side: 165 us for 64
+// x up to 8192 tokens of 64/8 heads, where this takes 95, 0.93 of what the cache's bytes take).
 // E4M3 is exact in FP16; q enters under a power of two of its row.
 //
 // Every warp is a worker of its own: the blocks of 32 tokens of all (row tile, sequence,
@@ -16,8 +18,10 @@
 // which its sum of weights is relative, and of logit + value scale (both as powers of two), to
 // which the FP16 weights are: a weight is rounded relative to the largest contribution to the
 // output, however far the blocks' scales lie apart.  What a worker leaves unfinished goes to
-// the workspace; its CTA joins the parts of its workers, and a second, small launch those of
-// the CTAs, in their order.
+// the workspace or, at its end, in its ring; its CTA joins the parts of its workers, and a
+// second, small launch those of the CTAs, in their order (all by the second launch: 1 x 131072
+// of 32/4 heads 82 us, so 33, of which the cache takes 20, what precedes the first block 5, and
+// the joins 7).
 //
 // Layouts: the order of channels in a product is free, so lane (g, t) = (lane / 4, lane % 4)
 // takes 16 consecutive bytes of keys g and g + 8 as four k-steps, and the queries are laid out
@@ -41,17 +45,15 @@ constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14: 2^-28 of it is s
 template <int DIM, int NT>
 struct Shape {
   static constexpr int kRows = 8 * NT;
-  // registers: DIM / 8 * NT sums and, in registers or shared memory, half as many for queries
-  static constexpr int kWarps = DIM == 64 ? (NT == 1 ? 16 : 12) : DIM == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 6 : 4);
-  static constexpr int kStages = DIM == 64 ? (NT == 1 ? 3 : 4) : DIM == 128 && NT == 2 ? 3 : 2;
+  // (registers: DIM / 4 * NT sums and half as many of queries a lane)
+  static constexpr int kWarps = DIM == 64 ? (NT == 1 ? 16 : 12) : DIM == 128 ? 12 : 6;
+  static constexpr int kStages = DIM == 64 ? (NT == 1 ? 3 : 4) : 2;
   static constexpr int kBlockBytes = 2 * kCacheBlock * DIM;  // keys, values
   static constexpr int kRing = kBlockBytes * kStages;
   static constexpr int kSteps = DIM / 16;    // k-steps of q . k
   static constexpr int kChunks = DIM / 64;   // 16-byte pieces of a key that a lane reads
   static constexpr int kRun = DIM == 64 ? 8 : 16;  // channels of a value that a lane reads at once
   static constexpr int kRuns = DIM / 8 / kRun;
-  static constexpr bool kQueriesInShared = DIM * NT >= 512;
-  static constexpr int kQueryBytes = kQueriesInShared ? NT * kSteps * 256 : 0;
 };
 
 // A (tile, sequence, head) that a CTA begins and others go on with: the last of them (-1: none).
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
   griddep_wait();
   const CacheArgs &c = a.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  uint32_t *const first = reinterpret_cast<uint32_t *>(smem + S::kWarps * (S::kRing + S::kQueryBytes));
+  uint32_t *const first = reinterpret_cast<uint32_t *>(smem + S::kWarps * S::kRing);
 
   // blocks before each sequence
   {
@@ -372,7 +374,6 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
 
   if (begin < end) {
     const uint32_t ring = smem_u32(smem) + warp * S::kRing;
-    [[maybe_unused]] const uint32_t query_at = smem_u32(smem) + S::kWarps * S::kRing + warp * S::kQueryBytes;
     const int64_t block_extent = c.pages * c.heads * static_cast<int64_t>(plan.blocks_per_page);
 
     // ---- copies, kStages - 1 blocks ahead.  next_*: the block to be copied next.
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     float out[NT][DIM / 16][4];  // [..][..][2 e + r]: channels 2 i + e of the lane's, rows 2 t + r
     float top[NT][2], ref[NT][2], weight[NT][2];
     float factor[NT][2];         // of a logit: scale, log2(e) and the row's power of two
-    [[maybe_unused]] uint32_t query[S::kQueriesInShared ? 1 : NT][S::kQueriesInShared ? 1 : S::kSteps][2];
+    uint32_t query[NT][S::kSteps][2];
     int length = 0, start = 0;
     bool from_start = false, fresh = true;
     int stage = 0;
@@ -509,14 +510,8 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
               const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
               const uint32_t h0 = half2_bits(__uint_as_float(w0 << 16) * f1 * f2, __uint_as_float(w0 & 0xFFFF0000u) * f1 * f2);
               const uint32_t h1 = half2_bits(__uint_as_float(w1 << 16) * f1 * f2, __uint_as_float(w1 & 0xFFFF0000u) * f1 * f2);
-              if constexpr (S::kQueriesInShared) {
-                asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(query_at + (nt * S::kSteps + i * 4 + u) * 256 + lane * 8),
-                             "r"(h0), "r"(h1)
-                             : "memory");
-              } else {
-                query[nt][i * 4 + u][0] = h0;
-                query[nt][i * 4 + u][1] = h1;
-              }
+              query[nt][i * 4 + u][0] = h0;
+              query[nt][i * 4 + u][1] = h1;
             }
 #pragma unroll
           for (int i = 0; i < DIM / 16; ++i)
@@ -543,16 +538,6 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
         for (int j = 0; j < 4; ++j) k[j] = lds128(keys + place<DIM>(8 * j + g, chunk));
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          uint32_t q[NT][2];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if constexpr (S::kQueriesInShared) {
-              const uint2 v = lds64(query_at + (nt * S::kSteps + i * 4 + u) * 256 + lane * 8);
-              q[nt][0] = v.x, q[nt][1] = v.y;
-            } else {
-              q[nt][0] = query[nt][i * 4 + u][0], q[nt][1] = query[nt][i * 4 + u][1];
-            }
-          }
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const uint4 &k0 = k[2 * j], &k1 = k[2 * j + 1];
@@ -560,7 +545,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
             half4_of(u == 0 ? k0.x : u == 1 ? k0.y : u == 2 ? k0.z : k0.w, a0, a2);
             half4_of(u == 0 ? k1.x : u == 1 ? k1.y : u == 2 ? k1.z : k1.w, a1, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt][j], a0, a1, a2, a3, q[nt][0], q[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt][j], a0, a1, a2, a3, query[nt][i * 4 + u][0], query[nt][i * 4 + u][1]);
           }
         }
       }
@@ -861,10 +846,12 @@ __global__ void __launch_bounds__(kJoinThreads)
 constexpr size_t kSplitBytes = kMaxSms * sizeof(Split);
 static_assert(kSplitBytes % 16 == 0, "alignment of the parts");
 
-// The rows of a tile: 8 where they do, else 16 (32 were slower than two tiles of 16, for lack of
-// registers: 16 x 4 x 8192 of 64/8 heads 99 us against 82, 7 x 4 x 5000 of 28/4 17.0 against 12.6).
-int tile_rows_of(int64_t rows) { return rows <= 8 ? 8 : 16; }
-int64_t part_rows_of(int64_t rows) { return rows < tile_rows_of(rows) ? rows : tile_rows_of(rows); }
+// The rows of a tile: 8, or 16 of 64 channels where there are more than 8.  A second tile reads
+// the cache again, from L2 mostly, but 16 rows take registers from as many warps (16 x 2 x 8192
+// of 64/8 heads, in tiles of 8 / of 16 rows: 128 channels 50 / 53 us, 256 110 / 116; 64 x 2 of 64
+// channels 97 / 86).
+int tile_rows_of(int64_t rows, int dim) { return rows <= 8 || dim > 64 ? 8 : 16; }
+int64_t part_rows_of(int64_t rows, int dim) { return rows < tile_rows_of(rows, dim) ? rows : tile_rows_of(rows, dim); }
 
 template <int DIM, int NT>
 cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
@@ -873,7 +860,7 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   plan.group = a.q_heads / a.c.heads;
   plan.rows = plan.group * a.q_tokens;
   plan.tiles = (plan.rows + S::kRows - 1) / S::kRows;
-  plan.part_rows = static_cast<int>(part_rows_of(plan.rows));
+  plan.part_rows = static_cast<int>(part_rows_of(plan.rows, DIM));
   plan.blocks_per_page = a.c.page_tokens / kCacheBlock;
   const int ctas = a.num_sms < kMaxSms ? a.num_sms : kMaxSms;
   plan.per_cta = S::kWarps;
@@ -881,7 +868,7 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   plan.splits = static_cast<Split *>(a.workspace);
   plan.cta_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kSplitBytes);
   plan.parts = plan.cta_parts + 2 * ctas * part_floats(plan.part_rows, DIM);
-  constexpr size_t kFixed = static_cast<size_t>(S::kWarps) * (S::kRing + S::kQueryBytes);
+  constexpr size_t kFixed = static_cast<size_t>(S::kWarps) * S::kRing;
   const size_t smem = kFixed + (static_cast<size_t>(a.c.sequences) + 1) * sizeof(uint32_t);
   const void *func = reinterpret_cast<const void *>(attention_kernel<DIM, NT>);
   if (!kernel_setup_get(func, nullptr)) {
@@ -898,28 +885,24 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
                     plan, S::kRows);
 }
 
-template <int DIM>
-cudaError_t launch_rows(const AttentionArgs &a, cudaStream_t s) {
-  const int64_t rows = static_cast<int64_t>(a.q_heads / a.c.heads) * a.q_tokens;
-  return tile_rows_of(rows) == 8 ? launch<DIM, 1>(a, s) : launch<DIM, 2>(a, s);
-}
-
 }  // namespace
 
 size_t attention_workspace_bytes(int64_t rows, int head_dim) {
-  const int nt = tile_rows_of(rows) / 8;
-  const int warps = head_dim == 64    ? (nt == 1 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps)
-                    : head_dim == 128 ? (nt == 1 ? Shape<128, 1>::kWarps : Shape<128, 2>::kWarps)
-                                      : (nt == 1 ? Shape<256, 1>::kWarps : Shape<256, 2>::kWarps);
+  const int warps = head_dim == 64    ? (tile_rows_of(rows, 64) == 8 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps)
+                    : head_dim == 128 ? Shape<128, 1>::kWarps
+                                      : Shape<256, 1>::kWarps;
   const int64_t parts = 2 * kMaxSms * (1 + warps);  // of the CTAs and of their warps
-  return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows), head_dim)) * sizeof(float);
+  return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows, head_dim), head_dim)) * sizeof(float);
 }
 
 cudaError_t launch_attention(const AttentionArgs &a, cudaStream_t s) {
   switch (a.c.head_dim) {
-    case 64: return launch_rows<64>(a, s);
-    case 128: return launch_rows<128>(a, s);
-    default: return launch_rows<256>(a, s);
+    case 64: {
+      const int64_t rows = static_cast<int64_t>(a.q_heads / a.c.heads) * a.q_tokens;
+      return tile_rows_of(rows, 64) == 8 ? launch<64, 1>(a, s) : launch<64, 2>(a, s);
+    }
+    case 128: return launch<128, 1>(a, s);
+    default: return launch<256, 1>(a, s);
   }
 }
 
