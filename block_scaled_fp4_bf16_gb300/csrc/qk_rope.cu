@@ -76,7 +76,8 @@ __device__ __forceinline__ uint4 pack(const float *v) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A part's weight in shared memory, in the lanes' order: lane j's 16 channels, four at a time.
+// A part's weight in shared memory, in the lanes' order: lane j's 16 channels, four at a time
+// (0 for a lane without channels: its terms go into its head's sums).
 struct Weights {
   float4 of[4][16];  // [four][lane j]
 };
@@ -85,10 +86,10 @@ __device__ __forceinline__ void load_weights(Weights &w, const uint16_t *weight,
     const int j = i >> 2, four = i & 3;
     const Chunks c = chunks_of(j, a);
     const int at = c.at[four >> 1] + 4 * (four & 1);
-    if (!c.in || !in_bounds(at, 4, a.head_dim, a.status)) continue;
-    float v[4];
+    float v[4] = {};
+    if (c.in && in_bounds(at, 4, a.head_dim, a.status))
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(static_cast<uint32_t>(weight[at + e]) << 16);
+      for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(static_cast<uint32_t>(weight[at + e]) << 16);
     w.of[four][j] = make_float4(v[0], v[1], v[2], v[3]);
   }
 }

@@ -210,6 +210,19 @@ def test_backward_gives_the_same_bits_again():
     assert torch.equal(one, two) and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dim, rotary", [(80, 80), (144, 64), (48, 0)])
+def test_backward_does_not_see_the_weights_of_a_call_before(dim, rotary, interleaved):
+    """A head of 5 x 16 channels leaves lanes without any: what another call left on chip stays out."""
+    c, last = Case(3000, 3, 2, dim, rotary, interleaved), Case(3000, 2, 2, 256, 256, interleaved)
+    bad = torch.full((256,), np.inf, dtype=torch.bfloat16, device="cuda")
+    last.norm = mx.qk_norm(2, 2, 256, bad, bad, last.inv_freq, 256, interleaved)
+    x, dy, dx = c.dev(c.x), c.dev(c.dy), c.buffer()
+    last_x, last_dx = last.dev(last.x), last.buffer()
+    backward(last, last_x, last_x, last_dx)
+    check_backward(c, dx, backward(c, x, dy, dx))
+
+
 def test_backward_of_no_tokens_clears_the_weights_gradients():
     c = Case(3, 2, 1, 64, 64, False)
     c.t = 0
