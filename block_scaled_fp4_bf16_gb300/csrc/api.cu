@@ -1563,6 +1563,11 @@ int cache_shape_check(const char *fn, const mx_kv_cache *c) {
                 static_cast<long long>(c->page_tokens), MX_CACHE_BLOCK);
   if (c->pages < 1 || c->pages >= (int64_t(1) << 31))
     return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: pages = %lld (1 .. 2^31 - 1)", fn, static_cast<long long>(c->pages));
+  // (page_tokens * head_dim <= 2^28, pages * kv_heads < 2^41)
+  if (c->pages * c->kv_heads > (int64_t(1) << 48) / (c->page_tokens * c->head_dim))
+    return fail(MX_ERR_UNSUPPORTED_SHAPE, "%s: %lld pages of %lld x %lld x %lld codes (2^48 in all)", fn,
+                static_cast<long long>(c->pages), static_cast<long long>(c->kv_heads),
+                static_cast<long long>(c->page_tokens), static_cast<long long>(c->head_dim));
   return MX_OK;
 }
 

@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   uint8_t *scale = c.scales[which] + base / kCacheBlock;
   const int64_t scales = c.pages * c.heads * (c.page_tokens / kCacheBlock);
   const int before = held > 0 && in_bounds(base / kCacheBlock, 1, scales, c.status) ? *scale - 127 : -127;
+  __syncwarp();  // (the scale is written at the end; a unit of several warps meets below)
 
   // magnitudes are ordered as the bits without the sign: two at a time
   uint32_t most = 0;

@@ -589,7 +589,8 @@ int mx_qk_norm_rope_backward_bf16(const void *q, int64_t ld_q, const void *k, in
  *   scale at (p * kv_heads + h) * (page_tokens / 32) + t / 32.
  * A sequence's token i is token i % page_tokens of the page page_table[i / page_tokens].
  * Nothing needs to start at any value.  Scale bytes are 0..254 (255, NaN in UE8M0, is never
- * written; a row that sees one gets unspecified numbers). */
+ * written; a row that sees one gets unspecified numbers).  Keys and values have at most
+ * 2^48 codes each. */
 typedef struct mx_kv_cache {
   void *k_codes, *k_scales, *v_codes, *v_scales; /* device */
   int64_t pages;       /* of the pool                                           */

@@ -144,6 +144,16 @@ def cache_of(a):
     return mx.mx_kv_cache(a["kc"], a["ks"], a["vc"], a["vs"], a["pages"], a["page"], a["kvh"], a["dim"])
 
 
+def test_a_cache_past_any_memory_is_refused(lib):
+    huge = dict(pages=(1 << 10) + 1, page=1 << 20, kvh=1024, dim=256)  # 2^48 codes and more: sizes stay in 64 bits
+    most = dict(pages=(1 << 31) - 1, page=1 << 20, kvh=1024, dim=256)
+    for a in (huge, most):
+        assert call_append(lib)({**APPEND, **a, "ldk": 1 << 18, "ldv": 1 << 18}) == SHAPE
+        assert call_attention(lib)({**ATTENTION, **a, "h": 1024, "ldq": 1 << 18, "ldo": 1 << 18}) == SHAPE
+        assert lib.mx_attention_workspace_bytes(4, 1, 1024, ctypes.byref(cache_of({**CACHE, **a}))) == 0
+    assert lib.mx_attention_workspace_bytes(4, 1, 1024, ctypes.byref(cache_of({**CACHE, **huge, "pages": 1 << 10}))) > 0
+
+
 APPEND = dict(CALL, k=FAKE, ldk=256, v=FAKE + MB, ldv=256, t=8, starts=FAKE + 2 * MB)
 
 
