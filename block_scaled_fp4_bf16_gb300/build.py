@@ -23,7 +23,7 @@ SOURCES = ["api.cu", "quantize.cu", "gemm.cu", "gemm_pair.cu", "gemm_swap.cu", "
            "calibrate.cu", "transpose.cu", "linear.cu", "linear_mma.cu", "moe.cu",
            "moe_mma.cu", "qk_rope.cu", "kv_append.cu", "attention.cu", "sample.cu"]
 HEADERS = ["mx_device.cuh", "mx_internal.h", "few_tokens.h", "few_tokens.cuh", "fp4_digits.cuh",
-           "moe_groups.cuh", "decode.h", "kv_cache.cuh"]
+           "moe_groups.cuh", "decode.h", "kv_cache.cuh", "async_copy.cuh"]
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH_FLAGS + [

@@ -31,6 +31,7 @@
 // load free of conflicts.
 #include <cuda_fp16.h>
 
+#include "async_copy.cuh"
 #include "kv_cache.cuh"
 
 namespace mx {
@@ -99,29 +100,6 @@ __device__ __forceinline__ int blocks_of(const AttentionArgs &a, int length) {
 }
 __device__ __forceinline__ int length_of(const AttentionArgs &a, int b) {
   return static_cast<int>(cache_length(a.c, b));  // (lengths are 32-bit numbers)
-}
-
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool in) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
 }
 
 // Where 16-byte piece `chunk` of row `row` lies in a block's shared memory.
