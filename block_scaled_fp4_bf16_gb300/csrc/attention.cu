@@ -7,7 +7,7 @@
 // values transposed, are the 16-row side of FP16 products (16 x 8 x 16, binary32 sums) and the
 // rows its 8 columns, so that the conversion of codes, which costs more than the products, is
 // done once for all rows and few rows waste little (the rows on the 16-row side: 165 us for 64
-// x up to 8192 tokens of 64/8 heads, where this takes 95, 0.93 of what the cache's bytes take).
+// x up to 8192 tokens of 64/8 heads, where this takes 94; the cache's bytes take 88).
 // E4M3 is exact in FP16; q enters under a power of two of its row.
 //
 // Every warp is a worker of its own: the blocks of 32 tokens of all (row tile, sequence,
@@ -20,7 +20,7 @@
 // output, however far the blocks' scales lie apart.  What a worker leaves unfinished goes to
 // the workspace or, at its end, in its ring; its CTA joins the parts of its workers, and a
 // second, small launch those of the CTAs, in their order (all by the second launch: 1 x 131072
-// of 32/4 heads 82 us, so 33, of which the cache takes 20, what precedes the first block 5, and
+// of 32/4 heads 82 us, so 31, of which the cache takes 20, what precedes the first block 4, and
 // the joins 7).
 //
 // Layouts: the order of channels in a product is free, so lane (g, t) = (lane / 4, lane % 4)
@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kMaxSms = 160;
 constexpr int64_t kMostBlocks = int64_t(1) << 31;  // of all sequences
-constexpr int kJoinThreads = 128;
+template <int DIM>
+constexpr int kJoinThreads = DIM == 256 ? 256 : 128;
 constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14: 2^-28 of it is still exact to 2^-11
 
 // NT: columns of the products in eights, the rows of a tile.
@@ -789,36 +790,95 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
   }
 }
 
-// Joins the CTAs' parts of a row: CTA (x, y, z) channels 64 z .. 64 z + 63 of row y of what CTA x
-// of the launch before began and left unfinished.  Groups of 16 threads take every so many-th
-// part.
+// Joins the CTAs' parts of a row: CTA (x, y) row y of what CTA x of the launch before began and
+// left unfinished.  Groups of a row's DIM / 4 threads take every so many-th part's sums; where
+// that is more than one, each warp takes the parts' states first, so that all loads of a thread go out
+// together (1 x 131072 of 32/4 heads 32.2 us with a state before each part's sums, so 31.1).
 template <int DIM>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads<DIM>)
     join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan, int tile_rows) {
-  constexpr int kSlice = 64, kGroups = kJoinThreads / (kSlice / 4);
-  __shared__ __align__(16) float sums[kGroups][kSlice];
-  __shared__ float states[kGroups][3];
+  constexpr int kThreads = kJoinThreads<DIM>, kLanes = DIM / 4, kGroups = kThreads / kLanes, kAhead = 6;
+  constexpr int kOwn = (kMaxSms + 31) / 32;  // states of a lane: each warp takes all of them for itself
+  __shared__ __align__(16) float sums[kGroups][DIM];
+  __shared__ float states[kGroups][3], factors[kThreads / 32][kOwn * 32];
   griddep_launch_dependents();
   griddep_wait();
-  const int p0 = blockIdx.x, pr = blockIdx.y;
+  const int p0 = blockIdx.x, pr = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const Split split = plan.splits[p0];
   if (split.last_cta < 0) return;
   const int row = split.tile * tile_rows + pr;
   if (row >= plan.rows) return;
-  const int group = threadIdx.x / (kSlice / 4), d = threadIdx.x % (kSlice / 4) * 4;
-  const int n = split.last_cta - p0 + 1, mine = n > group ? (n - group + kGroups - 1) / kGroups : 0;
+  const int group = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+  const int n = split.last_cta - p0 + 1;  // (at most as many as CTAs)
   // (the first CTA's part begins the row, the others' go on with it)
   const auto part = [&](int k) {
-    const int64_t p = p0 + group + static_cast<int64_t>(k) * kGroups;
-    return part_at(plan.cta_parts + (p * 2 + (p == p0)) * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
+    const int64_t p = p0 + k;
+    return part_at(plan.cta_parts + (p * 2 + (k == 0)) * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
   };
-  Joined j = join(mine, part, pr, blockIdx.z * kSlice + d, DIM);
-  put_part(Part{sums[group], states[group], 1}, 0, d, kSlice, j);
+  if (n <= kGroups) {
+    const Joined own = join(group < n, [&](int) { return part(group); }, pr, d, DIM);
+    put_part(Part{sums[group], states[group], 1}, 0, d, DIM, own);
+    __syncthreads();
+    if (group != 0) return;
+    const Joined j = join(n, [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, DIM);
+    finish(a, plan, split.b, split.h, row, d, DIM, j.v, factors_of(j.top, j.ref, j.weight), j.top, j.weight);
+    return;
+  }
+  const auto load = [&](int k) {
+    return k < n ? *reinterpret_cast<const float4 *>(part(k).sums + pr * DIM + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  };
+  float4 x[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) x[i] = load(group + i * kGroups);
+  float top[kOwn], ref[kOwn], weight[kOwn], all_top = -INFINITY, all_ref = -INFINITY, all_weight = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int k = lane + i * 32;
+    top[i] = ref[i] = -INFINITY;
+    weight[i] = 0.0f;
+    if (k < n) {
+      const Part p = part(k);
+      top[i] = p.state[pr], ref[i] = p.state[p.rows + pr], weight[i] = p.state[2 * p.rows + pr];
+    }
+    all_top = fmaxf(all_top, top[i]);
+    all_ref = fmaxf(all_ref, ref[i]);
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) {
+    all_top = fmaxf(all_top, __shfl_xor_sync(0xFFFFFFFFu, all_top, m));
+    all_ref = fmaxf(all_ref, __shfl_xor_sync(0xFFFFFFFFu, all_ref, m));
+  }
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    if (i * 32 >= n) break;
+    factors[warp][lane + i * 32] = exp2_approx(ref[i] - base_of_max(all_ref));
+    all_weight += weight[i] * exp2_approx(top[i] - base_of_max(all_top));
+  }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) all_weight += __shfl_xor_sync(0xFFFFFFFFu, all_weight, m);
+  __syncwarp();
+  float v[4] = {};
+  const auto add = [&](int k, const float4 &y) {
+    const float f = k < n ? factors[warp][k] : 0.0f;
+    v[0] += y.x * f, v[1] += y.y * f, v[2] += y.z * f, v[3] += y.w * f;
+  };
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) add(group + i * kGroups, x[i]);
+  for (int k0 = group + kAhead * kGroups; k0 < n; k0 += kAhead * kGroups) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) x[i] = load(k0 + i * kGroups);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) add(k0 + i * kGroups, x[i]);
+  }
+  *reinterpret_cast<float4 *>(&sums[group][d]) = make_float4(v[0], v[1], v[2], v[3]);
   __syncthreads();
   if (group != 0) return;
-  j = join(min(n, kGroups), [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, kSlice);
-  finish(a, plan, split.b, split.h, row, blockIdx.z * kSlice + d, DIM, j.v, factors_of(j.top, j.ref, j.weight), j.top,
-         j.weight);
+#pragma unroll
+  for (int g = 1; g < kGroups; ++g) {
+    const float4 y = *reinterpret_cast<const float4 *>(&sums[g][d]);
+    v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
+  }
+  finish(a, plan, split.b, split.h, row, d, DIM, v, factors_of(all_top, all_ref, all_weight), all_top, all_weight);
 }
 
 constexpr size_t kSplitBytes = kMaxSms * sizeof(Split);
@@ -859,7 +919,7 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   const cudaError_t e = launch_pdl(attention_kernel<DIM, NT>, dim3(static_cast<unsigned>(ctas)), dim3(S::kWarps * 32),
                                    smem, s, a, plan);
   if (e != cudaSuccess) return e;
-  return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(ctas), plan.part_rows, DIM / 64), dim3(kJoinThreads), 0, s, a,
+  return launch_pdl(join_kernel<DIM>, dim3(static_cast<unsigned>(ctas), plan.part_rows), dim3(kJoinThreads<DIM>), 0, s, a,
                     plan, S::kRows);
 }
 
