@@ -7,7 +7,7 @@
 //
 // A CTA takes the new tokens of one block of 32 of one sequence, for as many heads as come to
 // 256 channels (one head a CTA: 23 us for 16384 x 8 x 128, 35 for 16 x 64, where this takes 19 and
-// 20).  A unit of its threads has the keys or the values of a head: it reads each once, holds
+// 19).  A unit of its threads has the keys or the values of a head: it reads each once, holds
 // it in registers (8 channels a lane) while the largest magnitude goes across its warps, and
 // writes its codes.  What a value costs bounds a prompt (so the largest of two at a time, one
 // factor, no test for infinities where the block has none), the chain starts and lengths,
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     uint16_t out[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      float lo = __uint_as_float(w[k] << 16) * f, hi = __uint_as_float(w[k] & 0xFFFF0000u) * f;
+      const float2 v = mul_f32x2(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)), make_float2(f, f));
+      float lo = v.x, hi = v.y;
       if (wild) {  // (the conversion would make an infinity 448)
         if (fabsf(lo) == INFINITY) lo = NAN;
         if (fabsf(hi) == INFINITY) hi = NAN;
