@@ -1,5 +1,6 @@
-"""GB300 (sm_103a) MXFP4 / NVFP4 block-scaled GEMM, BF16 quantizer, and the
-few-token products of those weights (linear, mixture of experts).
+"""GB300 (sm_103a) MXFP4 / NVFP4 block-scaled GEMM, BF16 quantizer, the
+few-token products of those weights (linear, mixture of experts), and the rest
+of a decoding step (norm and rotation, paged cache, attention, sampling).
 
 The compute path is the C-ABI library libmxfp4.so (include/mxfp4.h), built
 from the CUDA sources in csrc/ by build.py; ``_binding`` exposes each entry

@@ -17,7 +17,7 @@
 //
 // A row is bound by the chain of its steps (a barrier of the cluster is 1 us) and by the forty
 // operations of a weight, many rows by how many CTAs fit an SM (registers and the slice: two).
-// 64 x 131072 with all kinds of rows: 59 us of which the logits' bytes take 5 (halving the range
+// 64 x 131072 with all kinds of rows: 53 us of which the logits' bytes take 5 (halving the range
 // of keys for each threshold: 686 us); 1 x 32000 with top-k 11.7 us.
 #include "decode.h"
 #include "mx_device.cuh"

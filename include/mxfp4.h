@@ -524,7 +524,9 @@ int mx_moe_layer_bf16(const void *x, int64_t tokens, int64_t ld_x, const void *r
  * queries and keys, stores keys and values, attends to what is stored and, at
  * its end, chooses a token.  The pages have no counterpart; these calls are this
  * library's own addition.  Arithmetic is binary32 unless said otherwise, and no
- * result depends on the run. */
+ * result depends on the run.  int32 and FP32 arrays (positions, lengths, tables,
+ * frequencies, parameters, log-sum-exps, weight gradients) need 4-byte alignment
+ * only. */
 
 /* The norm and rotation of a layer's queries and keys (host memory, read before
  * a call returns). */
