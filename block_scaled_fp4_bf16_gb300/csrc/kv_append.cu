@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     uint16_t out[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float2 v = mul_f32x2(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)), make_float2(f, f));
+      const float2 v = mul_f32x2(make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u)),
+                                 make_float2(f, f));
       float lo = v.x, hi = v.y;
       if (wild) {  // (the conversion would make an infinity 448)
         if (fabsf(lo) == INFINITY) lo = NAN;

@@ -221,7 +221,7 @@ __device__ __forceinline__ Item item_of(int64_t i, int slices, int per_slice, in
   Item t;
   if (slices == 1) {
     t = Item{i, 0, groups};
-  } else {  // (there are slices only where tokens are few)
+  } else {  // (there are slices only where 32 bits hold their number)
     const int n = static_cast<int>(i), token = n / slices, first = (n - token * slices) * per_slice;
     t = Item{token, first, min(first + per_slice, groups)};
   }
@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
     const uint32_t from = ring + stage * ForwardRing::kStage;
     Pairs v;
     unpack(lds128(from + lane * 16), lds128(from + kPiece + lane * 16), a.interleaved, v);
-    if (at.g == at.item.first && a.rotary_dim > 0) angles_of<LANES>(t, turns, static_cast<int>(lds32(from + 2 * kPiece + lane * 4)), lane);
+    if (at.g == at.item.first && a.rotary_dim > 0)
+      angles_of<LANES>(t, turns, static_cast<int>(lds32(from + 2 * kPiece + lane * 4)), lane);
     copy_next(stage == 0 ? kForwardStages - 1 : stage - 1);
     stage = stage + 1 == kForwardStages ? 0 : stage + 1;
     const int k = at.g >= queries, group = at.g - (k ? queries : 0);
@@ -410,7 +411,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
       Pairs v, n;
       unpack(lds128(from + 2 * kPiece + lane * 16), lds128(from + 3 * kPiece + lane * 16), a.interleaved, v);
       if (p.weight != nullptr) unpack(lds128(from + lane * 16), lds128(from + kPiece + lane * 16), a.interleaved, n);
-      if (at.g == at.item.first && a.rotary_dim > 0) angles_of<LANES>(t, turns, static_cast<int>(lds32(from + 4 * kPiece + lane * 4)), lane);
+      if (at.g == at.item.first && a.rotary_dim > 0)
+        angles_of<LANES>(t, turns, static_cast<int>(lds32(from + 4 * kPiece + lane * 4)), lane);
       copy_next(which, stage == 0 ? kBackwardStages - 1 : stage - 1);
       stage = stage + 1 == kBackwardStages ? 0 : stage + 1;
       const bool in = c.in && at.g * kHeads + sub < p.heads;
