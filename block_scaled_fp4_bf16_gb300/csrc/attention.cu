@@ -338,11 +338,13 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
       before += all;
       __syncthreads();
     }
-    if (threadIdx.x == 0) first[c.sequences] = static_cast<uint32_t>(before);
-    if (before > kMostBlocks) {  // (uniform) nothing is seen
-      if (threadIdx.x == 0) atomicOr(c.status, kStatusIndexBit);
-      for (int b = threadIdx.x; b <= c.sequences; b += S::kWarps * 32) first[b] = 0;
+    const bool seen = before <= kMostBlocks;  // (uniform; else nothing is)
+    if (threadIdx.x == 0) {
+      first[c.sequences] = seen ? static_cast<uint32_t>(before) : 0;
+      if (!seen) atomicOr(c.status, kStatusIndexBit);
     }
+    if (!seen)  // (each thread's own words of above)
+      for (int b = threadIdx.x; b < c.sequences; b += S::kWarps * 32) first[b] = 0;
     if (threadIdx.x < 2 * S::kWarps) infos[threadIdx.x >> 1][threadIdx.x & 1].valid = 0;
     __syncthreads();
   }
