@@ -10,17 +10,19 @@
 // x up to 8192 tokens of 64/8 heads, where this takes 94; the cache's bytes take 88).
 // E4M3 is exact in FP16; q enters under a power of two of its row, a weight as the sum of two FP16
 // numbers, each a product of its own: as one number its 11 bits showed in the BF16 outputs (0.0005 from
-// binary32's, where two leave 0.0002 and less; 64 x 8192 of 64 channels 92 us with one, 100 with two,
-// of 128 channels 129 and 131).
+// binary32's, where two leave 0.0002 and less; 64 x 8192 of 64 channels 92 us with one, 99 with two,
+// of 128 channels 129 and 130).
 //
 // Every warp is a worker of its own: the blocks of 32 tokens of all (row tile, sequence,
 // key head) together are shared out evenly and in order over the workers, so that uneven
 // lengths and few sequences fill the GPU alike.  A worker streams its blocks through its own
 // ring of shared memory (cp.async, no barrier wider than the warp) and keeps queries, sums
-// and the softmax's state in registers.  A row has two running maxima: of its logits, to
-// which its sum of weights is relative, and of logit + value scale (both as powers of two), to
-// which the FP16 weights are: a weight is rounded relative to the largest contribution to the
-// output, however far the blocks' scales lie apart.  What a worker leaves unfinished goes to
+// and the softmax's state in registers.  A row has two running maxima, as powers of two rounded up:
+// `top` of its logits, to which its sum of weights is relative, and `gap` of logit - top + value
+// scale, with which the FP16 weights are relative to the largest contribution to the output, however
+// far the blocks' scales lie apart.  Both are whole numbers, so that what a new maximum takes off the
+// sums is a power of two and exact; the second is one of differences, which binary32 has for logits
+// of any size (a maximum of logit + value scale would lose the scale from 2^24 on).  What a worker leaves unfinished goes to
 // the workspace or, at its end, in its ring; its CTA joins the parts of its workers, and a
 // second, small launch those of the CTAs, in their order (all by the second launch: 1 x 131072
 // of 32/4 heads 82 us, so 31, of which the cache takes 20, what precedes the first block 4, and
@@ -168,8 +170,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t codes) {
   return ((codes & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
 }
 
-// 0 for -inf: a maximum that numbers are taken relative to.
-__device__ __forceinline__ float base_of_max(float v) { return v == -INFINITY ? 0.0f : v; }
+// `top` and `gap` of a row without a logit yet: finite, so that -inf less one of them is -inf.
+constexpr float kNone = -0x1.fffffep127f;
 
 // Sequence, key head, tile and block of a place in the order of all blocks.
 struct Place {
@@ -222,8 +224,8 @@ __device__ __forceinline__ int query_shift(uint32_t largest) {
 struct Factors {
   float by_weight, by_scale;
 };
-__device__ __forceinline__ Factors factors_of(float top, float ref, float weight) {
-  return Factors{weight == 0.0f ? 0.0f : exp2f(-kLift) / weight, exp2f(base_of_max(ref) - base_of_max(top))};
+__device__ __forceinline__ Factors factors_of(float gap, float weight) {
+  return Factors{weight == 0.0f ? 0.0f : exp2f(-kLift) / weight, exp2f(gap)};
 }
 
 // Writes four channels of a finished row, and its log-sum-exp with the first.
@@ -253,26 +255,26 @@ __device__ __forceinline__ Part part_at(float *p, int rows, int dim) {
 
 // The sum of the parts part(0) .. part(n - 1) of a row, four channels from d on.
 struct Joined {
-  float v[4], top, ref, weight;
+  float v[4], top, gap, weight;
 };
 template <typename PartOf>
 __device__ __forceinline__ Joined join(int n, const PartOf &part, int row, int d, int dim) {
-  Joined j{{0.0f, 0.0f, 0.0f, 0.0f}, -INFINITY, -INFINITY, 0.0f};
+  Joined j{{0.0f, 0.0f, 0.0f, 0.0f}, kNone, kNone, 0.0f};
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const Part p = part(i);
-    const float top = p.state[row], ref = p.state[p.rows + row], weight = p.state[2 * p.rows + row];
+    const float top = p.state[row], gap = p.state[p.rows + row], weight = p.state[2 * p.rows + row];
     const float4 v = *reinterpret_cast<const float4 *>(p.sums + row * dim + d);
-    const float now = fmaxf(j.top, top), now_ref = fmaxf(j.ref, ref);
-    const float b = base_of_max(now), b_ref = base_of_max(now_ref);
-    j.weight = j.weight * exp2_approx(j.top - b) + weight * exp2_approx(top - b);
-    const float keep = exp2_approx(j.ref - b_ref), add = exp2_approx(ref - b_ref);
+    const float now = fmaxf(j.top, top);
+    j.weight = j.weight * exp2_approx(j.top - now) + weight * exp2_approx(top - now);
+    const float gap_j = j.gap + (j.top - now), gap_p = gap + (top - now), now_gap = fmaxf(fmaxf(gap_j, gap_p), kNone);
+    const float keep = exp2_approx(gap_j - now_gap), add = exp2_approx(gap_p - now_gap);
     j.v[0] = j.v[0] * keep + v.x * add;
     j.v[1] = j.v[1] * keep + v.y * add;
     j.v[2] = j.v[2] * keep + v.z * add;
     j.v[3] = j.v[3] * keep + v.w * add;
     j.top = now;
-    j.ref = now_ref;
+    j.gap = now_gap;
   }
   return j;
 }
@@ -281,7 +283,7 @@ __device__ __forceinline__ void put_part(const Part &p, int row, int d, int dim,
   *reinterpret_cast<float4 *>(p.sums + row * dim + d) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
   if (d == 0) {
     p.state[row] = j.top;
-    p.state[p.rows + row] = j.ref;
+    p.state[p.rows + row] = j.gap;
     p.state[2 * p.rows + row] = j.weight;
   }
 }
@@ -445,7 +447,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
 
     // ---- the blocks, one after the other
     float out[NT][DIM / 16][4];  // [..][..][2 e + r]: channels 2 i + e of the lane's, rows 2 t + r
-    float top[NT][2], ref[NT][2], weight[NT][2];
+    float top[NT][2], gap[NT][2], weight[NT][2];
     float factor[NT][2];         // of a logit: scale, log2(e) and the row's power of two
     uint32_t query[NT][S::kSteps][2];
     int length = 0, start = 0;
@@ -489,7 +491,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             factor[nt][r] = __shfl_sync(0xFFFFFFFFu, mine, (2 * t + r) * 4);
-            top[nt][r] = ref[nt][r] = -INFINITY;
+            top[nt][r] = gap[nt][r] = kNone;
             weight[nt][r] = 0.0f;
           }
 #pragma unroll
@@ -581,18 +583,20 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
           m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 8));
           m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
           most[nt][r] = m;
-          grows |= m > top[nt][r] || m + value_exp > ref[nt][r];
+          grows |= m > top[nt][r] || m - top[nt][r] > gap[nt][r] - value_exp;
         }
       if (__any_sync(0xFFFFFFFFu, grows)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float now = fmaxf(top[nt][r], most[nt][r]), now_ref = fmaxf(ref[nt][r], most[nt][r] + value_exp);
-            weight[nt][r] *= exp2_approx(top[nt][r] - base_of_max(now));
-            const float keep = exp2_approx(ref[nt][r] - base_of_max(now_ref));
+            const float now = fmaxf(top[nt][r], ceilf(most[nt][r])), down = top[nt][r] - now;
+            const float kept = gap[nt][r] + down;
+            const float now_gap = fmaxf(fmaxf(kept, ceilf(most[nt][r] - now) + value_exp), kNone);
+            weight[nt][r] *= exp2_approx(down);
+            const float keep = exp2_approx(kept - now_gap);
             top[nt][r] = now;
-            ref[nt][r] = now_ref;
+            gap[nt][r] = now_gap;
 #pragma unroll
             for (int i = 0; i < DIM / 16; ++i) {
               out[nt][i][r] *= keep;
@@ -607,11 +611,11 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
         float w[2][4];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          const float base = base_of_max(top[nt][r]), lift = value_exp + kLift - base_of_max(ref[nt][r]);
+          const float lift = value_exp + kLift - gap[nt][r];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float l = s[nt][i >> 1][2 * (i & 1) + r];
-            weight[nt][r] += exp2_approx(l - base);
+            const float l = s[nt][i >> 1][2 * (i & 1) + r] - top[nt][r];
+            weight[nt][r] += exp2_approx(l);
             w[r][i] = exp2_approx(l + lift);
           }
         }
@@ -734,10 +738,10 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
             j.weight += __shfl_xor_sync(0xFFFFFFFFu, j.weight, 8);
             j.weight += __shfl_xor_sync(0xFFFFFFFFu, j.weight, 16);
             j.top = top[nt][r];
-            j.ref = ref[nt][r];
+            j.gap = gap[nt][r];
             const int pr = nt * 8 + 2 * t + r, row = at.tile * S::kRows + pr;
             if (row >= plan.rows) continue;
-            const Factors factors = factors_of(j.top, j.ref, j.weight);
+            const Factors factors = factors_of(j.gap, j.weight);
 #pragma unroll
             for (int run = 0; run < S::kRuns; ++run)
 #pragma unroll
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     const auto part = [&](int k) { return infos[chain.warp + k][k == 0 && chain.begins].part; };
     const Joined j = join(chain.count, part, pr, d, DIM);
     if (chain.begins && chain.ends)
-      finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, factors_of(j.top, j.ref, j.weight), j.top, j.weight);
+      finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, factors_of(j.gap, j.weight), j.top, j.weight);
     else
       put_part(part_at(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
                        plan.part_rows, DIM),
@@ -839,7 +843,7 @@ __global__ void __launch_bounds__(kJoinThreads<DIM>)
     __syncthreads();
     if (group != 0) return;
     const Joined j = join(n, [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, DIM);
-    finish(a, plan, split.b, split.h, row, d, DIM, j.v, factors_of(j.top, j.ref, j.weight), j.top, j.weight);
+    finish(a, plan, split.b, split.h, row, d, DIM, j.v, factors_of(j.gap, j.weight), j.top, j.weight);
     return;
   }
   const auto load = [&](int k) {
@@ -848,29 +852,33 @@ __global__ void __launch_bounds__(kJoinThreads<DIM>)
   float4 x[kAhead];
 #pragma unroll
   for (int i = 0; i < kAhead; ++i) x[i] = load(group + i * kGroups);
-  float top[kOwn], ref[kOwn], weight[kOwn], all_top = -INFINITY, all_ref = -INFINITY, all_weight = 0.0f;
+  float top[kOwn], gap[kOwn], weight[kOwn], all_top = kNone, all_gap = kNone, all_weight = 0.0f;
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     const int k = lane + i * 32;
-    top[i] = ref[i] = -INFINITY;
+    top[i] = gap[i] = kNone;
     weight[i] = 0.0f;
     if (k < n) {
       const Part p = part(k);
-      top[i] = p.state[pr], ref[i] = p.state[p.rows + pr], weight[i] = p.state[2 * p.rows + pr];
+      top[i] = p.state[pr], gap[i] = p.state[p.rows + pr], weight[i] = p.state[2 * p.rows + pr];
     }
     all_top = fmaxf(all_top, top[i]);
-    all_ref = fmaxf(all_ref, ref[i]);
   }
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) {
-    all_top = fmaxf(all_top, __shfl_xor_sync(0xFFFFFFFFu, all_top, m));
-    all_ref = fmaxf(all_ref, __shfl_xor_sync(0xFFFFFFFFu, all_ref, m));
+  for (int m = 16; m > 0; m >>= 1) all_top = fmaxf(all_top, __shfl_xor_sync(0xFFFFFFFFu, all_top, m));
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const float down = top[i] - all_top;
+    gap[i] += down;
+    all_gap = fmaxf(all_gap, gap[i]);
+    all_weight += weight[i] * exp2_approx(down);
   }
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) all_gap = fmaxf(all_gap, __shfl_xor_sync(0xFFFFFFFFu, all_gap, m));
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
     if (i * 32 >= n) break;
-    factors[warp][lane + i * 32] = exp2_approx(ref[i] - base_of_max(all_ref));
-    all_weight += weight[i] * exp2_approx(top[i] - base_of_max(all_top));
+    factors[warp][lane + i * 32] = exp2_approx(gap[i] - all_gap);
   }
 #pragma unroll
   for (int m = 16; m > 0; m >>= 1) all_weight += __shfl_xor_sync(0xFFFFFFFFu, all_weight, m);
@@ -896,7 +904,7 @@ __global__ void __launch_bounds__(kJoinThreads<DIM>)
     const float4 y = *reinterpret_cast<const float4 *>(&sums[g][d]);
     v[0] += y.x, v[1] += y.y, v[2] += y.z, v[3] += y.w;
   }
-  finish(a, plan, split.b, split.h, row, d, DIM, v, factors_of(all_top, all_ref, all_weight), all_top, all_weight);
+  finish(a, plan, split.b, split.h, row, d, DIM, v, factors_of(all_gap, all_weight), all_top, all_weight);
 }
 
 constexpr size_t kSplitBytes = kMaxSms * sizeof(Split);

@@ -651,8 +651,8 @@ size_t mx_attention_workspace_bytes(int64_t sequences, int64_t q_tokens, int64_t
  * 2^36 together nothing is seen; mx_device_status then returns MX_ERR_DEVICE_INDEX.
  * Products are FP16 with binary32 sums: codes are exact in FP16, q is under a power of
  * two of its row and head (exact above 2^-29 of their largest), and the weights are sums
- * of two FP16 numbers (2^-22 relative, or 2^-39 of the row's largest weight times value
- * scale where their own times it is below 2^-17 of that); the sum of the weights is not
+ * of two FP16 numbers (2^-22 relative, or 2^-38 of the row's largest weight times value
+ * scale where their own times it is below 2^-16 of that); the sum of the weights is not
  * rounded.  No output overlaps an input or the workspace
  * (mx_attention_workspace_bytes(...) bytes, 16-byte aligned, contents arbitrary; one
  * call at a time may use it).  Launches two kernels. */
