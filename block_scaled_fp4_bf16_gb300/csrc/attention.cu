@@ -48,6 +48,8 @@ template <int DIM>
 constexpr int kJoinThreads = DIM == 256 ? 256 : 128;
 constexpr float kLift = 14.0f;  // FP16 weights are up to 2^14 (in two numbers: to 2^-22, at least to 2^-25)
 
+constexpr int kLeastExponent = -255;  // of a row's factor: under any keys' scale its logits are 0 to binary32
+
 // NT: columns of the products in eights, the rows of a tile.
 template <int DIM, int NT>
 struct Shape {
@@ -213,10 +215,11 @@ __device__ __forceinline__ bool advance(Place &p, const uint32_t *first, const C
   return true;
 }
 
-// The power of two that brings a row's largest (as binary32 bits) to 2^14 .. 2^15 is 2^-shift.
+// The power of two that brings a row's largest (as binary32 bits) to 2^14 .. 2^15 (a subnormal one
+// below that) is 2^-shift.
 __device__ __forceinline__ int query_shift(uint32_t largest) {
   const int e = static_cast<int>(largest >> 23);
-  return e == 0 || e == 255 ? 0 : e - 127 - 14;
+  return largest == 0 || e == 255 ? 0 : max(e, 1) - 127 - 14;
 }
 
 // What turns a row's sums into its output: two factors, which together may leave binary32's
@@ -361,6 +364,13 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
   }
   const int64_t total = static_cast<int64_t>(first[c.sequences]) * c.heads * plan.tiles;
   const Shares shares(total, plan.workers);
+  // What turns a sum into a logit is scale * log2(e) times powers of two of the row and the block's keys,
+  // of which each may leave binary32's range where the logit does not: the scale is taken apart, and a
+  // row's factor is kept as its bits, to which exponents are added.
+  int scale_exp;
+  const float part = frexpf(a.scale, &scale_exp);
+  const uint32_t scale_bits = __float_as_uint((part == 0.0f ? 1.0f : part) * 1.4426950408889634f);
+  if (part == 0.0f) scale_exp = kLeastExponent;
   const int worker = blockIdx.x * S::kWarps + warp;
   const int64_t begin = shares.begin(worker), end = shares.begin(worker + 1);
 
@@ -448,7 +458,8 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     // ---- the blocks, one after the other
     float out[NT][DIM / 16][4];  // [..][..][2 e + r]: channels 2 i + e of the lane's, rows 2 t + r
     float top[NT][2], gap[NT][2], weight[NT][2];
-    float factor[NT][2];         // of a logit: scale, log2(e) and the row's power of two
+    uint32_t factor[NT][2];      // of the rows' logits, as bits: scale, log2(e) and the row's power of two
+    int exponent_low = 0, exponent_high = 0;  // of all rows' powers of two
     uint32_t query[NT][S::kSteps][2];
     int length = 0, start = 0;
     bool from_start = false, fresh = true;
@@ -456,6 +467,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     for (int64_t f = begin; f < end; ++f) {
       if (fresh) {  // a new (tile, sequence, head): its queries
         fresh = false;
+        exponent_low = exponent_high = 0;
         from_start = at.block == 0;
         length = length_of(a, at.b);
         start = first_seen(a, length);
@@ -486,8 +498,10 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
           largest = max(largest, __shfl_xor_sync(0xFFFFFFFFu, largest, 2));
           const int shift = query_shift(largest);
           const float f1 = exp2_int(-shift / 2), f2 = exp2_int(-shift - -shift / 2);
-          // (back in two steps, for the ends of binary32's range)
-          const float mine = a.scale * 1.4426950408889634f * exp2_int(shift / 2) * exp2_int(shift - shift / 2);
+          const int exponent = max(scale_exp + shift, kLeastExponent);
+          exponent_low = min(exponent_low, __reduce_min_sync(0xFFFFFFFFu, exponent));
+          exponent_high = max(exponent_high, __reduce_max_sync(0xFFFFFFFFu, exponent));
+          const uint32_t mine = scale_bits + (static_cast<uint32_t>(exponent) << 23);
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             factor[nt][r] = __shfl_sync(0xFFFFFFFFu, mine, (2 * t + r) * 4);
@@ -547,17 +561,31 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
       // do all rows see all of the block?
       const bool whole = here.held && t0 + kCacheBlock - 1 <= position &&
                          (a.window == 0 || static_cast<int64_t>(t0) >= length - a.window);
-      const float key_scale = here.key_scale == 0 ? 0x1p-127f : __int_as_float(here.key_scale << 23);
+      const int key_exp = here.key_scale - 127;
       const float value_exp = static_cast<float>(here.value_scale - 127);
       float most[NT][2];
+      if (key_exp + exponent_low >= -125 && key_exp + exponent_high <= 126) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const float scaled = factor[nt][r];
+          for (int r = 0; r < 2; ++r) {
+            const float f = __uint_as_float(factor[nt][r] + (static_cast<uint32_t>(key_exp) << 23));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][i >> 1][2 * (i & 1) + r] *= scaled * key_scale;
-        }
+            for (int i = 0; i < 4; ++i) s[nt][i >> 1][2 * (i & 1) + r] *= f;
+          }
+      } else {  // in two steps of finite factors (0 stays 0)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const int e = (static_cast<int>(factor[nt][r] - scale_bits) >> 23) + key_exp;
+            const float f1 = exp2_int(min(max(e / 2, -126), 126)), f2 = exp2_int(min(max(e - e / 2, -126), 126));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nt][i >> 1][2 * (i & 1) + r] *= __uint_as_float(scale_bits) * f1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s[nt][i >> 1][2 * (i & 1) + r] *= f2;
+          }
+      }
       if (!whole) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
