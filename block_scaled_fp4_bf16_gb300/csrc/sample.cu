@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const float top = key_logit(static_cast<uint32_t>(best >> 32));
   const bool none = best == ~0ull || top == -INFINITY;
-  if (none || temperature <= 0.0f) {
+  if (none || temperature <= 0.0f || min_p > 1.0f) {  // (above 1 no weight reaches: the first alone is kept)
     if (rank == 0 && threadIdx.x == 0 && in_bounds(row, 1, a.rows, a.status)) {
       a.ids[row] = none ? -1 : static_cast<int32_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
       if (a.probability != nullptr) a.probability[row] = none ? 0.0f : 1.0f;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     cut(sh.piece, sh.piece, sh.found[1], true);
   }
   const uint64_t floor_weight =
-      min_p > 0.0f ? static_cast<uint64_t>(ceilf(fminf(min_p, 1.0f) * static_cast<float>(1ull << kUnit))) : 1;
+      min_p > 0.0f ? static_cast<uint64_t>(ceilf(min_p * static_cast<float>(1ull << kUnit))) : 1;
   auto final_weight = [&](float l, int i) -> uint64_t {
     if (!kept(l, i)) return 0;
     const uint64_t w = weight(l);

@@ -671,7 +671,7 @@ int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64_t sequ
  *   the first top_k (top_k <= 0 or > vocab: all), of these
  *   the fewest whose w add up to at least top_p times the sum of all of these
  *      (top_p >= 1: all; always the first), and of these
- *   those with w_j >= min_p (min_p <= 0: all; the first is always kept);
+ *   those with w_j >= min_p (min_p <= 0: all; the first is always kept, alone above 1);
  * ids is the first kept token, by index, up to which the kept w (in the order of
  * the indexes) add up to more than uniform times their sum, and probability its
  * w over that sum.  temperature <= 0 takes the largest logit, probability 1.
