@@ -28,22 +28,30 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kCtas = 2;  // of an SM
 
-// f / 2 pi modulo 1, in units of 2^-64: the phase of a position is then one 64-bit
-// product, exact modulo a turn.
+// f / 2 pi modulo 1, to the nearest unit of 2^-64: the phase of a position is then one 64-bit
+// product, off by at most 2^-34 of a turn (2^31 half units).  1 / 2 pi has 128 bits, of which a
+// frequency of 2^16 takes 80; 64 were right for frequencies up to 1 (2^-18 of a turn at 2^16).
 __device__ __forceinline__ uint64_t turns_of(float f) {
-  constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;  // 2^64 / 2 pi
+  constexpr uint64_t kHigh = 0x28BE60DB9391054Aull, kLow = 0x7F09D5F47D4D3770ull;  // 2^128 / 2 pi
   const uint32_t b = __float_as_uint(f);
   const int be = static_cast<int>((b >> 23) & 255u);
   const uint64_t m = (b & 0x7FFFFFu) | (be ? 0x800000u : 0u);
   const int e = (be ? be : 1) - 150;  // |f| = m 2^e
-  const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
-  uint64_t t;
-  if (e >= 0)
-    t = e < 64 ? lo << e : 0;
-  else if (e > -64)
-    t = (lo >> -e) | (hi << (64 + e));
-  else
-    t = e > -128 ? hi >> (-e - 64) : 0;
+  // m / 2 pi in units of 2^-128
+  const uint64_t p0 = m * kLow, carry = __umul64hi(m, kLow), p1 = m * kHigh + carry;
+  const uint64_t p2 = __umul64hi(m, kHigh) + (p1 < carry ? 1 : 0);
+  uint64_t t, half;  // times 2^e in units of 2^-64, and the next bit
+  if (e >= 0) {  // (frequencies of 2^23 and more)
+    t = e == 0 ? p1 : e < 64 ? p1 << e | p0 >> (64 - e) : 0;
+    half = e < 64 ? p0 << e >> 63 : 0;
+  } else if (e > -64) {
+    t = p1 >> -e | p2 << (64 + e);
+    half = p1 >> (-e - 1) & 1;
+  } else {
+    t = e > -128 ? p2 >> (-e - 64) : 0;
+    half = e == -64 ? p1 >> 63 : e > -128 ? p2 >> (-e - 65) & 1 : 0;
+  }
+  t += half;
   return (b >> 31) ? 0 - t : t;
 }
 
@@ -181,9 +189,9 @@ __device__ __forceinline__ void angles_of(Angles &t, const uint64_t *turns, int 
   float sin[kOwn], cos[kOwn];
 #pragma unroll
   for (int i = 0; i < kOwn; ++i) {
-    // (the upper 32 bits as a signed fraction of a turn: half turns in [-1, 1))
+    // (the upper 32 bits, to the nearest, as a signed fraction of a turn: half turns in [-1, 1))
     const uint64_t phase = turns[8 * (lane % LANES) + first + i] * static_cast<uint64_t>(static_cast<int64_t>(position));
-    const float half = static_cast<float>(static_cast<int32_t>(phase >> 32)) * 0x1p-31f;
+    const float half = static_cast<float>(static_cast<int32_t>((phase + 0x80000000ull) >> 32)) * 0x1p-31f;
     sincospif(half, &sin[i], &cos[i]);
   }
 #pragma unroll

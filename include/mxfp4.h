@@ -547,8 +547,9 @@ typedef struct mx_qk_norm {
  * without a weight), then for each pair (a, b) of rotating channels and its
  * angle phi = positions[token] * inv_freq[i]
  *   a' = a cos phi - b sin phi,  b' = b cos phi + a sin phi;
- * one rounding to BF16.  phi is reduced exactly (to 2^-32 of a turn) for any
- * position and |inv_freq| up to 2^16.
+ * one rounding to BF16.  phi is reduced to a turn in integers, right to 2^-32 of one
+ * for any position and |inv_freq| up to 2^16, and then rounded to binary32 (at most
+ * 2^-26 of a turn).
  *   q: BF16 [tokens, q_heads, head_dim], token stride ld_q (>= q_heads * head_dim,
  *      % 8 == 0); k, q_out, k_out likewise.  q and q_out (k and k_out) are NULL
  *      when there are no such heads.
