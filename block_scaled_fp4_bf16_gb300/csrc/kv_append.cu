@@ -40,7 +40,7 @@ template <int DIM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kLanes = DIM / 8, kRows = 4, kPasses = kCacheBlock / kRows;
   constexpr int kUnit = kLanes * kRows, kUnits = kThreads / kUnit;  // a unit: keys or values of a head
-  __shared__ int found;  // the sequence
+  __shared__ int found, descends, shared_slots;  // the sequence; are starts out of order; a slot that two take
   __shared__ uint32_t largest[kThreads / 32];
   griddep_launch_dependents();
   griddep_wait();
@@ -59,16 +59,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     row0 = b * n;
     stated = c.lengths[b];
   } else {
-    if (threadIdx.x == 0) found = 0x7FFFFFFF;
+    if (threadIdx.x == 0) found = 0x7FFFFFFF, descends = shared_slots = 0;
     __syncthreads();
     const int64_t slot = blockIdx.x;
     for (int i = threadIdx.x; i < c.sequences; i += kThreads) {
       const int64_t s0 = a.starts[i], s1 = a.starts[i + 1];
       if (s0 < 0 || s1 < s0 || s1 > a.tokens) {
         if (slot == 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndexBit);
+        descends = 1;
         continue;
       }
-      // (starts in order make a slot that of one sequence; out of order, the first one takes it)
+      // (starts in order make a slot that of one sequence; out of order, the first one takes it, see below)
       if (slot >= s0 / kCacheBlock + 2 * static_cast<int64_t>(i) &&
           slot < s1 / kCacheBlock + 2 * static_cast<int64_t>(i) + 2)
         atomicMin(&found, i);
@@ -78,6 +79,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (b == 0x7FFFFFFF) return;
     row0 = a.starts[b];
     n = a.starts[b + 1] - row0;
+    if (descends) {
+      // a sequence with slots that an earlier one has, too, is left out as a whole
+      for (int i = threadIdx.x; i < b; i += kThreads) {
+        const int64_t s0 = a.starts[i], s1 = a.starts[i + 1];
+        if (s0 >= 0 && s1 >= s0 && s1 <= a.tokens && s1 / kCacheBlock + 2 * static_cast<int64_t>(i) + 2 >
+                                                        row0 / kCacheBlock + 2 * static_cast<int64_t>(b))
+          shared_slots = 1;
+      }
+      __syncthreads();
+      if (shared_slots) return;
+    }
     stated = c.lengths[b];
     index = slot - (row0 / kCacheBlock + 2 * static_cast<int64_t>(b));
   }

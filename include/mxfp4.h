@@ -620,7 +620,8 @@ typedef struct mx_kv_cache {
  * A page that sequences go on in must belong to one of them.  Rows whose page is
  * not 0..pages - 1, or that max_pages does not reach, are left out, and
  * mx_device_status then returns MX_ERR_DEVICE_INDEX; likewise sequences whose
- * starts are out of order or range.  Launches one kernel. */
+ * starts are out of order or range, and, behind such ones, some (as a whole) that begin
+ * more than 64 rows before the end of an earlier sequence.  Launches one kernel. */
 int mx_kv_append_bf16(const void *k, int64_t ld_k, const void *v, int64_t ld_v, int64_t tokens,
                       const int32_t *starts, const int32_t *page_table, int64_t max_pages,
                       const int32_t *lengths, int64_t sequences, const mx_kv_cache *cache,

@@ -44,3 +44,12 @@ def test_the_others_are_stored(starts, stored, dim):
 def test_long_ones_beside_bad_ones():
     run([0, 100, 90, 230, 300], 260, [100, 50, 200, 80], [0, 2])
     run([0, 70, 71, 600, 200], 200, [130, 1, 64, 64], [0, 1])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_slots_of_two_sequences(dim):
+    """Behind starts that descend, a sequence may share slots with an earlier one: it is left out as a whole."""
+    run([0, 90, 0, 64], 100, [100, 20, 70], [0, 2], dim)
+    run([0, 100, 0, 64], 100, [100, 20, 70], [0], dim)
+    run([0, 1000, 0, 64, 1000, 1000], 1000, [1000, 20, 70, 950, 20], [0, 4], dim)
+    run([0, 30, 400, 100, 100, 390], 400, [40, 380, 64, 80, 290], [0, 1], dim)
