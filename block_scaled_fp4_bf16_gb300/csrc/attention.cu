@@ -73,11 +73,11 @@ struct Split {
 // What the two launches share.
 struct Plan {
   Split *splits;         // of each CTA
-  float *parts;          // two for each worker and two for each CTA (part_floats)
-  float *cta_parts;
+  float *parts;          // one for each worker (part_floats): of what another began and it ended
+  float *cta_parts;      // two for each CTA
   int tiles, rows, group;  // rows: of all tiles of a (sequence, key head)
   int part_rows;           // rows of a part
-  int workers, per_cta;
+  int workers;
   int blocks_per_page;
 };
 
@@ -745,10 +745,10 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
       if (last || f + 1 == end) {
         fresh = true;
         const bool whole_row = from_start && last;
-        // (the last part of a share takes the place of the ring, an earlier one goes to memory)
+        // (the last part of a share takes the place of the ring; an earlier one, which goes to memory, ends
+        // what another worker began)
         const bool in_ring = f + 1 == end;
-        Part part = part_at(plan.parts + (static_cast<int64_t>(worker) * 2 + from_start) * part_floats(plan.part_rows, DIM),
-                            plan.part_rows, DIM);
+        Part part = part_at(plan.parts + worker * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
         if (in_ring) {
           part = Part{reinterpret_cast<float *>(smem + warp * S::kRing), states[warp], S::kRows};
           cp_async_wait<0>();
@@ -955,7 +955,6 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   plan.part_rows = static_cast<int>(part_rows_of(plan.rows, DIM));
   plan.blocks_per_page = a.c.page_tokens / kCacheBlock;
   const int ctas = a.num_sms < kMaxSms ? a.num_sms : kMaxSms;
-  plan.per_cta = S::kWarps;
   plan.workers = ctas * S::kWarps;
   plan.splits = static_cast<Split *>(a.workspace);
   plan.cta_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kSplitBytes);
@@ -983,7 +982,7 @@ size_t attention_workspace_bytes(int64_t rows, int head_dim) {
   const int warps = head_dim == 64    ? (tile_rows_of(rows, 64) == 8 ? Shape<64, 1>::kWarps : Shape<64, 2>::kWarps)
                     : head_dim == 128 ? Shape<128, 1>::kWarps
                                       : Shape<256, 1>::kWarps;
-  const int64_t parts = 2 * kMaxSms * (1 + warps);  // of the CTAs and of their warps
+  const int64_t parts = kMaxSms * (2 + warps);  // of the CTAs and of their warps
   return kSplitBytes + static_cast<size_t>(parts * part_floats(part_rows_of(rows, head_dim), head_dim)) * sizeof(float);
 }
 
