@@ -77,7 +77,7 @@ struct Plan {
   float *cta_parts;      // two for each CTA
   int tiles, rows, group;  // rows: of all tiles of a (sequence, key head)
   int part_rows;           // rows of a part
-  int workers;
+  int workers, ctas;
   int blocks_per_page;
 };
 
@@ -243,8 +243,9 @@ __device__ __forceinline__ void finish(const AttentionArgs &a, const Plan &plan,
     *reinterpret_cast<uint2 *>(a.out + to) =
         make_uint2(bf16x2_bits(v[0] * f.by_weight * f.by_scale, v[1] * f.by_weight * f.by_scale),
                    bf16x2_bits(v[2] * f.by_weight * f.by_scale, v[3] * f.by_weight * f.by_scale));
-  if (a.lse != nullptr && d == 0)
-    a.lse[o_row * a.q_heads + head] = weight == 0.0f ? -INFINITY : (top + log2f(weight)) * 0.6931471805599453f;
+  const int64_t lse_at = o_row * a.q_heads + head;
+  if (a.lse != nullptr && d == 0 && in_bounds(lse_at, 1, static_cast<int64_t>(a.c.sequences) * a.q_tokens * a.q_heads, a.c.status))
+    a.lse[lse_at] = weight == 0.0f ? -INFINITY : (top + log2f(weight)) * 0.6931471805599453f;
 }
 
 // A part: sums [rows][dim]; each row's two maxima and its weight, `rows` apart.
@@ -252,8 +253,10 @@ struct Part {
   float *sums, *state;
   int rows;
 };
-__device__ __forceinline__ Part part_at(float *p, int rows, int dim) {
-  return Part{p, p + static_cast<int64_t>(rows) * dim, rows};
+// Part `index` of `count` in the workspace.
+__device__ __forceinline__ Part part_at(float *parts, int64_t index, int64_t count, int rows, int dim, uint32_t *status) {
+  float *const p = parts + index * part_floats(rows, dim);
+  return Part{p, p + static_cast<int64_t>(rows) * dim, in_bounds(index, 1, count, status) ? rows : 0};
 }
 
 // The sum of the parts part(0) .. part(n - 1) of a row, four channels from d on.
@@ -261,11 +264,12 @@ struct Joined {
   float v[4], top, gap, weight;
 };
 template <typename PartOf>
-__device__ __forceinline__ Joined join(int n, const PartOf &part, int row, int d, int dim) {
+__device__ __forceinline__ Joined join(int n, const PartOf &part, int row, int d, int dim, uint32_t *status) {
   Joined j{{0.0f, 0.0f, 0.0f, 0.0f}, kNone, kNone, 0.0f};
 #pragma unroll 4
   for (int i = 0; i < n; ++i) {
     const Part p = part(i);
+    if (!in_bounds(row, 1, p.rows, status)) continue;
     const float top = p.state[row], gap = p.state[p.rows + row], weight = p.state[2 * p.rows + row];
     const float4 v = *reinterpret_cast<const float4 *>(p.sums + row * dim + d);
     const float now = fmaxf(j.top, top);
@@ -282,7 +286,8 @@ __device__ __forceinline__ Joined join(int n, const PartOf &part, int row, int d
   return j;
 }
 
-__device__ __forceinline__ void put_part(const Part &p, int row, int d, int dim, const Joined &j) {
+__device__ __forceinline__ void put_part(const Part &p, int row, int d, int dim, const Joined &j, uint32_t *status) {
+  if (!in_bounds(row, 1, p.rows, status)) return;
   *reinterpret_cast<float4 *>(p.sums + row * dim + d) = make_float4(j.v[0], j.v[1], j.v[2], j.v[3]);
   if (d == 0) {
     p.state[row] = j.top;
@@ -748,7 +753,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
         // (the last part of a share takes the place of the ring; an earlier one, which goes to memory, ends
         // what another worker began)
         const bool in_ring = f + 1 == end;
-        Part part = part_at(plan.parts + worker * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
+        Part part = part_at(plan.parts, worker, plan.workers, plan.part_rows, DIM, c.status);
         if (in_ring) {
           part = Part{reinterpret_cast<float *>(smem + warp * S::kRing), states[warp], S::kRows};
           cp_async_wait<0>();
@@ -780,7 +785,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
                 if (whole_row)
                   finish(a, plan, at.b, at.h, row, d, DIM, j.v, factors, j.top, j.weight);
                 else
-                  put_part(part, pr, d, DIM, j);
+                  put_part(part, pr, d, DIM, j, c.status);
               }
           }
       }
@@ -822,7 +827,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
       const int64_t f0 = chain.tile * (total / plan.tiles) + static_cast<int64_t>(first[chain.b]) * c.heads + static_cast<int64_t>(chain.h) * chain.blocks;
       split = Split{static_cast<int>(shares.owner(f0 + chain.blocks - 1) / S::kWarps), chain.tile, chain.b, chain.h};
     }
-    plan.splits[blockIdx.x] = split;
+    if (in_bounds(blockIdx.x, 1, plan.ctas, c.status)) plan.splits[blockIdx.x] = split;
   }
   const int per_chain = plan.part_rows * (DIM / 4);
   for (int i = threadIdx.x; i < n_chains * per_chain; i += S::kWarps * 32) {
@@ -830,13 +835,12 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
     const int pr = i % per_chain / (DIM / 4), d = i % (DIM / 4) * 4, row = chain.tile * S::kRows + pr;
     if (row >= plan.rows) continue;
     const auto part = [&](int k) { return infos[chain.warp + k][k == 0 && chain.begins].part; };
-    const Joined j = join(chain.count, part, pr, d, DIM);
+    const Joined j = join(chain.count, part, pr, d, DIM, c.status);
     if (chain.begins && chain.ends)
       finish(a, plan, chain.b, chain.h, row, d, DIM, j.v, factors_of(j.gap, j.weight), j.top, j.weight);
     else
-      put_part(part_at(plan.cta_parts + (static_cast<int64_t>(blockIdx.x) * 2 + chain.begins) * part_floats(plan.part_rows, DIM),
-                       plan.part_rows, DIM),
-               pr, d, DIM, j);
+      put_part(part_at(plan.cta_parts, static_cast<int64_t>(blockIdx.x) * 2 + chain.begins, 2 * plan.ctas, plan.part_rows, DIM, c.status),
+               pr, d, DIM, j, c.status);
   }
 }
 
@@ -854,7 +858,7 @@ __global__ void __launch_bounds__(kJoinThreads<DIM>)
   griddep_launch_dependents();
   griddep_wait();
   const int p0 = blockIdx.x, pr = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const Split split = plan.splits[p0];
+  const Split split = in_bounds(p0, 1, plan.ctas, a.c.status) ? plan.splits[p0] : Split{-1, 0, 0, 0};
   if (split.last_cta < 0) return;
   const int row = split.tile * tile_rows + pr;
   if (row >= plan.rows) return;
@@ -862,20 +866,22 @@ __global__ void __launch_bounds__(kJoinThreads<DIM>)
   const int n = split.last_cta - p0 + 1;  // (at most as many as CTAs)
   // (the first CTA's part begins the row, the others' go on with it)
   const auto part = [&](int k) {
-    const int64_t p = p0 + k;
-    return part_at(plan.cta_parts + (p * 2 + (k == 0)) * part_floats(plan.part_rows, DIM), plan.part_rows, DIM);
+    return part_at(plan.cta_parts, static_cast<int64_t>(p0 + k) * 2 + (k == 0), 2 * plan.ctas, plan.part_rows, DIM, a.c.status);
   };
   if (n <= kGroups) {
-    const Joined own = join(group < n, [&](int) { return part(group); }, pr, d, DIM);
-    put_part(Part{sums[group], states[group], 1}, 0, d, DIM, own);
+    const Joined own = join(group < n, [&](int) { return part(group); }, pr, d, DIM, a.c.status);
+    put_part(Part{sums[group], states[group], 1}, 0, d, DIM, own, a.c.status);
     __syncthreads();
     if (group != 0) return;
-    const Joined j = join(n, [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, DIM);
+    const Joined j = join(n, [&](int k) { return Part{sums[k], states[k], 1}; }, 0, d, DIM, a.c.status);
     finish(a, plan, split.b, split.h, row, d, DIM, j.v, factors_of(j.gap, j.weight), j.top, j.weight);
     return;
   }
   const auto load = [&](int k) {
-    return k < n ? *reinterpret_cast<const float4 *>(part(k).sums + pr * DIM + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (k >= n) return make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const Part p = part(k);
+    return in_bounds(pr, 1, p.rows, a.c.status) ? *reinterpret_cast<const float4 *>(p.sums + pr * DIM + d)
+                                                : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   };
   float4 x[kAhead];
 #pragma unroll
@@ -888,6 +894,7 @@ __global__ void __launch_bounds__(kJoinThreads<DIM>)
     weight[i] = 0.0f;
     if (k < n) {
       const Part p = part(k);
+      if (!in_bounds(pr, 1, p.rows, a.c.status)) continue;
       top[i] = p.state[pr], gap[i] = p.state[p.rows + pr], weight[i] = p.state[2 * p.rows + pr];
     }
     all_top = fmaxf(all_top, top[i]);
@@ -956,6 +963,7 @@ cudaError_t launch(const AttentionArgs &a, cudaStream_t s) {
   plan.blocks_per_page = a.c.page_tokens / kCacheBlock;
   const int ctas = a.num_sms < kMaxSms ? a.num_sms : kMaxSms;
   plan.workers = ctas * S::kWarps;
+  plan.ctas = ctas;
   plan.splits = static_cast<Split *>(a.workspace);
   plan.cta_parts = reinterpret_cast<float *>(static_cast<uint8_t *>(a.workspace) + kSplitBytes);
   plan.parts = plan.cta_parts + 2 * ctas * part_floats(plan.part_rows, DIM);

@@ -36,6 +36,10 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   return r;
 }
 
+__device__ __forceinline__ int64_t start_of(const AppendArgs &a, int i) {
+  return in_bounds(i, 1, a.c.sequences + 1, a.c.status) ? a.starts[i] : 0;
+}
+
 template <int DIM>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendArgs a) {
   constexpr int kLanes = DIM / 8, kRows = 4, kPasses = kCacheBlock / kRows;
@@ -57,13 +61,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     b = static_cast<int>(blockIdx.x) / per;
     index = static_cast<int>(blockIdx.x) % per;
     row0 = b * n;
-    stated = c.lengths[b];
+    stated = stated_length(c, b);
   } else {
     if (threadIdx.x == 0) found = 0x7FFFFFFF, descends = shared_slots = 0;
     __syncthreads();
     const int64_t slot = blockIdx.x;
     for (int i = threadIdx.x; i < c.sequences; i += kThreads) {
-      const int64_t s0 = a.starts[i], s1 = a.starts[i + 1];
+      const int64_t s0 = start_of(a, i), s1 = start_of(a, i + 1);
       if (s0 < 0 || s1 < s0 || s1 > a.tokens) {
         if (slot == 0 && blockIdx.y == 0) atomicOr(c.status, kStatusIndexBit);
         descends = 1;
@@ -77,12 +81,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     __syncthreads();
     b = found;
     if (b == 0x7FFFFFFF) return;
-    row0 = a.starts[b];
-    n = a.starts[b + 1] - row0;
+    row0 = start_of(a, b);
+    n = start_of(a, b + 1) - row0;
     if (descends) {
       // a sequence with slots that an earlier one has, too, is left out as a whole
       for (int i = threadIdx.x; i < b; i += kThreads) {
-        const int64_t s0 = a.starts[i], s1 = a.starts[i + 1];
+        const int64_t s0 = start_of(a, i), s1 = start_of(a, i + 1);
         if (s0 >= 0 && s1 >= s0 && s1 <= a.tokens && s1 / kCacheBlock + 2 * static_cast<int64_t>(i) + 2 >
                                                         row0 / kCacheBlock + 2 * static_cast<int64_t>(b))
           shared_slots = 1;
@@ -90,7 +94,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       __syncthreads();
       if (shared_slots) return;
     }
-    stated = c.lengths[b];
+    stated = stated_length(c, b);
     index = slot - (row0 / kCacheBlock + 2 * static_cast<int64_t>(b));
   }
   if (head >= c.heads) return;

@@ -6,9 +6,14 @@
 
 namespace mx {
 
+// The length of sequence b as it stands in memory.
+__device__ __forceinline__ int64_t stated_length(const CacheArgs &c, int b) {
+  return in_bounds(b, 1, c.sequences, c.status) ? c.lengths[b] : 0;
+}
+
 // Tokens of sequence b: its length within 0 .. max_pages * page_tokens.
 __device__ __forceinline__ int64_t cache_length(const CacheArgs &c, int b) {
-  const int64_t n = in_bounds(b, 1, c.sequences, c.status) ? c.lengths[b] : 0;
+  const int64_t n = stated_length(c, b);
   const int64_t most = c.max_pages * c.page_tokens;
   if (n < 0 || n > most) {
     atomicOr(c.status, kStatusIndexBit);

@@ -173,7 +173,7 @@ __device__ __forceinline__ float head_sum(float v) {
 __device__ __forceinline__ void load_turns(uint64_t *turns, const RopeArgs &a) {
   for (int i = threadIdx.x; i < a.rotary_dim / 2; i += kWarps * 32) {
     const int j = i >> 3, e = i & 7, pair = a.interleaved ? 4 * j + (e >> 1) + (e & 1) * (a.rotary_dim / 4) : i;
-    turns[i] = turns_of(a.inv_freq[pair]);
+    turns[i] = in_bounds(pair, 1, a.rotary_dim / 2, a.status) ? turns_of(a.inv_freq[pair]) : 0;
   }
 }
 
@@ -469,7 +469,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
       float s = sums[0][d];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) s += sums[w][d];
-      a.partials[(static_cast<int64_t>(blockIdx.x) * 2 + k) * a.head_dim + d] = s;
+      const int64_t to = (static_cast<int64_t>(blockIdx.x) * 2 + k) * a.head_dim + d;
+      if (in_bounds(to, 1, kRopeBackCtas * 2 * a.head_dim, a.status)) a.partials[to] = s;
     }
   };
   const std::integral_constant<int, 0> queries;
@@ -502,7 +503,8 @@ __global__ void __launch_bounds__(kSumWarps * 32)
 #pragma unroll
     for (int k = 0; k < kRopeBackCtas / kSumWarps; ++k) {
       const int p = k * kSumWarps + warp;
-      if (p < ctas) s += a.partials[static_cast<int64_t>(p) * 2 * a.head_dim + i];
+      const int64_t at = static_cast<int64_t>(p) * 2 * a.head_dim + i;
+      if (p < ctas && in_bounds(at, 1, kRopeBackCtas * 2 * a.head_dim, a.status)) s += a.partials[at];
     }
   }
   sums[warp][lane] = s;
@@ -512,7 +514,7 @@ __global__ void __launch_bounds__(kSumWarps * 32)
   for (int w = 1; w < kSumWarps; ++w) s += sums[w][lane];
   const int k = i >= a.head_dim;
   float *out = a.part[k].dweight;
-  if (out != nullptr) out[i - k * a.head_dim] = s;
+  if (out != nullptr && in_bounds(i - k * a.head_dim, 1, a.head_dim, a.status)) out[i - k * a.head_dim] = s;
 }
 static_assert(kRopeBackCtas % kSumWarps == 0, "all partials are summed");
 
@@ -532,7 +534,7 @@ void slice(int64_t tokens, int groups, int64_t warps, int *slices, int *per_slic
   for (int p = groups; p >= 1; --p) {
     const int n = (groups + p - 1) / p;
     if (n > 1 && tokens * n >= (int64_t(1) << 31)) break;  // (the kernel divides 32-bit numbers)
-        const int64_t cost = (tokens * n + warps - 1) / warps * (2 * p + 1);
+    const int64_t cost = (tokens * n + warps - 1) / warps * (2 * p + 1);
     if (cost < least) least = cost, *slices = n, *per_slice = p;
   }
 }
