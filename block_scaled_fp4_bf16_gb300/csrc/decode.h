@@ -97,5 +97,17 @@ struct SampleArgs {
   uint32_t *status;
 };
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t s);
+constexpr int kSampleMaxCtas = 16, kSamplePortableCtas = 8;
+// The CTAs of a row: at least 4096 logits each; 16 (more than may be taken for granted: `most` is 8
+// where the context has no room for such a cluster) for few rows, and where rows fill the GPU as few as hold
+// a row in 16384 logits each (what a CTA does besides its logits takes 8 us; 256 x 32000: eight
+// a row 73 us, two 41).
+inline int sample_ctas(int64_t rows, int vocab, int num_sms, int most) {
+  int ctas = 1;
+  while (ctas < kSamplePortableCtas && ctas * 4096 < vocab) ctas *= 2;
+  if (rows * ctas * 2 <= num_sms && ctas == kSamplePortableCtas && vocab > 32768) ctas = most;
+  while (ctas > 1 && rows * ctas > 2 * num_sms && (vocab + ctas / 2 - 1) / (ctas / 2) <= 16384) ctas /= 2;
+  return ctas;
+}
 
 }  // namespace mx

@@ -26,7 +26,7 @@ namespace mx {
 namespace {
 
 constexpr int kWarps = 16, kThreads = kWarps * 32;
-constexpr int kMaxCtas = 16;
+constexpr int kMaxCtas = kSampleMaxCtas;
 constexpr int kUnit = 43;  // weights are in units of 2^-43
 constexpr int kTable = 256;
 constexpr int kBins = 1024;    // the last one: all lower logits
@@ -850,42 +850,50 @@ __global__ void __launch_bounds__(kThreads, 2)
   cluster_sync();  // (no CTA ends while another may still write to it)
 }
 
+// A launch of `grid` CTAs in clusters of `ctas`.
+cudaLaunchConfig_t config_of(int64_t grid, int ctas, size_t smem, cudaStream_t s, cudaLaunchAttribute (&attr)[2]) {
+  cudaLaunchConfig_t cfg = {};
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cfg;
+}
+
 template <bool FP32>
 cudaError_t launch(const SampleArgs &a, cudaStream_t s) {
-  // The CTAs of a row: at least 4096 logits each; 16 (more than may be taken for granted) for few
-  // rows, and where rows fill the GPU as few as hold a row in 16384 logits each (what a CTA
-  // does besides its logits takes 8 us; 256 x 32000: eight a row 73 us, two 41).
-  int ctas = 1;
-  while (ctas < 8 && ctas * 4096 < a.vocab) ctas *= 2;
-  const int64_t rows = a.rows;
-  if (rows * ctas * 2 <= a.num_sms && ctas == 8 && a.vocab > 32768) ctas = kMaxCtas;
-  while (ctas > 1 && rows * ctas > 2 * a.num_sms && (a.vocab + ctas / 2 - 1) / (ctas / 2) <= 16384) ctas /= 2;
   constexpr int kStep = kWarps * 128;  // a warp's segment is a multiple of 128
-  const int per = (a.vocab + ctas - 1) / ctas;
-  const int slice = (per + kStep - 1) / kStep * kStep;
   const void *func = reinterpret_cast<const void *>(sample_kernel<FP32>);
-  if (!kernel_setup_get(func, nullptr)) {
+  cudaLaunchAttribute attr[2];
+  int most = kSamplePortableCtas;  // CTAs of a cluster
+  if (!kernel_setup_get(func, &most)) {
     const cudaError_t e = cudaFuncSetAttribute(func, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                kSampleMaxVocab / 8 * static_cast<int>(sizeof(float)));
     if (e != cudaSuccess) return e;
     const cudaError_t n = cudaFuncSetAttribute(func, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (n != cudaSuccess) return n;
-    kernel_setup_put(func, 0);
+    // is there room for the largest cluster with the largest slice (a part of a GPU may have none)?
+    int clusters = 0;
+    const cudaLaunchConfig_t largest =
+        config_of(kMaxCtas, kMaxCtas, kSampleMaxVocab / kMaxCtas * sizeof(float), nullptr, attr);
+    most = cudaOccupancyMaxActiveClusters(&clusters, func, &largest) == cudaSuccess && clusters > 0 ? kMaxCtas
+                                                                                                    : kSamplePortableCtas;
+    (void)cudaGetLastError();  // (an answer, not an error of this call)
+    kernel_setup_put(func, most);
   }
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = ctas;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>(ctas) * static_cast<unsigned>(a.rows));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = static_cast<size_t>(slice) * sizeof(float);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  const int64_t rows = a.rows;
+  const int ctas = sample_ctas(rows, a.vocab, a.num_sms, most);
+  const int per = (a.vocab + ctas - 1) / ctas;
+  const int slice = (per + kStep - 1) / kStep * kStep;
+  const cudaLaunchConfig_t cfg = config_of(rows * ctas, ctas, static_cast<size_t>(slice) * sizeof(float), s, attr);
   const int sort_rows = a.top_p != nullptr && rows <= kThreads && rows * ctas > 2 * a.num_sms;
   return cudaLaunchKernelEx(&cfg, sample_kernel<FP32>, a, ctas, slice, sort_rows);
 }
