@@ -36,6 +36,22 @@ struct RopeArgs {
 };
 constexpr int kRopeMaxDim = 256;
 constexpr int kRopeBackCtas = 320;  // most CTAs of the backward kernel
+// Slices of a token's groups of heads: those with which the busiest warp has the least to do,
+// an item's angles counted as half a group (8192 tokens of 18 groups on 2432 warps: whole
+// tokens leave most warps with three and some with four, 57 us; halves 49).  Of the lengths that make
+// as many slices only the least counts, so that the most heads take some 500 steps, not 65535.
+inline void rope_slices(int64_t tokens, int groups, int64_t warps, int *slices, int *per_slice) {
+  *slices = 1;
+  *per_slice = groups;
+  int64_t least = INT64_MAX;
+  for (int p = groups; p >= 1; --p) {
+    const int n = (groups + p - 1) / p;
+    if (n > 1 && tokens * n >= (int64_t(1) << 31)) break;  // (the kernel divides 32-bit numbers)
+    p = (groups + n - 1) / n;
+    const int64_t cost = (tokens * n + warps - 1) / warps * (2 * p + 1);
+    if (cost < least) least = cost, *slices = n, *per_slice = p;
+  }
+}
 cudaError_t launch_qk_rope(const RopeArgs &a, cudaStream_t s);
 cudaError_t launch_qk_rope_backward(const RopeArgs &a, cudaStream_t s);
 

@@ -524,27 +524,12 @@ int lanes_of(int head_dim) {
   return lanes;
 }
 
-// Slices of a token's groups of heads: those with which the busiest warp has the least to do,
-// an item's angles counted as half a group (8192 tokens of 18 groups on 2432 warps: whole
-// tokens leave most warps with three and some with four, 57 us; halves 49).
-void slice(int64_t tokens, int groups, int64_t warps, int *slices, int *per_slice) {
-  *slices = 1;
-  *per_slice = groups;
-  int64_t least = INT64_MAX;
-  for (int p = groups; p >= 1; --p) {
-    const int n = (groups + p - 1) / p;
-    if (n > 1 && tokens * n >= (int64_t(1) << 31)) break;  // (the kernel divides 32-bit numbers)
-    const int64_t cost = (tokens * n + warps - 1) / warps * (2 * p + 1);
-    if (cost < least) least = cost, *slices = n, *per_slice = p;
-  }
-}
-
 Share share_of(const RopeArgs &a, int lanes, int64_t warps, bool together) {
   const int heads = 32 / lanes;
   Share s;
   for (int k = 0; k < 2; ++k) s.groups[k] = (a.part[k].heads + heads - 1) / heads;
   for (int k = 0; k < 2; ++k)
-    slice(a.tokens, together ? s.groups[0] + s.groups[1] : s.groups[k], warps, &s.slices[k], &s.per_slice[k]);
+    rope_slices(a.tokens, together ? s.groups[0] + s.groups[1] : s.groups[k], warps, &s.slices[k], &s.per_slice[k]);
   return s;
 }
 
