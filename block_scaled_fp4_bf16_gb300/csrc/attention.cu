@@ -3,15 +3,17 @@
 //   s_t = scale * 2^(ek) q . kcode_t,   out = sum_t softmax(s)_t 2^(ev) vcode_t
 //
 // The cache's bytes bound it: each is read once for the 8 (query token, head) rows that share
-// a key head (16 of 64 channels; more rows make more tiles, which find it in L2).  Keys, and
-// values transposed, are the 16-row side of FP16 products (16 x 8 x 16, binary32 sums) and the
-// rows its 8 columns, so that the conversion of codes, which costs more than the products, is
-// done once for all rows and few rows waste little (the rows on the 16-row side: 165 us for 64
-// x up to 8192 tokens of 64/8 heads, where this takes 94; the cache's bytes take 88).
+// a key head (16 of 64 channels).  More rows make more tiles, which read the cache again, some six
+// tenths of it from memory and the rest from L2 (16 x 2 x 8192 of 64/8 heads: 238 MB from memory for a
+// cache of some 145).  Keys, and values transposed, are the 16-row side of FP16 products (16 x 8 x 16,
+// binary32 sums) and the rows its 8 columns, so that the conversion of codes, which costs more than the
+// products, is done once for all rows of a tile and few rows waste little (the rows on the 16-row side: 165
+// us for 64 x up to 8192 tokens of 64/8 heads, where this took 94; now 101 over 568 MB that L2 has nothing
+// of, which take 85 at a copy's rate).
 // E4M3 is exact in FP16; q enters under a power of two of its row, a weight as the sum of two FP16
 // numbers, each a product of its own: as one number its 11 bits showed in the BF16 outputs (0.0005 from
-// binary32's, where two leave 0.0002 and less; 64 x 8192 of 64 channels 92 us with one, 99 with two,
-// of 128 channels 129 and 130).
+// binary32's, where two leave 0.0002 and less; 64 x up to 8192 of 128 channels 100 us with one, 101 with two, of
+// 64 channels 59 and 62, two tiles of those 91 and 98).
 //
 // Every warp is a worker of its own: the blocks of 32 tokens of all (row tile, sequence,
 // key head) together are shared out evenly and in order over the workers, so that uneven
@@ -22,11 +24,11 @@
 // scale, with which the FP16 weights are relative to the largest contribution to the output, however
 // far the blocks' scales lie apart.  Both are whole numbers, so that what a new maximum takes off the
 // sums is a power of two and exact; the second is one of differences, which binary32 has for logits
-// of any size (a maximum of logit + value scale would lose the scale from 2^24 on).  What a worker leaves unfinished goes to
-// the workspace or, at its end, in its ring; its CTA joins the parts of its workers, and a
-// second, small launch those of the CTAs, in their order (all by the second launch: 1 x 131072
-// of 32/4 heads 82 us, so 31, of which the cache takes 20, what precedes the first block 4, and
-// the joins 7).
+// of any size (a maximum of logit + value scale would lose the scale from 2^24 on).
+// What a worker leaves unfinished goes to the workspace or, at its end, in its ring; its CTA joins the
+// parts of its workers, and a second, small launch those of the CTAs, in their order (all by the second
+// launch: 1 x 131072 of 32/4 heads 82 us, so 32, of which the cache takes 20, what precedes the first
+// block 4, and the joins 8).
 //
 // Layouts: the order of channels in a product is free, so lane (g, t) = (lane / 4, lane % 4)
 // takes 16 consecutive bytes of keys g and g + 8 as four k-steps, and the queries are laid out
@@ -847,7 +849,7 @@ __global__ void __launch_bounds__(Shape<DIM, NT>::kWarps * 32, 1)
 // Joins the CTAs' parts of a row: CTA (x, y) row y of what CTA x of the launch before began and
 // left unfinished.  Groups of a row's DIM / 4 threads take every so many-th part's sums; where
 // that is more than one, each warp takes the parts' states first, so that all loads of a thread go out
-// together (1 x 131072 of 32/4 heads 32.2 us with a state before each part's sums, so 31.1).
+// together (1 x 131072 of 32/4 heads 32.2 us with a state before each part's sums, so 31.1 then).
 template <int DIM>
 __global__ void __launch_bounds__(kJoinThreads<DIM>)
     join_kernel(const __grid_constant__ AttentionArgs a, const __grid_constant__ Plan plan, int tile_rows) {
@@ -946,9 +948,9 @@ constexpr size_t kSplitBytes = kMaxSms * sizeof(Split);
 static_assert(kSplitBytes % 16 == 0, "alignment of the parts");
 
 // The rows of a tile: 8, or 16 of 64 channels where there are more than 8.  A second tile reads
-// the cache again, from L2 mostly, but 16 rows take registers from as many warps (16 x 2 x 8192
-// of 64/8 heads, in tiles of 8 / of 16 rows: 128 channels 50 / 53 us, 256 110 / 116; 64 x 2 of 64
-// channels 97 / 86).
+// the cache again, mostly from memory, but 16 rows take registers from as many warps (16 x 2 x 8192
+// of 64/8 heads, in tiles of 8 / of 16 rows: 128 channels 52 / 65 us; 64 x 2 of 64 channels 109 / 98;
+// 256 channels, before weights had two parts, 110 / 116).
 int tile_rows_of(int64_t rows, int dim) { return rows <= 8 || dim > 64 ? 8 : 16; }
 int64_t part_rows_of(int64_t rows, int dim) { return rows < tile_rows_of(rows, dim) ? rows : tile_rows_of(rows, dim); }
 

@@ -7,7 +7,7 @@
 //
 // A CTA takes the new tokens of one block of 32 of one sequence, for as many heads as come to
 // 256 channels (one head a CTA: 23 us for 16384 x 8 x 128, 35 for 16 x 64, where this takes 19 and
-// 19).  A unit of its threads has the keys or the values of a head: it reads each once, holds
+// 19 on one input again and again; 21.5 for the first over inputs in turn).  A unit of its threads has the keys or the values of a head: it reads each once, holds
 // it in registers (8 channels a lane) while the largest magnitude goes across its warps, and
 // writes its codes.  What a value costs bounds a prompt (so the largest of two at a time, one
 // factor, no test for infinities where the block has none), the chain starts and lengths,

@@ -351,7 +351,8 @@ __global__ void __launch_bounds__(kWarps * 32, kCtas)
 // The gradients of the inputs, and each CTA's sums of those of the weights: of the queries,
 // then of the keys (one part's sums in registers at a time).  The order of the sums follows
 // from the sizes and the number of SMs alone: a warp's tokens in order, then the lanes, then
-// the warps, then (backward_sum_kernel) the CTAs.
+// the warps, then (backward_sum_kernel) the CTAs.  They are binary32: shared out so, a chain of additions is
+// as long as a warp's tokens, of which there are thousands of times fewer than of all.
 template <int LANES>
 __global__ void __launch_bounds__(kWarps * 32, kCtas)
     rope_backward_kernel(const __grid_constant__ RopeArgs a, const __grid_constant__ Share share) {

@@ -226,7 +226,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     // begin first.  This cluster's row is the one of its number in that order.
     const int i = threadIdx.x;
     const bool in = i < a.rows;
-    const bool slow = in && in_bounds(i, 1, a.rows, a.status) && a.top_p[i] < 1.0f && (a.temperature == nullptr || a.temperature[i] > 0.0f);
+    const bool slow = in && in_bounds(i, 1, a.rows, a.status) && a.top_p[i] < 1.0f &&
+                      (a.temperature == nullptr || a.temperature[i] > 0.0f);
     const uint32_t slows = __ballot_sync(0xFFFFFFFFu, slow), others = __ballot_sync(0xFFFFFFFFu, in && !slow);
     if (lane == 0) sh.sums[0][warp] = static_cast<uint64_t>(__popc(slows)) << 32 | static_cast<uint32_t>(__popc(others));
     __syncthreads();
