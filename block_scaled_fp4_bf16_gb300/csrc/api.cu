@@ -9,6 +9,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -1376,7 +1377,7 @@ int qk_norm_check(const char *fn, const mx_qk_norm *n, int64_t tokens) {
                 static_cast<long long>(n->rotary_dim));
   if (n->interleaved != 0 && n->interleaved != 1)
     return fail(MX_ERR_INVALID_ARG, "%s: interleaved = %d (0 or 1)", fn, n->interleaved);
-  if (!(n->eps >= 0.0f) || n->eps > 3.0e38f)
+  if (!(n->eps >= 0.0f) || n->eps > FLT_MAX)
     return fail(MX_ERR_INVALID_ARG, "%s: eps = %g (0 or more, finite)", fn, static_cast<double>(n->eps));
   if ((n->rotary_dim > 0) != (n->inv_freq != nullptr))
     return fail(MX_ERR_INVALID_ARG, "%s: inv_freq %s", fn,
@@ -1697,7 +1698,7 @@ MX_API int mx_attention_bf16(const void *q, int64_t ld_q, int64_t q_heads, int64
   Range ranges[6];
   rc = cache_check(fn, cache, page_table, max_pages, lengths, sequences, MX_ATTENTION_MAX_SEQUENCES, &a.c, ranges);
   if (rc != MX_OK) return rc;
-  if (!(scale >= -3.0e38f && scale <= 3.0e38f))
+  if (!(scale >= -FLT_MAX && scale <= FLT_MAX))
     return fail(MX_ERR_INVALID_ARG, "%s: scale = %g (finite)", fn, static_cast<double>(scale));
   if (window < 0 || window >= (int64_t(1) << 31))
     return fail(MX_ERR_INVALID_ARG, "%s: window = %lld (0 .. 2^31 - 1)", fn, static_cast<long long>(window));

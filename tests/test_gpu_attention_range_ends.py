@@ -13,7 +13,8 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("scale,query,key", [
-    (3.0e38, 2.0 ** -120, -10), (-2.9e38, 2.0 ** -120, -10), (3.0e38, 2.0 ** -20, -110), (2.0 ** 127, 2.0 ** -128, -2),
+    (3.4028234e38, 2.0 ** -120, -10), (3.0e38, 2.0 ** -120, -10), (-2.9e38, 2.0 ** -120, -10), (3.0e38, 2.0 ** -20, -110),
+    (2.0 ** 127, 2.0 ** -128, -2),
     (2.0 ** 126, 2.0 ** -131, 2), (2.0 ** 10, 2.0 ** -130, 114), (2.0 ** -100, 2.0 ** -30, 120), (2.0 ** -126, 2.0 ** 120, 2),
     (2.0 ** -130, 2.0 ** 10, 114), (2.0 ** -140, 2.0 ** 110, 22), (2.0 ** 100, 2.0 ** 20, -126), (1.0, 2.0 ** 115, -125),
     (1.0, 2.0 ** -122, 115)])
